@@ -177,7 +177,7 @@ def prepare(case, seed):
             pos += held[b]
         free = np.zeros(total, np.int32)
         free[:total - pos] = ids[pos:]
-        s.update(P=T(P), n=T(n), zero=T(np.zeros(B, np.int32)), table=T(table), held=T(held.astype(np.int32)), free=T(free),
+        s.update(P=T(P), n=T(n), table=T(table), held=T(held.astype(np.int32)), free=T(free),
                  count=T(np.asarray([total - pos], np.int32)))
     elif op == "write":
         tokens, Hkv, D = case["T"], case["Hkv"], case["D"]
@@ -274,9 +274,10 @@ def _rows(cache):
     return v.transpose(1, 2).reshape(-1, v.shape[1], v.shape[3])
 
 
-def _plain_slots(s, n, trim):
+def _plain_slots(s, trim):
     P, table, held, free, count = s["P"], s["table"], s["held"], s["free"], s["count"]
-    want = (P + n + PAGE - 1) // PAGE
+    n = s["n"]
+    want = (P + (0 if trim else n) + PAGE - 1) // PAGE
     j = torch.arange(table.shape[1], device=table.device)[None, :]
     have = held[:, None].long()
     if trim:
@@ -370,8 +371,8 @@ def _plain_logprobs(x, token, k):
 def _plain(s):
     op = s["op"]
     if op == "slots":
-        slots = _plain_slots(s, s["n"], False)
-        _plain_slots(s, s["zero"], True)
+        slots = _plain_slots(s, False)
+        _plain_slots(s, True)
         return slots, s["table"], s["held"], s["free"], s["count"]
     if op == "write":
         page, row = s["slots"].long() // PAGE, s["slots"].long() % PAGE
@@ -413,7 +414,7 @@ def run(s):
     op = s["op"]
     if op == "slots":  # a step's two calls: room for its tokens, then what was not committed goes back
         slots = tsd.kv_slots_build(s["P"], s["n"], s["N"], s["table"], s["held"], s["free"], s["count"])
-        tsd.kv_slots_build(s["P"], s["zero"], 0, s["table"], s["held"], s["free"], s["count"], trim=True)
+        tsd.kv_blocks_release(s["P"], s["table"], s["held"], s["free"], s["count"])
         return slots, s["table"], s["held"], s["free"], s["count"]
     if op == "write":
         tsd.kv_write_q4(s["k"], s["v"], s["slots"], s["kc"], s["vc"])
