@@ -92,6 +92,8 @@ enum {
 #define TSD_STATUS_BAD_LEN 2  /* P_b < 0 or P_b + N_b beyond max_slots / the table */
 #define TSD_STATUS_BAD_PATH 4 /* accept_len / path inconsistent with the tree */
 #define TSD_STATUS_TIMEOUT 8  /* a bounded wait inside a kernel ran out: outputs unspecified */
+#define TSD_STATUS_NO_BLOCK 16 /* the free list does not hold what a sequence needs: skipped */
+#define TSD_STATUS_NONFINITE 32 /* a NaN or infinity in rows written to a 4-bit cache */
 
 /* Library version string (static storage). */
 const char *tsd_version(void);
@@ -573,6 +575,154 @@ int tsd_budget_calibrate(const double *t_roof, const double *t_meas, int count, 
                          double *beta);
 int tsd_budget_select(const float *rho, int B, int N_max, const float *cost, float l_ar,
                       int32_t *n_opt, float *s_opt, tsd_stream_t stream);
+
+/*
+ * Block tables and slot maps from the requests' lengths ([Blog] vLLM
+ * PagedAttention: a sequence's cache is a table of blocks from a pool).  No
+ * length has to reach the host.
+ *
+ * The caller keeps, on the device: block_table, how many blocks each sequence
+ * holds (held[b]; entries [0, held[b]) of its table row), and the pool's
+ * unused block ids as a stack free_list[0 .. *free_count).
+ *
+ * tsd_kv_slots_build: room for n_new[b] tokens after the first prefix_len[b].
+ *   need_b = max(0, ceil((P_b + n_b) / 16) - held_b) blocks are taken.  The
+ *   blocks a call takes are numbered by sequence, then by position in the
+ *   table; number i is free_list[*free_count - 1 - i].  A sequence is served
+ *   iff the needs of the sequences up to and including it fit *free_count; one
+ *   that is not takes nothing and sets TSD_STATUS_NO_BLOCK.
+ *   slots[b][i] = the pool slot (block id * 16 + row) of token P_b + i for
+ *   i < n_b, -1 beyond and for sequences not served: what tsd_kv_write_q4
+ *   takes.
+ * tsd_kv_blocks_release: gives back the blocks past ceil(keep_len[b] / 16)
+ *   (0: all of them), so that it undoes a build exactly: the blocks given back
+ *   are numbered the same way, of `all` of them number i becomes
+ *   free_list[*free_count + all - 1 - i].  Their table entries become -1.
+ *
+ * prefix_len, keep_len int32 [B]; n_new int32 [B] or NULL (N_max each);
+ * block_table int32 [B][max_blocks], held int32 [B], free_list int32
+ * [num_blocks], free_count int32 [1]: updated in place; slots int32
+ * [B][N_max] out (16-byte aligned when N_max is a multiple of 4).
+ * A sequence with a negative length, n_new outside [0, N_max], more tokens
+ * than its table covers or held outside [0, max_blocks] is left alone
+ * (TSD_STATUS_BAD_LEN).  *free_count outside [0, num_blocks], or more blocks
+ * given back than the list has room for: no block moves in the call
+ * (TSD_STATUS_BAD_LEN).  A block id outside [0, num_blocks) gives slot -1 and,
+ * if it was taken, table entry -1 (TSD_STATUS_BAD_PAGE).
+ * Limits: N_max <= 262144, 16 * num_blocks and 16 * max_blocks < 2^31.
+ * workspace >= tsd_kv_slots_workspace_bytes(B, N_max) bytes (for the release
+ * N_max = 0; no initial contents; 0 for small calls).  One launch for up to
+ * 64 sequences and 8192 tokens, else two (scan, fill).
+ */
+size_t tsd_kv_slots_workspace_bytes(int B, int N_max);
+int tsd_kv_slots_build(const int32_t *prefix_len, const int32_t *n_new, int B, int N_max,
+                       int32_t *block_table, int max_blocks, int32_t *held, int32_t *free_list,
+                       int32_t *free_count, int num_blocks, int32_t *slots, void *workspace,
+                       size_t ws_bytes, int32_t *status, tsd_stream_t stream);
+int tsd_kv_blocks_release(const int32_t *keep_len, int B, int32_t *block_table, int max_blocks,
+                          int32_t *held, int32_t *free_list, int32_t *free_count, int num_blocks,
+                          void *workspace, size_t ws_bytes, int32_t *status, tsd_stream_t stream);
+
+/*
+ * The 4-bit paged cache: k_cache and v_cache are uint8
+ * [num_blocks][Hkv][9 * D], one page of 16 token slots per (block, kv head):
+ * 16 rows of D / 2 code bytes (even column in the low nibble), then 16 rows
+ * of D / 16 scale bytes.  Each 16 consecutive columns of a row share a scale.
+ *   code:  E2M1 (sign, two exponent bits, one fraction bit): the magnitudes
+ *          0, 0.5, 1, 1.5, 2, 3, 4, 6;
+ *   scale: five exponent and three fraction bits, no sign: the half-precision
+ *          number with bits byte << 7; bytes above 0xE2 (10240) read as 0xE2.
+ * value = code * scale, exact in fp16 and bf16; 4.5 bits a value.  The block
+ * table, slot and limit conventions are those of the bf16 cache.
+ *
+ * tsd_kv_write_q4: for token t with slots[t] = s >= 0, quantises rows
+ *   k[t][h], v[t][h] (bf16, D values at k + t * k_stride + h * D) into slot s.
+ *   scale = the nearest (ties to even) to max |x| / 6, at most 10240; code =
+ *   the nearest (ties to even) to x / scale.  NaN is stored as 0 and an
+ *   infinity as the largest value of its group; either sets
+ *   TSD_STATUS_NONFINITE.  s = -1 skips the token; any other s outside the pool
+ *   skips it with TSD_STATUS_BAD_PAGE.  The slots of one call must differ (two
+ *   tokens with one slot leave a mixture of their rows in it).
+ *   k_stride, v_stride: elements between tokens, multiples of 8, >= Hkv * D.
+ * tsd_kv_read_q4: k, v bf16 [T][Hkv][D] out: the values at slots[t] (zeros for
+ *   -1, and for a slot outside the pool, which sets TSD_STATUS_BAD_PAGE).
+ * tsd_kv_commit_path_q4: tsd_kv_commit_path (tail_base NULL) and
+ *   tsd_kv_commit_path_from (tail_base int32 [B]) on 4-bit pools; layer_stride
+ *   in bytes, a multiple of 16.
+ * k, v and the caches are 16-byte aligned.
+ */
+int tsd_kv_write_q4(const uint16_t *k, int64_t k_stride, const uint16_t *v, int64_t v_stride,
+                    const int32_t *slots, int64_t T, int num_blocks, int Hkv, int D,
+                    uint8_t *k_cache, uint8_t *v_cache, int32_t *status, tsd_stream_t stream);
+int tsd_kv_read_q4(const uint8_t *k_cache, const uint8_t *v_cache, const int32_t *slots, int64_t T,
+                   int num_blocks, int Hkv, int D, uint16_t *k, uint16_t *v, int32_t *status,
+                   tsd_stream_t stream);
+int tsd_kv_commit_path_q4(uint8_t *k_cache, uint8_t *v_cache, int num_layers, int64_t layer_stride,
+                          const int32_t *block_table, int max_blocks, int num_blocks,
+                          const int32_t *prefix_len, const int32_t *n_nodes,
+                          const int32_t *accept_len, const int32_t *path, const int32_t *err,
+                          const int32_t *tail_base, int B, int N_max, int Hkv, int D, int D_max,
+                          int32_t *new_len, int32_t *moved, int32_t *status, tsd_stream_t stream);
+
+/*
+ * a2 over the 4-bit cache: arguments, masks, outputs and errors of
+ * tsd_tree_attn_fwd, with the caches as above; no deferred-commit record.
+ * mask NULL: node i sees the tree's nodes 0..i (a chain; with N_max = 1 the
+ * decoding of one token).  A row that sees no key gets 0 / -inf.  K and V are
+ * decoded without rounding; q is converted to fp16 after scaling each row by a
+ * power of two; P is rounded to fp16; every sum is fp32 and out is rounded once
+ * to bf16.  A sequence is skipped when a block id in its key range is bad.
+ * Unlike tsd_tree_attn_fwd, it reads nothing before the previous kernel on the
+ * stream has finished.
+ * workspace >= tsd_tree_attn_q4_workspace_bytes() (fp32 split partials; no
+ * initial contents; may be NULL when that is 0).
+ */
+size_t tsd_tree_attn_q4_workspace_bytes(int B, int N_max, int Hq, int Hkv, int D, int max_slots);
+int tsd_tree_attn_fwd_q4(const uint16_t *q, const uint8_t *k_cache, const uint8_t *v_cache,
+                         const int32_t *block_table, int max_blocks, int num_blocks,
+                         const int32_t *prefix_len, const int32_t *n_nodes, const uint32_t *mask,
+                         const int32_t *err, int B, int N_max, int Hq, int Hkv, int D, int max_slots,
+                         float scale, uint16_t *out, float *lse, void *workspace, size_t ws_bytes,
+                         int32_t *status, tsd_stream_t stream);
+
+/*
+ * Log probabilities of given tokens, with the entropy of each row and its k
+ * most probable tokens (no page counterpart: what a server answers with next
+ * to the tokens that a verify step emits).
+ *
+ * For a row x of V logits and a token t, lse = ln(sum exp(x)):
+ *   logprob = x[t] - lse (-inf for a token outside [0, V)),
+ *   entropy = -sum p ln p, p = exp(x - lse),
+ *   top_ids / top_logprobs [k]: by (logit descending, id ascending), x - lse.
+ * fp32 throughout.  Logits of -inf have probability 0; a row of only -inf
+ * gives logprob and top_logprobs -inf, entropy 0.  A NaN or +inf logit makes
+ * the row's results NaN (ids: NaN ranks first).
+ *
+ * tsd_token_logprobs: R rows: tokens[r] under row rows[r] (NULL: r) of logits
+ *   [num_rows][V].  rows[r] = -1: no row (below); any other outside
+ *   [0, num_rows) too, with TSD_STATUS_BAD_PATH.
+ * tsd_tree_path_logprobs: the tokens a verify step emits, from its outputs:
+ *   for k = 0..accept_len[b] the token after path node k (the token of node
+ *   k + 1 of the path, the bonus after the last) under that node's row of logits
+ *   [B][N_max][V]; emitted[b][k] is that token.  Sequences with err != 0 emit
+ *   nothing; an accept_len or path node out of range neither
+ *   (TSD_STATUS_BAD_PATH).  Outputs are [B][D_max+1] (and [..][k]).
+ * No row: emitted -1, logprob 0, entropy 0, top_ids -1, top_logprobs -inf.
+ *
+ * logits float (bf16 == 0) or bf16; entropy may be NULL, and top_ids /
+ * top_logprobs when k == 0; err int32 [B] or NULL.
+ * Limits: 0 <= k <= 32, k <= V <= 2^24; tsd_token_logprobs R <= 2^27;
+ * tsd_tree_path_logprobs B * (D_max + 1) <= 65535.
+ * One launch, no workspace: a cluster of up to 8 CTAs a row.
+ */
+int tsd_token_logprobs(const void *logits, int bf16, const int32_t *tokens, const int32_t *rows,
+                       int R, int64_t num_rows, int V, int k, float *logprob, float *entropy,
+                       int32_t *top_ids, float *top_logprobs, int32_t *status, tsd_stream_t stream);
+int tsd_tree_path_logprobs(const void *logits, int bf16, const int32_t *tokens, const int32_t *path,
+                           const int32_t *accept_len, const int32_t *bonus, const int32_t *err, int B,
+                           int N_max, int V, int D_max, int k, int32_t *emitted, float *logprob,
+                           float *entropy, int32_t *top_ids, float *top_logprobs, int32_t *status,
+                           tsd_stream_t stream);
 
 #ifdef __cplusplus
 } /* extern "C" */

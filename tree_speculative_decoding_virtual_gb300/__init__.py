@@ -13,6 +13,7 @@ been built (``tree_speculative_decoding_virtual_gb300._build.build()``).
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -26,6 +27,7 @@ _ERR_NAMES = {TSD_ERR_ARG: "TSD_ERR_ARG", TSD_ERR_LIMIT: "TSD_ERR_LIMIT",
 
 TREE_RANGE, TREE_CYCLE, TREE_TOO_DEEP, TREE_CLOSURE, TREE_ROOT, TREE_COUNT = 1, 2, 4, 8, 16, 32
 STATUS_BAD_PAGE, STATUS_BAD_LEN, STATUS_BAD_PATH, STATUS_TIMEOUT = 1, 2, 4, 8
+STATUS_NO_BLOCK, STATUS_NONFINITE = 16, 32
 OPT_WAIT_LIMIT_NS, OPT_TEST_STALL = 0, 1
 
 # C signatures: (name, restype, argtypes)
@@ -70,6 +72,19 @@ SIGNATURES = {
     "tsd_verify_step_cost": (_I, [_I, _I, _I, _I, _P, _I, _I, _I, _D, _D, _P, _P, _P]),
     "tsd_budget_calibrate": (_I, [_P, _P, _I, _P, _P]),
     "tsd_budget_select": (_I, [_P, _I, _I, _P, _F, _P, _P, _P]),
+    "tsd_kv_slots_workspace_bytes": (_SZ, [_I, _I]),
+    "tsd_kv_slots_build": (_I, [_P, _P, _I, _I, _P, _I, _P, _P, _P, _I, _P, _P, _SZ, _P, _P]),
+    "tsd_kv_blocks_release": (_I, [_P, _I, _P, _I, _P, _P, _P, _I, _P, _SZ, _P, _P]),
+    "tsd_kv_write_q4": (_I, [_P, _I64, _P, _I64, _P, _I64, _I, _I, _I, _P, _P, _P, _P]),
+    "tsd_kv_read_q4": (_I, [_P, _P, _P, _I64, _I, _I, _I, _P, _P, _P, _P]),
+    "tsd_kv_commit_path_q4": (_I, [_P, _P, _I, _I64, _P, _I, _I, _P, _P, _P, _P, _P, _P, _I, _I, _I,
+                                   _I, _I, _P, _P, _P, _P]),
+    "tsd_tree_attn_q4_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I, _I]),
+    "tsd_tree_attn_fwd_q4": (_I, [_P, _P, _P, _P, _I, _I, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F,
+                                  _P, _P, _P, _SZ, _P, _P]),
+    "tsd_token_logprobs": (_I, [_P, _I, _P, _P, _I, _I64, _I, _I, _P, _P, _P, _P, _P, _P]),
+    "tsd_tree_path_logprobs": (_I, [_P, _I, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P,
+                                    _P, _P]),
 }
 
 
@@ -585,6 +600,318 @@ def budget_select(rho, cost, l_ar, n_opt=None, s_opt=None, stream=None):
                                  _ptr(s_opt, torch.float32, "s_opt"), _stream(stream)),
            "budget_select")
     return n_opt, s_opt
+
+
+# ---------------------------------------------------------------------------
+# block tables, the 4-bit cache, log probabilities
+#
+# These calls check every shape, and refuse tensors that are not on the
+# current device (their kernels run there).
+# ---------------------------------------------------------------------------
+
+
+def _on_stream(fn):
+    """With stream= (a torch stream or a raw handle) the call runs under that
+    stream, so that what it allocates belongs to the stream that uses it."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kwargs):
+        if stream is None:
+            return fn(*args, **kwargs)
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream))
+        with torch.cuda.stream(stream):
+            return fn(*args, **kwargs)
+    return call
+
+
+def _device_of(t) -> int:
+    dev = t.get_device()
+    if dev >= 0 and dev != torch.cuda.current_device():
+        raise TsdError("tensors must be on the current CUDA device")
+    return dev
+
+
+def _arg(t, dtype, shape, name, dev):
+    """Pointer of a contiguous CUDA tensor of this dtype and shape on device
+    dev (None: a null pointer)."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise TsdError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if shape is not None and t.shape != shape:
+        raise TsdError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    if dev < 0 or t.get_device() != dev:
+        raise TsdError("%s must be a CUDA tensor on the same device as the others" % name)
+    if not t.is_contiguous():
+        raise TsdError("%s must be contiguous" % name)
+    return t.data_ptr()
+
+
+def _workspace_arg(workspace, need, like, dev):
+    """(pointer, bytes) of the caller's workspace, or of a new one."""
+    if workspace is None:
+        if need == 0:
+            return None, 0, None
+        workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
+    return (_arg(workspace, workspace.dtype, None, "workspace", dev),
+            workspace.numel() * workspace.element_size(), workspace)
+
+
+def kv_slots_workspace_bytes(B: int, N_max: int) -> int:
+    return int(lib.tsd_kv_slots_workspace_bytes(B, N_max))
+
+
+@_on_stream
+def kv_slots_build(prefix_len, n_new, N_max, block_table, held, free_list, free_count, slots=None,
+                   workspace=None, status=None):
+    """Room for n_new[b] (None: N_max) tokens after the first prefix_len[b] of
+    each sequence: takes the blocks they need from the free list (block_table
+    [B][max_blocks], held [B], free_list [num_blocks], free_count [1], all
+    int32, updated in place).  Returns slots int32 [B][N_max], the pool slot of
+    each new token (-1: none)."""
+    B = prefix_len.shape[0]
+    i32 = torch.int32
+    dev = _device_of(prefix_len)
+    if block_table.dim() != 2 or free_list.dim() != 1:
+        raise TsdError("block_table must be [B][max_blocks] and free_list [num_blocks]")
+    max_blocks, num_blocks = block_table.shape[1], free_list.shape[0]
+    if slots is None:
+        slots = torch.empty((B, max(N_max, 0)), dtype=i32, device=prefix_len.device)
+    args = (_arg(prefix_len, i32, (B,), "prefix_len", dev), _arg(n_new, i32, (B,), "n_new", dev), B, N_max,
+            _arg(block_table, i32, (B, max_blocks), "block_table", dev), max_blocks,
+            _arg(held, i32, (B,), "held", dev), _arg(free_list, i32, (num_blocks,), "free_list", dev),
+            _arg(free_count, i32, (1,), "free_count", dev), num_blocks,
+            _arg(slots, i32, (B, N_max), "slots", dev))
+    ws, ws_bytes, keep = _workspace_arg(workspace, kv_slots_workspace_bytes(B, N_max), prefix_len, dev)
+    _check(lib.tsd_kv_slots_build(*args, ws, ws_bytes, _arg(status, i32, None, "status", dev),
+                                  _stream(None)), "kv_slots_build")
+    return slots
+
+
+@_on_stream
+def kv_blocks_release(keep_len, block_table, held, free_list, free_count, workspace=None, status=None):
+    """Gives the blocks past the first keep_len[b] tokens of each sequence back
+    to the free list (arguments as kv_slots_build; keep_len 0 frees a
+    sequence)."""
+    B = keep_len.shape[0]
+    i32 = torch.int32
+    dev = _device_of(keep_len)
+    if block_table.dim() != 2 or free_list.dim() != 1:
+        raise TsdError("block_table must be [B][max_blocks] and free_list [num_blocks]")
+    max_blocks, num_blocks = block_table.shape[1], free_list.shape[0]
+    args = (_arg(keep_len, i32, (B,), "keep_len", dev), B,
+            _arg(block_table, i32, (B, max_blocks), "block_table", dev), max_blocks,
+            _arg(held, i32, (B,), "held", dev), _arg(free_list, i32, (num_blocks,), "free_list", dev),
+            _arg(free_count, i32, (1,), "free_count", dev), num_blocks)
+    ws, ws_bytes, keep = _workspace_arg(workspace, kv_slots_workspace_bytes(B, 0), keep_len, dev)
+    _check(lib.tsd_kv_blocks_release(*args, ws, ws_bytes, _arg(status, i32, None, "status", dev),
+                                     _stream(None)), "kv_blocks_release")
+
+
+def kv_q4_page_bytes(D: int) -> int:
+    """Bytes of one page (16 slots of one kv head) of a 4-bit cache."""
+    return 9 * D
+
+
+def _q4_dims(k_cache, v_cache):
+    """(num_blocks, Hkv, D) of a 4-bit pool, the layer axis left out."""
+    if k_cache.dim() < 3 or k_cache.shape != v_cache.shape:
+        raise TsdError("k_cache and v_cache must be [num_blocks][Hkv][9 * D], alike")
+    num_blocks, Hkv, page = k_cache.shape[-3:]
+    if page not in (9 * 64, 9 * 128):
+        raise TsdError("a 4-bit page holds 9 * D bytes, D 64 or 128")
+    return num_blocks, Hkv, page // 9
+
+
+def _token_rows(x, Hkv, D, name):
+    """(tokens, elements between tokens) of x [...][Hkv][D], whose leading axes
+    must step evenly."""
+    if x.dim() < 2 or x.shape[-2] != Hkv or x.shape[-1] != D:
+        raise TsdError("%s must be [...][%d][%d]" % (name, Hkv, D))
+    if x.stride(-1) != 1 or (Hkv > 1 and x.stride(-2) != D):
+        raise TsdError("%s: a token's heads must be contiguous" % name)
+    tokens, stride = 1, None
+    for n, st in zip(reversed(x.shape[:-2]), reversed(x.stride()[:-2])):
+        if n == 1:
+            continue
+        if stride is None:
+            stride = st
+        elif st != stride * tokens:
+            raise TsdError("%s: tokens must be evenly spaced" % name)
+        tokens *= n
+    return tokens, Hkv * D if stride is None else stride
+
+
+@_on_stream
+def kv_write_q4(k, v, slots, k_cache, v_cache, status=None):
+    """Quantises k, v bf16 [...][Hkv][D] into the 4-bit pool (uint8
+    [num_blocks][Hkv][9 * D]) at slots int32 [...] (-1: skip; as kv_slots_build
+    returns them).  Tokens may be strided (rows of a fused projection)."""
+    num_blocks, Hkv, D = _q4_dims(k_cache, v_cache)
+    if k_cache.dim() != 3:
+        raise TsdError("kv_write_q4 takes one layer's pool")
+    T, ks = _token_rows(k, Hkv, D, "k")
+    Tv, vs = _token_rows(v, Hkv, D, "v")
+    if T != Tv or slots.numel() != T:
+        raise TsdError("k, v and slots must hold the same tokens")
+    dev = _device_of(k)
+    for t, name in ((k, "k"), (v, "v")):
+        if t.dtype != torch.bfloat16 or dev < 0 or t.get_device() != dev:
+            raise TsdError("%s must be a bfloat16 CUDA tensor on the same device as the others" % name)
+    rc = lib.tsd_kv_write_q4(k.data_ptr(), ks, v.data_ptr(), vs, _arg(slots, torch.int32, None, "slots", dev),
+                             T, num_blocks, Hkv, D, _arg(k_cache, torch.uint8, None, "k_cache", dev),
+                             _arg(v_cache, torch.uint8, None, "v_cache", dev),
+                             _arg(status, torch.int32, None, "status", dev), _stream(None))
+    _check(rc, "kv_write_q4")
+
+
+@_on_stream
+def kv_read_q4(k_cache, v_cache, slots, k=None, v=None, status=None):
+    """Values of a 4-bit pool at slots int32 [T] (-1: zeros).  A pool with a
+    layer axis reads as one of layers * num_blocks blocks.  Returns (k, v) bf16
+    [T][Hkv][D]."""
+    num_blocks, Hkv, D = _q4_dims(k_cache, v_cache)
+    num_blocks = k_cache.numel() // (Hkv * 9 * D)
+    dev = _device_of(slots)
+    shape = (slots.numel(), Hkv, D)
+    if k is None:
+        k = torch.empty(shape, dtype=torch.bfloat16, device=slots.device)
+    if v is None:
+        v = torch.empty(shape, dtype=torch.bfloat16, device=slots.device)
+    rc = lib.tsd_kv_read_q4(_arg(k_cache, torch.uint8, None, "k_cache", dev),
+                            _arg(v_cache, torch.uint8, None, "v_cache", dev),
+                            _arg(slots, torch.int32, None, "slots", dev), shape[0], num_blocks, Hkv, D,
+                            _arg(k, torch.bfloat16, shape, "k", dev), _arg(v, torch.bfloat16, shape, "v", dev),
+                            _arg(status, torch.int32, None, "status", dev), _stream(None))
+    _check(rc, "kv_read_q4")
+    return k, v
+
+
+@_on_stream
+def kv_commit_path_q4(k_cache, v_cache, block_table, prefix_len, n_nodes, accept_len, path, err, N_max,
+                      D_max, tail_base=None, new_len=None, moved=None, status=None):
+    """kv_commit_path on 4-bit pools, uint8 [num_layers][num_blocks][Hkv][9 * D]
+    (or without the layer axis).  Returns (new_len [B], moved [B])."""
+    num_blocks, Hkv, D = _q4_dims(k_cache, v_cache)
+    layers = k_cache.shape[0] if k_cache.dim() == 4 else 1
+    B = prefix_len.shape[0]
+    i32 = torch.int32
+    dev = _device_of(prefix_len)
+    if k_cache.dim() > 4 or block_table.dim() != 2:
+        raise TsdError("the pools have at most a layer axis; block_table is [B][max_blocks]")
+    max_blocks = block_table.shape[1]
+    new_len = new_len if new_len is not None else torch.empty((B,), dtype=i32, device=prefix_len.device)
+    moved = moved if moved is not None else torch.empty((B,), dtype=i32, device=prefix_len.device)
+    rc = lib.tsd_kv_commit_path_q4(
+        _arg(k_cache, torch.uint8, None, "k_cache", dev), _arg(v_cache, torch.uint8, None, "v_cache", dev),
+        layers, num_blocks * Hkv * 9 * D, _arg(block_table, i32, (B, max_blocks), "block_table", dev),
+        max_blocks, num_blocks, _arg(prefix_len, i32, (B,), "prefix_len", dev),
+        _arg(n_nodes, i32, (B,), "n_nodes", dev), _arg(accept_len, i32, (B,), "accept_len", dev),
+        _arg(path, i32, (B, D_max + 1), "path", dev), _arg(err, i32, (B,), "err", dev),
+        _arg(tail_base, i32, (B,), "tail_base", dev), B, N_max, Hkv, D, D_max,
+        _arg(new_len, i32, (B,), "new_len", dev), _arg(moved, i32, (B,), "moved", dev),
+        _arg(status, i32, None, "status", dev), _stream(None))
+    _check(rc, "kv_commit_path_q4")
+    return new_len, moved
+
+
+def tree_attn_q4_workspace_bytes(B, N_max, Hq, Hkv, D, max_slots) -> int:
+    return int(lib.tsd_tree_attn_q4_workspace_bytes(B, N_max, Hq, Hkv, D, max_slots))
+
+
+@_on_stream
+def tree_attn_fwd_q4(q, k_cache, v_cache, block_table, prefix_len, n_nodes, mask, err, max_slots,
+                     scale=None, out=None, lse=None, want_lse=True, workspace=None, status=None):
+    """tree_attn_fwd over a 4-bit pool, uint8 [num_blocks][Hkv][9 * D].  mask
+    None: node i sees nodes 0..i (a chain, or one token).  Returns (out bf16
+    [B][N_max][Hq][D], lse float32 [B][N_max][Hq] or None)."""
+    num_blocks, Hkv, D = _q4_dims(k_cache, v_cache)
+    if q.dim() != 4 or q.shape[3] != D or k_cache.dim() != 3 or block_table.dim() != 2:
+        raise TsdError("q must be [B][N_max][Hq][D] with the pool's D, the pool one layer's, "
+                       "block_table [B][max_blocks]")
+    B, N_max, Hq, _ = q.shape
+    i32 = torch.int32
+    dev = _device_of(q)
+    max_blocks = block_table.shape[1]
+    max_slots = int(max_slots)
+    if out is None:
+        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    if lse is None and want_lse:
+        lse = torch.empty((B, N_max, Hq), dtype=torch.float32, device=q.device)
+    ws, ws_bytes, keep = _workspace_arg(
+        workspace, lib.tsd_tree_attn_q4_workspace_bytes(B, N_max, Hq, Hkv, D, max_slots), q, dev)
+    rc = lib.tsd_tree_attn_fwd_q4(
+        _arg(q, torch.bfloat16, None, "q", dev), _arg(k_cache, torch.uint8, None, "k_cache", dev),
+        _arg(v_cache, torch.uint8, None, "v_cache", dev),
+        _arg(block_table, i32, (B, max_blocks), "block_table", dev), max_blocks, num_blocks,
+        _arg(prefix_len, i32, (B,), "prefix_len", dev), _arg(n_nodes, i32, (B,), "n_nodes", dev),
+        _arg(mask, i32, (B, N_max, (N_max + 31) // 32), "mask", dev), _arg(err, i32, (B,), "err", dev), B,
+        N_max, Hq, Hkv, D, max_slots, D ** -0.5 if scale is None else float(scale),
+        _arg(out, torch.bfloat16, q.shape, "out", dev),
+        _arg(lse, torch.float32, (B, N_max, Hq), "lse", dev), ws, ws_bytes,
+        _arg(status, i32, None, "status", dev), _stream(None))
+    _check(rc, "tree_attn_fwd_q4")
+    return out, lse
+
+
+def _logits_kind(logits):
+    if logits.dtype == torch.float32:
+        return 0
+    if logits.dtype == torch.bfloat16:
+        return 1
+    raise TsdError("logits must be float32 or bfloat16, got %s" % logits.dtype)
+
+
+def _logprob_outputs(shape, k, like):
+    f32, i32 = dict(dtype=torch.float32, device=like.device), dict(dtype=torch.int32, device=like.device)
+    return (torch.empty(shape, **f32), torch.empty(shape, **f32), torch.empty(shape + (k,), **i32),
+            torch.empty(shape + (k,), **f32))
+
+
+@_on_stream
+def token_logprobs(logits, tokens, rows=None, k=0, status=None):
+    """Log probability of tokens int32 [R] under rows of logits [num_rows][V]
+    (float32 or bfloat16): row rows[r] (int32 [R], -1: none), or r.  Returns
+    (logprob [R], entropy [R], top_ids int32 [R][k], top_logprobs [R][k])."""
+    bf16 = _logits_kind(logits)
+    if logits.dim() != 2 or tokens.dim() != 1:
+        raise TsdError("logits must be [num_rows][V] and tokens [R]")
+    num_rows, V = logits.shape
+    R = tokens.shape[0]
+    dev = _device_of(logits)
+    lp, ent, ids, top = _logprob_outputs((R,), max(k, 0), logits)
+    rc = lib.tsd_token_logprobs(_arg(logits, logits.dtype, None, "logits", dev), bf16,
+                                _arg(tokens, torch.int32, None, "tokens", dev),
+                                _arg(rows, torch.int32, (R,), "rows", dev), R, num_rows, V, k, lp.data_ptr(),
+                                ent.data_ptr(), ids.data_ptr(), top.data_ptr(),
+                                _arg(status, torch.int32, None, "status", dev), _stream(None))
+    _check(rc, "token_logprobs")
+    return lp, ent, ids, top
+
+
+@_on_stream
+def tree_path_logprobs(logits, tokens, path, accept_len, bonus, err, D_max, k=0, status=None):
+    """The tokens a verify step emits (from the outputs of tree_verify_greedy
+    or tree_verify_stochastic) and their log probabilities under the path's
+    rows of logits [B][N_max][V] (float32 or bfloat16).  Returns (emitted int32
+    [B][D_max+1], logprob, entropy [B][D_max+1], top_ids int32, top_logprobs
+    [B][D_max+1][k])."""
+    bf16 = _logits_kind(logits)
+    if logits.dim() != 3:
+        raise TsdError("logits must be [B][N_max][V]")
+    B, N_max, V = logits.shape
+    i32 = torch.int32
+    dev = _device_of(logits)
+    lp, ent, ids, top = _logprob_outputs((B, D_max + 1), max(k, 0), logits)
+    emitted = torch.empty((B, D_max + 1), dtype=i32, device=logits.device)
+    rc = lib.tsd_tree_path_logprobs(
+        _arg(logits, logits.dtype, None, "logits", dev), bf16, _arg(tokens, i32, (B, N_max), "tokens", dev),
+        _arg(path, i32, (B, D_max + 1), "path", dev), _arg(accept_len, i32, (B,), "accept_len", dev),
+        _arg(bonus, i32, (B,), "bonus", dev), _arg(err, i32, (B,), "err", dev), B, N_max, V, D_max, k,
+        emitted.data_ptr(), lp.data_ptr(), ent.data_ptr(), ids.data_ptr(), top.data_ptr(),
+        _arg(status, i32, None, "status", dev), _stream(None))
+    _check(rc, "tree_path_logprobs")
+    return emitted, lp, ent, ids, top
 
 
 def set_option(key: int, value: int) -> None:

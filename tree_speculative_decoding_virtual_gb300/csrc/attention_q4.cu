@@ -1,0 +1,660 @@
+// Tree-masked attention over the 4-bit paged cache (format: q4.cuh), for one
+// query token per sequence as well as for draft trees.
+//
+// "EAGLE-Pangu: Accelerator-Safe Tree Speculative Decoding on Ascend NPUs",
+// technical summary 2.3: every node of the tree attends, in one pass, to the
+// committed prefix and to its own ancestor path; the rows of a kv head are
+// node-major (row = node * g + head-in-group), so a GQA group shares K and V.
+//
+// Few rows (tree_attn_q4_rows): the kernel is bound by the cache's bytes (9 D
+// a page, a quarter of bf16), so K and V go from the page to the tensor
+// core's operand registers without a second pass through shared memory.  A
+// warp owns whole pages: one lane fetches a page's K and V with two bulk
+// copies into the warp's ring, and the warp computes, for 8 rows at a time,
+//   S^T (16 keys x 8 rows) = K Q^T      A = K, decoded in registers
+//   P^T = exp2(S^T * c - m)             fp32, packed to fp16, transposed in
+//                                       registers by movmatrix
+//   O^T (D x 8 rows) += V^T P^T         A = V^T, decoded in registers
+// with fp16 operands and fp32 accumulation (m16n8k16).  Decoded values are
+// exact in fp16.  q (bf16) is scaled per row by a power of two that brings
+// its largest magnitude to [2^13, 2^14) and then converted: exact for every
+// element within 2^-27 of that magnitude, below which the rounding (2^-25 of
+// fp16's smallest normal) is lost in the fp32 accumulation anyway; the power
+// goes into the softmax's factor.  P lies in (0, 2^15] (the reference m is 8
+// above the row's first maximum and follows when a score passes it by 7), so
+// fp16 keeps 11 bits of every probability down to 2^-22 of the largest, 3
+// bits more than bf16 would; the row sum uses the unrounded fp32 values.
+//
+// Operand layout.  The contraction index of an MMA may be permuted freely, so
+// lane (i, t) = (lane / 4, lane % 4) takes, as A rows i and i + 8 of K, D/4
+// consecutive columns of two keys (one 16-byte read for D = 128), and of V
+// the D/8 consecutive columns from i D/8 on of four keys.  The order of a
+// page's keys over the A rows (i ^ (i >> 1 & 1)) makes the K reads free of
+// bank conflicts and the V reads two-way.
+//
+// Splits of the key range are merged by a second kernel in fp32.
+
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "attention_q4.cuh"
+#include "sm100_ptx.cuh"
+
+namespace tsd {
+namespace {
+
+constexpr int kRowsThreads = 256;
+constexpr int kRowsWarps = kRowsThreads / 32;
+constexpr int kRowsStages = 4;  // pages in flight per warp
+constexpr float kOffset = 8.f;  // P of the reference score is 2^8
+constexpr float kSlack = 7.f;   // P stays at or below 2^15
+constexpr float kRowsLn2 = 0.6931471805599453f;
+constexpr uint64_t kRowsDrainNs = 100000000ull;
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9},"
+      " {%0,%1,%2,%3};\n"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+template <int N>
+__device__ __forceinline__ void lds_words(const uint8_t *p, uint32_t (&w)[N]) {
+  if constexpr (N == 4) {
+    const uint4 x = *reinterpret_cast<const uint4 *>(p);
+    w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+  } else if constexpr (N == 2) {
+    const uint2 x = *reinterpret_cast<const uint2 *>(p);
+    w[0] = x.x; w[1] = x.y;
+  } else {
+    w[0] = *reinterpret_cast<const uint32_t *>(p);
+  }
+}
+
+// Power of two that brings amax to [2^13, 2^14); 1 for zero, inf or NaN.
+__device__ __forceinline__ int q_exponent(float amax) {
+  if (!(amax > 0.f) || !isfinite(amax)) return 0;
+  return 13 - (((int)(__float_as_uint(amax) >> 23) & 0xFF) - 127);
+}
+
+template <int D, int NT>
+struct RowsLayout {
+  static constexpr int kPageBytes = Q4Page<D>::kBytes;
+  static constexpr int kStage = 2 * kPageBytes;
+  static constexpr int kRing = kRowsWarps * kRowsStages * kStage;
+  static constexpr int kMerge = kRowsWarps * 8 * NT * D * 4;  // O of every warp
+  static constexpr int kBytes = kRing > kMerge ? kRing : kMerge;
+  static_assert(kStage % 16 == 0, "bulk copies start on 16 bytes");
+};
+
+struct RowsShared {
+  uint64_t full[kRowsWarps][kRowsStages];
+  float2 ml[kRowsWarps][16];  // (reference, sum) of each warp's rows
+  int bad, timeout;
+};
+
+// Grid (splits * row blocks * Hkv, B).  A block owns 8 NT rows of one kv head
+// and one piece of the key range; its warps take the piece's pages in turn.
+template <int D, int NT>
+__global__ void __launch_bounds__(kRowsThreads, 2) tree_attn_q4_rows_kernel(const Q4Attn p) {
+  using namespace sm100;
+  using L = RowsLayout<D, NT>;
+  using Page = Q4Page<D>;
+  constexpr int kSteps = D / 16;      // contraction steps of S
+  constexpr int kWordsK = D / 32;     // code words of a lane's part of a key
+  constexpr int kWordsV = D / 64;     // code words of a lane's part of a V row
+  constexpr int kTiles = D / 16;      // M tiles of O^T
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ RowsShared sh;
+  pdl_trigger();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int qi = lane >> 2, qt = lane & 3;  // (i, t)
+  const int split = blockIdx.x % p.splits, hr = blockIdx.x / p.splits;
+  const int h = hr / p.row_blocks, rb = hr % p.row_blocks;
+  const int b = blockIdx.y;
+  if (tid == 0) {
+    for (int w = 0; w < kRowsWarps; ++w)
+      for (int s = 0; s < kRowsStages; ++s) mbar_init(smem_addr(&sh.full[w][s]), 1);
+    fence_mbar_init();
+    sh.bad = 0;
+    sh.timeout = 0;
+  }
+  __syncthreads();
+  pdl_wait();
+  const int row0 = rb * 8 * NT;
+  int P, nb;
+  bool bad_len;
+  const bool ok = q4_seq(p, b, P, nb, bad_len);
+  if (bad_len && blockIdx.x == 0 && tid == 0 && p.status)
+    atomicOr(p.status, TSD_STATUS_BAD_LEN);
+  const int rows_valid = ok ? nb * p.g : 0;
+  const int pages = ok ? (P + nb + kPage - 1) / kPage : 0;
+  const int first = split * p.chunk, last = min(pages, first + p.chunk);
+  const bool work = row0 < rows_valid && first < last;
+  if (!work && p.splits > 1) return;
+
+  float o[NT][kTiles][4];
+  float l[NT][2], trig[NT][2], ref[NT][2], mul[NT][2];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+#pragma unroll
+    for (int j = 0; j < kTiles; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[n][j][e] = 0.f;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      l[n][e] = 0.f;
+      trig[n][e] = -INFINITY;  // the score that moves the reference
+      ref[n][e] = 0.f;
+      mul[n][e] = 0.f;
+    }
+  }
+
+  if (work) {
+    // ---- the page stream: lane 0 fetches, every lane knows the ids ----
+    const int32_t *trow = p.table + (size_t)b * p.max_blocks;
+    const int mine = last - first > warp ? (last - first - warp + kRowsWarps - 1) / kRowsWarps : 0;
+    const uint32_t ring = smem_addr(smem) + warp * kRowsStages * L::kStage;
+    const uint8_t *ring_p = smem + warp * kRowsStages * L::kStage;
+    int ids = 0;  // lane i: the id of this warp's page 32 * batch + i
+    bool stop = false;
+    auto fetch_ids = [&](int it) {
+      const int j = it + lane;
+      const int id = j < mine ? trow[first + warp + j * kRowsWarps] : 0;
+      const bool bad = id < 0 || id >= p.num_blocks;
+      if (__any_sync(0xffffffffu, bad)) {
+        stop = true;
+        if (lane == 0) sh.bad = 1;
+      }
+      ids = id;
+    };
+    auto issue = [&](int it) {
+      const int id = __shfl_sync(0xffffffffu, ids, it & 31);
+      if (lane == 0) {
+        const uint32_t bar = smem_addr(&sh.full[warp][it % kRowsStages]);
+        const uint32_t dst = ring + (it % kRowsStages) * L::kStage;
+        const size_t off = ((size_t)id * p.Hkv + h) * L::kPageBytes;
+        mbar_arrive_expect_tx(bar, L::kStage);
+        bulk_load(dst, p.k + off, L::kPageBytes, bar);
+        bulk_load(dst + L::kPageBytes, p.v + off, L::kPageBytes, bar);
+      }
+    };
+    if (mine > 0) fetch_ids(0);
+    int issued = 0;
+    for (; !stop && issued < min(mine, kRowsStages); ++issued) issue(issued);
+
+    // ---- Q^T as B operands: row i of each 8-row tile ----
+    uint32_t qf[NT][kSteps][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int r = row0 + 8 * n + qi;
+      uint32_t raw[D / 8];  // D/4 bf16 columns from qt * D/4 on
+      if (r < rows_valid) {
+        const uint4 *src = reinterpret_cast<const uint4 *>(p.q + q4_out_row(p, b, h, r) * D + qt * (D / 4));
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          const uint4 x = src[c];
+          raw[4 * c] = x.x; raw[4 * c + 1] = x.y; raw[4 * c + 2] = x.z; raw[4 * c + 3] = x.w;
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) raw[c] = 0u;
+      }
+      float amax = 0.f;
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) {
+        amax = fmaxf(amax, fabsf(__uint_as_float(raw[c] << 16)));
+        amax = fmaxf(amax, fabsf(__uint_as_float(raw[c] & 0xFFFF0000u)));
+      }
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+      const int e = q_exponent(amax);
+      // 2^e in two factors: e reaches 139 for the smallest q
+      const float up1 = __uint_as_float((uint32_t)(127 + e / 2) << 23);
+      const float up2 = __uint_as_float((uint32_t)(127 + e - e / 2) << 23);
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) {
+        const float lo = __uint_as_float(raw[c] << 16) * up1 * up2;
+        const float hi = __uint_as_float(raw[c] & 0xFFFF0000u) * up1 * up2;
+        // columns 4 s + {0, 1} feed b0 of step s, 4 s + {2, 3} its b1
+        qf[n][c / 2][c & 1] = pack_half2(lo, hi);
+      }
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {  // this lane's score columns are rows 2 t and 2 t + 1
+        const int er = __shfl_sync(0xffffffffu, e, (2 * qt + s) * 4);
+        mul[n][s] = p.scale_log2 * __uint_as_float((uint32_t)(127 - er / 2) << 23) *
+                    __uint_as_float((uint32_t)(127 - (er - er / 2)) << 23);
+      }
+    }
+
+    const int key_a = qi ^ ((qi >> 1) & 1);  // A row i; row i + 8 is key_a + 8
+    // V's contraction indices 2t, 2t+1, 2t+8, 2t+9 are A rows 2t, 2t+1, ...
+    const int kv0 = (2 * qt) ^ (qt & 1), kv1 = (2 * qt + 1) ^ (qt & 1);
+
+    for (int it = 0; it < mine && !stop; ++it) {
+      const int st = it % kRowsStages;
+      if (!mbar_wait(smem_addr(&sh.full[warp][st]), (it / kRowsStages) & 1, p.wait_limit_ns)) {
+        if (lane == 0) sh.timeout = 1;
+        stop = true;
+      }
+      if (__any_sync(0xffffffffu, stop)) {
+        stop = true;
+        break;
+      }
+      const uint8_t *kp = ring_p + st * L::kStage, *vp = kp + L::kPageBytes;
+      const int t0 = (first + warp + it * kRowsWarps) * kPage;  // first key slot
+
+      // S^T
+      float s[NT][4];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+      uint32_t wa[kWordsK], wb[kWordsK];
+      lds_words(kp + key_a * Page::kRow + qt * (D / 8), wa);
+      lds_words(kp + (key_a + 8) * Page::kRow + qt * (D / 8), wb);
+      uint32_t sa[2], sb[2];  // scales of the lane's (one or two) groups of 16 columns
+      if constexpr (D == 128) {
+        const uint32_t xa = *reinterpret_cast<const uint16_t *>(kp + Page::kScales + key_a * 8 + 2 * qt);
+        const uint32_t xb =
+            *reinterpret_cast<const uint16_t *>(kp + Page::kScales + (key_a + 8) * 8 + 2 * qt);
+        sa[0] = q4_scale2(xa & 0xFFu);
+        sa[1] = q4_scale2(xa >> 8);
+        sb[0] = q4_scale2(xb & 0xFFu);
+        sb[1] = q4_scale2(xb >> 8);
+      } else {
+        sa[0] = sa[1] = q4_scale2(kp[Page::kScales + key_a * 4 + qt]);
+        sb[0] = sb[1] = q4_scale2(kp[Page::kScales + (key_a + 8) * 4 + qt]);
+      }
+#pragma unroll
+      for (int w = 0; w < kWordsK; ++w) {
+        uint32_t ra[4], rb4[4];
+        q4_decode8(wa[w], ra);
+        q4_decode8(wb[w], rb4);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          ra[e] = q4_mul2(ra[e], sa[w / 2]);
+          rb4[e] = q4_mul2(rb4[e], sb[w / 2]);
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          mma_f16(s[n], ra[0], rb4[0], ra[1], rb4[1], qf[n][2 * w][0], qf[n][2 * w][1]);
+          mma_f16(s[n], ra[2], rb4[2], ra[3], rb4[3], qf[n][2 * w + 1][0], qf[n][2 * w + 1][1]);
+        }
+      }
+
+      // V's codes and scales; slots past the sequence read as zero
+      uint32_t wv[4][kWordsV], sv[4];
+      const int kk[4] = {kv0, kv1, kv0 + 8, kv1 + 8};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        lds_words(vp + kk[e] * Page::kRow + qi * (D / 16), wv[e]);
+        sv[e] = q4_scale2(vp[Page::kScales + kk[e] * Page::kScaleRow + qi * (D / 8) / kQ4Group]);
+      }
+      // the page is in registers: its stage can be refilled
+      __syncwarp();
+      if (issued < mine) {
+        if ((issued & 31) == 0) fetch_ids(issued);
+        if (!stop) issue(issued++);
+      }
+
+      // softmax: t = s * mul, and what the row may not see is -inf
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        s[n][0] *= mul[n][0];
+        s[n][1] *= mul[n][1];
+        s[n][2] *= mul[n][0];
+        s[n][3] *= mul[n][1];
+      }
+      if (t0 + kPage > P) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int r = row0 + 8 * n + 2 * qt + e;
+            const uint32_t vis = r < rows_valid ? q4_visible(p, b, r / p.g, t0 - P, nb) : 0u;
+            if (!((vis >> key_a) & 1u)) s[n][e] = -INFINITY;
+            if (!((vis >> (key_a + 8)) & 1u)) s[n][2 + e] = -INFINITY;
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (t0 + kk[e] >= P + nb) sv[e] = 0u;
+      }
+      bool over = false;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) over = over || fmaxf(s[n][e], s[n][2 + e]) > trig[n][e];
+      if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float m = fmaxf(s[n][e], s[n][2 + e]);
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+            if (m > trig[n][e]) {  // the same decision in the eight lanes of the row
+              const float f = trig[n][e] == -INFINITY ? 0.f : ex2_approx(ref[n][e] - (m - kOffset));
+              trig[n][e] = m + kSlack;
+              ref[n][e] = m - kOffset;
+              l[n][e] *= f;
+#pragma unroll
+              for (int j = 0; j < kTiles; ++j) {
+                o[n][j][e] *= f;
+                o[n][j][2 + e] *= f;
+              }
+            }
+          }
+        }
+      }
+      uint32_t pb[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const float p0 = ex2_approx(s[n][0] - ref[n][0]), p1 = ex2_approx(s[n][1] - ref[n][1]);
+        const float p2 = ex2_approx(s[n][2] - ref[n][0]), p3 = ex2_approx(s[n][3] - ref[n][1]);
+        l[n][0] += p0 + p2;
+        l[n][1] += p1 + p3;
+        pb[n][0] = transpose8x8(pack_half2(p0, p1));
+        pb[n][1] = transpose8x8(pack_half2(p2, p3));
+      }
+
+      // O^T: M tile j holds columns i D/8 + 2 j (row i) and the next (row i + 8)
+#pragma unroll
+      for (int w = 0; w < kWordsV; ++w) {
+        uint32_t rv[4][4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          q4_decode8(wv[e][w], rv[e]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) rv[e][j] = q4_mul2(rv[e][j], sv[e]);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t a0 = __byte_perm(rv[0][j], rv[1][j], 0x5410);
+          const uint32_t a1 = __byte_perm(rv[0][j], rv[1][j], 0x7632);
+          const uint32_t a2 = __byte_perm(rv[2][j], rv[3][j], 0x5410);
+          const uint32_t a3 = __byte_perm(rv[2][j], rv[3][j], 0x7632);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) mma_f16(o[n][4 * w + j], a0, a1, a2, a3, pb[n][0], pb[n][1]);
+        }
+      }
+    }
+    if (stop) {  // copies in flight land before the block's memory is reused
+      if (lane == 0)
+        for (int it = max(0, issued - kRowsStages); it < issued; ++it)
+          mbar_wait(smem_addr(&sh.full[warp][it % kRowsStages]), (it / kRowsStages) & 1, kRowsDrainNs);
+      __syncwarp();
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 4);
+        l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 8);
+        l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 16);
+      }
+  }
+
+  // ---- join the warps: every ring is drained, its memory holds their O ----
+  __syncthreads();
+  float *merge = reinterpret_cast<float *>(smem);
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int r = 8 * n + 2 * qt + e;
+      if (qi == 0)
+        sh.ml[warp][r] = make_float2(trig[n][e] == -INFINITY && l[n][e] == 0.f ? -INFINITY : ref[n][e], l[n][e]);
+      float *dst = merge + ((size_t)warp * 8 * NT + r) * D + qi * (D / 8);
+#pragma unroll
+      for (int j = 0; j < kTiles; j += 2)
+        *reinterpret_cast<float4 *>(dst + 2 * j) =
+            make_float4(o[n][j][e], o[n][j][2 + e], o[n][j + 1][e], o[n][j + 1][2 + e]);
+    }
+  }
+  __syncthreads();
+  const bool bad = sh.bad != 0;
+  if (tid == 0 && p.status) {
+    if (bad) atomicOr(p.status, TSD_STATUS_BAD_PAGE);
+    if (sh.timeout) atomicOr(p.status, TSD_STATUS_TIMEOUT);
+  }
+  constexpr int kVec = D / 4;  // float4 of a row
+  for (int x = tid; x < 8 * NT * kVec; x += kRowsThreads) {
+    const int rl = x / kVec, c = x % kVec, r = row0 + rl;
+    if (r >= p.rows) break;
+    float M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kRowsWarps; ++w) M = fmaxf(M, sh.ml[w][rl].x);
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    float sum = 0.f;
+    if (M > -INFINITY) {
+#pragma unroll
+      for (int w = 0; w < kRowsWarps; ++w) {
+        const float2 ml = sh.ml[w][rl];
+        const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - M);
+        const float4 v = *reinterpret_cast<const float4 *>(merge + ((size_t)w * 8 * NT + rl) * D + 4 * c);
+        a.x += f * v.x;
+        a.y += f * v.y;
+        a.z += f * v.z;
+        a.w += f * v.w;
+        sum += f * ml.y;
+      }
+    }
+    if (p.splits > 1) {
+      if (r >= rows_valid) continue;
+      const size_t pr = (((size_t)b * p.Hkv + h) * p.splits + split) * p.rows + r;
+      *reinterpret_cast<float4 *>(p.part_o + pr * D + 4 * c) = a;
+      if (c == 0) p.part_ml[pr] = make_float2(M, bad ? -1.f : sum);
+    } else {
+      const size_t orow = q4_out_row(p, b, h, r);
+      const bool empty = r >= rows_valid || bad || sum == 0.f;
+      const float inv = empty ? 0.f : 1.f / sum;
+      *reinterpret_cast<uint2 *>(p.out + orow * D + 4 * c) =
+          empty ? make_uint2(0u, 0u)
+                : make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
+      if (c == 0 && p.lse) p.lse[orow] = empty ? -INFINITY : (M + log2f(sum)) * kRowsLn2;
+    }
+  }
+}
+
+// One warp per output row: joins the pieces of its key range (fp32), rounds
+// once to bf16.  Rows of skipped sequences and padding nodes become 0 / -inf.
+template <int D>
+__global__ void __launch_bounds__(256) tree_attn_q4_join_kernel(const Q4Attn p) {
+  using namespace sm100;
+  constexpr int kPer = D / 32;  // columns of a lane
+  pdl_trigger();
+  pdl_wait();
+  const int64_t x = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (x >= (int64_t)p.B * p.Hkv * p.rows) return;
+  const int r = (int)(x % p.rows);
+  const int64_t bh = x / p.rows;
+  const int h = (int)(bh % p.Hkv), b = (int)(bh / p.Hkv);
+  int P, nb;
+  bool bad_len;
+  const bool ok = q4_seq(p, b, P, nb, bad_len) && r < nb * p.g;
+  const int pieces = ok ? ((P + nb + kPage - 1) / kPage + p.chunk - 1) / p.chunk : 0;
+  const size_t base = (size_t)bh * p.splits * p.rows + r;
+  // lane l holds the (reference, sum) of pieces l, l + 32, ...: at most 64
+  float2 ml[2] = {make_float2(-INFINITY, 0.f), make_float2(-INFINITY, 0.f)};
+#pragma unroll
+  for (int e = 0; e < 2; ++e)
+    if (lane + 32 * e < pieces) ml[e] = p.part_ml[base + (size_t)(lane + 32 * e) * p.rows];
+  const bool bad = __any_sync(0xffffffffu, ml[0].y == -1.f || ml[1].y == -1.f);
+  float M = fmaxf(ml[0].x, ml[1].x);
+#pragma unroll
+  for (int off = 16; off; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+  float f[2], sum = 0.f;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    f[e] = ml[e].x == -INFINITY ? 0.f : ex2_approx(ml[e].x - M);
+    sum += f[e] * ml[e].y;
+  }
+#pragma unroll
+  for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+  const bool empty = !ok || bad || sum == 0.f;
+  float a[kPer];
+#pragma unroll
+  for (int c = 0; c < kPer; ++c) a[c] = 0.f;
+  for (int s = 0; s < pieces; ++s) {
+    const float fs = __shfl_sync(0xffffffffu, s < 32 ? f[0] : f[1], s & 31);
+    const float *src = p.part_o + (base + (size_t)s * p.rows) * D + lane * kPer;
+    if constexpr (kPer == 4) {
+      const float4 v = *reinterpret_cast<const float4 *>(src);
+      a[0] += fs * v.x;
+      a[1] += fs * v.y;
+      a[2] += fs * v.z;
+      a[3] += fs * v.w;
+    } else {
+      const float2 v = *reinterpret_cast<const float2 *>(src);
+      a[0] += fs * v.x;
+      a[1] += fs * v.y;
+    }
+  }
+  const float inv = empty ? 0.f : 1.f / sum;
+  const size_t orow = q4_out_row(p, b, h, r);
+  uint32_t w[kPer / 2];
+#pragma unroll
+  for (int c = 0; c < kPer / 2; ++c) w[c] = empty ? 0u : pack_bf16x2(a[2 * c] * inv, a[2 * c + 1] * inv);
+  uint16_t *dst = p.out + orow * D + lane * kPer;
+  if constexpr (kPer == 4)
+    *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
+  else
+    *reinterpret_cast<uint32_t *>(dst) = w[0];
+  if (lane == 0 && p.lse) p.lse[orow] = empty ? -INFINITY : (M + log2f(sum)) * kRowsLn2;
+}
+
+constexpr int kQ4MaxSplits = 64;
+
+struct Q4Plan {
+  int nt, row_blocks, splits, chunk;
+  size_t ml_off, bytes;
+};
+
+// Host: how a call is cut up.
+Q4Plan q4_plan(int B, int N_max, int Hq, int Hkv, int D, int max_slots) {
+  Q4Plan pl;
+  const int rows = N_max * (Hq / Hkv);
+  pl.nt = rows > 8 ? 2 : 1;
+  pl.row_blocks = (rows + 8 * pl.nt - 1) / (8 * pl.nt);
+  const int pages = (max_slots + kPage - 1) / kPage;
+  const int64_t base = (int64_t)B * Hkv * pl.row_blocks;
+  const int64_t slots = 2ll * sm_count();
+  int64_t want = (4 * slots + base - 1) / base;  // pieces for four blocks per block slot
+  want = std::min<int64_t>(want, (pages + 2 * kRowsWarps - 1) / (2 * kRowsWarps));
+  want = std::max<int64_t>(1, std::min<int64_t>(want, kQ4MaxSplits));
+  pl.chunk = (int)((pages + want - 1) / want);
+  pl.splits = (pages + pl.chunk - 1) / pl.chunk;
+  const size_t n = (size_t)B * Hkv * pl.splits * rows;
+  pl.ml_off = align_up(n * D * 4, 256);
+  pl.bytes = pl.splits > 1 ? pl.ml_off + n * 8 : 0;
+  return pl;
+}
+
+template <int D, int NT>
+cudaError_t rows_launch(const Q4Attn &p, cudaStream_t s) {
+  const int smem = RowsLayout<D, NT>::kBytes;
+  if (!set_smem((const void *)tree_attn_q4_rows_kernel<D, NT>, smem)) return cudaErrorUnknown;
+  return launch(tree_attn_q4_rows_kernel<D, NT>, dim3((unsigned)p.splits * p.Hkv * p.row_blocks, p.B),
+                dim3(kRowsThreads), smem, s, p);
+}
+
+int q4_check(int B, int N_max, int Hq, int Hkv, int D, int max_slots) {
+  if (B < 0 || N_max < 1 || Hq < 1 || Hkv < 1 || max_slots < 1) return TSD_ERR_ARG;
+  if (D != 64 && D != 128) return TSD_ERR_LIMIT;
+  if (N_max > kMaxNodes || Hq % Hkv != 0 || Hq / Hkv > 16 || B > 65535 || Hkv > 65535 ||
+      max_slots > 262144)
+    return TSD_ERR_LIMIT;
+  return TSD_OK;
+}
+
+}  // namespace
+}  // namespace tsd
+
+TSD_API size_t tsd_tree_attn_q4_workspace_bytes(int B, int N_max, int Hq, int Hkv, int D,
+                                                int max_slots) {
+  using namespace tsd;
+  if (B == 0 || q4_check(B, N_max, Hq, Hkv, D, max_slots) != TSD_OK) return 0;
+  return q4_plan(B, N_max, Hq, Hkv, D, max_slots).bytes;
+}
+
+TSD_API int tsd_tree_attn_fwd_q4(const uint16_t *q, const uint8_t *k_cache, const uint8_t *v_cache,
+                                 const int32_t *block_table, int max_blocks, int num_blocks,
+                                 const int32_t *prefix_len, const int32_t *n_nodes,
+                                 const uint32_t *mask, const int32_t *err, int B, int N_max, int Hq,
+                                 int Hkv, int D, int max_slots, float scale, uint16_t *out, float *lse,
+                                 void *workspace, size_t ws_bytes, int32_t *status,
+                                 tsd_stream_t stream) {
+  using namespace tsd;
+  const int rc = q4_check(B, N_max, Hq, Hkv, D, max_slots);
+  if (rc != TSD_OK) return rc;
+  if (max_blocks < 1 || num_blocks < 1 || !std::isfinite(scale)) return TSD_ERR_ARG;
+  if (B == 0) return TSD_OK;
+  if (!q || !k_cache || !v_cache || !block_table || !prefix_len || !out) return TSD_ERR_ARG;
+  if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16))
+    return TSD_ERR_ARG;
+  const Q4Plan pl = q4_plan(B, N_max, Hq, Hkv, D, max_slots);
+  if (pl.bytes > 0 && (!workspace || ws_bytes < pl.bytes)) return TSD_ERR_WORKSPACE;
+  if (pl.bytes > 0 && !aligned(workspace, 16)) return TSD_ERR_ARG;
+  Q4Attn p = {};
+  p.q = q;
+  p.k = k_cache;
+  p.v = v_cache;
+  p.table = block_table;
+  p.max_blocks = max_blocks;
+  p.num_blocks = num_blocks;
+  p.prefix_len = prefix_len;
+  p.n_nodes = n_nodes;
+  p.mask = mask;
+  p.err = err;
+  p.B = B;
+  p.N_max = N_max;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.g = Hq / Hkv;
+  p.W = (N_max + 31) / 32;
+  p.max_slots = max_slots;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.rows = N_max * p.g;
+  p.row_blocks = pl.row_blocks;
+  p.splits = pl.splits;
+  p.chunk = pl.chunk;
+  p.part_o = reinterpret_cast<float *>(workspace);
+  p.part_ml = pl.bytes ? reinterpret_cast<float2 *>(reinterpret_cast<char *>(workspace) + pl.ml_off) : nullptr;
+  p.out = out;
+  p.lse = lse;
+  p.status = status;
+  p.wait_limit_ns = (uint64_t)option(TSD_OPT_WAIT_LIMIT_NS);
+  const cudaStream_t s = as_cuda(stream);
+  cudaError_t e;
+  if (D == 128)
+    e = pl.nt == 2 ? rows_launch<128, 2>(p, s) : rows_launch<128, 1>(p, s);
+  else
+    e = pl.nt == 2 ? rows_launch<64, 2>(p, s) : rows_launch<64, 1>(p, s);
+  if (e != cudaSuccess) return TSD_ERR_CUDA;
+  if (pl.splits > 1) {
+    const int64_t rows = (int64_t)B * Hkv * p.rows;
+    const dim3 grid((unsigned)((rows + 7) / 8));
+    e = D == 128 ? launch(tree_attn_q4_join_kernel<128>, grid, dim3(256), 0, s, p)
+                 : launch(tree_attn_q4_join_kernel<64>, grid, dim3(256), 0, s, p);
+    if (e != cudaSuccess) return TSD_ERR_CUDA;
+  }
+  return TSD_OK;
+}
