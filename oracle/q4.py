@@ -127,15 +127,16 @@ def visible(mask, b, i, n, N_max):
 
 
 def tree_attention_q4(q_bits, k_pool, v_pool, block_table, prefix_len, n_nodes, mask, err, scale):
-    """fp64 attention over 4-bit pools.  Returns (out, lse, weight, score):
-    weight [B][N_max][Hq][D] = sum p |v| and score [B][N_max][Hq] = max over the
-    visible keys of sum |q| |k| |scale|, which scale the rounding bounds."""
+    """fp64 attention over 4-bit pools.  Returns (out, lse, weight, total,
+    score): weight [B][N_max][Hq][D] = sum p |v|, total [B][N_max][Hq][D] = sum
+    |v| over the visible keys and score [B][N_max][Hq] = max over the visible
+    keys of sum |q| |k| |scale|, which scale the rounding bounds."""
     B, N_max, Hq, D = q_bits.shape
     Hkv = k_pool.shape[1]
     g = Hq // Hkv
     q = bf16_to_f64(q_bits)
     out = np.zeros(q.shape)
-    weight = np.zeros(q.shape)
+    weight, total = np.zeros(q.shape), np.zeros(q.shape)
     lse = np.full(q.shape[:3], -np.inf)
     score = np.zeros(q.shape[:3])
     for b in range(B):
@@ -158,5 +159,6 @@ def tree_attention_q4(q_bits, k_pool, v_pool, block_table, prefix_len, n_nodes, 
                     p = p / p.sum()
                     out[b, i, h] = p @ vv
                     weight[b, i, h] = p @ np.abs(vv)
+                    total[b, i, h] = np.abs(vv).sum(0)
                     score[b, i, h] = (np.abs(kk) @ np.abs(q[b, i, h])).max() * abs(scale)
-    return out, lse, weight, score
+    return out, lse, weight, total, score

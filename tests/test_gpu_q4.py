@@ -11,10 +11,12 @@ Attention tolerance.  Every value of K and V is exact; what rounds is
   absolute change of lse by at most it;
 - ex2.approx, the scale's product and the fp32 row sums: together below
   2^-20 relative;
-- P to fp16: 2^-11 relative, or 2^-25 absolute below 2^-14, where P of the
-  reference score is 2^8: at most n 2^-33 of the row's sum over n keys;
+- P to fp16: 2^-11 relative, or 2^-25 absolute below 2^-14; the P of a row sum
+  to 2^8 or more (the reference score's alone is 2^8), so a key's probability
+  is off by at most 2^-33, and out by 2^-33 sum |v|;
 - out to bf16: 2^-8 relative.
-So |out - ref| <= 2^-8 |ref| + (2^-11 + 2^-19 + 2 D 2^-24 score) sum p|v|, and
+So |out - ref| <= 2^-8 |ref| + (2^-11 + 2^-19 + 2 D 2^-24 score) sum p|v| +
+2^-33 sum |v| (times 1 + 2^-8 for the rounding of what is off), and
 |lse - ref| <= D 2^-24 score + 2^-19 + 2^-22 |ref|, with score the largest sum
 |q||k| |scale| of the row's keys.
 """
@@ -283,9 +285,10 @@ def _run(tsd, x, mask="tree", max_slots=None, status=None, **kw):
 
 
 def _check(x, got, lse, ref):
-    r_out, r_lse, weight, score = ref
+    r_out, r_lse, weight, total, score = ref
     D = x["D"]
-    tol = 2.0 ** -8 * np.abs(r_out) + (2.0 ** -11 + 2.0 ** -19 + 2 * D * 2.0 ** -24 * score[..., None]) * weight
+    off = (2.0 ** -11 + 2.0 ** -19 + 2 * D * 2.0 ** -24 * score[..., None]) * weight + 2.0 ** -33 * total
+    tol = 2.0 ** -8 * np.abs(r_out) + (1 + 2.0 ** -8) * off
     seen = np.isfinite(r_lse)
     assert np.array_equal(seen, np.isfinite(lse)) and np.isneginf(lse[~seen]).all()
     assert (got[~seen] == 0).all()
@@ -332,6 +335,91 @@ def test_attention(tsd, B, N, Hq, Hkv, D, prefix, nodes):
     assert int(st.item()) == 0
     # a looser bound on the lengths cuts the keys differently
     got, lse = _run(tsd, x, max_slots=x["max_slots"] * 7 + 3000)
+    _check(x, got, lse, _ref(x))
+
+
+def _ref_on_gpu(x, chain=False):
+    """tree_attention_q4 for long sequences, fp64 on the GPU (torch)."""
+    import torch
+    q = bf(x["q"]).double()
+    B, N, Hq, D = q.shape
+    Hkv = x["k"].shape[1]
+    g = Hq // Hkv
+    out, weight, total = torch.zeros_like(q), torch.zeros_like(q), torch.zeros_like(q)
+    lse = torch.full((B, N, Hq), -np.inf, dtype=torch.float64, device="cuda")
+    score = torch.zeros_like(lse)
+    for b in range(B):
+        P, n = int(x["P"][b]), int(x["n"][b])
+        slots = [int(x["table"][b, t // 16]) * 16 + t % 16 for t in range(P + n)]
+        k, v = (T(oq4.read_rows(x[c], slots)) for c in "kv")
+        seen = np.ones((n, P + n), bool)
+        for i in range(n):
+            seen[i, P:] = oq4.visible(None if chain else x["mask"], b, i, n, N)
+        rows = q[b, :n].reshape(n, Hkv, g, D)
+        s = torch.einsum("ihgd,thd->hgit", rows, k) * x["scale"]
+        s = s.masked_fill(~T(seen), -np.inf)
+        z = torch.logsumexp(s, -1)
+        pr = torch.exp(s - z[..., None])
+        out[b, :n] = torch.einsum("hgit,thd->ihgd", pr, v).reshape(n, Hq, D)
+        weight[b, :n] = torch.einsum("hgit,thd->ihgd", pr, v.abs()).reshape(n, Hq, D)
+        total[b, :n] = torch.einsum("it,thd->ihd", T(seen).double(), v.abs()).repeat_interleave(g, 1)
+        lse[b, :n] = z.permute(2, 0, 1).reshape(n, Hq)
+        for h in range(Hkv):
+            top = torch.einsum("igd,td->igt", rows[:, h].abs(), k[:, h].abs()).amax(-1) * x["scale"]
+            score[b, :n, h * g:(h + 1) * g] = top
+    return tuple(t.cpu().numpy() for t in (out, lse, weight, total, score))
+
+
+def _long_inputs(seed, B, N, Hq, Hkv, D, prefix, nodes):
+    """_attn_inputs with whole pages of quantised values (fast for long
+    sequences)."""
+    rng = np.random.default_rng(seed)
+    x = _attn_inputs(seed, B, N, Hq, Hkv, D, [0] * B, nodes)
+    P, n = np.array(prefix, np.int32), np.array(nodes, np.int32)
+    need = (P + n + 15) // 16
+    ids = rng.permutation(int(need.sum()) + 3).astype(np.int32)
+    table = np.full((B, int(need.max())), -1, np.int32)
+    at = 0
+    for b in range(B):
+        table[b, :need[b]] = ids[at:at + need[b]]
+        at += need[b]
+    for name in "kv":
+        pool = np.zeros((len(ids), Hkv, 9 * D), np.uint8)
+        codes, scales = oq4.split_pages(pool)
+        codes[:], scales[:] = oq4.quantise_rows(gen.normal_bf16(rng, (len(ids), Hkv, 16, D)))
+        x[name] = pool
+    x.update(P=P, table=table, max_slots=int((P + n).max()))
+    return x
+
+
+@pytest.mark.parametrize("B,N,Hq,Hkv,D,prefix,nodes", [
+    (1, 1, 8, 1, 128, [20011], [1]),
+    (3, 1, 32, 8, 128, [9000, 17, 4100], [1, 1, 1]),
+    (64, 1, 16, 8, 64, list(range(3, 3 + 64 * 29, 29)), [1] * 64),
+    (20, 4, 16, 8, 128, list(range(1000, 1000 + 20 * 61, 61)), [4, 1] * 10),
+    (16, 31, 32, 8, 128, list(range(64, 64 + 16 * 190, 190)), [31, 17] * 8),
+    (2, 127, 64, 8, 128, [5000, 2047], [127, 126]),
+    (40, 33, 16, 4, 128, list(range(700, 700 + 40 * 37, 37)), [33, 9] * 20),
+    (12, 100, 24, 8, 64, list(range(300, 300 + 12 * 333, 333)), [100, 65] * 6),
+    (1, 256, 16, 1, 128, [12345], [255]),
+    (5, 256, 128, 8, 128, [900, 1, 2000, 127, 128], [256, 255, 129, 1, 128]),
+])
+def test_attention_long(tsd, B, N, Hq, Hkv, D, prefix, nodes):
+    x = _long_inputs(B + N, B, N, Hq, Hkv, D, prefix, nodes)
+    st = status_word()
+    got, lse = _run(tsd, x, status=st)
+    _check(x, got, lse, _ref_on_gpu(x))
+    assert int(st.item()) == 0
+    got, lse = _run(tsd, x, mask=None, max_slots=2 * x["max_slots"])
+    _check(x, got, lse, _ref_on_gpu(x, chain=True))
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.3, 1e-30, 3.0])
+@pytest.mark.parametrize("N", [1, 40])
+def test_attention_scale(tsd, N, scale):
+    x = _attn_inputs(3, 1, N, 2, 1, 128, [150], [N])
+    x["scale"] = scale
+    got, lse = _run(tsd, x)
     _check(x, got, lse, _ref(x))
 
 

@@ -57,7 +57,7 @@ def test_attention_without_a_tree_is_softmax():
     pool = q4.write_rows(np.zeros((3, 2, 9 * 64), np.uint8), gen.normal_bf16(rng, (48, 2, 64)), np.arange(48))
     q = gen.normal_bf16(rng, (1, 1, 2, 64))
     table = np.array([[2, 0, 1]], np.int32)
-    out, lse, _, _ = q4.tree_attention_q4(q, pool, pool, table, [36], None, None, None, 0.125)
+    out, lse, _, _, _ = q4.tree_attention_q4(q, pool, pool, table, [36], None, None, None, 0.125)
     rows = torch.from_numpy(q4.read_rows(pool, [32 + i for i in range(16)] + list(range(16)) + list(range(16, 21))))
     x = torch.einsum("hd,thd->ht", torch.from_numpy(bf16_to_f64(q))[0, 0], rows) * 0.125
     ref = torch.einsum("ht,thd->hd", torch.softmax(x, -1), rows)

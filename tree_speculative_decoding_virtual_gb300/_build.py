@@ -21,7 +21,7 @@ LIB = os.path.join(PKG, "libtsd.so")
 
 SOURCES = ["runtime.cu", "ancestors.cu", "attention.cu", "verify.cu", "verify_stochastic.cu",
            "commit.cu", "best_first.cu", "budget.cu", "slots.cu", "kv_q4.cu", "attention_q4.cu",
-           "logprobs.cu"]
+           "attention_q4_tc.cu", "logprobs.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden",
          "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]

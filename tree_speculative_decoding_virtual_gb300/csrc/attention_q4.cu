@@ -87,12 +87,6 @@ __device__ __forceinline__ void lds_words(const uint8_t *p, uint32_t (&w)[N]) {
   }
 }
 
-// Power of two that brings amax to [2^13, 2^14); 1 for zero, inf or NaN.
-__device__ __forceinline__ int q_exponent(float amax) {
-  if (!(amax > 0.f) || !isfinite(amax)) return 0;
-  return 13 - (((int)(__float_as_uint(amax) >> 23) & 0xFF) - 127);
-}
-
 template <int D, int NT>
 struct RowsLayout {
   static constexpr int kPageBytes = Q4Page<D>::kBytes;
@@ -224,10 +218,8 @@ __global__ void __launch_bounds__(kRowsThreads, 2) tree_attn_q4_rows_kernel(cons
       }
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-      const int e = q_exponent(amax);
-      // 2^e in two factors: e reaches 139 for the smallest q
-      const float up1 = __uint_as_float((uint32_t)(127 + e / 2) << 23);
-      const float up2 = __uint_as_float((uint32_t)(127 + e - e / 2) << 23);
+      const int e = q4_exponent(amax);
+      const float up1 = q4_pow2(e / 2), up2 = q4_pow2(e - e / 2);
 #pragma unroll
       for (int c = 0; c < D / 8; ++c) {
         const float lo = __uint_as_float(raw[c] << 16) * up1 * up2;
@@ -238,8 +230,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2) tree_attn_q4_rows_kernel(cons
 #pragma unroll
       for (int s = 0; s < 2; ++s) {  // this lane's score columns are rows 2 t and 2 t + 1
         const int er = __shfl_sync(0xffffffffu, e, (2 * qt + s) * 4);
-        mul[n][s] = p.scale_log2 * __uint_as_float((uint32_t)(127 - er / 2) << 23) *
-                    __uint_as_float((uint32_t)(127 - (er - er / 2)) << 23);
+        mul[n][s] = p.scale_log2 * q4_pow2(-(er / 2)) * q4_pow2(-(er - er / 2));
       }
     }
 
@@ -544,23 +535,49 @@ __global__ void __launch_bounds__(256) tree_attn_q4_join_kernel(const Q4Attn p) 
 constexpr int kQ4MaxSplits = 64;
 
 struct Q4Plan {
-  int nt, row_blocks, splits, chunk;
+  bool tc;  // the many-row kernel
+  int nt, rows_per_block, row_blocks, splits, chunk;
   size_t ml_off, bytes;
 };
+
+// Rows of a kv head from which the many-row kernel runs.
+constexpr int kTcMinRows = 33;
 
 // Host: how a call is cut up.
 Q4Plan q4_plan(int B, int N_max, int Hq, int Hkv, int D, int max_slots) {
   Q4Plan pl;
   const int rows = N_max * (Hq / Hkv);
-  pl.nt = rows > 8 ? 2 : 1;
-  pl.row_blocks = (rows + 8 * pl.nt - 1) / (8 * pl.nt);
   const int pages = (max_slots + kPage - 1) / kPage;
+  pl.tc = rows >= kTcMinRows;
+  pl.nt = rows > 8 ? 2 : 1;
+  pl.rows_per_block = pl.tc ? (rows > 128 ? 256 : 128) : 8 * pl.nt;
+  pl.row_blocks = (rows + pl.rows_per_block - 1) / pl.rows_per_block;
   const int64_t base = (int64_t)B * Hkv * pl.row_blocks;
-  const int64_t slots = 2ll * sm_count();
-  int64_t want = (4 * slots + base - 1) / base;  // pieces for four blocks per block slot
-  want = std::min<int64_t>(want, (pages + 2 * kRowsWarps - 1) / (2 * kRowsWarps));
-  want = std::max<int64_t>(1, std::min<int64_t>(want, kQ4MaxSplits));
-  pl.chunk = (int)((pages + want - 1) / want);
+  if (pl.tc) {
+    // waves x (tiles of a block + 4 for its set-up and epilogue), and with
+    // several pieces the fp32 partials' way through memory (a 128-key tile
+    // takes about 1.5 us, memory moves about 7.5 MB in that time)
+    const int tiles = (pages + 7) / 8;
+    double best = 1e300;
+    int best_per = tiles;
+    for (int s = 1; s <= kQ4MaxSplits && s <= tiles; ++s) {
+      const int per = (tiles + s - 1) / s;
+      const int64_t waves = (base * ((tiles + per - 1) / per) + sm_count() - 1) / sm_count();
+      double cost = (double)waves * (per + 4);
+      if (per < tiles) cost += 3 + 2.0 * B * Hkv * s * rows * D * 4 / 7.5e6;
+      if (cost < best) {
+        best = cost;
+        best_per = per;
+      }
+    }
+    pl.chunk = best_per * 8;
+  } else {
+    const int64_t slots = 2ll * sm_count();
+    int64_t want = (4 * slots + base - 1) / base;  // pieces for four blocks per block slot
+    want = std::min<int64_t>(want, (pages + 2 * kRowsWarps - 1) / (2 * kRowsWarps));
+    want = std::max<int64_t>(1, std::min<int64_t>(want, kQ4MaxSplits));
+    pl.chunk = (int)((pages + want - 1) / want);
+  }
   pl.splits = (pages + pl.chunk - 1) / pl.chunk;
   const size_t n = (size_t)B * Hkv * pl.splits * rows;
   pl.ml_off = align_up(n * D * 4, 256);
@@ -644,7 +661,9 @@ TSD_API int tsd_tree_attn_fwd_q4(const uint16_t *q, const uint8_t *k_cache, cons
   p.wait_limit_ns = (uint64_t)option(TSD_OPT_WAIT_LIMIT_NS);
   const cudaStream_t s = as_cuda(stream);
   cudaError_t e;
-  if (D == 128)
+  if (pl.tc)
+    e = q4_tc_launch(p, D, pl.rows_per_block, s);
+  else if (D == 128)
     e = pl.nt == 2 ? rows_launch<128, 2>(p, s) : rows_launch<128, 1>(p, s);
   else
     e = pl.nt == 2 ? rows_launch<64, 2>(p, s) : rows_launch<64, 1>(p, s);

@@ -61,9 +61,21 @@ __device__ __forceinline__ uint32_t q4_visible(const Q4Attn &p, int b, int i, in
   return tail & 0xFFFFu;
 }
 
+// The exponent e for which 2^e brings amax to [2^13, 2^14); 0 for zero, inf or
+// NaN.  It reaches 140, so 2^e is applied as two factors.
+__device__ __forceinline__ int q4_exponent(float amax) {
+  if (!(amax > 0.f) || !isfinite(amax)) return 0;
+  return 13 - (((int)(__float_as_uint(amax) >> 23) & 0xFF) - 127);
+}
+// 2^e, |e| <= 126.
+__device__ __forceinline__ float q4_pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+
 // Output row of row r of kv head h of sequence b.
 __device__ __forceinline__ size_t q4_out_row(const Q4Attn &p, int b, int h, int r) {
   return ((size_t)b * p.N_max + r / p.g) * p.Hq + h * p.g + r % p.g;
 }
+
+// The many-row kernel (attention_q4_tc.cu).
+cudaError_t q4_tc_launch(const Q4Attn &p, int D, int rows_per_block, cudaStream_t s);
 
 }  // namespace tsd

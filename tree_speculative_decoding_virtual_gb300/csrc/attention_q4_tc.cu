@@ -1,0 +1,625 @@
+// Tree-masked attention over the 4-bit paged cache for many query rows, on the
+// 5th-generation tensor cores (tcgen05).  The few-row kernel, the format and
+// the precision choices are described in attention_q4.cu and q4.cuh.
+//
+// One block = 128 or 256 query rows of one kv head x one piece of the key
+// range, walked in 128-key tiles (8 pages).  Decoding costs a fixed number of
+// instructions per key, so the more rows share a decoded tile the better; from
+// about 64 rows on the kernel is bound by the tensor cores and the softmax.
+//   warp 0       block ids, and the pages' bulk copies (9 D bytes each) into a
+//                ring of packed tiles
+//   warp 1       owns TMEM; lane 0 issues every MMA
+//   warps 4-7    decode packed tiles to fp16 K and V tiles (128-byte swizzle)
+//   warps 8-11   softmax of chain 0, warps 12-15 of chain 1: one TMEM lane (=
+//                one query row) per thread
+// A chain is a row tile of 128 rows with its S (128 columns of TMEM, P over
+// the first 64) and O.  With more than 128 rows the two chains are two row
+// tiles that share every key tile; with fewer, chain c takes the key tiles j =
+// c mod 2 of the same rows and the two are joined at the end.  Per tile:
+//   S = Q K^T         M = 128, N = 128, fp16 in, fp32 accumulate
+//   P = exp2(S c - m) fp16 over S, taken 32 keys at a time
+//   O += P V          A from TMEM, V MN-major
+// The MMAs of a chain execute in issue order, S_{j+1} right behind P_j V_j, so
+// the softmax that sees S_j complete may rescale O and overwrite S_j.  The
+// reference m is a whole number (in log2 units), so moving it multiplies what
+// is already there, P in fp16 included, by an exact power of two; it moves
+// when 32 keys' P sum above 60000, i.e. before one of them can pass fp16's
+// range, and each row decides on its own scores alone.
+// Pages of a tile that lie past the sequence are not fetched: whatever their
+// bytes are, they decode to finite values and their P is 0.
+// Every wait is bounded; on expiry the block flags TSD_STATUS_TIMEOUT, drains
+// what it issued, frees its tensor memory and returns.
+
+#include <cuda_bf16.h>
+
+#include "attention_q4.cuh"
+#include "sm100_ptx.cuh"
+
+namespace tsd {
+namespace {
+
+constexpr int kTcThreads = 512;
+constexpr int kBM = 128;            // rows of a chain's MMA
+constexpr int kBN = 128;            // keys of a tile
+constexpr int kTilePages = kBN / kPage;
+constexpr int kPackSlots = 3;       // packed K or V tiles in flight
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kTmemChain = 256, kTmemO = 128;
+constexpr float kTcOffset = 8.f;    // P of the reference score is 2^8 .. 2^9
+constexpr float kTcMaxSum = 60000.f;
+constexpr float kTcLn2 = 0.6931471805599453f;
+constexpr uint64_t kTcDrainNs = 100000000ull;
+
+template <int D>
+struct TcLayout {
+  static constexpr uint32_t kHalf = kBM * 128;         // one 64-column half of a tile
+  static constexpr uint32_t kTile = kBM * D * 2;       // an fp16 Q, K or V tile
+  static constexpr uint32_t kPack = kTilePages * Q4Page<D>::kBytes;
+  static constexpr uint32_t kQ = 0;
+  static constexpr uint32_t kK = 2 * kTile;
+  static constexpr uint32_t kV = kK + 2 * kTile;
+  static constexpr uint32_t kP = kV + 2 * kTile;       // packed ring
+  static constexpr uint32_t kBytes = kP + kPackSlots * kPack;
+  static constexpr uint32_t kAlloc = kBytes + 1024;    // alignment slack
+  static_assert(kAlloc <= 227 * 1024, "shared memory");
+  static_assert(4 * kTile >= kBM * D * 4, "the joined chain's O fits the K and V tiles");
+};
+
+struct TcShared {
+  uint64_t pk_full[kPackSlots], pk_empty[kPackSlots];
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
+  uint64_t s_full[2], p_full[2], o_final[2], q_full, drain;
+  float2 ml[kBM];  // chain 1's (reference, sum) when it shares chain 0's rows
+  uint32_t tmem_base;
+  int abort, bad;
+};
+
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn_major) {
+  // fp16 A and B (format 0), fp32 accumulator
+  return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+__device__ __forceinline__ bool tc_wait(uint64_t &bar, uint32_t parity, uint64_t limit, volatile int *abort) {
+  using namespace sm100;
+  if (*abort) return false;
+  if (mbar_wait(smem_addr(&bar), parity, limit)) return true;
+  *abort = 1;
+  return false;
+}
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// Waits for this thread's TMEM loads; the registers are operands, so that no
+// use of them can be scheduled before it.
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;\n"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
+                 "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+
+// Item m of the packed stream: K_0, then K_i and V_{i-1} for i = 1 .. n - 1,
+// then V_{n-1}: the order the MMAs want them in.
+__device__ __forceinline__ void stream_item(int m, int n, int &tile, bool &is_v) {
+  if (m == 0) {
+    tile = 0;
+    is_v = false;
+  } else if (m == 2 * n - 1) {
+    tile = n - 1;
+    is_v = true;
+  } else {
+    is_v = (m & 1) == 0;
+    tile = is_v ? m / 2 - 1 : (m + 1) / 2;
+  }
+}
+
+// Grid (splits * row blocks * Hkv, B); p.row_blocks blocks of 256 rows, or of
+// 128 when the sequence has no more.
+template <int D>
+__global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4Attn p, int rows_per_block) {
+  using namespace sm100;
+  using L = TcLayout<D>;
+  using Page = Q4Page<D>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ TcShared sh;
+  pdl_trigger();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t raw = smem_addr(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t *gbase = smem_raw + (base - raw);
+  volatile int *abort = &sh.abort;
+  const uint64_t lim = p.wait_limit_ns;
+
+  const int split = blockIdx.x % p.splits, hr = blockIdx.x / p.splits;
+  const int h = hr / p.row_blocks, rb = hr % p.row_blocks;
+  const int b = blockIdx.y;
+  pdl_wait();
+  int P, nb;
+  bool bad_len;
+  const bool ok_seq = q4_seq(p, b, P, nb, bad_len);
+  if (bad_len && blockIdx.x == 0 && tid == 0 && p.status) atomicOr(p.status, TSD_STATUS_BAD_LEN);
+  const int rows_valid = ok_seq ? nb * p.g : 0;
+  const int pages = ok_seq ? (P + nb + kPage - 1) / kPage : 0;
+  const int first = split * p.chunk, last = min(pages, first + p.chunk);
+  const int row0 = rb * rows_per_block;
+  const bool work = row0 < rows_valid && first < last;
+  if (!work && p.splits > 1) return;
+
+  if (tid == 0) {
+    for (int i = 0; i < kPackSlots; ++i) {
+      mbar_init(smem_addr(&sh.pk_full[i]), 1);
+      mbar_init(smem_addr(&sh.pk_empty[i]), 4);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_addr(&sh.k_full[i]), 4);
+      mbar_init(smem_addr(&sh.k_empty[i]), 1);
+      mbar_init(smem_addr(&sh.v_full[i]), 4);
+      mbar_init(smem_addr(&sh.v_empty[i]), 1);
+      mbar_init(smem_addr(&sh.s_full[i]), 1);
+      mbar_init(smem_addr(&sh.p_full[i]), 4);
+      mbar_init(smem_addr(&sh.o_final[i]), 1);
+    }
+    mbar_init(smem_addr(&sh.q_full), 8);
+    mbar_init(smem_addr(&sh.drain), 1);
+    sh.abort = 0;
+    sh.bad = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) tmem_alloc(smem_addr(&sh.tmem_base), kTmemCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem_base;
+
+  const int n = work ? (last - first + kTilePages - 1) / kTilePages : 0;  // key tiles
+  // two row tiles (each with every key tile), or one row tile whose key tiles
+  // alternate between the chains
+  const bool two = row0 + kBM < rows_valid && rows_per_block > kBM;
+  const int chains = two ? 2 : (n > 1 ? 2 : 1);
+
+  if (!work) {
+    // straight to the teardown
+  } else if (warp == 0) {
+    // ---- loader: lane l < 8 copies page l of the item ----
+    const int32_t *trow = p.table + (size_t)b * p.max_blocks;
+    bool ok = true;
+    int issued = 0;
+    for (int m = 0; m < 2 * n; ++m) {
+      int tile;
+      bool is_v;
+      stream_item(m, n, tile, is_v);
+      const int slot = m % kPackSlots;
+      const int pg = first + tile * kTilePages + lane;
+      const bool mine = lane < kTilePages && pg < last;
+      const int id = mine ? __ldg(trow + pg) : 0;
+      const bool bad = id < 0 || id >= p.num_blocks;
+      if (bad) sh.bad = 1;
+      if (m >= kPackSlots)
+        ok = __all_sync(0xffffffffu, tc_wait(sh.pk_empty[slot], ((m / kPackSlots) - 1) & 1, lim, abort));
+      if (!ok) break;
+      const bool copy = mine && !bad;
+      const int copies = __popc(__ballot_sync(0xffffffffu, copy));
+      const uint32_t bar = smem_addr(&sh.pk_full[slot]);
+      if (lane == 0) mbar_arrive_expect_tx(bar, copies * Page::kBytes);
+      __syncwarp();
+      if (copy)
+        bulk_load(base + L::kP + slot * L::kPack + lane * Page::kBytes,
+                  (is_v ? p.v : p.k) + ((size_t)id * p.Hkv + h) * Page::kBytes, Page::kBytes, bar);
+      issued = m + 1;
+    }
+    // no copy is in flight when the block exits
+    for (int m = max(0, issued - kPackSlots); m < issued; ++m)
+      mbar_wait(smem_addr(&sh.pk_full[m % kPackSlots]), (m / kPackSlots) & 1, kTcDrainNs);
+  } else if (warp == 1) {
+    // ---- MMA issue ----
+    if (lane == 0) {
+      constexpr uint32_t idS = idesc_f16_f32(kBM, kBN, false);
+      constexpr uint32_t idPV = idesc_f16_f32(kBM, D, true);
+      auto issue_s = [&](int c, int qt, int st) {
+        const uint64_t qd = smem_desc_sw128(base + L::kQ + qt * L::kTile, 16, 1024);
+        const uint64_t kd = smem_desc_sw128(base + L::kK + st * L::kTile, 16, 1024);
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          umma_bf16(tmem + c * kTmemChain, desc_add(qd, (kk >> 2) * L::kHalf + (kk & 3) * 32),
+                    desc_add(kd, (kk >> 2) * L::kHalf + (kk & 3) * 32), idS, kk > 0);
+        umma_commit(smem_addr(&sh.s_full[c]));
+      };
+      auto issue_pv = [&](int c, int st, bool accum, bool final) {
+        const uint64_t vd = smem_desc_sw128(base + L::kV + st * L::kTile, L::kHalf, 1024);
+        uint64_t v8[8];
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) v8[kk] = desc_add(vd, kk * 16 * 128);
+        tc_fence_after();
+        umma8_ts(tmem + c * kTmemChain + kTmemO, tmem + c * kTmemChain, v8, idPV, accum ? 1u : 0u);
+        if (final) umma_commit(smem_addr(&sh.o_final[c]));
+      };
+      bool ok = tc_wait(sh.q_full, 0, lim, abort);
+      if (two) {
+        ok = ok && tc_wait(sh.k_full[0], 0, lim, abort);
+        if (ok) {
+          issue_s(0, 0, 0);
+          issue_s(1, 1, 0);
+          umma_commit(smem_addr(&sh.k_empty[0]));
+        }
+        for (int j = 0; ok && j < n; ++j) {
+          const int st = j & 1;
+          for (int c = 0; ok && c < 2; ++c) {
+            ok = tc_wait(sh.p_full[c], j & 1, lim, abort);
+            if (ok && c == 0) ok = tc_wait(sh.v_full[st], (j >> 1) & 1, lim, abort);
+            if (!ok) break;
+            issue_pv(c, st, j > 0, j == n - 1);
+            if (c == 1) umma_commit(smem_addr(&sh.v_empty[st]));
+            if (j + 1 < n) {
+              if (c == 0) ok = tc_wait(sh.k_full[st ^ 1], ((j + 1) >> 1) & 1, lim, abort);
+              if (!ok) break;
+              issue_s(c, c, st ^ 1);
+              if (c == 1) umma_commit(smem_addr(&sh.k_empty[st ^ 1]));
+            }
+          }
+        }
+      } else {
+        for (int j = 0; ok && j < chains; ++j) {
+          ok = tc_wait(sh.k_full[j], 0, lim, abort);
+          if (!ok) break;
+          issue_s(j, 0, j);
+          umma_commit(smem_addr(&sh.k_empty[j]));
+        }
+        for (int j = 0; ok && j < n; ++j) {
+          const int c = j & 1;
+          ok = tc_wait(sh.p_full[c], (j >> 1) & 1, lim, abort) && tc_wait(sh.v_full[c], (j >> 1) & 1, lim, abort);
+          if (!ok) break;
+          issue_pv(c, c, j > 1, j + 2 >= n);
+          umma_commit(smem_addr(&sh.v_empty[c]));
+          if (j + 2 < n) {
+            ok = tc_wait(sh.k_full[c], ((j + 2) >> 1) & 1, lim, abort);
+            if (!ok) break;
+            issue_s(c, 0, c);
+            umma_commit(smem_addr(&sh.k_empty[c]));
+          }
+        }
+      }
+      umma_commit(smem_addr(&sh.drain));
+      mbar_wait(smem_addr(&sh.drain), 0, kTcDrainNs);
+    }
+    __syncwarp();
+  } else if (warp >= 4 && warp < 8) {
+    // ---- decode: a lane takes one group (16 columns) of a key at a time ----
+    constexpr int kGroups = D / kQ4Group;        // lanes across one key
+    constexpr int kKeys = 32 / kGroups;          // keys per warp step
+    const int dw = warp - 4;
+    const int grp = lane % kGroups, kl = lane / kGroups;
+    for (int m = 0; m < 2 * n; ++m) {
+      int tile;
+      bool is_v;
+      stream_item(m, n, tile, is_v);
+      const int slot = m % kPackSlots, st = tile & 1;
+      bool ok = tc_wait(sh.pk_full[slot], (m / kPackSlots) & 1, lim, abort);
+      if (ok && tile >= 2)
+        ok = tc_wait(is_v ? sh.v_empty[st] : sh.k_empty[st], ((tile >> 1) - 1) & 1, lim, abort);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      const uint8_t *src = gbase + L::kP + slot * L::kPack;
+      uint8_t *dst = gbase + (is_v ? L::kV : L::kK) + st * L::kTile + (D == 128 ? (grp >> 2) * L::kHalf : 0);
+      const int c0 = (grp & 3) * 2;
+      // the two halves of a key are stored in opposite order, so that the
+      // eight lanes of a store's quarter touch different banks
+      const int flip = D == 128 ? grp >> 2 : 0;
+#pragma unroll 4
+      for (int s = 0; s < kBN / (4 * kKeys); ++s) {
+        const int key = (s * 4 + dw) * kKeys + kl;
+        const uint8_t *page = src + (key / kPage) * Page::kBytes;
+        const int r = key % kPage;
+        const uint2 code = *reinterpret_cast<const uint2 *>(page + r * Page::kRow + grp * 8);
+        const uint32_t sc = q4_scale2(page[Page::kScales + r * Page::kScaleRow + grp]);
+        uint32_t a[4], e[4];
+        q4_decode8(flip ? code.y : code.x, a);
+        q4_decode8(flip ? code.x : code.y, e);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          a[i] = q4_mul2(a[i], sc);
+          e[i] = q4_mul2(e[i], sc);
+        }
+        *reinterpret_cast<uint4 *>(dst + sw128_offset(key, c0 + flip)) = make_uint4(a[0], a[1], a[2], a[3]);
+        *reinterpret_cast<uint4 *>(dst + sw128_offset(key, c0 + 1 - flip)) = make_uint4(e[0], e[1], e[2], e[3]);
+      }
+      fence_proxy_async_smem();  // the tensor core reads the tile through the async proxy
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(smem_addr(is_v ? &sh.v_full[st] : &sh.k_full[st]));
+        mbar_arrive(smem_addr(&sh.pk_empty[slot]));
+      }
+    }
+  } else if (warp >= 8) {
+    // ---- softmax ----
+    const int c = (warp - 8) >> 2;             // chain
+    const int rt = two ? c : 0;                // its row tile
+    const int quarter = warp & 3;
+    const int rl = quarter * 32 + lane;        // row within the tile
+    const int row = row0 + rt * kBM + rl;
+    const bool rvalid = row < rows_valid;
+    const int node = rvalid ? row / p.g : 0;
+    const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+    const uint32_t tS = tmem + c * kTmemChain + lane_off, tO = tS + kTmemO;
+
+    // Q row -> fp16, scaled by a power of two (both chains know it)
+    float mul;
+    {
+      uint32_t q[D / 2];
+      const uint4 *src = reinterpret_cast<const uint4 *>(p.q + q4_out_row(p, b, h, rvalid ? row : 0) * D);
+      float amax = 0.f;
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        const uint4 x = rvalid ? src[i] : make_uint4(0u, 0u, 0u, 0u);
+        q[4 * i] = x.x;
+        q[4 * i + 1] = x.y;
+        q[4 * i + 2] = x.z;
+        q[4 * i + 3] = x.w;
+      }
+#pragma unroll
+      for (int i = 0; i < D / 2; ++i) {
+        amax = fmaxf(amax, fabsf(__uint_as_float(q[i] << 16)));
+        amax = fmaxf(amax, fabsf(__uint_as_float(q[i] & 0xFFFF0000u)));
+      }
+      const int e = q4_exponent(amax);
+      // the factor's sign goes into q, and it stays between the smallest and the
+      // largest normal number, so that a masked score (-inf) stays one
+      const float sign = p.scale_log2 < 0.f ? -1.f : p.scale_log2 > 0.f ? 1.f : 0.f;
+      const float up1 = sign * q4_pow2(e / 2), up2 = q4_pow2(e - e / 2);
+      mul = fabsf(p.scale_log2) * q4_pow2(-(e / 2)) * q4_pow2(-(e - e / 2));
+      mul = fminf(fmaxf(mul, 1.1754944e-38f), 3.4028235e38f);
+      if (two || c == 0) {
+        uint8_t *dst = gbase + L::kQ + rt * L::kTile;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          uint32_t w[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            w[k] = pack_half2(__uint_as_float(q[4 * i + k] << 16) * up1 * up2,
+                              __uint_as_float(q[4 * i + k] & 0xFFFF0000u) * up1 * up2);
+          *reinterpret_cast<uint4 *>(dst + (i >> 3) * L::kHalf + sw128_offset(rl, i & 7)) =
+              make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        fence_proxy_async_smem();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&sh.q_full));
+    }
+
+    float ref = 0.f, l = 0.f;
+    bool unset = true, ok = c < chains;
+    const unsigned long long mul2 = f2_pack(mul, mul);
+    int u = 0;  // this chain's tiles
+    for (int j = two ? 0 : c; ok && j < n; j += two ? 1 : 2, ++u) {
+      ok = __all_sync(0xffffffffu, tc_wait(sh.s_full[c], u & 1, lim, abort));
+      if (!ok) break;
+      tc_fence_after();
+      const int t0 = (first + j * kTilePages) * kPage;  // first key slot of the tile
+      const bool tail = t0 + kBN > P;
+      uint32_t x[2][32];
+      tmem_ld32(tS, x[0]);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint32_t (&s)[32] = x[k & 1];
+        tmem_wait_ld(s);
+        if (k < 3) tmem_ld32(tS + (k + 1) * 32, x[(k + 1) & 1]);
+        uint32_t vis = 0xFFFFFFFFu;
+        if (tail) {
+          vis = rvalid ? q4_visible(p, b, node, t0 + k * 32 - P, nb) |
+                             (q4_visible(p, b, node, t0 + k * 32 + 16 - P, nb) << 16)
+                       : 0u;
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (!((vis >> i) & 1u)) s[i] = 0xFF800000u;
+        }
+        uint32_t pk[16];
+        float sum;
+        auto probabilities = [&]() {
+          const unsigned long long ref2 = f2_pack(-ref, -ref);
+          unsigned long long acc0 = 0ull, acc1 = 0ull;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            // the product is rounded before the reference is taken off, as the
+            // reference itself was: one fused step would be off by half an ulp
+            // of a large score, which can be many powers of two
+            const float2 t = f2_unpack(
+                f2_add(f2_mul(f2_pack(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), mul2), ref2));
+            const float e0 = ex2_approx(t.x), e1 = ex2_approx(t.y);
+            pk[i] = pack_half2(e0, e1);
+            if (i & 1) acc1 = f2_add(acc1, f2_pack(e0, e1));
+            else acc0 = f2_add(acc0, f2_pack(e0, e1));
+          }
+          const float2 a = f2_unpack(f2_add(acc0, acc1));
+          sum = a.x + a.y;
+        };
+        probabilities();
+        const bool mine = (unset && vis != 0u) || !(sum <= kTcMaxSum);
+        if (__any_sync(0xffffffffu, mine)) {
+          float f = 1.f;
+          if (mine) {
+            float m = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) m = fmaxf(m, (vis >> i) & 1u ? __uint_as_float(s[i]) * mul : -INFINITY);
+            if (m > -INFINITY) {
+              const float to = floorf(m) - kTcOffset;
+              // (the exponent of a move down from a first, unset reference does
+              // not matter: nothing was added yet)
+              if (!unset) f = ex2_approx(ref - to);
+              ref = to;
+              unset = false;
+              l *= f;
+            }
+          }
+          probabilities();
+          // what is already in TMEM for these rows: O, and this tile's P
+          if (__any_sync(0xffffffffu, f != 1.f)) {
+            if (u > 0) {
+#pragma unroll 1
+              for (int q = 0; q < D / 32; ++q) {
+                uint32_t o[32];
+                tmem_ld32(tO + q * 32, o);
+                tmem_wait_ld(o);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                tmem_st32(tO + q * 32, o);
+              }
+            }
+            if (k > 0) {
+              tmem_wait_st();
+              const __half2 f2 = __floats2half2_rn(f, f);
+              uint32_t o[32];
+              tmem_ld32(tS, o);  // (k = 1: the second 16 are this chunk's scores, left as they are)
+              tmem_wait_ld(o);
+              uint32_t o2[32];
+              if (k > 2) {
+                tmem_ld32(tS + 32, o2);
+                tmem_wait_ld(o2);
+              }
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (i < 16 || k > 1) {
+                  const __half2 v = __hmul2(*reinterpret_cast<__half2 *>(&o[i]), f2);
+                  o[i] = *reinterpret_cast<const uint32_t *>(&v);
+                }
+              tmem_st32(tS, o);
+              if (k > 2) {
+                uint32_t o3[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                  const __half2 v = __hmul2(*reinterpret_cast<__half2 *>(&o2[i]), f2);
+                  o3[i] = *reinterpret_cast<const uint32_t *>(&v);
+                }
+                tmem_st16(tS + 32, o3);
+              }
+            }
+          }
+        }
+        l += sum;
+        tmem_st16(tS + k * 16, pk);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&sh.p_full[c]));
+    }
+
+    // ---- epilogue: O of this chain is complete ----
+    const bool joined = !two && chains == 2;
+    if (ok) ok = __all_sync(0xffffffffu, tc_wait(sh.o_final[c], 0, lim, abort));
+    // (joined: chain 1's O goes over the K and V tiles, which chain 0's last
+    // MMAs may still read)
+    if (ok && joined) ok = __all_sync(0xffffffffu, tc_wait(sh.o_final[c ^ 1], 0, lim, abort));
+    tc_fence_after();
+    float M = unset ? -INFINITY : ref;
+    if (unset && l != l) M = 0.f;  // only NaN scores so far
+    float *stage = reinterpret_cast<float *>(gbase + L::kK);  // K and V tiles are done with
+    if (joined && c == 1) {
+      // chain 1's part, transposed: column-major, so that lanes do not collide
+#pragma unroll 1
+      for (int q = 0; ok && q < D / 32; ++q) {
+        uint32_t o[32];
+        tmem_ld32(tO + q * 32, o);
+        tmem_wait_ld(o);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) stage[(q * 32 + i) * kBM + rl] = __uint_as_float(o[i]);
+      }
+      sh.ml[rl] = make_float2(M, l);
+    }
+    if (joined) asm volatile("bar.sync 1, 256;\n" ::: "memory");
+    if (c < (two ? 2 : 1)) {
+      float f0 = 1.f, f1 = 0.f;
+      if (joined) {
+        const float2 other = sh.ml[rl];
+        const float top = fmaxf(M, other.x);
+        f0 = M == -INFINITY ? 0.f : ex2_approx(M - top);
+        f1 = other.x == -INFINITY ? 0.f : ex2_approx(other.x - top);
+        l = f0 * l + f1 * other.y;
+        M = top;
+      }
+      const bool bad = sh.bad != 0;
+      const bool direct = p.splits == 1;
+      const bool empty = bad || l == 0.f;
+      const float inv = empty ? 0.f : 1.f / l;
+      const size_t pr = (((size_t)b * p.Hkv + h) * p.splits + split) * p.rows + row;
+      const size_t orow = rvalid ? q4_out_row(p, b, h, row) : 0;
+#pragma unroll 1
+      for (int q = 0; ok && q < D / 32; ++q) {
+        uint32_t o[32];
+        tmem_ld32(tO + q * 32, o);
+        tmem_wait_ld(o);
+        float v[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          v[i] = __uint_as_float(o[i]) * f0;
+          if (joined) v[i] = fmaf(f1, f1 == 0.f ? 0.f : stage[(q * 32 + i) * kBM + rl], v[i]);
+        }
+        if (rvalid) {
+          if (direct) {
+            uint4 *dst = reinterpret_cast<uint4 *>(p.out + orow * D + q * 32);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              dst[i] = empty ? make_uint4(0u, 0u, 0u, 0u)
+                             : make_uint4(pack_bf16x2(v[8 * i] * inv, v[8 * i + 1] * inv),
+                                          pack_bf16x2(v[8 * i + 2] * inv, v[8 * i + 3] * inv),
+                                          pack_bf16x2(v[8 * i + 4] * inv, v[8 * i + 5] * inv),
+                                          pack_bf16x2(v[8 * i + 6] * inv, v[8 * i + 7] * inv));
+          } else {
+            float4 *dst = reinterpret_cast<float4 *>(p.part_o + pr * D + q * 32);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              dst[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+          }
+        }
+      }
+      if (rvalid) {
+        if (!direct)
+          p.part_ml[pr] = make_float2(M, bad ? -1.f : l);
+        else if (p.lse)
+          p.lse[orow] = empty ? -INFINITY : (M + log2f(l)) * kTcLn2;
+      }
+    }
+  }
+  // rows that no chain computed, when they go straight to the output
+  if (p.splits == 1) {
+    const int end = min(p.rows, row0 + rows_per_block);
+    for (int x = tid; x < (end - row0) * (D / 8); x += kTcThreads) {
+      const int r = row0 + x / (D / 8);
+      if (work && r < rows_valid) continue;
+      const size_t orow = q4_out_row(p, b, h, r);
+      reinterpret_cast<uint4 *>(p.out + orow * D)[x % (D / 8)] = make_uint4(0u, 0u, 0u, 0u);
+      if (x % (D / 8) == 0 && p.lse) p.lse[orow] = -INFINITY;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, kTmemCols);
+  if (tid == 0 && p.status) {
+    if (sh.bad) atomicOr(p.status, TSD_STATUS_BAD_PAGE);
+    if (sh.abort) atomicOr(p.status, TSD_STATUS_TIMEOUT);
+  }
+}
+
+}  // namespace
+
+cudaError_t q4_tc_launch(const Q4Attn &p, int D, int rows_per_block, cudaStream_t s) {
+  const dim3 grid((unsigned)p.splits * p.row_blocks * p.Hkv, p.B);
+  if (D == 128) {
+    if (!set_smem((const void *)tree_attn_q4_tc_kernel<128>, TcLayout<128>::kAlloc)) return cudaErrorUnknown;
+    return launch(tree_attn_q4_tc_kernel<128>, grid, dim3(kTcThreads), TcLayout<128>::kAlloc, s, p, rows_per_block);
+  }
+  if (!set_smem((const void *)tree_attn_q4_tc_kernel<64>, TcLayout<64>::kAlloc)) return cudaErrorUnknown;
+  return launch(tree_attn_q4_tc_kernel<64>, grid, dim3(kTcThreads), TcLayout<64>::kAlloc, s, p, rows_per_block);
+}
+
+}  // namespace tsd

@@ -362,6 +362,11 @@ __device__ __forceinline__ unsigned long long f2_add(unsigned long long a, unsig
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+__device__ __forceinline__ unsigned long long f2_mul(unsigned long long a, unsigned long long b) {
+  unsigned long long r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 // acc_lo += the low bf16 of w and acc_hi += the high one: each is widened to
 // fp32 exactly and added with round-to-nearest (PTX mixed-precision add), so
 // no shift or mask is needed to unpack the pair.
