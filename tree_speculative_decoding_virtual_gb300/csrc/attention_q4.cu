@@ -93,18 +93,34 @@ struct RowsLayout {
   static constexpr int kStage = 2 * kPageBytes;
   static constexpr int kRing = kRowsWarps * kRowsStages * kStage;
   static constexpr int kMerge = kRowsWarps * 8 * NT * D * 4;  // O of every warp
-  static constexpr int kBytes = kRing > kMerge ? kRing : kMerge;
+  static constexpr int kBlock = 8 * NT * D * 4;               // O of the block
+  static constexpr int kBytes = kRing > kMerge + kBlock ? kRing : kMerge + kBlock;
   static_assert(kStage % 16 == 0, "bulk copies start on 16 bytes");
 };
+
+// Four columns of a finished row: O / sum in bf16, and the row's lse.
+__device__ __forceinline__ void rows_out(const Q4Attn &p, size_t orow, int D, int c, float4 a, float M,
+                                         float sum, bool skip) {
+  const bool empty = skip || sum == 0.f;
+  const float inv = empty ? 0.f : 1.f / sum;
+  *reinterpret_cast<uint2 *>(p.out + orow * D + 4 * c) =
+      empty ? make_uint2(0u, 0u)
+            : make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
+  if (c == 0 && p.lse) p.lse[orow] = empty ? -INFINITY : (M + log2f(sum)) * kRowsLn2;
+}
 
 struct RowsShared {
   uint64_t full[kRowsWarps][kRowsStages];
   float2 ml[kRowsWarps][16];  // (reference, sum) of each warp's rows
+  float4 block_ml[16];        // and of the block's (sum -1: bad page)
   int bad, timeout;
 };
 
 // Grid (splits * row blocks * Hkv, B).  A block owns 8 NT rows of one kv head
 // and one piece of the key range; its warps take the piece's pages in turn.
+// With p.cluster the pieces of a range are one thread-block cluster: each
+// sequence is cut into equal parts of its own length, and the parts meet
+// through distributed shared memory, without a workspace or a second kernel.
 template <int D, int NT>
 __global__ void __launch_bounds__(kRowsThreads, 2) tree_attn_q4_rows_kernel(const Q4Attn p) {
   using namespace sm100;
@@ -139,9 +155,10 @@ __global__ void __launch_bounds__(kRowsThreads, 2) tree_attn_q4_rows_kernel(cons
     atomicOr(p.status, TSD_STATUS_BAD_LEN);
   const int rows_valid = ok ? nb * p.g : 0;
   const int pages = ok ? (P + nb + kPage - 1) / kPage : 0;
-  const int first = split * p.chunk, last = min(pages, first + p.chunk);
+  const int chunk = p.cluster ? (pages + p.splits - 1) / p.splits : p.chunk;
+  const int first = split * chunk, last = min(pages, first + chunk);
   const bool work = row0 < rows_valid && first < last;
-  if (!work && p.splits > 1) return;
+  if (!work && p.splits > 1 && !p.cluster) return;
 
   float o[NT][kTiles][4];
   float l[NT][2], trig[NT][2], ref[NT][2], mul[NT][2];
@@ -405,6 +422,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2) tree_attn_q4_rows_kernel(cons
   // ---- join the warps: every ring is drained, its memory holds their O ----
   __syncthreads();
   float *merge = reinterpret_cast<float *>(smem);
+  float *block_o = reinterpret_cast<float *>(smem + L::kMerge);
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -447,21 +465,50 @@ __global__ void __launch_bounds__(kRowsThreads, 2) tree_attn_q4_rows_kernel(cons
         sum += f * ml.y;
       }
     }
-    if (p.splits > 1) {
+    if (p.cluster) {
+      *reinterpret_cast<float4 *>(block_o + rl * D + 4 * c) = a;
+      if (c == 0) sh.block_ml[rl] = make_float4(M, bad ? -1.f : sum, 0.f, 0.f);
+    } else if (p.splits > 1) {
       if (r >= rows_valid) continue;
       const size_t pr = (((size_t)b * p.Hkv + h) * p.splits + split) * p.rows + r;
       *reinterpret_cast<float4 *>(p.part_o + pr * D + 4 * c) = a;
       if (c == 0) p.part_ml[pr] = make_float2(M, bad ? -1.f : sum);
     } else {
-      const size_t orow = q4_out_row(p, b, h, r);
-      const bool empty = r >= rows_valid || bad || sum == 0.f;
-      const float inv = empty ? 0.f : 1.f / sum;
-      *reinterpret_cast<uint2 *>(p.out + orow * D + 4 * c) =
-          empty ? make_uint2(0u, 0u)
-                : make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
-      if (c == 0 && p.lse) p.lse[orow] = empty ? -INFINITY : (M + log2f(sum)) * kRowsLn2;
+      rows_out(p, q4_out_row(p, b, h, r), D, c, a, M, sum, r >= rows_valid || bad);
     }
   }
+  if (!p.cluster) return;
+  // every block of the cluster takes a share of the rows' columns
+  cluster_arrive();
+  cluster_wait();
+  for (int x = split * kRowsThreads + tid; x < 8 * NT * kVec; x += p.splits * kRowsThreads) {
+    const int rl = x / kVec, c = x % kVec, r = row0 + rl;
+    if (r >= p.rows) break;
+    float M = -INFINITY;
+    bool skip = r >= rows_valid;
+    for (int s = 0; s < p.splits; ++s) {
+      const float4 ml = ld_dsmem_f4(smem_addr(&sh.block_ml[rl]), s);
+      M = fmaxf(M, ml.x);
+      skip = skip || ml.y == -1.f;
+    }
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    float sum = 0.f;
+    if (M > -INFINITY) {
+      for (int s = 0; s < p.splits; ++s) {
+        const float4 ml = ld_dsmem_f4(smem_addr(&sh.block_ml[rl]), s);
+        const float4 v = ld_dsmem_f4(smem_addr(block_o + rl * D + 4 * c), s);
+        const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - M);
+        a.x += f * v.x;
+        a.y += f * v.y;
+        a.z += f * v.z;
+        a.w += f * v.w;
+        sum += f * ml.y;
+      }
+    }
+    rows_out(p, q4_out_row(p, b, h, r), D, c, a, M, sum, skip);
+  }
+  cluster_arrive();  // no block leaves while another reads its shared memory
+  cluster_wait();
 }
 
 // One warp per output row: joins the pieces of its key range (fp32), rounds
@@ -534,8 +581,13 @@ __global__ void __launch_bounds__(256) tree_attn_q4_join_kernel(const Q4Attn p) 
 
 constexpr int kQ4MaxSplits = 64;
 
+// Key ranges of up to this many pages are cut into at most 8 pieces (a
+// cluster) even where more would fill the GPU.
+constexpr int kClusterPages = 512;
+
 struct Q4Plan {
-  bool tc;  // the many-row kernel
+  bool tc;       // the many-row kernel
+  bool cluster;  // pieces joined inside a cluster
   int nt, rows_per_block, row_blocks, splits, chunk;
   size_t ml_off, bytes;
 };
@@ -545,7 +597,7 @@ constexpr int kTcMinRows = 33;
 
 // Host: how a call is cut up.
 Q4Plan q4_plan(int B, int N_max, int Hq, int Hkv, int D, int max_slots) {
-  Q4Plan pl;
+  Q4Plan pl = {};
   const int rows = N_max * (Hq / Hkv);
   const int pages = (max_slots + kPage - 1) / kPage;
   pl.tc = rows >= kTcMinRows;
@@ -577,6 +629,14 @@ Q4Plan q4_plan(int B, int N_max, int Hq, int Hkv, int D, int max_slots) {
     want = std::min<int64_t>(want, (pages + 2 * kRowsWarps - 1) / (2 * kRowsWarps));
     want = std::max<int64_t>(1, std::min<int64_t>(want, kQ4MaxSplits));
     pl.chunk = (int)((pages + want - 1) / want);
+    if (want > 1 && (want <= 8 || pages <= kClusterPages)) {
+      // a cluster of 2, 4 or 8
+      int c = 2;
+      while (c < want && c < 8) c *= 2;
+      pl.cluster = true;
+      pl.splits = c;
+      return pl;
+    }
   }
   pl.splits = (pages + pl.chunk - 1) / pl.chunk;
   const size_t n = (size_t)B * Hkv * pl.splits * rows;
@@ -589,8 +649,21 @@ template <int D, int NT>
 cudaError_t rows_launch(const Q4Attn &p, cudaStream_t s) {
   const int smem = RowsLayout<D, NT>::kBytes;
   if (!set_smem((const void *)tree_attn_q4_rows_kernel<D, NT>, smem)) return cudaErrorUnknown;
-  return launch(tree_attn_q4_rows_kernel<D, NT>, dim3((unsigned)p.splits * p.Hkv * p.row_blocks, p.B),
-                dim3(kRowsThreads), smem, s, p);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)p.splits * p.Hkv * p.row_blocks, p.B);
+  cfg.blockDim = dim3(kRowsThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = p.cluster ? p.splits : 1;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, tree_attn_q4_rows_kernel<D, NT>, p);
 }
 
 int q4_check(int B, int N_max, int Hq, int Hkv, int D, int max_slots) {
@@ -653,6 +726,7 @@ TSD_API int tsd_tree_attn_fwd_q4(const uint16_t *q, const uint8_t *k_cache, cons
   p.row_blocks = pl.row_blocks;
   p.splits = pl.splits;
   p.chunk = pl.chunk;
+  p.cluster = pl.cluster;
   p.part_o = reinterpret_cast<float *>(workspace);
   p.part_ml = pl.bytes ? reinterpret_cast<float2 *>(reinterpret_cast<char *>(workspace) + pl.ml_off) : nullptr;
   p.out = out;
@@ -668,7 +742,7 @@ TSD_API int tsd_tree_attn_fwd_q4(const uint16_t *q, const uint8_t *k_cache, cons
   else
     e = pl.nt == 2 ? rows_launch<64, 2>(p, s) : rows_launch<64, 1>(p, s);
   if (e != cudaSuccess) return TSD_ERR_CUDA;
-  if (pl.splits > 1) {
+  if (pl.splits > 1 && !pl.cluster) {
     const int64_t rows = (int64_t)B * Hkv * p.rows;
     const dim3 grid((unsigned)((rows + 7) / 8));
     e = D == 128 ? launch(tree_attn_q4_join_kernel<128>, grid, dim3(256), 0, s, p)

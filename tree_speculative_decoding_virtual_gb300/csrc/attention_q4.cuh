@@ -19,7 +19,8 @@ struct Q4Attn {
   int rows;        // N_max * g, query rows of one kv head
   int row_blocks;  // blocks over them
   int splits;      // pieces of the longest key range
-  int chunk;       // page slots (of 16 keys) in one piece
+  int chunk;       // pages (of 16 keys) in one piece
+  int cluster;     // few-row kernel: the pieces of a range are a thread-block cluster
   float *part_o;   // [B * Hkv][splits][rows][D]: unnormalised fp32 outputs
   float2 *part_ml;  // [B * Hkv][splits][rows]: (reference in log2 units, sum), sum -1: bad page
   uint16_t *out;

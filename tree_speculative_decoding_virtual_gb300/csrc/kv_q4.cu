@@ -13,36 +13,53 @@
 namespace tsd {
 namespace {
 
+// Writer and reader: a lane holds 8 consecutive values (16 bytes of bf16, 4 code
+// bytes), so a warp's loads and stores are contiguous on both sides; two lanes
+// share a group and its scale.
 constexpr int kRowThreads = 256;
+constexpr int kLaneValues = 8;
+constexpr int kBlockItems = 4 * kRowThreads;  // lanes' worth of work of a block
 
-// One group of 16 bf16 values -> eight code bytes and a scale byte.
+// A quotient x / s rounded to 16 significant bits, from a reciprocal of s that is
+// off by at most 2^-24.  The product is then off by less than 2^-22, so a true
+// quotient with at most 16 significant bits (a tie in particular) comes out
+// exact.
+__device__ __forceinline__ float near_quotient(float x, float recip) {
+  const float y = x * recip;
+  return __uint_as_float((__float_as_uint(y) + 0x80u) & 0xFFFFFF00u);
+}
+
+// Eight bf16 values -> four code bytes and the group's scale byte; `lane ^ 1`
+// holds the group's other half.
 //   scale = nearest (ties to even) to amax / 6, at most 10240;
 //   code  = nearest (ties to even) to x / scale.
 // amax and x have 8 significant bits and every rounding boundary (times 6, or
 // times the scale) at most 7, so a quotient that is not a tie differs from
-// the boundary by 2^-9 relative or more: deciding on the correctly rounded
-// fp32 quotient gives the decision of exact arithmetic.  NaN counts as 0 and
-// an infinity as the largest value; both are reported.
-__device__ __forceinline__ uint2 q4_encode(const uint4 (&in)[2], uint32_t &scale_byte, bool &odd) {
-  float x[16];
-  const uint32_t w[8] = {in[0].x, in[0].y, in[0].z, in[0].w, in[1].x, in[1].y, in[1].z, in[1].w};
+// the boundary by 2^-9 relative or more: deciding on the quotient rounded to
+// 16 bits gives the decision of exact arithmetic.  NaN counts as 0 and an
+// infinity as the largest value; both are reported.
+__device__ __forceinline__ uint32_t q4_encode(uint4 in, uint32_t &scale_byte, bool &odd) {
+  float x[8];
+  const uint32_t w[4] = {in.x, in.y, in.z, in.w};
   float amax = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 4; ++i) {
     x[2 * i] = __uint_as_float(w[i] << 16);
     x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
   }
-  bool finite = true;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    if (!isfinite(x[i])) {
-      finite = false;
-      if (isnan(x[i])) x[i] = 0.f;
-    }
-    amax = fmaxf(amax, fabsf(x[i]));
+  for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(x[i]));  // (drops NaN)
+  bool finite = amax < INFINITY;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) finite = finite && x[i] == x[i];
+  if (!finite) {
+    odd = true;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      x[i] = x[i] != x[i] ? 0.f : fminf(fmaxf(x[i], -3e38f), 3e38f);
   }
-  odd = odd || !finite;
-  const float r = fminf(__fdiv_rn(amax, 6.f), 10240.f);
+  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+  const float r = near_quotient(fminf(amax, 61440.f), 0x1.555556p-3f);
   uint32_t byte;
   if (r < 6.103515625e-05f) {  // below 2^-14: steps of 2^-17
     byte = (uint32_t)rintf(r * 131072.f);
@@ -54,54 +71,72 @@ __device__ __forceinline__ uint2 q4_encode(const uint4 (&in)[2], uint32_t &scale
   scale_byte = byte;
   const float scale =
       byte < 8 ? (float)byte * 7.62939453125e-06f : __uint_as_float((byte + (112u << 3)) << 20);
-  uint32_t code[2] = {0u, 0u};
+  const float recip = byte ? __frcp_rn(scale) : 0.f;
+  uint32_t code = 0u;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float a = byte ? __fdiv_rn(x[2 * i], scale) : copysignf(0.f, x[2 * i]);
-    const float b = byte ? __fdiv_rn(x[2 * i + 1], scale) : copysignf(0.f, x[2 * i + 1]);
+  for (int i = 0; i < 4; ++i) {
     uint16_t two;  // the first source of the conversion goes to the high nibble
     asm("{\n .reg .b8 t;\n cvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n cvt.u16.u8 %0, t;\n}\n"
         : "=h"(two)
-        : "f"(b), "f"(a));
-    code[i / 4] |= (uint32_t)two << (8 * (i % 4));
+        : "f"(near_quotient(x[2 * i + 1], recip)), "f"(near_quotient(x[2 * i], recip)));
+    code |= (uint32_t)two << (8 * i);
   }
-  return make_uint2(code[0], code[1]);
+  return code;
 }
 
-// One thread per (token, kv head, group): reads 32 bytes of K and of V, writes
-// 8 code bytes and a scale byte of each.
+struct RowArgs {
+  const int32_t *slots;
+  int64_t T;
+  int num_blocks, Hkv, tokens;  // tokens: of one block
+  int32_t *status;
+};
+
+// Slot of token t; -1 when there is none (the one lane that `report`s tells).
+__device__ __forceinline__ int row_slot(const RowArgs &a, int64_t t, bool report) {
+  const int slot = a.slots[t];
+  if (slot >= 0 && (int64_t)slot < (int64_t)a.num_blocks * kPage) return slot;
+  if (slot != -1 && report && a.status) atomicOr(a.status, TSD_STATUS_BAD_PAGE);
+  return -1;
+}
+
+// A block takes a.tokens tokens, K and V.
 template <int D>
 __global__ void __launch_bounds__(kRowThreads)
-kv_write_q4_kernel(const uint16_t *__restrict__ k, int64_t k_stride, const uint16_t *__restrict__ v,
-                   int64_t v_stride, const int32_t *__restrict__ slots, int64_t items, int num_blocks,
-                   int Hkv, uint8_t *__restrict__ kc, uint8_t *__restrict__ vc, int32_t *status) {
+kv_write_q4_kernel(const RowArgs a, const uint16_t *__restrict__ k, int64_t k_stride,
+                   const uint16_t *__restrict__ v, int64_t v_stride, uint8_t *__restrict__ kc,
+                   uint8_t *__restrict__ vc) {
   using L = Q4Page<D>;
-  constexpr int kGroups = D / kQ4Group;
+  constexpr int kLanes = D / kLaneValues;  // of one head's row
   pdl_wait();
-  const int64_t x = (int64_t)blockIdx.x * kRowThreads + threadIdx.x;
-  if (x >= items) return;
-  const int per = Hkv * kGroups;  // groups of one token
-  const int64_t t = x / per;
-  const int hg = (int)(x - t * per);
-  const int h = hg / kGroups, gi = hg % kGroups;
-  const int slot = slots[t];
-  if (slot < 0 || (int64_t)slot >= (int64_t)num_blocks * kPage) {
-    if (slot != -1 && hg == 0 && status) atomicOr(status, TSD_STATUS_BAD_PAGE);
-    return;
+  const int per = a.Hkv * kLanes;
+  const int64_t t0 = (int64_t)blockIdx.x * a.tokens;
+  const int items = (int)min((int64_t)a.tokens, a.T - t0) * per;
+  // (whole warps: a lane past the end encodes zeros for its partner's sake)
+#pragma unroll 2
+  for (int x = threadIdx.x; x < (items + 31) / 32 * 32; x += kRowThreads) {
+    const int tl = min(x, items - 1) / per, c = min(x, items - 1) - tl * per;
+    const int64_t t = t0 + tl;
+    const int slot = x < items ? row_slot(a, t, c == 0) : -1;
+    uint4 kin = make_uint4(0u, 0u, 0u, 0u), vin = kin;
+    if (slot >= 0) {
+      kin = __ldcs(reinterpret_cast<const uint4 *>(k + t * k_stride + c * kLaneValues));
+      vin = __ldcs(reinterpret_cast<const uint4 *>(v + t * v_stride + c * kLaneValues));
+    }
+    bool odd = false;
+    uint32_t sk, sv;
+    const uint32_t ck = q4_encode(kin, sk, odd), cv = q4_encode(vin, sv, odd);
+    if (slot < 0) continue;
+    const int h = c / kLanes, i = c % kLanes;
+    const size_t page = ((size_t)(slot / kPage) * a.Hkv + h) * L::kBytes;
+    const int row = slot % kPage;
+    *reinterpret_cast<uint32_t *>(kc + page + row * L::kRow + i * 4) = ck;
+    *reinterpret_cast<uint32_t *>(vc + page + row * L::kRow + i * 4) = cv;
+    if ((i & 1) == 0) {
+      kc[page + L::kScales + row * L::kScaleRow + i / 2] = (uint8_t)sk;
+      vc[page + L::kScales + row * L::kScaleRow + i / 2] = (uint8_t)sv;
+    }
+    if (odd && a.status) atomicOr(a.status, TSD_STATUS_NONFINITE);
   }
-  const uint4 *ks = reinterpret_cast<const uint4 *>(k + t * k_stride + hg * kQ4Group);
-  const uint4 *vs = reinterpret_cast<const uint4 *>(v + t * v_stride + hg * kQ4Group);
-  const uint4 kin[2] = {ks[0], ks[1]}, vin[2] = {vs[0], vs[1]};
-  const size_t page = ((size_t)(slot / kPage) * Hkv + h) * L::kBytes;
-  const int row = slot % kPage;
-  bool odd = false;
-  uint32_t sk, sv;
-  const uint2 ck = q4_encode(kin, sk, odd), cv = q4_encode(vin, sv, odd);
-  *reinterpret_cast<uint2 *>(kc + page + row * L::kRow + gi * 8) = ck;
-  kc[page + L::kScales + row * L::kScaleRow + gi] = (uint8_t)sk;
-  *reinterpret_cast<uint2 *>(vc + page + row * L::kRow + gi * 8) = cv;
-  vc[page + L::kScales + row * L::kScaleRow + gi] = (uint8_t)sv;
-  if (odd && status) atomicOr(status, TSD_STATUS_NONFINITE);
 }
 
 // Two fp16 values of a page (exact in bf16) as a bf16 pair.
@@ -111,51 +146,44 @@ __device__ __forceinline__ uint32_t half2_to_bf16x2(uint32_t h) {
   return *reinterpret_cast<const uint32_t *>(&b);
 }
 
-__device__ __forceinline__ void q4_row_out(uint2 code, uint32_t scale_byte, uint16_t *dst) {
+__device__ __forceinline__ uint4 q4_values(uint32_t code, uint32_t scale_byte) {
   const uint32_t s = q4_scale2(scale_byte);
-  uint32_t a[4], b[4];
-  q4_decode8(code.x, a);
-  q4_decode8(code.y, b);
+  uint32_t a[4];
+  q4_decode8(code, a);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    a[i] = half2_to_bf16x2(q4_mul2(a[i], s));
-    b[i] = half2_to_bf16x2(q4_mul2(b[i], s));
-  }
-  uint4 *d = reinterpret_cast<uint4 *>(dst);
-  d[0] = make_uint4(a[0], a[1], a[2], a[3]);
-  d[1] = make_uint4(b[0], b[1], b[2], b[3]);
+  for (int i = 0; i < 4; ++i) a[i] = half2_to_bf16x2(q4_mul2(a[i], s));
+  return make_uint4(a[0], a[1], a[2], a[3]);
 }
 
-// One thread per (token, kv head, group), K and V: 9 bytes in, 32 out.
 template <int D>
 __global__ void __launch_bounds__(kRowThreads)
-kv_read_q4_kernel(const uint8_t *__restrict__ kc, const uint8_t *__restrict__ vc,
-                  const int32_t *__restrict__ slots, int64_t items, int num_blocks, int Hkv,
-                  uint16_t *__restrict__ k, uint16_t *__restrict__ v, int32_t *status) {
+kv_read_q4_kernel(const RowArgs a, const uint8_t *__restrict__ kc, const uint8_t *__restrict__ vc,
+                  uint16_t *__restrict__ k, uint16_t *__restrict__ v) {
   using L = Q4Page<D>;
-  constexpr int kGroups = D / kQ4Group;
+  constexpr int kLanes = D / kLaneValues;
   pdl_wait();
-  const int64_t x = (int64_t)blockIdx.x * kRowThreads + threadIdx.x;
-  if (x >= items) return;
-  const int per = Hkv * kGroups;
-  const int64_t t = x / per;
-  const int hg = (int)(x - t * per);
-  const int h = hg / kGroups, gi = hg % kGroups;
-  const int slot = slots[t];
-  uint2 ck = make_uint2(0u, 0u), cv = ck;
-  uint32_t sk = 0, sv = 0;
-  if (slot >= 0 && (int64_t)slot < (int64_t)num_blocks * kPage) {
-    const size_t page = ((size_t)(slot / kPage) * Hkv + h) * L::kBytes;
-    const int row = slot % kPage;
-    ck = *reinterpret_cast<const uint2 *>(kc + page + row * L::kRow + gi * 8);
-    cv = *reinterpret_cast<const uint2 *>(vc + page + row * L::kRow + gi * 8);
-    sk = kc[page + L::kScales + row * L::kScaleRow + gi];
-    sv = vc[page + L::kScales + row * L::kScaleRow + gi];
-  } else if (slot != -1 && hg == 0 && status) {
-    atomicOr(status, TSD_STATUS_BAD_PAGE);
+  const int per = a.Hkv * kLanes;
+  const int64_t t0 = (int64_t)blockIdx.x * a.tokens;
+  const int items = (int)min((int64_t)a.tokens, a.T - t0) * per;
+#pragma unroll 4
+  for (int x = threadIdx.x; x < items; x += kRowThreads) {
+    const int tl = x / per, c = x - tl * per;
+    const int64_t t = t0 + tl;
+    const int slot = row_slot(a, t, c == 0);
+    uint32_t ck = 0, cv = 0, sk = 0, sv = 0;
+    if (slot >= 0) {
+      const int h = c / kLanes, i = c % kLanes;
+      const size_t page = ((size_t)(slot / kPage) * a.Hkv + h) * L::kBytes;
+      const int row = slot % kPage;
+      ck = *reinterpret_cast<const uint32_t *>(kc + page + row * L::kRow + i * 4);
+      cv = *reinterpret_cast<const uint32_t *>(vc + page + row * L::kRow + i * 4);
+      sk = kc[page + L::kScales + row * L::kScaleRow + i / 2];
+      sv = vc[page + L::kScales + row * L::kScaleRow + i / 2];
+    }
+    const size_t at = (size_t)t * per + c;
+    __stcs(reinterpret_cast<uint4 *>(k) + at, q4_values(ck, sk));
+    __stcs(reinterpret_cast<uint4 *>(v) + at, q4_values(cv, sv));
   }
-  q4_row_out(ck, sk, k + x * kQ4Group);
-  q4_row_out(cv, sv, v + x * kQ4Group);
 }
 
 constexpr int kCommitThreads = 128;
@@ -208,8 +236,17 @@ int rows_check(int64_t T, int num_blocks, int Hkv, int D) {
   if (T < 0 || num_blocks < 1 || Hkv < 1) return TSD_ERR_ARG;
   if (D != 64 && D != 128) return TSD_ERR_LIMIT;
   if (Hkv > 65535 || (int64_t)num_blocks * kPage > 0x7FFFFFFFll || T > 0x7FFFFFFFll) return TSD_ERR_LIMIT;
-  if ((T * Hkv * (D / kQ4Group) + kRowThreads - 1) / kRowThreads > 0x7FFFFFFFll) return TSD_ERR_LIMIT;
   return TSD_OK;
+}
+
+RowArgs row_args(const int32_t *slots, int64_t T, int num_blocks, int Hkv, int D, int32_t *status) {
+  // a block's work: kBlockItems lanes, or fewer so that a step's tree still
+  // reaches every SM
+  const int per = Hkv * (D / kLaneValues);
+  const int64_t fill = (T * per + 2 * sm_count() - 1) / (2 * sm_count());
+  const int64_t lanes = fill < kBlockItems ? fill : kBlockItems;
+  const int tokens = (int)(lanes / per);
+  return RowArgs{slots, T, num_blocks, Hkv, tokens > 0 ? tokens : 1, status};
 }
 
 }  // namespace
@@ -227,13 +264,13 @@ TSD_API int tsd_kv_write_q4(const uint16_t *k, int64_t k_stride, const uint16_t 
   const int64_t row = (int64_t)Hkv * D;
   if (T > 1 && (k_stride < row || v_stride < row)) return TSD_ERR_ARG;
   if (k_stride % 8 != 0 || v_stride % 8 != 0) return TSD_ERR_ARG;
-  const int64_t items = T * Hkv * (D / kQ4Group);
-  const dim3 grid((unsigned)((items + kRowThreads - 1) / kRowThreads));
+  const RowArgs a = row_args(slots, T, num_blocks, Hkv, D, status);
+  const dim3 grid((unsigned)((T + a.tokens - 1) / a.tokens));
   const cudaError_t e =
-      D == 128 ? launch(kv_write_q4_kernel<128>, grid, dim3(kRowThreads), 0, as_cuda(stream), k,
-                        k_stride, v, v_stride, slots, items, num_blocks, Hkv, k_cache, v_cache, status)
-               : launch(kv_write_q4_kernel<64>, grid, dim3(kRowThreads), 0, as_cuda(stream), k,
-                        k_stride, v, v_stride, slots, items, num_blocks, Hkv, k_cache, v_cache, status);
+      D == 128 ? launch(kv_write_q4_kernel<128>, grid, dim3(kRowThreads), 0, as_cuda(stream), a, k,
+                        k_stride, v, v_stride, k_cache, v_cache)
+               : launch(kv_write_q4_kernel<64>, grid, dim3(kRowThreads), 0, as_cuda(stream), a, k,
+                        k_stride, v, v_stride, k_cache, v_cache);
   return e == cudaSuccess ? TSD_OK : TSD_ERR_CUDA;
 }
 
@@ -246,13 +283,13 @@ TSD_API int tsd_kv_read_q4(const uint8_t *k_cache, const uint8_t *v_cache, const
   if (!k || !v || !slots || !k_cache || !v_cache) return TSD_ERR_ARG;
   if (!aligned(k, 16) || !aligned(v, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16))
     return TSD_ERR_ARG;
-  const int64_t items = T * Hkv * (D / kQ4Group);
-  const dim3 grid((unsigned)((items + kRowThreads - 1) / kRowThreads));
+  const RowArgs a = row_args(slots, T, num_blocks, Hkv, D, status);
+  const dim3 grid((unsigned)((T + a.tokens - 1) / a.tokens));
   const cudaError_t e =
-      D == 128 ? launch(kv_read_q4_kernel<128>, grid, dim3(kRowThreads), 0, as_cuda(stream), k_cache,
-                        v_cache, slots, items, num_blocks, Hkv, k, v, status)
-               : launch(kv_read_q4_kernel<64>, grid, dim3(kRowThreads), 0, as_cuda(stream), k_cache,
-                        v_cache, slots, items, num_blocks, Hkv, k, v, status);
+      D == 128 ? launch(kv_read_q4_kernel<128>, grid, dim3(kRowThreads), 0, as_cuda(stream), a, k_cache,
+                        v_cache, k, v)
+               : launch(kv_read_q4_kernel<64>, grid, dim3(kRowThreads), 0, as_cuda(stream), a, k_cache,
+                        v_cache, k, v);
   return e == cudaSuccess ? TSD_OK : TSD_ERR_CUDA;
 }
 

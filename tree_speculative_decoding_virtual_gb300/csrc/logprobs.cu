@@ -12,16 +12,26 @@
 // any rows.
 //
 // One pass over the logits, so the kernel is bound by HBM (4 or 2 bytes a
-// logit).  A cluster of up to 8 CTAs takes a row; a CTA holds kChunk logits at
-// a time in registers (32 a thread), which serve the maximum, the sums and the
-// selection without a second read.  Selection: the minimum of the maxima of 32
-// disjoint groups of the chunk is at most its 32nd largest value, so only
-// values at or above it can be among the k <= 32 best; for independent logits
-// about 110 of 8192 remain, and their ranks are counted in shared memory.
-// Rows with long ties (masked vocabularies) can leave more than the buffer
-// holds: then the k-th largest value is found bit by bit and its ties are
-// taken in id order.  The CTAs' results meet through distributed shared
-// memory; nothing is written but the outputs.
+// logit).  A cluster of up to 8 CTAs takes a row (one CTA where the rows alone
+// fill the GPU); a CTA walks its slice in chunks of 4096 logits, 16 a thread, with
+// the next 16 already on the way.
+//   reference  the maximum of the CTA's first chunk is the m of its sums; a warp
+//              that meets a value more than 40 above its m moves it (e^40 leaves
+//              fp32 sums far from overflow)
+//   threshold  the k-th largest of the 256 threads' maxima over the first chunk:
+//              at least k values reach it, so only what does can be among the k
+//              best.  For independent logits hardly more than k of 4096 do.
+//   a chunk    S and T by thread, and what passes the threshold into a list in
+//              shared memory; no barrier
+//   settling   after chunks 4, 16, 64, ... and at the end the list is cut down to
+//              its k best (ranks counted) and the k-th becomes the threshold:
+//              later ids lose its ties, so from then on only more passes
+// Values that equal the first threshold are listed apart: where there are more
+// of them than that list holds (masked vocabularies), the first ones in id order
+// are looked up.  Where more pass than the list holds, the slice is taken again
+// at the end, chunk by chunk, each chunk's k-th largest value found bit by bit.
+// The CTAs' results meet through distributed shared memory; nothing is written
+// but the outputs.
 
 #include <cuda_bf16.h>
 
@@ -33,11 +43,12 @@ namespace {
 
 constexpr int kLpThreads = 256;
 constexpr int kLpWarps = kLpThreads / 32;
-constexpr int kPerThread = 32;
+constexpr int kPerThread = 16;
 constexpr int kChunk = kLpThreads * kPerThread;  // logits held at a time
 constexpr int kMaxTop = 32;
-constexpr int kGroups = 32;  // groups of 8 threads
-constexpr int kCap = 512;    // candidates the shared buffer holds
+constexpr int kCap = 512;      // candidates the list holds (kMaxTop more for ties)
+constexpr int kTies = 64;      // values equal to the threshold that are listed
+constexpr float kMove = 40.f;  // the reference follows a value so far above it
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct LpArgs {
@@ -57,14 +68,16 @@ struct LpArgs {
 };
 
 struct LpShared {
-  uint32_t group_max[kGroups];
-  float sum[kLpWarps], dsum[kLpWarps];
-  unsigned long long cand[kCap];
-  alignas(16) unsigned long long best[kMaxTop];  // this CTA's best so far, descending
-  int n_cand, n_best;
+  uint32_t sorted[kLpWarps][32];  // the threads' first maxima, descending by warp
+  float sum[kLpWarps], dsum[kLpWarps], ref[kLpWarps];
+  alignas(16) unsigned long long cand[kCap + kTies];
+  int tie[kTies];
+  int found[kLpWarps][kMaxTop], n_found[kLpWarps];
+  int n_cand, n_tie, lost;  // lost: more passed than the list holds
+  uint32_t thr;
   int reduce[kLpWarps];
   alignas(16) float m;
-  float S, T, xt;  // running: maximum, sum e^d, sum e^d d, the token's logit
+  float S, T, xt;  // the CTA's reference, sum e^d, sum e^d d, and the token's logit
 };
 
 // Integers that order as the floats do; both zeros alike, NaN above all.
@@ -114,132 +127,198 @@ __device__ __forceinline__ int chunk_pos(int e, int tid) {
   return ((e / kW) * kLpThreads + tid) * kW + e % kW;
 }
 
-// The thread's logits of [c0, end); -inf past it.
+// The thread's part of [c0, end) as loaded: 32 fp32 words, or 16 of bf16 pairs
+// (one word a logit without vector loads); -inf past the end.
 template <bool kBf16, bool kVec>
-__device__ __forceinline__ void load_chunk(const void *row, int c0, int end, int tid,
-                                           float (&x)[kPerThread]) {
-  constexpr int kW = kVec ? (kBf16 ? 8 : 4) : 1;
-  if constexpr (!kVec) {
+struct LpRaw {
+  static constexpr int kWords = kBf16 && kVec ? kPerThread / 2 : kPerThread;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void load(const void *row, int c0, int end, int tid) {
+    if constexpr (!kVec) {
 #pragma unroll
-    for (int e = 0; e < kPerThread; ++e) {
-      const int i = c0 + chunk_pos<kBf16, kVec>(e, tid);
-      if (kBf16) {
-        const uint16_t *p = reinterpret_cast<const uint16_t *>(row);
-        x[e] = i < end ? __uint_as_float((uint32_t)__ldcs(p + i) << 16) : -INFINITY;
-      } else {
-        const float *p = reinterpret_cast<const float *>(row);
-        x[e] = i < end ? __ldcs(p + i) : -INFINITY;
+      for (int e = 0; e < kPerThread; ++e) {
+        const int i = c0 + chunk_pos<kBf16, kVec>(e, tid);
+        if (kBf16)
+          w[e] = i < end ? (uint32_t)__ldcs(reinterpret_cast<const uint16_t *>(row) + i) << 16 : 0xFF800000u;
+        else
+          w[e] = i < end ? __ldcs(reinterpret_cast<const uint32_t *>(row) + i) : 0xFF800000u;
       }
-    }
-  } else {
-    uint4 w[kPerThread / kW];
+    } else {
+      constexpr int kW = kBf16 ? 8 : 4;
+      constexpr uint32_t none = kBf16 ? 0xFF80FF80u : 0xFF800000u;
 #pragma unroll
-    for (int g = 0; g < kPerThread / kW; ++g) {
-      const int i = c0 + chunk_pos<kBf16, kVec>(g * kW, tid);
-      const uint32_t none = kBf16 ? 0xFF80FF80u : 0xFF800000u;
-      w[g] = i < end ? __ldcs(reinterpret_cast<const uint4 *>(row) + i / kW)
-                     : make_uint4(none, none, none, none);
-    }
-#pragma unroll
-    for (int g = 0; g < kPerThread / kW; ++g) {
-      const uint32_t u[4] = {w[g].x, w[g].y, w[g].z, w[g].w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (kBf16) {
-          x[g * kW + 2 * j] = __uint_as_float(u[j] << 16);
-          x[g * kW + (2 * j + 1) % kW] = __uint_as_float(u[j] & 0xFFFF0000u);
-        } else {
-          x[g * kW + j] = __uint_as_float(u[j]);
-        }
+      for (int g = 0; g < kPerThread / kW; ++g) {
+        const int i = c0 + chunk_pos<kBf16, kVec>(g * kW, tid);
+        const uint4 v = i < end ? __ldcs(reinterpret_cast<const uint4 *>(row) + i / kW)
+                                : make_uint4(none, none, none, none);
+        w[4 * g] = v.x;
+        w[4 * g + 1] = v.y;
+        w[4 * g + 2] = v.z;
+        w[4 * g + 3] = v.w;
       }
     }
   }
-}
-
-// Merges the chunk's candidates with the best so far (all of them in
-// sh.cand[0, n)) into sh.best.
-__device__ __forceinline__ void rank_candidates(LpShared &sh, int n, int k) {
-  __syncthreads();
-  for (int c = threadIdx.x; c < n; c += kLpThreads) {
-    const unsigned long long mine = sh.cand[c];
-    int rank = 0;
-    for (int o = 0; o < n; ++o) rank += sh.cand[o] > mine ? 1 : 0;
-    if (rank < k) sh.best[rank] = mine;
+  __device__ __forceinline__ float get(int e) const {
+    if constexpr (kBf16 && kVec)
+      return __uint_as_float((e & 1) ? w[e / 2] & 0xFFFF0000u : w[e / 2] << 16);
+    else
+      return __uint_as_float(w[e]);
   }
-  if (threadIdx.x == 0) sh.n_best = min(n, k);
-  __syncthreads();
+};
+
+template <bool kBf16>
+__device__ __forceinline__ float one_logit(const void *row, int i) {
+  if constexpr (kBf16)
+    return __uint_as_float((uint32_t)reinterpret_cast<const uint16_t *>(row)[i] << 16);
+  else
+    return reinterpret_cast<const float *>(row)[i];
 }
 
-// The chunk's part in the k best (see the head of the file).  floor_ord: the
-// minimum of the groups' maxima.
+// Keeps the k best of sh.cand[0, n), descending, in place; returns how many
+// there are.  Called by the whole block with the buffer complete; leaves it
+// complete.
+__device__ __forceinline__ int keep_best(LpShared &sh, int n, int k) {
+  __syncthreads();
+  constexpr int kMine = (kCap + kTies + kLpThreads - 1) / kLpThreads;
+  unsigned long long mine[kMine];
+  int rank[kMine];
+#pragma unroll
+  for (int q = 0; q < kMine; ++q) {
+    const int c = threadIdx.x + q * kLpThreads;
+    mine[q] = c < n ? sh.cand[c] : 0ull;
+    rank[q] = kCap;
+    if (c < n) {
+      int r = 0;
+#pragma unroll 4
+      for (int o = 0; o < n; ++o) r += sh.cand[o] > mine[q] ? 1 : 0;
+      rank[q] = r;
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < kMine; ++q)
+    if (rank[q] < k) sh.cand[rank[q]] = mine[q];
+  const int left = min(n, k);
+  if (threadIdx.x == 0) sh.n_cand = left;
+  __syncthreads();
+  return left;
+}
+
+// The k best of a slice in which more values pass the threshold than the list
+// holds: chunk by chunk, the k-th largest value T of the chunk bit by bit (the
+// largest T that k values reach), then T's ties in id order.  Out of line: it is
+// rare, and its registers are not the main path's.
 template <bool kBf16, bool kVec>
-__device__ __forceinline__ void select_chunk(LpShared &sh, const float (&x)[kPerThread], int c0,
-                                             int end, int k, uint32_t floor_ord) {
+__device__ __noinline__ void select_exact(LpShared &sh, const void *row, int first, int last, int k) {
   const int tid = threadIdx.x;
-  const int nb = sh.n_best;
-  if (nb == k) floor_ord = max(floor_ord, (uint32_t)(sh.best[k - 1] >> 32));
-  if (tid < nb) sh.cand[tid] = sh.best[tid];
-  if (tid == 0) sh.n_cand = nb;
-  __syncthreads();
-  const float lowest = unordered(floor_ord);
+  int held = 0;
+  for (int c0 = first; c0 < last; c0 += kChunk) {
+    const int end = min(last, c0 + kChunk);
+    LpRaw<kBf16, kVec> x;
+    x.load(row, c0, end, tid);
+    uint32_t T = 0;
+    for (int bit = 31; bit >= 0; --bit) {
+      const uint32_t t = T | (1u << bit);
+      int mine = 0;
 #pragma unroll
-  for (int e = 0; e < kPerThread; ++e) {
-    // (a NaN floor leaves only NaN, a NaN logit passes any floor)
-    if (!(x[e] < lowest)) {
-      const int id = c0 + chunk_pos<kBf16, kVec>(e, tid);
-      const uint32_t o = ordered(x[e]);
-      if (id < end && o >= floor_ord) {
-        const int at = atomicAdd(&sh.n_cand, 1);
-        if (at < kCap) sh.cand[at] = lp_key(o, id);
-      }
+      for (int e = 0; e < kPerThread; ++e)
+        mine += (c0 + chunk_pos<kBf16, kVec>(e, tid) < end && ordered(x.get(e)) >= t) ? 1 : 0;
+      if (block_sum(mine, sh.reduce) >= k) T = t;
     }
-  }
-  __syncthreads();
-  const int n = sh.n_cand;
-  if (n <= kCap) {
-    rank_candidates(sh, n, k);
-    return;
-  }
-  // Too many: the k-th largest value of the chunk, bit by bit (the largest T
-  // with at least k values >= T), then its ties in id order.
-  uint32_t T = 0;
-  for (int bit = 31; bit >= 0; --bit) {
-    const uint32_t t = T | (1u << bit);
-    int mine = 0;
-#pragma unroll
-    for (int e = 0; e < kPerThread; ++e)
-      mine += (c0 + chunk_pos<kBf16, kVec>(e, tid) < end && ordered(x[e]) >= t) ? 1 : 0;
-    if (block_sum(mine, sh.reduce) >= k) T = t;
-  }
-  __syncthreads();
-  if (tid == 0) sh.n_cand = nb;
-  __syncthreads();
-  int above = 0;
-#pragma unroll
-  for (int e = 0; e < kPerThread; ++e) {
-    const int id = c0 + chunk_pos<kBf16, kVec>(e, tid);
-    const uint32_t o = ordered(x[e]);
-    if (id < end && o > T) {  // fewer than k of them
-      sh.cand[atomicAdd(&sh.n_cand, 1)] = lp_key(o, id);
-      ++above;
-    }
-  }
-  int left = k - block_sum(above, sh.reduce);
-  int after = -1;  // the last tie taken
-  for (; left > 0; --left) {
-    int id = 0x7FFFFFFF;
+    __syncthreads();
+    if (tid == 0) sh.n_cand = held;
+    __syncthreads();
+    int above = 0;
 #pragma unroll
     for (int e = 0; e < kPerThread; ++e) {
-      const int i = c0 + chunk_pos<kBf16, kVec>(e, tid);
-      if (i < end && i > after && ordered(x[e]) == T) id = min(id, i);
+      const int id = c0 + chunk_pos<kBf16, kVec>(e, tid);
+      const uint32_t o = ordered(x.get(e));
+      if (id < end && o > T) {  // fewer than k of them
+        sh.cand[atomicAdd(&sh.n_cand, 1)] = lp_key(o, id);
+        ++above;
+      }
     }
-    id = block_min(id, sh.reduce);
-    if (id == 0x7FFFFFFF) break;
-    if (tid == 0) sh.cand[sh.n_cand++] = lp_key(T, id);
-    after = id;
+    int left = k - block_sum(above, sh.reduce);
+    int after = -1;  // the last tie taken
+    for (; left > 0; --left) {
+      int id = 0x7FFFFFFF;
+#pragma unroll
+      for (int e = 0; e < kPerThread; ++e) {
+        const int i = c0 + chunk_pos<kBf16, kVec>(e, tid);
+        if (i < end && i > after && ordered(x.get(e)) == T) id = min(id, i);
+      }
+      id = block_min(id, sh.reduce);
+      if (id == 0x7FFFFFFF) break;
+      if (tid == 0) sh.cand[sh.n_cand++] = lp_key(T, id);
+      after = id;
+    }
+    __syncthreads();
+    held = keep_best(sh, sh.n_cand, k);
+  }
+}
+
+// The first `need` (at most 32) ids of [first, last) whose logit equals the
+// threshold, appended to the list: every warp looks through its share from the
+// front, then the shares' finds are taken in order.
+template <bool kBf16>
+__device__ __noinline__ void find_ties(LpShared &sh, const void *row, int first, int last, int need) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t thr = sh.thr;
+  const int share = (last - first + kLpWarps - 1) / kLpWarps;
+  const int a = first + warp * share, z = min(last, a + share);
+  int got = 0;
+  for (int i0 = a; i0 < z && got < need; i0 += 32) {
+    const int i = i0 + lane;
+    const bool hit = i < z && ordered(one_logit<kBf16>(row, i)) == thr;
+    const unsigned hits = __ballot_sync(0xffffffffu, hit);
+    const int at = got + __popc(hits & ((1u << lane) - 1u));
+    if (hit && at < need) sh.found[warp][at] = i;
+    got += __popc(hits);
+  }
+  if (lane == 0) sh.n_found[warp] = min(got, need);
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    int n = sh.n_cand;
+    for (int w = 0; w < kLpWarps && need > 0; ++w)
+      for (int f = 0; f < sh.n_found[w] && need > 0; ++f, --need) sh.cand[n++] = lp_key(thr, sh.found[w][f]);
+    sh.n_cand = n;
   }
   __syncthreads();
-  rank_candidates(sh, sh.n_cand, k);
+}
+
+// Cuts the list down to the k best of [first, end), the part of the slice seen so
+// far, and makes the k-th the threshold when there are k.  `settled`: the
+// threshold is such a one, and its ties are not wanted.  Returns whether it is
+// now.  Called by the whole block.
+template <bool kBf16>
+__device__ __forceinline__ bool settle(LpShared &sh, const void *row, int first, int end, int k, bool settled) {
+  __syncthreads();
+  int n = sh.n_cand;
+  const int ties = sh.n_tie;
+  __syncthreads();
+  if (n > kCap) {  // (stays lost; the list goes on from nothing)
+    if (threadIdx.x == 0) {
+      sh.lost = 1;
+      sh.n_cand = 0;
+    }
+    __syncthreads();
+    return settled;
+  }
+  if (!settled && n < k) {
+    if (ties > kTies) {
+      find_ties<kBf16>(sh, row, first, end, k - n);
+    } else {
+      if (threadIdx.x < ties) sh.cand[n + threadIdx.x] = lp_key(sh.thr, sh.tie[threadIdx.x]);
+      if (threadIdx.x == 0) sh.n_cand = n + ties;
+      __syncthreads();
+    }
+    n = sh.n_cand;
+  }
+  n = keep_best(sh, n, k);
+  if (n < k) return settled;
+  if (threadIdx.x == 0) sh.thr = (uint32_t)(sh.cand[k - 1] >> 32);
+  __syncthreads();
+  return true;
 }
 
 // Output row r: its row of logits and its token; false where there is none
@@ -275,7 +354,7 @@ __device__ __forceinline__ bool lp_resolve(const LpArgs &a, int r, int64_t &row,
 }
 
 template <bool kBf16, bool kVec>
-__global__ void __launch_bounds__(kLpThreads, 3) logprobs_kernel(const LpArgs a) {
+__global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const LpArgs a) {
   using namespace sm100;
   __shared__ LpShared sh;
   pdl_trigger();
@@ -304,93 +383,152 @@ __global__ void __launch_bounds__(kLpThreads, 3) logprobs_kernel(const LpArgs a)
   }
   const void *src = reinterpret_cast<const char *>(a.logits) + (size_t)row * a.V * (kBf16 ? 2 : 4);
   if (tid == 0) {
-    sh.n_best = 0;
-    sh.m = -INFINITY;
-    sh.S = 0.f;
-    sh.T = 0.f;
+    sh.n_cand = 0;
+    sh.n_tie = 0;
+    sh.lost = 0;
     sh.xt = -INFINITY;
   }
   const int first = rank * a.per, last = min(a.V, first + a.per);
-  for (int c0 = first; c0 < last; c0 += kChunk) {
-    const int end = min(last, c0 + kChunk);
-    float x[kPerThread];
-    load_chunk<kBf16, kVec>(src, c0, end, tid, x);
-    float top = -INFINITY;  // fmaxf drops a NaN, so those are looked for apart
-    bool nan = false;
+  if (first < last) {
+    // the logit asked for, read apart from the stream (its line is in flight
+    // anyway)
+    if (tid == 0 && token >= first && token < last) sh.xt = one_logit<kBf16>(src, token);
+    LpRaw<kBf16, kVec> x, next;
+    x.load(src, first, min(last, first + kChunk), tid);
+    // (fmaxf drops a NaN: a threshold may be too low, not too high, and the sums
+    // keep the NaN)
+    float top = -INFINITY;
 #pragma unroll
-    for (int e = 0; e < kPerThread; ++e) {
-      top = fmaxf(top, x[e]);
-      nan = nan || x[e] != x[e];
-    }
-    uint32_t best = nan ? 0xFFFFFFFFu : ordered(top);
+    for (int e = 0; e < kPerThread; ++e) top = fmaxf(top, x.get(e));
+    uint32_t o = ordered(top);
+    if (k > 0) {  // descending over the warp's lanes
 #pragma unroll
-    for (int off = 1; off < 8; off <<= 1)
-      best = max(best, __shfl_xor_sync(0xffffffffu, best, off));
-    __syncthreads();  // the previous chunk's shared state is read
-    if ((lane & 7) == 0) sh.group_max[tid >> 3] = best;
-    __syncthreads();
-    const uint32_t gm = sh.group_max[lane];
-    const float m = unordered(__reduce_max_sync(0xffffffffu, gm));
-    const uint32_t floor_ord = __reduce_min_sync(0xffffffffu, gm);
-    // d = -200 stands for every d that e^d rounds to zero for (-inf included);
-    // a maximum that is NaN or +inf makes the row's sums NaN below
-    float S = 0.f, T = 0.f;
+      for (int size = 2; size <= 32; size <<= 1) {
 #pragma unroll
-    for (int e = 0; e < kPerThread; ++e) {
-      const float d = fmaxf(x[e] - m, -200.f);
-      const float p = ex2_approx(d * kLog2e);
-      S += p;
-      T = fmaf(p, d, T);
-    }
-    if (token >= c0 && token < end && kVec) {
-      const int o = token - c0;
-      constexpr int kW = kBf16 ? 8 : 4;
-      if ((o / kW) % kLpThreads == tid) {
-#pragma unroll
-        for (int e = 0; e < kPerThread; ++e)
-          if (chunk_pos<kBf16, kVec>(e, tid) == o) sh.xt = x[e];
+        for (int step = size >> 1; step; step >>= 1) {
+          const uint32_t other = __shfl_xor_sync(0xffffffffu, o, step);
+          const bool high = ((lane & step) == 0) == ((lane & size) == 0 || size == 32);
+          o = high ? max(o, other) : min(o, other);
+        }
       }
-    } else if (token >= c0 && token < end) {
+    } else {
+      o = __reduce_max_sync(0xffffffffu, o);
+    }
+    sh.sorted[warp][lane] = o;
+    __syncthreads();
+    float m = unordered(__reduce_max_sync(0xffffffffu, sh.sorted[lane & (kLpWarps - 1)][0]));
+    if (lane < k) {
+      // rank of this thread's maximum among all 256 (equal ones by warp)
+      int above = lane;
+      for (int w = 0; w < kLpWarps; ++w) {
+        if (w == warp) continue;
+        int lo = 0, hi = 32;
+        while (lo < hi) {
+          const int mid = (lo + hi) >> 1;
+          const uint32_t v = sh.sorted[w][mid];
+          if (v > o || (v == o && w < warp)) lo = mid + 1; else hi = mid;
+        }
+        above += lo;
+      }
+      if (above == k - 1) sh.thr = o;
+    }
+    __syncthreads();
+    // what reaches `gate` passes (without alternatives: what moves the reference)
+    uint32_t thr_ord = k > 0 ? sh.thr : ordered(m + kMove);
+    float gate = unordered(thr_ord);
+    bool settled = false;
+    int next_settle = first + 4 * kChunk;
+
+    float S = 0.f, T = 0.f;
+    for (int c0 = first; c0 < last; c0 += kChunk) {
+      const int end = min(last, c0 + kChunk);
+      if (end < last) next.load(src, end, min(last, end + kChunk), tid);
+      bool below = true;
 #pragma unroll
-      for (int e = 0; e < kPerThread; ++e)
-        if (chunk_pos<kBf16, kVec>(e, tid) == token - c0) sh.xt = x[e];
+      for (int e = 0; e < kPerThread; ++e) below = below && x.get(e) < gate;  // (false for a NaN)
+      if (!below) {
+        uint32_t mine = 0u;
+#pragma unroll
+        for (int e = 0; e < kPerThread; ++e) mine |= (x.get(e) < gate ? 0u : 1u) << e;
+        top = -INFINITY;
+        // (the few that pass are read again: indexing the registers would spill them)
+        for (; mine; mine &= mine - 1) {
+          const int id = c0 + chunk_pos<kBf16, kVec>(__ffs(mine) - 1, tid);
+          if (id >= end) continue;
+          const float v = one_logit<kBf16>(src, id);
+          const uint32_t vo = ordered(v);
+          top = fmaxf(top, v);
+          if (k == 0) continue;
+          if (vo > thr_ord) {
+            const int at = atomicAdd(&sh.n_cand, 1);
+            if (at < kCap) sh.cand[at] = lp_key(vo, id);
+          } else if (vo == thr_ord && !settled && sh.n_tie <= kTies) {
+            const int at = atomicAdd(&sh.n_tie, 1);
+            if (at < kTies) sh.tie[at] = id;
+          }
+        }
+      }
+      __syncwarp();
+      if (__any_sync(0xffffffffu, !below && top > m + kMove)) {  // the warp's reference follows
+        const float up = unordered(__reduce_max_sync(0xffffffffu, ordered(below ? -INFINITY : top)));
+        const float f = m == -INFINITY ? 0.f : ex2_approx((m - up) * kLog2e);
+        T = f == 0.f ? 0.f : f * (T + S * (m - up));
+        S = f * S;
+        m = up;
+      }
+      // d = -200 stands for every d that e^d rounds to zero for, -inf included; a
+      // NaN reaches S and T through e^d, and so does +inf (m = +inf: inf - inf)
+      const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll
+      for (int e = 0; e < kPerThread; ++e) {
+        const float d = x.get(e) - base;
+        const float p = ex2_approx(d * kLog2e);
+        S += p;
+        T = fmaf(p, fmaxf(d, -200.f), T);
+      }
+      if (k > 0 && (end == next_settle || end == last)) {
+        settled = settle<kBf16>(sh, src, first, end, k, settled);
+        if (settled) {
+          thr_ord = sh.thr;
+          gate = unordered(thr_ord == 0xFFFFFFFFu ? thr_ord : thr_ord + 1u);
+        }
+        next_settle = first + 4 * (next_settle - first);
+      }
+      x = next;
     }
     S = warp_sum(S);
     T = warp_sum(T);
     if (lane == 0) {
       sh.sum[warp] = S;
       sh.dsum[warp] = T;
+      sh.ref[warp] = m;
     }
     __syncthreads();
     if (tid == 0) {
+      float M = -INFINITY;
+      for (int w = 0; w < kLpWarps; ++w) M = fmaxf(M, sh.ref[w]);
       S = 0.f;
       T = 0.f;
-#pragma unroll
       for (int w = 0; w < kLpWarps; ++w) {
-        S += sh.sum[w];
-        T += sh.dsum[w];
-      }
-      if (m == -INFINITY) S = T = 0.f;
-      if (!(m < INFINITY)) S = T = __uint_as_float(0x7FC00000u);
-      // join with the chunks before it
-      const float m0 = sh.m;
-      const float M = (m0 != m0 || m != m) ? __uint_as_float(0x7FC00000u) : fmaxf(m0, m);
-      float S1 = 0.f, T1 = 0.f;
-      if (m0 != -INFINITY) {
-        const float f = ex2_approx((m0 - M) * kLog2e);
-        S1 = f * sh.S;
-        T1 = f == 0.f ? 0.f : f * (sh.T + sh.S * (m0 - M));
-      }
-      if (m != -INFINITY) {
-        const float f = ex2_approx((m - M) * kLog2e);
-        S1 += f * S;
-        T1 += f == 0.f ? 0.f : f * (T + S * (m - M));
+        const float r = sh.ref[w];
+        // (a reference of -inf: nothing but -inf, or NaN)
+        const float f = r == M || r == -INFINITY ? 1.f : ex2_approx((r - M) * kLog2e);
+        const float by = r == M || r == -INFINITY ? 0.f : r - M;
+        S += f * sh.sum[w];
+        T += f == 0.f ? 0.f : f * (sh.dsum[w] + sh.sum[w] * by);
       }
       sh.m = M;
-      sh.S = S1;
-      sh.T = T1;
+      sh.S = S;
+      sh.T = T;
     }
-    if (k > 0) select_chunk<kBf16, kVec>(sh, x, c0, end, k, floor_ord);
+    if (sh.lost) {  // (the barriers above made it visible)
+      __syncthreads();
+      select_exact<kBf16, kVec>(sh, src, first, last, k);
+    }
+  } else if (tid == 0) {
+    sh.m = -INFINITY;
+    sh.S = 0.f;
+    sh.T = 0.f;
   }
   __syncthreads();
   if (ctas > 1) {
@@ -409,7 +547,7 @@ __global__ void __launch_bounds__(kLpThreads, 3) logprobs_kernel(const LpArgs a)
       cm[c] = v.x;
       cS[c] = v.y;
       cT[c] = v.z;
-      nan = nan || v.x != v.x;
+      nan = nan || v.y != v.y;
       M = fmaxf(M, v.x);
       if (token >= c * a.per && token < (c + 1) * a.per) xt = v.w;
     }
@@ -434,7 +572,7 @@ __global__ void __launch_bounds__(kLpThreads, 3) logprobs_kernel(const LpArgs a)
     for (int c = warp; c < ctas; c += kLpWarps) {
       // lane l reads entries 2 (l % 16) and 2 (l % 16) + 1 of the list of CTA c
       if (lane < kMaxTop / 2) {
-        const float4 v = ld_dsmem_f4(smem_addr(&sh.best[lane * 2]), c);
+        const float4 v = ld_dsmem_f4(smem_addr(&sh.cand[lane * 2]), c);
         const unsigned long long k0 =
             (unsigned long long)__float_as_uint(v.x) | ((unsigned long long)__float_as_uint(v.y) << 32);
         const unsigned long long k1 =
@@ -491,9 +629,11 @@ cudaError_t lp_launch(const LpArgs &a, int R, int ctas, cudaStream_t stream) {
 }
 
 int lp_run(LpArgs &a, int R, int bf16, tsd_stream_t stream) {
-  // a CTA for every chunk of a row, up to 8 (a power of two)
+  // CTAs of a row: as many (a power of two, up to 8, at most one a chunk) as let
+  // all rows run at once at four CTAs an SM, because a slice's first chunk and
+  // its end cost more than its stream
   int ctas = 1;
-  while (ctas < 8 && (int64_t)ctas * kChunk < a.V) ctas *= 2;
+  while (ctas < 8 && (int64_t)ctas * kChunk < a.V && 2ll * ctas * R <= 4ll * sm_count()) ctas *= 2;
   a.per = ((a.V + ctas - 1) / ctas + 7) / 8 * 8;
   const bool vec = aligned(a.logits, 16) && a.V % (bf16 ? 8 : 4) == 0;
   const cudaStream_t s = as_cuda(stream);
