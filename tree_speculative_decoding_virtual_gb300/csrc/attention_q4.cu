@@ -358,9 +358,11 @@ __global__ void __launch_bounds__(kRowsThreads, 2) tree_attn_q4_rows_kernel(cons
             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
             if (m > trig[n][e]) {  // the same decision in the eight lanes of the row
-              const float f = trig[n][e] == -INFINITY ? 0.f : ex2_approx(ref[n][e] - (m - kOffset));
-              trig[n][e] = m + kSlack;
-              ref[n][e] = m - kOffset;
+              // (for scores whose ulp is coarser than these steps: at the maximum)
+              const float to = m - (m - kOffset) <= kOffset ? m - kOffset : m;
+              const float f = trig[n][e] == -INFINITY ? 0.f : ex2_approx(ref[n][e] - to);
+              trig[n][e] = (m + kSlack) - m <= kSlack ? m + kSlack : m;
+              ref[n][e] = to;
               l[n][e] *= f;
 #pragma unroll
               for (int j = 0; j < kTiles; ++j) {

@@ -47,6 +47,7 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemChain = 256, kTmemO = 128;
 constexpr float kTcOffset = 8.f;    // P of the reference score is 2^8 .. 2^9
 constexpr float kTcMaxSum = 60000.f;
+constexpr float kTcLargeRef = 65536.f;  // a product there is off by 2^-8 at most
 constexpr float kTcLn2 = 0.6931471805599453f;
 constexpr uint64_t kTcDrainNs = 100000000ull;
 
@@ -192,18 +193,31 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4
     // straight to the teardown
   } else if (warp == 0) {
     // ---- loader: lane l < 8 copies page l of the item ----
+    // Block ids come 32 (four tiles) at a time and a batch ahead: read for each
+    // item, their latency was on every item's path (1.35 us a tile).
     const int32_t *trow = p.table + (size_t)b * p.max_blocks;
+    auto read_ids = [&](int tile) {  // of the batch that starts at `tile`
+      const int pg = first + tile * kTilePages + lane;
+      return pg < last ? __ldg(trow + pg) : 0;
+    };
+    int before = 0, ids = read_ids(0), ahead = read_ids(4);  // V runs a tile behind K
     bool ok = true;
     int issued = 0;
     for (int m = 0; m < 2 * n; ++m) {
       int tile;
       bool is_v;
       stream_item(m, n, tile, is_v);
+      if (!is_v && tile > 0 && (tile & 3) == 0) {
+        before = ids;
+        ids = ahead;
+        ahead = read_ids(tile + 4);
+      }
       const int slot = m % kPackSlots;
-      const int pg = first + tile * kTilePages + lane;
-      const bool mine = lane < kTilePages && pg < last;
-      const int id = mine ? __ldg(trow + pg) : 0;
-      const bool bad = id < 0 || id >= p.num_blocks;
+      // (a V tile whose K's batch is not the current one: the last before a new batch)
+      const bool old = is_v && (tile & 3) == 3 && tile + 1 < n;
+      const int id = __shfl_sync(0xffffffffu, old ? before : ids, (tile & 3) * kTilePages + (lane & 7));
+      const bool mine = lane < kTilePages && first + tile * kTilePages + lane < last;
+      const bool bad = mine && (id < 0 || id >= p.num_blocks);
       if (bad) sh.bad = 1;
       if (m >= kPackSlots)
         ok = __all_sync(0xffffffffu, tc_wait(sh.pk_empty[slot], ((m / kPackSlots) - 1) & 1, lim, abort));
@@ -315,16 +329,27 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4
       // the two halves of a key are stored in opposite order, so that the
       // eight lanes of a store's quarter touch different banks
       const int flip = D == 128 ? grp >> 2 : 0;
-#pragma unroll 4
-      for (int s = 0; s < kBN / (4 * kKeys); ++s) {
+      // every read comes before the first store: the compiler must assume that a
+      // store changes what the next read sees, and would wait out each one's
+      // latency (1.4 us a 128-key tile that way)
+      constexpr int kSteps = kBN / (4 * kKeys);
+      uint2 code[kSteps];
+      uint32_t scale[kSteps];
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
         const int key = (s * 4 + dw) * kKeys + kl;
         const uint8_t *page = src + (key / kPage) * Page::kBytes;
         const int r = key % kPage;
-        const uint2 code = *reinterpret_cast<const uint2 *>(page + r * Page::kRow + grp * 8);
-        const uint32_t sc = q4_scale2(page[Page::kScales + r * Page::kScaleRow + grp]);
+        code[s] = *reinterpret_cast<const uint2 *>(page + r * Page::kRow + grp * 8);
+        scale[s] = page[Page::kScales + r * Page::kScaleRow + grp];
+      }
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+        const int key = (s * 4 + dw) * kKeys + kl;
+        const uint32_t sc = q4_scale2(scale[s]);
         uint32_t a[4], e[4];
-        q4_decode8(flip ? code.y : code.x, a);
-        q4_decode8(flip ? code.x : code.y, e);
+        q4_decode8(flip ? code[s].y : code[s].x, a);
+        q4_decode8(flip ? code[s].x : code[s].y, e);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           a[i] = q4_mul2(a[i], sc);
@@ -423,44 +448,49 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4
             if (!((vis >> i) & 1u)) s[i] = 0xFF800000u;
         }
         uint32_t pk[16];
-        float sum;
-        auto probabilities = [&]() {
-          const unsigned long long ref2 = f2_pack(-ref, -ref);
-          unsigned long long acc0 = 0ull, acc1 = 0ull;
+        // P against the reference, the fp16 pairs and their sum
+        unsigned long long acc0 = 0ull, acc1 = 0ull;
+        const unsigned long long ref2 = f2_pack(-ref, -ref);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            // the product is rounded before the reference is taken off, as the
-            // reference itself was: one fused step would be off by half an ulp
-            // of a large score, which can be many powers of two
-            const float2 t = f2_unpack(
-                f2_add(f2_mul(f2_pack(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), mul2), ref2));
-            const float e0 = ex2_approx(t.x), e1 = ex2_approx(t.y);
-            pk[i] = pack_half2(e0, e1);
-            if (i & 1) acc1 = f2_add(acc1, f2_pack(e0, e1));
-            else acc0 = f2_add(acc0, f2_pack(e0, e1));
-          }
-          const float2 a = f2_unpack(f2_add(acc0, acc1));
-          sum = a.x + a.y;
-        };
-        probabilities();
-        const bool mine = (unset && vis != 0u) || !(sum <= kTcMaxSum);
-        if (__any_sync(0xffffffffu, mine)) {
+        for (int i = 0; i < 16; ++i) {
+          const float2 t = f2_unpack(
+              f2_fma(f2_pack(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), mul2, ref2));
+          const float e0 = ex2_approx(t.x), e1 = ex2_approx(t.y);
+          pk[i] = pack_half2(e0, e1);
+          if (i & 1) acc1 = f2_add(acc1, f2_pack(e0, e1));
+          else acc0 = f2_add(acc0, f2_pack(e0, e1));
+        }
+        const float2 acc = f2_unpack(f2_add(acc0, acc1));
+        float sum = acc.x + acc.y;
+        // Rows that need more than that: no reference yet, P out of fp16's range, or
+        // a reference (itself a rounded product) so large that the exact product
+        // above lies powers of two away from it; those round the product first.
+        const bool mine = (unset && vis != 0u) || !(sum <= kTcMaxSum) || fabsf(ref) >= kTcLargeRef;
+        if (__builtin_expect(__any_sync(0xffffffffu, mine), 0)) {
           float f = 1.f;
           if (mine) {
             float m = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) m = fmaxf(m, (vis >> i) & 1u ? __uint_as_float(s[i]) * mul : -INFINITY);
-            if (m > -INFINITY) {
-              const float to = floorf(m) - kTcOffset;
-              // (the exponent of a move down from a first, unset reference does
-              // not matter: nothing was added yet)
+            for (int i = 0; i < 32; ++i)
+              m = fmaxf(m, (vis >> i) & 1u ? __fmul_rn(__uint_as_float(s[i]), mul) : -INFINITY);
+            if (m > -INFINITY && (unset || !(m - ref <= kTcOffset + 2.f))) {
+              float to = floorf(m) - kTcOffset;
+              if (!(m - to <= kTcOffset + 1.f)) to = m;  // 8 is less than an ulp of m
+              // (nothing was added yet to a row without a reference)
               if (!unset) f = ex2_approx(ref - to);
               ref = to;
               unset = false;
               l *= f;
             }
+            sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float e0 = ex2_approx(__fsub_rn(__fmul_rn(__uint_as_float(s[2 * i]), mul), ref));
+              const float e1 = ex2_approx(__fsub_rn(__fmul_rn(__uint_as_float(s[2 * i + 1]), mul), ref));
+              pk[i] = pack_half2(e0, e1);
+              sum += e0 + e1;
+            }
           }
-          probabilities();
           // what is already in TMEM for these rows: O, and this tile's P
           if (__any_sync(0xffffffffu, f != 1.f)) {
             if (u > 0) {
