@@ -10,21 +10,24 @@
 //                ring of packed tiles
 //   warp 1       owns TMEM; lane 0 issues every MMA
 //   warps 4-7    decode packed tiles to fp16 K and V tiles (128-byte swizzle)
-//   warps 8-11   softmax of chain 0, warps 12-15 of chain 1: one TMEM lane (=
-//                one query row) per thread
+//   warps 8-15   softmax of chain 0, warps 16-23 of chain 1: one TMEM lane (=
+//                one query row) per thread, two threads a row (64 keys each)
 // A chain is a row tile of 128 rows with its S (128 columns of TMEM, P over
 // the first 64) and O.  With more than 128 rows the two chains are two row
 // tiles that share every key tile; with fewer, chain c takes the key tiles j =
 // c mod 2 of the same rows and the two are joined at the end.  Per tile:
 //   S = Q K^T         M = 128, N = 128, fp16 in, fp32 accumulate
-//   P = exp2(S c - m) fp16 over S, taken 32 keys at a time
+//   P = exp2(S c - m) fp16, over the first half of S
 //   O += P V          A from TMEM, V MN-major
 // The MMAs of a chain execute in issue order, S_{j+1} right behind P_j V_j, so
-// the softmax that sees S_j complete may rescale O and overwrite S_j.  The
-// reference m is a whole number (in log2 units), so moving it multiplies what
-// is already there, P in fp16 included, by an exact power of two; it moves
-// when 32 keys' P sum above 60000, i.e. before one of them can pass fp16's
-// range, and each row decides on its own scores alone.
+// the softmax that sees S_j complete may rescale O and overwrite S_j.  A chain
+// is a loop of S, softmax, P V: for the tensor cores to stay busy the softmax has
+// to take no longer than the other chain's MMAs (about 1280 cycles a tile), hence
+// two threads a row.  They use one reference m, which moves before 64 keys' P can
+// sum above 60000, i.e. before one of them can pass fp16's range; each row
+// decides on its own scores alone.  Every tile ends in one barrier of the chain's
+// softmax threads, after which P may go over S, and which says whether some row
+// needs more than the plain path (no reference yet, or one to move).
 // Pages of a tile that lie past the sequence are not fetched: whatever their
 // bytes are, they decode to finite values and their P is 0.
 // Every wait is bounded; on expiry the block flags TSD_STATUS_TIMEOUT, drains
@@ -38,7 +41,7 @@
 namespace tsd {
 namespace {
 
-constexpr int kTcThreads = 512;
+constexpr int kTcThreads = 768;
 constexpr int kBM = 128;            // rows of a chain's MMA
 constexpr int kBN = 128;            // keys of a tile
 constexpr int kTilePages = kBN / kPage;
@@ -70,7 +73,10 @@ struct TcShared {
   uint64_t pk_full[kPackSlots], pk_empty[kPackSlots];
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
   uint64_t s_full[2], p_full[2], o_final[2], q_full, drain;
-  float2 ml[kBM];  // chain 1's (reference, sum) when it shares chain 0's rows
+  float2 ml[kBM];           // chain 1's (reference, sum) when it shares chain 0's rows
+  float half[2][2][kBM];    // by chain, thread of the row, row: exchange between the two
+  uint8_t asks[2][2][kBM];  // likewise
+  int stop[2][2];           // by chain and tile parity: a wait ran out
   uint32_t tmem_base;
   int abort, bad;
 };
@@ -108,6 +114,45 @@ __device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32]) {
                  "+r"(r[30]), "+r"(r[31])
                :
                : "memory");
+}
+
+// Register split of the six warpgroups (80 a thread at launch, 480 in all).
+template <int kRegs>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kRegs));
+}
+constexpr int kRegsLaunch = 80, kRegsIssue = 56, kRegsDecode = 72, kRegsSoftmax = 88;
+static_assert(kRegsIssue + kRegsDecode + 4 * kRegsSoftmax <= 6 * kRegsLaunch, "what the block was launched with");
+
+// Barrier of a chain's 256 softmax threads; returns whether any passed true.
+__device__ __forceinline__ bool chain_any(int c, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, 256, p;\n"
+      " selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"((uint32_t)x), "r"(2 + c)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void chain_sync(int c) {
+  asm volatile("barrier.cta.sync %0, 256;\n" ::"r"(2 + c) : "memory");
+}
+
+// Scores of the 32 keys from tail index j0 on: what the row may not see becomes
+// -inf.  Returns the visible ones.
+__device__ __forceinline__ uint32_t mask_scores(const Q4Attn &p, int b, int node, bool rvalid, int j0, int nb,
+                                                uint32_t (&s)[32]) {
+  const uint32_t vis =
+      rvalid ? q4_visible(p, b, node, j0, nb) | (q4_visible(p, b, node, j0 + 16, nb) << 16) : 0u;
+#pragma unroll
+  for (int i = 0; i < 32; ++i)
+    if (!((vis >> i) & 1u)) s[i] = 0xFF800000u;
+  return vis;
 }
 
 // Item m of the packed stream: K_0, then K_i and V_{i-1} for i = 1 .. n - 1,
@@ -168,13 +213,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4
       mbar_init(smem_addr(&sh.v_full[i]), 4);
       mbar_init(smem_addr(&sh.v_empty[i]), 1);
       mbar_init(smem_addr(&sh.s_full[i]), 1);
-      mbar_init(smem_addr(&sh.p_full[i]), 4);
+      mbar_init(smem_addr(&sh.p_full[i]), 8);
       mbar_init(smem_addr(&sh.o_final[i]), 1);
     }
-    mbar_init(smem_addr(&sh.q_full), 8);
+    mbar_init(smem_addr(&sh.q_full), 16);
     mbar_init(smem_addr(&sh.drain), 1);
     sh.abort = 0;
     sh.bad = 0;
+    sh.stop[0][0] = sh.stop[0][1] = sh.stop[1][0] = sh.stop[1][1] = 0;
     fence_mbar_init();
   }
   if (warp == 1) tmem_alloc(smem_addr(&sh.tmem_base), kTmemCols);
@@ -189,126 +235,122 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4
   const bool two = row0 + kBM < rows_valid && rows_per_block > kBM;
   const int chains = two ? 2 : (n > 1 ? 2 : 1);
 
-  if (!work) {
-    // straight to the teardown
-  } else if (warp == 0) {
-    // ---- loader: lane l < 8 copies page l of the item ----
-    // Block ids come 32 (four tiles) at a time and a batch ahead: read for each
-    // item, their latency was on every item's path (1.35 us a tile).
-    const int32_t *trow = p.table + (size_t)b * p.max_blocks;
-    auto read_ids = [&](int tile) {  // of the batch that starts at `tile`
-      const int pg = first + tile * kTilePages + lane;
-      return pg < last ? __ldg(trow + pg) : 0;
-    };
-    int before = 0, ids = read_ids(0), ahead = read_ids(4);  // V runs a tile behind K
-    bool ok = true;
-    int issued = 0;
-    for (int m = 0; m < 2 * n; ++m) {
-      int tile;
-      bool is_v;
-      stream_item(m, n, tile, is_v);
-      if (!is_v && tile > 0 && (tile & 3) == 0) {
-        before = ids;
-        ids = ahead;
-        ahead = read_ids(tile + 4);
-      }
-      const int slot = m % kPackSlots;
-      // (a V tile whose K's batch is not the current one: the last before a new batch)
-      const bool old = is_v && (tile & 3) == 3 && tile + 1 < n;
-      const int id = __shfl_sync(0xffffffffu, old ? before : ids, (tile & 3) * kTilePages + (lane & 7));
-      const bool mine = lane < kTilePages && first + tile * kTilePages + lane < last;
-      const bool bad = mine && (id < 0 || id >= p.num_blocks);
-      if (bad) sh.bad = 1;
-      if (m >= kPackSlots)
-        ok = __all_sync(0xffffffffu, tc_wait(sh.pk_empty[slot], ((m / kPackSlots) - 1) & 1, lim, abort));
-      if (!ok) break;
-      const bool copy = mine && !bad;
-      const int copies = __popc(__ballot_sync(0xffffffffu, copy));
-      const uint32_t bar = smem_addr(&sh.pk_full[slot]);
-      if (lane == 0) mbar_arrive_expect_tx(bar, copies * Page::kBytes);
-      __syncwarp();
-      if (copy)
-        bulk_load(base + L::kP + slot * L::kPack + lane * Page::kBytes,
-                  (is_v ? p.v : p.k) + ((size_t)id * p.Hkv + h) * Page::kBytes, Page::kBytes, bar);
-      issued = m + 1;
-    }
-    // no copy is in flight when the block exits
-    for (int m = max(0, issued - kPackSlots); m < issued; ++m)
-      mbar_wait(smem_addr(&sh.pk_full[m % kPackSlots]), (m / kPackSlots) & 1, kTcDrainNs);
-  } else if (warp == 1) {
-    // ---- MMA issue ----
-    if (lane == 0) {
-      constexpr uint32_t idS = idesc_f16_f32(kBM, kBN, false);
-      constexpr uint32_t idPV = idesc_f16_f32(kBM, D, true);
-      auto issue_s = [&](int c, int qt, int st) {
-        const uint64_t qd = smem_desc_sw128(base + L::kQ + qt * L::kTile, 16, 1024);
-        const uint64_t kd = smem_desc_sw128(base + L::kK + st * L::kTile, 16, 1024);
-        tc_fence_after();
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          umma_bf16(tmem + c * kTmemChain, desc_add(qd, (kk >> 2) * L::kHalf + (kk & 3) * 32),
-                    desc_add(kd, (kk >> 2) * L::kHalf + (kk & 3) * 32), idS, kk > 0);
-        umma_commit(smem_addr(&sh.s_full[c]));
+  if (warp < 4) {
+    regs_down<kRegsIssue>();
+    if (work && warp == 0) {
+      // ---- loader: lane l < 8 copies page l of the item ----
+      // Block ids come 32 (four tiles) at a time and a batch ahead: read for each
+      // item, their latency was on every item's path (1.35 us a tile).
+      const int32_t *trow = p.table + (size_t)b * p.max_blocks;
+      auto read_ids = [&](int tile) {  // of the batch that starts at `tile`
+        const int pg = first + tile * kTilePages + lane;
+        return pg < last ? __ldg(trow + pg) : 0;
       };
-      auto issue_pv = [&](int c, int st, bool accum, bool final) {
-        const uint64_t vd = smem_desc_sw128(base + L::kV + st * L::kTile, L::kHalf, 1024);
-        uint64_t v8[8];
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk) v8[kk] = desc_add(vd, kk * 16 * 128);
-        tc_fence_after();
-        umma8_ts(tmem + c * kTmemChain + kTmemO, tmem + c * kTmemChain, v8, idPV, accum ? 1u : 0u);
-        if (final) umma_commit(smem_addr(&sh.o_final[c]));
-      };
-      bool ok = tc_wait(sh.q_full, 0, lim, abort);
-      if (two) {
-        ok = ok && tc_wait(sh.k_full[0], 0, lim, abort);
-        if (ok) {
-          issue_s(0, 0, 0);
-          issue_s(1, 1, 0);
-          umma_commit(smem_addr(&sh.k_empty[0]));
+      int before = 0, ids = read_ids(0), ahead = read_ids(4);  // V runs a tile behind K
+      bool ok = true;
+      int issued = 0;
+      for (int m = 0; m < 2 * n; ++m) {
+        int tile;
+        bool is_v;
+        stream_item(m, n, tile, is_v);
+        if (!is_v && tile > 0 && (tile & 3) == 0) {
+          before = ids;
+          ids = ahead;
+          ahead = read_ids(tile + 4);
         }
-        for (int j = 0; ok && j < n; ++j) {
-          const int st = j & 1;
-          for (int c = 0; ok && c < 2; ++c) {
-            ok = tc_wait(sh.p_full[c], j & 1, lim, abort);
-            if (ok && c == 0) ok = tc_wait(sh.v_full[st], (j >> 1) & 1, lim, abort);
-            if (!ok) break;
-            issue_pv(c, st, j > 0, j == n - 1);
-            if (c == 1) umma_commit(smem_addr(&sh.v_empty[st]));
-            if (j + 1 < n) {
-              if (c == 0) ok = tc_wait(sh.k_full[st ^ 1], ((j + 1) >> 1) & 1, lim, abort);
+        const int slot = m % kPackSlots;
+        // (a V tile whose K's batch is not the current one: the last before a new batch)
+        const bool old = is_v && (tile & 3) == 3 && tile + 1 < n;
+        const int id = __shfl_sync(0xffffffffu, old ? before : ids, (tile & 3) * kTilePages + (lane & 7));
+        const bool mine = lane < kTilePages && first + tile * kTilePages + lane < last;
+        const bool bad = mine && (id < 0 || id >= p.num_blocks);
+        if (bad) sh.bad = 1;
+        if (m >= kPackSlots)
+          ok = __all_sync(0xffffffffu, tc_wait(sh.pk_empty[slot], ((m / kPackSlots) - 1) & 1, lim, abort));
+        if (!ok) break;
+        const bool copy = mine && !bad;
+        const int copies = __popc(__ballot_sync(0xffffffffu, copy));
+        const uint32_t bar = smem_addr(&sh.pk_full[slot]);
+        if (lane == 0) mbar_arrive_expect_tx(bar, copies * Page::kBytes);
+        __syncwarp();
+        if (copy)
+          bulk_load(base + L::kP + slot * L::kPack + lane * Page::kBytes,
+                    (is_v ? p.v : p.k) + ((size_t)id * p.Hkv + h) * Page::kBytes, Page::kBytes, bar);
+        issued = m + 1;
+      }
+      // no copy is in flight when the block exits
+      for (int m = max(0, issued - kPackSlots); m < issued; ++m)
+        mbar_wait(smem_addr(&sh.pk_full[m % kPackSlots]), (m / kPackSlots) & 1, kTcDrainNs);
+    } else if (work && warp == 1) {
+      // ---- MMA issue ----
+      if (lane == 0) {
+        constexpr uint32_t idS = idesc_f16_f32(kBM, kBN, false);
+        constexpr uint32_t idPV = idesc_f16_f32(kBM, D, true);
+        auto issue_s = [&](int c, int qt, int st) {
+          const uint64_t qd = smem_desc_sw128(base + L::kQ + qt * L::kTile, 16, 1024);
+          const uint64_t kd = smem_desc_sw128(base + L::kK + st * L::kTile, 16, 1024);
+          tc_fence_after();
+  #pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            umma_bf16(tmem + c * kTmemChain, desc_add(qd, (kk >> 2) * L::kHalf + (kk & 3) * 32),
+                      desc_add(kd, (kk >> 2) * L::kHalf + (kk & 3) * 32), idS, kk > 0);
+          umma_commit(smem_addr(&sh.s_full[c]));
+        };
+        auto issue_pv = [&](int c, int st, bool accum, bool final) {
+          const uint64_t vd = smem_desc_sw128(base + L::kV + st * L::kTile, L::kHalf, 1024);
+          uint64_t v8[8];
+  #pragma unroll
+          for (int kk = 0; kk < 8; ++kk) v8[kk] = desc_add(vd, kk * 16 * 128);
+          tc_fence_after();
+          umma8_ts(tmem + c * kTmemChain + kTmemO, tmem + c * kTmemChain, v8, idPV, accum ? 1u : 0u);
+          if (final) umma_commit(smem_addr(&sh.o_final[c]));
+        };
+        bool ok = tc_wait(sh.q_full, 0, lim, abort);
+        if (two) {
+          ok = ok && tc_wait(sh.k_full[0], 0, lim, abort);
+          if (ok) {
+            issue_s(0, 0, 0);
+            issue_s(1, 1, 0);
+          }
+          for (int j = 0; ok && j < n; ++j) {
+            const int st = j & 1;
+            for (int c = 0; ok && c < 2; ++c) {
+              ok = tc_wait(sh.p_full[c], j & 1, lim, abort);
+              if (ok && c == 0) ok = tc_wait(sh.v_full[st], (j >> 1) & 1, lim, abort);
               if (!ok) break;
-              issue_s(c, c, st ^ 1);
-              if (c == 1) umma_commit(smem_addr(&sh.k_empty[st ^ 1]));
+              issue_pv(c, st, j > 0, j == n - 1);
+              if (j + 1 < n) {
+                if (c == 0) ok = tc_wait(sh.k_full[st ^ 1], ((j + 1) >> 1) & 1, lim, abort);
+                if (!ok) break;
+                issue_s(c, c, st ^ 1);
+              }
+            }
+          }
+        } else {
+          for (int j = 0; ok && j < chains; ++j) {
+            ok = tc_wait(sh.k_full[j], 0, lim, abort);
+            if (!ok) break;
+            issue_s(j, 0, j);
+          }
+          for (int j = 0; ok && j < n; ++j) {
+            const int c = j & 1;
+            ok = tc_wait(sh.p_full[c], (j >> 1) & 1, lim, abort) && tc_wait(sh.v_full[c], (j >> 1) & 1, lim, abort);
+            if (!ok) break;
+            issue_pv(c, c, j > 1, j + 2 >= n);
+            if (j + 2 < n) {
+              ok = tc_wait(sh.k_full[c], ((j + 2) >> 1) & 1, lim, abort);
+              if (!ok) break;
+              issue_s(c, 0, c);
             }
           }
         }
-      } else {
-        for (int j = 0; ok && j < chains; ++j) {
-          ok = tc_wait(sh.k_full[j], 0, lim, abort);
-          if (!ok) break;
-          issue_s(j, 0, j);
-          umma_commit(smem_addr(&sh.k_empty[j]));
-        }
-        for (int j = 0; ok && j < n; ++j) {
-          const int c = j & 1;
-          ok = tc_wait(sh.p_full[c], (j >> 1) & 1, lim, abort) && tc_wait(sh.v_full[c], (j >> 1) & 1, lim, abort);
-          if (!ok) break;
-          issue_pv(c, c, j > 1, j + 2 >= n);
-          umma_commit(smem_addr(&sh.v_empty[c]));
-          if (j + 2 < n) {
-            ok = tc_wait(sh.k_full[c], ((j + 2) >> 1) & 1, lim, abort);
-            if (!ok) break;
-            issue_s(c, 0, c);
-            umma_commit(smem_addr(&sh.k_empty[c]));
-          }
-        }
+        umma_commit(smem_addr(&sh.drain));
+        mbar_wait(smem_addr(&sh.drain), 0, kTcDrainNs);
       }
-      umma_commit(smem_addr(&sh.drain));
-      mbar_wait(smem_addr(&sh.drain), 0, kTcDrainNs);
+      __syncwarp();
     }
-    __syncwarp();
-  } else if (warp >= 4 && warp < 8) {
+  } else if (warp < 8) {
+    regs_down<kRegsDecode>();
     // ---- decode: a lane takes one group (16 columns) of a key at a time ----
     constexpr int kGroups = D / kQ4Group;        // lanes across one key
     constexpr int kKeys = 32 / kGroups;          // keys per warp step
@@ -365,9 +407,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4
         mbar_arrive(smem_addr(&sh.pk_empty[slot]));
       }
     }
-  } else if (warp >= 8) {
+  } else {
+    regs_up<kRegsSoftmax>();
     // ---- softmax ----
-    const int c = (warp - 8) >> 2;             // chain
+    const int c = (warp - 8) >> 3;             // chain
+    const int half = ((warp - 8) >> 2) & 1;    // which 64 keys of a tile, and columns of O
     const int rt = two ? c : 0;                // its row tile
     const int quarter = warp & 3;
     const int rl = quarter * 32 + lane;        // row within the tile
@@ -377,14 +421,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
     const uint32_t tS = tmem + c * kTmemChain + lane_off, tO = tS + kTmemO;
 
-    // Q row -> fp16, scaled by a power of two (both chains know it)
+    // half a Q row -> fp16, scaled by a power of two (both chains know it)
     float mul;
     {
-      uint32_t q[D / 2];
-      const uint4 *src = reinterpret_cast<const uint4 *>(p.q + q4_out_row(p, b, h, rvalid ? row : 0) * D);
+      uint32_t q[D / 4];
+      const uint4 *src =
+          reinterpret_cast<const uint4 *>(p.q + q4_out_row(p, b, h, rvalid ? row : 0) * D + half * (D / 2));
       float amax = 0.f;
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i) {
+      for (int i = 0; i < D / 16; ++i) {
         const uint4 x = rvalid ? src[i] : make_uint4(0u, 0u, 0u, 0u);
         q[4 * i] = x.x;
         q[4 * i + 1] = x.y;
@@ -392,10 +437,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4
         q[4 * i + 3] = x.w;
       }
 #pragma unroll
-      for (int i = 0; i < D / 2; ++i) {
+      for (int i = 0; i < D / 4; ++i) {
         amax = fmaxf(amax, fabsf(__uint_as_float(q[i] << 16)));
         amax = fmaxf(amax, fabsf(__uint_as_float(q[i] & 0xFFFF0000u)));
       }
+      sh.half[c][half][rl] = amax;
+      chain_sync(c);
+      amax = fmaxf(amax, sh.half[c][half ^ 1][rl]);
       const int e = q4_exponent(amax);
       // the factor's sign goes into q, and it stays between the smallest and the
       // largest normal number, so that a masked score (-inf) stays one
@@ -406,13 +454,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4
       if (two || c == 0) {
         uint8_t *dst = gbase + L::kQ + rt * L::kTile;
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
+        for (int i = 0; i < D / 16; ++i) {
           uint32_t w[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             w[k] = pack_half2(__uint_as_float(q[4 * i + k] << 16) * up1 * up2,
                               __uint_as_float(q[4 * i + k] & 0xFFFF0000u) * up1 * up2);
-          *reinterpret_cast<uint4 *>(dst + (i >> 3) * L::kHalf + sw128_offset(rl, i & 7)) =
+          const int ch = half * (D / 16) + i;  // 16-byte chunk of the row
+          *reinterpret_cast<uint4 *>(dst + (ch >> 3) * L::kHalf + sw128_offset(rl, ch & 7)) =
               make_uint4(w[0], w[1], w[2], w[3]);
         }
         fence_proxy_async_smem();
@@ -421,122 +470,119 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4
       if (lane == 0) mbar_arrive(smem_addr(&sh.q_full));
     }
 
-    float ref = 0.f, l = 0.f;
-    bool unset = true, ok = c < chains;
+    float ref = 0.f, l = 0.f;  // the row's reference, this thread's part of its sum
+    bool unset = true, ok = work && c < chains;
     const unsigned long long mul2 = f2_pack(mul, mul);
     int u = 0;  // this chain's tiles
     for (int j = two ? 0 : c; ok && j < n; j += two ? 1 : 2, ++u) {
-      ok = __all_sync(0xffffffffu, tc_wait(sh.s_full[c], u & 1, lim, abort));
-      if (!ok) break;
+      const bool got = __all_sync(0xffffffffu, tc_wait(sh.s_full[c], u & 1, lim, abort));
+      if (!got) sh.stop[c][u & 1] = 1;
       tc_fence_after();
-      const int t0 = (first + j * kTilePages) * kPage;  // first key slot of the tile
-      const bool tail = t0 + kBN > P;
-      uint32_t x[2][32];
-      tmem_ld32(tS, x[0]);
+      if ((two ? c == 1 : true) && half == 0 && quarter == 0 && lane == 0) {
+        // A commit follows every earlier MMA of its thread, so K_j and the V tile
+        // that the P V in front of S_j read are free.  (Commits of their own for
+        // that cost 0.3 us each on the tensor pipe.)
+        mbar_arrive(smem_addr(&sh.k_empty[j & 1]));
+        const int jv = two ? j - 1 : j - 2;
+        if (jv >= 0) mbar_arrive(smem_addr(&sh.v_empty[jv & 1]));
+      }
+      const int t0 = (first + j * kTilePages) * kPage + half * 64;  // this thread's first key slot
+      const bool tail = t0 + 64 > P;
+      const unsigned long long ref2 = f2_pack(-ref, -ref);
+      unsigned long long acc0 = 0ull, acc1 = 0ull;
+      uint32_t pk[32], seen = 0u;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        uint32_t (&s)[32] = x[k & 1];
+      for (int k = 0; k < 2; ++k) {
+        uint32_t s[32];
+        tmem_ld32(tS + half * 64 + k * 32, s);
         tmem_wait_ld(s);
-        if (k < 3) tmem_ld32(tS + (k + 1) * 32, x[(k + 1) & 1]);
-        uint32_t vis = 0xFFFFFFFFu;
-        if (tail) {
-          vis = rvalid ? q4_visible(p, b, node, t0 + k * 32 - P, nb) |
-                             (q4_visible(p, b, node, t0 + k * 32 + 16 - P, nb) << 16)
-                       : 0u;
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (!((vis >> i) & 1u)) s[i] = 0xFF800000u;
-        }
-        uint32_t pk[16];
-        // P against the reference, the fp16 pairs and their sum
-        unsigned long long acc0 = 0ull, acc1 = 0ull;
-        const unsigned long long ref2 = f2_pack(-ref, -ref);
+        if (tail) seen |= mask_scores(p, b, node, rvalid, t0 + k * 32 - P, nb, s);
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const float2 t = f2_unpack(
               f2_fma(f2_pack(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), mul2, ref2));
           const float e0 = ex2_approx(t.x), e1 = ex2_approx(t.y);
-          pk[i] = pack_half2(e0, e1);
+          pk[k * 16 + i] = pack_half2(e0, e1);
           if (i & 1) acc1 = f2_add(acc1, f2_pack(e0, e1));
           else acc0 = f2_add(acc0, f2_pack(e0, e1));
         }
-        const float2 acc = f2_unpack(f2_add(acc0, acc1));
-        float sum = acc.x + acc.y;
-        // Rows that need more than that: no reference yet, P out of fp16's range, or
-        // a reference (itself a rounded product) so large that the exact product
-        // above lies powers of two away from it; those round the product first.
-        const bool mine = (unset && vis != 0u) || !(sum <= kTcMaxSum) || fabsf(ref) >= kTcLargeRef;
-        if (__builtin_expect(__any_sync(0xffffffffu, mine), 0)) {
-          float f = 1.f;
-          if (mine) {
-            float m = -INFINITY;
+      }
+      const float2 acc = f2_unpack(f2_add(acc0, acc1));
+      float sum = acc.x + acc.y;
+      // Rows that need more than that: no reference yet, P out of fp16's range, or
+      // a reference (itself a rounded product) so large that the exact product
+      // above lies powers of two away from it; those round the product first.
+      const bool mine = (unset && (!tail || seen != 0u)) || !(sum <= kTcMaxSum) || fabsf(ref) >= kTcLargeRef;
+      tc_fence_before();
+      const bool any = chain_any(c, mine || !got);
+      tc_fence_after();
+      if (__builtin_expect(any, 0)) {
+        if (sh.stop[c][u & 1]) {  // the same for every warp of the chain
+          ok = false;
+          break;
+        }
+        float m = -INFINITY;
+#pragma unroll 1
+        for (int k = 0; k < 2; ++k) {
+          uint32_t s[32];
+          tmem_ld32(tS + half * 64 + k * 32, s);
+          tmem_wait_ld(s);
+          if (tail) mask_scores(p, b, node, rvalid, t0 + k * 32 - P, nb, s);
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              m = fmaxf(m, (vis >> i) & 1u ? __fmul_rn(__uint_as_float(s[i]), mul) : -INFINITY);
-            if (m > -INFINITY && (unset || !(m - ref <= kTcOffset + 2.f))) {
-              float to = floorf(m) - kTcOffset;
-              if (!(m - to <= kTcOffset + 1.f)) to = m;  // 8 is less than an ulp of m
-              // (nothing was added yet to a row without a reference)
-              if (!unset) f = ex2_approx(ref - to);
-              ref = to;
-              unset = false;
-              l *= f;
-            }
-            sum = 0.f;
+          for (int i = 0; i < 32; ++i) m = fmaxf(m, __fmul_rn(__uint_as_float(s[i]), mul));
+        }
+        // what the row's two threads know: its maximum, and whether either asked
+        sh.half[c][half][rl] = m;
+        sh.asks[c][half][rl] = mine;
+        chain_sync(c);
+        const bool row_asks = mine || sh.asks[c][half ^ 1][rl];
+        m = fmaxf(m, sh.half[c][half ^ 1][rl]);
+        float f = 1.f;
+        if (row_asks && m > -INFINITY && (unset || !(m - ref <= kTcOffset + 2.f))) {
+          float to = m - kTcOffset;
+          if (!(m - to <= kTcOffset + 1.f)) to = m;  // 8 is less than an ulp of m
+          // (nothing was added yet to a row without a reference)
+          if (!unset) f = ex2_approx(ref - to);
+          ref = to;
+          unset = false;
+          l *= f;
+        }
+        if (__any_sync(0xffffffffu, row_asks)) {
+          float again = 0.f;
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            uint32_t s[32];
+            tmem_ld32(tS + half * 64 + k * 32, s);
+            tmem_wait_ld(s);
+            if (tail) mask_scores(p, b, node, rvalid, t0 + k * 32 - P, nb, s);
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               const float e0 = ex2_approx(__fsub_rn(__fmul_rn(__uint_as_float(s[2 * i]), mul), ref));
               const float e1 = ex2_approx(__fsub_rn(__fmul_rn(__uint_as_float(s[2 * i + 1]), mul), ref));
-              pk[i] = pack_half2(e0, e1);
-              sum += e0 + e1;
+              again += e0 + e1;
+              pk[k * 16 + i] = row_asks ? pack_half2(e0, e1) : pk[k * 16 + i];
             }
           }
-          // what is already in TMEM for these rows: O, and this tile's P
-          if (__any_sync(0xffffffffu, f != 1.f)) {
-            if (u > 0) {
+          if (row_asks) sum = again;
+        }
+        if (u > 0 && __any_sync(0xffffffffu, f != 1.f)) {  // this thread's half of O
 #pragma unroll 1
-              for (int q = 0; q < D / 32; ++q) {
-                uint32_t o[32];
-                tmem_ld32(tO + q * 32, o);
-                tmem_wait_ld(o);
+          for (int q = 0; q < D / 64; ++q) {
+            uint32_t o[32];
+            const uint32_t at = tO + half * (D / 2) + q * 32;
+            tmem_ld32(at, o);
+            tmem_wait_ld(o);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                tmem_st32(tO + q * 32, o);
-              }
-            }
-            if (k > 0) {
-              tmem_wait_st();
-              const __half2 f2 = __floats2half2_rn(f, f);
-              uint32_t o[32];
-              tmem_ld32(tS, o);  // (k = 1: the second 16 are this chunk's scores, left as they are)
-              tmem_wait_ld(o);
-              uint32_t o2[32];
-              if (k > 2) {
-                tmem_ld32(tS + 32, o2);
-                tmem_wait_ld(o2);
-              }
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (i < 16 || k > 1) {
-                  const __half2 v = __hmul2(*reinterpret_cast<__half2 *>(&o[i]), f2);
-                  o[i] = *reinterpret_cast<const uint32_t *>(&v);
-                }
-              tmem_st32(tS, o);
-              if (k > 2) {
-                uint32_t o3[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                  const __half2 v = __hmul2(*reinterpret_cast<__half2 *>(&o2[i]), f2);
-                  o3[i] = *reinterpret_cast<const uint32_t *>(&v);
-                }
-                tmem_st16(tS + 32, o3);
-              }
-            }
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+            tmem_st32(at, o);
           }
         }
-        l += sum;
-        tmem_st16(tS + k * 16, pk);
+        tc_fence_before();
+        chain_sync(c);  // S has been read again
+        tc_fence_after();
       }
+      l += sum;
+      tmem_st32(tS + half * 32, pk);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -550,22 +596,26 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4
     // MMAs may still read)
     if (ok && joined) ok = __all_sync(0xffffffffu, tc_wait(sh.o_final[c ^ 1], 0, lim, abort));
     tc_fence_after();
+    sh.half[c][half][rl] = l;
+    chain_sync(c);
+    l += sh.half[c][half ^ 1][rl];
     float M = unset ? -INFINITY : ref;
     if (unset && l != l) M = 0.f;  // only NaN scores so far
     float *stage = reinterpret_cast<float *>(gbase + L::kK);  // K and V tiles are done with
+    const int q0 = half * (D / 64);  // this thread's 32-column parts of O
     if (joined && c == 1) {
       // chain 1's part, transposed: column-major, so that lanes do not collide
 #pragma unroll 1
-      for (int q = 0; ok && q < D / 32; ++q) {
+      for (int q = q0; ok && q < q0 + D / 64; ++q) {
         uint32_t o[32];
         tmem_ld32(tO + q * 32, o);
         tmem_wait_ld(o);
 #pragma unroll
         for (int i = 0; i < 32; ++i) stage[(q * 32 + i) * kBM + rl] = __uint_as_float(o[i]);
       }
-      sh.ml[rl] = make_float2(M, l);
+      if (half == 0) sh.ml[rl] = make_float2(M, l);
     }
-    if (joined) asm volatile("bar.sync 1, 256;\n" ::: "memory");
+    if (joined) asm volatile("barrier.cta.sync 1, 512;\n" ::: "memory");
     if (c < (two ? 2 : 1)) {
       float f0 = 1.f, f1 = 0.f;
       if (joined) {
@@ -583,17 +633,18 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4
       const size_t pr = (((size_t)b * p.Hkv + h) * p.splits + split) * p.rows + row;
       const size_t orow = rvalid ? q4_out_row(p, b, h, row) : 0;
 #pragma unroll 1
-      for (int q = 0; ok && q < D / 32; ++q) {
+      for (int q = q0; ok && q < q0 + D / 64; ++q) {
         uint32_t o[32];
         tmem_ld32(tO + q * 32, o);
         tmem_wait_ld(o);
-        float v[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
-          v[i] = __uint_as_float(o[i]) * f0;
-          if (joined) v[i] = fmaf(f1, f1 == 0.f ? 0.f : stage[(q * 32 + i) * kBM + rl], v[i]);
+          float v = __uint_as_float(o[i]) * f0;
+          if (joined) v = fmaf(f1, f1 == 0.f ? 0.f : stage[(q * 32 + i) * kBM + rl], v);
+          o[i] = __float_as_uint(v);
         }
         if (rvalid) {
+          const float *v = reinterpret_cast<const float *>(o);
           if (direct) {
             uint4 *dst = reinterpret_cast<uint4 *>(p.out + orow * D + q * 32);
 #pragma unroll
@@ -611,7 +662,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4
           }
         }
       }
-      if (rvalid) {
+      if (rvalid && half == 0) {
         if (!direct)
           p.part_ml[pr] = make_float2(M, bad ? -1.f : l);
         else if (p.lse)
@@ -642,13 +693,26 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4
 
 }  // namespace
 
+namespace {
+// The register split draws on what the block was launched with: a build that
+// gives a thread fewer registers must not run (it would wait forever).
+template <int D>
+bool tc_ready() {
+  static const bool enough = [] {
+    cudaFuncAttributes a;
+    return cudaFuncGetAttributes(&a, tree_attn_q4_tc_kernel<D>) == cudaSuccess && a.numRegs >= kRegsLaunch;
+  }();
+  return enough && set_smem((const void *)tree_attn_q4_tc_kernel<D>, TcLayout<D>::kAlloc);
+}
+}  // namespace
+
 cudaError_t q4_tc_launch(const Q4Attn &p, int D, int rows_per_block, cudaStream_t s) {
   const dim3 grid((unsigned)p.splits * p.row_blocks * p.Hkv, p.B);
   if (D == 128) {
-    if (!set_smem((const void *)tree_attn_q4_tc_kernel<128>, TcLayout<128>::kAlloc)) return cudaErrorUnknown;
+    if (!tc_ready<128>()) return cudaErrorUnknown;
     return launch(tree_attn_q4_tc_kernel<128>, grid, dim3(kTcThreads), TcLayout<128>::kAlloc, s, p, rows_per_block);
   }
-  if (!set_smem((const void *)tree_attn_q4_tc_kernel<64>, TcLayout<64>::kAlloc)) return cudaErrorUnknown;
+  if (!tc_ready<64>()) return cudaErrorUnknown;
   return launch(tree_attn_q4_tc_kernel<64>, grid, dim3(kTcThreads), TcLayout<64>::kAlloc, s, p, rows_per_block);
 }
 
