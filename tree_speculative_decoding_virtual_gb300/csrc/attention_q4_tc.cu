@@ -76,7 +76,7 @@ struct TcShared {
   float2 ml[kBM];           // chain 1's (reference, sum) when it shares chain 0's rows
   float half[2][2][kBM];    // by chain, thread of the row, row: exchange between the two
   uint8_t asks[2][2][kBM];  // likewise
-  int stop[2][2];           // by chain and tile parity: a wait ran out
+  int stop[3][2];           // by chain (2: decode) and tile parity: a wait ran out
   uint32_t tmem_base;
   int abort, bad;
 };
@@ -201,6 +201,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4
   const int row0 = rb * rows_per_block;
   const bool work = row0 < rows_valid && first < last;
   if (!work && p.splits > 1) return;
+  const int n = work ? (last - first + kTilePages - 1) / kTilePages : 0;  // key tiles
+  // two row tiles (each with every key tile), or one row tile whose key tiles
+  // alternate between the chains
+  const bool two = row0 + kBM < rows_valid && rows_per_block > kBM;
+  const int chains = two ? 2 : (n > 1 ? 2 : 1);
 
   if (tid == 0) {
     for (int i = 0; i < kPackSlots; ++i) {
@@ -213,14 +218,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4
       mbar_init(smem_addr(&sh.v_full[i]), 4);
       mbar_init(smem_addr(&sh.v_empty[i]), 1);
       mbar_init(smem_addr(&sh.s_full[i]), 1);
-      mbar_init(smem_addr(&sh.p_full[i]), 8);
+      mbar_init(smem_addr(&sh.p_full[i]), two && i == 1 ? 8 : 9);  // softmax warps, hand-over
       mbar_init(smem_addr(&sh.o_final[i]), 1);
     }
     mbar_init(smem_addr(&sh.q_full), 16);
     mbar_init(smem_addr(&sh.drain), 1);
     sh.abort = 0;
     sh.bad = 0;
-    sh.stop[0][0] = sh.stop[0][1] = sh.stop[1][0] = sh.stop[1][1] = 0;
+    for (int i = 0; i < 6; ++i) sh.stop[i >> 1][i & 1] = 0;
     fence_mbar_init();
   }
   if (warp == 1) tmem_alloc(smem_addr(&sh.tmem_base), kTmemCols);
@@ -228,12 +233,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem_base;
-
-  const int n = work ? (last - first + kTilePages - 1) / kTilePages : 0;  // key tiles
-  // two row tiles (each with every key tile), or one row tile whose key tiles
-  // alternate between the chains
-  const bool two = row0 + kBM < rows_valid && rows_per_block > kBM;
-  const int chains = two ? 2 : (n > 1 ? 2 : 1);
 
   if (warp < 4) {
     regs_down<kRegsIssue>();
@@ -305,47 +304,57 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4
           umma8_ts(tmem + c * kTmemChain + kTmemO, tmem + c * kTmemChain, v8, idPV, accum ? 1u : 0u);
           if (final) umma_commit(smem_addr(&sh.o_final[c]));
         };
+        // This thread paces the tensor cores, so its only wait in the loop is the
+        // one for P: warp 2 adds to that barrier once V_j and the next K are there.
+        // (With waits of its own for them it lost 200 to 500 cycles each, behind
+        // the shared-memory traffic of the other warps.)
         bool ok = tc_wait(sh.q_full, 0, lim, abort);
+        ok = ok && tc_wait(sh.k_full[0], 0, lim, abort);
+        if (ok) issue_s(0, 0, 0);
+        if (chains == 2) {
+          if (!two) ok = ok && tc_wait(sh.k_full[1], 0, lim, abort);
+          if (ok) issue_s(1, two ? 1 : 0, two ? 0 : 1);
+        }
         if (two) {
-          ok = ok && tc_wait(sh.k_full[0], 0, lim, abort);
-          if (ok) {
-            issue_s(0, 0, 0);
-            issue_s(1, 1, 0);
-          }
           for (int j = 0; ok && j < n; ++j) {
             const int st = j & 1;
-            for (int c = 0; ok && c < 2; ++c) {
-              ok = tc_wait(sh.p_full[c], j & 1, lim, abort);
-              if (ok && c == 0) ok = tc_wait(sh.v_full[st], (j >> 1) & 1, lim, abort);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              ok = ok && mbar_wait(smem_addr(&sh.p_full[c]), j & 1, lim);
               if (!ok) break;
               issue_pv(c, st, j > 0, j == n - 1);
-              if (j + 1 < n) {
-                if (c == 0) ok = tc_wait(sh.k_full[st ^ 1], ((j + 1) >> 1) & 1, lim, abort);
-                if (!ok) break;
-                issue_s(c, c, st ^ 1);
-              }
+              if (j + 1 < n) issue_s(c, c, st ^ 1);
             }
           }
         } else {
-          for (int j = 0; ok && j < chains; ++j) {
-            ok = tc_wait(sh.k_full[j], 0, lim, abort);
-            if (!ok) break;
-            issue_s(j, 0, j);
-          }
           for (int j = 0; ok && j < n; ++j) {
             const int c = j & 1;
-            ok = tc_wait(sh.p_full[c], (j >> 1) & 1, lim, abort) && tc_wait(sh.v_full[c], (j >> 1) & 1, lim, abort);
+            ok = mbar_wait(smem_addr(&sh.p_full[c]), (j >> 1) & 1, lim);
             if (!ok) break;
             issue_pv(c, c, j > 1, j + 2 >= n);
-            if (j + 2 < n) {
-              ok = tc_wait(sh.k_full[c], ((j + 2) >> 1) & 1, lim, abort);
-              if (!ok) break;
-              issue_s(c, 0, c);
-            }
+            if (j + 2 < n) issue_s(c, 0, c);
           }
         }
+        if (!ok) *abort = 1;
         umma_commit(smem_addr(&sh.drain));
         mbar_wait(smem_addr(&sh.drain), 0, kTcDrainNs);
+      }
+      __syncwarp();
+    } else if (work && warp == 2) {
+      // ---- hand-over: phase j of p_full also means that V_j and the K tile of the
+      // S behind P_j V_j are in shared memory.  (An arrival counts toward the phase
+      // that is open: the one before has to be complete.) ----
+      if (lane == 0) {
+        const int step = two ? 1 : 2;  // the chain's next tile
+        for (int j = 0; j < n; ++j) {
+          const int c = two ? 0 : j & 1, u = two ? j : j >> 1;
+          bool ok = tc_wait(sh.v_full[j & 1], (j >> 1) & 1, lim, abort);
+          const int k = j + step;
+          if (ok && k < n) ok = tc_wait(sh.k_full[k & 1], (k >> 1) & 1, lim, abort);
+          if (ok && u > 0) ok = tc_wait(sh.p_full[c], (u - 1) & 1, lim, abort);
+          if (!ok) break;
+          mbar_arrive(smem_addr(&sh.p_full[c]));
+        }
       }
       __syncwarp();
     }
@@ -361,10 +370,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4
       bool is_v;
       stream_item(m, n, tile, is_v);
       const int slot = m % kPackSlots, st = tile & 1;
-      bool ok = tc_wait(sh.pk_full[slot], (m / kPackSlots) & 1, lim, abort);
-      if (ok && tile >= 2)
-        ok = tc_wait(is_v ? sh.v_empty[st] : sh.k_empty[st], ((tile >> 1) - 1) & 1, lim, abort);
-      if (!__all_sync(0xffffffffu, ok)) break;
+      // one warp looks at the barriers, the others wait for it without polling
+      if (dw == 0) {
+        bool ok = tc_wait(sh.pk_full[slot], (m / kPackSlots) & 1, lim, abort);
+        if (ok && tile >= 2) ok = tc_wait(is_v ? sh.v_empty[st] : sh.k_empty[st], ((tile >> 1) - 1) & 1, lim, abort);
+        if (!ok) sh.stop[2][m & 1] = 1;
+      }
+      asm volatile("barrier.cta.sync 4, 128;\n" ::: "memory");
+      if (sh.stop[2][m & 1]) break;
       const uint8_t *src = gbase + L::kP + slot * L::kPack;
       uint8_t *dst = gbase + (is_v ? L::kV : L::kK) + st * L::kTile + (D == 128 ? (grp >> 2) * L::kHalf : 0);
       const int c0 = (grp & 3) * 2;
@@ -475,8 +488,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4
     const unsigned long long mul2 = f2_pack(mul, mul);
     int u = 0;  // this chain's tiles
     for (int j = two ? 0 : c; ok && j < n; j += two ? 1 : 2, ++u) {
-      const bool got = __all_sync(0xffffffffu, tc_wait(sh.s_full[c], u & 1, lim, abort));
-      if (!got) sh.stop[c][u & 1] = 1;
+      // one warp looks at the barrier, the others wait for it without polling
+      bool got = true;
+      if (((warp - 8) & 7) == 0) {
+        got = __all_sync(0xffffffffu, tc_wait(sh.s_full[c], u & 1, lim, abort));
+        if (!got) sh.stop[c][u & 1] = 1;
+      }
+      chain_sync(c);
       tc_fence_after();
       if ((two ? c == 1 : true) && half == 0 && quarter == 0 && lane == 0) {
         // A commit follows every earlier MMA of its thread, so K_j and the V tile
