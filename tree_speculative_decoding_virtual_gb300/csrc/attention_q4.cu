@@ -9,8 +9,9 @@
 // Few rows (tree_attn_q4_rows): the kernel is bound by the cache's bytes (9 D
 // a page, a quarter of bf16), so K and V go from the page to the tensor
 // core's operand registers without a second pass through shared memory.  A
-// warp owns whole pages: one lane fetches a page's K and V with two bulk
-// copies into the warp's ring, and the warp computes, for 8 rows at a time,
+// warp owns whole pages: its lanes copy a page's K and V asynchronously, 16 bytes
+// each, into the warp's ring (bulk copies of a page's 9 D bytes took 80 ns each,
+// whatever the ring's depth), and it computes, for 8 rows at a time,
 //   S^T (16 keys x 8 rows) = K Q^T      A = K, decoded in registers
 //   P^T = exp2(S^T * c - m)             fp32, packed to fp16, transposed in
 //                                       registers by movmatrix
@@ -51,7 +52,6 @@ constexpr int kRowsStages = 4;  // pages in flight per warp
 constexpr float kOffset = 8.f;  // P of the reference score is 2^8
 constexpr float kSlack = 7.f;   // P stays at or below 2^15
 constexpr float kRowsLn2 = 0.6931471805599453f;
-constexpr uint64_t kRowsDrainNs = 100000000ull;
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                         uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -91,11 +91,12 @@ template <int D, int NT>
 struct RowsLayout {
   static constexpr int kPageBytes = Q4Page<D>::kBytes;
   static constexpr int kStage = 2 * kPageBytes;
+  static constexpr int kChunks = kStage / 16;  // 16-byte copies of a K and a V page
   static constexpr int kRing = kRowsWarps * kRowsStages * kStage;
   static constexpr int kMerge = kRowsWarps * 8 * NT * D * 4;  // O of every warp
   static constexpr int kBlock = 8 * NT * D * 4;               // O of the block
   static constexpr int kBytes = kRing > kMerge + kBlock ? kRing : kMerge + kBlock;
-  static_assert(kStage % 16 == 0, "bulk copies start on 16 bytes");
+  static_assert(kPageBytes % 16 == 0, "copies start on 16 bytes");
 };
 
 // Four columns of a finished row: O / sum in bf16, and the row's lse.
@@ -110,10 +111,9 @@ __device__ __forceinline__ void rows_out(const Q4Attn &p, size_t orow, int D, in
 }
 
 struct RowsShared {
-  uint64_t full[kRowsWarps][kRowsStages];
   float2 ml[kRowsWarps][16];  // (reference, sum) of each warp's rows
   float4 block_ml[16];        // and of the block's (sum -1: bad page)
-  int bad, timeout;
+  int bad;
 };
 
 // Grid (splits * row blocks * Hkv, B).  A block owns 8 NT rows of one kv head
@@ -138,13 +138,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2) tree_attn_q4_rows_kernel(cons
   const int split = blockIdx.x % p.splits, hr = blockIdx.x / p.splits;
   const int h = hr / p.row_blocks, rb = hr % p.row_blocks;
   const int b = blockIdx.y;
-  if (tid == 0) {
-    for (int w = 0; w < kRowsWarps; ++w)
-      for (int s = 0; s < kRowsStages; ++s) mbar_init(smem_addr(&sh.full[w][s]), 1);
-    fence_mbar_init();
-    sh.bad = 0;
-    sh.timeout = 0;
-  }
+  if (tid == 0) sh.bad = 0;
   __syncthreads();
   pdl_wait();
   const int row0 = rb * 8 * NT;
@@ -178,7 +172,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2) tree_attn_q4_rows_kernel(cons
   }
 
   if (work) {
-    // ---- the page stream: lane 0 fetches, every lane knows the ids ----
+    // ---- the page stream: each page is one group of the lanes' copies ----
     const int32_t *trow = p.table + (size_t)b * p.max_blocks;
     const int mine = last - first > warp ? (last - first - warp + kRowsWarps - 1) / kRowsWarps : 0;
     const uint32_t ring = smem_addr(smem) + warp * kRowsStages * L::kStage;
@@ -197,18 +191,22 @@ __global__ void __launch_bounds__(kRowsThreads, 2) tree_attn_q4_rows_kernel(cons
     };
     auto issue = [&](int it) {
       const int id = __shfl_sync(0xffffffffu, ids, it & 31);
-      if (lane == 0) {
-        const uint32_t bar = smem_addr(&sh.full[warp][it % kRowsStages]);
-        const uint32_t dst = ring + (it % kRowsStages) * L::kStage;
-        const size_t off = ((size_t)id * p.Hkv + h) * L::kPageBytes;
-        mbar_arrive_expect_tx(bar, L::kStage);
-        bulk_load(dst, p.k + off, L::kPageBytes, bar);
-        bulk_load(dst + L::kPageBytes, p.v + off, L::kPageBytes, bar);
+      const size_t off = ((size_t)id * p.Hkv + h) * L::kPageBytes;
+      const uint32_t dst = ring + (it % kRowsStages) * L::kStage;
+#pragma unroll
+      for (int c = 0; c < (L::kChunks + 31) / 32; ++c) {
+        const int x = c * 32 + lane;  // K's chunks, then V's: they lie one after the other
+        const uint8_t *src = x < L::kChunks / 2 ? p.k + off + 16 * x : p.v + off + 16 * (x - L::kChunks / 2);
+        if (x < L::kChunks) cp_async_16(dst + 16 * x, src);
       }
     };
+    auto commit = [] { asm volatile("cp.async.commit_group;\n" ::: "memory"); };
     if (mine > 0) fetch_ids(0);
     int issued = 0;
-    for (; !stop && issued < min(mine, kRowsStages); ++issued) issue(issued);
+    for (int i = 0; i < kRowsStages; ++i) {  // one group a stage, an empty one past the end
+      if (!stop && issued < mine) issue(issued++);
+      commit();
+    }
 
     // ---- Q^T as B operands: row i of each 8-row tile ----
     uint32_t qf[NT][kSteps][2];
@@ -257,14 +255,8 @@ __global__ void __launch_bounds__(kRowsThreads, 2) tree_attn_q4_rows_kernel(cons
 
     for (int it = 0; it < mine && !stop; ++it) {
       const int st = it % kRowsStages;
-      if (!mbar_wait(smem_addr(&sh.full[warp][st]), (it / kRowsStages) & 1, p.wait_limit_ns)) {
-        if (lane == 0) sh.timeout = 1;
-        stop = true;
-      }
-      if (__any_sync(0xffffffffu, stop)) {
-        stop = true;
-        break;
-      }
+      asm volatile("cp.async.wait_group %0;\n" ::"n"(kRowsStages - 1) : "memory");
+      __syncwarp();
       const uint8_t *kp = ring_p + st * L::kStage, *vp = kp + L::kPageBytes;
       const int t0 = (first + warp + it * kRowsWarps) * kPage;  // first key slot
 
@@ -319,6 +311,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2) tree_attn_q4_rows_kernel(cons
         if ((issued & 31) == 0) fetch_ids(issued);
         if (!stop) issue(issued++);
       }
+      commit();
 
       // softmax: t = s * mul, and what the row may not see is -inf
 #pragma unroll
@@ -405,12 +398,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2) tree_attn_q4_rows_kernel(cons
         }
       }
     }
-    if (stop) {  // copies in flight land before the block's memory is reused
-      if (lane == 0)
-        for (int it = max(0, issued - kRowsStages); it < issued; ++it)
-          mbar_wait(smem_addr(&sh.full[warp][it % kRowsStages]), (it / kRowsStages) & 1, kRowsDrainNs);
-      __syncwarp();
-    }
+    cp_async_wait_all();  // before the ring's memory is used again
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -441,10 +429,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2) tree_attn_q4_rows_kernel(cons
   }
   __syncthreads();
   const bool bad = sh.bad != 0;
-  if (tid == 0 && p.status) {
-    if (bad) atomicOr(p.status, TSD_STATUS_BAD_PAGE);
-    if (sh.timeout) atomicOr(p.status, TSD_STATUS_TIMEOUT);
-  }
+  if (tid == 0 && bad && p.status) atomicOr(p.status, TSD_STATUS_BAD_PAGE);
   constexpr int kVec = D / 4;  // float4 of a row
   for (int x = tid; x < 8 * NT * kVec; x += kRowsThreads) {
     const int rl = x / kVec, c = x % kVec, r = row0 + rl;

@@ -6,9 +6,9 @@
 // range, walked in 128-key tiles (8 pages).  Decoding costs a fixed number of
 // instructions per key, so the more rows share a decoded tile the better; from
 // about 64 rows on the kernel is bound by the tensor cores and the softmax.
-//   warp 0       block ids, and the pages' bulk copies (9 D bytes each) into a
-//                ring of packed tiles
+//   warp 0       block ids, and the pages' copies into a ring of packed tiles
 //   warp 1       owns TMEM; lane 0 issues every MMA
+//   warp 2       tells it when the decoded tiles are there
 //   warps 4-7    decode packed tiles to fp16 K and V tiles (128-byte swizzle)
 //   warps 8-15   softmax of chain 0, warps 16-23 of chain 1: one TMEM lane (=
 //                one query row) per thread, two threads a row (64 keys each)
@@ -45,7 +45,9 @@ constexpr int kTcThreads = 768;
 constexpr int kBM = 128;            // rows of a chain's MMA
 constexpr int kBN = 128;            // keys of a tile
 constexpr int kTilePages = kBN / kPage;
-constexpr int kPackSlots = 3;       // packed K or V tiles in flight
+constexpr int kItemPages = 4;       // pages of a packed item: half a tile
+constexpr int kPackSlots = 3;       // packed items of K, and of V, in flight with two row tiles
+constexpr int kPackMost = 6;        // with one: the second Q tile's memory holds the others
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemChain = 256, kTmemO = 128;
 constexpr float kTcOffset = 8.f;    // P of the reference score is 2^8 .. 2^9
@@ -58,25 +60,30 @@ template <int D>
 struct TcLayout {
   static constexpr uint32_t kHalf = kBM * 128;         // one 64-column half of a tile
   static constexpr uint32_t kTile = kBM * D * 2;       // an fp16 Q, K or V tile
-  static constexpr uint32_t kPack = kTilePages * Q4Page<D>::kBytes;
+  static constexpr uint32_t kPack = kItemPages * Q4Page<D>::kBytes;
   static constexpr uint32_t kQ = 0;
   static constexpr uint32_t kK = 2 * kTile;
   static constexpr uint32_t kV = kK + 2 * kTile;
-  static constexpr uint32_t kP = kV + 2 * kTile;       // packed ring
-  static constexpr uint32_t kBytes = kP + kPackSlots * kPack;
+  static constexpr uint32_t kP = kV + 2 * kTile;       // packed rings
+  static constexpr uint32_t kBytes = kP + 2 * kPackSlots * kPack;
   static constexpr uint32_t kAlloc = kBytes + 1024;    // alignment slack
   static_assert(kAlloc <= 227 * 1024, "shared memory");
-  static_assert(4 * kTile >= kBM * D * 4, "the joined chain's O fits the K and V tiles");
+  static_assert(2 * (kPackMost - kPackSlots) * kPack <= kTile, "packed items in place of a Q tile");
+  // slot of the ring of K (v = 0) or V (v = 1)
+  static __device__ __forceinline__ uint32_t pack(int v, int slot) {
+    return slot < kPackSlots ? kP + (v * kPackSlots + slot) * kPack
+                             : kQ + kTile + (v * (kPackMost - kPackSlots) + slot - kPackSlots) * kPack;
+  }
 };
 
 struct TcShared {
-  uint64_t pk_full[kPackSlots], pk_empty[kPackSlots];
+  uint64_t pk_full[2][kPackMost], pk_empty[2][kPackMost];  // K, V
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
   uint64_t s_full[2], p_full[2], o_final[2], q_full, drain;
   float2 ml[kBM];           // chain 1's (reference, sum) when it shares chain 0's rows
   float half[2][2][kBM];    // by chain, thread of the row, row: exchange between the two
   uint8_t asks[2][2][kBM];  // likewise
-  int stop[3][2];           // by chain (2: decode) and tile parity: a wait ran out
+  int stop[2][2];           // by chain and tile parity: a wait ran out
   uint32_t tmem_base;
   int abort, bad;
 };
@@ -155,21 +162,6 @@ __device__ __forceinline__ uint32_t mask_scores(const Q4Attn &p, int b, int node
   return vis;
 }
 
-// Item m of the packed stream: K_0, then K_i and V_{i-1} for i = 1 .. n - 1,
-// then V_{n-1}: the order the MMAs want them in.
-__device__ __forceinline__ void stream_item(int m, int n, int &tile, bool &is_v) {
-  if (m == 0) {
-    tile = 0;
-    is_v = false;
-  } else if (m == 2 * n - 1) {
-    tile = n - 1;
-    is_v = true;
-  } else {
-    is_v = (m & 1) == 0;
-    tile = is_v ? m / 2 - 1 : (m + 1) / 2;
-  }
-}
-
 // Grid (splits * row blocks * Hkv, B); p.row_blocks blocks of 256 rows, or of
 // 128 when the sequence has no more.
 template <int D>
@@ -206,16 +198,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4
   // alternate between the chains
   const bool two = row0 + kBM < rows_valid && rows_per_block > kBM;
   const int chains = two ? 2 : (n > 1 ? 2 : 1);
+  const int ring = two ? kPackSlots : kPackMost;
 
   if (tid == 0) {
-    for (int i = 0; i < kPackSlots; ++i) {
-      mbar_init(smem_addr(&sh.pk_full[i]), 1);
-      mbar_init(smem_addr(&sh.pk_empty[i]), 4);
+    for (int i = 0; i < 2 * kPackMost; ++i) {
+      mbar_init(smem_addr(&sh.pk_full[i / kPackMost][i % kPackMost]), 1);
+      mbar_init(smem_addr(&sh.pk_empty[i / kPackMost][i % kPackMost]), 2);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_addr(&sh.k_full[i]), 4);
+      mbar_init(smem_addr(&sh.k_full[i]), 2);
       mbar_init(smem_addr(&sh.k_empty[i]), 1);
-      mbar_init(smem_addr(&sh.v_full[i]), 4);
+      mbar_init(smem_addr(&sh.v_full[i]), 2);
       mbar_init(smem_addr(&sh.v_empty[i]), 1);
       mbar_init(smem_addr(&sh.s_full[i]), 1);
       mbar_init(smem_addr(&sh.p_full[i]), two && i == 1 ? 8 : 9);  // softmax warps, hand-over
@@ -225,7 +218,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4
     mbar_init(smem_addr(&sh.drain), 1);
     sh.abort = 0;
     sh.bad = 0;
-    for (int i = 0; i < 6; ++i) sh.stop[i >> 1][i & 1] = 0;
+    for (int i = 0; i < 4; ++i) sh.stop[i >> 1][i & 1] = 0;
     fence_mbar_init();
   }
   if (warp == 1) tmem_alloc(smem_addr(&sh.tmem_base), kTmemCols);
@@ -234,52 +227,65 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4
   tc_fence_after();
   const uint32_t tmem = sh.tmem_base;
 
+  // rows that no chain computes, when they go straight to the output
+  if (p.splits == 1) {
+    const int end = min(p.rows, row0 + rows_per_block);
+    for (int x = tid; x < (end - row0) * (D / 8); x += kTcThreads) {
+      const int r = row0 + x / (D / 8);
+      if (work && r < rows_valid) continue;
+      const size_t orow = q4_out_row(p, b, h, r);
+      reinterpret_cast<uint4 *>(p.out + orow * D)[x % (D / 8)] = make_uint4(0u, 0u, 0u, 0u);
+      if (x % (D / 8) == 0 && p.lse) p.lse[orow] = -INFINITY;
+    }
+  }
+
+  // The roles.  What follows them is compiled for all of them, so it has to fit
+  // the smallest share of registers: nothing but the teardown.
   if (warp < 4) {
     regs_down<kRegsIssue>();
-    if (work && warp == 0) {
-      // ---- loader: lane l < 8 copies page l of the item ----
-      // Block ids come 32 (four tiles) at a time and a batch ahead: read for each
-      // item, their latency was on every item's path (1.35 us a tile).
+    if (work && (warp == 0 || warp == 3)) {
+      // ---- loaders: warp 0 K, warp 3 V, half a tile at a time; lane l < 4 copies the
+      // item's page l.  (A warp needs some 60 ns to issue a copy: one warp for K and V
+      // bound the blocks of one row tile.)  K and V have rings of their own, so that
+      // each slot has one loader and one pair of decoders, which take its items in
+      // order.  Block ids come 32 (eight items) at a time and a batch ahead: read for
+      // each item, their latency was on every item's path. ----
+      const int v = warp == 3 ? 1 : 0;
+      const uint8_t *pool = v ? p.v : p.k;
       const int32_t *trow = p.table + (size_t)b * p.max_blocks;
-      auto read_ids = [&](int tile) {  // of the batch that starts at `tile`
-        const int pg = first + tile * kTilePages + lane;
+      auto read_ids = [&](int batch) {
+        const int pg = first + batch * 32 + lane;
         return pg < last ? __ldg(trow + pg) : 0;
       };
-      int before = 0, ids = read_ids(0), ahead = read_ids(4);  // V runs a tile behind K
+      int ids = read_ids(0), ahead = read_ids(1);
       bool ok = true;
       int issued = 0;
       for (int m = 0; m < 2 * n; ++m) {
-        int tile;
-        bool is_v;
-        stream_item(m, n, tile, is_v);
-        if (!is_v && tile > 0 && (tile & 3) == 0) {
-          before = ids;
+        if (m > 0 && (m & 7) == 0) {
           ids = ahead;
-          ahead = read_ids(tile + 4);
+          ahead = read_ids((m >> 3) + 1);
         }
-        const int slot = m % kPackSlots;
-        // (a V tile whose K's batch is not the current one: the last before a new batch)
-        const bool old = is_v && (tile & 3) == 3 && tile + 1 < n;
-        const int id = __shfl_sync(0xffffffffu, old ? before : ids, (tile & 3) * kTilePages + (lane & 7));
-        const bool mine = lane < kTilePages && first + tile * kTilePages + lane < last;
+        const int slot = m % ring;
+        const int id = __shfl_sync(0xffffffffu, ids, (m & 7) * kItemPages + (lane & (kItemPages - 1)));
+        const bool mine = lane < kItemPages && first + m * kItemPages + lane < last;
         const bool bad = mine && (id < 0 || id >= p.num_blocks);
         if (bad) sh.bad = 1;
-        if (m >= kPackSlots)
-          ok = __all_sync(0xffffffffu, tc_wait(sh.pk_empty[slot], ((m / kPackSlots) - 1) & 1, lim, abort));
+        if (m >= ring)
+          ok = __all_sync(0xffffffffu, tc_wait(sh.pk_empty[v][slot], ((m / ring) - 1) & 1, lim, abort));
         if (!ok) break;
         const bool copy = mine && !bad;
         const int copies = __popc(__ballot_sync(0xffffffffu, copy));
-        const uint32_t bar = smem_addr(&sh.pk_full[slot]);
+        const uint32_t bar = smem_addr(&sh.pk_full[v][slot]);
         if (lane == 0) mbar_arrive_expect_tx(bar, copies * Page::kBytes);
         __syncwarp();
         if (copy)
-          bulk_load(base + L::kP + slot * L::kPack + lane * Page::kBytes,
-                    (is_v ? p.v : p.k) + ((size_t)id * p.Hkv + h) * Page::kBytes, Page::kBytes, bar);
+          bulk_load(base + L::pack(v, slot) + lane * Page::kBytes,
+                    pool + ((size_t)id * p.Hkv + h) * Page::kBytes, Page::kBytes, bar);
         issued = m + 1;
       }
       // no copy is in flight when the block exits
-      for (int m = max(0, issued - kPackSlots); m < issued; ++m)
-        mbar_wait(smem_addr(&sh.pk_full[m % kPackSlots]), (m / kPackSlots) & 1, kTcDrainNs);
+      for (int m = max(0, issued - ring); m < issued; ++m)
+        mbar_wait(smem_addr(&sh.pk_full[v][m % ring]), (m / ring) & 1, kTcDrainNs);
     } else if (work && warp == 1) {
       // ---- MMA issue ----
       if (lane == 0) {
@@ -360,39 +366,35 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4
     }
   } else if (warp < 8) {
     regs_down<kRegsDecode>();
-    // ---- decode: a lane takes one group (16 columns) of a key at a time ----
+    // ---- decode: warps 4 and 5 K tiles, 6 and 7 V tiles (two tiles at a time hide
+    // each other's waits and fences: 128-row blocks were bound by four warps on
+    // one tile); a lane takes one group (16 columns) of a key at a time ----
     constexpr int kGroups = D / kQ4Group;        // lanes across one key
     constexpr int kKeys = 32 / kGroups;          // keys per warp step
-    const int dw = warp - 4;
+    constexpr int kSteps = kItemPages * kPage / (2 * kKeys);  // steps of a warp
+    const int v = warp >= 6 ? 1 : 0;
+    const int dw = warp & 1;
     const int grp = lane % kGroups, kl = lane / kGroups;
-    for (int m = 0; m < 2 * n; ++m) {
-      int tile;
-      bool is_v;
-      stream_item(m, n, tile, is_v);
-      const int slot = m % kPackSlots, st = tile & 1;
-      // one warp looks at the barriers, the others wait for it without polling
-      if (dw == 0) {
-        bool ok = tc_wait(sh.pk_full[slot], (m / kPackSlots) & 1, lim, abort);
-        if (ok && tile >= 2) ok = tc_wait(is_v ? sh.v_empty[st] : sh.k_empty[st], ((tile >> 1) - 1) & 1, lim, abort);
-        if (!ok) sh.stop[2][m & 1] = 1;
-      }
-      asm volatile("barrier.cta.sync 4, 128;\n" ::: "memory");
-      if (sh.stop[2][m & 1]) break;
-      const uint8_t *src = gbase + L::kP + slot * L::kPack;
-      uint8_t *dst = gbase + (is_v ? L::kV : L::kK) + st * L::kTile + (D == 128 ? (grp >> 2) * L::kHalf : 0);
-      const int c0 = (grp & 3) * 2;
-      // the two halves of a key are stored in opposite order, so that the
-      // eight lanes of a store's quarter touch different banks
-      const int flip = D == 128 ? grp >> 2 : 0;
+    // the two halves of a key are stored in opposite order, so that the eight
+    // lanes of a store's quarter touch different banks
+    const int flip = D == 128 ? grp >> 2 : 0;
+    const int c0 = (grp & 3) * 2;
+    for (int m = 0; m < 2 * n; ++m) {  // half tiles
+      const int tile = m >> 1, st = tile & 1, slot = m % ring;
+      bool ok = tc_wait(sh.pk_full[v][slot], (m / ring) & 1, lim, abort);
+      if (ok && tile >= 2 && (m & 1) == 0)
+        ok = tc_wait(v ? sh.v_empty[st] : sh.k_empty[st], ((tile >> 1) - 1) & 1, lim, abort);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      const uint8_t *src = gbase + L::pack(v, slot);
+      uint8_t *dst = gbase + (v ? L::kV : L::kK) + st * L::kTile + (D == 128 ? (grp >> 2) * L::kHalf : 0) +
+                     (m & 1) * (kBN / 2) * 128;
       // every read comes before the first store: the compiler must assume that a
-      // store changes what the next read sees, and would wait out each one's
-      // latency (1.4 us a 128-key tile that way)
-      constexpr int kSteps = kBN / (4 * kKeys);
+      // store changes what the next read sees, and would wait out each one's latency
       uint2 code[kSteps];
       uint32_t scale[kSteps];
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) {
-        const int key = (s * 4 + dw) * kKeys + kl;
+        const int key = (s * 2 + dw) * kKeys + kl;
         const uint8_t *page = src + (key / kPage) * Page::kBytes;
         const int r = key % kPage;
         code[s] = *reinterpret_cast<const uint2 *>(page + r * Page::kRow + grp * 8);
@@ -400,7 +402,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4
       }
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) {
-        const int key = (s * 4 + dw) * kKeys + kl;
+        const int key = (s * 2 + dw) * kKeys + kl;
         const uint32_t sc = q4_scale2(scale[s]);
         uint32_t a[4], e[4];
         q4_decode8(flip ? code[s].y : code[s].x, a);
@@ -413,11 +415,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4
         *reinterpret_cast<uint4 *>(dst + sw128_offset(key, c0 + flip)) = make_uint4(a[0], a[1], a[2], a[3]);
         *reinterpret_cast<uint4 *>(dst + sw128_offset(key, c0 + 1 - flip)) = make_uint4(e[0], e[1], e[2], e[3]);
       }
-      fence_proxy_async_smem();  // the tensor core reads the tile through the async proxy
+      if (m & 1) fence_proxy_async_smem();  // the tensor core reads the tile through the async proxy
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(smem_addr(is_v ? &sh.v_full[st] : &sh.k_full[st]));
-        mbar_arrive(smem_addr(&sh.pk_empty[slot]));
+        if (m & 1) mbar_arrive(smem_addr(v ? &sh.v_full[st] : &sh.k_full[st]));
+        mbar_arrive(smem_addr(&sh.pk_empty[v][slot]));
       }
     }
   } else {
@@ -509,20 +511,28 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4
       const unsigned long long ref2 = f2_pack(-ref, -ref);
       unsigned long long acc0 = 0ull, acc1 = 0ull;
       uint32_t pk[32], seen = 0u;
+      {
+        // both loads before the one wait: a load's latency is some 250 cycles
+        uint32_t x[2][32];
+        tmem_ld32(tS + half * 64, x[0]);
+        tmem_ld32(tS + half * 64 + 32, x[1]);
+        tmem_wait_ld(x[0]);
+        tmem_wait_ld(x[1]);
+        if (tail) {
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        uint32_t s[32];
-        tmem_ld32(tS + half * 64 + k * 32, s);
-        tmem_wait_ld(s);
-        if (tail) seen |= mask_scores(p, b, node, rvalid, t0 + k * 32 - P, nb, s);
+          for (int k = 0; k < 2; ++k) seen |= mask_scores(p, b, node, rvalid, t0 + k * 32 - P, nb, x[k]);
+        }
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float2 t = f2_unpack(
-              f2_fma(f2_pack(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), mul2, ref2));
-          const float e0 = ex2_approx(t.x), e1 = ex2_approx(t.y);
-          pk[k * 16 + i] = pack_half2(e0, e1);
-          if (i & 1) acc1 = f2_add(acc1, f2_pack(e0, e1));
-          else acc0 = f2_add(acc0, f2_pack(e0, e1));
+        for (int k = 0; k < 2; ++k) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float2 t = f2_unpack(f2_fma(
+                f2_pack(__uint_as_float(x[k][2 * i]), __uint_as_float(x[k][2 * i + 1])), mul2, ref2));
+            const float e0 = ex2_approx(t.x), e1 = ex2_approx(t.y);
+            pk[k * 16 + i] = pack_half2(e0, e1);
+            if (i & 1) acc1 = f2_add(acc1, f2_pack(e0, e1));
+            else acc0 = f2_add(acc0, f2_pack(e0, e1));
+          }
         }
       }
       const float2 acc = f2_unpack(f2_add(acc0, acc1));
@@ -686,17 +696,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4
         else if (p.lse)
           p.lse[orow] = empty ? -INFINITY : (M + log2f(l)) * kTcLn2;
       }
-    }
-  }
-  // rows that no chain computed, when they go straight to the output
-  if (p.splits == 1) {
-    const int end = min(p.rows, row0 + rows_per_block);
-    for (int x = tid; x < (end - row0) * (D / 8); x += kTcThreads) {
-      const int r = row0 + x / (D / 8);
-      if (work && r < rows_valid) continue;
-      const size_t orow = q4_out_row(p, b, h, r);
-      reinterpret_cast<uint4 *>(p.out + orow * D)[x % (D / 8)] = make_uint4(0u, 0u, 0u, 0u);
-      if (x % (D / 8) == 0 && p.lse) p.lse[orow] = -INFINITY;
     }
   }
   tc_fence_before();
