@@ -403,6 +403,8 @@ def _long_inputs(seed, B, N, Hq, Hkv, D, prefix, nodes):
     (12, 100, 24, 8, 64, list(range(300, 300 + 12 * 333, 333)), [100, 65] * 6),
     (1, 256, 16, 1, 128, [12345], [255]),
     (5, 256, 128, 8, 128, [900, 1, 2000, 127, 128], [256, 255, 129, 1, 128]),
+    (70, 1, 4, 1, 128, list(range(1, 1 + 70 * 37, 37)), [1] * 70),
+    (66, 20, 4, 2, 64, list(range(5, 5 + 66 * 23, 23)), [20, 7, 1] * 22),
 ])
 def test_attention_long(tsd, B, N, Hq, Hkv, D, prefix, nodes):
     x = _long_inputs(B + N, B, N, Hq, Hkv, D, prefix, nodes)
@@ -412,6 +414,34 @@ def test_attention_long(tsd, B, N, Hq, Hkv, D, prefix, nodes):
     assert int(st.item()) == 0
     got, lse = _run(tsd, x, mask=None, max_slots=2 * x["max_slots"])
     _check(x, got, lse, _ref_on_gpu(x, chain=True))
+
+
+@pytest.mark.parametrize("B,N,Hq,Hkv,prefix", [
+    (16, 31, 32, 8, list(range(64, 64 + 16 * 190, 190))),   # 128-row blocks: alternate key tiles
+    (6, 100, 32, 8, [2000, 130, 900, 4000, 17, 1200]),      # 256-row blocks: two row tiles
+    (24, 2, 32, 8, list(range(100, 100 + 24 * 173, 173))),  # the few-row kernel
+])
+def test_attention_repeats_exactly(tsd, B, N, Hq, Hkv, prefix):
+    """The same call many times over, other work between: every result is the
+    first one, bit for bit (a missing wait shows as a rare wrong tile)."""
+    import torch
+    x = _long_inputs(B, B, N, Hq, Hkv, 128, prefix, [N] * B)
+    a = {k: T(v) for k, v in x.items() if k in ("k", "v", "table", "P", "n", "err")}
+    q, m = bf(x["q"]), T(x["mask"].view(np.int32))
+    noise = torch.empty(1 << 24, device="cuda")
+
+    def call():
+        return tsd.tree_attn_fwd_q4(q, a["k"], a["v"], a["table"], a["P"], a["n"], m, a["err"], x["max_slots"])
+
+    out, lse = call()
+    _check(x, oracle.bf16_to_f64(np_of(out, np.uint16)), np_of(lse).astype(np.float64), _ref_on_gpu(x))
+    wrong = torch.zeros(1, dtype=torch.int64, device="cuda")
+    for i in range(200):
+        if i % 3 == 0:
+            noise.normal_()  # other lines in L2
+        o2, l2 = call()
+        wrong += (o2.view(torch.int16) != out.view(torch.int16)).sum() + (l2 != lse).sum()
+    assert int(wrong.item()) == 0
 
 
 @pytest.mark.parametrize("scale", [0.0, -0.3, 1e-30, 3.0])

@@ -114,6 +114,7 @@ struct RowsShared {
   float2 ml[kRowsWarps][16];  // (reference, sum) of each warp's rows
   float4 block_ml[16];        // and of the block's (sum -1: bad page)
   int bad;
+  Q4PlanShared plan;
 };
 
 // Grid (splits * row blocks * Hkv, B).  A block owns 8 NT rows of one kv head
@@ -135,12 +136,28 @@ __global__ void __launch_bounds__(kRowsThreads, 2) tree_attn_q4_rows_kernel(cons
   pdl_trigger();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int qi = lane >> 2, qt = lane & 3;  // (i, t)
-  const int split = blockIdx.x % p.splits, hr = blockIdx.x / p.splits;
-  const int h = hr / p.row_blocks, rb = hr % p.row_blocks;
-  const int b = blockIdx.y;
   if (tid == 0) sh.bad = 0;
-  __syncthreads();
   pdl_wait();
+  int split, h, rb, b, pieces = p.splits, chunk = p.chunk;
+  if (p.planned) {
+    if (warp == 0) q4_plan_item(p, sh.plan, blockIdx.x);
+    __syncthreads();
+    const Q4Item item = sh.plan.item;
+    if (item.b < 0) return;
+    b = item.b;
+    h = item.h;
+    rb = item.rb;
+    split = item.split;
+    pieces = item.pieces;
+    chunk = item.chunk;
+  } else {
+    split = blockIdx.x % p.splits;
+    const int hr = blockIdx.x / p.splits;
+    h = hr / p.row_blocks;
+    rb = hr % p.row_blocks;
+    b = blockIdx.y;
+    __syncthreads();
+  }
   const int row0 = rb * 8 * NT;
   int P, nb;
   bool bad_len;
@@ -149,10 +166,10 @@ __global__ void __launch_bounds__(kRowsThreads, 2) tree_attn_q4_rows_kernel(cons
     atomicOr(p.status, TSD_STATUS_BAD_LEN);
   const int rows_valid = ok ? nb * p.g : 0;
   const int pages = ok ? (P + nb + kPage - 1) / kPage : 0;
-  const int chunk = p.cluster ? (pages + p.splits - 1) / p.splits : p.chunk;
+  if (p.cluster) chunk = (pages + p.splits - 1) / p.splits;
   const int first = split * chunk, last = min(pages, first + chunk);
   const bool work = row0 < rows_valid && first < last;
-  if (!work && p.splits > 1 && !p.cluster) return;
+  if (!work && pieces > 1 && !p.cluster) return;
 
   float o[NT][kTiles][4];
   float l[NT][2], trig[NT][2], ref[NT][2], mul[NT][2];
@@ -455,12 +472,13 @@ __global__ void __launch_bounds__(kRowsThreads, 2) tree_attn_q4_rows_kernel(cons
     if (p.cluster) {
       *reinterpret_cast<float4 *>(block_o + rl * D + 4 * c) = a;
       if (c == 0) sh.block_ml[rl] = make_float4(M, bad ? -1.f : sum, 0.f, 0.f);
-    } else if (p.splits > 1) {
+    } else if (pieces > 1) {
       if (r >= rows_valid) continue;
-      const size_t pr = (((size_t)b * p.Hkv + h) * p.splits + split) * p.rows + r;
+      const size_t pr =
+          (p.planned ? (size_t)blockIdx.x * p.rows_per_block : q4_part_row(p, b, h, rb, split)) + rl;
       *reinterpret_cast<float4 *>(p.part_o + pr * D + 4 * c) = a;
       if (c == 0) p.part_ml[pr] = make_float2(M, bad ? -1.f : sum);
-    } else {
+    } else if (!p.planned || r < rows_valid) {  // (planned: the join writes the others)
       rows_out(p, q4_out_row(p, b, h, r), D, c, a, M, sum, r >= rows_valid || bad);
     }
   }
@@ -515,13 +533,25 @@ __global__ void __launch_bounds__(256) tree_attn_q4_join_kernel(const Q4Attn p) 
   int P, nb;
   bool bad_len;
   const bool ok = q4_seq(p, b, P, nb, bad_len) && r < nb * p.g;
-  const int pieces = ok ? ((P + nb + kPage - 1) / kPage + p.chunk - 1) / p.chunk : 0;
-  const size_t base = (size_t)bh * p.splits * p.rows + r;
+  const int rb = r / p.rows_per_block;
+  int pieces = 0;
+  size_t base = 0, step = 0;  // partial row of the first piece, and from one piece to the next
+  if (ok && p.planned) {
+    const int4 plan = p.plan[b];
+    pieces = plan.y;
+    if (pieces == 1) return;  // its block has written it
+    base = (size_t)(plan.x + h * pieces * plan.w + rb) * p.rows_per_block + r % p.rows_per_block;
+    step = (size_t)plan.w * p.rows_per_block;
+  } else if (ok) {
+    pieces = ((P + nb + kPage - 1) / kPage + p.chunk - 1) / p.chunk;
+    base = q4_part_row(p, b, h, rb, 0) + r % p.rows_per_block;
+    step = p.rows_per_block;
+  }
   // lane l holds the (reference, sum) of pieces l, l + 32, ...: at most 64
   float2 ml[2] = {make_float2(-INFINITY, 0.f), make_float2(-INFINITY, 0.f)};
 #pragma unroll
   for (int e = 0; e < 2; ++e)
-    if (lane + 32 * e < pieces) ml[e] = p.part_ml[base + (size_t)(lane + 32 * e) * p.rows];
+    if (lane + 32 * e < pieces) ml[e] = p.part_ml[base + (size_t)(lane + 32 * e) * step];
   const bool bad = __any_sync(0xffffffffu, ml[0].y == -1.f || ml[1].y == -1.f);
   float M = fmaxf(ml[0].x, ml[1].x);
 #pragma unroll
@@ -540,7 +570,7 @@ __global__ void __launch_bounds__(256) tree_attn_q4_join_kernel(const Q4Attn p) 
   for (int c = 0; c < kPer; ++c) a[c] = 0.f;
   for (int s = 0; s < pieces; ++s) {
     const float fs = __shfl_sync(0xffffffffu, s < 32 ? f[0] : f[1], s & 31);
-    const float *src = p.part_o + (base + (size_t)s * p.rows) * D + lane * kPer;
+    const float *src = p.part_o + (base + (size_t)s * step) * D + lane * kPer;
     if constexpr (kPer == 4) {
       const float4 v = *reinterpret_cast<const float4 *>(src);
       a[0] += fs * v.x;
@@ -566,8 +596,6 @@ __global__ void __launch_bounds__(256) tree_attn_q4_join_kernel(const Q4Attn p) 
   if (lane == 0 && p.lse) p.lse[orow] = empty ? -INFINITY : (M + log2f(sum)) * kRowsLn2;
 }
 
-constexpr int kQ4MaxSplits = 64;
-
 // Key ranges of up to this many pages are cut into at most 8 pieces (a
 // cluster) even where more would fill the GPU.
 constexpr int kClusterPages = 512;
@@ -575,12 +603,16 @@ constexpr int kClusterPages = 512;
 struct Q4Plan {
   bool tc;       // the many-row kernel
   bool cluster;  // pieces joined inside a cluster
-  int nt, rows_per_block, row_blocks, splits, chunk;
-  size_t ml_off, bytes;
+  bool planned;  // pieces from the actual lengths
+  int nt, rows_per_block, row_blocks, splits, chunk, blocks;
+  size_t plan_bytes, ml_bytes, bytes;  // workspace: the plan, (reference, sum) of the partial rows, the rows
 };
 
 // Rows of a kv head from which the many-row kernel runs.
 constexpr int kTcMinRows = 33;
+// Set-up and end of a block, in units of 8 pages: 4 tiles of the many-row kernel,
+// 8 pages a warp of the few-row kernel (about 6 and 3 us).
+constexpr int kTcFixed = 4, kRowsFixed = 8;
 
 // Host: how a call is cut up.
 Q4Plan q4_plan(int B, int N_max, int Hq, int Hkv, int D, int max_slots) {
@@ -592,52 +624,48 @@ Q4Plan q4_plan(int B, int N_max, int Hq, int Hkv, int D, int max_slots) {
   pl.rows_per_block = pl.tc ? (rows > 128 ? 256 : 128) : 8 * pl.nt;
   pl.row_blocks = (rows + pl.rows_per_block - 1) / pl.rows_per_block;
   const int64_t base = (int64_t)B * Hkv * pl.row_blocks;
-  if (pl.tc) {
-    // waves x (tiles of a block + 4 for its set-up and epilogue), and with
-    // several pieces the fp32 partials' way through memory (a 128-key tile
-    // takes about 1.5 us, memory moves about 7.5 MB in that time)
-    const int tiles = (pages + 7) / 8;
-    double best = 1e300;
-    int best_per = tiles;
-    for (int s = 1; s <= kQ4MaxSplits && s <= tiles; ++s) {
-      const int per = (tiles + s - 1) / s;
-      const int64_t waves = (base * ((tiles + per - 1) / per) + sm_count() - 1) / sm_count();
-      double cost = (double)waves * (per + 4);
-      if (per < tiles) cost += 3 + 2.0 * B * Hkv * s * rows * D * 4 / 7.5e6;
-      if (cost < best) {
-        best = cost;
-        best_per = per;
-      }
-    }
-    pl.chunk = best_per * 8;
-  } else {
-    const int64_t slots = 2ll * sm_count();
-    int64_t want = (4 * slots + base - 1) / base;  // pieces for four blocks per block slot
-    want = std::min<int64_t>(want, (pages + 2 * kRowsWarps - 1) / (2 * kRowsWarps));
-    want = std::max<int64_t>(1, std::min<int64_t>(want, kQ4MaxSplits));
-    pl.chunk = (int)((pages + want - 1) / want);
-    if (want > 1 && (want <= 8 || pages <= kClusterPages)) {
-      // a cluster of 2, 4 or 8
-      int c = 2;
-      while (c < want && c < 8) c *= 2;
-      pl.cluster = true;
-      pl.splits = c;
-      return pl;
-    }
+  const int slots = (pl.tc ? 1 : 2) * sm_count();
+  pl.splits = 1;
+  pl.chunk = pages;
+  pl.blocks = (int)base;
+  const int units = (pages + kUnitPages - 1) / kUnitPages;
+  if (units <= 2 || base >= 16ll * slots) return pl;  // nothing to gain from cutting
+  if (!pl.tc && pages <= kClusterPages && base < slots) {
+    // Short ranges of few blocks: a cluster of 2, 4 or 8 (a workspace and a second
+    // launch would cost more than the pieces it could add).
+    const int64_t want = std::min<int64_t>((2 * slots + base - 1) / base, (pages + kRowsWarps - 1) / kRowsWarps);
+    int c = 2;
+    while (c < want && c < 8) c *= 2;
+    pl.cluster = true;
+    pl.splits = c;
+    pl.blocks = (int)base * c;
+    return pl;
   }
-  pl.splits = (pages + pl.chunk - 1) / pl.chunk;
-  const size_t n = (size_t)B * Hkv * pl.splits * rows;
-  pl.ml_off = align_up(n * D * 4, 256);
-  pl.bytes = pl.splits > 1 ? pl.ml_off + n * 8 : 0;
+  if (B <= kPlanSeqs) {
+    pl.planned = true;
+    pl.blocks = (int)std::min<int64_t>(base * std::min(units, kPlanPieces), base + 2ll * slots);
+  } else {
+    // Batches too large to plan: enough pieces of the longest range for four
+    // blocks a slot.
+    const int64_t want = std::min<int64_t>((4ll * slots + base - 1) / base, std::min(units, kPlanPieces));
+    pl.chunk = (int)((units + want - 1) / want) * kUnitPages;
+    pl.splits = (pages + pl.chunk - 1) / pl.chunk;
+    pl.blocks = (int)base * pl.splits;
+    if (pl.splits == 1) return pl;
+  }
+  const size_t part_rows = (size_t)pl.blocks * pl.rows_per_block;
+  pl.plan_bytes = align_up(kPlanSeqs * sizeof(int4), 256);
+  pl.ml_bytes = align_up(part_rows * sizeof(float2), 256);
+  pl.bytes = pl.plan_bytes + pl.ml_bytes + part_rows * D * sizeof(float);
   return pl;
 }
 
 template <int D, int NT>
-cudaError_t rows_launch(const Q4Attn &p, cudaStream_t s) {
+cudaError_t rows_launch(const Q4Attn &p, int blocks, cudaStream_t s) {
   const int smem = RowsLayout<D, NT>::kBytes;
   if (!set_smem((const void *)tree_attn_q4_rows_kernel<D, NT>, smem)) return cudaErrorUnknown;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)p.splits * p.Hkv * p.row_blocks, p.B);
+  cfg.gridDim = p.planned ? dim3(blocks) : dim3((unsigned)p.splits * p.Hkv * p.row_blocks, p.B);
   cfg.blockDim = dim3(kRowsThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
@@ -710,12 +738,23 @@ TSD_API int tsd_tree_attn_fwd_q4(const uint16_t *q, const uint8_t *k_cache, cons
   p.max_slots = max_slots;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.rows = N_max * p.g;
+  p.rows_per_block = pl.rows_per_block;
   p.row_blocks = pl.row_blocks;
   p.splits = pl.splits;
   p.chunk = pl.chunk;
-  p.cluster = pl.cluster;
-  p.part_o = reinterpret_cast<float *>(workspace);
-  p.part_ml = pl.bytes ? reinterpret_cast<float2 *>(reinterpret_cast<char *>(workspace) + pl.ml_off) : nullptr;
+  p.cluster = pl.cluster ? pl.splits : 0;
+  p.planned = pl.planned;
+  p.slots = (pl.tc ? 1 : 2) * sm_count();
+  p.fixed = pl.tc ? kTcFixed : kRowsFixed;
+  // a partial row goes out and comes back at about 5 GB a ms; a unit takes 1.8 us in
+  // the many-row kernel and 0.4 us in the other
+  p.join_units = (int)(1024.0 * pl.rows_per_block * D * 8 / 5.0e6 / (pl.tc ? 1.8 : 0.4));
+  if (pl.bytes) {
+    char *ws = reinterpret_cast<char *>(workspace);
+    p.plan = reinterpret_cast<int4 *>(ws);
+    p.part_ml = reinterpret_cast<float2 *>(ws + pl.plan_bytes);
+    p.part_o = reinterpret_cast<float *>(ws + pl.plan_bytes + pl.ml_bytes);
+  }
   p.out = out;
   p.lse = lse;
   p.status = status;
@@ -723,13 +762,13 @@ TSD_API int tsd_tree_attn_fwd_q4(const uint16_t *q, const uint8_t *k_cache, cons
   const cudaStream_t s = as_cuda(stream);
   cudaError_t e;
   if (pl.tc)
-    e = q4_tc_launch(p, D, pl.rows_per_block, s);
+    e = q4_tc_launch(p, D, pl.blocks, s);
   else if (D == 128)
-    e = pl.nt == 2 ? rows_launch<128, 2>(p, s) : rows_launch<128, 1>(p, s);
+    e = pl.nt == 2 ? rows_launch<128, 2>(p, pl.blocks, s) : rows_launch<128, 1>(p, pl.blocks, s);
   else
-    e = pl.nt == 2 ? rows_launch<64, 2>(p, s) : rows_launch<64, 1>(p, s);
+    e = pl.nt == 2 ? rows_launch<64, 2>(p, pl.blocks, s) : rows_launch<64, 1>(p, pl.blocks, s);
   if (e != cudaSuccess) return TSD_ERR_CUDA;
-  if (pl.splits > 1 && !pl.cluster) {
+  if (pl.bytes) {
     const int64_t rows = (int64_t)B * Hkv * p.rows;
     const dim3 grid((unsigned)((rows + 7) / 8));
     e = D == 128 ? launch(tree_attn_q4_join_kernel<128>, grid, dim3(256), 0, s, p)

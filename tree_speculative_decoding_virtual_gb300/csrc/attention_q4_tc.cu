@@ -86,6 +86,7 @@ struct TcShared {
   int stop[2][2];           // by chain and tile parity: a wait ran out
   uint32_t tmem_base;
   int abort, bad;
+  Q4PlanShared plan;
 };
 
 __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn_major) {
@@ -162,10 +163,10 @@ __device__ __forceinline__ uint32_t mask_scores(const Q4Attn &p, int b, int node
   return vis;
 }
 
-// Grid (splits * row blocks * Hkv, B); p.row_blocks blocks of 256 rows, or of
-// 128 when the sequence has no more.
+// A block an item of the plan, or grid (splits * row blocks * Hkv, B); blocks of
+// 256 rows, or of 128 where a kv head has no more.
 template <int D>
-__global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4Attn p, int rows_per_block) {
+__global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4Attn p) {
   using namespace sm100;
   using L = TcLayout<D>;
   using Page = Q4Page<D>;
@@ -179,24 +180,40 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4
   volatile int *abort = &sh.abort;
   const uint64_t lim = p.wait_limit_ns;
 
-  const int split = blockIdx.x % p.splits, hr = blockIdx.x / p.splits;
-  const int h = hr / p.row_blocks, rb = hr % p.row_blocks;
-  const int b = blockIdx.y;
   pdl_wait();
+  int split, h, rb, b, pieces = p.splits, chunk = p.chunk;
+  if (p.planned) {
+    if (warp == 0) q4_plan_item(p, sh.plan, blockIdx.x);
+    __syncthreads();
+    const Q4Item item = sh.plan.item;
+    if (item.b < 0) return;
+    b = item.b;
+    h = item.h;
+    rb = item.rb;
+    split = item.split;
+    pieces = item.pieces;
+    chunk = item.chunk;
+  } else {
+    split = blockIdx.x % p.splits;
+    const int hr = blockIdx.x / p.splits;
+    h = hr / p.row_blocks;
+    rb = hr % p.row_blocks;
+    b = blockIdx.y;
+  }
   int P, nb;
   bool bad_len;
   const bool ok_seq = q4_seq(p, b, P, nb, bad_len);
   if (bad_len && blockIdx.x == 0 && tid == 0 && p.status) atomicOr(p.status, TSD_STATUS_BAD_LEN);
   const int rows_valid = ok_seq ? nb * p.g : 0;
   const int pages = ok_seq ? (P + nb + kPage - 1) / kPage : 0;
-  const int first = split * p.chunk, last = min(pages, first + p.chunk);
-  const int row0 = rb * rows_per_block;
+  const int first = split * chunk, last = min(pages, first + chunk);
+  const int row0 = rb * p.rows_per_block;
   const bool work = row0 < rows_valid && first < last;
-  if (!work && p.splits > 1) return;
+  if (!work && pieces > 1) return;
   const int n = work ? (last - first + kTilePages - 1) / kTilePages : 0;  // key tiles
   // two row tiles (each with every key tile), or one row tile whose key tiles
   // alternate between the chains
-  const bool two = row0 + kBM < rows_valid && rows_per_block > kBM;
+  const bool two = row0 + kBM < rows_valid && p.rows_per_block > kBM;
   const int chains = two ? 2 : (n > 1 ? 2 : 1);
   const int ring = two ? kPackSlots : kPackMost;
 
@@ -228,8 +245,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4
   const uint32_t tmem = sh.tmem_base;
 
   // rows that no chain computes, when they go straight to the output
-  if (p.splits == 1) {
-    const int end = min(p.rows, row0 + rows_per_block);
+  if (pieces == 1 && !p.planned) {  // (planned: the join writes them)
+    const int end = min(p.rows, row0 + p.rows_per_block);
     for (int x = tid; x < (end - row0) * (D / 8); x += kTcThreads) {
       const int r = row0 + x / (D / 8);
       if (work && r < rows_valid) continue;
@@ -352,6 +369,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4
       // that is open: the one before has to be complete.) ----
       if (lane == 0) {
         const int step = two ? 1 : 2;  // the chain's next tile
+        // Each barrier's phases are waited for one after the other (a wait for a
+        // phase whose predecessor is still open returns at once): the first K tiles
+        // too, which the issuing thread waits for itself.
+        for (int k = 0; k < step && k < n; ++k) tc_wait(sh.k_full[k], 0, lim, abort);
         for (int j = 0; j < n; ++j) {
           const int c = two ? 0 : j & 1, u = two ? j : j >> 1;
           bool ok = tc_wait(sh.v_full[j & 1], (j >> 1) & 1, lim, abort);
@@ -655,10 +676,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4
         M = top;
       }
       const bool bad = sh.bad != 0;
-      const bool direct = p.splits == 1;
+      const bool direct = pieces == 1;
       const bool empty = bad || l == 0.f;
       const float inv = empty ? 0.f : 1.f / l;
-      const size_t pr = (((size_t)b * p.Hkv + h) * p.splits + split) * p.rows + row;
+      const size_t pr =
+          (p.planned ? (size_t)blockIdx.x * p.rows_per_block : q4_part_row(p, b, h, rb, split)) + row - row0;
       const size_t orow = rvalid ? q4_out_row(p, b, h, row) : 0;
 #pragma unroll 1
       for (int q = q0; ok && q < q0 + D / 64; ++q) {
@@ -723,14 +745,14 @@ bool tc_ready() {
 }
 }  // namespace
 
-cudaError_t q4_tc_launch(const Q4Attn &p, int D, int rows_per_block, cudaStream_t s) {
-  const dim3 grid((unsigned)p.splits * p.row_blocks * p.Hkv, p.B);
+cudaError_t q4_tc_launch(const Q4Attn &p, int D, int blocks, cudaStream_t s) {
+  const dim3 grid = p.planned ? dim3(blocks) : dim3((unsigned)p.splits * p.row_blocks * p.Hkv, p.B);
   if (D == 128) {
     if (!tc_ready<128>()) return cudaErrorUnknown;
-    return launch(tree_attn_q4_tc_kernel<128>, grid, dim3(kTcThreads), TcLayout<128>::kAlloc, s, p, rows_per_block);
+    return launch(tree_attn_q4_tc_kernel<128>, grid, dim3(kTcThreads), TcLayout<128>::kAlloc, s, p);
   }
   if (!tc_ready<64>()) return cudaErrorUnknown;
-  return launch(tree_attn_q4_tc_kernel<64>, grid, dim3(kTcThreads), TcLayout<64>::kAlloc, s, p, rows_per_block);
+  return launch(tree_attn_q4_tc_kernel<64>, grid, dim3(kTcThreads), TcLayout<64>::kAlloc, s, p);
 }
 
 }  // namespace tsd
