@@ -206,15 +206,19 @@ __global__ void __launch_bounds__(kRowsThreads, 2) tree_attn_q4_rows_kernel(cons
       }
       ids = id;
     };
+    // The lane's c-th copy is chunk 32 c + lane of K's page followed by V's; only
+    // round kMixed (chunks of both) depends on the lane.
+    constexpr int kHalfChunks = L::kChunks / 2, kMixed = kHalfChunks / 32;
+    const uint8_t *k_lane = p.k + 16 * lane, *v_lane = p.v - 16 * kHalfChunks + 16 * lane;
+    const uint8_t *mixed = kMixed * 32 + lane < kHalfChunks ? k_lane : v_lane;
     auto issue = [&](int it) {
       const int id = __shfl_sync(0xffffffffu, ids, it & 31);
       const size_t off = ((size_t)id * p.Hkv + h) * L::kPageBytes;
-      const uint32_t dst = ring + (it % kRowsStages) * L::kStage;
+      const uint32_t dst = ring + (it % kRowsStages) * L::kStage + 16 * lane;
 #pragma unroll
       for (int c = 0; c < (L::kChunks + 31) / 32; ++c) {
-        const int x = c * 32 + lane;  // K's chunks, then V's: they lie one after the other
-        const uint8_t *src = x < L::kChunks / 2 ? p.k + off + 16 * x : p.v + off + 16 * (x - L::kChunks / 2);
-        if (x < L::kChunks) cp_async_16(dst + 16 * x, src);
+        const uint8_t *src = (c < kMixed ? k_lane : c == kMixed ? mixed : v_lane) + off + 512 * c;
+        if ((c + 1) * 32 <= L::kChunks || c * 32 + lane < L::kChunks) cp_async_16(dst + 512 * c, src);
       }
     };
     auto commit = [] { asm volatile("cp.async.commit_group;\n" ::: "memory"); };
@@ -289,13 +293,13 @@ __global__ void __launch_bounds__(kRowsThreads, 2) tree_attn_q4_rows_kernel(cons
         const uint32_t xa = *reinterpret_cast<const uint16_t *>(kp + Page::kScales + key_a * 8 + 2 * qt);
         const uint32_t xb =
             *reinterpret_cast<const uint16_t *>(kp + Page::kScales + (key_a + 8) * 8 + 2 * qt);
-        sa[0] = q4_scale2(xa & 0xFFu);
-        sa[1] = q4_scale2(xa >> 8);
-        sb[0] = q4_scale2(xb & 0xFFu);
-        sb[1] = q4_scale2(xb >> 8);
+        sa[0] = (xa & 0xFFu) * 0x00800080u;
+        sa[1] = (xa >> 8) * 0x00800080u;
+        sb[0] = (xb & 0xFFu) * 0x00800080u;
+        sb[1] = (xb >> 8) * 0x00800080u;
       } else {
-        sa[0] = sa[1] = q4_scale2(kp[Page::kScales + key_a * 4 + qt]);
-        sb[0] = sb[1] = q4_scale2(kp[Page::kScales + (key_a + 8) * 4 + qt]);
+        sa[0] = sa[1] = kp[Page::kScales + key_a * 4 + qt] * 0x00800080u;
+        sb[0] = sb[1] = kp[Page::kScales + (key_a + 8) * 4 + qt] * 0x00800080u;
       }
 #pragma unroll
       for (int w = 0; w < kWordsK; ++w) {
@@ -320,7 +324,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2) tree_attn_q4_rows_kernel(cons
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         lds_words(vp + kk[e] * Page::kRow + qi * (D / 16), wv[e]);
-        sv[e] = q4_scale2(vp[Page::kScales + kk[e] * Page::kScaleRow + qi * (D / 8) / kQ4Group]);
+        sv[e] = vp[Page::kScales + kk[e] * Page::kScaleRow + qi * (D / 8) / kQ4Group];
       }
       // the page is in registers: its stage can be refilled
       __syncwarp();
@@ -349,9 +353,11 @@ __global__ void __launch_bounds__(kRowsThreads, 2) tree_attn_q4_rows_kernel(cons
             if (!((vis >> (key_a + 8)) & 1u)) s[n][2 + e] = -INFINITY;
           }
         }
+        // V's slots past the sequence read as zero.  Scale bytes that no writer makes
+        // can only be met here, in slots of the tree that were not written: they read
+        // as the largest scale, so that P = 0 really leaves them out.
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (t0 + kk[e] >= P + nb) sv[e] = 0u;
+        for (int e = 0; e < 4; ++e) sv[e] = t0 + kk[e] >= P + nb ? 0u : min(sv[e], kQ4MaxScale);
       }
       bool over = false;
 #pragma unroll
@@ -394,24 +400,27 @@ __global__ void __launch_bounds__(kRowsThreads, 2) tree_attn_q4_rows_kernel(cons
         pb[n][1] = transpose8x8(pack_half2(p2, p3));
       }
 
-      // O^T: M tile j holds columns i D/8 + 2 j (row i) and the next (row i + 8)
+      // O^T: M tile j holds columns i D/8 + 2 j (row i) and the next (row i + 8).  An
+      // operand register holds one column of two keys, so the codes of two keys are
+      // interleaved before they are decoded (three operations for eight registers;
+      // after, it takes a byte permutation each, on the pipe that also converts).
+      const uint32_t s01 = sv[0] * 0x80u + sv[1] * 0x00800000u, s23 = sv[2] * 0x80u + sv[3] * 0x00800000u;
 #pragma unroll
       for (int w = 0; w < kWordsV; ++w) {
-        uint32_t rv[4][4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          q4_decode8(wv[e][w], rv[e]);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) rv[e][j] = q4_mul2(rv[e][j], sv[e]);
-        }
+        uint32_t a0[4], a1[4], a2[4], a3[4];
+        q4_decode8((wv[0][w] & 0x0F0F0F0Fu) | (wv[1][w] * 16u & 0xF0F0F0F0u), a0);
+        q4_decode8(((wv[0][w] >> 4) & 0x0F0F0F0Fu) | (wv[1][w] & 0xF0F0F0F0u), a1);
+        q4_decode8((wv[2][w] & 0x0F0F0F0Fu) | (wv[3][w] * 16u & 0xF0F0F0F0u), a2);
+        q4_decode8(((wv[2][w] >> 4) & 0x0F0F0F0Fu) | (wv[3][w] & 0xF0F0F0F0u), a3);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const uint32_t a0 = __byte_perm(rv[0][j], rv[1][j], 0x5410);
-          const uint32_t a1 = __byte_perm(rv[0][j], rv[1][j], 0x7632);
-          const uint32_t a2 = __byte_perm(rv[2][j], rv[3][j], 0x5410);
-          const uint32_t a3 = __byte_perm(rv[2][j], rv[3][j], 0x7632);
+          a0[j] = q4_mul2(a0[j], s01);
+          a1[j] = q4_mul2(a1[j], s01);
+          a2[j] = q4_mul2(a2[j], s23);
+          a3[j] = q4_mul2(a3[j], s23);
 #pragma unroll
-          for (int n = 0; n < NT; ++n) mma_f16(o[n][4 * w + j], a0, a1, a2, a3, pb[n][0], pb[n][1]);
+          for (int n = 0; n < NT; ++n)
+            mma_f16(o[n][4 * w + j], a0[j], a1[j], a2[j], a3[j], pb[n][0], pb[n][1]);
         }
       }
     }
