@@ -114,7 +114,7 @@ struct RowsShared {
   float2 ml[kRowsWarps][16];  // (reference, sum) of each warp's rows
   float4 block_ml[16];        // and of the block's (sum -1: bad page)
   int bad;
-  Q4PlanShared plan;
+  Q4Plan plan;
 };
 
 // Grid (splits * row blocks * Hkv, B).  A block owns 8 NT rows of one kv head
@@ -136,393 +136,374 @@ __global__ void __launch_bounds__(kRowsThreads, 2) tree_attn_q4_rows_kernel(cons
   pdl_trigger();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int qi = lane >> 2, qt = lane & 3;  // (i, t)
-  if (tid == 0) sh.bad = 0;
   pdl_wait();
-  int split, h, rb, b, pieces = p.splits, chunk = p.chunk;
-  if (p.planned) {
-    if (warp == 0) q4_plan_item(p, sh.plan, blockIdx.x);
+  if (p.planned && warp == 0) q4_plan(p, sh.plan);
+  __syncthreads();
+  Q4Seg seg;
+  int g = p.planned ? blockIdx.x * sh.plan.part : 0;
+  while (q4_next(p, sh.plan, g, seg)) {
+    __syncthreads();  // the last segment's shared memory is read
+    if (tid == 0) sh.bad = 0;
     __syncthreads();
-    const Q4Item item = sh.plan.item;
-    if (item.b < 0) return;
-    b = item.b;
-    h = item.h;
-    rb = item.rb;
-    split = item.split;
-    pieces = item.pieces;
-    chunk = item.chunk;
-  } else {
-    split = blockIdx.x % p.splits;
-    const int hr = blockIdx.x / p.splits;
-    h = hr / p.row_blocks;
-    rb = hr % p.row_blocks;
-    b = blockIdx.y;
-    __syncthreads();
-  }
-  const int row0 = rb * 8 * NT;
-  int P, nb;
-  bool bad_len;
-  const bool ok = q4_seq(p, b, P, nb, bad_len);
-  if (bad_len && blockIdx.x == 0 && tid == 0 && p.status)
-    atomicOr(p.status, TSD_STATUS_BAD_LEN);
-  const int rows_valid = ok ? nb * p.g : 0;
-  const int pages = ok ? (P + nb + kPage - 1) / kPage : 0;
-  if (p.cluster) chunk = (pages + p.splits - 1) / p.splits;
-  const int first = split * chunk, last = min(pages, first + chunk);
-  const bool work = row0 < rows_valid && first < last;
-  if (!work && pieces > 1 && !p.cluster) return;
+    const int b = seg.b, h = seg.h, P = seg.P, nb = seg.nb, first = seg.first, last = seg.last;
+    const int row0 = seg.rb * 8 * NT;
+    const int rows_valid = nb * p.g;
+    const bool work = row0 < rows_valid && first < last;
+    if (!work && !seg.direct && !p.cluster) continue;
 
-  float o[NT][kTiles][4];
-  float l[NT][2], trig[NT][2], ref[NT][2], mul[NT][2];
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-#pragma unroll
-    for (int j = 0; j < kTiles; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[n][j][e] = 0.f;
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      l[n][e] = 0.f;
-      trig[n][e] = -INFINITY;  // the score that moves the reference
-      ref[n][e] = 0.f;
-      mul[n][e] = 0.f;
-    }
-  }
-
-  if (work) {
-    // ---- the page stream: each page is one group of the lanes' copies ----
-    const int32_t *trow = p.table + (size_t)b * p.max_blocks;
-    const int mine = last - first > warp ? (last - first - warp + kRowsWarps - 1) / kRowsWarps : 0;
-    const uint32_t ring = smem_addr(smem) + warp * kRowsStages * L::kStage;
-    const uint8_t *ring_p = smem + warp * kRowsStages * L::kStage;
-    int ids = 0;  // lane i: the id of this warp's page 32 * batch + i
-    bool stop = false;
-    auto fetch_ids = [&](int it) {
-      const int j = it + lane;
-      const int id = j < mine ? trow[first + warp + j * kRowsWarps] : 0;
-      const bool bad = id < 0 || id >= p.num_blocks;
-      if (__any_sync(0xffffffffu, bad)) {
-        stop = true;
-        if (lane == 0) sh.bad = 1;
-      }
-      ids = id;
-    };
-    // The lane's c-th copy is chunk 32 c + lane of K's page followed by V's; only
-    // round kMixed (chunks of both) depends on the lane.
-    constexpr int kHalfChunks = L::kChunks / 2, kMixed = kHalfChunks / 32;
-    const uint8_t *k_lane = p.k + 16 * lane, *v_lane = p.v - 16 * kHalfChunks + 16 * lane;
-    const uint8_t *mixed = kMixed * 32 + lane < kHalfChunks ? k_lane : v_lane;
-    auto issue = [&](int it) {
-      const int id = __shfl_sync(0xffffffffu, ids, it & 31);
-      const size_t off = ((size_t)id * p.Hkv + h) * L::kPageBytes;
-      const uint32_t dst = ring + (it % kRowsStages) * L::kStage + 16 * lane;
-#pragma unroll
-      for (int c = 0; c < (L::kChunks + 31) / 32; ++c) {
-        const uint8_t *src = (c < kMixed ? k_lane : c == kMixed ? mixed : v_lane) + off + 512 * c;
-        if ((c + 1) * 32 <= L::kChunks || c * 32 + lane < L::kChunks) cp_async_16(dst + 512 * c, src);
-      }
-    };
-    auto commit = [] { asm volatile("cp.async.commit_group;\n" ::: "memory"); };
-    if (mine > 0) fetch_ids(0);
-    int issued = 0;
-    for (int i = 0; i < kRowsStages; ++i) {  // one group a stage, an empty one past the end
-      if (!stop && issued < mine) issue(issued++);
-      commit();
-    }
-
-    // ---- Q^T as B operands: row i of each 8-row tile ----
-    uint32_t qf[NT][kSteps][2];
+    float o[NT][kTiles][4];
+    float l[NT][2], trig[NT][2], ref[NT][2], mul[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const int r = row0 + 8 * n + qi;
-      uint32_t raw[D / 8];  // D/4 bf16 columns from qt * D/4 on
-      if (r < rows_valid) {
-        const uint4 *src = reinterpret_cast<const uint4 *>(p.q + q4_out_row(p, b, h, r) * D + qt * (D / 4));
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          const uint4 x = src[c];
-          raw[4 * c] = x.x; raw[4 * c + 1] = x.y; raw[4 * c + 2] = x.z; raw[4 * c + 3] = x.w;
-        }
-      } else {
+      for (int j = 0; j < kTiles; ++j)
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) raw[c] = 0u;
-      }
-      float amax = 0.f;
+        for (int e = 0; e < 4; ++e) o[n][j][e] = 0.f;
 #pragma unroll
-      for (int c = 0; c < D / 8; ++c) {
-        amax = fmaxf(amax, fabsf(__uint_as_float(raw[c] << 16)));
-        amax = fmaxf(amax, fabsf(__uint_as_float(raw[c] & 0xFFFF0000u)));
-      }
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-      const int e = q4_exponent(amax);
-      const float up1 = q4_pow2(e / 2), up2 = q4_pow2(e - e / 2);
-#pragma unroll
-      for (int c = 0; c < D / 8; ++c) {
-        const float lo = __uint_as_float(raw[c] << 16) * up1 * up2;
-        const float hi = __uint_as_float(raw[c] & 0xFFFF0000u) * up1 * up2;
-        // columns 4 s + {0, 1} feed b0 of step s, 4 s + {2, 3} its b1
-        qf[n][c / 2][c & 1] = pack_half2(lo, hi);
-      }
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {  // this lane's score columns are rows 2 t and 2 t + 1
-        const int er = __shfl_sync(0xffffffffu, e, (2 * qt + s) * 4);
-        mul[n][s] = p.scale_log2 * q4_pow2(-(er / 2)) * q4_pow2(-(er - er / 2));
+      for (int e = 0; e < 2; ++e) {
+        l[n][e] = 0.f;
+        trig[n][e] = -INFINITY;  // the score that moves the reference
+        ref[n][e] = 0.f;
+        mul[n][e] = 0.f;
       }
     }
 
-    const int key_a = qi ^ ((qi >> 1) & 1);  // A row i; row i + 8 is key_a + 8
-    // V's contraction indices 2t, 2t+1, 2t+8, 2t+9 are A rows 2t, 2t+1, ...
-    const int kv0 = (2 * qt) ^ (qt & 1), kv1 = (2 * qt + 1) ^ (qt & 1);
-
-    for (int it = 0; it < mine && !stop; ++it) {
-      const int st = it % kRowsStages;
-      asm volatile("cp.async.wait_group %0;\n" ::"n"(kRowsStages - 1) : "memory");
-      __syncwarp();
-      const uint8_t *kp = ring_p + st * L::kStage, *vp = kp + L::kPageBytes;
-      const int t0 = (first + warp + it * kRowsWarps) * kPage;  // first key slot
-
-      // S^T
-      float s[NT][4];
-#pragma unroll
-      for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
-      uint32_t wa[kWordsK], wb[kWordsK];
-      lds_words(kp + key_a * Page::kRow + qt * (D / 8), wa);
-      lds_words(kp + (key_a + 8) * Page::kRow + qt * (D / 8), wb);
-      uint32_t sa[2], sb[2];  // scales of the lane's (one or two) groups of 16 columns
-      if constexpr (D == 128) {
-        const uint32_t xa = *reinterpret_cast<const uint16_t *>(kp + Page::kScales + key_a * 8 + 2 * qt);
-        const uint32_t xb =
-            *reinterpret_cast<const uint16_t *>(kp + Page::kScales + (key_a + 8) * 8 + 2 * qt);
-        sa[0] = (xa & 0xFFu) * 0x00800080u;
-        sa[1] = (xa >> 8) * 0x00800080u;
-        sb[0] = (xb & 0xFFu) * 0x00800080u;
-        sb[1] = (xb >> 8) * 0x00800080u;
-      } else {
-        sa[0] = sa[1] = kp[Page::kScales + key_a * 4 + qt] * 0x00800080u;
-        sb[0] = sb[1] = kp[Page::kScales + (key_a + 8) * 4 + qt] * 0x00800080u;
-      }
-#pragma unroll
-      for (int w = 0; w < kWordsK; ++w) {
-        uint32_t ra[4], rb4[4];
-        q4_decode8(wa[w], ra);
-        q4_decode8(wb[w], rb4);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          ra[e] = q4_mul2(ra[e], sa[w / 2]);
-          rb4[e] = q4_mul2(rb4[e], sb[w / 2]);
+    if (work) {
+      // ---- the page stream: each page is one group of the lanes' copies ----
+      const int32_t *trow = p.table + (size_t)b * p.max_blocks;
+      const int mine = last - first > warp ? (last - first - warp + kRowsWarps - 1) / kRowsWarps : 0;
+      const uint32_t ring = smem_addr(smem) + warp * kRowsStages * L::kStage;
+      const uint8_t *ring_p = smem + warp * kRowsStages * L::kStage;
+      int ids = 0;  // lane i: the id of this warp's page 32 * batch + i
+      bool stop = false;
+      auto fetch_ids = [&](int it) {
+        const int j = it + lane;
+        const int id = j < mine ? trow[first + warp + j * kRowsWarps] : 0;
+        const bool bad = id < 0 || id >= p.num_blocks;
+        if (__any_sync(0xffffffffu, bad)) {
+          stop = true;
+          if (lane == 0) sh.bad = 1;
         }
+        ids = id;
+      };
+      // The lane's c-th copy is chunk 32 c + lane of K's page followed by V's; only
+      // round kMixed (chunks of both) depends on the lane.
+      constexpr int kHalfChunks = L::kChunks / 2, kMixed = kHalfChunks / 32;
+      const uint8_t *k_lane = p.k + 16 * lane, *v_lane = p.v - 16 * kHalfChunks + 16 * lane;
+      const uint8_t *mixed = kMixed * 32 + lane < kHalfChunks ? k_lane : v_lane;
+      auto issue = [&](int it) {
+        const int id = __shfl_sync(0xffffffffu, ids, it & 31);
+        const size_t off = ((size_t)id * p.Hkv + h) * L::kPageBytes;
+        const uint32_t dst = ring + (it % kRowsStages) * L::kStage + 16 * lane;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          mma_f16(s[n], ra[0], rb4[0], ra[1], rb4[1], qf[n][2 * w][0], qf[n][2 * w][1]);
-          mma_f16(s[n], ra[2], rb4[2], ra[3], rb4[3], qf[n][2 * w + 1][0], qf[n][2 * w + 1][1]);
+        for (int c = 0; c < (L::kChunks + 31) / 32; ++c) {
+          const uint8_t *src = (c < kMixed ? k_lane : c == kMixed ? mixed : v_lane) + off + 512 * c;
+          if ((c + 1) * 32 <= L::kChunks || c * 32 + lane < L::kChunks) cp_async_16(dst + 512 * c, src);
         }
+      };
+      auto commit = [] { asm volatile("cp.async.commit_group;\n" ::: "memory"); };
+      if (mine > 0) fetch_ids(0);
+      int issued = 0;
+      for (int i = 0; i < kRowsStages; ++i) {  // one group a stage, an empty one past the end
+        if (!stop && issued < mine) issue(issued++);
+        commit();
       }
 
-      // V's codes and scales; slots past the sequence read as zero
-      uint32_t wv[4][kWordsV], sv[4];
-      const int kk[4] = {kv0, kv1, kv0 + 8, kv1 + 8};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        lds_words(vp + kk[e] * Page::kRow + qi * (D / 16), wv[e]);
-        sv[e] = vp[Page::kScales + kk[e] * Page::kScaleRow + qi * (D / 8) / kQ4Group];
-      }
-      // the page is in registers: its stage can be refilled
-      __syncwarp();
-      if (issued < mine) {
-        if ((issued & 31) == 0) fetch_ids(issued);
-        if (!stop) issue(issued++);
-      }
-      commit();
-
-      // softmax: t = s * mul, and what the row may not see is -inf
+      // ---- Q^T as B operands: row i of each 8-row tile ----
+      uint32_t qf[NT][kSteps][2];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        s[n][0] *= mul[n][0];
-        s[n][1] *= mul[n][1];
-        s[n][2] *= mul[n][0];
-        s[n][3] *= mul[n][1];
+        const int r = row0 + 8 * n + qi;
+        uint32_t raw[D / 8];  // D/4 bf16 columns from qt * D/4 on
+        if (r < rows_valid) {
+          const uint4 *src = reinterpret_cast<const uint4 *>(p.q + q4_out_row(p, b, h, r) * D + qt * (D / 4));
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            const uint4 x = src[c];
+            raw[4 * c] = x.x; raw[4 * c + 1] = x.y; raw[4 * c + 2] = x.z; raw[4 * c + 3] = x.w;
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < D / 8; ++c) raw[c] = 0u;
+        }
+        float amax = 0.f;
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          amax = fmaxf(amax, fabsf(__uint_as_float(raw[c] << 16)));
+          amax = fmaxf(amax, fabsf(__uint_as_float(raw[c] & 0xFFFF0000u)));
+        }
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        const int e = q4_exponent(amax);
+        const float up1 = q4_pow2(e / 2), up2 = q4_pow2(e - e / 2);
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          const float lo = __uint_as_float(raw[c] << 16) * up1 * up2;
+          const float hi = __uint_as_float(raw[c] & 0xFFFF0000u) * up1 * up2;
+          // columns 4 s + {0, 1} feed b0 of step s, 4 s + {2, 3} its b1
+          qf[n][c / 2][c & 1] = pack_half2(lo, hi);
+        }
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {  // this lane's score columns are rows 2 t and 2 t + 1
+          const int er = __shfl_sync(0xffffffffu, e, (2 * qt + s) * 4);
+          mul[n][s] = p.scale_log2 * q4_pow2(-(er / 2)) * q4_pow2(-(er - er / 2));
+        }
       }
-      if (t0 + kPage > P) {
+
+      const int key_a = qi ^ ((qi >> 1) & 1);  // A row i; row i + 8 is key_a + 8
+      // V's contraction indices 2t, 2t+1, 2t+8, 2t+9 are A rows 2t, 2t+1, ...
+      const int kv0 = (2 * qt) ^ (qt & 1), kv1 = (2 * qt + 1) ^ (qt & 1);
+
+      for (int it = 0; it < mine && !stop; ++it) {
+        const int st = it % kRowsStages;
+        asm volatile("cp.async.wait_group %0;\n" ::"n"(kRowsStages - 1) : "memory");
+        __syncwarp();
+        const uint8_t *kp = ring_p + st * L::kStage, *vp = kp + L::kPageBytes;
+        const int t0 = (first + warp + it * kRowsWarps) * kPage;  // first key slot
+
+        // S^T
+        float s[NT][4];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
+        for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+        uint32_t wa[kWordsK], wb[kWordsK];
+        lds_words(kp + key_a * Page::kRow + qt * (D / 8), wa);
+        lds_words(kp + (key_a + 8) * Page::kRow + qt * (D / 8), wb);
+        uint32_t sa[2], sb[2];  // scales of the lane's (one or two) groups of 16 columns
+        if constexpr (D == 128) {
+          const uint32_t xa = *reinterpret_cast<const uint16_t *>(kp + Page::kScales + key_a * 8 + 2 * qt);
+          const uint32_t xb =
+              *reinterpret_cast<const uint16_t *>(kp + Page::kScales + (key_a + 8) * 8 + 2 * qt);
+          sa[0] = (xa & 0xFFu) * 0x00800080u;
+          sa[1] = (xa >> 8) * 0x00800080u;
+          sb[0] = (xb & 0xFFu) * 0x00800080u;
+          sb[1] = (xb >> 8) * 0x00800080u;
+        } else {
+          sa[0] = sa[1] = kp[Page::kScales + key_a * 4 + qt] * 0x00800080u;
+          sb[0] = sb[1] = kp[Page::kScales + (key_a + 8) * 4 + qt] * 0x00800080u;
+        }
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int r = row0 + 8 * n + 2 * qt + e;
-            const uint32_t vis = r < rows_valid ? q4_visible(p, b, r / p.g, t0 - P, nb) : 0u;
-            if (!((vis >> key_a) & 1u)) s[n][e] = -INFINITY;
-            if (!((vis >> (key_a + 8)) & 1u)) s[n][2 + e] = -INFINITY;
+        for (int w = 0; w < kWordsK; ++w) {
+          uint32_t ra[4], rb4[4];
+          q4_decode8(wa[w], ra);
+          q4_decode8(wb[w], rb4);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            ra[e] = q4_mul2(ra[e], sa[w / 2]);
+            rb4[e] = q4_mul2(rb4[e], sb[w / 2]);
+          }
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            mma_f16(s[n], ra[0], rb4[0], ra[1], rb4[1], qf[n][2 * w][0], qf[n][2 * w][1]);
+            mma_f16(s[n], ra[2], rb4[2], ra[3], rb4[3], qf[n][2 * w + 1][0], qf[n][2 * w + 1][1]);
           }
         }
-        // V's slots past the sequence read as zero.  Scale bytes that no writer makes
-        // can only be met here, in slots of the tree that were not written: they read
-        // as the largest scale, so that P = 0 really leaves them out.
+
+        // V's codes and scales; slots past the sequence read as zero
+        uint32_t wv[4][kWordsV], sv[4];
+        const int kk[4] = {kv0, kv1, kv0 + 8, kv1 + 8};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sv[e] = t0 + kk[e] >= P + nb ? 0u : min(sv[e], kQ4MaxScale);
-      }
-      bool over = false;
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) over = over || fmaxf(s[n][e], s[n][2 + e]) > trig[n][e];
-      if (__any_sync(0xffffffffu, over)) {
+        for (int e = 0; e < 4; ++e) {
+          lds_words(vp + kk[e] * Page::kRow + qi * (D / 16), wv[e]);
+          sv[e] = vp[Page::kScales + kk[e] * Page::kScaleRow + qi * (D / 8) / kQ4Group];
+        }
+        // the page is in registers: its stage can be refilled
+        __syncwarp();
+        if (issued < mine) {
+          if ((issued & 31) == 0) fetch_ids(issued);
+          if (!stop) issue(issued++);
+        }
+        commit();
+
+        // softmax: t = s * mul, and what the row may not see is -inf
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
+          s[n][0] *= mul[n][0];
+          s[n][1] *= mul[n][1];
+          s[n][2] *= mul[n][0];
+          s[n][3] *= mul[n][1];
+        }
+        if (t0 + kPage > P) {
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float m = fmaxf(s[n][e], s[n][2 + e]);
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-            if (m > trig[n][e]) {  // the same decision in the eight lanes of the row
-              // (for scores whose ulp is coarser than these steps: at the maximum)
-              const float to = m - (m - kOffset) <= kOffset ? m - kOffset : m;
-              const float f = trig[n][e] == -INFINITY ? 0.f : ex2_approx(ref[n][e] - to);
-              trig[n][e] = (m + kSlack) - m <= kSlack ? m + kSlack : m;
-              ref[n][e] = to;
-              l[n][e] *= f;
+          for (int n = 0; n < NT; ++n) {
 #pragma unroll
-              for (int j = 0; j < kTiles; ++j) {
-                o[n][j][e] *= f;
-                o[n][j][2 + e] *= f;
+            for (int e = 0; e < 2; ++e) {
+              const int r = row0 + 8 * n + 2 * qt + e;
+              const uint32_t vis = r < rows_valid ? q4_visible(p, b, r / p.g, t0 - P, nb) : 0u;
+              if (!((vis >> key_a) & 1u)) s[n][e] = -INFINITY;
+              if (!((vis >> (key_a + 8)) & 1u)) s[n][2 + e] = -INFINITY;
+            }
+          }
+          // V's slots past the sequence read as zero.  Scale bytes that no writer makes
+          // can only be met here, in slots of the tree that were not written: they read
+          // as the largest scale, so that P = 0 really leaves them out.
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sv[e] = t0 + kk[e] >= P + nb ? 0u : min(sv[e], kQ4MaxScale);
+        }
+        bool over = false;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) over = over || fmaxf(s[n][e], s[n][2 + e]) > trig[n][e];
+        if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float m = fmaxf(s[n][e], s[n][2 + e]);
+              m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+              m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+              m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+              if (m > trig[n][e]) {  // the same decision in the eight lanes of the row
+                // (for scores whose ulp is coarser than these steps: at the maximum)
+                const float to = m - (m - kOffset) <= kOffset ? m - kOffset : m;
+                const float f = trig[n][e] == -INFINITY ? 0.f : ex2_approx(ref[n][e] - to);
+                trig[n][e] = (m + kSlack) - m <= kSlack ? m + kSlack : m;
+                ref[n][e] = to;
+                l[n][e] *= f;
+#pragma unroll
+                for (int j = 0; j < kTiles; ++j) {
+                  o[n][j][e] *= f;
+                  o[n][j][2 + e] *= f;
+                }
               }
             }
           }
         }
-      }
-      uint32_t pb[NT][2];
+        uint32_t pb[NT][2];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const float p0 = ex2_approx(s[n][0] - ref[n][0]), p1 = ex2_approx(s[n][1] - ref[n][1]);
-        const float p2 = ex2_approx(s[n][2] - ref[n][0]), p3 = ex2_approx(s[n][3] - ref[n][1]);
-        l[n][0] += p0 + p2;
-        l[n][1] += p1 + p3;
-        pb[n][0] = transpose8x8(pack_half2(p0, p1));
-        pb[n][1] = transpose8x8(pack_half2(p2, p3));
-      }
+        for (int n = 0; n < NT; ++n) {
+          const float p0 = ex2_approx(s[n][0] - ref[n][0]), p1 = ex2_approx(s[n][1] - ref[n][1]);
+          const float p2 = ex2_approx(s[n][2] - ref[n][0]), p3 = ex2_approx(s[n][3] - ref[n][1]);
+          l[n][0] += p0 + p2;
+          l[n][1] += p1 + p3;
+          pb[n][0] = transpose8x8(pack_half2(p0, p1));
+          pb[n][1] = transpose8x8(pack_half2(p2, p3));
+        }
 
-      // O^T: M tile j holds columns i D/8 + 2 j (row i) and the next (row i + 8).  An
-      // operand register holds one column of two keys, so the codes of two keys are
-      // interleaved before they are decoded (three operations for eight registers;
-      // after, it takes a byte permutation each, on the pipe that also converts).
-      const uint32_t s01 = sv[0] * 0x80u + sv[1] * 0x00800000u, s23 = sv[2] * 0x80u + sv[3] * 0x00800000u;
+        // O^T: M tile j holds columns i D/8 + 2 j (row i) and the next (row i + 8).  An
+        // operand register holds one column of two keys, so the codes of two keys are
+        // interleaved before they are decoded (three operations for eight registers;
+        // after, it takes a byte permutation each, on the pipe that also converts).
+        const uint32_t s01 = sv[0] * 0x80u + sv[1] * 0x00800000u, s23 = sv[2] * 0x80u + sv[3] * 0x00800000u;
 #pragma unroll
-      for (int w = 0; w < kWordsV; ++w) {
-        uint32_t a0[4], a1[4], a2[4], a3[4];
-        q4_decode8((wv[0][w] & 0x0F0F0F0Fu) | (wv[1][w] * 16u & 0xF0F0F0F0u), a0);
-        q4_decode8(((wv[0][w] >> 4) & 0x0F0F0F0Fu) | (wv[1][w] & 0xF0F0F0F0u), a1);
-        q4_decode8((wv[2][w] & 0x0F0F0F0Fu) | (wv[3][w] * 16u & 0xF0F0F0F0u), a2);
-        q4_decode8(((wv[2][w] >> 4) & 0x0F0F0F0Fu) | (wv[3][w] & 0xF0F0F0F0u), a3);
+        for (int w = 0; w < kWordsV; ++w) {
+          uint32_t a0[4], a1[4], a2[4], a3[4];
+          q4_decode8((wv[0][w] & 0x0F0F0F0Fu) | (wv[1][w] * 16u & 0xF0F0F0F0u), a0);
+          q4_decode8(((wv[0][w] >> 4) & 0x0F0F0F0Fu) | (wv[1][w] & 0xF0F0F0F0u), a1);
+          q4_decode8((wv[2][w] & 0x0F0F0F0Fu) | (wv[3][w] * 16u & 0xF0F0F0F0u), a2);
+          q4_decode8(((wv[2][w] >> 4) & 0x0F0F0F0Fu) | (wv[3][w] & 0xF0F0F0F0u), a3);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          a0[j] = q4_mul2(a0[j], s01);
-          a1[j] = q4_mul2(a1[j], s01);
-          a2[j] = q4_mul2(a2[j], s23);
-          a3[j] = q4_mul2(a3[j], s23);
+          for (int j = 0; j < 4; ++j) {
+            a0[j] = q4_mul2(a0[j], s01);
+            a1[j] = q4_mul2(a1[j], s01);
+            a2[j] = q4_mul2(a2[j], s23);
+            a3[j] = q4_mul2(a3[j], s23);
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
-            mma_f16(o[n][4 * w + j], a0[j], a1[j], a2[j], a3[j], pb[n][0], pb[n][1]);
+            for (int n = 0; n < NT; ++n)
+              mma_f16(o[n][4 * w + j], a0[j], a1[j], a2[j], a3[j], pb[n][0], pb[n][1]);
+          }
         }
       }
-    }
-    cp_async_wait_all();  // before the ring's memory is used again
+      cp_async_wait_all();  // before the ring's memory is used again
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 4);
+          l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 8);
+          l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 16);
+        }
+    }
+
+    // ---- join the warps: every ring is drained, its memory holds their O ----
+    __syncthreads();
+    float *merge = reinterpret_cast<float *>(smem);
+    float *block_o = reinterpret_cast<float *>(smem + L::kMerge);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 4);
-        l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 8);
-        l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 16);
-      }
-  }
-
-  // ---- join the warps: every ring is drained, its memory holds their O ----
-  __syncthreads();
-  float *merge = reinterpret_cast<float *>(smem);
-  float *block_o = reinterpret_cast<float *>(smem + L::kMerge);
+        const int r = 8 * n + 2 * qt + e;
+        if (qi == 0)
+          sh.ml[warp][r] = make_float2(trig[n][e] == -INFINITY && l[n][e] == 0.f ? -INFINITY : ref[n][e], l[n][e]);
+        float *dst = merge + ((size_t)warp * 8 * NT + r) * D + qi * (D / 8);
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int r = 8 * n + 2 * qt + e;
-      if (qi == 0)
-        sh.ml[warp][r] = make_float2(trig[n][e] == -INFINITY && l[n][e] == 0.f ? -INFINITY : ref[n][e], l[n][e]);
-      float *dst = merge + ((size_t)warp * 8 * NT + r) * D + qi * (D / 8);
-#pragma unroll
-      for (int j = 0; j < kTiles; j += 2)
-        *reinterpret_cast<float4 *>(dst + 2 * j) =
-            make_float4(o[n][j][e], o[n][j][2 + e], o[n][j + 1][e], o[n][j + 1][2 + e]);
-    }
-  }
-  __syncthreads();
-  const bool bad = sh.bad != 0;
-  if (tid == 0 && bad && p.status) atomicOr(p.status, TSD_STATUS_BAD_PAGE);
-  constexpr int kVec = D / 4;  // float4 of a row
-  for (int x = tid; x < 8 * NT * kVec; x += kRowsThreads) {
-    const int rl = x / kVec, c = x % kVec, r = row0 + rl;
-    if (r >= p.rows) break;
-    float M = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kRowsWarps; ++w) M = fmaxf(M, sh.ml[w][rl].x);
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    float sum = 0.f;
-    if (M > -INFINITY) {
-#pragma unroll
-      for (int w = 0; w < kRowsWarps; ++w) {
-        const float2 ml = sh.ml[w][rl];
-        const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - M);
-        const float4 v = *reinterpret_cast<const float4 *>(merge + ((size_t)w * 8 * NT + rl) * D + 4 * c);
-        a.x += f * v.x;
-        a.y += f * v.y;
-        a.z += f * v.z;
-        a.w += f * v.w;
-        sum += f * ml.y;
+        for (int j = 0; j < kTiles; j += 2)
+          *reinterpret_cast<float4 *>(dst + 2 * j) =
+              make_float4(o[n][j][e], o[n][j][2 + e], o[n][j + 1][e], o[n][j + 1][2 + e]);
       }
     }
-    if (p.cluster) {
-      *reinterpret_cast<float4 *>(block_o + rl * D + 4 * c) = a;
-      if (c == 0) sh.block_ml[rl] = make_float4(M, bad ? -1.f : sum, 0.f, 0.f);
-    } else if (pieces > 1) {
-      if (r >= rows_valid) continue;
-      const size_t pr =
-          (p.planned ? (size_t)blockIdx.x * p.rows_per_block : q4_part_row(p, b, h, rb, split)) + rl;
-      *reinterpret_cast<float4 *>(p.part_o + pr * D + 4 * c) = a;
-      if (c == 0) p.part_ml[pr] = make_float2(M, bad ? -1.f : sum);
-    } else if (!p.planned || r < rows_valid) {  // (planned: the join writes the others)
-      rows_out(p, q4_out_row(p, b, h, r), D, c, a, M, sum, r >= rows_valid || bad);
+    __syncthreads();
+    const bool bad = sh.bad != 0;
+    if (tid == 0 && bad && p.status) atomicOr(p.status, TSD_STATUS_BAD_PAGE);
+    constexpr int kVec = D / 4;  // float4 of a row
+    for (int x = tid; x < 8 * NT * kVec; x += kRowsThreads) {
+      const int rl = x / kVec, c = x % kVec, r = row0 + rl;
+      if (r >= p.rows) break;
+      float M = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kRowsWarps; ++w) M = fmaxf(M, sh.ml[w][rl].x);
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+      float sum = 0.f;
+      if (M > -INFINITY) {
+#pragma unroll
+        for (int w = 0; w < kRowsWarps; ++w) {
+          const float2 ml = sh.ml[w][rl];
+          const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - M);
+          const float4 v = *reinterpret_cast<const float4 *>(merge + ((size_t)w * 8 * NT + rl) * D + 4 * c);
+          a.x += f * v.x;
+          a.y += f * v.y;
+          a.z += f * v.z;
+          a.w += f * v.w;
+          sum += f * ml.y;
+        }
+      }
+      if (p.cluster) {
+        *reinterpret_cast<float4 *>(block_o + rl * D + 4 * c) = a;
+        if (c == 0) sh.block_ml[rl] = make_float4(M, bad ? -1.f : sum, 0.f, 0.f);
+      } else if (!seg.direct) {
+        if (r >= rows_valid) continue;
+        const size_t pr = seg.part + rl;
+        *reinterpret_cast<float4 *>(p.part_o + pr * D + 4 * c) = a;
+        if (c == 0) p.part_ml[pr] = make_float2(M, bad ? -1.f : sum);
+      } else if (!p.planned || r < rows_valid) {  // (planned: the join writes the others)
+        rows_out(p, q4_out_row(p, b, h, r), D, c, a, M, sum, r >= rows_valid || bad);
+      }
     }
-  }
-  if (!p.cluster) return;
-  // every block of the cluster takes a share of the rows' columns
-  cluster_arrive();
-  cluster_wait();
-  for (int x = split * kRowsThreads + tid; x < 8 * NT * kVec; x += p.splits * kRowsThreads) {
-    const int rl = x / kVec, c = x % kVec, r = row0 + rl;
-    if (r >= p.rows) break;
-    float M = -INFINITY;
-    bool skip = r >= rows_valid;
-    for (int s = 0; s < p.splits; ++s) {
-      const float4 ml = ld_dsmem_f4(smem_addr(&sh.block_ml[rl]), s);
-      M = fmaxf(M, ml.x);
-      skip = skip || ml.y == -1.f;
-    }
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    float sum = 0.f;
-    if (M > -INFINITY) {
+    if (!p.cluster) continue;
+    // every block of the cluster takes a share of the rows' columns
+    const int split = cluster_ctarank();
+    cluster_arrive();
+    cluster_wait();
+    for (int x = split * kRowsThreads + tid; x < 8 * NT * kVec; x += p.splits * kRowsThreads) {
+      const int rl = x / kVec, c = x % kVec, r = row0 + rl;
+      if (r >= p.rows) break;
+      float M = -INFINITY;
+      bool skip = r >= rows_valid;
       for (int s = 0; s < p.splits; ++s) {
         const float4 ml = ld_dsmem_f4(smem_addr(&sh.block_ml[rl]), s);
-        const float4 v = ld_dsmem_f4(smem_addr(block_o + rl * D + 4 * c), s);
-        const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - M);
-        a.x += f * v.x;
-        a.y += f * v.y;
-        a.z += f * v.z;
-        a.w += f * v.w;
-        sum += f * ml.y;
+        M = fmaxf(M, ml.x);
+        skip = skip || ml.y == -1.f;
       }
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+      float sum = 0.f;
+      if (M > -INFINITY) {
+        for (int s = 0; s < p.splits; ++s) {
+          const float4 ml = ld_dsmem_f4(smem_addr(&sh.block_ml[rl]), s);
+          const float4 v = ld_dsmem_f4(smem_addr(block_o + rl * D + 4 * c), s);
+          const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - M);
+          a.x += f * v.x;
+          a.y += f * v.y;
+          a.z += f * v.z;
+          a.w += f * v.w;
+          sum += f * ml.y;
+        }
+      }
+      rows_out(p, q4_out_row(p, b, h, r), D, c, a, M, sum, skip);
     }
-    rows_out(p, q4_out_row(p, b, h, r), D, c, a, M, sum, skip);
+    cluster_arrive();  // no block leaves while another reads its shared memory
+    cluster_wait();
   }
-  cluster_arrive();  // no block leaves while another reads its shared memory
-  cluster_wait();
 }
 
 // One warp per output row: joins the pieces of its key range (fp32), rounds
@@ -543,24 +524,28 @@ __global__ void __launch_bounds__(256) tree_attn_q4_join_kernel(const Q4Attn p) 
   bool bad_len;
   const bool ok = q4_seq(p, b, P, nb, bad_len) && r < nb * p.g;
   const int rb = r / p.rows_per_block;
-  int pieces = 0;
-  size_t base = 0, step = 0;  // partial row of the first piece, and from one piece to the next
+  const int rl = r % p.rows_per_block;
+  int pieces = 0, k0 = 0, part = 0, start = 0;  // planned: the range's first block, unit
   if (ok && p.planned) {
     const int4 plan = p.plan[b];
-    pieces = plan.y;
+    part = plan.w;
+    start = plan.x + (h * plan.z + rb) * plan.y;
+    k0 = start / part;
+    pieces = (start + plan.y - 1) / part - k0 + 1;
     if (pieces == 1) return;  // its block has written it
-    base = (size_t)(plan.x + h * pieces * plan.w + rb) * p.rows_per_block + r % p.rows_per_block;
-    step = (size_t)plan.w * p.rows_per_block;
   } else if (ok) {
     pieces = ((P + nb + kPage - 1) / kPage + p.chunk - 1) / p.chunk;
-    base = q4_part_row(p, b, h, rb, 0) + r % p.rows_per_block;
-    step = p.rows_per_block;
   }
+  const size_t base = p.planned ? 0 : q4_part_row(p, b, h, rb, 0);
+  auto part_row = [&](int s) -> size_t {
+    if (!p.planned) return base + (size_t)s * p.rows_per_block + rl;
+    return ((size_t)(k0 + s) * 2 + (start > (k0 + s) * part ? 1 : 0)) * p.rows_per_block + rl;
+  };
   // lane l holds the (reference, sum) of pieces l, l + 32, ...: at most 64
   float2 ml[2] = {make_float2(-INFINITY, 0.f), make_float2(-INFINITY, 0.f)};
 #pragma unroll
   for (int e = 0; e < 2; ++e)
-    if (lane + 32 * e < pieces) ml[e] = p.part_ml[base + (size_t)(lane + 32 * e) * step];
+    if (lane + 32 * e < pieces) ml[e] = p.part_ml[part_row(lane + 32 * e)];
   const bool bad = __any_sync(0xffffffffu, ml[0].y == -1.f || ml[1].y == -1.f);
   float M = fmaxf(ml[0].x, ml[1].x);
 #pragma unroll
@@ -579,7 +564,7 @@ __global__ void __launch_bounds__(256) tree_attn_q4_join_kernel(const Q4Attn p) 
   for (int c = 0; c < kPer; ++c) a[c] = 0.f;
   for (int s = 0; s < pieces; ++s) {
     const float fs = __shfl_sync(0xffffffffu, s < 32 ? f[0] : f[1], s & 31);
-    const float *src = p.part_o + (base + (size_t)s * step) * D + lane * kPer;
+    const float *src = p.part_o + part_row(s) * D + lane * kPer;
     if constexpr (kPer == 4) {
       const float4 v = *reinterpret_cast<const float4 *>(src);
       a[0] += fs * v.x;
@@ -609,23 +594,20 @@ __global__ void __launch_bounds__(256) tree_attn_q4_join_kernel(const Q4Attn p) 
 // cluster) even where more would fill the GPU.
 constexpr int kClusterPages = 512;
 
-struct Q4Plan {
+struct Q4Shape {
   bool tc;       // the many-row kernel
   bool cluster;  // pieces joined inside a cluster
-  bool planned;  // pieces from the actual lengths
+  bool planned;  // equal parts of all ranges end to end
   int nt, rows_per_block, row_blocks, splits, chunk, blocks;
   size_t plan_bytes, ml_bytes, bytes;  // workspace: the plan, (reference, sum) of the partial rows, the rows
 };
 
 // Rows of a kv head from which the many-row kernel runs.
 constexpr int kTcMinRows = 33;
-// Set-up and end of a block, in units of 8 pages: 4 tiles of the many-row kernel,
-// 8 pages a warp of the few-row kernel (about 6 and 3 us).
-constexpr int kTcFixed = 4, kRowsFixed = 8;
 
 // Host: how a call is cut up.
-Q4Plan q4_plan(int B, int N_max, int Hq, int Hkv, int D, int max_slots) {
-  Q4Plan pl = {};
+Q4Shape q4_shape(int B, int N_max, int Hq, int Hkv, int D, int max_slots) {
+  Q4Shape pl = {};
   const int rows = N_max * (Hq / Hkv);
   const int pages = (max_slots + kPage - 1) / kPage;
   pl.tc = rows >= kTcMinRows;
@@ -636,9 +618,9 @@ Q4Plan q4_plan(int B, int N_max, int Hq, int Hkv, int D, int max_slots) {
   const int slots = (pl.tc ? 1 : 2) * sm_count();
   pl.splits = 1;
   pl.chunk = pages;
-  pl.blocks = (int)base;
   const int units = (pages + kUnitPages - 1) / kUnitPages;
-  if (units <= 2 || base >= 16ll * slots) return pl;  // nothing to gain from cutting
+  // one piece a range: short ranges, or so many that they fill the GPU many times
+  if (units <= 2 || base >= 64ll * slots) return pl;
   if (!pl.tc && pages <= kClusterPages && base < slots) {
     // Short ranges of few blocks: a cluster of 2, 4 or 8 (a workspace and a second
     // launch would cost more than the pieces it could add).
@@ -647,22 +629,25 @@ Q4Plan q4_plan(int B, int N_max, int Hq, int Hkv, int D, int max_slots) {
     while (c < want && c < 8) c *= 2;
     pl.cluster = true;
     pl.splits = c;
-    pl.blocks = (int)base * c;
     return pl;
   }
-  if (B <= kPlanSeqs) {
+  size_t pieces;
+  if (B <= kPlanSeqs && base * units < (1ll << 30)) {
     pl.planned = true;
-    pl.blocks = (int)std::min<int64_t>(base * std::min(units, kPlanPieces), base + 2ll * slots);
+    // as many parts as blocks run at a time; parts are longer where that would cut
+    // a range into more than kPlanPieces
+    pl.blocks = slots;
+    pieces = 2 * (size_t)pl.blocks;
   } else {
     // Batches too large to plan: enough pieces of the longest range for four
     // blocks a slot.
-    const int64_t want = std::min<int64_t>((4ll * slots + base - 1) / base, std::min(units, kPlanPieces));
+    const int64_t want = std::min<int64_t>((4ll * slots + base - 1) / base, std::min(units, 32));
     pl.chunk = (int)((units + want - 1) / want) * kUnitPages;
     pl.splits = (pages + pl.chunk - 1) / pl.chunk;
-    pl.blocks = (int)base * pl.splits;
     if (pl.splits == 1) return pl;
+    pieces = (size_t)base * pl.splits;
   }
-  const size_t part_rows = (size_t)pl.blocks * pl.rows_per_block;
+  const size_t part_rows = pieces * pl.rows_per_block;
   pl.plan_bytes = align_up(kPlanSeqs * sizeof(int4), 256);
   pl.ml_bytes = align_up(part_rows * sizeof(float2), 256);
   pl.bytes = pl.plan_bytes + pl.ml_bytes + part_rows * D * sizeof(float);
@@ -706,7 +691,7 @@ TSD_API size_t tsd_tree_attn_q4_workspace_bytes(int B, int N_max, int Hq, int Hk
                                                 int max_slots) {
   using namespace tsd;
   if (B == 0 || q4_check(B, N_max, Hq, Hkv, D, max_slots) != TSD_OK) return 0;
-  return q4_plan(B, N_max, Hq, Hkv, D, max_slots).bytes;
+  return q4_shape(B, N_max, Hq, Hkv, D, max_slots).bytes;
 }
 
 TSD_API int tsd_tree_attn_fwd_q4(const uint16_t *q, const uint8_t *k_cache, const uint8_t *v_cache,
@@ -724,7 +709,7 @@ TSD_API int tsd_tree_attn_fwd_q4(const uint16_t *q, const uint8_t *k_cache, cons
   if (!q || !k_cache || !v_cache || !block_table || !prefix_len || !out) return TSD_ERR_ARG;
   if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16))
     return TSD_ERR_ARG;
-  const Q4Plan pl = q4_plan(B, N_max, Hq, Hkv, D, max_slots);
+  const Q4Shape pl = q4_shape(B, N_max, Hq, Hkv, D, max_slots);
   if (pl.bytes > 0 && (!workspace || ws_bytes < pl.bytes)) return TSD_ERR_WORKSPACE;
   if (pl.bytes > 0 && !aligned(workspace, 16)) return TSD_ERR_ARG;
   Q4Attn p = {};
@@ -753,11 +738,8 @@ TSD_API int tsd_tree_attn_fwd_q4(const uint16_t *q, const uint8_t *k_cache, cons
   p.chunk = pl.chunk;
   p.cluster = pl.cluster ? pl.splits : 0;
   p.planned = pl.planned;
-  p.slots = (pl.tc ? 1 : 2) * sm_count();
-  p.fixed = pl.tc ? kTcFixed : kRowsFixed;
-  // a partial row goes out and comes back at about 5 GB a ms; a unit takes 1.8 us in
-  // the many-row kernel and 0.4 us in the other
-  p.join_units = (int)(1024.0 * pl.rows_per_block * D * 8 / 5.0e6 / (pl.tc ? 1.8 : 0.4));
+  p.slots = pl.blocks;
+  p.min_units = 2;  // a shorter part would be mostly set-up
   if (pl.bytes) {
     char *ws = reinterpret_cast<char *>(workspace);
     p.plan = reinterpret_cast<int4 *>(ws);

@@ -20,16 +20,14 @@ struct Q4Attn {
   int rows_per_block, row_blocks;  // row_blocks blocks over them
   // Cutting up the key ranges.
   //   cluster > 0: a range's pieces are a thread-block cluster of that size
-  //   planned: pieces from the actual lengths (q4_item), one block each
+  //   planned: all ranges end to end, cut into equal parts, one a block (Q4Plan)
   //   else: pieces of `chunk` pages, `splits` of the longest range
   int cluster, planned;
   int splits, chunk;
-  int slots;       // blocks that run at a time
-  int fixed;       // a block's set-up and end, in units of 8 pages
-  int join_units;  // what a further piece costs in memory traffic, in 1/1024 unit per row block
-  int4 *plan;      // planned: per sequence (first item, pieces, pages of a piece, row blocks)
-  float *part_o;   // [blocks][rows_per_block][D]: unnormalised fp32 outputs
-  float2 *part_ml;  // [blocks][rows_per_block]: (reference in log2 units, sum), sum -1: bad page
+  int slots, min_units;  // planned: blocks that run at a time; least part of one
+  int4 *plan;      // planned: per sequence (first unit, units, row blocks, units of a part)
+  float *part_o;   // [pieces][rows_per_block][D]: unnormalised fp32 outputs
+  float2 *part_ml;  // [pieces][rows_per_block]: (reference in log2 units, sum), sum -1: bad page
   uint16_t *out;
   float *lse;
   int32_t *status;
@@ -83,102 +81,125 @@ __device__ __forceinline__ size_t q4_out_row(const Q4Attn &p, int b, int h, int 
   return ((size_t)b * p.N_max + r / p.g) * p.Hq + h * p.g + r % p.g;
 }
 
-// First partial row of a uniformly cut piece (a planned one's: its block's).
+// First partial row of a uniformly cut piece.
 __device__ __forceinline__ size_t q4_part_row(const Q4Attn &p, int b, int h, int rb, int split) {
   return ((((size_t)b * p.Hkv + h) * p.row_blocks + rb) * p.splits + split) * p.rows_per_block;
 }
 
-// A block's piece of work.
-struct Q4Item {
-  int b, h, rb;       // sequence, kv head, row block; b = -1: none
-  int pieces, split;  // pieces of its key range, and which
-  int chunk;          // pages of a piece
+// The plan of a batch of up to 64 sequences.  Every (sequence, kv head, row block)
+// has a key range of t units of 8 pages (128 keys).  The ranges are laid end to
+// end and cut into equal parts, as many as blocks run at a time, so every block
+// has the same work whatever the lengths; a block takes the segments of its part
+// in turn, and only a range that a cut goes through leaves partial rows.  Every
+// block computes the plan for itself (about a microsecond), which spares a kernel
+// before this one.
+constexpr int kPlanSeqs = 64;
+constexpr int kPlanPieces = 64;  // pieces of one range at most
+constexpr int kUnitPages = 8;
+
+struct Q4Plan {
+  int start[kPlanSeqs + 1];  // first unit of each sequence
+  int units[kPlanSeqs], rbs[kPlanSeqs], P[kPlanSeqs], nb[kPlanSeqs];
+  int part;  // units of a block
 };
 
-constexpr int kPlanSeqs = 64;    // sequences of a planned batch
-constexpr int kPlanPieces = 32;  // pieces of one range at most
-constexpr int kUnitPages = 8;    // ranges are cut at multiples of 8 pages
-
-struct Q4PlanShared {
-  int units[kPlanSeqs], mult[kPlanSeqs];  // of each sequence: key range, blocks per piece
-  Q4Item item;
+// One segment: pages [first, last) of a key range.
+struct Q4Seg {
+  int b, h, rb, P, nb;
+  int first, last;
+  bool direct;   // the whole range: rows go straight to the output
+  size_t part;   // else the first partial row
 };
 
-// The batch's plan and this block's item of it, by warp 0; the others learn it
-// after the block's next barrier.  Candidate i cuts the longest range into i + 1
-// pieces, of C units, and every other one into pieces of at most C; the plan is
-// the candidate of least estimated time, with a = T / items the mean piece,
-//   max(ceil(items / slots) (a + fixed), items / slots (a + fixed) + longest - a)
-// plus the further pieces' traffic: whole waves for equal ranges, the last
-// piece's excess for ragged ones.  Every block computes it (B <= 64: about a
-// microsecond), which spares a kernel of its own before this one.
-__device__ __forceinline__ void q4_plan_item(const Q4Attn &p, Q4PlanShared &sh, int k) {
+// The plan, by warp 0; the block's other threads see it after its next barrier.
+__device__ __forceinline__ void q4_plan(const Q4Attn &p, Q4Plan &sh) {
   const int lane = threadIdx.x & 31;
-  int units[2], mult[2], longest = 0;
+  int cnt[2], longest = 0;
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
     const int b = 2 * lane + e;
-    int P, nb;
-    bool bad;
+    int P = 0, nb = 0;
+    bool bad = false;
     const bool ok = b < p.B && q4_seq(p, b, P, nb, bad);
-    units[e] = ok ? (P + nb + kUnitPages * kPage - 1) / (kUnitPages * kPage) : 0;
-    mult[e] = ok ? p.Hkv * ((nb * p.g + p.rows_per_block - 1) / p.rows_per_block) : 0;
-    sh.units[b] = units[e];
-    sh.mult[b] = mult[e];
-    longest = max(longest, units[e]);
-    if (k == 0 && b < p.B && !ok && bad && p.status) atomicOr(p.status, TSD_STATUS_BAD_LEN);
+    const int t = ok ? (P + nb + kUnitPages * kPage - 1) / (kUnitPages * kPage) : 0;
+    const int rbs = ok ? (nb * p.g + p.rows_per_block - 1) / p.rows_per_block : 0;
+    sh.units[b] = t;
+    sh.rbs[b] = rbs;
+    sh.P[b] = P;
+    sh.nb[b] = nb;
+    cnt[e] = t * rbs * p.Hkv;
+    longest = max(longest, t);
+    if (blockIdx.x == 0 && bad && p.status) atomicOr(p.status, TSD_STATUS_BAD_LEN);
   }
   longest = __reduce_max_sync(0xffffffffu, longest);
-  __syncwarp();
-  const int C = max(1, (longest + lane) / (lane + 1));  // this lane's candidate
-  const float inv = 1.f / (float)C;
-  int items = 0, extra = 0, total = 0;
-  for (int b = 0; b < p.B; ++b) {
-    const int t = sh.units[b], m = sh.mult[b], x = t + C - 1;
-    int n = (int)((float)x * inv);
-    n -= n * C > x ? 1 : 0;
-    n += (n + 1) * C <= x ? 1 : 0;
-    items += n * m;
-    extra += n > 1 ? n * m : 0;
-    total += t * m;
-  }
-  float est = 3.0e38f;
-  if (items > 0 && (items <= (int)gridDim.x || lane == 0)) {
-    const float mean = (float)total / (float)items, x = (float)items / (float)p.slots;
-    est = fmaxf(ceilf(x) * (mean + p.fixed), x * (mean + p.fixed) + (float)C - mean);
-    est += (float)extra * (float)p.join_units * (1.f / 1024.f);
-  }
-  const uint32_t key = __float_as_uint(est);  // (positive floats order as integers)
-  const uint32_t least = __reduce_min_sync(0xffffffffu, key);
-  const int who = __ffs(__ballot_sync(0xffffffffu, key == least)) - 1;
-  const int best = __shfl_sync(0xffffffffu, C, who);
-  // number the items: this lane's two sequences
-  int n[2], cnt[2];
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    n[e] = (units[e] + best - 1) / best;
-    cnt[e] = n[e] * mult[e];
-  }
   int incl = cnt[0] + cnt[1];
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
     const int y = __shfl_up_sync(0xffffffffu, incl, off);
     if (lane >= off) incl += y;
   }
-  if (lane == 31 && k >= incl) sh.item.b = -1;
-  int first = incl - cnt[0] - cnt[1];
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const int b = 2 * lane + e;
-    const int rbs = mult[e] / p.Hkv;
-    const int chunk = n[e] > 0 ? (units[e] + n[e] - 1) / n[e] * kUnitPages : 0;
-    if (k >= first && k < first + cnt[e]) {
-      const int x = (k - first) / rbs;  // row blocks of a piece next to each other: they share its pages
-      sh.item = Q4Item{b, x / n[e], (k - first) % rbs, n[e], x % n[e], chunk};
-    }
-    if (k == 0 && b < p.B) p.plan[b] = make_int4(first, n[e], chunk, rbs);
-    first += cnt[e];
+  const int total = __shfl_sync(0xffffffffu, incl, 31);
+  const int part = max(max((total + p.slots - 1) / p.slots, p.min_units),
+                       (longest + kPlanPieces - 3) / (kPlanPieces - 2));
+  const int first = incl - cnt[0] - cnt[1];
+  sh.start[2 * lane] = first;
+  sh.start[2 * lane + 1] = first + cnt[0];
+  if (lane == 31) {
+    sh.start[kPlanSeqs] = total;
+    sh.part = part;
   }
+  if (blockIdx.x == 0) {  // for the join
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int b = 2 * lane + e;
+      if (b < p.B) p.plan[b] = make_int4(first + (e ? cnt[0] : 0), sh.units[b], sh.rbs[b], part);
+    }
+  }
+}
+
+// The next segment of this block; g counts its units (start at blockIdx.x *
+// part when planned, else at 0).  False: there is none.
+__device__ __forceinline__ bool q4_next(const Q4Attn &p, const Q4Plan &sh, int &g, Q4Seg &s) {
+  if (p.planned) {
+    const int g0 = blockIdx.x * sh.part, end = min(sh.start[kPlanSeqs], g0 + sh.part);
+    if (g >= end) return false;
+    int b = 0;  // the last sequence that starts at or before g and is not empty
+#pragma unroll
+    for (int step = kPlanSeqs / 2; step; step >>= 1)
+      if (sh.start[b + step] <= g) b += step;
+    const int t = sh.units[b], local = g - sh.start[b];
+    const int range = local / t, off = local - range * t, len = min(t - off, end - g);
+    s.b = b;
+    s.h = range / sh.rbs[b];
+    s.rb = range - s.h * sh.rbs[b];
+    s.P = sh.P[b];
+    s.nb = sh.nb[b];
+    s.first = off * kUnitPages;
+    s.last = min((s.P + s.nb + kPage - 1) / kPage, (off + len) * kUnitPages);
+    s.direct = len == t;
+    // a cut leaves a block at most one range that started before it and one that
+    // goes on after it
+    s.part = ((size_t)blockIdx.x * 2 + (g - off > g0 ? 1 : 0)) * p.rows_per_block;
+    g += len;
+    return true;
+  }
+  if (g != 0) return false;
+  g = 1;
+  const int split = blockIdx.x % p.splits, hr = blockIdx.x / p.splits;
+  s.b = blockIdx.y;
+  s.h = hr / p.row_blocks;
+  s.rb = hr % p.row_blocks;
+  bool bad;
+  const bool ok = q4_seq(p, s.b, s.P, s.nb, bad);
+  if (bad && blockIdx.x == 0 && threadIdx.x == 0 && p.status) atomicOr(p.status, TSD_STATUS_BAD_LEN);
+  if (!ok) s.nb = 0;  // (no valid row)
+  const int pages = ok ? (s.P + s.nb + kPage - 1) / kPage : 0;
+  const int chunk = p.cluster ? (pages + p.splits - 1) / p.splits : p.chunk;
+  s.first = split * chunk;
+  s.last = min(pages, s.first + chunk);
+  s.direct = p.splits == 1;
+  s.part = p.cluster ? 0 : q4_part_row(p, s.b, s.h, s.rb, split);
+  return true;
 }
 
 // The many-row kernel (attention_q4_tc.cu); blocks: its grid when planned.

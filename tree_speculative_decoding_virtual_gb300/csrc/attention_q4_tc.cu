@@ -76,17 +76,29 @@ struct TcLayout {
   }
 };
 
+constexpr int kTcBarriers = 4 * kPackMost + 16;
+
+struct TcSeg {
+  Q4Seg s;
+  int n;     // its key tiles
+  bool two;  // two row tiles (each with every key tile), or one row tile whose key
+             // tiles alternate between the chains
+  bool more;
+};
+
 struct TcShared {
   uint64_t pk_full[2][kPackMost], pk_empty[2][kPackMost];  // K, V
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
-  uint64_t s_full[2], p_full[2], o_final[2], q_full, drain;
+  uint64_t s_full[2], p_full[2], o_final[2], q_full, drain;  // (kTcBarriers in all)
   float2 ml[kBM];           // chain 1's (reference, sum) when it shares chain 0's rows
   float half[2][2][kBM];    // by chain, thread of the row, row: exchange between the two
   uint8_t asks[2][2][kBM];  // likewise
   int stop[2][2];           // by chain and tile parity: a wait ran out
   uint32_t tmem_base;
   int abort, bad;
-  Q4PlanShared plan;
+  int g;       // units of the block's part that were taken (q4_next)
+  TcSeg seg;   // the segment in work; here, not in registers, which the roles lack
+  Q4Plan plan;
 };
 
 __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn_major) {
@@ -94,10 +106,22 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn_maj
   return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
+// mbar_wait with its polling loop kept a loop: unrolled at every wait, it made two
+// thirds of the kernel's code, and instruction fetch bound the blocks.
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
+  using namespace sm100;
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+#pragma unroll 1
+  for (int i = 1;; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 63) == 0 && global_timer_ns() - t0 > limit_ns) return false;
+  }
+}
 __device__ __forceinline__ bool tc_wait(uint64_t &bar, uint32_t parity, uint64_t limit, volatile int *abort) {
   using namespace sm100;
   if (*abort) return false;
-  if (mbar_wait(smem_addr(&bar), parity, limit)) return true;
+  if (wait_phase(smem_addr(&bar), parity, limit)) return true;
   *abort = 1;
   return false;
 }
@@ -163,7 +187,57 @@ __device__ __forceinline__ uint32_t mask_scores(const Q4Attn &p, int b, int node
   return vis;
 }
 
-// A block an item of the plan, or grid (splits * row blocks * Hkv, B); blocks of
+__device__ __forceinline__ void mbar_inval(uint32_t bar) {
+  asm volatile("mbarrier.inval.shared::cta.b64 [%0];\n" ::"r"(bar) : "memory");
+}
+
+// The block's next segment, and its barriers; every thread of the block calls it,
+// after everything of the segment before has completed.  `fresh`: there was none.
+__device__ __forceinline__ bool tc_segment(const Q4Attn &p, TcShared &sh, bool fresh, int tid) {
+  using namespace sm100;
+  tc_fence_before();
+  __syncthreads();
+  if (tid == 0) {
+    if (!fresh) {
+      if (sh.bad && p.status) atomicOr(p.status, TSD_STATUS_BAD_PAGE);
+      sh.bad = 0;
+    }
+    TcSeg sg;
+    int g = sh.g;
+    sg.more = q4_next(p, sh.plan, g, sg.s);
+    sh.g = g;
+    if (sg.more) {
+      sg.n = (sg.s.last - sg.s.first + kTilePages - 1) / kTilePages;
+      sg.two = sg.s.rb * p.rows_per_block + kBM < sg.s.nb * p.g && p.rows_per_block > kBM;
+      // the barriers lie one after the other, from pk_full to drain
+      uint64_t *all = &sh.pk_full[0][0];
+      if (!fresh)
+        for (int i = 0; i < kTcBarriers; ++i) mbar_inval(smem_addr(all + i));
+      for (int i = 0; i < 2 * kPackMost; ++i) {
+        mbar_init(smem_addr(&sh.pk_full[i / kPackMost][i % kPackMost]), 1);
+        mbar_init(smem_addr(&sh.pk_empty[i / kPackMost][i % kPackMost]), 2);
+      }
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(smem_addr(&sh.k_full[i]), 2);
+        mbar_init(smem_addr(&sh.k_empty[i]), 1);
+        mbar_init(smem_addr(&sh.v_full[i]), 2);
+        mbar_init(smem_addr(&sh.v_empty[i]), 1);
+        mbar_init(smem_addr(&sh.s_full[i]), 1);
+        mbar_init(smem_addr(&sh.p_full[i]), sg.two && i == 1 ? 8 : 9);  // softmax warps, hand-over
+        mbar_init(smem_addr(&sh.o_final[i]), 1);
+      }
+      mbar_init(smem_addr(&sh.q_full), 16);
+      mbar_init(smem_addr(&sh.drain), 1);
+      fence_mbar_init();
+    }
+    sh.seg = sg;
+  }
+  __syncthreads();
+  tc_fence_after();
+  return sh.seg.more;
+}
+
+// A block a part of the plan, or grid (splits * row blocks * Hkv, B); blocks of
 // 256 rows, or of 128 where a kv head has no more.
 template <int D>
 __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4Attn p) {
@@ -181,62 +255,34 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4
   const uint64_t lim = p.wait_limit_ns;
 
   pdl_wait();
-  int split, h, rb, b, pieces = p.splits, chunk = p.chunk;
-  if (p.planned) {
-    if (warp == 0) q4_plan_item(p, sh.plan, blockIdx.x);
-    __syncthreads();
-    const Q4Item item = sh.plan.item;
-    if (item.b < 0) return;
-    b = item.b;
-    h = item.h;
-    rb = item.rb;
-    split = item.split;
-    pieces = item.pieces;
-    chunk = item.chunk;
-  } else {
-    split = blockIdx.x % p.splits;
-    const int hr = blockIdx.x / p.splits;
-    h = hr / p.row_blocks;
-    rb = hr % p.row_blocks;
-    b = blockIdx.y;
-  }
-  int P, nb;
-  bool bad_len;
-  const bool ok_seq = q4_seq(p, b, P, nb, bad_len);
-  if (bad_len && blockIdx.x == 0 && tid == 0 && p.status) atomicOr(p.status, TSD_STATUS_BAD_LEN);
-  const int rows_valid = ok_seq ? nb * p.g : 0;
-  const int pages = ok_seq ? (P + nb + kPage - 1) / kPage : 0;
-  const int first = split * chunk, last = min(pages, first + chunk);
-  const int row0 = rb * p.rows_per_block;
-  const bool work = row0 < rows_valid && first < last;
-  if (!work && pieces > 1) return;
-  const int n = work ? (last - first + kTilePages - 1) / kTilePages : 0;  // key tiles
-  // two row tiles (each with every key tile), or one row tile whose key tiles
-  // alternate between the chains
-  const bool two = row0 + kBM < rows_valid && p.rows_per_block > kBM;
-  const int chains = two ? 2 : (n > 1 ? 2 : 1);
-  const int ring = two ? kPackSlots : kPackMost;
-
+  if (p.planned && warp == 0) q4_plan(p, sh.plan);
   if (tid == 0) {
-    for (int i = 0; i < 2 * kPackMost; ++i) {
-      mbar_init(smem_addr(&sh.pk_full[i / kPackMost][i % kPackMost]), 1);
-      mbar_init(smem_addr(&sh.pk_empty[i / kPackMost][i % kPackMost]), 2);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_addr(&sh.k_full[i]), 2);
-      mbar_init(smem_addr(&sh.k_empty[i]), 1);
-      mbar_init(smem_addr(&sh.v_full[i]), 2);
-      mbar_init(smem_addr(&sh.v_empty[i]), 1);
-      mbar_init(smem_addr(&sh.s_full[i]), 1);
-      mbar_init(smem_addr(&sh.p_full[i]), two && i == 1 ? 8 : 9);  // softmax warps, hand-over
-      mbar_init(smem_addr(&sh.o_final[i]), 1);
-    }
-    mbar_init(smem_addr(&sh.q_full), 16);
-    mbar_init(smem_addr(&sh.drain), 1);
     sh.abort = 0;
     sh.bad = 0;
     for (int i = 0; i < 4; ++i) sh.stop[i >> 1][i & 1] = 0;
-    fence_mbar_init();
+  }
+  __syncthreads();
+  {  // a block without work leaves before the set-up
+    Q4Seg seg;
+    int g = p.planned ? blockIdx.x * sh.plan.part : 0;
+    if (tid == 0) sh.g = g;
+    if (!q4_next(p, sh.plan, g, seg)) return;
+    if (!p.planned) {
+      const bool work = seg.rb * p.rows_per_block < seg.nb * p.g && seg.first < seg.last;
+      // rows that no chain computes, when they go straight to the output (planned:
+      // the join writes them)
+      if (seg.direct) {
+        const int row0 = seg.rb * p.rows_per_block, end = min(p.rows, row0 + p.rows_per_block);
+        for (int x = tid; x < (end - row0) * (D / 8); x += kTcThreads) {
+          const int r = row0 + x / (D / 8);
+          if (work && r < seg.nb * p.g) continue;
+          const size_t orow = q4_out_row(p, seg.b, seg.h, r);
+          reinterpret_cast<uint4 *>(p.out + orow * D)[x % (D / 8)] = make_uint4(0u, 0u, 0u, 0u);
+          if (x % (D / 8) == 0 && p.lse) p.lse[orow] = -INFINITY;
+        }
+      }
+      if (!work) return;
+    }
   }
   if (warp == 1) tmem_alloc(smem_addr(&sh.tmem_base), kTmemCols);
   tc_fence_before();
@@ -244,23 +290,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4
   tc_fence_after();
   const uint32_t tmem = sh.tmem_base;
 
-  // rows that no chain computes, when they go straight to the output
-  if (pieces == 1 && !p.planned) {  // (planned: the join writes them)
-    const int end = min(p.rows, row0 + p.rows_per_block);
-    for (int x = tid; x < (end - row0) * (D / 8); x += kTcThreads) {
-      const int r = row0 + x / (D / 8);
-      if (work && r < rows_valid) continue;
-      const size_t orow = q4_out_row(p, b, h, r);
-      reinterpret_cast<uint4 *>(p.out + orow * D)[x % (D / 8)] = make_uint4(0u, 0u, 0u, 0u);
-      if (x % (D / 8) == 0 && p.lse) p.lse[orow] = -INFINITY;
-    }
-  }
-
-  // The roles.  What follows them is compiled for all of them, so it has to fit
-  // the smallest share of registers: nothing but the teardown.
+  // The roles; each takes the block's segments in turn, all of them the same ones.
+  // What follows the roles is compiled for all of them, so it has to fit the
+  // smallest share of registers: nothing but the teardown.
+  const volatile TcSeg &sg = sh.seg;
   if (warp < 4) {
     regs_down<kRegsIssue>();
-    if (work && (warp == 0 || warp == 3)) {
+    for (bool fresh = true; tc_segment(p, sh, fresh, tid); fresh = false) {
+    const int b = sg.s.b, h = sg.s.h, first = sg.s.first, last = sg.s.last, n = sg.n;
+    const bool two = sg.two;
+    const int chains = two || n > 1 ? 2 : 1, ring = two ? kPackSlots : kPackMost;
+    if (warp == 0 || warp == 3) {
       // ---- loaders: warp 0 K, warp 3 V, half a tile at a time; lane l < 4 copies the
       // item's page l.  (A warp needs some 60 ns to issue a copy: one warp for K and V
       // bound the blocks of one row tile.)  K and V have rings of their own, so that
@@ -302,8 +342,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4
       }
       // no copy is in flight when the block exits
       for (int m = max(0, issued - ring); m < issued; ++m)
-        mbar_wait(smem_addr(&sh.pk_full[v][m % ring]), (m / ring) & 1, kTcDrainNs);
-    } else if (work && warp == 1) {
+        wait_phase(smem_addr(&sh.pk_full[v][m % ring]), (m / ring) & 1, kTcDrainNs);
+    } else if (warp == 1) {
       // ---- MMA issue ----
       if (lane == 0) {
         constexpr uint32_t idS = idesc_f16_f32(kBM, kBN, false);
@@ -343,7 +383,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4
             const int st = j & 1;
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              ok = ok && mbar_wait(smem_addr(&sh.p_full[c]), j & 1, lim);
+              ok = ok && wait_phase(smem_addr(&sh.p_full[c]), j & 1, lim);
               if (!ok) break;
               issue_pv(c, st, j > 0, j == n - 1);
               if (j + 1 < n) issue_s(c, c, st ^ 1);
@@ -352,7 +392,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4
         } else {
           for (int j = 0; ok && j < n; ++j) {
             const int c = j & 1;
-            ok = mbar_wait(smem_addr(&sh.p_full[c]), (j >> 1) & 1, lim);
+            ok = wait_phase(smem_addr(&sh.p_full[c]), (j >> 1) & 1, lim);
             if (!ok) break;
             issue_pv(c, c, j > 1, j + 2 >= n);
             if (j + 2 < n) issue_s(c, 0, c);
@@ -360,10 +400,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4
         }
         if (!ok) *abort = 1;
         umma_commit(smem_addr(&sh.drain));
-        mbar_wait(smem_addr(&sh.drain), 0, kTcDrainNs);
+        wait_phase(smem_addr(&sh.drain), 0, kTcDrainNs);
       }
       __syncwarp();
-    } else if (work && warp == 2) {
+    } else if (warp == 2) {
       // ---- hand-over: phase j of p_full also means that V_j and the K tile of the
       // S behind P_j V_j are in shared memory.  (An arrival counts toward the phase
       // that is open: the one before has to be complete.) ----
@@ -385,8 +425,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4
       }
       __syncwarp();
     }
+    }
   } else if (warp < 8) {
     regs_down<kRegsDecode>();
+    for (bool fresh = true; tc_segment(p, sh, fresh, tid); fresh = false) {
+    const int n = sg.n, ring = sg.two ? kPackSlots : kPackMost;
     // ---- decode: warps 4 and 5 K tiles, 6 and 7 V tiles (two tiles at a time hide
     // each other's waits and fences: 128-row blocks were bound by four warps on
     // one tile); a lane takes one group (16 columns) of a key at a time ----
@@ -443,17 +486,21 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4
         mbar_arrive(smem_addr(&sh.pk_empty[v][slot]));
       }
     }
+    }
   } else {
     regs_up<kRegsSoftmax>();
+    for (bool fresh = true; tc_segment(p, sh, fresh, tid); fresh = false) {
+    const int n = sg.n;
+    const bool two = sg.two;
+    const int chains = two || n > 1 ? 2 : 1;
+    // (what the tile loop does not need is read again from the segment)
+    auto row_of = [&](int rl, int rt) { return sg.s.rb * p.rows_per_block + rt * kBM + rl; };
     // ---- softmax ----
     const int c = (warp - 8) >> 3;             // chain
     const int half = ((warp - 8) >> 2) & 1;    // which 64 keys of a tile, and columns of O
     const int rt = two ? c : 0;                // its row tile
     const int quarter = warp & 3;
     const int rl = quarter * 32 + lane;        // row within the tile
-    const int row = row0 + rt * kBM + rl;
-    const bool rvalid = row < rows_valid;
-    const int node = rvalid ? row / p.g : 0;
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
     const uint32_t tS = tmem + c * kTmemChain + lane_off, tO = tS + kTmemO;
 
@@ -461,8 +508,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4
     float mul;
     {
       uint32_t q[D / 4];
-      const uint4 *src =
-          reinterpret_cast<const uint4 *>(p.q + q4_out_row(p, b, h, rvalid ? row : 0) * D + half * (D / 2));
+      const int row = row_of(rl, rt);
+      const bool rvalid = row < sg.s.nb * p.g;
+      const uint4 *src = reinterpret_cast<const uint4 *>(
+          p.q + q4_out_row(p, sg.s.b, sg.s.h, rvalid ? row : 0) * D + half * (D / 2));
       float amax = 0.f;
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) {
@@ -507,9 +556,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4
     }
 
     float ref = 0.f, l = 0.f;  // the row's reference, this thread's part of its sum
-    bool unset = true, ok = work && c < chains;
+    bool unset = true, ok = c < chains;
     const unsigned long long mul2 = f2_pack(mul, mul);
     int u = 0;  // this chain's tiles
+    // this thread's first key slot in tile j is 128 j + slot0; the tile reaches the
+    // tree where it passes tree_from
+    const int slot0 = sg.s.first * kPage + half * 64, tree_from = sg.s.P - 64 - slot0;
+    auto mask = [&](int j, int k, uint32_t (&s)[32]) {
+      const int row = row_of(rl, rt);
+      const bool rvalid = row < sg.s.nb * p.g;
+      return mask_scores(p, sg.s.b, rvalid ? row / p.g : 0, rvalid, j * kBN + slot0 + k * 32 - sg.s.P, sg.s.nb, s);
+    };
     for (int j = two ? 0 : c; ok && j < n; j += two ? 1 : 2, ++u) {
       // one warp looks at the barrier, the others wait for it without polling
       bool got = true;
@@ -527,8 +584,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4
         const int jv = two ? j - 1 : j - 2;
         if (jv >= 0) mbar_arrive(smem_addr(&sh.v_empty[jv & 1]));
       }
-      const int t0 = (first + j * kTilePages) * kPage + half * 64;  // this thread's first key slot
-      const bool tail = t0 + 64 > P;
+      const bool tail = j * kBN > tree_from;
       const unsigned long long ref2 = f2_pack(-ref, -ref);
       unsigned long long acc0 = 0ull, acc1 = 0ull;
       uint32_t pk[32], seen = 0u;
@@ -541,7 +597,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4
         tmem_wait_ld(x[1]);
         if (tail) {
 #pragma unroll
-          for (int k = 0; k < 2; ++k) seen |= mask_scores(p, b, node, rvalid, t0 + k * 32 - P, nb, x[k]);
+          for (int k = 0; k < 2; ++k) seen |= mask(j, k, x[k]);
         }
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
@@ -576,7 +632,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4
           uint32_t s[32];
           tmem_ld32(tS + half * 64 + k * 32, s);
           tmem_wait_ld(s);
-          if (tail) mask_scores(p, b, node, rvalid, t0 + k * 32 - P, nb, s);
+          if (tail) mask(j, k, s);
 #pragma unroll
           for (int i = 0; i < 32; ++i) m = fmaxf(m, __fmul_rn(__uint_as_float(s[i]), mul));
         }
@@ -603,7 +659,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4
             uint32_t s[32];
             tmem_ld32(tS + half * 64 + k * 32, s);
             tmem_wait_ld(s);
-            if (tail) mask_scores(p, b, node, rvalid, t0 + k * 32 - P, nb, s);
+            if (tail) mask(j, k, s);
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               const float e0 = ex2_approx(__fsub_rn(__fmul_rn(__uint_as_float(s[2 * i]), mul), ref));
@@ -676,12 +732,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4
         M = top;
       }
       const bool bad = sh.bad != 0;
-      const bool direct = pieces == 1;
+      const bool direct = sg.s.direct;
       const bool empty = bad || l == 0.f;
       const float inv = empty ? 0.f : 1.f / l;
-      const size_t pr =
-          (p.planned ? (size_t)blockIdx.x * p.rows_per_block : q4_part_row(p, b, h, rb, split)) + row - row0;
-      const size_t orow = rvalid ? q4_out_row(p, b, h, row) : 0;
+      const int row = row_of(rl, rt);
+      const bool rvalid = row < sg.s.nb * p.g;
+      const size_t pr = sg.s.part + rt * kBM + rl;
+      const size_t orow = rvalid ? q4_out_row(p, sg.s.b, sg.s.h, row) : 0;
 #pragma unroll 1
       for (int q = q0; ok && q < q0 + D / 64; ++q) {
         uint32_t o[32];
@@ -719,15 +776,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4
           p.lse[orow] = empty ? -INFINITY : (M + log2f(l)) * kTcLn2;
       }
     }
+    }
   }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
+  // (the last tc_segment ended with a barrier)
   if (warp == 1) tmem_dealloc(tmem, kTmemCols);
-  if (tid == 0 && p.status) {
-    if (sh.bad) atomicOr(p.status, TSD_STATUS_BAD_PAGE);
-    if (sh.abort) atomicOr(p.status, TSD_STATUS_TIMEOUT);
-  }
+  if (tid == 0 && p.status && sh.abort) atomicOr(p.status, TSD_STATUS_TIMEOUT);
 }
 
 }  // namespace
