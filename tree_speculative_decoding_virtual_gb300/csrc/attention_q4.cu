@@ -464,7 +464,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2) tree_attn_q4_rows_kernel(cons
       } else if (!seg.direct) {
         if (r >= rows_valid) continue;
         const size_t pr = seg.part + rl;
-        *reinterpret_cast<float4 *>(p.part_o + pr * D + 4 * c) = a;
+        *reinterpret_cast<float4 *>(p.part_o + pr * D + 4 * (c ^ (rl & 7))) = a;  // (see the join)
         if (c == 0) p.part_ml[pr] = make_float2(M, bad ? -1.f : sum);
       } else if (!p.planned || r < rows_valid) {  // (planned: the join writes the others)
         rows_out(p, q4_out_row(p, b, h, r), D, c, a, M, sum, r >= rows_valid || bad);
@@ -564,7 +564,9 @@ __global__ void __launch_bounds__(256) tree_attn_q4_join_kernel(const Q4Attn p) 
   for (int c = 0; c < kPer; ++c) a[c] = 0.f;
   for (int s = 0; s < pieces; ++s) {
     const float fs = __shfl_sync(0xffffffffu, s < 32 ? f[0] : f[1], s & 31);
-    const float *src = p.part_o + part_row(s) * D + lane * kPer;
+    // (a partial row's 16-byte chunks are swizzled by its place in the block, which
+    // spreads the many-row kernel's stores over the banks)
+    const float *src = p.part_o + part_row(s) * D + ((lane * kPer / 4) ^ (rl & 7)) * 4 + lane * kPer % 4;
     if constexpr (kPer == 4) {
       const float4 v = *reinterpret_cast<const float4 *>(src);
       a[0] += fs * v.x;

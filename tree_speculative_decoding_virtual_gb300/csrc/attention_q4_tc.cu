@@ -89,7 +89,7 @@ struct TcSeg {
 struct TcShared {
   uint64_t pk_full[2][kPackMost], pk_empty[2][kPackMost];  // K, V
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
-  uint64_t s_full[2], p_full[2], o_final[2], q_full, drain;  // (kTcBarriers in all)
+  uint64_t s_full[2], p_full[2], o_final[2], q_full, drain;  // (kTcBarriers in all, in the order tc_segment counts on)
   float2 ml[kBM];           // chain 1's (reference, sum) when it shares chain 0's rows
   float half[2][2][kBM];    // by chain, thread of the row, row: exchange between the two
   uint8_t asks[2][2][kBM];  // likewise
@@ -175,16 +175,26 @@ __device__ __forceinline__ void chain_sync(int c) {
   asm volatile("barrier.cta.sync %0, 256;\n" ::"r"(2 + c) : "memory");
 }
 
-// Scores of the 32 keys from tail index j0 on: what the row may not see becomes
-// -inf.  Returns the visible ones.
-__device__ __forceinline__ uint32_t mask_scores(const Q4Attn &p, int b, int node, bool rvalid, int j0, int nb,
-                                                uint32_t (&s)[32]) {
-  const uint32_t vis =
-      rvalid ? q4_visible(p, b, node, j0, nb) | (q4_visible(p, b, node, j0 + 16, nb) << 16) : 0u;
+// Visibility of the 32 keys from tail index j0 on.  Out of line, once: tiles that
+// reach the tree are few.
+__device__ __noinline__ uint32_t visible32(const Q4Attn &p, int b, int row, int j0, int nb) {
+  if (row >= nb * p.g) return 0u;
+  const int node = row / p.g;
+  return q4_visible(p, b, node, j0, nb) | (q4_visible(p, b, node, j0 + 16, nb) << 16);
+}
+
+// The reference for a row whose largest score is m: 8 below, or m where 8 is less
+// than its ulp.
+__device__ __forceinline__ float reference(float m) {
+  const float to = m - kTcOffset;
+  return m - to <= kTcOffset + 1.f ? to : m;
+}
+
+// What the row may not see becomes -inf.
+__device__ __forceinline__ void mask_scores(uint32_t vis, uint32_t (&s)[32]) {
 #pragma unroll
   for (int i = 0; i < 32; ++i)
     if (!((vis >> i) & 1u)) s[i] = 0xFF800000u;
-  return vis;
 }
 
 __device__ __forceinline__ void mbar_inval(uint32_t bar) {
@@ -197,40 +207,34 @@ __device__ __forceinline__ bool tc_segment(const Q4Attn &p, TcShared &sh, bool f
   using namespace sm100;
   tc_fence_before();
   __syncthreads();
-  if (tid == 0) {
-    if (!fresh) {
-      if (sh.bad && p.status) atomicOr(p.status, TSD_STATUS_BAD_PAGE);
-      sh.bad = 0;
-    }
-    TcSeg sg;
+  if (tid < 32) {
     int g = sh.g;
+    TcSeg sg;
     sg.more = q4_next(p, sh.plan, g, sg.s);
-    sh.g = g;
     if (sg.more) {
       sg.n = (sg.s.last - sg.s.first + kTilePages - 1) / kTilePages;
       sg.two = sg.s.rb * p.rows_per_block + kBM < sg.s.nb * p.g && p.rows_per_block > kBM;
       // the barriers lie one after the other, from pk_full to drain
-      uint64_t *all = &sh.pk_full[0][0];
-      if (!fresh)
-        for (int i = 0; i < kTcBarriers; ++i) mbar_inval(smem_addr(all + i));
-      for (int i = 0; i < 2 * kPackMost; ++i) {
-        mbar_init(smem_addr(&sh.pk_full[i / kPackMost][i % kPackMost]), 1);
-        mbar_init(smem_addr(&sh.pk_empty[i / kPackMost][i % kPackMost]), 2);
+      for (int i = tid; i < kTcBarriers; i += 32) {
+        const uint32_t bar = smem_addr(&sh.pk_full[0][0] + i);
+        const int k = i - 4 * kPackMost;  // the barriers behind the rings'
+        int count = 1;
+        if (i >= 2 * kPackMost && k < 0) count = 2;               // pk_empty: a pair of decoders
+        if (k == 0 || k == 1 || k == 4 || k == 5) count = 2;      // k_full, v_full: likewise
+        if (k == 10 || k == 11) count = sg.two && k == 11 ? 8 : 9;  // p_full: softmax warps, hand-over
+        if (k == 14) count = 16;                                  // q_full: softmax warps
+        if (!fresh) mbar_inval(bar);
+        mbar_init(bar, count);
       }
-      for (int i = 0; i < 2; ++i) {
-        mbar_init(smem_addr(&sh.k_full[i]), 2);
-        mbar_init(smem_addr(&sh.k_empty[i]), 1);
-        mbar_init(smem_addr(&sh.v_full[i]), 2);
-        mbar_init(smem_addr(&sh.v_empty[i]), 1);
-        mbar_init(smem_addr(&sh.s_full[i]), 1);
-        mbar_init(smem_addr(&sh.p_full[i]), sg.two && i == 1 ? 8 : 9);  // softmax warps, hand-over
-        mbar_init(smem_addr(&sh.o_final[i]), 1);
-      }
-      mbar_init(smem_addr(&sh.q_full), 16);
-      mbar_init(smem_addr(&sh.drain), 1);
       fence_mbar_init();
     }
-    sh.seg = sg;
+    __syncwarp();
+    if (tid == 0) {
+      if (!fresh && sh.bad && p.status) atomicOr(p.status, TSD_STATUS_BAD_PAGE);
+      sh.bad = 0;
+      sh.g = g;
+      sh.seg = sg;
+    }
   }
   __syncthreads();
   tc_fence_after();
@@ -507,28 +511,24 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4
     // half a Q row -> fp16, scaled by a power of two (both chains know it)
     float mul;
     {
-      uint32_t q[D / 4];
       const int row = row_of(rl, rt);
       const bool rvalid = row < sg.s.nb * p.g;
       const uint4 *src = reinterpret_cast<const uint4 *>(
           p.q + q4_out_row(p, sg.s.b, sg.s.h, rvalid ? row : 0) * D + half * (D / 2));
-      float amax = 0.f;
+      uint4 x[D / 16];
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) x[i] = rvalid ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
+      uint32_t most = 0u;  // bf16 magnitudes order as integers (NaN above all)
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) {
-        const uint4 x = rvalid ? src[i] : make_uint4(0u, 0u, 0u, 0u);
-        q[4 * i] = x.x;
-        q[4 * i + 1] = x.y;
-        q[4 * i + 2] = x.z;
-        q[4 * i + 3] = x.w;
+        most = __vmaxu2(__vmaxu2(most, x[i].x & 0x7FFF7FFFu), x[i].y & 0x7FFF7FFFu);
+        most = __vmaxu2(__vmaxu2(most, x[i].z & 0x7FFF7FFFu), x[i].w & 0x7FFF7FFFu);
       }
-#pragma unroll
-      for (int i = 0; i < D / 4; ++i) {
-        amax = fmaxf(amax, fabsf(__uint_as_float(q[i] << 16)));
-        amax = fmaxf(amax, fabsf(__uint_as_float(q[i] & 0xFFFF0000u)));
-      }
+      float amax = __uint_as_float(max(most << 16, most & 0xFFFF0000u));
       sh.half[c][half][rl] = amax;
       chain_sync(c);
-      amax = fmaxf(amax, sh.half[c][half ^ 1][rl]);
+      const float other = sh.half[c][half ^ 1][rl];
+      amax = __uint_as_float(max(__float_as_uint(amax), __float_as_uint(other)));
       const int e = q4_exponent(amax);
       // the factor's sign goes into q, and it stays between the smallest and the
       // largest normal number, so that a masked score (-inf) stays one
@@ -540,11 +540,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4
         uint8_t *dst = gbase + L::kQ + rt * L::kTile;
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
-          uint32_t w[4];
+          uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            w[k] = pack_half2(__uint_as_float(q[4 * i + k] << 16) * up1 * up2,
-                              __uint_as_float(q[4 * i + k] & 0xFFFF0000u) * up1 * up2);
+            w[k] = pack_half2(__uint_as_float(w[k] << 16) * up1 * up2,
+                              __uint_as_float(w[k] & 0xFFFF0000u) * up1 * up2);
           const int ch = half * (D / 16) + i;  // 16-byte chunk of the row
           *reinterpret_cast<uint4 *>(dst + (ch >> 3) * L::kHalf + sw128_offset(rl, ch & 7)) =
               make_uint4(w[0], w[1], w[2], w[3]);
@@ -562,10 +562,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4
     // this thread's first key slot in tile j is 128 j + slot0; the tile reaches the
     // tree where it passes tree_from
     const int slot0 = sg.s.first * kPage + half * 64, tree_from = sg.s.P - 64 - slot0;
-    auto mask = [&](int j, int k, uint32_t (&s)[32]) {
-      const int row = row_of(rl, rt);
-      const bool rvalid = row < sg.s.nb * p.g;
-      return mask_scores(p, sg.s.b, rvalid ? row / p.g : 0, rvalid, j * kBN + slot0 + k * 32 - sg.s.P, sg.s.nb, s);
+    auto visible = [&](int j, int k) {
+      return visible32(p, sg.s.b, row_of(rl, rt), j * kBN + slot0 + k * 32 - sg.s.P, sg.s.nb);
     };
     for (int j = two ? 0 : c; ok && j < n; j += two ? 1 : 2, ++u) {
       // one warp looks at the barrier, the others wait for it without polling
@@ -585,7 +583,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4
         if (jv >= 0) mbar_arrive(smem_addr(&sh.v_empty[jv & 1]));
       }
       const bool tail = j * kBN > tree_from;
-      const unsigned long long ref2 = f2_pack(-ref, -ref);
       unsigned long long acc0 = 0ull, acc1 = 0ull;
       uint32_t pk[32], seen = 0u;
       {
@@ -597,8 +594,26 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4
         tmem_wait_ld(x[1]);
         if (tail) {
 #pragma unroll
-          for (int k = 0; k < 2; ++k) seen |= mask(j, k, x[k]);
+          for (int k = 0; k < 2; ++k) {
+            const uint32_t vis = visible(j, k);
+            seen |= vis;
+            mask_scores(vis, x[k]);
+          }
         }
+        if (u == 0) {
+          // the chain's first tile: the row's maximum over it is the reference
+          float m = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) m = fmax3(m, __uint_as_float(x[0][i]), __uint_as_float(x[1][i]));
+          sh.half[c][half][rl] = m;
+          chain_sync(c);
+          m = __fmul_rn(fmaxf(m, sh.half[c][half ^ 1][rl]), mul);
+          if (m > -INFINITY) {
+            ref = reference(m);
+            unset = false;
+          }
+        }
+        const unsigned long long ref2 = f2_pack(-ref, -ref);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
 #pragma unroll
@@ -632,7 +647,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4
           uint32_t s[32];
           tmem_ld32(tS + half * 64 + k * 32, s);
           tmem_wait_ld(s);
-          if (tail) mask(j, k, s);
+          if (tail) mask_scores(visible(j, k), s);
 #pragma unroll
           for (int i = 0; i < 32; ++i) m = fmaxf(m, __fmul_rn(__uint_as_float(s[i]), mul));
         }
@@ -644,8 +659,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4
         m = fmaxf(m, sh.half[c][half ^ 1][rl]);
         float f = 1.f;
         if (row_asks && m > -INFINITY && (unset || !(m - ref <= kTcOffset + 2.f))) {
-          float to = m - kTcOffset;
-          if (!(m - to <= kTcOffset + 1.f)) to = m;  // 8 is less than an ulp of m
+          const float to = reference(m);
           // (nothing was added yet to a row without a reference)
           if (!unset) f = ex2_approx(ref - to);
           ref = to;
@@ -659,7 +673,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4
             uint32_t s[32];
             tmem_ld32(tS + half * 64 + k * 32, s);
             tmem_wait_ld(s);
-            if (tail) mask(j, k, s);
+            if (tail) mask_scores(visible(j, k), s);
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               const float e0 = ex2_approx(__fsub_rn(__fmul_rn(__uint_as_float(s[2 * i]), mul), ref));
@@ -697,19 +711,22 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4
     // ---- epilogue: O of this chain is complete ----
     const bool joined = !two && chains == 2;
     if (ok) ok = __all_sync(0xffffffffu, tc_wait(sh.o_final[c], 0, lim, abort));
-    // (joined: chain 1's O goes over the K and V tiles, which chain 0's last
-    // MMAs may still read)
-    if (ok && joined) ok = __all_sync(0xffffffffu, tc_wait(sh.o_final[c ^ 1], 0, lim, abort));
+    // (the rows go over the K and V tiles, which the other chain's last MMAs may
+    // still read)
+    if (ok && chains == 2) ok = __all_sync(0xffffffffu, tc_wait(sh.o_final[c ^ 1], 0, lim, abort));
     tc_fence_after();
     sh.half[c][half][rl] = l;
     chain_sync(c);
     l += sh.half[c][half ^ 1][rl];
     float M = unset ? -INFINITY : ref;
     if (unset && l != l) M = 0.f;  // only NaN scores so far
-    float *stage = reinterpret_cast<float *>(gbase + L::kK);  // K and V tiles are done with
+    // K and V tiles are done with: chain 1's O when it shares chain 0's rows
+    // (column-major, so that lanes do not collide), then the finished rows
+    float *stage = reinterpret_cast<float *>(gbase + L::kK);
+    const uint32_t rows_at = (two && c == 0 ? L::kK : L::kV);
+    uint8_t *rows_out = gbase + rows_at;
     const int q0 = half * (D / 64);  // this thread's 32-column parts of O
     if (joined && c == 1) {
-      // chain 1's part, transposed: column-major, so that lanes do not collide
 #pragma unroll 1
       for (int q = q0; ok && q < q0 + D / 64; ++q) {
         uint32_t o[32];
@@ -731,52 +748,75 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4
         l = f0 * l + f1 * other.y;
         M = top;
       }
-      const bool bad = sh.bad != 0;
-      const bool direct = sg.s.direct;
-      const bool empty = bad || l == 0.f;
-      const float inv = empty ? 0.f : 1.f / l;
-      const int row = row_of(rl, rt);
-      const bool rvalid = row < sg.s.nb * p.g;
-      const size_t pr = sg.s.part + rt * kBM + rl;
-      const size_t orow = rvalid ? q4_out_row(p, sg.s.b, sg.s.h, row) : 0;
+      const bool bad = sh.bad != 0, direct = sg.s.direct;
+      const bool empty = direct && (bad || l == 0.f);
+      // O times this; a row that is left out becomes 0 whatever its sums are
+      if (direct) {
+        const float inv = empty ? 0.f : 1.f / l;
+        f0 *= inv;
+        f1 *= inv;
+      }
 #pragma unroll 1
       for (int q = q0; ok && q < q0 + D / 64; ++q) {
         uint32_t o[32];
         tmem_ld32(tO + q * 32, o);
         tmem_wait_ld(o);
+        if (empty) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          float v = __uint_as_float(o[i]) * f0;
-          if (joined) v = fmaf(f1, f1 == 0.f ? 0.f : stage[(q * 32 + i) * kBM + rl], v);
-          o[i] = __float_as_uint(v);
+          for (int i = 0; i < 32; ++i) o[i] = 0u;
         }
-        if (rvalid) {
-          const float *v = reinterpret_cast<const float *>(o);
-          if (direct) {
-            uint4 *dst = reinterpret_cast<uint4 *>(p.out + orow * D + q * 32);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              dst[i] = empty ? make_uint4(0u, 0u, 0u, 0u)
-                             : make_uint4(pack_bf16x2(v[8 * i] * inv, v[8 * i + 1] * inv),
-                                          pack_bf16x2(v[8 * i + 2] * inv, v[8 * i + 3] * inv),
-                                          pack_bf16x2(v[8 * i + 4] * inv, v[8 * i + 5] * inv),
-                                          pack_bf16x2(v[8 * i + 6] * inv, v[8 * i + 7] * inv));
-          } else {
-            float4 *dst = reinterpret_cast<float4 *>(p.part_o + pr * D + q * 32);
+        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f0);
+        if (joined && f1 != 0.f) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              dst[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-          }
+          for (int i = 0; i < 32; ++i)
+            o[i] = __float_as_uint(fmaf(f1, stage[(q * 32 + i) * kBM + rl], __uint_as_float(o[i])));
+        }
+        const float *v = reinterpret_cast<const float *>(o);
+        // whole rows in shared memory, their 16-byte chunks swizzled by row
+        if (direct) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<uint4 *>(rows_out + rl * (D * 2) + (((q * 4 + i) ^ (rl & 7)) << 4)) =
+                make_uint4(pack_bf16x2(v[8 * i], v[8 * i + 1]), pack_bf16x2(v[8 * i + 2], v[8 * i + 3]),
+                           pack_bf16x2(v[8 * i + 4], v[8 * i + 5]), pack_bf16x2(v[8 * i + 6], v[8 * i + 7]));
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<float4 *>(rows_out + rl * (D * 4) + (((q * 8 + i) ^ (rl & 7)) << 4)) =
+                make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
         }
       }
-      if (rvalid && half == 0) {
+      const int row = row_of(rl, rt);
+      if (half == 0 && row < sg.s.nb * p.g) {
         if (!direct)
-          p.part_ml[pr] = make_float2(M, bad ? -1.f : l);
+          p.part_ml[sg.s.part + rt * kBM + rl] = make_float2(M, bad ? -1.f : l);
         else if (p.lse)
-          p.lse[orow] = empty ? -INFINITY : (M + log2f(l)) * kTcLn2;
+          p.lse[q4_out_row(p, sg.s.b, sg.s.h, row)] = empty ? -INFINITY : (M + log2f(l)) * kTcLn2;
+      }
+      if (!direct) fence_proxy_async_smem();
+      chain_sync(c);
+      const int w = (warp - 8) & 7;
+      if (direct) {
+        constexpr int kLanes = D / 8;  // of a row
+#pragma unroll 1
+        for (int r0 = w * (32 / kLanes); ok && r0 < kBM; r0 += 8 * (32 / kLanes)) {
+          const int r = r0 + lane / kLanes, ch = lane % kLanes, orow = row_of(r, rt);
+          if (orow < sg.s.nb * p.g)
+            reinterpret_cast<uint4 *>(p.out + q4_out_row(p, sg.s.b, sg.s.h, orow) * D)[ch] =
+                *reinterpret_cast<const uint4 *>(rows_out + r * (D * 2) + ((ch ^ (r & 7)) << 4));
+        }
+      } else if (lane == 0 && ok) {  // 16 partial rows a warp, in one piece and as they lie
+        const int rows = min(kBM / 8, sg.s.nb * p.g - row_of(w * (kBM / 8), rt));
+        if (rows > 0) {
+          bulk_store(p.part_o + (sg.s.part + rt * kBM + w * (kBM / 8)) * D,
+                     base + rows_at + w * (kBM / 8) * (D * 4), rows * D * 4);
+          bulk_wait_read();
+        }
       }
     }
     }
+    if (lane == 0) bulk_wait();  // (the last segments' partial rows are written)
   }
   // (the last tc_segment ended with a barrier)
   if (warp == 1) tmem_dealloc(tmem, kTmemCols);
