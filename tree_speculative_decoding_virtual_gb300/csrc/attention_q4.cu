@@ -525,13 +525,14 @@ __global__ void __launch_bounds__(256) tree_attn_q4_join_kernel(const Q4Attn p) 
   const bool ok = q4_seq(p, b, P, nb, bad_len) && r < nb * p.g;
   const int rb = r / p.rows_per_block;
   const int rl = r % p.rows_per_block;
-  int pieces = 0, k0 = 0, part = 0, start = 0;  // planned: the range's first block, unit
+  int pieces = 0, k0 = 0;  // planned: the block of the range's first unit
   if (ok && p.planned) {
     const int4 plan = p.plan[b];
-    part = plan.w;
-    start = plan.x + (h * plan.z + rb) * plan.y;
-    k0 = start / part;
-    pieces = (start + plan.y - 1) / part - k0 + 1;
+    const int t = plan.y, rbs = plan.z >> 2, last_w = plan.z & 3, part = plan.w;
+    const int full = p.range_cost + t * p.row_tiles;
+    const int first = plan.x + h * (rbs * full - t * (p.row_tiles - last_w)) + rb * full + p.range_cost;
+    k0 = first / part;
+    pieces = (first + (t - 1) * (rb == rbs - 1 ? last_w : p.row_tiles)) / part - k0 + 1;
     if (pieces == 1) return;  // its block has written it
   } else if (ok) {
     pieces = ((P + nb + kPage - 1) / kPage + p.chunk - 1) / p.chunk;
@@ -539,7 +540,7 @@ __global__ void __launch_bounds__(256) tree_attn_q4_join_kernel(const Q4Attn p) 
   const size_t base = p.planned ? 0 : q4_part_row(p, b, h, rb, 0);
   auto part_row = [&](int s) -> size_t {
     if (!p.planned) return base + (size_t)s * p.rows_per_block + rl;
-    return ((size_t)(k0 + s) * 2 + (start > (k0 + s) * part ? 1 : 0)) * p.rows_per_block + rl;
+    return ((size_t)(k0 + s) * 2 + (s == 0 ? 1 : 0)) * p.rows_per_block + rl;
   };
   // lane l holds the (reference, sum) of pieces l, l + 32, ...: at most 64
   float2 ml[2] = {make_float2(-INFINITY, 0.f), make_float2(-INFINITY, 0.f)};
@@ -607,6 +608,12 @@ struct Q4Shape {
 // Rows of a kv head from which the many-row kernel runs.
 constexpr int kTcMinRows = 33;
 
+// Fixed cost of a key range, in units of 128 keys of one row tile.  Measured, 16
+// trees of up to 127 nodes over 128 to 8064 slots, many-row kernel: 0: 110 us, 4: 79,
+// 6: 74, 8: 71, 10: 71, 16: 78; 64 tokens over 64 to 16320 slots, few-row kernel:
+// 0: 94 us, 2: 83, 4: 76, 5: 75, 8: 77.  Equal long ranges take the same time with any.
+constexpr int kTcRangeCost = 8, kRowsRangeCost = 5;
+
 // Host: how a call is cut up.
 Q4Shape q4_shape(int B, int N_max, int Hq, int Hkv, int D, int max_slots) {
   Q4Shape pl = {};
@@ -634,7 +641,7 @@ Q4Shape q4_shape(int B, int N_max, int Hq, int Hkv, int D, int max_slots) {
     return pl;
   }
   size_t pieces;
-  if (B <= kPlanSeqs && base * units < (1ll << 30)) {
+  if (B <= kPlanSeqs && base * (2 * units + 64) < (1ll << 30)) {
     pl.planned = true;
     // as many parts as blocks run at a time; parts are longer where that would cut
     // a range into more than kPlanPieces
@@ -741,7 +748,9 @@ TSD_API int tsd_tree_attn_fwd_q4(const uint16_t *q, const uint8_t *k_cache, cons
   p.cluster = pl.cluster ? pl.splits : 0;
   p.planned = pl.planned;
   p.slots = pl.blocks;
-  p.min_units = 2;  // a shorter part would be mostly set-up
+  p.row_tiles = pl.tc ? pl.rows_per_block / 128 : 1;
+  p.range_cost = pl.tc ? kTcRangeCost : kRowsRangeCost;
+  p.min_part = p.range_cost + 2 * p.row_tiles;  // a shorter part would be mostly set-up
   if (pl.bytes) {
     char *ws = reinterpret_cast<char *>(workspace);
     p.plan = reinterpret_cast<int4 *>(ws);

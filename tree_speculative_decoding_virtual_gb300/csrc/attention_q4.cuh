@@ -24,8 +24,9 @@ struct Q4Attn {
   //   else: pieces of `chunk` pages, `splits` of the longest range
   int cluster, planned;
   int splits, chunk;
-  int slots, min_units;  // planned: blocks that run at a time; least part of one
-  int4 *plan;      // planned: per sequence (first unit, units, row blocks, units of a part)
+  int slots, min_part;  // planned: blocks that run at a time; least part of one
+  int range_cost, row_tiles;  // planned: a range's fixed cost; a unit's cost in a full row block
+  int4 *plan;      // planned: per sequence (start, units, row blocks * 4 + cost of a unit in the last, part)
   float *part_o;   // [pieces][rows_per_block][D]: unnormalised fp32 outputs
   float2 *part_ml;  // [pieces][rows_per_block]: (reference in log2 units, sum), sum -1: bad page
   uint16_t *out;
@@ -87,20 +88,21 @@ __device__ __forceinline__ size_t q4_part_row(const Q4Attn &p, int b, int h, int
 }
 
 // The plan of a batch of up to 64 sequences.  Every (sequence, kv head, row block)
-// has a key range of t units of 8 pages (128 keys).  The ranges are laid end to
-// end and cut into equal parts, as many as blocks run at a time, so every block
-// has the same work whatever the lengths; a block takes the segments of its part
-// in turn, and only a range that a cut goes through leaves partial rows.  Every
-// block computes the plan for itself (about a microsecond), which spares a kernel
-// before this one.
+// has a key range of t units of 8 pages (128 keys).  A unit costs w, 1 or 2 (the
+// many-row kernel's row tiles), and a range F more for its set-up, so unit u of a
+// range begins at F + u w.  The ranges are laid end to end and cut into equal
+// parts, as many as blocks run at a time, and a block takes the units that begin in
+// its part: every block has the same work whatever the lengths, and only a range
+// that a cut goes through leaves partial rows.  Every block computes the plan for
+// itself (about a microsecond), which spares a kernel before this one.
 constexpr int kPlanSeqs = 64;
 constexpr int kPlanPieces = 64;  // pieces of one range at most
 constexpr int kUnitPages = 8;
 
 struct Q4Plan {
-  int start[kPlanSeqs + 1];  // first unit of each sequence
-  int units[kPlanSeqs], rbs[kPlanSeqs], P[kPlanSeqs], nb[kPlanSeqs];
-  int part;  // units of a block
+  int start[kPlanSeqs + 1];  // where each sequence begins
+  int units[kPlanSeqs], rbs[kPlanSeqs], last_w[kPlanSeqs], P[kPlanSeqs], nb[kPlanSeqs];
+  int part;  // length of a block's part
 };
 
 // One segment: pages [first, last) of a key range.
@@ -123,12 +125,14 @@ __device__ __forceinline__ void q4_plan(const Q4Attn &p, Q4Plan &sh) {
     const bool ok = b < p.B && q4_seq(p, b, P, nb, bad);
     const int t = ok ? (P + nb + kUnitPages * kPage - 1) / (kUnitPages * kPage) : 0;
     const int rbs = ok ? (nb * p.g + p.rows_per_block - 1) / p.rows_per_block : 0;
+    const int last_w = p.row_tiles > 1 && nb * p.g - (rbs - 1) * p.rows_per_block > p.rows_per_block / 2 ? 2 : 1;
     sh.units[b] = t;
     sh.rbs[b] = rbs;
+    sh.last_w[b] = last_w;
     sh.P[b] = P;
     sh.nb[b] = nb;
-    cnt[e] = t * rbs * p.Hkv;
-    longest = max(longest, t);
+    cnt[e] = rbs ? (rbs * p.range_cost + t * ((rbs - 1) * p.row_tiles + last_w)) * p.Hkv : 0;
+    longest = max(longest, t * p.row_tiles + p.range_cost);
     if (blockIdx.x == 0 && bad && p.status) atomicOr(p.status, TSD_STATUS_BAD_LEN);
   }
   longest = __reduce_max_sync(0xffffffffu, longest);
@@ -139,7 +143,7 @@ __device__ __forceinline__ void q4_plan(const Q4Attn &p, Q4Plan &sh) {
     if (lane >= off) incl += y;
   }
   const int total = __shfl_sync(0xffffffffu, incl, 31);
-  const int part = max(max((total + p.slots - 1) / p.slots, p.min_units),
+  const int part = max(max((total + p.slots - 1) / p.slots, p.min_part),
                        (longest + kPlanPieces - 3) / (kPlanPieces - 2));
   const int first = incl - cnt[0] - cnt[1];
   sh.start[2 * lane] = first;
@@ -152,36 +156,45 @@ __device__ __forceinline__ void q4_plan(const Q4Attn &p, Q4Plan &sh) {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int b = 2 * lane + e;
-      if (b < p.B) p.plan[b] = make_int4(first + (e ? cnt[0] : 0), sh.units[b], sh.rbs[b], part);
+      if (b < p.B) p.plan[b] = make_int4(first + (e ? cnt[0] : 0), sh.units[b], sh.rbs[b] * 4 + sh.last_w[b], part);
     }
   }
 }
 
-// The next segment of this block; g counts its units (start at blockIdx.x *
+// The next segment of this block; g counts along its part (start at blockIdx.x *
 // part when planned, else at 0).  False: there is none.
 __device__ __forceinline__ bool q4_next(const Q4Attn &p, const Q4Plan &sh, int &g, Q4Seg &s) {
   if (p.planned) {
-    const int g0 = blockIdx.x * sh.part, end = min(sh.start[kPlanSeqs], g0 + sh.part);
-    if (g >= end) return false;
-    int b = 0;  // the last sequence that starts at or before g and is not empty
+    const int end = min(sh.start[kPlanSeqs], (int)(blockIdx.x + 1) * sh.part);
+    while (g < end) {
+      int b = 0;  // the last sequence that starts at or before g and is not empty
 #pragma unroll
-    for (int step = kPlanSeqs / 2; step; step >>= 1)
-      if (sh.start[b + step] <= g) b += step;
-    const int t = sh.units[b], local = g - sh.start[b];
-    const int range = local / t, off = local - range * t, len = min(t - off, end - g);
-    s.b = b;
-    s.h = range / sh.rbs[b];
-    s.rb = range - s.h * sh.rbs[b];
-    s.P = sh.P[b];
-    s.nb = sh.nb[b];
-    s.first = off * kUnitPages;
-    s.last = min((s.P + s.nb + kPage - 1) / kPage, (off + len) * kUnitPages);
-    s.direct = len == t;
-    // a cut leaves a block at most one range that started before it and one that
-    // goes on after it
-    s.part = ((size_t)blockIdx.x * 2 + (g - off > g0 ? 1 : 0)) * p.rows_per_block;
-    g += len;
-    return true;
+      for (int step = kPlanSeqs / 2; step; step >>= 1)
+        if (sh.start[b + step] <= g) b += step;
+      const int t = sh.units[b], last_w = sh.last_w[b], rbs = sh.rbs[b];
+      const int full = p.range_cost + t * p.row_tiles;
+      const int head = rbs * full - t * (p.row_tiles - last_w);
+      const int local = g - sh.start[b];
+      s.b = b;
+      s.h = local / head;
+      s.rb = min((local - s.h * head) / full, rbs - 1);
+      const int w = s.rb == rbs - 1 ? last_w : p.row_tiles;
+      const int x0 = local - s.h * head - s.rb * full;
+      const int x1 = min(p.range_cost + t * w, x0 + end - g);
+      g += x1 - x0;
+      const int u0 = (max(x0 - p.range_cost, 0) + w - 1) / w, u1 = (max(x1 - p.range_cost, 0) + w - 1) / w;
+      if (u0 >= u1) continue;
+      s.P = sh.P[b];
+      s.nb = sh.nb[b];
+      s.first = u0 * kUnitPages;
+      s.last = min((s.P + s.nb + kPage - 1) / kPage, u1 * kUnitPages);
+      s.direct = u1 - u0 == t;
+      // a cut leaves a block at most one range whose start it has but not its end,
+      // and one whose start it has not
+      s.part = ((size_t)blockIdx.x * 2 + (u0 == 0 ? 1 : 0)) * p.rows_per_block;
+      return true;
+    }
+    return false;
   }
   if (g != 0) return false;
   g = 1;
