@@ -118,12 +118,21 @@ __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, uint64
     if ((i & 63) == 0 && global_timer_ns() - t0 > limit_ns) return false;
   }
 }
+// The same, and it gives up when another wait of the block ran out.
 __device__ __forceinline__ bool tc_wait(uint64_t &bar, uint32_t parity, uint64_t limit, volatile int *abort) {
   using namespace sm100;
-  if (*abort) return false;
-  if (wait_phase(smem_addr(&bar), parity, limit)) return true;
-  *abort = 1;
-  return false;
+  if (mbar_try_wait(smem_addr(&bar), parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+#pragma unroll 1
+  for (int i = 1;; ++i) {
+    if (mbar_try_wait(smem_addr(&bar), parity)) return true;
+    if ((i & 63) != 0) continue;
+    if (*abort) return false;
+    if (global_timer_ns() - t0 > limit) {
+      *abort = 1;
+      return false;
+    }
+  }
 }
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
@@ -321,18 +330,20 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4
       int ids = read_ids(0), ahead = read_ids(1);
       bool ok = true;
       int issued = 0;
-      for (int m = 0; m < 2 * n; ++m) {
+      // (slot and phase are counted: a division by the ring's size takes as long as
+      // a wait)
+      uint32_t phase = 1;
+      for (int m = 0, slot = 0; m < 2 * n; ++m) {
         if (m > 0 && (m & 7) == 0) {
           ids = ahead;
           ahead = read_ids((m >> 3) + 1);
         }
-        const int slot = m % ring;
         const int id = __shfl_sync(0xffffffffu, ids, (m & 7) * kItemPages + (lane & (kItemPages - 1)));
         const bool mine = lane < kItemPages && first + m * kItemPages + lane < last;
         const bool bad = mine && (id < 0 || id >= p.num_blocks);
         if (bad) sh.bad = 1;
         if (m >= ring)
-          ok = __all_sync(0xffffffffu, tc_wait(sh.pk_empty[v][slot], ((m / ring) - 1) & 1, lim, abort));
+          ok = __all_sync(0xffffffffu, tc_wait(sh.pk_empty[v][slot], phase, lim, abort));
         if (!ok) break;
         const bool copy = mine && !bad;
         const int copies = __popc(__ballot_sync(0xffffffffu, copy));
@@ -343,6 +354,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4
           bulk_load(base + L::pack(v, slot) + lane * Page::kBytes,
                     pool + ((size_t)id * p.Hkv + h) * Page::kBytes, Page::kBytes, bar);
         issued = m + 1;
+        if (++slot == ring) {
+          slot = 0;
+          phase ^= 1;
+        }
       }
       // no copy is in flight when the block exits
       for (int m = max(0, issued - ring); m < issued; ++m)
@@ -447,9 +462,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4
     // lanes of a store's quarter touch different banks
     const int flip = D == 128 ? grp >> 2 : 0;
     const int c0 = (grp & 3) * 2;
-    for (int m = 0; m < 2 * n; ++m) {  // half tiles
-      const int tile = m >> 1, st = tile & 1, slot = m % ring;
-      bool ok = tc_wait(sh.pk_full[v][slot], (m / ring) & 1, lim, abort);
+    uint32_t phase = 0;
+    for (int m = 0, slot = 0; m < 2 * n; ++m) {  // half tiles
+      const int tile = m >> 1, st = tile & 1;
+      bool ok = tc_wait(sh.pk_full[v][slot], phase, lim, abort);
       if (ok && tile >= 2 && (m & 1) == 0)
         ok = tc_wait(v ? sh.v_empty[st] : sh.k_empty[st], ((tile >> 1) - 1) & 1, lim, abort);
       if (!__all_sync(0xffffffffu, ok)) break;
@@ -488,6 +504,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4
       if (lane == 0) {
         if (m & 1) mbar_arrive(smem_addr(v ? &sh.v_full[st] : &sh.k_full[st]));
         mbar_arrive(smem_addr(&sh.pk_empty[v][slot]));
+      }
+      if (++slot == ring) {
+        slot = 0;
+        phase ^= 1;
       }
     }
     }
