@@ -13,8 +13,12 @@
 //
 // One pass over the logits, so the kernel is bound by HBM (4 or 2 bytes a
 // logit).  A cluster of up to 8 CTAs takes a row (one CTA where the rows alone
-// fill the GPU); a CTA walks its slice in chunks of 4096 logits, 16 a thread, with
-// the next 16 already on the way.
+// fill the GPU); a CTA walks its slice in chunks of 4096 logits, 16 a thread, which
+// come through a ring in shared memory (three chunks ahead: it keeps the stream going
+// while the CTA settles its first chunk, and what passes the threshold is looked up
+// there; with the next 16 logits in registers and looked up in memory, 1216 rows of
+// 128256 and their 20 best took 115 us instead of 103, without a best list 95 instead
+// of 99).  Rows without 16-byte alignment go through registers.
 //   reference  the maximum of the CTA's first chunk is the m of its sums; a warp
 //              that meets a value more than 40 above its m moves it (e^40 leaves
 //              fp32 sums far from overflow)
@@ -46,6 +50,7 @@ constexpr int kLpWarps = kLpThreads / 32;
 constexpr int kPerThread = 16;
 constexpr int kChunk = kLpThreads * kPerThread;  // logits held at a time
 constexpr int kMaxTop = 32;
+constexpr int kLpRing = 3 * kChunk * 4;  // bytes of a CTA's copies in flight
 constexpr int kCap = 512;      // candidates the list holds (kMaxTop more for ties)
 constexpr int kTies = 64;      // values equal to the threshold that are listed
 constexpr float kMove = 40.f;  // the reference follows a value so far above it
@@ -158,6 +163,43 @@ struct LpRaw {
       }
     }
   }
+  // The same part by way of shared memory: every thread copies, and later reads,
+  // its own 16 bytes of each group, so that no barrier is needed.
+  static constexpr int kGroups = kWords / 4;
+  static constexpr int kStage = kLpThreads * kGroups * 16;
+  static constexpr int kStages = kLpRing / kStage;
+  static __device__ __forceinline__ void fetch(uint32_t stage, const void *row, int c0, int end, int tid) {
+    constexpr int kW = kBf16 ? 8 : 4;
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+      const int i = c0 + chunk_pos<kBf16, kVec>(g * kW, tid);
+      if (i < end) sm100::cp_async_16(stage + (g * kLpThreads + tid) * 16, reinterpret_cast<const uint4 *>(row) + i / kW);
+    }
+    asm volatile("cp.async.commit_group;\n" ::: "memory");
+  }
+  __device__ __forceinline__ void read(const uint8_t *stage, int c0, int end, int tid) {
+    constexpr int kW = kBf16 ? 8 : 4;
+    constexpr uint32_t none = kBf16 ? 0xFF80FF80u : 0xFF800000u;
+    asm volatile("cp.async.wait_group %0;\n" ::"n"(kStages - 1) : "memory");
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+      const int i = c0 + chunk_pos<kBf16, kVec>(g * kW, tid);
+      uint4 v = *reinterpret_cast<const uint4 *>(stage + (g * kLpThreads + tid) * 16);
+      if (i >= end) v = make_uint4(none, none, none, none);
+      w[4 * g] = v.x;
+      w[4 * g + 1] = v.y;
+      w[4 * g + 2] = v.z;
+      w[4 * g + 3] = v.w;
+    }
+  }
+  static __device__ __forceinline__ float one(const uint8_t *stage, int e, int tid) {
+    constexpr int kW = kBf16 ? 8 : 4;
+    const uint8_t *p = stage + (e / kW * kLpThreads + tid) * 16;
+    if constexpr (kBf16)
+      return __uint_as_float((uint32_t)reinterpret_cast<const uint16_t *>(p)[e % kW] << 16);
+    else
+      return reinterpret_cast<const float *>(p)[e % kW];
+  }
   __device__ __forceinline__ float get(int e) const {
     if constexpr (kBf16 && kVec)
       return __uint_as_float((e & 1) ? w[e / 2] & 0xFFFF0000u : w[e / 2] << 16);
@@ -188,9 +230,13 @@ __device__ __forceinline__ int keep_best(LpShared &sh, int n, int k) {
     mine[q] = c < n ? sh.cand[c] : 0ull;
     rank[q] = kCap;
     if (c < n) {
-      int r = 0;
+      int r = 0, o = 0;
 #pragma unroll 4
-      for (int o = 0; o < n; ++o) r += sh.cand[o] > mine[q] ? 1 : 0;
+      for (; o + 1 < n; o += 2) {  // two at a time
+        const ulonglong2 two = *reinterpret_cast<const ulonglong2 *>(sh.cand + o);
+        r += (two.x > mine[q] ? 1 : 0) + (two.y > mine[q] ? 1 : 0);
+      }
+      if (o < n) r += sh.cand[o] > mine[q] ? 1 : 0;
       rank[q] = r;
     }
   }
@@ -357,6 +403,7 @@ template <bool kBf16, bool kVec>
 __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const LpArgs a) {
   using namespace sm100;
   __shared__ LpShared sh;
+  extern __shared__ __align__(16) uint8_t ring[];
   pdl_trigger();
   pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -393,8 +440,17 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const LpArgs a)
     // the logit asked for, read apart from the stream (its line is in flight
     // anyway)
     if (tid == 0 && token >= first && token < last) sh.xt = one_logit<kBf16>(src, token);
-    LpRaw<kBf16, kVec> x, next;
-    x.load(src, first, min(last, first + kChunk), tid);
+    using Raw = LpRaw<kBf16, kVec>;
+    Raw x, next;
+    const uint32_t ring_at = smem_addr(ring);
+    if constexpr (kVec) {
+#pragma unroll
+      for (int i = 0; i < Raw::kStages; ++i)  // one group a stage, an empty one past the end
+        Raw::fetch(ring_at + i * Raw::kStage, src, first + i * kChunk, last, tid);
+      x.read(ring, first, last, tid);
+    } else {
+      x.load(src, first, min(last, first + kChunk), tid);
+    }
     // (fmaxf drops a NaN: a threshold may be too low, not too high, and the sums
     // keep the NaN)
     float top = -INFINITY;
@@ -439,13 +495,17 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const LpArgs a)
     bool settled = false;
     int next_settle = first + 4 * kChunk;
 
-    float S = 0.f, T = 0.f;
+    unsigned long long S2 = 0ull, T2 = 0ull;  // two sums each
+    int stage = 0;  // x's
     for (int c0 = first; c0 < last; c0 += kChunk) {
       const int end = min(last, c0 + kChunk);
-      if (end < last) next.load(src, end, min(last, end + kChunk), tid);
-      bool below = true;
+      if constexpr (!kVec) {
+        if (end < last) next.load(src, end, min(last, end + kChunk), tid);
+      }
+      float most = x.get(0);
 #pragma unroll
-      for (int e = 0; e < kPerThread; ++e) below = below && x.get(e) < gate;  // (false for a NaN)
+      for (int e = 1; e + 1 < kPerThread; e += 2) most = fmax3_nan(most, x.get(e), x.get(e + 1));
+      const bool below = fmax3_nan(most, most, x.get(kPerThread - 1)) < gate;  // (false for a NaN)
       if (!below) {
         uint32_t mine = 0u;
 #pragma unroll
@@ -453,9 +513,9 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const LpArgs a)
         top = -INFINITY;
         // (the few that pass are read again: indexing the registers would spill them)
         for (; mine; mine &= mine - 1) {
-          const int id = c0 + chunk_pos<kBf16, kVec>(__ffs(mine) - 1, tid);
+          const int e = __ffs(mine) - 1, id = c0 + chunk_pos<kBf16, kVec>(e, tid);
           if (id >= end) continue;
-          const float v = one_logit<kBf16>(src, id);
+          const float v = kVec ? Raw::one(ring + stage * Raw::kStage, e, tid) : one_logit<kBf16>(src, id);
           const uint32_t vo = ordered(v);
           top = fmaxf(top, v);
           if (k == 0) continue;
@@ -468,23 +528,29 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const LpArgs a)
           }
         }
       }
+      // (x and what was read again are used: the stage can be refilled)
+      if constexpr (kVec)
+        Raw::fetch(ring_at + stage * Raw::kStage, src, c0 + Raw::kStages * kChunk, last, tid);
       __syncwarp();
       if (__any_sync(0xffffffffu, !below && top > m + kMove)) {  // the warp's reference follows
         const float up = unordered(__reduce_max_sync(0xffffffffu, ordered(below ? -INFINITY : top)));
         const float f = m == -INFINITY ? 0.f : ex2_approx((m - up) * kLog2e);
-        T = f == 0.f ? 0.f : f * (T + S * (m - up));
-        S = f * S;
+        const float2 s = f2_unpack(S2), t = f2_unpack(T2);
+        T2 = f == 0.f ? 0ull : f2_pack(f * (t.x + s.x * (m - up)), f * (t.y + s.y * (m - up)));
+        S2 = f2_pack(f * s.x, f * s.y);
         m = up;
       }
       // d = -200 stands for every d that e^d rounds to zero for, -inf included; a
       // NaN reaches S and T through e^d, and so does +inf (m = +inf: inf - inf)
-      const float base = m == -INFINITY ? 0.f : m;
+      const float base = m == -INFINITY ? 0.f : -m;
+      const unsigned long long base2 = f2_pack(base, base), log2e = f2_pack(kLog2e, kLog2e);
 #pragma unroll
-      for (int e = 0; e < kPerThread; ++e) {
-        const float d = x.get(e) - base;
-        const float p = ex2_approx(d * kLog2e);
-        S += p;
-        T = fmaf(p, fmaxf(d, -200.f), T);
+      for (int e = 0; e < kPerThread; e += 2) {
+        const unsigned long long d2 = f2_add(f2_pack(x.get(e), x.get(e + 1)), base2);
+        const float2 d = f2_unpack(d2), t = f2_unpack(f2_mul(d2, log2e));
+        const unsigned long long p = f2_pack(ex2_approx(t.x), ex2_approx(t.y));
+        S2 = f2_add(S2, p);
+        T2 = f2_fma(p, f2_pack(fmaxf(d.x, -200.f), fmaxf(d.y, -200.f)), T2);
       }
       if (k > 0 && (end == next_settle || end == last)) {
         settled = settle<kBf16>(sh, src, first, end, k, settled);
@@ -494,10 +560,16 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const LpArgs a)
         }
         next_settle = first + 4 * (next_settle - first);
       }
-      x = next;
+      if constexpr (kVec) {
+        if (++stage == Raw::kStages) stage = 0;
+        if (end < last) x.read(ring + stage * Raw::kStage, end, last, tid);
+      } else {
+        x = next;
+      }
     }
-    S = warp_sum(S);
-    T = warp_sum(T);
+    if constexpr (kVec) cp_async_wait_all();
+    float S = warp_sum(f2_unpack(S2).x + f2_unpack(S2).y);
+    float T = warp_sum(f2_unpack(T2).x + f2_unpack(T2).y);
     if (lane == 0) {
       sh.sum[warp] = S;
       sh.dsum[warp] = T;
@@ -615,6 +687,10 @@ cudaError_t lp_launch(const LpArgs &a, int R, int ctas, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)ctas * (unsigned)R);
   cfg.blockDim = dim3(kLpThreads);
+  if (kVec) {
+    if (!set_smem((const void *)logprobs_kernel<kBf16, kVec>, kLpRing)) return cudaErrorUnknown;
+    cfg.dynamicSmemBytes = kLpRing;
+  }
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

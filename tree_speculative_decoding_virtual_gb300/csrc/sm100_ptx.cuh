@@ -382,6 +382,12 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
+// NaN where an operand is one
+__device__ __forceinline__ float fmax3_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 // 2^x with the hardware approximation (PTX ex2.approx.ftz.f32); ex2(-inf) = 0.
 __device__ __forceinline__ float ex2_approx(float x) {
   float y;
