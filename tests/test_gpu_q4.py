@@ -326,6 +326,13 @@ SHAPES = [
 ]
 
 
+@pytest.fixture(params=[None, 262144], ids=["close", "far"])
+def bound(request):
+    """max_slots: the longest sequence, or far above it.  It decides which kernel
+    runs: with the far one more than 16 rows always are the many-row kernel's."""
+    return request.param
+
+
 @pytest.mark.parametrize("B,N,Hq,Hkv,D,prefix,nodes", SHAPES)
 def test_attention(tsd, B, N, Hq, Hkv, D, prefix, nodes):
     x = _attn_inputs(N * Hq + D, B, N, Hq, Hkv, D, prefix, nodes)
@@ -333,9 +340,12 @@ def test_attention(tsd, B, N, Hq, Hkv, D, prefix, nodes):
     got, lse = _run(tsd, x, status=st)
     _check(x, got, lse, _ref(x))
     assert int(st.item()) == 0
-    # a looser bound on the lengths cuts the keys differently
-    got, lse = _run(tsd, x, max_slots=x["max_slots"] * 7 + 3000)
-    _check(x, got, lse, _ref(x))
+    # a looser bound on the lengths cuts the keys differently, and takes many rows to
+    # the kernel for them
+    for loose in (x["max_slots"] * 7 + 3000, 262144):
+        got, lse = _run(tsd, x, max_slots=loose, status=st)
+        _check(x, got, lse, _ref(x))
+    assert int(st.item()) == 0
 
 
 def _ref_on_gpu(x, chain=False):
@@ -405,6 +415,9 @@ def _long_inputs(seed, B, N, Hq, Hkv, D, prefix, nodes):
     (5, 256, 128, 8, 128, [900, 1, 2000, 127, 128], [256, 255, 129, 1, 128]),
     (70, 1, 4, 1, 128, list(range(1, 1 + 70 * 37, 37)), [1] * 70),
     (66, 20, 4, 2, 64, list(range(5, 5 + 66 * 23, 23)), [20, 7, 1] * 22),
+    (70, 20, 16, 4, 128, list(range(0, 70 * 3, 3)), [20, 7] * 35),  # one piece a range
+    (3, 40, 16, 8, 128, [300, 40, 128], [40, 1, 39]),               # row blocks of 16, in clusters
+    (1, 20, 8, 2, 64, [16000], [20]),
 ])
 def test_attention_long(tsd, B, N, Hq, Hkv, D, prefix, nodes):
     x = _long_inputs(B + N, B, N, Hq, Hkv, D, prefix, nodes)
@@ -446,33 +459,33 @@ def test_attention_repeats_exactly(tsd, B, N, Hq, Hkv, prefix):
 
 @pytest.mark.parametrize("scale", [0.0, -0.3, 1e-30, 3.0])
 @pytest.mark.parametrize("N", [1, 40])
-def test_attention_scale(tsd, N, scale):
+def test_attention_scale(tsd, N, scale, bound):
     x = _attn_inputs(3, 1, N, 2, 1, 128, [150], [N])
     x["scale"] = scale
-    got, lse = _run(tsd, x)
+    got, lse = _run(tsd, x, max_slots=bound)
     _check(x, got, lse, _ref(x))
 
 
 @pytest.mark.parametrize("N,Hq", [(1, 4), (6, 4), (40, 8), (200, 2)])
-def test_attention_chain_mask(tsd, N, Hq):
+def test_attention_chain_mask(tsd, N, Hq, bound):
     x = _attn_inputs(N, 2, N, Hq, 2, 128, [70, 0], [N, max(1, N - 1)])
-    got, lse = _run(tsd, x, mask=None)
+    got, lse = _run(tsd, x, mask=None, max_slots=bound)
     _check(x, got, lse, _ref(x, mask=None))
 
 
 @pytest.mark.parametrize("N,Hq", [(3, 2), (20, 2), (90, 4)])
-def test_attention_rows_that_see_nothing(tsd, N, Hq):
+def test_attention_rows_that_see_nothing(tsd, N, Hq, bound):
     """No prefix and mask rows without a bit: 0 and -inf, whatever the other
     rows see."""
     x = _attn_inputs(N + 3, 2, N, Hq, 2, 64, [0, 40], [N, N])
     x["mask"][:, 1::2] = 0
-    got, lse = _run(tsd, x)
+    got, lse = _run(tsd, x, max_slots=bound)
     _check(x, got, lse, _ref(x))
     assert np.isneginf(lse[0, 1::2]).all() and np.isfinite(lse[1]).all()
 
 
 @pytest.mark.parametrize("N,Hq", [(1, 8), (20, 8), (64, 8)])
-def test_attention_value_ranges(tsd, N, Hq):
+def test_attention_value_ranges(tsd, N, Hq, bound):
     """Rows of q from 2^-130 to 2^100, all zero, and scores that rise along the
     keys so that the reference moves many times."""
     x = _attn_inputs(7 + N, 1, N, Hq, 1, 128, [700], [N])
@@ -489,16 +502,16 @@ def test_attention_value_ranges(tsd, N, Hq):
     rows += (np.arange(700 + N, dtype=np.float32) / 60)[:, None, None]
     slots = [int(x["table"][0, t // 16]) * 16 + t % 16 for t in range(700 + N)]
     x["k"] = oq4.write_rows(x["k"], gen.bf16_bits(rows), slots)
-    got, lse = _run(tsd, x)
+    got, lse = _run(tsd, x, max_slots=bound)
     _check(x, got, lse, _ref(x))
 
 
-def test_attention_nan_query_stays_in_its_row(tsd):
+def test_attention_nan_query_stays_in_its_row(tsd, bound):
     for N in (1, 30, 64):
         x = _attn_inputs(11, 1, N, 4, 1, 128, [50], [N])
         ref = _ref(x)
         x["q"][0, 0, 2, 5] = 0x7FC0
-        got, lse = _run(tsd, x)
+        got, lse = _run(tsd, x, max_slots=bound)
         assert np.isnan(got[0, 0, 2]).all() and np.isnan(lse[0, 0, 2])
         keep = np.ones(lse.shape, bool)
         keep[0, 0, 2] = False
@@ -507,7 +520,7 @@ def test_attention_nan_query_stays_in_its_row(tsd):
 
 
 @pytest.mark.parametrize("N,Hq", [(1, 4), (40, 8), (130, 4)])
-def test_attention_skips_bad_sequences(tsd, N, Hq):
+def test_attention_skips_bad_sequences(tsd, N, Hq, bound):
     """Tree errors, lengths that do not fit and bad block ids: 0 / -inf rows and
     the status bit, the other sequences unharmed."""
     x = _attn_inputs(13 + N, 5, N, Hq, 2, 128, [100, 40, 333, 64, 20], [N] * 5)
@@ -516,7 +529,7 @@ def test_attention_skips_bad_sequences(tsd, N, Hq):
     x["table"][3, 0] = -1
     x["n"][4] = N + 1
     st = status_word()
-    got, lse = _run(tsd, x, status=st)
+    got, lse = _run(tsd, x, max_slots=bound, status=st)
     assert int(st.item()) == tsd.STATUS_BAD_PAGE | tsd.STATUS_BAD_LEN
     y = dict(x, err=np.array([0, 1, 1, 1, 1], np.int32))
     _check(y, got, lse, _ref(y))
@@ -524,19 +537,19 @@ def test_attention_skips_bad_sequences(tsd, N, Hq):
     z = dict(x, err=np.array([0, 1, 1, 1, 1], np.int32), table=x["table"].copy())
     z["table"][0, (100 + N + 15) // 16:] = 10 ** 9
     st.zero_()
-    got, lse = _run(tsd, z, status=st)
+    got, lse = _run(tsd, z, max_slots=bound, status=st)
     assert int(st.item()) == 0
     _check(z, got, lse, _ref(y))
 
 
-def test_attention_is_deterministic_and_capturable(tsd):
+def test_attention_is_deterministic_and_capturable(tsd, bound):
     import torch
     x = _attn_inputs(17, 2, 40, 8, 2, 128, [900, 333], [40, 22])
     a = {k: T(v) for k, v in x.items() if k in ("k", "v", "table", "P", "n", "err")}
     q, m = bf(x["q"]), T(x["mask"].view(np.int32))
 
     def call(stream=None):
-        return tsd.tree_attn_fwd_q4(q, a["k"], a["v"], a["table"], a["P"], a["n"], m, a["err"], x["max_slots"],
+        return tsd.tree_attn_fwd_q4(q, a["k"], a["v"], a["table"], a["P"], a["n"], m, a["err"], bound or x["max_slots"],
                                     stream=stream)
 
     out, lse = call()

@@ -593,9 +593,13 @@ __global__ void __launch_bounds__(256) tree_attn_q4_join_kernel(const Q4Attn p) 
   if (lane == 0 && p.lse) p.lse[orow] = empty ? -INFINITY : (M + log2f(sum)) * kRowsLn2;
 }
 
-// Key ranges of up to this many pages are cut into at most 8 pieces (a
-// cluster) even where more would fill the GPU.
-constexpr int kClusterPages = 512;
+// Key ranges of up to this many pages are the work of one cluster where all clusters
+// run at once: no workspace, and no second launch.  Alone, a cluster is faster up
+// to 16384 keys or so (one token, 8 kv heads, clusters / planned parts: 1024 keys 7.0 /
+// 12.2 us, 4096 9.0 / 13.0, 8192 11.8 / 16.1, 16384 17.9 / 19.1, 32768 28 / 24).  In a
+// batch every cluster has the same number of blocks, and the longest range is what
+// counts: 16 sequences of 4096 keys 22.8 / 25.9 us, of 64 to 8192 keys 41 / 29.
+constexpr int kClusterPages = 1024, kClusterPagesBatch = 288;
 
 struct Q4Shape {
   bool tc;       // the many-row kernel
@@ -605,8 +609,6 @@ struct Q4Shape {
   size_t plan_bytes, ml_bytes, bytes;  // workspace: the plan, (reference, sum) of the partial rows, the rows
 };
 
-// Rows of a kv head from which the many-row kernel runs.
-constexpr int kTcMinRows = 33;
 
 // Fixed cost of a key range, in units of 128 keys of one row tile.  Measured, 16
 // trees of up to 127 nodes over 128 to 8064 slots, many-row kernel: 0: 110 us, 4: 79,
@@ -614,12 +616,20 @@ constexpr int kTcMinRows = 33;
 // 0: 94 us, 2: 83, 4: 76, 5: 75, 8: 77.  Equal long ranges take the same time with any.
 constexpr int kTcRangeCost = 8, kRowsRangeCost = 5;
 
+// The many-row kernel needs some 15 us more to get going, and then takes 128 or 256 rows
+// through a decoded tile where the few-row kernel takes 16: it runs from this much
+// work on, in units of 128 keys of 16 rows and with a range's fixed cost.  Measured, few
+// / many rows (8 kv heads; rows of one, sequences, keys): 32, 1, 2048: 14 / 27 us; 252,
+// 1, 2048: 23 / 30; 32, 8, 1024: 17 / 28; 64, 1, 8192: 27 / 29; 64, 8, 512: 27 / 24;
+// 64, 8, 1024: 32 / 28; 64, 1, 16384: 39 / 31; 32, 32, 8192: 212 / 163.
+constexpr int64_t kTcMinWork = 3000;
+
 // Host: how a call is cut up.
 Q4Shape q4_shape(int B, int N_max, int Hq, int Hkv, int D, int max_slots) {
   Q4Shape pl = {};
   const int rows = N_max * (Hq / Hkv);
-  const int pages = (max_slots + kPage - 1) / kPage;
-  pl.tc = rows >= kTcMinRows;
+  const int pages = (max_slots + kPage - 1) / kPage, units = (pages + kUnitPages - 1) / kUnitPages;
+  pl.tc = rows > 16 && (int64_t)B * Hkv * ((rows + 15) / 16) * (units + kRowsRangeCost) > kTcMinWork;
   pl.nt = rows > 8 ? 2 : 1;
   pl.rows_per_block = pl.tc ? (rows > 128 ? 256 : 128) : 8 * pl.nt;
   pl.row_blocks = (rows + pl.rows_per_block - 1) / pl.rows_per_block;
@@ -627,15 +637,12 @@ Q4Shape q4_shape(int B, int N_max, int Hq, int Hkv, int D, int max_slots) {
   const int slots = (pl.tc ? 1 : 2) * sm_count();
   pl.splits = 1;
   pl.chunk = pages;
-  const int units = (pages + kUnitPages - 1) / kUnitPages;
   // one piece a range: short ranges, or so many that they fill the GPU many times
   if (units <= 2 || base >= 64ll * slots) return pl;
-  if (!pl.tc && pages <= kClusterPages && base < slots) {
-    // Short ranges of few blocks: a cluster of 2, 4 or 8 (a workspace and a second
-    // launch would cost more than the pieces it could add).
-    const int64_t want = std::min<int64_t>((2 * slots + base - 1) / base, (pages + kRowsWarps - 1) / kRowsWarps);
+  if (!pl.tc && pages <= (B == 1 ? kClusterPages : kClusterPagesBatch) && 2 * base <= slots) {
+    // Short ranges of few blocks: a cluster of 2, 4 or 8, as long as all run at once.
     int c = 2;
-    while (c < want && c < 8) c *= 2;
+    while (c < 8 && 2 * c * base <= slots && c < units) c *= 2;
     pl.cluster = true;
     pl.splits = c;
     return pl;

@@ -705,11 +705,13 @@ cudaError_t lp_launch(const LpArgs &a, int R, int ctas, cudaStream_t stream) {
 }
 
 int lp_run(LpArgs &a, int R, int bf16, tsd_stream_t stream) {
-  // CTAs of a row: as many (a power of two, up to 8, at most one a chunk) as let
-  // all rows run at once at four CTAs an SM, because a slice's first chunk and
-  // its end cost more than its stream
+  // CTAs of a row: as many (a power of two, up to 8, at most one a chunk) as leave
+  // no SM with two; a slice's first chunk and its end cost more than sharing saves.
+  // Measured (128256 fp32 logits, 20 best; 1, 2, 4, 8 CTAs): 8 rows 22.6, 17.5, 14.4,
+  // 13.4 us; 38 rows 24.1, 18.3, 16.8, 19.7; 76 rows 24.1, 19.3, 23.6, 29.7; 152 rows
+  // 25.6, 24.4, 34.6; 304 rows 33.3, 37.7.
   int ctas = 1;
-  while (ctas < 8 && (int64_t)ctas * kChunk < a.V && 2ll * ctas * R <= 4ll * sm_count()) ctas *= 2;
+  while (ctas < 8 && (int64_t)ctas * kChunk < a.V && 2ll * ctas * R <= sm_count()) ctas *= 2;
   a.per = ((a.V + ctas - 1) / ctas + 7) / 8 * 8;
   const bool vec = aligned(a.logits, 16) && a.V % (bf16 ? 8 : 4) == 0;
   const cudaStream_t s = as_cuda(stream);

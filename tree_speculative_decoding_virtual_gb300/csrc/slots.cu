@@ -26,7 +26,10 @@ namespace {
 constexpr int kScanThreads = 1024;
 constexpr int kFillThreads = 256;
 constexpr int kFillTokens = 4 * kFillThreads;  // tokens one fill block maps
-// Calls of at most this many sequences and tokens run in one block, one launch.
+// Calls of at most this many sequences and tokens run in one block: one launch, and
+// no workspace.  Measured on the device, one block / two kernels: 64 tokens 2.8 / 3.6
+// us, 2048 3.0 / 3.6, 8192 4.4 / 3.6 (less than a launch and a workspace cost the
+// host), 32768 9.9 / 3.6.
 constexpr int kSmallSeqs = 64;
 constexpr int kSmallTokens = 8192;
 
