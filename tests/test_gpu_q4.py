@@ -114,6 +114,25 @@ def test_write_every_tie_and_special(tsd):
     assert int(st.item()) == tsd.STATUS_NONFINITE
 
 
+@pytest.mark.parametrize("amax", [6e-6, 3e-5, 3.7e-4, 0.011, 1.0, 5.8125, 100.0, 61440.0, 3e38])
+def test_write_every_bf16(tsd, amax):
+    """Groups of one largest value and 15 others, which together are every bf16
+    value up to it, both signs and zeros."""
+    top = int(gen.bf16_bits(np.array([amax], np.float32))[0])
+    vals = np.concatenate([np.arange(top + 1), np.arange(top + 1) | 0x8000]).astype(np.uint16)
+    vals = np.concatenate([vals, np.zeros(-len(vals) % (15 * 64), np.uint16)]).reshape(-1, 15)
+    x = np.concatenate([np.full((len(vals), 1), top, np.uint16), vals], 1).reshape(-1, 8, 128)
+    slots = np.arange(len(x), dtype=np.int32)
+    pool = np.zeros(((len(x) + 15) // 16, 8, 9 * 128), np.uint8)
+    kc, vc = T(pool), T(pool)
+    flipped = x ^ 0x8000
+    st = status_word()
+    tsd.kv_write_q4(bf(x), bf(flipped), T(slots), kc, vc, status=st)
+    assert np.array_equal(np_of(kc), oq4.write_rows(pool, x, slots))
+    assert np.array_equal(np_of(vc), oq4.write_rows(pool, flipped, slots))
+    assert int(st.item()) == 0
+
+
 def test_write_strided_and_bad_slots(tsd):
     import torch
     rng = np.random.default_rng(5)

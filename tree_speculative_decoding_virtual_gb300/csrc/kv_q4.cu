@@ -1,13 +1,19 @@
 // The 4-bit paged cache: its writer, its reader and the commit of an accepted
 // path (format: q4.cuh).
 //
-// All three move a few bytes per value and compute next to nothing, so they
-// are bound by HBM for prompts and by launch latency for a step's tree.
+// All three move a few bytes per value.  For a step's tree they are bound by launch
+// latency.  For prompts the reader and the commit are bound by HBM; the writer by the
+// pipe of the integer and conversion instructions (32768 tokens, 8 heads of 128: 35
+// us for 172 MB, that pipe 70% busy; the reader of the same 30 us), which is why its
+// two lanes of a group share the scales' computation (one K's, one V's), quotients
+// are rounded by packed fp32 sums, and item positions are counted, not divided for:
+// 47 us without these.
 
 #include <cuda_bf16.h>
 
 #include "commit_core.cuh"
 #include "q4.cuh"
+#include "sm100_ptx.cuh"
 #include "tsd_common.cuh"
 
 namespace tsd {
@@ -20,46 +26,45 @@ constexpr int kRowThreads = 256;
 constexpr int kLaneValues = 8;
 constexpr int kBlockItems = 4 * kRowThreads;  // lanes' worth of work of a block
 
-// A quotient x / s rounded to 16 significant bits, from a reciprocal of s that is
-// off by at most 2^-24.  The product is then off by less than 2^-22, so a true
-// quotient with at most 16 significant bits (a tie in particular) comes out
-// exact.
-__device__ __forceinline__ float near_quotient(float x, float recip) {
-  const float y = x * recip;
-  return __uint_as_float((__float_as_uint(y) + 0x80u) & 0xFFFFFF00u);
-}
-
-// Eight bf16 values -> four code bytes and the group's scale byte; `lane ^ 1`
-// holds the group's other half.
+// Quantisation of a group of 16 values:
 //   scale = nearest (ties to even) to amax / 6, at most 10240;
 //   code  = nearest (ties to even) to x / scale.
-// amax and x have 8 significant bits and every rounding boundary (times 6, or
-// times the scale) at most 7, so a quotient that is not a tie differs from
-// the boundary by 2^-9 relative or more: deciding on the quotient rounded to
-// 16 bits gives the decision of exact arithmetic.  NaN counts as 0 and an
-// infinity as the largest value; both are reported.
-__device__ __forceinline__ uint32_t q4_encode(uint4 in, uint32_t &scale_byte, bool &odd) {
-  float x[8];
-  const uint32_t w[4] = {in.x, in.y, in.z, in.w};
-  float amax = 0.f;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(x[i]));  // (drops NaN)
-  bool finite = amax < INFINITY;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) finite = finite && x[i] == x[i];
-  if (!finite) {
+// amax and x have 8 significant bits and every rounding boundary (times 6, or times
+// the scale) at most 7, so a quotient that is not a tie differs from the boundary by
+// 2^-9 relative or more: a quotient that is off by 2^-20 and then rounded to 16 bits,
+// or to multiples of 2^-14 where the boundaries are multiples of 1/4, gives the
+// decision of exact arithmetic.  NaN counts as 0 and an infinity as the largest
+// value; both are reported.
+
+// The largest magnitude of eight bf16 values, as the bits of a float; NaN becomes 0.
+__device__ __forceinline__ uint32_t q4_amax(uint4 &in, bool &odd) {
+  uint32_t w[4] = {in.x, in.y, in.z, in.w};
+  // bf16 magnitudes order as integers, infinity and then NaN above the others
+  auto largest = [&]() {
+    const uint32_t m = __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu),
+                                __vmaxu2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
+    return max(m << 16, m & 0xFFFF0000u);
+  };
+  uint32_t most = largest();
+  if (most >= 0x7F800000u) {
     odd = true;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      x[i] = x[i] != x[i] ? 0.f : fminf(fmaxf(x[i], -3e38f), 3e38f);
+    for (int i = 0; i < 4; ++i) {
+      if ((w[i] & 0x7FFFu) > 0x7F80u) w[i] &= 0xFFFF0000u;
+      if ((w[i] & 0x7FFF0000u) > 0x7F800000u) w[i] &= 0xFFFFu;
+    }
+    most = largest();
+    in = make_uint4(w[0], w[1], w[2], w[3]);
   }
-  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-  const float r = near_quotient(fminf(amax, 61440.f), 0x1.555556p-3f);
+  return most;
+}
+
+// The scale byte of a group, and the reciprocal of its scale to 2^-23.  (1 for the
+// scale 0: the group's values are below 2^-15 then, which makes every code 0.)
+__device__ __forceinline__ uint32_t q4_group_scale(float amax, float &recip) {
+  // amax / 6 to 16 bits
+  const float y = fminf(amax, 61440.f) * 0x1.555556p-3f;
+  const float r = __uint_as_float((__float_as_uint(y) + 0x80u) & 0xFFFFFF00u);
   uint32_t byte;
   if (r < 6.103515625e-05f) {  // below 2^-14: steps of 2^-17
     byte = (uint32_t)rintf(r * 131072.f);
@@ -68,19 +73,45 @@ __device__ __forceinline__ uint32_t q4_encode(uint4 in, uint32_t &scale_byte, bo
     u += 0x7FFFFu + ((u >> 20) & 1u);
     byte = (u >> 20) - (112u << 3);
   }
-  scale_byte = byte;
   const float scale =
       byte < 8 ? (float)byte * 7.62939453125e-06f : __uint_as_float((byte + (112u << 3)) << 20);
-  const float recip = byte ? __frcp_rn(scale) : 0.f;
-  uint32_t code = 0u;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(recip) : "f"(scale));
+  if (byte == 0u) recip = 1.f;
+  return byte;
+}
+
+// Rounds down: a - a is -0.
+__device__ __forceinline__ unsigned long long f2_add_down(unsigned long long a, unsigned long long b) {
+  unsigned long long r;
+  asm("add.rm.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// Eight values -> four code bytes.
+__device__ __forceinline__ uint32_t q4_codes(uint4 in, float recip) {
+  using namespace sm100;
+  const uint32_t w[4] = {in.x, in.y, in.z, in.w};
+  // x / scale to a multiple of 2^-14, the sum's last place; then 2^-30 of the quotient,
+  // which is lost unless that was 0 and then keeps the sign of x.  (The difference is
+  // exact; a zero of it is -0, so that -0 x stays -0.)
+  constexpr float kGrid = 768.f;  // 1.5 * 2^9
+  const unsigned long long recip2 = f2_pack(recip, recip), up = f2_pack(kGrid, kGrid),
+                           down = f2_pack(-kGrid, -kGrid),
+                           trace = f2_pack(recip * 0x1p-30f, recip * 0x1p-30f);
+  float z[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    uint16_t two;  // the first source of the conversion goes to the high nibble
-    asm("{\n .reg .b8 t;\n cvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n cvt.u16.u8 %0, t;\n}\n"
-        : "=h"(two)
-        : "f"(near_quotient(x[2 * i + 1], recip)), "f"(near_quotient(x[2 * i], recip)));
-    code |= (uint32_t)two << (8 * i);
+    const unsigned long long x = f2_pack(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+    const float2 y = f2_unpack(f2_fma(x, trace, f2_add_down(f2_fma(x, recip2, up), down)));
+    z[2 * i] = y.x;
+    z[2 * i + 1] = y.y;
   }
+  uint32_t code;  // (a conversion's first source goes to the high nibble)
+  asm("{\n .reg .b8 a, b, c, d;\n cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n mov.b32 %0, {a, b, c, d};\n}\n"
+      : "=r"(code)
+      : "f"(z[0]), "f"(z[1]), "f"(z[2]), "f"(z[3]), "f"(z[4]), "f"(z[5]), "f"(z[6]), "f"(z[7]));
   return code;
 }
 
@@ -111,10 +142,12 @@ kv_write_q4_kernel(const RowArgs a, const uint16_t *__restrict__ k, int64_t k_st
   const int per = a.Hkv * kLanes;
   const int64_t t0 = (int64_t)blockIdx.x * a.tokens;
   const int items = (int)min((int64_t)a.tokens, a.T - t0) * per;
+  const int step_t = kRowThreads / per, step_c = kRowThreads % per;
+  int tl = threadIdx.x / per, c = threadIdx.x % per;  // of item x: token, lane of its row
+  const bool second = threadIdx.x & 1;  // of the two lanes of a group
   // (whole warps: a lane past the end encodes zeros for its partner's sake)
 #pragma unroll 2
   for (int x = threadIdx.x; x < (items + 31) / 32 * 32; x += kRowThreads) {
-    const int tl = min(x, items - 1) / per, c = min(x, items - 1) - tl * per;
     const int64_t t = t0 + tl;
     const int slot = x < items ? row_slot(a, t, c == 0) : -1;
     uint4 kin = make_uint4(0u, 0u, 0u, 0u), vin = kin;
@@ -123,19 +156,28 @@ kv_write_q4_kernel(const RowArgs a, const uint16_t *__restrict__ k, int64_t k_st
       vin = __ldcs(reinterpret_cast<const uint4 *>(v + t * v_stride + c * kLaneValues));
     }
     bool odd = false;
-    uint32_t sk, sv;
-    const uint32_t ck = q4_encode(kin, sk, odd), cv = q4_encode(vin, sv, odd);
-    if (slot < 0) continue;
-    const int h = c / kLanes, i = c % kLanes;
-    const size_t page = ((size_t)(slot / kPage) * a.Hkv + h) * L::kBytes;
-    const int row = slot % kPage;
-    *reinterpret_cast<uint32_t *>(kc + page + row * L::kRow + i * 4) = ck;
-    *reinterpret_cast<uint32_t *>(vc + page + row * L::kRow + i * 4) = cv;
-    if ((i & 1) == 0) {
-      kc[page + L::kScales + row * L::kScaleRow + i / 2] = (uint8_t)sk;
-      vc[page + L::kScales + row * L::kScaleRow + i / 2] = (uint8_t)sv;
+    const uint32_t k_most = q4_amax(kin, odd), v_most = q4_amax(vin, odd);
+    // the group's first lane finds K's scale, the second V's
+    const uint32_t theirs = __shfl_xor_sync(0xffffffffu, second ? k_most : v_most, 1);
+    float recip;
+    const uint32_t byte = q4_group_scale(__uint_as_float(max(second ? v_most : k_most, theirs)), recip);
+    const float other = __shfl_xor_sync(0xffffffffu, recip, 1);
+    const uint32_t ck = q4_codes(kin, second ? other : recip), cv = q4_codes(vin, second ? recip : other);
+    if (slot >= 0) {
+      const int h = c / kLanes, i = c % kLanes;
+      const size_t page = ((size_t)(slot / kPage) * a.Hkv + h) * L::kBytes;
+      const int row = slot % kPage;
+      *reinterpret_cast<uint32_t *>(kc + page + row * L::kRow + i * 4) = ck;
+      *reinterpret_cast<uint32_t *>(vc + page + row * L::kRow + i * 4) = cv;
+      (second ? vc : kc)[page + L::kScales + row * L::kScaleRow + i / 2] = (uint8_t)byte;
+      if (odd && a.status) atomicOr(a.status, TSD_STATUS_NONFINITE);
     }
-    if (odd && a.status) atomicOr(a.status, TSD_STATUS_NONFINITE);
+    tl += step_t;
+    c += step_c;
+    if (c >= per) {
+      c -= per;
+      ++tl;
+    }
   }
 }
 
@@ -165,9 +207,10 @@ kv_read_q4_kernel(const RowArgs a, const uint8_t *__restrict__ kc, const uint8_t
   const int per = a.Hkv * kLanes;
   const int64_t t0 = (int64_t)blockIdx.x * a.tokens;
   const int items = (int)min((int64_t)a.tokens, a.T - t0) * per;
+  const int step_t = kRowThreads / per, step_c = kRowThreads % per;
+  int tl = threadIdx.x / per, c = threadIdx.x % per;  // of item x: token, lane of its row
 #pragma unroll 4
   for (int x = threadIdx.x; x < items; x += kRowThreads) {
-    const int tl = x / per, c = x - tl * per;
     const int64_t t = t0 + tl;
     const int slot = row_slot(a, t, c == 0);
     uint32_t ck = 0, cv = 0, sk = 0, sv = 0;
@@ -183,6 +226,12 @@ kv_read_q4_kernel(const RowArgs a, const uint8_t *__restrict__ kc, const uint8_t
     const size_t at = (size_t)t * per + c;
     __stcs(reinterpret_cast<uint4 *>(k) + at, q4_values(ck, sk));
     __stcs(reinterpret_cast<uint4 *>(v) + at, q4_values(cv, sv));
+    tl += step_t;
+    c += step_c;
+    if (c >= per) {
+      c -= per;
+      ++tl;
+    }
   }
 }
 
