@@ -631,7 +631,9 @@ int tsd_kv_blocks_release(const int32_t *keep_len, int B, int32_t *block_table, 
  *   code:  E2M1 (sign, two exponent bits, one fraction bit): the magnitudes
  *          0, 0.5, 1, 1.5, 2, 3, 4, 6;
  *   scale: five exponent and three fraction bits, no sign: the half-precision
- *          number with bits byte << 7; bytes above 0xE2 (10240) read as 0xE2.
+ *          number with bits byte << 7.  No writer makes a byte above 0xE2
+ *          (10240): tsd_kv_read_q4 reads one as 0xE2, and the attention may
+ *          meet one only in slots that were not written, which no row sees.
  * value = code * scale, exact in fp16 and bf16; 4.5 bits a value.  The block
  * table, slot and limit conventions are those of the bf16 cache.
  *
@@ -674,8 +676,13 @@ int tsd_kv_commit_path_q4(uint8_t *k_cache, uint8_t *v_cache, int num_layers, in
  * to bf16.  A sequence is skipped when a block id in its key range is bad.
  * Unlike tsd_tree_attn_fwd, it reads nothing before the previous kernel on the
  * stream has finished.
- * workspace >= tsd_tree_attn_q4_workspace_bytes() (fp32 split partials; no
- * initial contents; may be NULL when that is 0).
+ * workspace >= tsd_tree_attn_q4_workspace_bytes() (fp32 split partials and the
+ * plan of the call; no initial contents; may be NULL when that is 0), 16-byte
+ * aligned; calls that may run at the same time need workspaces of their own.
+ * One launch where that is 0 (short ranges, or one piece a range), else two: up
+ * to 64 sequences are cut into equal parts of their actual lengths on the device,
+ * larger batches into pieces of max_slots.  max_slots and the shapes alone decide
+ * which kernels run, so a call can be captured once and replayed with other lengths.
  */
 size_t tsd_tree_attn_q4_workspace_bytes(int B, int N_max, int Hq, int Hkv, int D, int max_slots);
 int tsd_tree_attn_fwd_q4(const uint16_t *q, const uint8_t *k_cache, const uint8_t *v_cache,

@@ -33,7 +33,16 @@
 // page's keys over the A rows (i ^ (i >> 1 & 1)) makes the K reads free of
 // bank conflicts and the V reads two-way.
 //
-// Splits of the key range are merged by a second kernel in fp32.
+// Cutting up the key ranges: one cluster a range, equal parts of all ranges end to
+// end (attention_q4.cuh), or, for batches beyond a plan, uniform pieces; partial rows are
+// joined in fp32, in shared memory or by a second kernel.
+//
+// Measured (device time): one token behind 4096 keys, 32 query and 8 kv heads of 128: 9 us; 32
+// tokens behind 512 to 16384 keys, 64 / 8 heads: 75 us for 312 MB (62% of the copy
+// bandwidth).  There it takes about 350 instructions a page and warp at 0.6 a cycle and
+// scheduler: the copies alone take 56 us, the arithmetic alone 66.  Ten warps a block
+// (96 registers) took 80 us, three blocks an SM (80 registers) 125, the next page's
+// scores ahead of this page's products 77, a ring of five pages 76.
 
 #include <cuda_bf16.h>
 

@@ -2,16 +2,25 @@
 // 5th-generation tensor cores (tcgen05).  The few-row kernel, the format and
 // the precision choices are described in attention_q4.cu and q4.cuh.
 //
-// One block = 128 or 256 query rows of one kv head x one piece of the key
-// range, walked in 128-key tiles (8 pages).  Decoding costs a fixed number of
-// instructions per key, so the more rows share a decoded tile the better; from
-// about 64 rows on the kernel is bound by the tensor cores and the softmax.
-//   warp 0       block ids, and the pages' copies into a ring of packed tiles
+// One block = 128 or 256 query rows of one kv head x a run of key-range segments (a
+// part of the plan, attention_q4.cuh), each walked in 128-key tiles (8 pages).
+// Decoding costs a fixed number of instructions per key, so the more rows share a
+// decoded tile the better.
+//   warps 0, 3   block ids, and the copies of K's and of V's pages into rings of packed
+//                half tiles
 //   warp 1       owns TMEM; lane 0 issues every MMA
 //   warp 2       tells it when the decoded tiles are there
 //   warps 4-7    decode packed tiles to fp16 K and V tiles (128-byte swizzle)
 //   warps 8-15   softmax of chain 0, warps 16-23 of chain 1: one TMEM lane (=
 //                one query row) per thread, two threads a row (64 keys each)
+// Measured (device time): 4 trees of 127 nodes behind 32768 keys, 64 query and 8 kv heads of
+// 128: 434 us, 1260 TFLOP/s (67% of the measured bf16 rate; 2900 cycles for the 32 MMAs
+// of a tile, 80 each, and their two commits); 16 trees of 16 to 31 nodes behind 512 to 8192
+// keys, 32 / 8 heads: 68 us.  There a tile has 16 MMAs and takes 2700 cycles: the
+// chain from a tile's S through the release of its stage, the decoding of the tile
+// two further (some 2000 cycles for a pair of warps), its hand-over and its MMAs. Four
+// warps for K and four for V (896 threads, smaller register shares) took as long,
+// decoding a half tile ahead in registers 73 us.
 // A chain is a row tile of 128 rows with its S (128 columns of TMEM, P over
 // the first 64) and O.  With more than 128 rows the two chains are two row
 // tiles that share every key tile; with fewer, chain c takes the key tiles j =

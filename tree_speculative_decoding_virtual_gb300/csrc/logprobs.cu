@@ -99,6 +99,17 @@ __device__ __forceinline__ unsigned long long lp_key(uint32_t ord, int id) {
   return ((unsigned long long)ord << 32) | (uint32_t)~id;
 }
 
+__device__ __forceinline__ unsigned long long f2_mul(unsigned long long a, unsigned long long b) {
+  unsigned long long r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// NaN where an operand is one
+__device__ __forceinline__ float fmax3_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 __device__ __forceinline__ float warp_sum(float x) {
 #pragma unroll
   for (int off = 16; off; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);

@@ -8,8 +8,9 @@
 //          are 0, 0.5, 1, 1.5, 2, 3, 4, 6.
 //   scale  five exponent and three fraction bits, no sign (a scale is never
 //          negative): the half-precision number whose bits are byte << 7.
-//          Bytes above kQ4MaxScale (10240) read as kQ4MaxScale, so every
-//          value read from a page is finite, whatever the page holds.
+//          No writer makes a byte above kQ4MaxScale (10240).  Where a page may
+//          hold slots that were not written, its bytes are read as at most that,
+//          so that a value is finite whatever the page holds.
 // A value is code * scale: at most six significant bits and between 2^-18
 // and 61440 in magnitude, so it is exact in fp16 (and bf16), which is what
 // lets the attention decode straight to fp16 MMA operands without rounding.

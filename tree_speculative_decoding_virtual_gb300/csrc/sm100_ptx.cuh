@@ -362,11 +362,6 @@ __device__ __forceinline__ unsigned long long f2_add(unsigned long long a, unsig
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-__device__ __forceinline__ unsigned long long f2_mul(unsigned long long a, unsigned long long b) {
-  unsigned long long r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 // acc_lo += the low bf16 of w and acc_hi += the high one: each is widened to
 // fp32 exactly and added with round-to-nearest (PTX mixed-precision add), so
 // no shift or mask is needed to unpack the pair.
@@ -380,12 +375,6 @@ __device__ __forceinline__ void add_bf16x2(float &acc_lo, float &acc_hi, uint32_
 __device__ __forceinline__ float fmax3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-// NaN where an operand is one
-__device__ __forceinline__ float fmax3_nan(float a, float b, float c) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
 // 2^x with the hardware approximation (PTX ex2.approx.ftz.f32); ex2(-inf) = 0.
