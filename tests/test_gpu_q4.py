@@ -591,6 +591,30 @@ def test_attention_is_deterministic_and_capturable(tsd, bound):
         assert torch.equal(out, o5) and torch.equal(lse, l5)
 
 
+@pytest.mark.parametrize("B,N,Hq,prefix", [(6, 100, 32, [2000, 130, 900, 4000, 17, 1200]),
+                                           (16, 31, 32, list(range(64, 64 + 16 * 190, 190)))])
+def test_attention_wait_limit(tsd, B, N, Hq, prefix):
+    """A wait of the many-row kernel that runs out: the status says so, the kernel
+    returns, and the next call is right."""
+    import torch
+    x = _long_inputs(B, B, N, Hq, 8, 128, prefix, [N] * B)
+    st = status_word()
+    old = tsd.get_option(tsd.OPT_WAIT_LIMIT_NS)
+    try:
+        tsd.set_option(tsd.OPT_WAIT_LIMIT_NS, 1_000_000)
+        tsd.set_option(tsd.OPT_TEST_STALL, 1)
+        _run(tsd, x, status=st)
+        torch.cuda.synchronize()
+    finally:
+        tsd.set_option(tsd.OPT_TEST_STALL, 0)
+        tsd.set_option(tsd.OPT_WAIT_LIMIT_NS, old)
+    assert int(st.item()) == tsd.STATUS_TIMEOUT
+    st.zero_()
+    got, lse = _run(tsd, x, status=st)
+    assert int(st.item()) == 0
+    _check(x, got, lse, _ref_on_gpu(x))
+
+
 # ---------------------------------------------------------------------------
 # commit
 # ---------------------------------------------------------------------------

@@ -777,6 +777,7 @@ TSD_API int tsd_tree_attn_fwd_q4(const uint16_t *q, const uint8_t *k_cache, cons
   p.lse = lse;
   p.status = status;
   p.wait_limit_ns = (uint64_t)option(TSD_OPT_WAIT_LIMIT_NS);
+  p.test_stall = (int)option(TSD_OPT_TEST_STALL);
   const cudaStream_t s = as_cuda(stream);
   cudaError_t e;
   if (pl.tc)

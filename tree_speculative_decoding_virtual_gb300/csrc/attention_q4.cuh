@@ -33,6 +33,7 @@ struct Q4Attn {
   float *lse;
   int32_t *status;
   uint64_t wait_limit_ns;
+  int test_stall;  // the many-row kernel waits for a barrier that nothing signals
 };
 
 // Lengths of sequence b; false when it is skipped (and then `bad` says whether

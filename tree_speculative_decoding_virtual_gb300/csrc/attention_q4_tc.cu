@@ -85,7 +85,7 @@ struct TcLayout {
   }
 };
 
-constexpr int kTcBarriers = 4 * kPackMost + 16;
+constexpr int kTcBarriers = 4 * kPackMost + 17;
 
 struct TcSeg {
   Q4Seg s;
@@ -98,7 +98,8 @@ struct TcSeg {
 struct TcShared {
   uint64_t pk_full[2][kPackMost], pk_empty[2][kPackMost];  // K, V
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
-  uint64_t s_full[2], p_full[2], o_final[2], q_full, drain;  // (kTcBarriers in all, in the order tc_segment counts on)
+  uint64_t s_full[2], p_full[2], o_final[2], q_full, drain;
+  uint64_t never;  // (kTcBarriers in all, in the order tc_segment counts on)
   float2 ml[kBM];           // chain 1's (reference, sum) when it shares chain 0's rows
   float half[2][2][kBM];    // by chain, thread of the row, row: exchange between the two
   uint8_t asks[2][2][kBM];  // likewise
@@ -232,7 +233,7 @@ __device__ __forceinline__ bool tc_segment(const Q4Attn &p, TcShared &sh, bool f
     if (sg.more) {
       sg.n = (sg.s.last - sg.s.first + kTilePages - 1) / kTilePages;
       sg.two = sg.s.rb * p.rows_per_block + kBM < sg.s.nb * p.g && p.rows_per_block > kBM;
-      // the barriers lie one after the other, from pk_full to drain
+      // the barriers lie one after the other, from pk_full to never
       for (int i = tid; i < kTcBarriers; i += 32) {
         const uint32_t bar = smem_addr(&sh.pk_full[0][0] + i);
         const int k = i - 4 * kPackMost;  // the barriers behind the rings'
@@ -399,7 +400,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4
         // one for P: warp 2 adds to that barrier once V_j and the next K are there.
         // (With waits of its own for them it lost 200 to 500 cycles each, behind
         // the shared-memory traffic of the other warps.)
-        bool ok = tc_wait(sh.q_full, 0, lim, abort);
+        bool ok = !p.test_stall || tc_wait(sh.never, 0, lim, abort);
+        ok = ok && tc_wait(sh.q_full, 0, lim, abort);
         ok = ok && tc_wait(sh.k_full[0], 0, lim, abort);
         if (ok) issue_s(0, 0, 0);
         if (chains == 2) {
