@@ -161,7 +161,7 @@ def test_write_strided_and_bad_slots(tsd):
 # ---------------------------------------------------------------------------
 
 
-@pytest.mark.parametrize("B,N,P_max", [(1, 1, 0), (1, 63, 4096), (3, 7, 50), (64, 31, 300), (65, 31, 300), (64, 128, 90),
+@pytest.mark.parametrize("B,N,P_max", [(1, 1, 0), (1, 63, 4096), (3, 7, 50), (64, 31, 300), (65, 31, 300), (64, 128, 90), (3, 2001, 5000), (64, 700, 900), (1, 8192, 100), (2, 4099, 40),
                                        (5, 4097, 2000), (1500, 3, 60), (2, 0, 70), (300, 37, 0)])
 @pytest.mark.parametrize("tight", [False, True])
 def test_slots_build_and_release(tsd, B, N, P_max, tight):

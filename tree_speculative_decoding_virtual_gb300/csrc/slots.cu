@@ -18,6 +18,7 @@
 // batch is one block's, and the map (4 bytes a token) is written by a second
 // grid, or by the same block when it is small.
 
+#include "sm100_ptx.cuh"
 #include "tsd_common.cuh"
 
 namespace tsd {
@@ -40,6 +41,8 @@ struct SlotWork {
   int64_t *start;  // [B]
   int32_t *held;   // [B]
   int32_t *count;  // [1]: free blocks before the call
+  int32_t *after;  // [B + 1] or null: blocks held and free blocks after it, for whoever
+                   // stores them; null: the scan does
 };
 
 __host__ __device__ inline size_t slot_ws_bytes(int B) {
@@ -50,6 +53,7 @@ __host__ __device__ inline SlotWork slot_ws(void *ws, int B) {
   w.start = reinterpret_cast<int64_t *>(ws);
   w.held = reinterpret_cast<int32_t *>(w.start + B);
   w.count = w.held + B;
+  w.after = nullptr;
   return w;
 }
 
@@ -108,9 +112,10 @@ __device__ __forceinline__ int64_t seq_blocks(const SlotArgs &a, int b, int held
   return d > 0 ? d : 0;
 }
 
-// The scan, by one block: fills `w`, updates held and free_count.
+// The scan, by one block: fills `w`, updates held and free_count.  `report`: this
+// block tells the status.
 template <bool kTake>
-__device__ void scan_sequences(const SlotArgs &a, const SlotWork &w) {
+__device__ void scan_sequences(const SlotArgs &a, const SlotWork &w, bool report = true) {
   __shared__ int64_t warp_sums[32];
   __shared__ int s_served_end;  // blocks taken by the sequences that were served
   const int count = *a.free_count;
@@ -148,7 +153,7 @@ __device__ void scan_sequences(const SlotArgs &a, const SlotWork &w) {
       if (d > 0) {
         served = move && (!kTake || start + d <= count);
         if (served) {
-          a.held[b] = kTake ? held + (int)d : held - (int)d;
+          if (!w.after) a.held[b] = kTake ? held + (int)d : held - (int)d;
           if (kTake) atomicMax(&s_served_end, (int)(start + d));
         } else if (kTake && count_ok) {
           bad |= TSD_STATUS_NO_BLOCK;
@@ -156,13 +161,18 @@ __device__ void scan_sequences(const SlotArgs &a, const SlotWork &w) {
       }
       w.start[b] = served ? start : -1;
       w.held[b] = held;
+      if (w.after) w.after[b] = !served ? held : kTake ? held + (int)d : held - (int)d;
     }
   }
-  if (bad && a.status) atomicOr(a.status, bad);
+  if (report && bad && a.status) atomicOr(a.status, bad);
   __syncthreads();
   if (threadIdx.x == 0) {
     *w.count = count;
-    if (move) *a.free_count = kTake ? count - s_served_end : count + (int)all;
+    const int left = !move ? count : kTake ? count - s_served_end : count + (int)all;
+    if (w.after)
+      w.after[a.B] = left;
+    else if (move)
+      *a.free_count = left;
   }
 }
 
@@ -219,13 +229,13 @@ __device__ __forceinline__ void fill_sequence(const SlotArgs &a, int b, int64_t 
   if (bad && a.status) atomicOr(a.status, TSD_STATUS_BAD_PAGE);
 }
 
-// Gives blocks [held - d, held) of sequence b back and clears their entries.
-__device__ __forceinline__ void release_sequence(const SlotArgs &a, int b, int64_t start, int held,
-                                                 int count, int worker, int workers) {
-  const int keep = a.held[b];  // already lowered by the scan
+// Gives blocks [keep, held) of sequence b back and clears their entries; `after`: free
+// blocks when the call is done.
+__device__ __forceinline__ void release_sequence(const SlotArgs &a, int b, int64_t start, int keep,
+                                                 int held, int worker, int workers, int after) {
   if (start < 0) return;
-  // the call's last given-back block is number all - 1 and lands at `count`
-  const int top = *a.free_count - 1;
+  // the call's last given-back block is number all - 1 and lands at the old count
+  const int top = after - 1;
   for (int j = keep + worker; j < held; j += workers) {
     int32_t *e = a.table + (size_t)b * a.max_blocks + j;
     a.free_list[top - (start + (j - keep))] = *e;
@@ -233,30 +243,46 @@ __device__ __forceinline__ void release_sequence(const SlotArgs &a, int b, int64
   }
 }
 
-// Everything in one block: small calls.
-template <bool kTake>
-__global__ void __launch_bounds__(kScanThreads) slots_small_kernel(const SlotArgs a) {
+// Taking, small calls: everything in one block.
+__global__ void __launch_bounds__(kScanThreads) slots_take_kernel(const SlotArgs a) {
   __shared__ int64_t s_start[kSmallSeqs];
   __shared__ int32_t s_held[kSmallSeqs], s_count;
   pdl_wait();
-  SlotWork w;
-  w.start = s_start;
-  w.held = s_held;
-  w.count = &s_count;
-  scan_sequences<kTake>(a, w);
+  scan_sequences<true>(a, SlotWork{s_start, s_held, &s_count, nullptr});
   __syncthreads();
-  if (kTake) {
-    // every thread takes four tokens of one sequence at a time
-    const int per = (a.N_max + 3) / 4;  // quads of one sequence
-    const int q = max(per, 1);
-    for (int x = threadIdx.x; x < a.B * q; x += blockDim.x) {
-      const int b = x / q, i = (x % q) * 4;
-      fill_sequence(a, b, s_start[b], s_held[b], s_count, i, max(a.N_max, 1), x % q, q);
-    }
-  } else {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int b = warp; b < a.B; b += blockDim.x >> 5)
-      release_sequence(a, b, s_start[b], s_held[b], s_count, lane, 32);
+  // every thread takes four tokens of one sequence at a time
+  const int q = max((a.N_max + 3) / 4, 1);  // quads of one sequence
+  for (int x = threadIdx.x; x < a.B * q; x += blockDim.x) {
+    const int b = x / q, i = (x % q) * 4;
+    fill_sequence(a, b, s_start[b], s_held[b], s_count, i, max(a.N_max, 1), x % q, q);
+  }
+}
+
+// Giving back, up to kSmallSeqs sequences: a cluster, whose blocks all make the scan.
+// The first stores what it found once all have read what was there.  (How many
+// blocks come back is known on the device only; with one block 32768 of them took 10
+// us, with eight 3.)
+__global__ void __launch_bounds__(kScanThreads) slots_release_kernel(const SlotArgs a) {
+  using namespace sm100;
+  __shared__ int64_t s_start[kSmallSeqs];
+  __shared__ int32_t s_held[kSmallSeqs], s_count, s_after[kSmallSeqs + 1];
+  pdl_wait();
+  const int rank = cluster_ctarank(), ctas = cluster_nctarank();
+  scan_sequences<false>(a, SlotWork{s_start, s_held, &s_count, s_after}, rank == 0);
+  __syncthreads();
+  if (ctas > 1) {
+    cluster_arrive();
+    cluster_wait();
+  }
+  if (rank == 0 && threadIdx.x < a.B && s_after[threadIdx.x] != s_held[threadIdx.x])
+    a.held[threadIdx.x] = s_after[threadIdx.x];
+  if (rank == 0 && threadIdx.x == 0 && s_after[a.B] != s_count) *a.free_count = s_after[a.B];
+  // the warps are dealt out over the sequences
+  const int warps = ctas * (kScanThreads / 32), each = max(warps / a.B, 1);
+  for (int x = rank * (kScanThreads / 32) + (threadIdx.x >> 5); x < a.B * each; x += warps) {
+    const int b = x / each;
+    release_sequence(a, b, s_start[b], s_after[b], s_held[b], (x - b * each) * 32 + (threadIdx.x & 31), each * 32,
+                     s_after[a.B]);
   }
 }
 
@@ -275,17 +301,35 @@ __global__ void __launch_bounds__(kFillThreads) slots_fill_kernel(const SlotArgs
     if (kTake)
       fill_sequence(a, b, w.start[b], w.held[b], *w.count, worker * 4, workers * 4, worker, workers);
     else
-      release_sequence(a, b, w.start[b], w.held[b], *w.count, worker, workers);
+      // (the scan has stored what is held and free now)
+      release_sequence(a, b, w.start[b], a.held[b], w.held[b], worker, workers, *a.free_count);
   }
 }
 
 template <bool kTake>
 int slots_launch(const SlotArgs &a, void *workspace, size_t ws_bytes, tsd_stream_t stream) {
   const cudaStream_t s = as_cuda(stream);
-  if (a.B <= kSmallSeqs && (int64_t)a.B * a.N_max <= kSmallTokens)
-    return launch(slots_small_kernel<kTake>, dim3(1), dim3(kScanThreads), 0, s, a) == cudaSuccess
-               ? TSD_OK
-               : TSD_ERR_CUDA;
+  if (a.B <= kSmallSeqs && (int64_t)a.B * a.N_max <= kSmallTokens) {
+    if (kTake)
+      return launch(slots_take_kernel, dim3(1), dim3(kScanThreads), 0, s, a) == cudaSuccess ? TSD_OK : TSD_ERR_CUDA;
+    // at most max_blocks a sequence come back; 256 a block of the cluster at least
+    int ctas = 1;
+    while (ctas < 8 && ctas * 256ll < (int64_t)a.B * a.max_blocks) ctas *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(kScanThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = ctas;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = ctas > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, slots_release_kernel, a) == cudaSuccess ? TSD_OK : TSD_ERR_CUDA;
+  }
   if (!workspace || ws_bytes < slot_ws_bytes(a.B)) return TSD_ERR_WORKSPACE;
   if (!aligned(workspace, 8)) return TSD_ERR_ARG;
   const SlotWork w = slot_ws(workspace, a.B);
