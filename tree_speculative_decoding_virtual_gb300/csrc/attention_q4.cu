@@ -38,11 +38,13 @@
 // joined in fp32, in shared memory or by a second kernel.
 //
 // Measured (device time): one token behind 4096 keys, 32 query and 8 kv heads of 128: 9 us; 32
-// tokens behind 512 to 16384 keys, 64 / 8 heads: 75 us for 312 MB (62% of the copy
-// bandwidth).  There it takes about 350 instructions a page and warp at 0.6 a cycle and
-// scheduler: the copies alone take 56 us, the arithmetic alone 66.  Ten warps a block
-// (96 registers) took 80 us, three blocks an SM (80 registers) 125, the next page's
-// scores ahead of this page's products 77, a ring of five pages 76.
+// tokens behind 512 to 16384 keys, 64 / 8 heads: 70 us for 312 MB (66% of the copy
+// bandwidth); behind 16384 each, 32 / 8 heads: 111 us for 604 MB (80%).  A warp takes two
+// pages at a time (with up to 8 rows; more would not leave the registers): one at a
+// time, with some 350 instructions a page, the three took 9, 75 and 125 us, the copies
+// of the second alone 56 and its arithmetic alone 66; and of that kernel ten
+// warps a block (96 registers) took 80 us, three blocks an SM (80 registers) 125, the
+// next page's scores ahead of this page's products 77, a ring of five pages 76.
 
 #include <cuda_bf16.h>
 
@@ -57,7 +59,6 @@ namespace {
 
 constexpr int kRowsThreads = 256;
 constexpr int kRowsWarps = kRowsThreads / 32;
-constexpr int kRowsStages = 4;  // pages in flight per warp
 constexpr float kOffset = 8.f;  // P of the reference score is 2^8
 constexpr float kSlack = 7.f;   // P stays at or below 2^15
 constexpr float kRowsLn2 = 0.6931471805599453f;
@@ -99,9 +100,12 @@ __device__ __forceinline__ void lds_words(const uint8_t *p, uint32_t (&w)[N]) {
 template <int D, int NT>
 struct RowsLayout {
   static constexpr int kPageBytes = Q4Page<D>::kBytes;
-  static constexpr int kStage = 2 * kPageBytes;
-  static constexpr int kChunks = kStage / 16;  // 16-byte copies of a K and a V page
-  static constexpr int kRing = kRowsWarps * kRowsStages * kStage;
+  // Pages that a warp takes at a time, and the stages of its ring of such items
+  static constexpr int kItem = NT == 1 ? 2 : 1, kStages = 4 / kItem;
+  static constexpr int kPair = 2 * kPageBytes;  // a page's K and V
+  static constexpr int kStage = kItem * kPair;
+  static constexpr int kChunks = kPair / 16;  // 16-byte copies of a K and a V page
+  static constexpr int kRing = kRowsWarps * kStages * kStage;
   static constexpr int kMerge = kRowsWarps * 8 * NT * D * 4;  // O of every warp
   static constexpr int kBlock = 8 * NT * D * 4;               // O of the block
   static constexpr int kBytes = kRing > kMerge + kBlock ? kRing : kMerge + kBlock;
@@ -140,6 +144,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2) tree_attn_q4_rows_kernel(cons
   constexpr int kWordsK = D / 32;     // code words of a lane's part of a key
   constexpr int kWordsV = D / 64;     // code words of a lane's part of a V row
   constexpr int kTiles = D / 16;      // M tiles of O^T
+  constexpr int kItem = L::kItem, kStages = L::kStages;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ RowsShared sh;
   pdl_trigger();
@@ -178,16 +183,19 @@ __global__ void __launch_bounds__(kRowsThreads, 2) tree_attn_q4_rows_kernel(cons
     }
 
     if (work) {
-      // ---- the page stream: each page is one group of the lanes' copies ----
+      // ---- the page stream: each item is one group of the lanes' copies ----
       const int32_t *trow = p.table + (size_t)b * p.max_blocks;
-      const int mine = last - first > warp ? (last - first - warp + kRowsWarps - 1) / kRowsWarps : 0;
-      const uint32_t ring = smem_addr(smem) + warp * kRowsStages * L::kStage;
-      const uint8_t *ring_p = smem + warp * kRowsStages * L::kStage;
+      const int items = (last - first + kItem - 1) / kItem;
+      const int mine = items > warp ? (items - warp + kRowsWarps - 1) / kRowsWarps : 0;
+      const uint32_t ring = smem_addr(smem) + warp * kStages * L::kStage;
+      const uint8_t *ring_p = smem + warp * kStages * L::kStage;
+      auto page_of = [&](int it, int h) { return first + (warp + it * kRowsWarps) * kItem + h; };
       int ids = 0;  // lane i: the id of this warp's page 32 * batch + i
       bool stop = false;
+      constexpr int kBatch = 32 / kItem;  // items whose ids are read together
       auto fetch_ids = [&](int it) {
-        const int j = it + lane;
-        const int id = j < mine ? trow[first + warp + j * kRowsWarps] : 0;
+        const int j = it + lane / kItem, page = page_of(j, lane % kItem);
+        const int id = j < mine && page < last ? trow[page] : 0;
         const bool bad = id < 0 || id >= p.num_blocks;
         if (__any_sync(0xffffffffu, bad)) {
           stop = true;
@@ -201,19 +209,24 @@ __global__ void __launch_bounds__(kRowsThreads, 2) tree_attn_q4_rows_kernel(cons
       const uint8_t *k_lane = p.k + 16 * lane, *v_lane = p.v - 16 * kHalfChunks + 16 * lane;
       const uint8_t *mixed = kMixed * 32 + lane < kHalfChunks ? k_lane : v_lane;
       auto issue = [&](int it) {
-        const int id = __shfl_sync(0xffffffffu, ids, it & 31);
-        const size_t off = ((size_t)id * p.Hkv + h) * L::kPageBytes;
-        const uint32_t dst = ring + (it % kRowsStages) * L::kStage + 16 * lane;
+        const uint32_t dst0 = ring + (it % kStages) * L::kStage + 16 * lane;
 #pragma unroll
-        for (int c = 0; c < (L::kChunks + 31) / 32; ++c) {
-          const uint8_t *src = (c < kMixed ? k_lane : c == kMixed ? mixed : v_lane) + off + 512 * c;
-          if ((c + 1) * 32 <= L::kChunks || c * 32 + lane < L::kChunks) cp_async_16(dst + 512 * c, src);
+        for (int hp = 0; hp < kItem; ++hp) {
+          if (hp > 0 && page_of(it, hp) >= last) break;  // (an odd end; its scores are masked)
+          const int id = __shfl_sync(0xffffffffu, ids, (it % kBatch) * kItem + hp);
+          const size_t off = ((size_t)id * p.Hkv + h) * L::kPageBytes;
+          const uint32_t dst = dst0 + hp * L::kPair;
+#pragma unroll
+          for (int c = 0; c < (L::kChunks + 31) / 32; ++c) {
+            const uint8_t *src = (c < kMixed ? k_lane : c == kMixed ? mixed : v_lane) + off + 512 * c;
+            if ((c + 1) * 32 <= L::kChunks || c * 32 + lane < L::kChunks) cp_async_16(dst + 512 * c, src);
+          }
         }
       };
       auto commit = [] { asm volatile("cp.async.commit_group;\n" ::: "memory"); };
       if (mine > 0) fetch_ids(0);
       int issued = 0;
-      for (int i = 0; i < kRowsStages; ++i) {  // one group a stage, an empty one past the end
+      for (int i = 0; i < kStages; ++i) {  // one group a stage, an empty one past the end
         if (!stop && issued < mine) issue(issued++);
         commit();
       }
@@ -264,101 +277,119 @@ __global__ void __launch_bounds__(kRowsThreads, 2) tree_attn_q4_rows_kernel(cons
       const int kv0 = (2 * qt) ^ (qt & 1), kv1 = (2 * qt + 1) ^ (qt & 1);
 
       for (int it = 0; it < mine && !stop; ++it) {
-        const int st = it % kRowsStages;
-        asm volatile("cp.async.wait_group %0;\n" ::"n"(kRowsStages - 1) : "memory");
+        asm volatile("cp.async.wait_group %0;\n" ::"n"(kStages - 1) : "memory");
         __syncwarp();
-        const uint8_t *kp = ring_p + st * L::kStage, *vp = kp + L::kPageBytes;
-        const int t0 = (first + warp + it * kRowsWarps) * kPage;  // first key slot
+        const uint8_t *item = ring_p + (it % kStages) * L::kStage;
+        const int t0 = page_of(it, 0) * kPage;  // first key slot
 
         // S^T
-        float s[NT][4];
+        float s[kItem][NT][4];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
-        uint32_t wa[kWordsK], wb[kWordsK];
-        lds_words(kp + key_a * Page::kRow + qt * (D / 8), wa);
-        lds_words(kp + (key_a + 8) * Page::kRow + qt * (D / 8), wb);
-        uint32_t sa[2], sb[2];  // scales of the lane's (one or two) groups of 16 columns
-        if constexpr (D == 128) {
-          const uint32_t xa = *reinterpret_cast<const uint16_t *>(kp + Page::kScales + key_a * 8 + 2 * qt);
-          const uint32_t xb =
-              *reinterpret_cast<const uint16_t *>(kp + Page::kScales + (key_a + 8) * 8 + 2 * qt);
-          sa[0] = (xa & 0xFFu) * 0x00800080u;
-          sa[1] = (xa >> 8) * 0x00800080u;
-          sb[0] = (xb & 0xFFu) * 0x00800080u;
-          sb[1] = (xb >> 8) * 0x00800080u;
-        } else {
-          sa[0] = sa[1] = kp[Page::kScales + key_a * 4 + qt] * 0x00800080u;
-          sb[0] = sb[1] = kp[Page::kScales + (key_a + 8) * 4 + qt] * 0x00800080u;
-        }
+        for (int hp = 0; hp < kItem; ++hp) {
+          const uint8_t *kp = item + hp * L::kPair;
 #pragma unroll
-        for (int w = 0; w < kWordsK; ++w) {
-          uint32_t ra[4], rb4[4];
-          q4_decode8(wa[w], ra);
-          q4_decode8(wb[w], rb4);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            ra[e] = q4_mul2(ra[e], sa[w / 2]);
-            rb4[e] = q4_mul2(rb4[e], sb[w / 2]);
+          for (int n = 0; n < NT; ++n) s[hp][n][0] = s[hp][n][1] = s[hp][n][2] = s[hp][n][3] = 0.f;
+          uint32_t wa[kWordsK], wb[kWordsK];
+          lds_words(kp + key_a * Page::kRow + qt * (D / 8), wa);
+          lds_words(kp + (key_a + 8) * Page::kRow + qt * (D / 8), wb);
+          uint32_t sa[2], sb[2];  // scales of the lane's (one or two) groups of 16 columns
+          if constexpr (D == 128) {
+            const uint32_t xa = *reinterpret_cast<const uint16_t *>(kp + Page::kScales + key_a * 8 + 2 * qt);
+            const uint32_t xb =
+                *reinterpret_cast<const uint16_t *>(kp + Page::kScales + (key_a + 8) * 8 + 2 * qt);
+            sa[0] = (xa & 0xFFu) * 0x00800080u;
+            sa[1] = (xa >> 8) * 0x00800080u;
+            sb[0] = (xb & 0xFFu) * 0x00800080u;
+            sb[1] = (xb >> 8) * 0x00800080u;
+          } else {
+            sa[0] = sa[1] = kp[Page::kScales + key_a * 4 + qt] * 0x00800080u;
+            sb[0] = sb[1] = kp[Page::kScales + (key_a + 8) * 4 + qt] * 0x00800080u;
           }
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            mma_f16(s[n], ra[0], rb4[0], ra[1], rb4[1], qf[n][2 * w][0], qf[n][2 * w][1]);
-            mma_f16(s[n], ra[2], rb4[2], ra[3], rb4[3], qf[n][2 * w + 1][0], qf[n][2 * w + 1][1]);
+          for (int w = 0; w < kWordsK; ++w) {
+            uint32_t ra[4], rb4[4];
+            q4_decode8(wa[w], ra);
+            q4_decode8(wb[w], rb4);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              ra[e] = q4_mul2(ra[e], sa[w / 2]);
+              rb4[e] = q4_mul2(rb4[e], sb[w / 2]);
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              mma_f16(s[hp][n], ra[0], rb4[0], ra[1], rb4[1], qf[n][2 * w][0], qf[n][2 * w][1]);
+              mma_f16(s[hp][n], ra[2], rb4[2], ra[3], rb4[3], qf[n][2 * w + 1][0], qf[n][2 * w + 1][1]);
+            }
           }
         }
 
         // V's codes and scales; slots past the sequence read as zero
-        uint32_t wv[4][kWordsV], sv[4];
+        uint32_t wv[kItem][4][kWordsV], sv[kItem][4];
         const int kk[4] = {kv0, kv1, kv0 + 8, kv1 + 8};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          lds_words(vp + kk[e] * Page::kRow + qi * (D / 16), wv[e]);
-          sv[e] = vp[Page::kScales + kk[e] * Page::kScaleRow + qi * (D / 8) / kQ4Group];
+        for (int hp = 0; hp < kItem; ++hp) {
+          const uint8_t *vp = item + hp * L::kPair + L::kPageBytes;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            lds_words(vp + kk[e] * Page::kRow + qi * (D / 16), wv[hp][e]);
+            sv[hp][e] = vp[Page::kScales + kk[e] * Page::kScaleRow + qi * (D / 8) / kQ4Group];
+          }
         }
-        // the page is in registers: its stage can be refilled
+        // the item is in registers: its stage can be refilled
         __syncwarp();
         if (issued < mine) {
-          if ((issued & 31) == 0) fetch_ids(issued);
+          if (issued % kBatch == 0) fetch_ids(issued);
           if (!stop) issue(issued++);
         }
         commit();
 
         // softmax: t = s * mul, and what the row may not see is -inf
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          s[n][0] *= mul[n][0];
-          s[n][1] *= mul[n][1];
-          s[n][2] *= mul[n][0];
-          s[n][3] *= mul[n][1];
-        }
-        if (t0 + kPage > P) {
+        for (int hp = 0; hp < kItem; ++hp)
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int r = row0 + 8 * n + 2 * qt + e;
-              const uint32_t vis = r < rows_valid ? q4_visible(p, b, r / p.g, t0 - P, nb) : 0u;
-              if (!((vis >> key_a) & 1u)) s[n][e] = -INFINITY;
-              if (!((vis >> (key_a + 8)) & 1u)) s[n][2 + e] = -INFINITY;
-            }
+            s[hp][n][0] *= mul[n][0];
+            s[hp][n][1] *= mul[n][1];
+            s[hp][n][2] *= mul[n][0];
+            s[hp][n][3] *= mul[n][1];
           }
-          // V's slots past the sequence read as zero.  Scale bytes that no writer makes
-          // can only be met here, in slots of the tree that were not written: they read
-          // as the largest scale, so that P = 0 really leaves them out.
+        if (t0 + kItem * kPage > P) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) sv[e] = t0 + kk[e] >= P + nb ? 0u : min(sv[e], kQ4MaxScale);
+          for (int hp = 0; hp < kItem; ++hp) {
+            const int at = t0 + hp * kPage;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int r = row0 + 8 * n + 2 * qt + e;
+                const uint32_t vis = r < rows_valid ? q4_visible(p, b, r / p.g, at - P, nb) : 0u;
+                if (!((vis >> key_a) & 1u)) s[hp][n][e] = -INFINITY;
+                if (!((vis >> (key_a + 8)) & 1u)) s[hp][n][2 + e] = -INFINITY;
+              }
+            }
+            // V's slots past the sequence read as zero.  Scale bytes that no writer makes
+            // can only be met here, in slots of the tree that were not written: they read
+            // as the largest scale, so that P = 0 really leaves them out.
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sv[hp][e] = at + kk[e] >= P + nb ? 0u : min(sv[hp][e], kQ4MaxScale);
+          }
         }
+        float most[NT][2];  // the lane's largest scores
         bool over = false;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) over = over || fmaxf(s[n][e], s[n][2 + e]) > trig[n][e];
+          for (int e = 0; e < 2; ++e) {
+            most[n][e] = fmaxf(s[0][n][e], s[0][n][2 + e]);
+            if constexpr (kItem == 2) most[n][e] = fmax3(most[n][e], s[1][n][e], s[1][n][2 + e]);
+            over = over || most[n][e] > trig[n][e];
+          }
         if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              float m = fmaxf(s[n][e], s[n][2 + e]);
+              float m = most[n][e];
               m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
               m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
               m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
@@ -378,38 +409,43 @@ __global__ void __launch_bounds__(kRowsThreads, 2) tree_attn_q4_rows_kernel(cons
             }
           }
         }
-        uint32_t pb[NT][2];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const float p0 = ex2_approx(s[n][0] - ref[n][0]), p1 = ex2_approx(s[n][1] - ref[n][1]);
-          const float p2 = ex2_approx(s[n][2] - ref[n][0]), p3 = ex2_approx(s[n][3] - ref[n][1]);
-          l[n][0] += p0 + p2;
-          l[n][1] += p1 + p3;
-          pb[n][0] = transpose8x8(pack_half2(p0, p1));
-          pb[n][1] = transpose8x8(pack_half2(p2, p3));
-        }
+        for (int hp = 0; hp < kItem; ++hp) {
+          uint32_t pb[NT][2];
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            const float p0 = ex2_approx(s[hp][n][0] - ref[n][0]), p1 = ex2_approx(s[hp][n][1] - ref[n][1]);
+            const float p2 = ex2_approx(s[hp][n][2] - ref[n][0]), p3 = ex2_approx(s[hp][n][3] - ref[n][1]);
+            l[n][0] += p0 + p2;
+            l[n][1] += p1 + p3;
+            pb[n][0] = transpose8x8(pack_half2(p0, p1));
+            pb[n][1] = transpose8x8(pack_half2(p2, p3));
+          }
 
-        // O^T: M tile j holds columns i D/8 + 2 j (row i) and the next (row i + 8).  An
-        // operand register holds one column of two keys, so the codes of two keys are
-        // interleaved before they are decoded (three operations for eight registers;
-        // after, it takes a byte permutation each, on the pipe that also converts).
-        const uint32_t s01 = sv[0] * 0x80u + sv[1] * 0x00800000u, s23 = sv[2] * 0x80u + sv[3] * 0x00800000u;
+          // O^T: M tile j holds columns i D/8 + 2 j (row i) and the next (row i + 8).  An
+          // operand register holds one column of two keys, so the codes of two keys are
+          // interleaved before they are decoded (three operations for eight registers;
+          // after, it takes a byte permutation each, on the pipe that also converts).
+          const uint32_t s01 = sv[hp][0] * 0x80u + sv[hp][1] * 0x00800000u;
+          const uint32_t s23 = sv[hp][2] * 0x80u + sv[hp][3] * 0x00800000u;
 #pragma unroll
-        for (int w = 0; w < kWordsV; ++w) {
-          uint32_t a0[4], a1[4], a2[4], a3[4];
-          q4_decode8((wv[0][w] & 0x0F0F0F0Fu) | (wv[1][w] * 16u & 0xF0F0F0F0u), a0);
-          q4_decode8(((wv[0][w] >> 4) & 0x0F0F0F0Fu) | (wv[1][w] & 0xF0F0F0F0u), a1);
-          q4_decode8((wv[2][w] & 0x0F0F0F0Fu) | (wv[3][w] * 16u & 0xF0F0F0F0u), a2);
-          q4_decode8(((wv[2][w] >> 4) & 0x0F0F0F0Fu) | (wv[3][w] & 0xF0F0F0F0u), a3);
+          for (int w = 0; w < kWordsV; ++w) {
+            const uint32_t v0 = wv[hp][0][w], v1 = wv[hp][1][w], v2 = wv[hp][2][w], v3 = wv[hp][3][w];
+            uint32_t a0[4], a1[4], a2[4], a3[4];
+            q4_decode8((v0 & 0x0F0F0F0Fu) | (v1 * 16u & 0xF0F0F0F0u), a0);
+            q4_decode8(((v0 >> 4) & 0x0F0F0F0Fu) | (v1 & 0xF0F0F0F0u), a1);
+            q4_decode8((v2 & 0x0F0F0F0Fu) | (v3 * 16u & 0xF0F0F0F0u), a2);
+            q4_decode8(((v2 >> 4) & 0x0F0F0F0Fu) | (v3 & 0xF0F0F0F0u), a3);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            a0[j] = q4_mul2(a0[j], s01);
-            a1[j] = q4_mul2(a1[j], s01);
-            a2[j] = q4_mul2(a2[j], s23);
-            a3[j] = q4_mul2(a3[j], s23);
+            for (int j = 0; j < 4; ++j) {
+              a0[j] = q4_mul2(a0[j], s01);
+              a1[j] = q4_mul2(a1[j], s01);
+              a2[j] = q4_mul2(a2[j], s23);
+              a3[j] = q4_mul2(a3[j], s23);
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-              mma_f16(o[n][4 * w + j], a0[j], a1[j], a2[j], a3[j], pb[n][0], pb[n][1]);
+              for (int n = 0; n < NT; ++n)
+                mma_f16(o[n][4 * w + j], a0[j], a1[j], a2[j], a3[j], pb[n][0], pb[n][1]);
+            }
           }
         }
       }
@@ -619,11 +655,13 @@ struct Q4Shape {
 };
 
 
-// Fixed cost of a key range, in units of 128 keys of one row tile.  Measured, 16
-// trees of up to 127 nodes over 128 to 8064 slots, many-row kernel: 0: 110 us, 4: 79,
-// 6: 74, 8: 71, 10: 71, 16: 78; 64 tokens over 64 to 16320 slots, few-row kernel:
-// 0: 94 us, 2: 83, 4: 76, 5: 75, 8: 77.  Equal long ranges take the same time with any.
-constexpr int kTcRangeCost = 8, kRowsRangeCost = 5;
+// Fixed cost of a key range, in units of 128 keys of one row tile.  Measured (with
+// kernels a little slower than these), 16 trees of up to 31 nodes over 512 to 8192 slots,
+// many-row kernel: 0: 110 us, 4: 79, 6: 74, 8: 71, 10: 71, 16: 78; 32 tokens over 512
+// to 16384 slots, few-row kernel: 0: 94 us, 2: 83, 5: 73, 7: 70, 10: 70.  64 trees
+// take 216 us with 7, 208 with 8, 203 with 9 and 10.  Equal long ranges take the same
+// time with any.
+constexpr int kTcRangeCost = 9, kRowsRangeCost = 7;
 
 // The many-row kernel needs some 15 us more to get going, and then takes 128 or 256 rows
 // through a decoded tile where the few-row kernel takes 16: it runs from this much
@@ -631,7 +669,7 @@ constexpr int kTcRangeCost = 8, kRowsRangeCost = 5;
 // / many rows (8 kv heads; rows of one, sequences, keys): 32, 1, 2048: 14 / 27 us; 252,
 // 1, 2048: 23 / 30; 32, 8, 1024: 17 / 28; 64, 1, 8192: 27 / 29; 64, 8, 512: 27 / 24;
 // 64, 8, 1024: 32 / 28; 64, 1, 16384: 39 / 31; 32, 32, 8192: 212 / 163.
-constexpr int64_t kTcMinWork = 3000;
+constexpr int64_t kTcMinWork = 3072;
 
 // Host: how a call is cut up.
 Q4Shape q4_shape(int B, int N_max, int Hq, int Hkv, int D, int max_slots) {

@@ -208,7 +208,8 @@ __device__ __forceinline__ bool q4_next(const Q4Attn &p, const Q4Plan &sh, int &
   if (bad && blockIdx.x == 0 && threadIdx.x == 0 && p.status) atomicOr(p.status, TSD_STATUS_BAD_LEN);
   if (!ok) s.nb = 0;  // (no valid row)
   const int pages = ok ? (s.P + s.nb + kPage - 1) / kPage : 0;
-  const int chunk = p.cluster ? (pages + p.splits - 1) / p.splits : p.chunk;
+  // (even, so that a warp's two pages at a time are in one piece)
+  const int chunk = p.cluster ? ((pages + p.splits - 1) / p.splits + 1) & ~1 : p.chunk;
   s.first = split * chunk;
   s.last = min(pages, s.first + chunk);
   s.direct = p.splits == 1;
