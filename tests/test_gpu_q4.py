@@ -591,6 +591,105 @@ def test_attention_is_deterministic_and_capturable(tsd, bound):
         assert torch.equal(out, o5) and torch.equal(lse, l5)
 
 
+@pytest.mark.parametrize("N,Hq", [(1, 8), (5, 8), (40, 16)])
+def test_attention_replayed_with_other_lengths(tsd, N, Hq, bound):
+    """A captured call is cut up on the device: it holds for whatever lengths,
+    errors and block tables its buffers have when it is replayed."""
+    import torch
+    prefixes = ([900, 333, 64], [1, 1200, 700], [15, 16, 17], [0, 1300, 0])
+    x = _long_inputs(N, 3, N, Hq, 2, 128, [1300] * 3, [N] * 3)
+    x["P"] = np.array(prefixes[0], np.int32)
+    a = {k: T(v) for k, v in x.items() if k in ("k", "v", "table", "P", "n", "err")}
+    q, m = bf(x["q"]), T(x["mask"].view(np.int32))
+    out, lse = (torch.empty(x["q"].shape, dtype=torch.bfloat16, device="cuda"),
+                torch.empty(x["q"].shape[:3], dtype=torch.float32, device="cuda"))
+
+    def call():
+        tsd.tree_attn_fwd_q4(q, a["k"], a["v"], a["table"], a["P"], a["n"], m, a["err"], bound or x["max_slots"],
+                             scale=x["scale"], out=out, lse=lse)
+
+    call()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    for i, prefix in enumerate(prefixes):
+        x["P"][:] = prefix
+        x["n"][:] = [N, max(1, N - i), 1]
+        x["err"][:] = [0, i == 2, 0]
+        x["table"] = np.ascontiguousarray(np.roll(x["table"], 1, 0))
+        for k in ("P", "n", "err", "table"):
+            a[k].copy_(T(x[k]))
+        out.fill_(float("nan"))
+        lse.fill_(float("nan"))
+        g.replay()
+        torch.cuda.synchronize()
+        _check(x, oracle.bf16_to_f64(np_of(out, np.uint16)), np_of(lse).astype(np.float64), _ref(x))
+
+
+def test_two_streams_at_once(tsd):
+    """The calls of two streams overlap, each with what it allocates, and give what
+    they give alone."""
+    import torch
+    xs = [_long_inputs(5, 8, 3, 16, 4, 128, list(range(500, 500 + 8 * 211, 211)), [3] * 8),
+          _long_inputs(6, 6, 60, 16, 4, 128, list(range(700, 700 + 6 * 307, 307)), [60] * 6)]
+    logits = torch.randn(40, 50000, device="cuda")
+    tokens = torch.arange(40, dtype=torch.int32, device="cuda")
+    args = []
+    for x in xs:
+        a = {k: T(v) for k, v in x.items() if k in ("k", "v", "table", "P", "n", "err")}
+        args.append((bf(x["q"]), a["k"], a["v"], a["table"], a["P"], a["n"], T(x["mask"].view(np.int32)), a["err"],
+                     x["max_slots"]))
+    alone = [tsd.tree_attn_fwd_q4(*a) + tsd.token_logprobs(logits, tokens, k=7) for a in args]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i in (0, 1):
+            got[i].append(tsd.tree_attn_fwd_q4(*args[i], stream=streams[i])
+                          + tsd.token_logprobs(logits, tokens, k=7, stream=streams[i]))
+    torch.cuda.synchronize()
+    for i in (0, 1):
+        for one in got[i]:
+            assert all(torch.equal(x, y) for x, y in zip(one, alone[i]))
+
+
+def test_blocks_beyond_four_gigabytes(tsd):
+    """Blocks at the end of a pool of 4.6 GB: the byte offsets pass 32 bits."""
+    import torch
+    blocks, Hkv, D, P, N = 500000, 8, 128, 200, 6
+    k, v = (torch.empty((blocks, Hkv, 9 * D), dtype=torch.uint8, device="cuda") for _ in range(2))
+    need = (P + N + 15) // 16
+    table = np.arange(blocks - 1, blocks - 1 - 7 * need, -7, dtype=np.int32)[None]
+    slots = np.array([table[0, t // 16] * 16 + t % 16 for t in range(P + N)], np.int32)
+    rng = np.random.default_rng(2)
+    rows = [gen.normal_bf16(rng, (P + N, Hkv, D)) for _ in range(2)]
+    st = status_word()
+    tsd.kv_write_q4(bf(rows[0]), bf(rows[1]), T(slots), k, v, status=st)
+    # the oracle has the last blocks only
+    first = int(table.min())
+    near = slots - first * 16
+    pools = [oq4.write_rows(np.zeros((blocks - first, Hkv, 9 * D), np.uint8), r, near) for r in rows]
+    for got, pool in zip(tsd.kv_read_q4(k, v, T(slots), status=st), pools):
+        assert np.array_equal(oracle.bf16_to_f64(np_of(got, np.uint16)), oq4.read_rows(pool, near))
+    mask, err = _mask(np.array([[-1, 0, 0, 1, 1, 2]], np.int32), np.array([N], np.int32))
+    x = dict(q=gen.normal_bf16(rng, (1, N, 32, D)), k=pools[0], v=pools[1], table=table - first,
+             P=np.array([P], np.int32), n=np.array([N], np.int32), mask=mask, err=err, D=D, max_slots=P + N,
+             scale=0.09)
+    ref = _ref(x)
+    for bound in (P + N, 262144):
+        out, lse = tsd.tree_attn_fwd_q4(bf(x["q"]), k, v, T(table), T(x["P"]), T(x["n"]), T(mask.view(np.int32)),
+                                        T(err), bound, scale=0.09, status=st)
+        _check(x, oracle.bf16_to_f64(np_of(out, np.uint16)), np_of(lse).astype(np.float64), ref)
+    path, accept = np.array([[1, 3, 6, 0, 0]], np.int32), np.array([2], np.int32)
+    new_len, moved = tsd.kv_commit_path_q4(k, v, T(table), T(x["P"]), T(x["n"]), T(accept), T(path), T(err), N, 4,
+                                           status=st)
+    ok, ov, o_len, o_moved = oq4.commit_path(pools[0], pools[1], x["table"], x["P"], accept, path, err)[:4]
+    assert np.array_equal(np_of(new_len), o_len) and np.array_equal(np_of(moved), o_moved)
+    for got, pool in zip((k, v), (ok, ov)):
+        assert np.array_equal(np_of(got[table[0].astype(np.int64)]), pool[x["table"][0]])
+    assert int(st.item()) == 0
+
+
 @pytest.mark.parametrize("B,N,Hq,prefix", [(6, 100, 32, [2000, 130, 900, 4000, 17, 1200]),
                                            (16, 31, 32, list(range(64, 64 + 16 * 190, 190)))])
 def test_attention_wait_limit(tsd, B, N, Hq, prefix):
