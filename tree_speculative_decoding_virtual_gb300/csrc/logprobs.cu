@@ -13,12 +13,12 @@
 //
 // One pass over the logits, so the kernel is bound by HBM (4 or 2 bytes a
 // logit).  A cluster of up to 8 CTAs takes a row (one CTA where the rows alone
-// fill the GPU); a CTA walks its slice in chunks of 4096 logits, 16 a thread, which
-// come through a ring in shared memory (three chunks ahead: it keeps the stream going
-// while the CTA settles its first chunk, and what passes the threshold is looked up
-// there; with the next 16 logits in registers and looked up in memory, 1216 rows of
-// 128256 and their 20 best took 115 us instead of 103, without a best list 95 instead
-// of 99).  Rows without 16-byte alignment go through registers.
+// fill the GPU); a CTA walks its slice in chunks of 4096 logits, 16 a thread.  With
+// alternatives they come through a ring in shared memory, three chunks ahead: it keeps
+// the stream going while the CTA settles its first chunk, and what passes the
+// threshold is looked up there.  Without, and where rows are not aligned to 16
+// bytes, the next 16 are on the way to registers.  (1216 rows of 128256 fp32, ring /
+// registers: 20 best 103 / 115 us, 1 best as long, none 99 / 95.)
 //   reference  the maximum of the CTA's first chunk is the m of its sums; a warp
 //              that meets a value more than 40 above its m moves it (e^40 leaves
 //              fp32 sums far from overflow)
@@ -410,7 +410,7 @@ __device__ __forceinline__ bool lp_resolve(const LpArgs &a, int r, int64_t &row,
   return true;
 }
 
-template <bool kBf16, bool kVec>
+template <bool kBf16, bool kVec, bool kRing>
 __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const LpArgs a) {
   using namespace sm100;
   __shared__ LpShared sh;
@@ -454,7 +454,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const LpArgs a)
     using Raw = LpRaw<kBf16, kVec>;
     Raw x, next;
     const uint32_t ring_at = smem_addr(ring);
-    if constexpr (kVec) {
+    if constexpr (kRing) {
 #pragma unroll
       for (int i = 0; i < Raw::kStages; ++i)  // one group a stage, an empty one past the end
         Raw::fetch(ring_at + i * Raw::kStage, src, first + i * kChunk, last, tid);
@@ -510,7 +510,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const LpArgs a)
     int stage = 0;  // x's
     for (int c0 = first; c0 < last; c0 += kChunk) {
       const int end = min(last, c0 + kChunk);
-      if constexpr (!kVec) {
+      if constexpr (!kRing) {
         if (end < last) next.load(src, end, min(last, end + kChunk), tid);
       }
       float most = x.get(0);
@@ -526,7 +526,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const LpArgs a)
         for (; mine; mine &= mine - 1) {
           const int e = __ffs(mine) - 1, id = c0 + chunk_pos<kBf16, kVec>(e, tid);
           if (id >= end) continue;
-          const float v = kVec ? Raw::one(ring + stage * Raw::kStage, e, tid) : one_logit<kBf16>(src, id);
+          const float v = kRing ? Raw::one(ring + stage * Raw::kStage, e, tid) : one_logit<kBf16>(src, id);
           const uint32_t vo = ordered(v);
           top = fmaxf(top, v);
           if (k == 0) continue;
@@ -540,7 +540,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const LpArgs a)
         }
       }
       // (x and what was read again are used: the stage can be refilled)
-      if constexpr (kVec)
+      if constexpr (kRing)
         Raw::fetch(ring_at + stage * Raw::kStage, src, c0 + Raw::kStages * kChunk, last, tid);
       __syncwarp();
       if (__any_sync(0xffffffffu, !below && top > m + kMove)) {  // the warp's reference follows
@@ -571,14 +571,14 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const LpArgs a)
         }
         next_settle = first + 4 * (next_settle - first);
       }
-      if constexpr (kVec) {
+      if constexpr (kRing) {
         if (++stage == Raw::kStages) stage = 0;
         if (end < last) x.read(ring + stage * Raw::kStage, end, last, tid);
       } else {
         x = next;
       }
     }
-    if constexpr (kVec) cp_async_wait_all();
+    if constexpr (kRing) cp_async_wait_all();
     float S = warp_sum(f2_unpack(S2).x + f2_unpack(S2).y);
     float T = warp_sum(f2_unpack(T2).x + f2_unpack(T2).y);
     if (lane == 0) {
@@ -693,13 +693,13 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const LpArgs a)
   }
 }
 
-template <bool kBf16, bool kVec>
+template <bool kBf16, bool kVec, bool kRing>
 cudaError_t lp_launch(const LpArgs &a, int R, int ctas, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)ctas * (unsigned)R);
   cfg.blockDim = dim3(kLpThreads);
-  if (kVec) {
-    if (!set_smem((const void *)logprobs_kernel<kBf16, kVec>, kLpRing)) return cudaErrorUnknown;
+  if (kRing) {
+    if (!set_smem((const void *)logprobs_kernel<kBf16, kVec, kRing>, kLpRing)) return cudaErrorUnknown;
     cfg.dynamicSmemBytes = kLpRing;
   }
   cfg.stream = stream;
@@ -712,7 +712,7 @@ cudaError_t lp_launch(const LpArgs &a, int R, int ctas, cudaStream_t stream) {
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, logprobs_kernel<kBf16, kVec>, a);
+  return cudaLaunchKernelEx(&cfg, logprobs_kernel<kBf16, kVec, kRing>, a);
 }
 
 int lp_run(LpArgs &a, int R, int bf16, tsd_stream_t stream) {
@@ -726,8 +726,13 @@ int lp_run(LpArgs &a, int R, int bf16, tsd_stream_t stream) {
   a.per = ((a.V + ctas - 1) / ctas + 7) / 8 * 8;
   const bool vec = aligned(a.logits, 16) && a.V % (bf16 ? 8 : 4) == 0;
   const cudaStream_t s = as_cuda(stream);
-  const cudaError_t e = bf16 ? (vec ? lp_launch<true, true>(a, R, ctas, s) : lp_launch<true, false>(a, R, ctas, s))
-                             : (vec ? lp_launch<false, true>(a, R, ctas, s) : lp_launch<false, false>(a, R, ctas, s));
+  const bool ring = vec && a.k > 0;
+  const cudaError_t e = bf16 ? (ring  ? lp_launch<true, true, true>(a, R, ctas, s)
+                                : vec ? lp_launch<true, true, false>(a, R, ctas, s)
+                                      : lp_launch<true, false, false>(a, R, ctas, s))
+                             : (ring  ? lp_launch<false, true, true>(a, R, ctas, s)
+                                : vec ? lp_launch<false, true, false>(a, R, ctas, s)
+                                      : lp_launch<false, false, false>(a, R, ctas, s));
   return e == cudaSuccess ? TSD_OK : TSD_ERR_CUDA;
 }
 
