@@ -9,18 +9,20 @@
 //   warps 0, 3   block ids, and the copies of K's and of V's pages into rings of packed
 //                half tiles
 //   warp 1       owns TMEM; lane 0 issues every MMA
-//   warp 2       tells it when the decoded tiles are there
+//   warp 2       with two row tiles tells it when the decoded tiles are there (with one
+//                the decoders do)
 //   warps 4-7    decode packed tiles to fp16 K and V tiles (128-byte swizzle)
 //   warps 8-15   softmax of chain 0, warps 16-23 of chain 1: one TMEM lane (=
 //                one query row) per thread, two threads a row (64 keys each)
 // Measured (device time): 4 trees of 127 nodes behind 32768 keys, 64 query and 8 kv heads of
-// 128: 434 us, 1260 TFLOP/s (67% of the measured bf16 rate; 2900 cycles for the 32 MMAs
+// 128: 436 us, 1260 TFLOP/s (67% of the measured bf16 rate; 2900 cycles for the 32 MMAs
 // of a tile, 80 each, and their two commits); 16 trees of 16 to 31 nodes behind 512 to 8192
-// keys, 32 / 8 heads: 68 us.  There a tile has 16 MMAs and takes 2700 cycles: the
+// keys, 32 / 8 heads: 66 us.  There a tile has 16 MMAs and takes 2600 cycles: the
 // chain from a tile's S through the release of its stage, the decoding of the tile
 // two further (some 2000 cycles for a pair of warps), its hand-over and its MMAs. Four
 // warps for K and four for V (896 threads, smaller register shares) took as long,
-// decoding a half tile ahead in registers 73 us.
+// decoding a half tile ahead in registers 73 us, the hand-over warp between them and the
+// issuing thread 68.
 // A chain is a row tile of 128 rows with its S (128 columns of TMEM, P over
 // the first 64) and O.  With more than 128 rows the two chains are two row
 // tiles that share every key tile; with fewer, chain c takes the key tiles j =
@@ -240,7 +242,8 @@ __device__ __forceinline__ bool tc_segment(const Q4Attn &p, TcShared &sh, bool f
         int count = 1;
         if (i >= 2 * kPackMost && k < 0) count = 2;               // pk_empty: a pair of decoders
         if (k == 0 || k == 1 || k == 4 || k == 5) count = 2;      // k_full, v_full: likewise
-        if (k == 10 || k == 11) count = sg.two && k == 11 ? 8 : 9;  // p_full: softmax warps, hand-over
+        // p_full: the softmax warps, and the hand-over or both pairs of decoders
+        if (k == 10 || k == 11) count = !sg.two ? 12 : k == 10 ? 9 : 8;
         if (k == 14) count = 16;                                  // q_full: softmax warps
         if (!fresh) mbar_inval(bar);
         mbar_init(bar, count);
@@ -433,24 +436,23 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4
         wait_phase(smem_addr(&sh.drain), 0, kTcDrainNs);
       }
       __syncwarp();
-    } else if (warp == 2) {
+    } else if (warp == 2 && two) {
       // ---- hand-over: phase j of p_full also means that V_j and the K tile of the
       // S behind P_j V_j are in shared memory.  (An arrival counts toward the phase
-      // that is open: the one before has to be complete.) ----
+      // that is open: the one before has to be complete.  With one row tile the
+      // decoders arrive there themselves, see there.) ----
       if (lane == 0) {
-        const int step = two ? 1 : 2;  // the chain's next tile
         // Each barrier's phases are waited for one after the other (a wait for a
-        // phase whose predecessor is still open returns at once): the first K tiles
+        // phase whose predecessor is still open returns at once): the first K tile
         // too, which the issuing thread waits for itself.
-        for (int k = 0; k < step && k < n; ++k) tc_wait(sh.k_full[k], 0, lim, abort);
+        tc_wait(sh.k_full[0], 0, lim, abort);
         for (int j = 0; j < n; ++j) {
-          const int c = two ? 0 : j & 1, u = two ? j : j >> 1;
           bool ok = tc_wait(sh.v_full[j & 1], (j >> 1) & 1, lim, abort);
-          const int k = j + step;
+          const int k = j + 1;
           if (ok && k < n) ok = tc_wait(sh.k_full[k & 1], (k >> 1) & 1, lim, abort);
-          if (ok && u > 0) ok = tc_wait(sh.p_full[c], (u - 1) & 1, lim, abort);
+          if (ok && j > 0) ok = tc_wait(sh.p_full[0], (j - 1) & 1, lim, abort);
           if (!ok) break;
-          mbar_arrive(smem_addr(&sh.p_full[c]));
+          mbar_arrive(smem_addr(&sh.p_full[0]));
         }
       }
       __syncwarp();
@@ -460,6 +462,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4
     regs_down<kRegsDecode>();
     for (bool fresh = true; tc_segment(p, sh, fresh, tid); fresh = false) {
     const int n = sg.n, ring = sg.two ? kPackSlots : kPackMost;
+    const bool two = sg.two;
     // ---- decode: warps 4 and 5 K tiles, 6 and 7 V tiles (two tiles at a time hide
     // each other's waits and fences: 128-row blocks were bound by four warps on
     // one tile); a lane takes one group (16 columns) of a key at a time ----
@@ -473,6 +476,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4
     // lanes of a store's quarter touch different banks
     const int flip = D == 128 ? grp >> 2 : 0;
     const int c0 = (grp & 3) * 2;
+    // Where a decoded tile is reported.  With one row tile straight to the barrier that
+    // the issuing thread waits for, which saves a hop of some 450 cycles: its phase of
+    // tile j wants V_j and K_{j+2}, both decoded only after S_j was seen (the first two V
+    // at once), so after the phase before was complete.
+    const uint32_t full_first = smem_addr(v == 0 ? sh.k_full : two ? sh.v_full : sh.p_full);
+    const uint32_t full = two ? full_first : smem_addr(sh.p_full);
     uint32_t phase = 0;
     for (int m = 0, slot = 0; m < 2 * n; ++m) {  // half tiles
       const int tile = m >> 1, st = tile & 1;
@@ -513,13 +522,18 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4
       if (m & 1) fence_proxy_async_smem();  // the tensor core reads the tile through the async proxy
       __syncwarp();
       if (lane == 0) {
-        if (m & 1) mbar_arrive(smem_addr(v ? &sh.v_full[st] : &sh.k_full[st]));
+        if (m & 1) mbar_arrive((tile < 2 ? full_first : full) + st * 8);
         mbar_arrive(smem_addr(&sh.pk_empty[v][slot]));
       }
       if (++slot == ring) {
         slot = 0;
         phase ^= 1;
       }
+    }
+    // the last tiles' phases have no K_{j+2}
+    for (int tile = max(n, 2); !two && v == 0 && tile < n + 2; ++tile) {
+      if (!tc_wait(sh.k_empty[tile & 1], ((tile >> 1) - 1) & 1, lim, abort)) break;
+      if (lane == 0) mbar_arrive(smem_addr(&sh.p_full[tile & 1]));
     }
     }
   } else {
