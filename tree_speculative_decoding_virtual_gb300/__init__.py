@@ -654,12 +654,21 @@ def _arg(t, dtype, shape, name, dev):
     return t.data_ptr()
 
 
+def _out_arg(t, dtype, shape, name, dev, device):
+    """(tensor, pointer) of an output: the caller's, checked, or a new one."""
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device=device)
+        return t, t.data_ptr()
+    return t, _arg(t, dtype, shape, name, dev)
+
+
 def _workspace_arg(workspace, need, like, dev):
     """(pointer, bytes) of the caller's workspace, or of a new one."""
     if workspace is None:
         if need == 0:
             return None, 0, None
         workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
+        return workspace.data_ptr(), need, workspace
     return (_arg(workspace, workspace.dtype, None, "workspace", dev),
             workspace.numel() * workspace.element_size(), workspace)
 
@@ -682,13 +691,12 @@ def kv_slots_build(prefix_len, n_new, N_max, block_table, held, free_list, free_
     if block_table.dim() != 2 or free_list.dim() != 1:
         raise TsdError("block_table must be [B][max_blocks] and free_list [num_blocks]")
     max_blocks, num_blocks = block_table.shape[1], free_list.shape[0]
-    if slots is None:
-        slots = torch.empty((B, max(N_max, 0)), dtype=i32, device=prefix_len.device)
+    slots, slots_p = _out_arg(slots, i32, (B, max(N_max, 0)), "slots", dev, prefix_len.device)
     args = (_arg(prefix_len, i32, (B,), "prefix_len", dev), _arg(n_new, i32, (B,), "n_new", dev), B, N_max,
             _arg(block_table, i32, (B, max_blocks), "block_table", dev), max_blocks,
             _arg(held, i32, (B,), "held", dev), _arg(free_list, i32, (num_blocks,), "free_list", dev),
             _arg(free_count, i32, (1,), "free_count", dev), num_blocks,
-            _arg(slots, i32, (B, N_max), "slots", dev))
+            slots_p)
     ws, ws_bytes, keep = _workspace_arg(workspace, kv_slots_workspace_bytes(B, N_max), prefix_len, dev)
     _check(lib.tsd_kv_slots_build(*args, ws, ws_bytes, _arg(status, i32, None, "status", dev),
                                   _raw_stream(dev)), "kv_slots_build")
@@ -733,8 +741,11 @@ def _q4_dims(k_cache, v_cache):
 def _token_rows(x, Hkv, D, name):
     """(tokens, elements between tokens) of x [...][Hkv][D], whose leading axes
     must step evenly."""
-    if x.dim() < 2 or x.shape[-2] != Hkv or x.shape[-1] != D:
+    shape = x.shape
+    if len(shape) < 2 or shape[-2] != Hkv or shape[-1] != D:
         raise TsdError("%s must be [...][%d][%d]" % (name, Hkv, D))
+    if x.is_contiguous():
+        return x.numel() // (Hkv * D), Hkv * D
     if x.stride(-1) != 1 or (Hkv > 1 and x.stride(-2) != D):
         raise TsdError("%s: a token's heads must be contiguous" % name)
     tokens, stride = 1, None
@@ -781,15 +792,13 @@ def kv_read_q4(k_cache, v_cache, slots, k=None, v=None, status=None):
     num_blocks = k_cache.numel() // (Hkv * 9 * D)
     dev = _device_of(slots)
     shape = (slots.numel(), Hkv, D)
-    if k is None:
-        k = torch.empty(shape, dtype=torch.bfloat16, device=slots.device)
-    if v is None:
-        v = torch.empty(shape, dtype=torch.bfloat16, device=slots.device)
+    bf16, device = torch.bfloat16, slots.device
+    k, k_out = _out_arg(k, bf16, shape, "k", dev, device)
+    v, v_out = _out_arg(v, bf16, shape, "v", dev, device)
     rc = lib.tsd_kv_read_q4(_arg(k_cache, torch.uint8, None, "k_cache", dev),
                             _arg(v_cache, torch.uint8, None, "v_cache", dev),
                             _arg(slots, torch.int32, None, "slots", dev), shape[0], num_blocks, Hkv, D,
-                            _arg(k, torch.bfloat16, shape, "k", dev), _arg(v, torch.bfloat16, shape, "v", dev),
-                            _arg(status, torch.int32, None, "status", dev), _raw_stream(dev))
+                            k_out, v_out, _arg(status, torch.int32, None, "status", dev), _raw_stream(dev))
     _check(rc, "kv_read_q4")
     return k, v
 
@@ -807,8 +816,9 @@ def kv_commit_path_q4(k_cache, v_cache, block_table, prefix_len, n_nodes, accept
     if k_cache.dim() > 4 or block_table.dim() != 2:
         raise TsdError("the pools have at most a layer axis; block_table is [B][max_blocks]")
     max_blocks = block_table.shape[1]
-    new_len = new_len if new_len is not None else torch.empty((B,), dtype=i32, device=prefix_len.device)
-    moved = moved if moved is not None else torch.empty((B,), dtype=i32, device=prefix_len.device)
+    device = prefix_len.device
+    new_len, new_len_out = _out_arg(new_len, i32, (B,), "new_len", dev, device)
+    moved, moved_out = _out_arg(moved, i32, (B,), "moved", dev, device)
     rc = lib.tsd_kv_commit_path_q4(
         _arg(k_cache, torch.uint8, None, "k_cache", dev), _arg(v_cache, torch.uint8, None, "v_cache", dev),
         layers, num_blocks * Hkv * 9 * D, _arg(block_table, i32, (B, max_blocks), "block_table", dev),
@@ -816,8 +826,7 @@ def kv_commit_path_q4(k_cache, v_cache, block_table, prefix_len, n_nodes, accept
         _arg(n_nodes, i32, (B,), "n_nodes", dev), _arg(accept_len, i32, (B,), "accept_len", dev),
         _arg(path, i32, (B, D_max + 1), "path", dev), _arg(err, i32, (B,), "err", dev),
         _arg(tail_base, i32, (B,), "tail_base", dev), B, N_max, Hkv, D, D_max,
-        _arg(new_len, i32, (B,), "new_len", dev), _arg(moved, i32, (B,), "moved", dev),
-        _arg(status, i32, None, "status", dev), _raw_stream(dev))
+        new_len_out, moved_out, _arg(status, i32, None, "status", dev), _raw_stream(dev))
     _check(rc, "kv_commit_path_q4")
     return new_len, moved
 
@@ -841,10 +850,11 @@ def tree_attn_fwd_q4(q, k_cache, v_cache, block_table, prefix_len, n_nodes, mask
     dev = _device_of(q)
     max_blocks = block_table.shape[1]
     max_slots = int(max_slots)
-    if out is None:
-        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-    if lse is None and want_lse:
-        lse = torch.empty((B, N_max, Hq), dtype=torch.float32, device=q.device)
+    device = q.device
+    out, out_p = _out_arg(out, torch.bfloat16, q.shape, "out", dev, device)
+    lse_p = None
+    if lse is not None or want_lse:
+        lse, lse_p = _out_arg(lse, torch.float32, (B, N_max, Hq), "lse", dev, device)
     ws, ws_bytes, keep = _workspace_arg(
         workspace, lib.tsd_tree_attn_q4_workspace_bytes(B, N_max, Hq, Hkv, D, max_slots), q, dev)
     rc = lib.tsd_tree_attn_fwd_q4(
@@ -854,9 +864,7 @@ def tree_attn_fwd_q4(q, k_cache, v_cache, block_table, prefix_len, n_nodes, mask
         _arg(prefix_len, i32, (B,), "prefix_len", dev), _arg(n_nodes, i32, (B,), "n_nodes", dev),
         _arg(mask, i32, (B, N_max, (N_max + 31) // 32), "mask", dev), _arg(err, i32, (B,), "err", dev), B,
         N_max, Hq, Hkv, D, max_slots, D ** -0.5 if scale is None else float(scale),
-        _arg(out, torch.bfloat16, q.shape, "out", dev),
-        _arg(lse, torch.float32, (B, N_max, Hq), "lse", dev), ws, ws_bytes,
-        _arg(status, i32, None, "status", dev), _raw_stream(dev))
+        out_p, lse_p, ws, ws_bytes, _arg(status, i32, None, "status", dev), _raw_stream(dev))
     _check(rc, "tree_attn_fwd_q4")
     return out, lse
 
