@@ -669,7 +669,7 @@ constexpr int kTcRangeCost = 9, kRowsRangeCost = 7;
 // / many rows (8 kv heads; rows of one, sequences, keys): 32, 1, 2048: 14 / 27 us; 252,
 // 1, 2048: 23 / 30; 32, 8, 1024: 17 / 28; 64, 1, 8192: 27 / 29; 64, 8, 512: 27 / 24;
 // 64, 8, 1024: 32 / 28; 64, 1, 16384: 39 / 31; 32, 32, 8192: 212 / 163.
-constexpr int64_t kTcMinWork = 3072;
+constexpr int64_t kTcMinWork = 3080;
 
 // Host: how a call is cut up.
 Q4Shape q4_shape(int B, int N_max, int Hq, int Hkv, int D, int max_slots) {
