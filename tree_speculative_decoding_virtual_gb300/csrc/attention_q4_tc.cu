@@ -447,9 +447,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4
         // too, which the issuing thread waits for itself.
         tc_wait(sh.k_full[0], 0, lim, abort);
         for (int j = 0; j < n; ++j) {
-          bool ok = tc_wait(sh.v_full[j & 1], (j >> 1) & 1, lim, abort);
           const int k = j + 1;
-          if (ok && k < n) ok = tc_wait(sh.k_full[k & 1], (k >> 1) & 1, lim, abort);
+          bool ok = k >= n || tc_wait(sh.k_full[k & 1], (k >> 1) & 1, lim, abort);
+          if (ok) ok = tc_wait(sh.v_full[j & 1], (j >> 1) & 1, lim, abort);
           if (ok && j > 0) ok = tc_wait(sh.p_full[0], (j - 1) & 1, lim, abort);
           if (!ok) break;
           mbar_arrive(smem_addr(&sh.p_full[0]));
