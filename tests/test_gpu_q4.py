@@ -863,6 +863,137 @@ def test_logprobs_special_rows(tsd):
             assert (np.abs(a[fine] - b[fine]) <= 65 * 2.0 ** -22 + np.abs(b[fine]) * 2.0 ** -22).all(), (r, a, b)
 
 
+def _masked_rows(rng, V, mask, n):
+    """n rows of V logits, `mask` but for allowed ids that leave out the first
+    chunk of 4096: twelve runs of 32 ids with logits in [0, 8], the even rows'
+    largest ones before id 16384 (before a first settlement can raise the
+    threshold) and all others 2 at most."""
+    x = np.full((n, V), mask, np.float32)
+    for r in range(n):
+        for run in range(12):
+            early = run < 6
+            at = rng.integers(4096, 16384 - 32) if early else rng.integers(16384, V - 32)
+            top = 8.0 if r % 2 or early else 2.0
+            x[r, at:at + 32] = rng.uniform(6.0 if early and r % 2 == 0 else 0.0, top, 32)
+    x[0] = mask  # and two ids alone
+    x[0, [5000, 20000]] = [2, 1]
+    return x
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("mask", [-np.inf, -100.0, -1e4, -1e30, -3.38e38])
+@pytest.mark.parametrize("R,V", [(1, 128256), (20, 128256), (20, 128251), (160, 128256), (1, 262144)])
+def test_logprobs_masked_vocabulary(tsd, R, V, mask, bf16):
+    """Tolerance, in units of 2^-24: a term e^d of a sum has d from -8 to 8 (a
+    reference is the mask, which has no weight next to an allowed logit, or an
+    allowed logit), so 2 * 8 for d and its product with log2 e and 4 for ex2;
+    as much for the factor of a warp and of a CTA; 384 terms and 24 levels of
+    joining: 468 relative in S, so absolute in log S, and with logf's last place
+    (16 at 14), the difference's (16) and the logits' (8) below 512.  The
+    entropy's quotient is 8 at most and off by that much relative in numerator and
+    denominator: 16 * 468 + 512 < 2^13.  Results far off zero round to 2^-24 of
+    themselves, twice."""
+    n = min(R, 6)
+    x = _masked_rows(np.random.default_rng(R + V), V, mask, n)
+    if bf16:
+        bits = gen.bf16_bits(x)
+        x = oracle.bf16_to_f64(bits)
+    rows = np.arange(R) % n
+    logits = bf(bits[rows]) if bf16 else T(x[rows])
+    x = x.astype(np.float64)
+    tokens = np.where(np.arange(n) % 3 == 0, 5000, np.argmax(x, axis=1)).astype(np.int32)
+    want = [ologp.row_logprobs(x[r], int(tokens[r]), 32) for r in range(n)]
+    for k in (0, 1, 5, 20, 32):
+        lp, ent, ids, top = [np_of(t) for t in tsd.token_logprobs(logits, T(tokens[rows]), k=k)]
+        for r in range(R):
+            e_lp, e_ent, e_ids, e_top = want[rows[r]]
+            assert np.array_equal(ids[r], e_ids[:k]), (k, r)
+            for a, e, units in ((lp[r], e_lp, 512), (ent[r], e_ent, 8192), (top[r], e_top[:k], 512)):
+                a, e = np.atleast_1d(a).astype(np.float64), np.atleast_1d(e)
+                fine = np.isfinite(e)
+                assert np.array_equal(np.isneginf(a), np.isneginf(e)), (k, r, a, e)
+                assert (np.abs(a[fine] - e[fine]) <= units * 2.0 ** -24 + np.abs(e[fine]) * 2.0 ** -23).all(), (k, r, a, e)
+
+
+def test_path_logprobs_masked_vocabulary(tsd):
+    """The same rows on an accepted path (tolerance as above)."""
+    V, D_max = 262144, 3
+    x = _masked_rows(np.random.default_rng(4), V, -np.inf, 4).reshape(1, 4, V)
+    best = np.argmax(x, axis=2).astype(np.int32)
+    tokens = np.array([[9, best[0, 0], best[0, 1], best[0, 2]]], np.int32)
+    path, A, bonus = np.array([[1, 2, 3, 4]], np.int32), np.array([3], np.int32), best[:, 3].copy()
+    for k in (0, 1, 5):
+        emitted, lp, ent, ids, top = [np_of(t) for t in tsd.tree_path_logprobs(T(x), T(tokens), T(path), T(A), T(bonus),
+                                                                               None, D_max, k=k)]
+        assert np.array_equal(emitted, best)
+        for s in range(4):
+            e_lp, e_ent, e_ids, e_top = ologp.row_logprobs(x[0, s], int(best[0, s]), k)
+            assert abs(lp[0, s] - e_lp) <= 512 * 2.0 ** -24 and abs(ent[0, s] - e_ent) <= 8192 * 2.0 ** -24, (k, s)
+            fine = np.isfinite(e_top)
+            assert np.array_equal(ids[0, s], e_ids) and np.array_equal(np.isneginf(top[0, s]), ~fine), (k, s)
+            assert (np.abs(top[0, s][fine] - e_top[fine]) <= 512 * 2.0 ** -24).all(), (k, s)
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("V", [40008, 40011])  # through shared memory, and unaligned
+@pytest.mark.parametrize("alone", [True, False])  # a cluster a row, and a CTA a row
+def test_logprobs_special_rows_every_form(tsd, V, alone, bf16):
+    """Masked first chunks, ties, infinities and NaN under every k and in every
+    form of the kernel.  Tolerance, in units of 2^-24 (as for the masked rows):
+    rows climb up to 40 above their reference, so d and its product 80, ex2 4, as much
+    for two factors, 80 terms of a thread's sum, 24 levels: 356; logf, the
+    difference and the logits 96 more: 512.  Entropy: two terms of up to 48, the quotient
+    off by 2 * 356 relative: 48 * 712 + 512 < 2^16."""
+    rng = np.random.default_rng(V)
+    late = np.arange(V) >= 4096
+    rows = []
+    for mask in (-np.inf, -100.0, -1e4, -3.38e38):
+        x = np.full(V, mask)
+        x[[5000, 9001, 20128, 33000]] = [5, 4.5, 4, 3]
+        rows.append(x)
+        rows.append(np.where(late & (rng.random(V) < 0.01), rng.uniform(0, 8, V), mask))
+        rows.append(np.where(late, np.minimum(np.round(rng.standard_normal(V) * 2), 4), mask))
+        x = np.full(V, mask)
+        x[7] = -60
+        x[[4100, 16390, 39990]] = [0, 60, -20]
+        rows.append(x)
+    rows.append(np.full(V, -np.inf))
+    rows.append(np.zeros(V))
+    rows.append(np.arange(V) * (40 / V))
+    rows.append(np.arange(V) * (-40 / V))
+    rows.append(np.arange(V) * (300 / V))
+    for special, at in ((np.nan, 3), (np.nan, 20000), (np.inf, 4), (np.inf, 20000)):
+        x = rng.standard_normal(V)
+        x[[at, 39999]] = special
+        rows.append(x)
+        rows.append(np.where(np.arange(V) == at, special, -np.inf))
+    x = np.array(rows, np.float32)
+    if bf16:
+        bits = gen.bf16_bits(x)
+        x = oracle.bf16_to_f64(bits)
+    n = len(x)
+    x64 = x.astype(np.float64)
+    tokens = np.where(np.arange(n) % 2 == 0, 5000, 20128).astype(np.int32)
+    want = [ologp.row_logprobs(x64[r], int(tokens[r]), 32) for r in range(n)]
+    if alone:
+        calls = [(np.array([r]), (bf(bits[r:r + 1]) if bf16 else T(x[r:r + 1]))) for r in range(n)]
+    else:
+        which = np.arange(3 * n) % n
+        calls = [(which, bf(bits[which]) if bf16 else T(x[which]))]
+    for which, logits in calls:
+        for k in (0, 1, 5, 32):
+            lp, ent, ids, top = [np_of(t) for t in tsd.token_logprobs(logits, T(tokens[which]), k=k)]
+            for i, r in enumerate(which):
+                e_lp, e_ent, e_ids, e_top = want[r]
+                assert np.array_equal(ids[i], e_ids[:k]), (k, r)
+                for a, e, units in ((lp[i], e_lp, 512), (ent[i], e_ent, 65536), (top[i], e_top[:k], 512)):
+                    a, e = np.atleast_1d(a).astype(np.float64), np.atleast_1d(e)
+                    fine = np.isfinite(e)
+                    assert np.array_equal(np.isnan(a), np.isnan(e)), (k, r, a, e)
+                    assert np.array_equal(np.isneginf(a), np.isneginf(e)), (k, r, a, e)
+                    assert (np.abs(a[fine] - e[fine]) <= units * 2.0 ** -24 + np.abs(e[fine]) * 2.0 ** -23).all(), (k, r, a, e)
+
+
 def test_logprobs_chosen_rows(tsd):
     rng = np.random.default_rng(10)
     x = rng.standard_normal((6, 501)).astype(np.float32)

@@ -21,7 +21,9 @@
 // registers: 20 best 103 / 115 us, 1 best as long, none 99 / 95.)
 //   reference  the maximum of the CTA's first chunk is the m of its sums; a warp
 //              that meets a value more than 40 above its m moves it (e^40 leaves
-//              fp32 sums far from overflow)
+//              fp32 sums far from overflow), whether it is among the k best or
+//              not: with a masked first chunk m is the mask's value, and the
+//              threshold, which all warps raise, says nothing about a warp's own m
 //   threshold  the k-th largest of the 256 threads' maxima over the first chunk:
 //              at least k values reach it, so only what does can be among the k
 //              best.  For independent logits hardly more than k of 4096 do.
@@ -500,10 +502,18 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const LpArgs a)
       if (above == k - 1) sh.thr = o;
     }
     __syncthreads();
-    // what reaches `gate` passes (without alternatives: what moves the reference)
-    uint32_t thr_ord = k > 0 ? sh.thr : ordered(m + kMove);
-    float gate = unordered(thr_ord);
+    // What reaches `gate` is looked at: it may be listed (it reaches the threshold; a
+    // settled one it has to pass), or it moves the reference (it is above m + 40, as
+    // rounded: for a mask of -1e30 above m, for one of -inf anything else).  Both
+    // bounds can be beyond the largest number; then +inf itself is looked at.
+    uint32_t thr_ord = k > 0 ? sh.thr : 0xFFFFFFFFu;
     bool settled = false;
+    auto gate_of = [&] {
+      const float moves = unordered(ordered(m + kMove) + 1u);
+      const float lists = unordered(settled && thr_ord != 0xFFFFFFFFu ? thr_ord + 1u : thr_ord);
+      return fminf(fminf(lists, moves), INFINITY);  // (of a NaN and a number the number)
+    };
+    float gate = gate_of();
     int next_settle = first + 4 * kChunk;
 
     unsigned long long S2 = 0ull, T2 = 0ull;  // two sums each
@@ -550,6 +560,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const LpArgs a)
         T2 = f == 0.f ? 0ull : f2_pack(f * (t.x + s.x * (m - up)), f * (t.y + s.y * (m - up)));
         S2 = f2_pack(f * s.x, f * s.y);
         m = up;
+        gate = gate_of();
       }
       // d = -200 stands for every d that e^d rounds to zero for, -inf included; a
       // NaN reaches S and T through e^d, and so does +inf (m = +inf: inf - inf)
@@ -567,7 +578,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const LpArgs a)
         settled = settle<kBf16>(sh, src, first, end, k, settled);
         if (settled) {
           thr_ord = sh.thr;
-          gate = unordered(thr_ord == 0xFFFFFFFFu ? thr_ord : thr_ord + 1u);
+          gate = gate_of();
         }
         next_settle = first + 4 * (next_settle - first);
       }
@@ -594,7 +605,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const LpArgs a)
       T = 0.f;
       for (int w = 0; w < kLpWarps; ++w) {
         const float r = sh.ref[w];
-        // (a reference of -inf: nothing but -inf, or NaN)
+        // (a reference of -inf: nothing but -inf, or NaN, since all else moves it)
         const float f = r == M || r == -INFINITY ? 1.f : ex2_approx((r - M) * kLog2e);
         const float by = r == M || r == -INFINITY ? 0.f : r - M;
         S += f * sh.sum[w];
