@@ -595,9 +595,12 @@ int tsd_budget_select(const float *rho, int B, int N_max, const float *cost, flo
  *   i < n_b, -1 beyond and for sequences not served: what tsd_kv_write_q4
  *   takes.
  * tsd_kv_blocks_release: gives back the blocks past ceil(keep_len[b] / 16)
- *   (0: all of them), so that it undoes a build exactly: the blocks given back
+ *   (0: all of them), so that it undoes a build (exactly, where every id taken
+ *   names a block of the pool): the blocks given back
  *   are numbered the same way, of `all` of them number i becomes
- *   free_list[*free_count + all - 1 - i].  Their table entries become -1.
+ *   free_list[*free_count + all - 1 - i].  Their table entries become -1.  An
+ *   entry outside [0, num_blocks) goes onto the list as it stands
+ *   (TSD_STATUS_BAD_PAGE), where the build that takes it reports it again.
  *
  * prefix_len, keep_len int32 [B]; n_new int32 [B] or NULL (N_max each);
  * block_table int32 [B][max_blocks], held int32 [B], free_list int32

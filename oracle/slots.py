@@ -4,7 +4,8 @@ A sequence of P + n tokens wants ceil((P + n) / 16) blocks; what it does not
 hold is popped from the free list (a stack), in sequence order and then table
 order.  The sequences are served in order as long as the needs so far fit;
 from the first one that does not fit on, only sequences that need nothing are
-served.  Releasing pushes blocks so that it undoes the pops exactly.
+served.  Releasing pushes blocks so that it undoes the pops exactly (a popped id
+that names no block of the pool is -1 in the table, and comes back as that).
 """
 
 from __future__ import annotations
@@ -75,6 +76,8 @@ def blocks_release(keep_len, block_table, held, free_list, free_count):
     if not 0 <= count <= len(free) or len(given) > len(free) - count:
         return table, held, free, count, status | BAD_LEN
     for i, (b, j) in enumerate(given):
+        if not 0 <= table[b, j] < len(free):
+            status |= BAD_PAGE
         free[count + len(given) - 1 - i] = table[b, j]
         table[b, j] = -1
     return table, after, free, count + len(given), status

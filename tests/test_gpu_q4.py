@@ -248,6 +248,48 @@ def test_slots_fail_closed(tsd, B):
         assert np.array_equal(np_of(d[1]), h) and int(d[3].item()) == c, case
 
 
+@pytest.mark.parametrize("B", [3, 70])  # a cluster, and scan and fill
+def test_release_reports_bad_blocks(tsd, B):
+    """A block id outside the pool that comes back is reported, keeps its place on
+    the list as it stands, and is met again by the build that takes it."""
+    rng = np.random.default_rng(B)
+    blocks = 4 * B
+    table, held = np.full((B, 4), -1, np.int32), np.ones(B, np.int32)
+    table[:, 0] = np.arange(B)
+    free = np.concatenate([rng.permutation(np.arange(B, blocks)), np.zeros(B)]).astype(np.int32)
+    count = blocks - B
+    free[[count - 1, count - 2 * B]] = [10 ** 6, -7]  # taken first and last
+    table[B - 1, 0] = blocks
+    d = [T(x) for x in (table, held, free, np.array([count], np.int32))]
+    P = np.full(B, 16, np.int32)
+    zero = np.zeros(B, np.int32)
+
+    def build():
+        nonlocal table, held, count
+        st = status_word()
+        got = tsd.kv_slots_build(T(P), None, 32, *d, status=st)
+        slots, table, held, count, s = oslots.slots_build(P, None, 32, table, held, free, count)
+        assert int(st.item()) == s == tsd.STATUS_BAD_PAGE
+        assert np.array_equal(np_of(got), slots) and np.array_equal(np_of(d[0]), table)
+
+    def release(keep):
+        nonlocal table, held, free, count
+        st = status_word()
+        tsd.kv_blocks_release(T(keep), *d, status=st)
+        table, held, free, count, s = oslots.blocks_release(keep, table, held, free, count)
+        assert int(st.item()) == s
+        for a, b in zip(d, (table, held, free, np.array([count]))):
+            assert np.array_equal(np_of(a), b)
+        return s
+
+    build()
+    assert release(np.full(B, 16, np.int32)) == tsd.STATUS_BAD_PAGE
+    assert free[count - 1] == -1 and free[count - 2 * B] == -1
+    build()
+    assert release(zero) == tsd.STATUS_BAD_PAGE and count == blocks and (free == blocks).sum() == 1
+    assert release(zero) == 0  # nothing comes back
+
+
 # ---------------------------------------------------------------------------
 # attention
 # ---------------------------------------------------------------------------

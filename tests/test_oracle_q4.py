@@ -88,6 +88,14 @@ def test_slots_fail_closed():
     assert st == slots.BAD_LEN and h.tolist() == [0, 9, 0] and c == 4
 
 
+def test_release_reports_bad_blocks():
+    table, free = np.array([[2, -1, 9], [7, 1, 0]], np.int32), np.array([3, 0, 0, 0, 0, 0, 0], np.int32)
+    t, h, f, c, st = slots.blocks_release([16, 32], table, np.array([3, 3]), free, 1)
+    assert st == slots.BAD_PAGE and c == 4 and f[:4].tolist() == [3, 0, 9, -1]
+    assert t.tolist() == [[2, -1, -1], [7, 1, -1]] and h.tolist() == [1, 2]  # (the bad id 7 stays held)
+    assert slots.blocks_release([48, 32], table, np.array([3, 3]), free, 1)[4] == 0
+
+
 def test_logprobs_against_torch():
     rng = np.random.default_rng(3)
     x = rng.standard_normal(1000) * 3

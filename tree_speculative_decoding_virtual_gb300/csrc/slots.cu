@@ -230,17 +230,23 @@ __device__ __forceinline__ void fill_sequence(const SlotArgs &a, int b, int64_t 
 }
 
 // Gives blocks [keep, held) of sequence b back and clears their entries; `after`: free
-// blocks when the call is done.
+// blocks when the call is done.  An entry that names no block of the pool (the build
+// left -1 for such an id) takes its place on the list as it stands, so that the
+// numbering holds, and is reported.
 __device__ __forceinline__ void release_sequence(const SlotArgs &a, int b, int64_t start, int keep,
                                                  int held, int worker, int workers, int after) {
   if (start < 0) return;
   // the call's last given-back block is number all - 1 and lands at the old count
   const int top = after - 1;
+  bool bad = false;
   for (int j = keep + worker; j < held; j += workers) {
     int32_t *e = a.table + (size_t)b * a.max_blocks + j;
-    a.free_list[top - (start + (j - keep))] = *e;
+    const int id = *e;
+    bad |= id < 0 || id >= a.num_blocks;
+    a.free_list[top - (start + (j - keep))] = id;
     *e = -1;
   }
+  if (bad && a.status) atomicOr(a.status, TSD_STATUS_BAD_PAGE);
 }
 
 // Taking, small calls: everything in one block.
