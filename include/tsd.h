@@ -589,8 +589,9 @@ int tsd_budget_select(const float *rho, int B, int N_max, const float *cost, flo
  *   need_b = max(0, ceil((P_b + n_b) / 16) - held_b) blocks are taken.  The
  *   blocks a call takes are numbered by sequence, then by position in the
  *   table; number i is free_list[*free_count - 1 - i].  A sequence is served
- *   iff the needs of the sequences up to and including it fit *free_count; one
- *   that is not takes nothing and sets TSD_STATUS_NO_BLOCK.
+ *   iff it needs no block or the needs of the sequences up to and including it
+ *   fit *free_count; one that is not takes nothing and sets
+ *   TSD_STATUS_NO_BLOCK.
  *   slots[b][i] = the pool slot (block id * 16 + row) of token P_b + i for
  *   i < n_b, -1 beyond and for sequences not served: what tsd_kv_write_q4
  *   takes.

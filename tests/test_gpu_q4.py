@@ -248,6 +248,24 @@ def test_slots_fail_closed(tsd, B):
         assert np.array_equal(np_of(d[1]), h) and int(d[3].item()) == c, case
 
 
+@pytest.mark.parametrize("count_ok", [True, False])
+@pytest.mark.parametrize("B", [3, 70])  # one block, and scan and fill
+def test_slots_of_a_sequence_that_needs_no_block(tsd, B, count_ok):
+    """Behind sequences whose needs no longer fit, and with a count that is refused."""
+    P = np.where(np.arange(B) % 3 == 2, 10, 16).astype(np.int32)
+    table, held = np.full((B, 3), -1, np.int32), np.ones(B, np.int32)
+    table[:, 0] = np.arange(B)
+    free, count = np.full(B + 1, B, np.int32), 1 if count_ok else -1
+    n = np.where(np.arange(B) % 3 == 2, 6, 20).astype(np.int32)
+    d = [T(x) for x in (table, held, free, np.array([count], np.int32))]
+    st = status_word()
+    got = np_of(tsd.kv_slots_build(T(P), T(n), 20, *d, status=st))
+    slots, t, h, c, s = oslots.slots_build(P, n, 20, table, held, free, count)
+    assert int(st.item()) == s == (tsd.STATUS_NO_BLOCK if count_ok else tsd.STATUS_BAD_LEN)
+    assert np.array_equal(got, slots) and np.array_equal(np_of(d[0]), t) and np.array_equal(np_of(d[1]), h)
+    assert int(d[3].item()) == c == count and (got[2::3, :6] >= 0).all() and (got[0::3] == -1).all()
+
+
 @pytest.mark.parametrize("B", [3, 70])  # a cluster, and scan and fill
 def test_release_reports_bad_blocks(tsd, B):
     """A block id outside the pool that comes back is reported, keeps its place on

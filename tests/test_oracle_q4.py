@@ -88,6 +88,13 @@ def test_slots_fail_closed():
     assert st == slots.BAD_LEN and h.tolist() == [0, 9, 0] and c == 4
 
 
+def test_slots_of_a_sequence_that_needs_no_block():
+    table, free = np.array([[0, -1, -1], [1, -1, -1], [2, -1, -1]], np.int32), np.array([3, 0, 0, 0], np.int32)
+    s, t, h, c, st = slots.slots_build([16, 16, 10], [20, 4, 4], 20, table, [1, 1, 1], free, 1)
+    assert st == slots.NO_BLOCK and (s[0] == -1).all() and (s[1] == -1).all()  # (the first one's need counts on)
+    assert s[2].tolist() == [42, 43, 44, 45] + [-1] * 16 and h.tolist() == [1, 1, 1] and c == 1
+
+
 def test_release_reports_bad_blocks():
     table, free = np.array([[2, -1, 9], [7, 1, 0]], np.int32), np.array([3, 0, 0, 0, 0, 0, 0], np.int32)
     t, h, f, c, st = slots.blocks_release([16, 32], table, np.array([3, 3]), free, 1)

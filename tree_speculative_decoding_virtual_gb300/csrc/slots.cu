@@ -9,10 +9,10 @@
 // The pool's unused blocks are a stack, free_list[0 .. free_count).  With
 // want_b = ceil((P_b + n_b) / 16) and need_b = max(0, want_b - held_b), the
 // blocks taken are numbered by sequence, then by position in its table: the
-// i-th is free_list[free_count - 1 - i].  A sequence is served when its whole
-// need fits under an exclusive scan of the needs, so the result does not
-// depend on the order in which threads run; giving blocks back numbers them
-// the same way and undoes a take exactly.
+// i-th is free_list[free_count - 1 - i].  A sequence is served when it needs no
+// block or its whole need fits under an exclusive scan of the needs, so the
+// result does not depend on the order in which threads run; giving blocks back
+// numbers them the same way and undoes a take exactly.
 //
 // Nothing here is bound by bandwidth in a decoding step: the scan over the
 // batch is one block's, and the map (4 bytes a token) is written by a second
