@@ -707,7 +707,8 @@ def kv_slots_build(prefix_len, n_new, N_max, block_table, held, free_list, free_
 def kv_blocks_release(keep_len, block_table, held, free_list, free_count, workspace=None, status=None):
     """Gives the blocks past the first keep_len[b] tokens of each sequence back
     to the free list (arguments as kv_slots_build; keep_len 0 frees a
-    sequence)."""
+    sequence).  A block id outside the pool comes back as it stands, with
+    STATUS_BAD_PAGE."""
     B = keep_len.shape[0]
     i32 = torch.int32
     dev = _device_of(keep_len)

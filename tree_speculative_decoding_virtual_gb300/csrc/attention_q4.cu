@@ -19,12 +19,12 @@
 // with fp16 operands and fp32 accumulation (m16n8k16).  Decoded values are
 // exact in fp16.  q (bf16) is scaled per row by a power of two that brings
 // its largest magnitude to [2^13, 2^14) and then converted: exact for every
-// element within 2^-27 of that magnitude, below which the rounding (2^-25 of
-// fp16's smallest normal) is lost in the fp32 accumulation anyway; the power
-// goes into the softmax's factor.  P lies in (0, 2^15] (the reference m is 8
-// above the row's first maximum and follows when a score passes it by 7), so
-// fp16 keeps 11 bits of every probability down to 2^-22 of the largest, 3
-// bits more than bf16 would; the row sum uses the unrounded fp32 values.
+// element within 2^-27 of that magnitude, below which the rounding (2^-25
+// absolute) is lost in the fp32 accumulation anyway; the power goes into the
+// softmax's factor.  P lies in (0, 2^15] (the reference m is 8 below the row's
+// first maximum and follows when a score passes that maximum by 7), so fp16
+// keeps 11 bits of every probability down to 2^-22 of the largest, 3 bits more
+// than bf16 would; the row sum uses the unrounded fp32 values.
 //
 // Operand layout.  The contraction index of an MMA may be permuted freely, so
 // lane (i, t) = (lane / 4, lane % 4) takes, as A rows i and i + 8 of K, D/4
@@ -39,7 +39,10 @@
 //
 // Measured (device time): one token behind 4096 keys, 32 query and 8 kv heads of 128: 9 us; 32
 // tokens behind 512 to 16384 keys, 64 / 8 heads: 70 us for 312 MB (66% of the copy
-// bandwidth); behind 16384 each, 32 / 8 heads: 111 us for 604 MB (80%).  A warp takes two
+// bandwidth); behind 16384 each, 32 / 8 heads: 111 us for 604 MB (80%).  Batches of 128 and
+// 256 tokens behind 512 to 16384 keys, 64 / 8 heads, in uniform pieces: 252 and 455 us (73
+// and 81%), with a bound of 131072 keys 262 and 455; 65 tokens 139, with that bound 170 (64
+// tokens, planned: 125 with any bound).  A warp takes two
 // pages at a time (with up to 8 rows; more would not leave the registers): one at a
 // time, with some 350 instructions a page, the three took 9, 75 and 125 us, the copies
 // of the second alone 56 and its arithmetic alone 66; and of that kernel ten

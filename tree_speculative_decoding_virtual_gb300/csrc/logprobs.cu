@@ -17,8 +17,8 @@
 // alternatives they come through a ring in shared memory, three chunks ahead: it keeps
 // the stream going while the CTA settles its first chunk, and what passes the
 // threshold is looked up there.  Without, and where rows are not aligned to 16
-// bytes, the next 16 are on the way to registers.  (1216 rows of 128256 fp32, ring /
-// registers: 20 best 103 / 115 us, 1 best as long, none 99 / 95.)
+// bytes, the next 16 are on the way to registers.  (Rows of 128256 fp32, ring /
+// registers: 1216 rows, 20 best 106 / 114 us, none 102 / 95; 508 rows, 1 best 51 / 49.)
 //   reference  the maximum of the CTA's first chunk is the m of its sums; a warp
 //              that meets a value more than 40 above its m moves it (e^40 leaves
 //              fp32 sums far from overflow), whether it is among the k best or
@@ -35,7 +35,9 @@
 // Values that equal the first threshold are listed apart: where there are more
 // of them than that list holds (masked vocabularies), the first ones in id order
 // are looked up.  Where more pass than the list holds, the slice is taken again
-// at the end, chunk by chunk, each chunk's k-th largest value found bit by bit.
+// at the end, chunk by chunk, each chunk's k-th largest value found bit by bit
+// (508 rows of 128256 with the first 4096 logits masked and a tenth of the others
+// not: 0.9 ms; with a tenth of all, as long as without a mask).
 // The CTAs' results meet through distributed shared memory; nothing is written
 // but the outputs.
 
@@ -145,7 +147,7 @@ __device__ __forceinline__ int chunk_pos(int e, int tid) {
   return ((e / kW) * kLpThreads + tid) * kW + e % kW;
 }
 
-// The thread's part of [c0, end) as loaded: 32 fp32 words, or 16 of bf16 pairs
+// The thread's part of [c0, end) as loaded: 16 fp32 words, or 8 of bf16 pairs
 // (one word a logit without vector loads); -inf past the end.
 template <bool kBf16, bool kVec>
 struct LpRaw {
