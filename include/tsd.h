@@ -735,6 +735,95 @@ int tsd_tree_path_logprobs(const void *logits, int bf16, const int32_t *tokens, 
                            float *entropy, int32_t *top_ids, float *top_logprobs, int32_t *status,
                            tsd_stream_t stream);
 
+/*
+ * Keys and values into the paged cache, with the norms and the position rotation
+ * of queries and keys on the way ([EP-zh] 2.1: a branch's entries are written
+ * behind the committed prefix, node i at position P_b + depth).
+ *
+ * For token t < T, with fp32 arithmetic and one rounding to bf16:
+ *   norm      y = x / sqrt(mean(x^2) + eps) * weight for each head's row of q
+ *             (q_weight) and of k (k_weight), bf16 [D]; a NULL weight: no norm.
+ *   rotation  of the first R columns of each such row (0: none; a multiple of 32, at
+ *             most D): for f < R / 2 columns (f, R/2 + f), or with `interleaved`
+ *             (2f, 2f + 1), as (a cos - b sin, b cos + a sin) with the angle
+ *             p * inv_freq[f], cos and sin times rot_scale.  The angle is
+ *             exact to 2^-24 of a turn for every position.
+ *   position  p = pos[axis][t] + base[t / per_base], axis = freq_axis[f].
+ *             pos int32 [axes][T] (NULL: t % per_base, the place in the sequence);
+ *             base int32 [ceil(T / per_base)] or NULL (0); freq_axis int32 [R/2]
+ *             or NULL (axis 0; so does an entry outside [0, axes)), 1 <= axes <= 4:
+ *             the axes of images and video are time, height and width.  With pos = the
+ *             depths of tsd_tree_build_ancestors, base = prefix_len and per_base =
+ *             N_max this is P_b + depth.
+ *   append    k and v of the token go to pool slot slots[t] (as tsd_kv_slots_build gives
+ *             them; -1: not stored; any other outside the pool neither, with
+ *             TSD_STATUS_BAD_PAGE).  The slots of one call must differ.  Every
+ *             token's queries go to q_out.
+ * q [T][Hq][D], k and v [T][Hkv][D], q_out: a token's rows are contiguous, tokens
+ * *_stride elements apart (multiples of 8).  q_out may be q itself with its stride,
+ * and overlaps no input otherwise.  Hq 0: no queries (q and q_out NULL).
+ * tsd_kv_append_rope_q4: the same into the 4-bit cache below; the bf16 rows are
+ * quantised as tsd_kv_write_q4 does (TSD_STATUS_NONFINITE as there).
+ * All bf16 arrays and caches are 16-byte aligned.  One launch, no workspace.
+ */
+int tsd_kv_append_rope(const uint16_t *q, int64_t q_stride, const uint16_t *k, int64_t k_stride,
+                       const uint16_t *v, int64_t v_stride, const int32_t *slots, int64_t T, int Hq,
+                       int Hkv, int D, const float *inv_freq, int R, const int32_t *freq_axis,
+                       int axes, int interleaved, float rot_scale, const int32_t *pos,
+                       const int32_t *base, int64_t per_base, const uint16_t *q_weight,
+                       const uint16_t *k_weight, float eps, int num_blocks, uint16_t *k_cache,
+                       uint16_t *v_cache, uint16_t *q_out, int64_t q_out_stride, int32_t *status,
+                       tsd_stream_t stream);
+int tsd_kv_append_rope_q4(const uint16_t *q, int64_t q_stride, const uint16_t *k, int64_t k_stride,
+                          const uint16_t *v, int64_t v_stride, const int32_t *slots, int64_t T, int Hq,
+                          int Hkv, int D, const float *inv_freq, int R, const int32_t *freq_axis,
+                          int axes, int interleaved, float rot_scale, const int32_t *pos,
+                          const int32_t *base, int64_t per_base, const uint16_t *q_weight,
+                          const uint16_t *k_weight, float eps, int num_blocks, uint8_t *k_cache,
+                          uint8_t *v_cache, uint16_t *q_out, int64_t q_out_stride, int32_t *status,
+                          tsd_stream_t stream);
+
+/*
+ * Sampling with temperature, top-k, top-p and min-p ([Blog] modified rejection
+ * sampling: the draft tokens are drawn from the distribution that the verification
+ * then divides by).
+ *
+ * For a row x of V logits: m = max x, d = (x - m) * (1 / T), w = exp(d), all fp32.
+ * Tokens are ranked by (logit descending, id ascending), -inf left out; of the
+ * ranks r = 0, 1, ... these are kept, one filter after the other:
+ *   top-k  r < k                       (k <= 0 or >= V: off)
+ *   top-p  the sum of w over ranks 0..r-1 is below p times the sum over what top-k
+ *          left; rank 0 always        (p >= 1: off)
+ *   min-p  w >= min(min_p, 1)          (min_p <= 0: off; the largest w is 1)
+ * T below 2^-126 (0, for instance) keeps rank 0 alone, undivided.  The sums are exact
+ * to 2^-43 a token, so the result does not depend on how a row is cut up.
+ *
+ * tsd_token_sample: `draws` tokens of each of R rows: tokens[r][i] = the first
+ *   kept id whose cumulative weight, in id order, exceeds u[r][i] times the sum of
+ *   what is kept (u in [0, 1)); logprob = d - log(that sum), the token's log
+ *   probability under the filtered distribution.  Row rows[r] of logits [num_rows][V]
+ *   (NULL: r); rows[r] = -1: token -1, logprob 0; any other outside
+ *   [0, num_rows) too, with TSD_STATUS_BAD_PATH.
+ * tsd_logits_filter: out float [R][V]: d where kept, -inf elsewhere (what
+ *   tsd_tree_verify_stochastic takes as logits: its softmax is the filtered
+ *   distribution), or with `probs` that distribution (its q_draft).  out may
+ *   be the logits themselves when those are float; otherwise it must not overlap them.
+ * A row of only -inf has token -1, logprob -inf (out: -inf, or 0); a row with a NaN
+ * or +inf token -1 and NaN, with TSD_STATUS_NONFINITE.
+ *
+ * logits float (bf16 == 0) or bf16; temperature, top_p, min_p float, top_k int32,
+ * each NULL (off) or [ceil(R / per_param)]: entry r / per_param is row r's.
+ * Limits: V <= 262144, draws <= 64, R <= 2^24.
+ * One launch, no workspace: a cluster of up to 8 CTAs a row.
+ */
+int tsd_token_sample(const void *logits, int bf16, const int32_t *rows, int R, int64_t num_rows, int V,
+                     const float *u, int draws, const float *temperature, const int32_t *top_k,
+                     const float *top_p, const float *min_p, int per_param, int32_t *tokens,
+                     float *logprob, int32_t *status, tsd_stream_t stream);
+int tsd_logits_filter(const void *logits, int bf16, int R, int V, int probs, const float *temperature,
+                      const int32_t *top_k, const float *top_p, const float *min_p, int per_param,
+                      float *out, int32_t *status, tsd_stream_t stream);
+
 #ifdef __cplusplus
 } /* extern "C" */
 #endif

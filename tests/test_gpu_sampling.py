@@ -1,0 +1,236 @@
+"""Sampling and the filtered distribution against the fp64 oracle.
+
+Tolerance.  A weight e^d, d = (x - m) fl(1/T), carries three roundings of d (3 2^-24
+|d|) and expf's error (2^-22).  Weights below 2^-44 do not count, so |d| <= 31 where it
+matters: below 2^-17 relative.  Sums are exact to V 2^-44 <= 2^-26.  A border or a
+draw compares two such sums: it may go either way within 2^-16.  Log probabilities:
+|d| 3 2^-24 + 2^-16 (the sum's) and one rounding.
+"""
+
+import numpy as np
+import pytest
+
+from oracle import sampling as osa
+
+pytestmark = pytest.mark.gpu
+TOL = 2.0 ** -16
+
+
+@pytest.fixture(scope="module")
+def tsd():
+    import tree_speculative_decoding_virtual_gb300 as m
+    return m
+
+
+def T(a, dtype=None):
+    from _gpu_path import dev_tensor
+    return dev_tensor(a, dtype)
+
+
+def rows_of(rng, R, V, kind):
+    x = rng.standard_normal((R, V)).astype(np.float32) * 2
+    if kind == "peaked":
+        up = rng.integers(0, V, (R, max(1, V // 500)))
+        np.put_along_axis(x, up, (3 * rng.exponential(size=up.shape) + 2).astype(np.float32), 1)
+    elif kind == "ties":
+        x = np.round(x)
+    elif kind == "equal":
+        x[:] = 1.5
+    elif kind == "masked":
+        x[rng.random((R, V)) < 0.9] = -np.inf
+        x[:, V // 2] = 0.0
+    elif kind == "wide":
+        x *= 40
+    elif kind == "lowest":  # masked with the type's lowest value
+        x[rng.random((R, V)) < 0.5] = np.finfo(np.float32).min
+        x[:, V // 3] = 1.0
+    return x
+
+
+SETTINGS = [(1.0, 0, 1.0, 0.0), (0.7, 50, 1.0, 0.0), (1.0, 0, 0.9, 0.0), (1.3, 1000, 0.95, 0.0), (1.0, 0, 1.0, 0.05),
+            (0.8, 40, 0.5, 0.02), (0.0, 0, 0.9, 0.5), (1.0, 1, 1.0, 0.0), (1.0, 0, 0.0, 0.0), (1.0, 0, 1e-6, 0.0),
+            (1.0, 0, 0.99999, 0.0), (2.0, 0, 1.0, 1.0), (1e-3, 0, 0.99, 0.0), (1.0, 7, 0.999, 0.0), (1.0, 0, 1.0, 3.0)]
+
+
+def check_row(x, setting, row, probs, tokens, logprob, u):
+    """The filtered row, the probabilities and the draws of one row."""
+    t, k, p, m = setting
+    order = osa.ranking(x)
+    kept = np.flatnonzero(row > -np.inf)
+    n = len(kept)
+    assert set(kept) == set(order[:n]), "not a prefix of the ranking"
+    lo, hi = osa.kept_bounds(x, t, k, p, m, TOL)
+    assert lo <= n <= hi, (setting, lo, n, hi)
+    d, w = osa.weights(x, t)
+    assert (np.abs(row[kept] - d[kept]) <= 3 * 2.0 ** -24 * np.abs(d[kept])).all()
+    total = w[kept].sum()
+    d = np.where(x > -np.inf, d, 0.0)
+    want = np.zeros(len(x))
+    want[kept] = w[kept] / total
+    assert (np.abs(probs - want) <= (TOL + 3 * 2.0 ** -24 * np.abs(d)) * want + 2.0 ** -100).all()
+    for token, lp, v in zip(tokens, logprob, u):
+        assert osa.draw_ok(x, kept, token, float(v), t, TOL), (setting, token, v)
+        ref = d[token] - np.log(total)
+        assert abs(lp - ref) <= 3 * 2.0 ** -24 * abs(d[token]) + TOL + 2.0 ** -22 * abs(ref)
+
+
+@pytest.mark.parametrize("V,kind,bf16", [
+    (1, "plain", False), (2, "plain", False), (33, "plain", True), (1000, "ties", False), (1000, "equal", True),
+    (4097, "peaked", False), (5003, "masked", True), (32000, "peaked", False), (32000, "ties", True),
+    (32768, "equal", False), (50257, "wide", False), (128256, "peaked", False), (128256, "plain", False),
+    (128256, "plain", True), (20001, "lowest", False), (262144, "peaked", True), (262144, "ties", False)])
+def test_filters_and_draws(tsd, V, kind, bf16):
+    import torch
+    R = len(SETTINGS)
+    rng = np.random.default_rng(V + R + len(kind))
+    x = rows_of(rng, R, V, kind)
+    if bf16:
+        x = torch.from_numpy(x).bfloat16().float().numpy()
+    logits = T(x).bfloat16() if bf16 else T(x)
+    t, k, p, m = [T(np.array([s[i] for s in SETTINGS], np.int32 if i == 1 else np.float32)) for i in range(4)]
+    u = rng.random((R, 5)).astype(np.float32)
+    u[:, 0], u[:, 1] = 0.0, np.float32(1 - 2.0 ** -24)
+    args = dict(temperature=t, top_k=k, top_p=p, min_p=m)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    tokens, lp = tsd.token_sample(logits, T(u), status=st, **args)
+    rows = tsd.logits_filter(logits, status=st, **args)
+    probs = tsd.logits_filter(logits, probs=True, status=st, **args)
+    assert int(st.item()) == 0
+    tokens, lp, rows, probs = [a.cpu().numpy() for a in (tokens, lp, rows, probs)]
+    for r, setting in enumerate(SETTINGS):
+        f32 = tuple(float(np.float32(s)) if i != 1 else s for i, s in enumerate(setting))
+        check_row(x[r].astype(np.float64), f32, rows[r].astype(np.float64), probs[r].astype(np.float64), tokens[r], lp[r], u[r])
+    # ties are cut by id, exactly, and in-place filtering gives the same
+    if not bf16:
+        again = logits.clone()
+        assert tsd.logits_filter(again, out=again, **args) is again
+        assert np.array_equal(again.cpu().numpy(), rows)
+
+
+@pytest.mark.parametrize("V,k,p", [(1000, 10, 1.0), (30000, 777, 1.0), (30000, 0, 0.25), (262144, 100000, 1.0), (1024, 0, 0.5)])
+def test_equal_logits_are_cut_by_id(tsd, V, k, p):
+    """All weights are 1, sums are whole: the kept ids are exactly the first ones, and so is a draw's."""
+    x = T(np.full((2, V), -3.25, np.float32))
+    args = dict(top_k=T(np.array([k, k], np.int32)), top_p=T(np.array([p, p], np.float32)))
+    n = k if k else int(np.ceil(p * V))
+    row = tsd.logits_filter(x, **args).cpu().numpy()
+    assert (row[:, :n] == 0).all() and np.isneginf(row[:, n:]).all()
+    u = np.array([[0.0, 0.5, 1 - 2.0 ** -24], [0.25, 0.75, 0.125]], np.float32)
+    tokens, _ = tsd.token_sample(x, T(u), **args)
+    assert np.array_equal(tokens.cpu().numpy(), np.floor(u.astype(np.float64) * n).astype(np.int32))
+
+
+def test_zero_signs_tie(tsd):
+    x = np.full((1, 64), -5.0, np.float32)
+    x[0, [10, 20, 30]] = [-0.0, 0.0, -0.0]
+    row = tsd.logits_filter(T(x), top_k=T(np.array([2], np.int32))).cpu().numpy()
+    assert list(np.flatnonzero(row[0] > -np.inf)) == [10, 20]
+
+
+def test_special_rows(tsd):
+    import torch
+    V = 5000
+    x = np.random.default_rng(0).standard_normal((6, V)).astype(np.float32)
+    x[0] = -np.inf
+    x[1, 4000] = np.nan
+    x[2, 17] = np.inf
+    x[3] = -np.inf
+    x[3, V - 1] = -7.0  # a single token
+    x[4, :] = np.finfo(np.float32).max
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    u = T(np.full((6, 2), 0.5, np.float32))
+    p = T(np.full(6, 0.9, np.float32))
+    tokens, lp = [a.cpu().numpy() for a in tsd.token_sample(T(x), u, top_p=p, status=st)]
+    assert int(st.item()) == tsd.STATUS_NONFINITE
+    assert (tokens[:3] == -1).all() and np.isneginf(lp[0]).all() and np.isnan(lp[1:3]).all()
+    assert (tokens[3] == V - 1).all() and (lp[3] == 0).all()
+    assert (tokens[4] == int(0.5 * np.ceil(np.float64(np.float32(0.9)) * V))).all() and (tokens[5] >= 0).all()
+    row = tsd.logits_filter(T(x), top_p=p).cpu().numpy()
+    pr = tsd.logits_filter(T(x), top_p=p, probs=True).cpu().numpy()
+    assert np.isneginf(row[0]).all() and np.isnan(row[1:3]).all() and (pr[0] == 0).all() and np.isnan(pr[1:3]).all()
+    assert row[3, V - 1] == 0 and np.isneginf(row[3, :-1]).all() and pr[3, V - 1] == 1
+    # masked by the lowest value and by -inf alike: what is not masked is drawn
+    st.zero_()
+    tokens, _ = tsd.token_sample(T(x[4:]), u[4:], status=st)
+    assert int(st.item()) == 0
+
+
+def test_chosen_rows_and_shared_settings(tsd):
+    import torch
+    rng = np.random.default_rng(3)
+    x = rows_of(rng, 12, 3001, "peaked")  # odd: rows start at every alignment
+    u = rng.random((12, 1)).astype(np.float32)
+    t = np.array([0.5, 0.0, 1.5], np.float32)
+    whole, lp = tsd.token_sample(T(x), T(u), temperature=T(np.repeat(t, 4)))
+    grouped, lp2 = tsd.token_sample(T(x.reshape(3, 4, -1)), T(u.reshape(3, 4)), temperature=T(t))
+    assert torch.equal(whole.view(3, 4), grouped) and torch.equal(lp.view(3, 4), lp2)
+    rows = np.array([5, -1, 0, 11, 12, -3], np.int32)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    some, lp3 = tsd.token_sample(T(x), T(u[[5, 0, 0, 11, 0, 0], 0]), rows=T(rows), status=st)
+    plain, lp4 = tsd.token_sample(T(x), T(u[:, 0]))
+    assert int(st.item()) == tsd.STATUS_BAD_PATH
+    assert some.tolist()[:4] == [plain[5].item(), -1, plain[0].item(), plain[11].item()] and some.tolist()[4:] == [-1, -1]
+    assert lp3.tolist() == [lp4[5].item(), 0.0, lp4[0].item(), lp4[11].item(), 0.0, 0.0]
+    none, _ = tsd.token_sample(T(x)[:0], T(u)[:0])
+    assert none.shape == (0, 1)
+
+
+def test_draws_follow_the_distribution(tsd):
+    """Evenly spread numbers draw each token in proportion to its weight, to one draw."""
+    rng = np.random.default_rng(4)
+    V, n = 40, 64
+    x = rng.standard_normal((32, V)).astype(np.float32)
+    x[:] = x[0]
+    u = ((np.arange(32 * n) + 0.5) / (32 * n)).astype(np.float32).reshape(32, n)
+    tokens, _ = tsd.token_sample(T(x), T(u))
+    count = np.bincount(tokens.cpu().numpy().ravel(), minlength=V)
+    w = np.exp(x[0].astype(np.float64))
+    assert (np.abs(count - 32 * n * w / w.sum()) <= 1 + 32 * n * TOL).all()
+
+
+def test_filter_draw_verify_and_score(tsd):
+    """A step: the drafter's children are drawn from its filtered distribution, the verification divides by the same one."""
+    import torch
+    rng = np.random.default_rng(12)
+    B, N, V, D_max = 2, 7, 1500, 3
+    parent = np.array([[-1, 0, 0, 1, 1, 2, 2]] * B, np.int32)
+    target, draft = [T(rows_of(rng, B * N, V, "peaked").reshape(B, N, V)) for _ in range(2)]
+    t, p = T(np.array([0.9, 0.0], np.float32)), T(np.array([0.8, 0.9], np.float32))
+    q = tsd.logits_filter(draft, temperature=t, top_p=p, probs=True)
+    drawn, _ = tsd.token_sample(draft, T(rng.random((B, N, 2)).astype(np.float32)), temperature=t, top_p=p)
+    tokens = torch.zeros((B, N), dtype=torch.int32, device="cuda")
+    tokens[:, 1:3], tokens[:, 3:5], tokens[:, 5:7] = drawn[:, 0], drawn[:, 1], drawn[:, 2]
+    x = tsd.logits_filter(target, temperature=t, top_p=p)
+    anc, depth, mask, err = tsd.tree_build_ancestors(T(parent), None, D_max)
+    u1, u2 = [T(rng.random((B, N)).astype(np.float32)) for _ in range(2)]
+    nxt, draw, A, leaf, path, bonus = tsd.tree_verify_stochastic(x, q, tokens, T(parent), None, err, u1, u2, D_max)
+    emitted, lp, _, _, _ = tsd.tree_path_logprobs(x, tokens, path, A, bonus, err, D_max)
+    for b in range(B):
+        for i in range(int(A[b]) + 1):  # nothing is emitted that the target's filters removed
+            node = int(path[b, i]) - 1
+            assert x[b, node, emitted[b, i]] > -np.inf and np.isfinite(lp[b, i].item())
+    # temperature 0 is greedy verification with the most probable tokens
+    node = 0
+    best = target[1].argmax(-1)
+    assert int(emitted[1, 0]) == int(best[node])
+
+
+def test_replayed_with_other_settings(tsd):
+    import torch
+    rng = np.random.default_rng(13)
+    x = T(rows_of(rng, 3, 9000, "peaked"))
+    u, t = T(rng.random((3, 2)).astype(np.float32)), T(np.ones(3, np.float32))
+    k = T(np.zeros(3, np.int32))
+    tokens = torch.empty((3, 2), dtype=torch.int32, device="cuda")
+    lp = torch.empty((3, 2), device="cuda")
+    tsd.token_sample(x, u, temperature=t, top_k=k, tokens=tokens, logprob=lp)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        tsd.token_sample(x, u, temperature=t, top_k=k, tokens=tokens, logprob=lp)
+    t.fill_(0.6)
+    k.fill_(30)
+    x.mul_(-1)
+    g.replay()
+    want, want_lp = tsd.token_sample(x, u, temperature=t, top_k=k)
+    assert torch.equal(tokens, want) and torch.equal(lp, want_lp)

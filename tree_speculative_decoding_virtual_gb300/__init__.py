@@ -85,6 +85,12 @@ SIGNATURES = {
     "tsd_token_logprobs": (_I, [_P, _I, _P, _P, _I, _I64, _I, _I, _P, _P, _P, _P, _P, _P]),
     "tsd_tree_path_logprobs": (_I, [_P, _I, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P,
                                     _P, _P]),
+    "tsd_kv_append_rope": (_I, [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _I, _I, _I, _P, _I, _P, _I, _I, _F,
+                                _P, _P, _I64, _P, _P, _F, _I, _P, _P, _P, _I64, _P, _P]),
+    "tsd_kv_append_rope_q4": (_I, [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _I, _I, _I, _P, _I, _P, _I, _I,
+                                   _F, _P, _P, _I64, _P, _P, _F, _I, _P, _P, _P, _I64, _P, _P]),
+    "tsd_token_sample": (_I, [_P, _I, _P, _I, _I64, _I, _P, _I, _P, _P, _P, _P, _I, _P, _P, _P, _P]),
+    "tsd_logits_filter": (_I, [_P, _I, _I, _I, _I, _P, _P, _P, _P, _I, _P, _P, _P]),
 }
 
 
@@ -928,6 +934,170 @@ def tree_path_logprobs(logits, tokens, path, accept_len, bonus, err, D_max, k=0,
         _arg(status, i32, None, "status", dev), _raw_stream(dev))
     _check(rc, "tree_path_logprobs")
     return emitted, lp, ent, ids, top
+
+
+# ---------------------------------------------------------------------------
+# keys and values with their rotation, sampling (checks as above)
+# ---------------------------------------------------------------------------
+
+
+def _rows_arg(x, H, D, name, dev):
+    """(tokens, stride, pointer) of bf16 rows x [...][H][D]."""
+    T, stride = _token_rows(x, H, D, name)
+    if x.dtype != torch.bfloat16 or dev < 0 or x.get_device() != dev:
+        raise TsdError("%s must be a bfloat16 CUDA tensor on the same device as the others" % name)
+    return T, stride, x.data_ptr()
+
+
+def _append(call, what, q, k, v, slots, k_cache, v_cache, num_blocks, Hkv, D, cache_type, inv_freq, positions,
+            base, freq_axis, q_weight, k_weight, eps, interleaved, rot_scale, q_out, status):
+    i32, bf16 = torch.int32, torch.bfloat16
+    dev = _device_of(k)
+    T, ks, kp = _rows_arg(k, Hkv, D, "k", dev)
+    Tv, vs, vp = _rows_arg(v, Hkv, D, "v", dev)
+    Hq, qs, qp, os, op = 0, 0, None, 0, None
+    Tq = T
+    if q is not None:
+        if q.dim() < 2:
+            raise TsdError("q must be [...][Hq][D]")
+        Hq = q.shape[-2]
+        Tq, qs, qp = _rows_arg(q, Hq, D, "q", dev)
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=bf16, device=q.device)
+        elif q_out.shape != q.shape:
+            raise TsdError("q_out must have q's shape")
+        _, os, op = _rows_arg(q_out, Hq, D, "q_out", dev)
+    elif q_out is not None:
+        raise TsdError("q_out without q")
+    if T != Tv or T != Tq or slots.numel() != T:
+        raise TsdError("q, k, v and slots must hold the same tokens")
+    R = 0 if inv_freq is None else 2 * inv_freq.numel()
+    axes = 1
+    if positions is not None:
+        axes = positions.numel() // T if T else 1
+        if positions.numel() != axes * T or (axes > 1 and positions.shape[0] != axes):
+            raise TsdError("positions must be [...] like slots, or [axes][...]")
+    per_base = max(T, 1)
+    if base is not None:
+        n = base.numel()
+        if n == 0 and T or n and T % n:
+            raise TsdError("base must have an entry for each sequence of equally many tokens")
+        per_base = max(T // max(n, 1), 1)
+    elif positions is None and slots.dim() > 1:
+        per_base = max(slots.shape[-1], 1)
+    rc = call(qp, qs, kp, ks, vp, vs, _arg(slots, i32, None, "slots", dev), T, Hq, Hkv, D,
+              _arg(inv_freq, torch.float32, None, "inv_freq", dev), R,
+              _arg(freq_axis, i32, (R // 2,), "freq_axis", dev), axes, int(bool(interleaved)), float(rot_scale),
+              _arg(positions, i32, None, "positions", dev), _arg(base, i32, None, "base", dev), per_base,
+              _arg(q_weight, bf16, (D,), "q_weight", dev), _arg(k_weight, bf16, (D,), "k_weight", dev),
+              float(eps), num_blocks, _arg(k_cache, cache_type, None, "k_cache", dev),
+              _arg(v_cache, cache_type, None, "v_cache", dev), op, os, _arg(status, i32, None, "status", dev),
+              _raw_stream(dev))
+    _check(rc, what)
+    return q_out
+
+
+@_on_stream
+def kv_append_rope(q, k, v, slots, k_cache, v_cache, inv_freq=None, positions=None, base=None, freq_axis=None,
+                   q_weight=None, k_weight=None, eps=1e-6, interleaved=False, rot_scale=1.0, q_out=None,
+                   status=None):
+    """Norms (q_weight, k_weight bf16 [D], or None) and rotates the heads of q
+    bf16 [...][Hq][D] (or None) and k [...][Hkv][D], and stores k and v at slots
+    int32 [...] (-1: not stored) of the bf16 pool [num_blocks][Hkv][16][D].
+    inv_freq float32 [R/2] (None: no rotation); positions int32 like slots or
+    [axes][...] (None: the place in the sequence), plus base [B], where sequence b
+    starts: tree_build_ancestors' depth with base = prefix_len gives a tree's
+    positions.  freq_axis int32 [R/2]: which axis a frequency turns by.
+    interleaved: pairs of neighbouring columns instead of halves.  Tokens may be
+    strided (rows of a fused projection).  Returns the queries (q_out, which may
+    be q)."""
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.shape[2] != 16:
+        raise TsdError("k_cache and v_cache must be [num_blocks][Hkv][16][D], alike")
+    num_blocks, Hkv, _, D = k_cache.shape
+    return _append(lib.tsd_kv_append_rope, "kv_append_rope", q, k, v, slots, k_cache, v_cache, num_blocks, Hkv,
+                   D, torch.bfloat16, inv_freq, positions, base, freq_axis, q_weight, k_weight, eps,
+                   interleaved, rot_scale, q_out, status)
+
+
+@_on_stream
+def kv_append_rope_q4(q, k, v, slots, k_cache, v_cache, inv_freq=None, positions=None, base=None,
+                      freq_axis=None, q_weight=None, k_weight=None, eps=1e-6, interleaved=False, rot_scale=1.0,
+                      q_out=None, status=None):
+    """kv_append_rope into a 4-bit pool, uint8 [num_blocks][Hkv][9 * D]."""
+    num_blocks, Hkv, D = _q4_dims(k_cache, v_cache)
+    if k_cache.dim() != 3:
+        raise TsdError("kv_append_rope_q4 takes one layer's pool")
+    return _append(lib.tsd_kv_append_rope_q4, "kv_append_rope_q4", q, k, v, slots, k_cache, v_cache, num_blocks,
+                   Hkv, D, torch.uint8, inv_freq, positions, base, freq_axis, q_weight, k_weight, eps,
+                   interleaved, rot_scale, q_out, status)
+
+
+def _filters(temperature, top_k, top_p, min_p, R, dev):
+    """The filters' pointers, and how many rows share an entry."""
+    n = None
+    for t in (temperature, top_k, top_p, min_p):
+        if t is not None:
+            if n is not None and t.numel() != n:
+                raise TsdError("temperature, top_k, top_p and min_p must have equally many entries")
+            n = t.numel()
+    if n is not None and (n == 0 and R or n and R % n):
+        raise TsdError("temperature, top_k, top_p and min_p must have an entry for each run of equally many rows")
+    f32 = torch.float32
+    return (_arg(temperature, f32, None, "temperature", dev), _arg(top_k, torch.int32, None, "top_k", dev),
+            _arg(top_p, f32, None, "top_p", dev), _arg(min_p, f32, None, "min_p", dev), max(R // (n or 1), 1))
+
+
+@_on_stream
+def token_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, rows=None, tokens=None,
+                 logprob=None, status=None):
+    """Draws tokens from rows of logits [...][V] (float32 or bfloat16), one for
+    each number of u float32 [...] or [...][draws] in [0, 1), after temperature
+    (0: the most probable token), top_k, top_p and min_p: each None or a tensor
+    with an entry for each row, or for each run of equally many rows (a
+    sequence's nodes).  rows int32: which row of logits [num_rows][V] each row of u
+    draws from (-1: none).  Returns (tokens int32, logprob float32) like u."""
+    bf16 = _logits_kind(logits)
+    if logits.dim() < 2:
+        raise TsdError("logits must be [...][V]")
+    V = logits.shape[-1]
+    num_rows = logits.shape[:-1].numel()
+    lead = logits.shape[:-1] if rows is None else rows.shape
+    if u.shape != lead and u.shape[:-1] != lead:
+        raise TsdError("u must have a number, or a row of numbers, for each row")
+    draws = 1 if u.shape == lead else u.shape[-1]
+    R = lead.numel()
+    dev = _device_of(logits)
+    device = logits.device
+    tokens, tokens_p = _out_arg(tokens, torch.int32, u.shape, "tokens", dev, device)
+    logprob, logprob_p = _out_arg(logprob, torch.float32, u.shape, "logprob", dev, device)
+    t, k, p, m, per = _filters(temperature, top_k, top_p, min_p, R, dev)
+    rc = lib.tsd_token_sample(_arg(logits, logits.dtype, None, "logits", dev), bf16,
+                              _arg(rows, torch.int32, None, "rows", dev), R, num_rows, V,
+                              _arg(u, torch.float32, None, "u", dev), draws, t, k, p, m, per, tokens_p, logprob_p,
+                              _arg(status, torch.int32, None, "status", dev), _raw_stream(dev))
+    _check(rc, "token_sample")
+    return tokens, logprob
+
+
+@_on_stream
+def logits_filter(logits, temperature=None, top_k=None, top_p=None, min_p=None, probs=False, out=None,
+                  status=None):
+    """The distribution token_sample draws from, for every row of logits [...][V]:
+    scaled logits with -inf for what the filters removed (tree_verify_stochastic's
+    logits), or with probs its probabilities (its q_draft).  Returns out float32
+    [...][V] (which may be the logits when those are float32)."""
+    bf16 = _logits_kind(logits)
+    if logits.dim() < 2:
+        raise TsdError("logits must be [...][V]")
+    V = logits.shape[-1]
+    R = logits.shape[:-1].numel()
+    dev = _device_of(logits)
+    out, out_p = _out_arg(out, torch.float32, logits.shape, "out", dev, logits.device)
+    t, k, p, m, per = _filters(temperature, top_k, top_p, min_p, R, dev)
+    rc = lib.tsd_logits_filter(_arg(logits, logits.dtype, None, "logits", dev), bf16, R, V, int(bool(probs)), t, k,
+                               p, m, per, out_p, _arg(status, torch.int32, None, "status", dev), _raw_stream(dev))
+    _check(rc, "logits_filter")
+    return out
 
 
 def set_option(key: int, value: int) -> None:
