@@ -736,6 +736,43 @@ int tsd_tree_path_logprobs(const void *logits, int bf16, const int32_t *tokens, 
                            tsd_stream_t stream);
 
 /*
+ * a2 for groups of sequences that share a prefix ([Blog] paged cache: the blocks of
+ * a common prompt are held once): tsd_tree_attn_fwd's result, with the shared slots
+ * read and multiplied once for all trees of a group.
+ *
+ * group_first int32 [G + 1]: group j is the sequences group_first[j] ..
+ *   group_first[j + 1] - 1; the groups are runs that hold every sequence (0 =
+ *   group_first[0] <= ... <= group_first[G] = B), else all are skipped
+ *   (TSD_STATUS_BAD_LEN).  A group may be empty, or one sequence.
+ * shared_len int32 [G]: slots [0, S) of all sequences of the group hold the same
+ *   keys and values, for any S from 0 to the shortest prefix: they are read through
+ *   the table of the group's first sequence that is not skipped.
+ * Other arguments, outputs and errors as tsd_tree_attn_fwd; a sequence with a
+ * prefix shorter than S is skipped (TSD_STATUS_BAD_LEN), and so is one with a bad
+ * block id in its key range, or in the shared range that is read for it.  mask
+ * NULL: node i sees the tree's nodes 0..i (a chain; with N_max = 1 the decoding of
+ * one token).  A row that sees no key gets 0 / -inf.  What lies in slots outside a
+ * sequence's keys does not matter, NaN included; a row that sees a tree node whose V has
+ * a NaN or an infinity gets NaN, the rows that do not see it are as without it.
+ * P is rounded to bf16; sums, and the partial results that are joined, are fp32.
+ * Limits: B <= 1024, 1 <= G <= B.
+ * workspace >= tsd_tree_attn_shared_workspace_bytes(), 16-byte aligned (the plan of the
+ * call and fp32 partial rows; no initial contents); calls that may run at the same time
+ * need workspaces of their own.  Three launches (plan, attention, join) whose shapes
+ * depend on the arguments' sizes alone, so a call can be captured once and replayed
+ * with other lengths and groups.  Nothing is read before the previous kernel on the
+ * stream has finished.
+ */
+size_t tsd_tree_attn_shared_workspace_bytes(int B, int N_max, int Hq, int Hkv, int D, int G);
+int tsd_tree_attn_fwd_shared(const uint16_t *q, const uint16_t *k_cache, const uint16_t *v_cache,
+                             const int32_t *block_table, int max_blocks, int num_blocks,
+                             const int32_t *prefix_len, const int32_t *n_nodes, const uint32_t *mask,
+                             const int32_t *err, const int32_t *group_first, const int32_t *shared_len,
+                             int G, int B, int N_max, int Hq, int Hkv, int D, float scale,
+                             uint16_t *out, float *lse, void *workspace, size_t ws_bytes,
+                             int32_t *status, tsd_stream_t stream);
+
+/*
  * Keys and values into the paged cache, with the norms and the position rotation
  * of queries and keys on the way ([EP-zh] 2.1: a branch's entries are written
  * behind the committed prefix, node i at position P_b + depth).

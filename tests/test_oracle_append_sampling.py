@@ -77,6 +77,11 @@ def _append(t, q=(3, 4, 64), k=(3, 2, 64), v=(3, 2, 64), slots=3, pool=(4, 2, 16
     return t.kv_append_rope(_bf(*q), _bf(*k), _bf(*v), _i32(slots), _bf(*pool), _bf(*pool), **kw)
 
 
+def _shared(t, q=(2, 1, 4, 64), pool=(4, 2, 16, 64), first=(2,)):
+    return t.tree_attn_fwd_shared(_bf(*q), _bf(*pool), _bf(*pool), _i32(2, 3), _i32(2), None, None, None, _i32(*first),
+                                  _i32(1))
+
+
 REFUSED = {
     "cpu": lambda t: _append(t),
     "pool page": lambda t: _append(t, pool=(4, 2, 8, 64)),
@@ -93,6 +98,10 @@ REFUSED = {
     "sample settings": lambda t: t.token_sample(torch.zeros(6, 9), torch.zeros(6), temperature=torch.ones(4)),
     "sample settings differ": lambda t: t.token_sample(torch.zeros(6, 9), torch.zeros(6), temperature=torch.ones(3),
                                                        top_k=_i32(2)),
+    "shared cpu": lambda t: _shared(t),
+    "shared pool": lambda t: _shared(t, pool=(4, 2, 8, 64)),
+    "shared head dim": lambda t: _shared(t, q=(2, 1, 4, 128)),
+    "shared groups": lambda t: _shared(t, first=(3,)),
     "filter row": lambda t: t.logits_filter(torch.zeros(9)),
     "filter cpu": lambda t: t.logits_filter(torch.zeros(2, 9)),
 }
@@ -135,3 +144,17 @@ def test_c_entry_points_check_before_any_launch():
 
     assert filt(R=0) == 0 and filt(V=262145) == LIMIT and filt(x=None) == ARG and filt(out=None) == ARG
     assert filt(out=p + 2) == ARG and filt(R=-1) == ARG
+
+    def attn(B=1, N=1, Hq=2, Hkv=2, D=64, G=1, scale=1.0, q=p, ws=None, ws_bytes=0, blocks=4, first=p):
+        return L.tsd_tree_attn_fwd_shared(q, p, p, p, 2, blocks, p, None, None, None, first, p, G, B, N, Hq, Hkv, D, scale,
+                                          p, None, ws, ws_bytes, None, None)
+
+    assert attn(B=0, G=0) == 0
+    assert attn(D=96) == LIMIT and attn(N=257) == LIMIT and attn(Hq=3) == LIMIT and attn(Hq=34) == LIMIT
+    assert attn(B=1025) == LIMIT and attn(blocks=1 << 27) == LIMIT
+    assert attn(G=0) == ARG and attn(G=2) == ARG and attn(q=None) == ARG and attn(q=p + 2) == ARG and attn(first=None) == ARG
+    assert attn(scale=0.0) == ARG and attn(scale=float("nan")) == ARG and attn(blocks=0) == ARG
+    need = L.tsd_tree_attn_shared_workspace_bytes(1, 1, 2, 2, 64, 1)
+    assert need > 0 and L.tsd_tree_attn_shared_workspace_bytes(1, 1, 2, 2, 96, 1) == 0
+    assert attn() == tsd.TSD_ERR_WORKSPACE and attn(ws=p, ws_bytes=need - 1) == tsd.TSD_ERR_WORKSPACE
+    assert attn(ws=p + 4, ws_bytes=need) == ARG

@@ -85,6 +85,9 @@ SIGNATURES = {
     "tsd_token_logprobs": (_I, [_P, _I, _P, _P, _I, _I64, _I, _I, _P, _P, _P, _P, _P, _P]),
     "tsd_tree_path_logprobs": (_I, [_P, _I, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P,
                                     _P, _P]),
+    "tsd_tree_attn_shared_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I, _I]),
+    "tsd_tree_attn_fwd_shared": (_I, [_P, _P, _P, _P, _I, _I, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I,
+                                      _F, _P, _P, _P, _SZ, _P, _P]),
     "tsd_kv_append_rope": (_I, [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _I, _I, _I, _P, _I, _P, _I, _I, _F,
                                 _P, _P, _I64, _P, _P, _F, _I, _P, _P, _P, _I64, _P, _P]),
     "tsd_kv_append_rope_q4": (_I, [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _I, _I, _I, _P, _I, _P, _I, _I,
@@ -937,8 +940,52 @@ def tree_path_logprobs(logits, tokens, path, accept_len, bonus, err, D_max, k=0,
 
 
 # ---------------------------------------------------------------------------
-# keys and values with their rotation, sampling (checks as above)
+# shared prefixes, keys and values with their rotation, sampling (checks as above)
 # ---------------------------------------------------------------------------
+
+
+def tree_attn_shared_workspace_bytes(B, N_max, Hq, Hkv, D, G) -> int:
+    return int(lib.tsd_tree_attn_shared_workspace_bytes(B, N_max, Hq, Hkv, D, G))
+
+
+@_on_stream
+def tree_attn_fwd_shared(q, k_cache, v_cache, block_table, prefix_len, n_nodes, mask, err, group_first,
+                         shared_len, scale=None, out=None, lse=None, want_lse=True, workspace=None,
+                         status=None):
+    """tree_attn_fwd for groups of sequences that hold the same keys and values in
+    their first shared_len[j] slots (int32 [G]); group j is the sequences
+    group_first[j] .. group_first[j + 1] - 1 (int32 [G + 1]).  mask None: node i sees
+    nodes 0..i (a chain, or one token).  Returns (out bf16 [B][N_max][Hq][D], lse
+    float32 [B][N_max][Hq] or None)."""
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.shape[2] != 16:
+        raise TsdError("k_cache and v_cache must be [num_blocks][Hkv][16][D], alike")
+    num_blocks, Hkv, _, D = k_cache.shape
+    if q.dim() != 4 or q.shape[3] != D or block_table.dim() != 2 or shared_len.dim() != 1:
+        raise TsdError("q must be [B][N_max][Hq][D] with the pool's D, block_table [B][max_blocks], "
+                       "shared_len [G]")
+    B, N_max, Hq, _ = q.shape
+    G = shared_len.shape[0]
+    i32, bf16 = torch.int32, torch.bfloat16
+    dev = _device_of(q)
+    max_blocks = block_table.shape[1]
+    device = q.device
+    out, out_p = _out_arg(out, bf16, q.shape, "out", dev, device)
+    lse_p = None
+    if lse is not None or want_lse:
+        lse, lse_p = _out_arg(lse, torch.float32, (B, N_max, Hq), "lse", dev, device)
+    ws, ws_bytes, keep = _workspace_arg(
+        workspace, lib.tsd_tree_attn_shared_workspace_bytes(B, N_max, Hq, Hkv, D, G), q, dev)
+    rc = lib.tsd_tree_attn_fwd_shared(
+        _arg(q, bf16, None, "q", dev), _arg(k_cache, bf16, None, "k_cache", dev),
+        _arg(v_cache, bf16, None, "v_cache", dev),
+        _arg(block_table, i32, (B, max_blocks), "block_table", dev), max_blocks, num_blocks,
+        _arg(prefix_len, i32, (B,), "prefix_len", dev), _arg(n_nodes, i32, (B,), "n_nodes", dev),
+        _arg(mask, i32, (B, N_max, (N_max + 31) // 32), "mask", dev), _arg(err, i32, (B,), "err", dev),
+        _arg(group_first, i32, (G + 1,), "group_first", dev), _arg(shared_len, i32, (G,), "shared_len", dev), G,
+        B, N_max, Hq, Hkv, D, D ** -0.5 if scale is None else float(scale), out_p, lse_p, ws, ws_bytes,
+        _arg(status, i32, None, "status", dev), _raw_stream(dev))
+    _check(rc, "tree_attn_fwd_shared")
+    return out, lse
 
 
 def _rows_arg(x, H, D, name, dev):

@@ -19,14 +19,13 @@
 // skip masking; tiles that reach the tree tail apply each row's ancestor
 // bitmask.  The splits of one key range are merged into the bf16 output.
 
-#include <cuda.h>
-#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include <algorithm>
 #include <cmath>
 
+#include "cache_map.cuh"
 #include "sm100_ptx.cuh"
 #include "tsd_common.cuh"
 
@@ -2055,36 +2054,6 @@ AttnPlan plan_attn(int B, int N_max, int Hq, int Hkv, int D, int max_slots) {
   a.ml_bytes = rows * sizeof(float4);
   a.plan_bytes = a.mode == 2 ? ((size_t)B + (size_t)a.grid_items) * sizeof(int4) : 0;
   return a;
-}
-
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  if (!fn) {
-    cudaDriverEntryPointQueryResult q;
-    void *f = nullptr;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
-                                         &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      return nullptr;
-    fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-  }
-  return fn;
-}
-
-// 4-D view [block][kv head][slot][D] of a paged cache; a box covers 64
-// columns of 16 slots of `pages` consecutive blocks of one head.
-bool make_cache_map(CUtensorMap *m, const uint16_t *cache, int num_blocks, int Hkv, int D,
-                    int pages) {
-  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
-  if (!enc) return false;
-  cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)kPage, (cuuint64_t)Hkv, (cuuint64_t)num_blocks};
-  cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)kPage * D * 2,
-                           (cuuint64_t)Hkv * kPage * D * 2};
-  cuuint32_t box[4] = {64, (cuuint32_t)kPage, 1, (cuuint32_t)pages};
-  cuuint32_t estr[4] = {1, 1, 1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<uint16_t *>(cache), dims, strides,
-             box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int D>
