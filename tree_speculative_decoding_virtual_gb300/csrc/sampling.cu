@@ -16,11 +16,22 @@
 // A border that a sum decides moves with the sum's rounding, so weights are fp32 and
 // their sums exact: fixed point of 2^-43, which no order of additions changes.
 //
-// One cluster of up to 8 CTAs a row; the row stays in shared memory, each warp with a
-// run of consecutive ids.
+// One cluster of up to 8 CTAs a row; the row is read once and stays in shared memory,
+// each warp with a run of consecutive ids.  A filter's border is found by
+//   histogram  1024 bins of (m - x) / T, 32 a unit: counts for top-k, and for top-p
+//              weights relative to the bin's (13 bits a weight: good to 1e-4) besides the
+//              exact sum of all; the first CTA adds up the cluster's and finds the bin, or
+//              the few bins, that must hold the border
+//   list       what lies in them (a handful to some hundred) goes to the first CTA, with
+//              the exact weight above them, and is ranked there
+// When what lies in those bins and above fits the list (ordinary settings of top-k and
+// top-p), the first CTA has all that can be kept, and finishes alone: both filters, min-p
+// and the draws.  Bins that hold more than the list are cut into 1024 again; where that does
+// not part them either (hundreds of equal logits), the border is found bit by bit.
 #include <cuda_bf16.h>
 
 #include <cmath>
+#include <type_traits>
 
 #include "sm100_ptx.cuh"
 #include "tsd_common.cuh"
@@ -28,11 +39,17 @@
 namespace tsd {
 namespace {
 
-constexpr int kSpThreads = 512;
+constexpr int kSpThreads = 256;
 constexpr int kSpWarps = kSpThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kMaxVocab = 262144;
 constexpr int kMaxDraws = 64;
+constexpr int kBins = 1024;
+constexpr int kThreadBins = kBins / kSpThreads;
+constexpr int kList = 512;
+constexpr float kBinScale = 32.f;   // bins a unit of (m - x) / T, first level
+constexpr float kShare = 8192.f;    // a bin's own weight (262144 of them fit 32 bits)
+constexpr double kShareError = 1e-4;
 enum { kSample, kLogits, kProbs };
 
 struct SpArgs {
@@ -50,18 +67,59 @@ struct SpArgs {
   int32_t *status;
 };
 
+// What is kept: everything from (hi, lo) on, in (ordered logit, kMaxVocab - 1 - id).
+struct Border {
+  uint32_t hi = 0u, lo = 0u;
+  __device__ __forceinline__ bool has(uint32_t key, int id) const {
+    return key > hi || (key == hi && (uint32_t)(kMaxVocab - 1 - id) >= lo);
+  }
+};
+
+// Bins of (m - x) / T from `from` on, `scale` a unit.
+struct Bins {
+  float from, scale;
+};
+
+enum { kNone, kZoom, kCollect, kGather, kBitwise };  // what follows a histogram
+
+struct Verdict {
+  int what, lo, hi;  // the border is in bins lo..hi
+};
+
 struct SpShared {
-  float max[2];
-  int count[2];
-  long long sum[2];
+  union {
+    uint32_t hist[kBins];
+    struct {
+      unsigned long long list[kList];    // (ordered logit, ~id)
+      unsigned long long weight[kList];  // fixed point
+    };
+  };
   float wmax[kSpWarps];
   int wcount[kSpWarps];
   long long wsum[kSpWarps];
+  double scan[kSpWarps];
+  float max;
+  // added up in the first CTA
+  unsigned long long sum_all, sum_above;
+  int count_all, count_above, listed;
+  // exchanged by the bitwise search and the draws (two places, by turn)
+  int count[2];
+  long long sum[2];
+  // the first CTA's findings
+  Verdict verdict;
+  uint32_t border_hi, border_lo;
+  long long total;
+  float in_border, up_to;  // how many logits the bins hold
+  int mine;
+  bool failed;
 };
 
 __device__ __forceinline__ uint32_t ordered(float x) {  // no NaN; both zeros alike
   const uint32_t u = __float_as_uint(x + 0.f);
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ float unordered(uint32_t o) {
+  return __uint_as_float((o & 0x80000000u) ? (o & 0x7FFFFFFFu) : ~o);
 }
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
@@ -83,7 +141,23 @@ __device__ __forceinline__ unsigned long long ld_peer64(const void *p, uint32_t 
   asm volatile("ld.shared::cluster.u64 %0, [%1];\n" : "=l"(v) : "r"(peer(p, rank)) : "memory");
   return v;
 }
+// Into the first CTA's shared memory.
+__device__ __forceinline__ void add_first32(void *p, uint32_t v) {
+  asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;\n" ::"r"(peer(p, 0)), "r"(v) : "memory");
+}
+__device__ __forceinline__ void add_first64(void *p, unsigned long long v) {
+  asm volatile("red.relaxed.cluster.shared::cluster.add.u64 [%0], %1;\n" ::"r"(peer(p, 0)), "l"(v) : "memory");
+}
+__device__ __forceinline__ uint32_t take_first32(void *p, uint32_t v) {
+  uint32_t r;
+  asm volatile("atom.relaxed.cluster.shared::cluster.add.u32 %0, [%1], %2;\n" : "=r"(r) : "r"(peer(p, 0)), "r"(v) : "memory");
+  return r;
+}
+__device__ __forceinline__ void st_first64(void *p, unsigned long long v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;\n" ::"r"(peer(p, 0)), "l"(v) : "memory");
+}
 __device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
   sm100::cluster_arrive();
   sm100::cluster_wait();
 }
@@ -104,6 +178,11 @@ struct Fixed {
 };
 constexpr float kUnit = 0x1p-43f;
 
+__device__ __forceinline__ long long fixed(float w) {
+  Fixed f;
+  f.add(w);
+  return f.value();
+}
 __device__ __forceinline__ long long warp_sum(long long x) {
 #pragma unroll
   for (int off = 16; off; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
@@ -130,19 +209,185 @@ struct SpVec {
   }
 };
 
-// What is kept: everything from (hi, lo) on, in (ordered logit, kMaxVocab - 1 - id).
-struct Border {
-  uint32_t hi = 0u, lo = 0u;
-  __device__ __forceinline__ bool has(uint32_t key, int id) const {
-    return key > hi || (key == hi && (uint32_t)(kMaxVocab - 1 - id) >= lo);
+// A warp's run of the row in shared memory, and what its logits mean.
+template <bool kBf16>
+struct Run {
+  static constexpr int kN = SpVec<kBf16>::kN;
+  const uint4 *at;  // this lane's vectors, 32 apart
+  int steps, id;    // id of this lane's first logit; 32 * kN further a step
+  float m, inv_t;
+  uint32_t rank, ranks;
+
+  __device__ __forceinline__ float scaled(float x) const { return __fmul_rn(__fsub_rn(x, m), inv_t); }
+  // Calls f(logit, id) for every logit of this lane.
+  template <class F>
+  __device__ __forceinline__ void each(F f) const {
+    for (int s = 0; s < steps; ++s) {
+      SpVec<kBf16> v;
+      v.read(at + s * 32);
+#pragma unroll
+      for (int i = 0; i < kN; ++i) f(v.x[i], id + s * (32 * kN) + i);
+    }
   }
 };
 
+// The bin of d = (x - m) / T: -1 above the bins, kBins below them.  The same rounding
+// for every logit, so that a larger logit is never in a later bin; y - kRound is the bin.
+constexpr float kRound = 12582912.f;  // 1.5 * 2^23
+__device__ __forceinline__ int bin_of(float d, const Bins &b, float &rest) {
+  const float at = fminf(fmaxf(__fmul_rn(__fsub_rn(-d, b.from), b.scale), -1.f), (float)kBins);
+  const float y = __fadd_rn(at, kRound);
+  rest = __fsub_rn(at, __fsub_rn(y, kRound));
+  return (int)(__float_as_uint(y) - 0x4B400000u);
+}
+
+// Count and weight over the block, in every thread.
+__device__ __forceinline__ long long block_total(SpShared &sh, int &count, long long mine) {
+  const int warp = threadIdx.x >> 5;
+  const long long sum = warp_sum(mine);
+  count = __reduce_add_sync(0xffffffffu, count);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) {
+    sh.wsum[warp] = sum;
+    sh.wcount[warp] = count;
+  }
+  __syncthreads();
+  long long t = 0;
+  count = 0;
+#pragma unroll
+  for (int w = 0; w < kSpWarps; ++w) {
+    t += sh.wsum[w];
+    count += sh.wcount[w];
+  }
+  return t;
+}
+
+// The same over the cluster; `turn` is which of the two places is used.
+__device__ __forceinline__ long long cluster_total(SpShared &sh, int &turn, uint32_t ranks, int &count, long long mine) {
+  const long long t = block_total(sh, count, mine);
+  if (threadIdx.x == 0) {
+    sh.sum[turn] = t;
+    sh.count[turn] = count;
+  }
+  cluster_sync();
+  long long all = 0;
+  count = 0;
+  for (uint32_t p = 0; p < ranks; ++p) {
+    all += (long long)ld_peer64(&sh.sum[turn], p);
+    count += (int)ld_peer32(&sh.count[turn], p);
+  }
+  turn ^= 1;
+  return all;
+}
+
+// The border of what is kept, bit by bit: the highest one above which there are `k`
+// logits, or (k = 0) a share p of the weight above `kept`.  50 passes: for hundreds of equal
+// logits at the border.
+template <bool kBf16>
+__device__ __noinline__ Border bitwise_border(SpShared &sh, const Run<kBf16> &run, int &turn, const Border kept, int k, float p) {
+  auto above = [&](const Border &b, int &count) -> long long {
+    Fixed f;
+    int c = 0;
+    run.each([&](float x, int id) {
+      const bool in = x > -INFINITY && b.has(ordered(x), id) && kept.has(ordered(x), id);
+      c += in;
+      if (in && k == 0) f.add(expf(run.scaled(x)));
+    });
+    count = c;
+    return cluster_total(sh, turn, run.ranks, count, f.value());
+  };
+  int n;
+  long long least = 0;
+  if (k == 0) {
+    const double want = (double)p * (double)above(kept, n);
+    least = want > 1.0 ? (long long)ceil(want) : 1;
+  }
+  Border b;
+#pragma unroll 1
+  for (int bit = 49; bit >= 0; --bit) {
+    Border t = b;
+    if (bit >= 18) t.hi |= 1u << (bit - 18);
+    else t.lo |= 1u << bit;
+    const long long sum = above(t, n);
+    if (k ? n >= k : sum >= least) b = t;
+  }
+  return b.hi > kept.hi || (b.hi == kept.hi && b.lo > kept.lo) ? b : kept;
+}
+
+// First CTA: the bins that hold the border, from the cluster's histogram.  `above`:
+// count or weight above the bins; `all`: the whole weight where the first level's
+// bins are looked at for top-p (their sum is then known better from below).
+__device__ __forceinline__ void find_bins(SpShared &sh, const Bins bins, bool by_count, double target, double above,
+                                          double all, int level, int V) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  double v[kThreadBins], mine = 0.0;
+  float n[kThreadBins];
+#pragma unroll
+  for (int i = 0; i < kThreadBins; ++i) {
+    const int b = tid * kThreadBins + i;
+    const uint32_t h = sh.hist[b];
+    n[i] = by_count ? (float)h : (float)h * (1.02f / kShare);
+    v[i] = by_count ? (double)h : h ? (double)h * (double)(expf(-(bins.from + (float)b / bins.scale)) / kShare) : 0.0;
+    mine += v[i];
+  }
+  double upto = mine;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const double y = __shfl_up_sync(0xffffffffu, upto, off);
+    if (lane >= off) upto += y;
+  }
+  if (lane == 31) sh.scan[warp] = upto;
+  if (tid == 0) {
+    sh.verdict.lo = sh.verdict.hi = kBins;
+    sh.in_border = sh.up_to = 0.f;
+  }
+  __syncthreads();
+  double before = upto - mine, total = 0.0;
+#pragma unroll
+  for (int w = 0; w < kSpWarps; ++w) {
+    if (w < warp) before += sh.scan[w];
+    total += sh.scan[w];
+  }
+  // (a logit's share is off by 2^-14, and by 2^-22 for the bin's own weight)
+  const double e = by_count ? 0.0 : kShareError, beyond = V * 1.3e-14;
+  const bool from_below = !by_count && level == 0;
+#pragma unroll
+  for (int i = 0; i < kThreadBins; ++i) {
+    before += v[i];
+    const double rest = max(total - before, 0.0);
+    const bool may = from_below ? all - rest * (1.0 - e) >= target : above + before * (1.0 + e) >= target;
+    const bool must = from_below ? all - rest * (1.0 + e) - beyond >= target : above + before * (1.0 - e) >= target;
+    if (may) atomicMin(&sh.verdict.lo, tid * kThreadBins + i);
+    if (must) atomicMin(&sh.verdict.hi, tid * kThreadBins + i);
+  }
+  __syncthreads();
+  const int lo = sh.verdict.lo, hi = min(sh.verdict.hi, kBins - 1);
+  float in = 0.f, up = 0.f;
+#pragma unroll
+  for (int i = 0; i < kThreadBins; ++i) {
+    const int b = tid * kThreadBins + i;
+    if (b >= lo && b <= hi) in += n[i];
+    if (b <= hi) up += n[i];
+  }
+  if (in > 0.f) atomicAdd(&sh.in_border, in);
+  if (up > 0.f) atomicAdd(&sh.up_to, up);
+  __syncthreads();
+  if (tid == 0) {
+    const bool found = lo < kBins;
+    sh.verdict.hi = hi;
+    sh.verdict.what = !found                                   ? kBitwise
+                      : level == 0 && sh.up_to <= (float)kList ? kGather
+                      : sh.in_border <= (float)kList           ? kCollect
+                      : level == 0                             ? kZoom
+                                                               : kBitwise;
+  }
+}
+
 template <bool kBf16, int kMode>
-__global__ void __launch_bounds__(kSpThreads) sampling_kernel(const SpArgs a) {
+__global__ void __launch_bounds__(kSpThreads, 3) sampling_kernel(const SpArgs a) {
   using namespace sm100;
   using Vec = SpVec<kBf16>;
-  constexpr int kStep = 32 * Vec::kN;  // logits of a warp step
+  constexpr int kN = Vec::kN, kStep = 32 * kN;  // logits of a warp step
   extern __shared__ uint4 smem[];
   __shared__ SpShared sh;
   pdl_trigger();
@@ -164,88 +409,63 @@ __global__ void __launch_bounds__(kSpThreads) sampling_kernel(const SpArgs a) {
   const int pr = r / a.per_param;
   const float T = a.temperature ? a.temperature[pr] : 1.f;
   const bool greedy = !(T >= 1.1754944e-38f);
-  const float inv_t = greedy ? 1.f : __fdiv_rn(1.f, T);
   int k = a.top_k ? a.top_k[pr] : 0;
   if (k <= 0 || k > V) k = V;
   if (greedy) k = 1;
   const float top_p = a.top_p ? a.top_p[pr] : 1.f;
   const float min_p = a.min_p ? fminf(a.min_p[pr], 1.f) : 0.f;
 
-  // ---- the run [id0, id0 + per_warp) of this warp, -inf past the row's end ----
+  // ---- the run of this warp, -inf past the row's end; a lane reads what it wrote itself ----
   const int id0 = ((int)rank * kSpWarps + warp) * a.per_warp;
-  const int steps = a.per_warp / kStep;
-  uint4 *run = smem + (size_t)warp * (a.per_warp / Vec::kN);
-  float m = -INFINITY;
+  uint4 *mine = smem + (size_t)warp * (a.per_warp / kN) + lane;
+  Run<kBf16> run;
+  run.at = mine;
+  run.steps = a.per_warp / kStep;
+  run.id = id0 + lane * kN;
+  run.inv_t = greedy ? 1.f : __fdiv_rn(1.f, T);
+  run.rank = rank;
+  run.ranks = ranks;
   {
     using Raw = typename std::conditional<kBf16, uint16_t, uint32_t>::type;
     const Raw *src = reinterpret_cast<const Raw *>(a.logits) + row * V;
     const bool vec = (reinterpret_cast<uintptr_t>(src) & 15) == 0;
     const uint32_t none = kBf16 ? 0xFF80FF80u : 0xFF800000u;
-    for (int s = 0; s < steps; ++s) {
-      const int id = id0 + s * kStep + lane * Vec::kN;
-      uint4 v = make_uint4(none, none, none, none);
-      if (vec && id + Vec::kN <= V) {
-        v = __ldcs(reinterpret_cast<const uint4 *>(src + id));
+    for (int s = 0; s < run.steps; ++s) {
+      const int id = run.id + s * kStep;
+      if (vec && id + kN <= V) {
+        cp_async_16(smem_addr(mine + s * 32), src + id);
       } else {
-        Raw e[Vec::kN];
+        Raw e[kN];
 #pragma unroll
-        for (int i = 0; i < Vec::kN; ++i) e[i] = id + i < V ? src[id + i] : (Raw)none;
+        for (int i = 0; i < kN; ++i) e[i] = id + i < V ? src[id + i] : (Raw)none;
         if constexpr (kBf16)
-          v = make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
+          mine[s * 32] = make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
         else
-          v = make_uint4(e[0], e[1], e[2], e[3]);
+          mine[s * 32] = make_uint4(e[0], e[1], e[2], e[3]);
       }
-      run[s * 32 + lane] = v;
-      Vec x;
-      x.read(&v);
-#pragma unroll
-      for (int i = 0; i < Vec::kN; ++i) m = max_nan(m, x.x[i]);
     }
-  }
-  // (a lane reads what it wrote itself until the draws)
-
-  int turn = 0;  // which of the exchanged values' two places
-  auto cluster_total = [&](int &count, Fixed f) -> long long {
-    const long long sum = warp_sum(f.value());
-    count = __reduce_add_sync(0xffffffffu, count);
-    __syncthreads();
-    if (lane == 0) {
-      sh.wsum[warp] = sum;
-      sh.wcount[warp] = count;
-    }
-    __syncthreads();
+    for (int b = tid; b < kBins; b += kSpThreads) sh.hist[b] = 0u;
     if (tid == 0) {
-      long long t = 0;
-      int c = 0;
-      for (int w = 0; w < kSpWarps; ++w) {
-        t += sh.wsum[w];
-        c += sh.wcount[w];
-      }
-      sh.sum[turn] = t;
-      sh.count[turn] = c;
+      sh.sum_all = sh.sum_above = 0ull;
+      sh.count_all = sh.count_above = sh.listed = sh.mine = 0;
+      sh.failed = false;
     }
-    cluster_sync();
-    long long t = 0;
-    count = 0;
-    for (uint32_t p = 0; p < ranks; ++p) {
-      t += (long long)ld_peer64(&sh.sum[turn], p);
-      count += (int)ld_peer32(&sh.count[turn], p);
-    }
-    turn ^= 1;
-    return t;
-  };
-
+    cp_async_wait_all();
+  }
+  float m = -INFINITY;
+  run.each([&](float x, int) { m = max_nan(m, x); });
 #pragma unroll
   for (int off = 16; off; off >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, off));
   if (lane == 0) sh.wmax[warp] = m;
   __syncthreads();
   if (tid == 0) {
     for (int w = 0; w < kSpWarps; ++w) m = max_nan(m, sh.wmax[w]);
-    sh.max[0] = m;
+    sh.max = m;
   }
   cluster_sync();
   m = -INFINITY;
-  for (uint32_t p = 0; p < ranks; ++p) m = max_nan(m, __uint_as_float(ld_peer32(&sh.max[0], p)));
+  for (uint32_t p = 0; p < ranks; ++p) m = max_nan(m, __uint_as_float(ld_peer32(&sh.max, p)));
+  run.m = m;
 
   const bool bad = !(m < INFINITY), empty = m == -INFINITY;
   if (bad || empty) {
@@ -264,91 +484,297 @@ __global__ void __launch_bounds__(kSpThreads) sampling_kernel(const SpArgs a) {
     return;
   }
 
-  auto scaled = [&](float x) { return __fmul_rn(__fsub_rn(x, m), inv_t); };
-  // number and weight of what lies above a border
-  auto above = [&](const Border &b, int &count) -> long long {
-    Fixed f;
-    count = 0;
-    for (int s = 0; s < steps; ++s) {
-      Vec x;
-      x.read(run + s * 32 + lane);
-#pragma unroll
-      for (int i = 0; i < Vec::kN; ++i) {
-        const bool in = x.x[i] > -INFINITY && b.has(ordered(x.x[i]), id0 + s * kStep + lane * Vec::kN + i);
-        count += in;
-        if (in) f.add(expf(scaled(x.x[i])));
-      }
-    }
-    return cluster_total(count, f);
-  };
-  // the highest border that enough lies above
-  auto settle = [&](auto enough) -> Border {
-    Border b;
-    for (int bit = 31; bit >= 0; --bit) {
-      Border t{b.hi | 1u << bit, 0u};
-      int n;
-      const long long sum = above(t, n);
-      if (enough(n, sum)) b = t;
-    }
-    for (int bit = 17; bit >= 0; --bit) {
-      Border t{b.hi, b.lo | 1u << bit};
-      int n;
-      const long long sum = above(t, n);
-      if (enough(n, sum)) b = t;
-    }
-    return b;
-  };
+  int turn = 0;
   Border kept;
-  if (k < V) {
-    int n;
-    above(kept, n);
-    if (n > k) kept = settle([&](int c, long long) { return c >= k; });
-  }
-  if (top_p < 1.f) {
-    int n;
-    const double want = (double)top_p * (double)above(kept, n);
-    const long long least = want > 1.0 ? (long long)ceil(want) : 1;
-    const Border b = settle([&](int, long long s) { return s >= least; });
-    if (b.hi > kept.hi || (b.hi == kept.hi && b.lo > kept.lo)) kept = b;
+  long long total = -1;  // weight of what is kept, once known
+
+  // ---- the filters' borders ----
+#pragma unroll 1
+  for (int stage = 0; stage < 2; ++stage) {
+    const bool by_count = stage == 0;
+    if (by_count ? k >= V : top_p >= 1.f) continue;
+    Bins bins{0.f, kBinScale};
+    Verdict v;
+#pragma unroll 1
+    for (int level = 0;; ++level) {
+      // histogram of what is kept so far
+      const float inv_scale = 1.f / bins.scale;
+      Fixed all, over;
+      int count = 0, count_over = 0;
+      run.each([&](float x, int id) {
+        if (!(x > -INFINITY) || !kept.has(ordered(x), id)) return;
+        const float d = run.scaled(x);
+        float rest;
+        const int b = bin_of(d, bins, rest);
+        ++count;
+        if (by_count) {
+          if ((unsigned)b < (unsigned)kBins) atomicAdd(&sh.hist[b], 1u);
+          count_over += b < 0;
+        } else {
+          if (level == 0) all.add(expf(d));
+          else if (b < 0) over.add(expf(d));
+          if ((unsigned)b < (unsigned)kBins) {
+            const float z = rest * inv_scale;  // ln of (the bin's weight / this one)
+            const float share = fmaf(z, fmaf(z, 0.5f, -1.f), 1.f) * kShare;
+            atomicAdd(&sh.hist[b], __float_as_uint(__fadd_rn(share, kRound)) - 0x4B400000u);
+          }
+        }
+      });
+      const long long sums = block_total(sh, count, level == 0 ? all.value() : over.value());
+      count_over = __reduce_add_sync(0xffffffffu, count_over);
+      if (lane == 0 && count_over) add_first32(&sh.count_above, count_over);
+      if (tid == 0) {
+        if (level == 0) add_first32(&sh.count_all, count);
+        add_first64(level == 0 ? &sh.sum_all : &sh.sum_above, (unsigned long long)sums);
+      }
+      if (rank != 0)
+        for (int b = tid; b < kBins; b += kSpThreads) {
+          const uint32_t h = sh.hist[b];
+          if (h) add_first32(&sh.hist[b], h);
+          sh.hist[b] = 0u;  // (for the next one)
+        }
+      cluster_sync();
+      if (rank == 0) {
+        const double target = by_count ? (double)k : (double)top_p * (double)(long long)sh.sum_all * (double)kUnit;
+        const double above = by_count ? (double)sh.count_above : (double)(long long)sh.sum_above * (double)kUnit;
+        if (by_count && sh.count_all <= k) {
+          if (tid == 0) sh.verdict.what = kNone;
+        } else {
+          find_bins(sh, bins, by_count, by_count ? target : max(target, (double)kUnit), above,
+                    (double)(long long)sh.sum_all * (double)kUnit, level, V);
+        }
+        __syncthreads();
+        for (int b = tid; b < kBins; b += kSpThreads) sh.hist[b] = 0u;
+        if (tid == 0) {
+          sh.sum_above = 0ull;
+          sh.count_above = 0;
+          if (sh.verdict.what == kNone || sh.verdict.what == kBitwise) {
+            sh.sum_all = 0ull;
+            sh.count_all = 0;
+          }
+        }
+      }
+      cluster_sync();
+      v.what = (int)ld_peer32(&sh.verdict.what, 0);
+      v.lo = (int)ld_peer32(&sh.verdict.lo, 0);
+      v.hi = (int)ld_peer32(&sh.verdict.hi, 0);
+      if (v.what != kZoom) break;
+      // the border's bins, a little widened, are cut again
+      const float width = (float)(v.hi - v.lo + 1) / bins.scale;
+      bins.from += ((float)v.lo - 0.5f) / bins.scale - 0.01f * width;
+      bins.scale = (float)(kBins - 1) / (1.02f * width);
+    }
+    if (v.what == kNone) continue;
+    if (v.what != kBitwise) {
+      // ---- what lies in the border's bins (kGather: and above them) goes to the first CTA ----
+      const int lo = v.what == kGather ? -1 : v.lo;
+      Fixed over;
+      int count = 0;
+      run.each([&](float x, int id) {
+        if (!(x > -INFINITY) || !kept.has(ordered(x), id)) return;
+        const float d = run.scaled(x);
+        float rest;
+        const int b = bin_of(d, bins, rest);
+        if (b > v.hi) return;
+        if (b < lo) {
+          ++count;
+          if (!by_count) over.add(expf(d));
+          return;
+        }
+        const int at = atomicAdd(rank == 0 ? &sh.listed : &sh.mine, 1);
+        if (at < kList) sh.list[at] = ((unsigned long long)ordered(x) << 32) | (uint32_t)~id;
+      });
+      if (v.what == kCollect) {
+        const long long sums = block_total(sh, count, over.value());
+        if (tid == 0) {
+          add_first32(&sh.count_above, count);
+          add_first64(&sh.sum_above, (unsigned long long)sums);
+        }
+      }
+      __syncthreads();
+      if (rank != 0) {
+        const int n = sh.mine;
+        if (tid == 0) sh.wcount[0] = (int)take_first32(&sh.listed, n);
+        __syncthreads();
+        const int at = sh.wcount[0];
+        for (int i = tid; i < min(n, kList); i += kSpThreads)
+          if (at + i < kList) st_first64(&sh.list[at + i], sh.list[i]);
+        __syncthreads();
+        if (tid == 0) sh.mine = 0;
+      }
+      cluster_sync();
+      if (rank == 0) {
+        const int n = sh.listed;
+        const long long base = (long long)sh.sum_above, everything = (long long)sh.sum_all;
+        const int more = sh.count_above;
+        __syncthreads();
+        if (tid == 0) {
+          sh.failed = n > kList;
+          sh.border_hi = kept.hi;
+          sh.border_lo = kept.lo;
+          sh.total = 0;
+        }
+        constexpr int kMine = kList / kSpThreads;
+        unsigned long long c[kMine];
+        float w[kMine];
+        long long before[kMine], fw[kMine];
+        int place[kMine];
+        const bool weigh = v.what == kGather || !by_count;
+#pragma unroll
+        for (int e = 0; e < kMine; ++e) {
+          const int i = tid + e * kSpThreads;
+          c[e] = i < min(n, kList) ? sh.list[i] : 0ull;
+          w[e] = 0.f;
+          if (c[e] && weigh) {
+            w[e] = expf(run.scaled(unordered((uint32_t)(c[e] >> 32))));
+            sh.weight[i] = (unsigned long long)fixed(w[e]);
+          }
+          fw[e] = fixed(w[e]);
+          before[e] = 0;
+          place[e] = 0;
+        }
+        __syncthreads();
+        if (n <= kList) {
+          // rank, and the weight of what ranks higher
+          for (int j = 0; j < n; ++j) {
+            const unsigned long long o = sh.list[j];
+            const long long ow = weigh ? (long long)sh.weight[j] : 0;
+#pragma unroll
+            for (int e = 0; e < kMine; ++e)
+              if (o > c[e]) {
+                ++place[e];
+                before[e] += ow;
+              }
+          }
+          bool in[kMine];
+          if (v.what == kGather) {
+            // all that may be kept is here: top-k, then top-p of what that left, then min-p
+            long long s = 0;
+            int unused = 0;
+#pragma unroll
+            for (int e = 0; e < kMine; ++e) {
+              in[e] = c[e] != 0ull && (stage == 1 || place[e] < k);
+              if (in[e]) s += fw[e];
+            }
+            if (top_p < 1.f) {
+              s = block_total(sh, unused, s);
+              const double want = (double)top_p * (double)(stage == 0 ? s : everything);
+#pragma unroll
+              for (int e = 0; e < kMine; ++e) in[e] = in[e] && (place[e] == 0 || (double)before[e] < want);
+            }
+          } else {
+            // one filter's border
+            const double want = (double)top_p * (double)everything;
+            if (!by_count && (double)base >= want) sh.failed = true;  // (it lies above the list)
+#pragma unroll
+            for (int e = 0; e < kMine; ++e)
+              in[e] = c[e] != 0ull && (by_count ? more + place[e] < k : (double)(base + before[e]) < want);
+          }
+          // the border is the lowest that is kept
+          int kept_here = 0;
+          long long s = 0;
+#pragma unroll
+          for (int e = 0; e < kMine; ++e) kept_here += in[e];
+          block_total(sh, kept_here, 0);
+#pragma unroll
+          for (int e = 0; e < kMine; ++e) {
+            if (in[e] && place[e] == kept_here - 1) {
+              sh.border_hi = (uint32_t)(c[e] >> 32);
+              sh.border_lo = (uint32_t)(kMaxVocab - 1) - ~(uint32_t)c[e];
+            }
+            if (v.what == kGather) in[e] = in[e] && !(w[e] < min_p);
+            if (in[e]) s += fw[e];
+          }
+          if (kept_here == 0) sh.failed = true;
+          int unused = 0;
+          s = block_total(sh, unused, s);
+          if (tid == 0) sh.total = v.what == kGather ? s : by_count || min_p > 0.f ? -1 : base + s;
+          if constexpr (kMode == kSample) {
+            if (v.what == kGather) {
+              // the draws: the weight of what is kept and has a lower id
+#pragma unroll
+              for (int e = 0; e < kMine; ++e) {
+                if (c[e]) sh.weight[tid + e * kSpThreads] = in[e] ? (unsigned long long)fw[e] : 0ull;
+                before[e] = 0;
+              }
+              __syncthreads();
+              for (int j = 0; j < n; ++j) {
+                const uint32_t o = (uint32_t)sh.list[j];
+                const long long ow = (long long)sh.weight[j];
+#pragma unroll
+                for (int e = 0; e < kMine; ++e)
+                  if (o > (uint32_t)c[e]) before[e] += ow;
+              }
+              const float log_total = logf((float)s * kUnit);
+              for (int q = 0; q < a.draws; ++q) {
+                const float u = a.u[(size_t)r * a.draws + q];
+                long long at = u > 0.f ? (long long)floor((double)u * (double)s) : 0;
+                at = min(at, s - 1);
+#pragma unroll
+                for (int e = 0; e < kMine; ++e)
+                  if (in[e] && at >= before[e] && at < before[e] + fw[e]) {
+                    a.tokens[(size_t)r * a.draws + q] = (int32_t)~(uint32_t)c[e];
+                    a.logprob[(size_t)r * a.draws + q] = run.scaled(unordered((uint32_t)(c[e] >> 32))) - log_total;
+                  }
+              }
+            }
+          }
+        }
+        __syncthreads();
+        for (int b = tid; b < kBins; b += kSpThreads) sh.hist[b] = 0u;  // (it lies over the list)
+        if (tid == 0) {
+          sh.listed = sh.count_all = sh.count_above = 0;
+          sh.sum_all = sh.sum_above = 0ull;
+        }
+      } else {
+        for (int b = tid; b < kBins; b += kSpThreads) sh.hist[b] = 0u;
+      }
+      if (kMode == kSample && v.what == kGather) return;  // (nothing of this CTA is read any more)
+      cluster_sync();
+      if (ld_peer32(&sh.failed, 0) & 0xFFu) v.what = kBitwise;
+      kept.hi = ld_peer32(&sh.border_hi, 0);
+      kept.lo = ld_peer32(&sh.border_lo, 0);
+      total = (long long)ld_peer64(&sh.total, 0);
+    }
+    if (v.what == kBitwise) {
+      kept = bitwise_border(sh, run, turn, kept, by_count ? k : 0, top_p);
+      total = -1;
+    }
+    if (v.what == kGather) break;
   }
 
-  // ---- what is kept, by warp ----
+  // ---- what is kept ----
   auto weight = [&](float x, int id) -> float {  // 0: not kept
     if (!(x > -INFINITY) || !kept.has(ordered(x), id)) return 0.f;
-    const float w = expf(scaled(x));
+    const float w = expf(run.scaled(x));
     return w < min_p ? 0.f : w;
   };
-  Fixed f;
-  for (int s = 0; s < steps; ++s) {
-    Vec x;
-    x.read(run + s * 32 + lane);
-#pragma unroll
-    for (int i = 0; i < Vec::kN; ++i) f.add(weight(x.x[i], id0 + s * kStep + lane * Vec::kN + i));
+  if (kMode == kSample || (kMode == kProbs && total < 0)) {
+    Fixed f;
+    run.each([&](float x, int id) { f.add(weight(x, id)); });
+    int unused = 0;
+    total = cluster_total(sh, turn, ranks, unused, f.value());
   }
-  int unused = 0;
-  const long long total = cluster_total(unused, f);
   if constexpr (kMode == kSample) {
     long long before = 0;  // of this warp's run
     for (uint32_t p = 0; p < rank; ++p) before += (long long)ld_peer64(&sh.sum[turn ^ 1], p);
     for (int w = 0; w < warp; ++w) before += sh.wsum[w];
-    const long long mine = sh.wsum[warp];
+    const long long here = sh.wsum[warp];
     const float log_total = logf((float)total * kUnit);
     for (int q = 0; q < a.draws; ++q) {
       const float u = a.u[(size_t)r * a.draws + q];
       long long at = u > 0.f ? (long long)floor((double)u * (double)total) : 0;
       at = min(at, total - 1) - before;
-      if (at < 0 || at >= mine) continue;
-      for (int s = 0; s < steps; ++s) {
+      if (at < 0 || at >= here) continue;
+      for (int s = 0; s < run.steps; ++s) {
         Vec x;
-        x.read(run + s * 32 + lane);
-        float w[Vec::kN];
+        x.read(run.at + s * 32);
+        float w[kN];
         long long sum = 0;
 #pragma unroll
-        for (int i = 0; i < Vec::kN; ++i) {
-          w[i] = weight(x.x[i], id0 + s * kStep + lane * Vec::kN + i);
-          Fixed one;
-          one.add(w[i]);
-          sum += one.value();
+        for (int i = 0; i < kN; ++i) {
+          w[i] = weight(x.x[i], run.id + s * kStep + i);
+          sum += fixed(w[i]);
         }
         long long upto = sum;
 #pragma unroll
@@ -361,20 +787,19 @@ __global__ void __launch_bounds__(kSpThreads) sampling_kernel(const SpArgs a) {
           long long left = at - (upto - sum);
           if (left >= 0 && left < sum) {
             int i = 0;
-#pragma unroll
-            for (int j = 0; j < Vec::kN - 1; ++j) {
-              Fixed one;
-              one.add(w[j]);
-              if (i == j && left >= one.value()) {
-                left -= one.value();
-                ++i;
-              }
-            }
             float d = 0.f;
 #pragma unroll
-            for (int j = 0; j < Vec::kN; ++j)
-              if (j == i) d = scaled(x.x[j]);
-            a.tokens[(size_t)r * a.draws + q] = id0 + s * kStep + lane * Vec::kN + i;
+            for (int j = 0; j < kN; ++j) {
+              const long long one = fixed(w[j]);
+              if (i == j) {
+                d = run.scaled(x.x[j]);
+                if (left >= one && j + 1 < kN) {
+                  left -= one;
+                  ++i;
+                }
+              }
+            }
+            a.tokens[(size_t)r * a.draws + q] = run.id + s * kStep + i;
             a.logprob[(size_t)r * a.draws + q] = d - log_total;
           }
           break;
@@ -384,17 +809,32 @@ __global__ void __launch_bounds__(kSpThreads) sampling_kernel(const SpArgs a) {
     }
   } else {
     const float inv = 1.f / ((float)total * kUnit);
-    for (int s = 0; s < steps; ++s) {
+    float *dst = a.out + (size_t)r * V;
+    const bool vec = (reinterpret_cast<uintptr_t>(dst) & 15) == 0;
+    for (int s = 0; s < run.steps; ++s) {
       Vec x;
-      x.read(run + s * 32 + lane);
+      x.read(run.at + s * 32);
+      const int id = run.id + s * kStep;
+      float y[kN];
 #pragma unroll
-      for (int i = 0; i < Vec::kN; ++i) {
-        const int id = id0 + s * kStep + lane * Vec::kN + i;
-        if (id >= V) continue;
-        const bool in = x.x[i] > -INFINITY && kept.has(ordered(x.x[i]), id) &&
-                        !(min_p > 0.f && expf(scaled(x.x[i])) < min_p);
-        a.out[(size_t)r * V + id] =
-            kMode == kProbs ? (in ? expf(scaled(x.x[i])) * inv : 0.f) : in ? scaled(x.x[i]) : -INFINITY;
+      for (int i = 0; i < kN; ++i) {
+        const float d = run.scaled(x.x[i]);
+        bool in = x.x[i] > -INFINITY && kept.has(ordered(x.x[i]), id + i);
+        float w = 0.f;
+        if (in && (kMode == kProbs || min_p > 0.f)) {
+          w = expf(d);
+          in = !(w < min_p);
+        }
+        y[i] = kMode == kProbs ? (in ? w * inv : 0.f) : in ? d : -INFINITY;
+      }
+      if (vec && id + kN <= V) {
+#pragma unroll
+        for (int i = 0; i < kN; i += 4)
+          __stcs(reinterpret_cast<float4 *>(dst + id + i), make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]));
+      } else {
+#pragma unroll
+        for (int i = 0; i < kN; ++i)
+          if (id + i < V) dst[id + i] = y[i];
       }
     }
   }
