@@ -47,9 +47,10 @@ constexpr int kMaxDraws = 64;
 constexpr int kBins = 1024;
 constexpr int kThreadBins = kBins / kSpThreads;
 constexpr int kList = 512;
-constexpr float kBinScale = 32.f;   // bins a unit of (m - x) / T, first level
+constexpr float kCountScale = 16.f, kWideScale = 0.25f, kWeightScale = 32.f;  // bins a unit at first
+constexpr int kLevels = 3;          // times bins are cut again at most
 constexpr float kShare = 8192.f;    // a bin's own weight (262144 of them fit 32 bits)
-constexpr double kShareError = 1e-4;
+constexpr float kShareError = 1e-4f;  // (a logit's share is off by 2^-14, sums and exponentials by less)
 enum { kSample, kLogits, kProbs };
 
 struct SpArgs {
@@ -67,20 +68,20 @@ struct SpArgs {
   int32_t *status;
 };
 
-// What is kept: everything from (hi, lo) on, in (ordered logit, kMaxVocab - 1 - id).
+// What is kept: everything down to logit x, of those equal to it the ids up to id.
 struct Border {
-  uint32_t hi = 0u, lo = 0u;
-  __device__ __forceinline__ bool has(uint32_t key, int id) const {
-    return key > hi || (key == hi && (uint32_t)(kMaxVocab - 1 - id) >= lo);
-  }
+  float x = -INFINITY;
+  int id = -1;
+  __device__ __forceinline__ bool has(float y, int i) const { return y > x || (y == x && i <= id); }
 };
 
-// Bins of (m - x) / T from `from` on, `scale` a unit.
+// Bins of a logit's distance from the maximum, from `from` on, `scale` a unit.  Top-k's
+// distance is m - x (its border has nothing to do with T), top-p's (m - x) / T.
 struct Bins {
   float from, scale;
 };
 
-enum { kNone, kZoom, kCollect, kGather, kBitwise };  // what follows a histogram
+enum { kNone, kWiden, kZoom, kCollect, kGather, kBitwise };  // what follows a histogram
 
 struct Verdict {
   int what, lo, hi;  // the border is in bins lo..hi
@@ -88,7 +89,7 @@ struct Verdict {
 
 struct SpShared {
   union {
-    uint32_t hist[kBins];
+    alignas(16) uint32_t hist[kBins];
     struct {
       unsigned long long list[kList];    // (ordered logit, ~id)
       unsigned long long weight[kList];  // fixed point
@@ -97,17 +98,20 @@ struct SpShared {
   float wmax[kSpWarps];
   int wcount[kSpWarps];
   long long wsum[kSpWarps];
-  double scan[kSpWarps];
+  float scan[kSpWarps];
+  float need, room, skipped;
+  long long at[kMaxDraws];
   float max;
   // added up in the first CTA
-  unsigned long long sum_all, sum_above;
+  unsigned long long sum_all, sum_near, sum_above;
   int count_all, count_above, listed;
   // exchanged by the bitwise search and the draws (two places, by turn)
   int count[2];
   long long sum[2];
   // the first CTA's findings
   Verdict verdict;
-  uint32_t border_hi, border_lo;
+  float border_x;
+  int border_id;
   long long total;
   float in_border, up_to;  // how many logits the bins hold
   int mine;
@@ -126,6 +130,11 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 __device__ __forceinline__ uint32_t peer(const void *p, uint32_t rank) {
   uint32_t r;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(r) : "r"(sm100::smem_addr(p)), "r"(rank));
@@ -139,6 +148,14 @@ __device__ __forceinline__ uint32_t ld_peer32(const void *p, uint32_t rank) {
 __device__ __forceinline__ unsigned long long ld_peer64(const void *p, uint32_t rank) {
   unsigned long long v;
   asm volatile("ld.shared::cluster.u64 %0, [%1];\n" : "=l"(v) : "r"(peer(p, rank)) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint4 ld_peer128(const void *p, uint32_t rank) {
+  uint4 v;
+  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];\n"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(peer(p, rank))
+               : "memory");
   return v;
 }
 // Into the first CTA's shared memory.
@@ -173,6 +190,15 @@ struct Fixed {
     const float b = __fadd_rn(__fsub_rn(w, __fsub_rn(a, 8.f)), 0x1.8p-20f);
     hi += __float_as_uint(a) - 0x41000000u;
     lo += (int)(__float_as_uint(b) - 0x35C00000u);
+  }
+  // two at a time, on packed pairs
+  __device__ __forceinline__ void add2(float w0, float w1) {
+    using namespace sm100;
+    const unsigned long long w = f2_pack(w0, w1), a = f2_add(w, f2_pack(8.f, 8.f));
+    const unsigned long long rest = f2_fma(f2_add(a, f2_pack(-8.f, -8.f)), f2_pack(-1.f, -1.f), w);
+    const float2 x = f2_unpack(a), y = f2_unpack(f2_add(rest, f2_pack(0x1.8p-20f, 0x1.8p-20f)));
+    hi += __float_as_uint(x.x) + __float_as_uint(x.y) - 0x82000000u;
+    lo += (int)(__float_as_uint(y.x) + __float_as_uint(y.y) - 0x6B800000u);
   }
   __device__ __forceinline__ long long value() const { return ((long long)hi << 23) + lo; }
 };
@@ -219,26 +245,43 @@ struct Run {
   uint32_t rank, ranks;
 
   __device__ __forceinline__ float scaled(float x) const { return __fmul_rn(__fsub_rn(x, m), inv_t); }
-  // Calls f(logit, id) for every logit of this lane.
+  // Calls f(logits, id of the first) for every vector of this lane that holds a logit of
+  // `from` or more.
   template <class F>
-  __device__ __forceinline__ void each(F f) const {
+  __device__ __forceinline__ void each_vec(float from, F f) const {
+#pragma unroll 2
     for (int s = 0; s < steps; ++s) {
       SpVec<kBf16> v;
       v.read(at + s * 32);
+      float most = fmaxf(v.x[0], v.x[1]);
 #pragma unroll
-      for (int i = 0; i < kN; ++i) f(v.x[i], id + s * (32 * kN) + i);
+      for (int i = 2; i < kN; i += 2) most = sm100::fmax3(most, v.x[i], v.x[i + 1]);
+      if (most >= from) f(v.x, id + s * (32 * kN));
     }
+  }
+  // Calls f(logit, id) for every logit of `from` or more (and some others).
+  template <class F>
+  __device__ __forceinline__ void each(float from, F f) const {
+    each_vec(from, [&](const float (&x)[kN], int first) {
+#pragma unroll
+      for (int i = 0; i < kN; ++i) f(x[i], first + i);
+    });
   }
 };
 
-// The bin of d = (x - m) / T: -1 above the bins, kBins below them.  The same rounding
-// for every logit, so that a larger logit is never in a later bin; y - kRound is the bin.
+// The bin of a distance: -1 above the bins, kBins below them.  The same rounding for
+// every logit, so that a larger logit is never in a later bin; y - kRound is the bin.
 constexpr float kRound = 12582912.f;  // 1.5 * 2^23
-__device__ __forceinline__ int bin_of(float d, const Bins &b, float &rest) {
-  const float at = fminf(fmaxf(__fmul_rn(__fsub_rn(-d, b.from), b.scale), -1.f), (float)kBins);
+__device__ __forceinline__ int bin_of(float distance, const Bins &b, float &rest) {
+  const float at = fminf(fmaxf(__fmul_rn(__fsub_rn(distance, b.from), b.scale), -1.f), (float)kBins);
   const float y = __fadd_rn(at, kRound);
   rest = __fsub_rn(at, __fsub_rn(y, kRound));
   return (int)(__float_as_uint(y) - 0x4B400000u);
+}
+// A logit that is no larger than any of bin `last` (two bins and some rounding lower).
+__device__ __forceinline__ float logit_of(const Bins &b, int last, float m, float inv_unit) {
+  const float far = b.from + (float)(last + 2) / b.scale;
+  return m - far * inv_unit * 1.00001f - fabsf(m) * 0x1p-21f;
 }
 
 // Count and weight over the block, in every thread.
@@ -285,11 +328,13 @@ __device__ __forceinline__ long long cluster_total(SpShared &sh, int &turn, uint
 // logits at the border.
 template <bool kBf16>
 __device__ __noinline__ Border bitwise_border(SpShared &sh, const Run<kBf16> &run, int &turn, const Border kept, int k, float p) {
-  auto above = [&](const Border &b, int &count) -> long long {
+  // (ordered logit, kMaxVocab - 1 - id) and above
+  auto above = [&](uint32_t hi, uint32_t lo, int &count) -> long long {
     Fixed f;
     int c = 0;
-    run.each([&](float x, int id) {
-      const bool in = x > -INFINITY && b.has(ordered(x), id) && kept.has(ordered(x), id);
+    run.each(-INFINITY, [&](float x, int id) {
+      const uint32_t o = ordered(x);
+      const bool in = kept.has(x, id) && (o > hi || (o == hi && (uint32_t)(kMaxVocab - 1 - id) >= lo));
       c += in;
       if (in && k == 0) f.add(expf(run.scaled(x)));
     });
@@ -299,86 +344,97 @@ __device__ __noinline__ Border bitwise_border(SpShared &sh, const Run<kBf16> &ru
   int n;
   long long least = 0;
   if (k == 0) {
-    const double want = (double)p * (double)above(kept, n);
+    const double want = (double)p * (double)above(0u, 0u, n);
     least = want > 1.0 ? (long long)ceil(want) : 1;
   }
-  Border b;
+  uint32_t hi = 0u, lo = 0u;
 #pragma unroll 1
   for (int bit = 49; bit >= 0; --bit) {
-    Border t = b;
-    if (bit >= 18) t.hi |= 1u << (bit - 18);
-    else t.lo |= 1u << bit;
-    const long long sum = above(t, n);
-    if (k ? n >= k : sum >= least) b = t;
+    const uint32_t h = hi | (bit >= 18 ? 1u << (bit - 18) : 0u), l = lo | (bit < 18 ? 1u << bit : 0u);
+    const long long sum = above(h, l, n);
+    if (k ? n >= k : sum >= least) {
+      hi = h;
+      lo = l;
+    }
   }
-  return b.hi > kept.hi || (b.hi == kept.hi && b.lo > kept.lo) ? b : kept;
+  Border b;
+  b.x = unordered(hi);
+  b.id = kMaxVocab - 1 - (int)lo;
+  return b;
 }
 
-// First CTA: the bins that hold the border, from the cluster's histogram.  `above`:
-// count or weight above the bins; `all`: the whole weight where the first level's
-// bins are looked at for top-p (their sum is then known better from below).
-__device__ __forceinline__ void find_bins(SpShared &sh, const Bins bins, bool by_count, double target, double above,
-                                          double all, int level, int V) {
+// First CTA: the bins that hold the border, from the cluster's histograms.
+// Counts, and the first level of top-p from its end: `need` more from the bins' top
+// on, or at most `room` left behind the border (the exact sum less the share wanted: what
+// is left is small, and known better by itself than as a difference); `skipped`: the weight
+// that was not binned.
+__device__ __forceinline__ void find_bins(SpShared &sh, const Bins bins, bool by_count, float need, float room,
+                                          bool from_end, float skipped, uint32_t ranks, int level, int V) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  double v[kThreadBins], mine = 0.0;
-  float n[kThreadBins];
+  static_assert(kThreadBins == 4, "");
+  uint32_t h[4] = {0u, 0u, 0u, 0u};
+  for (uint32_t p = 0; p < ranks; ++p) {
+    const uint4 x = ld_peer128(&sh.hist[tid * 4], p);
+    h[0] += x.x;
+    h[1] += x.y;
+    h[2] += x.z;
+    h[3] += x.w;
+  }
+  float v[4], mine = 0.f;
 #pragma unroll
-  for (int i = 0; i < kThreadBins; ++i) {
-    const int b = tid * kThreadBins + i;
-    const uint32_t h = sh.hist[b];
-    n[i] = by_count ? (float)h : (float)h * (1.02f / kShare);
-    v[i] = by_count ? (double)h : h ? (double)h * (double)(expf(-(bins.from + (float)b / bins.scale)) / kShare) : 0.0;
+  for (int i = 0; i < 4; ++i) {
+    const float at = bins.from + (float)(tid * 4 + i) / bins.scale;
+    v[i] = by_count ? (float)h[i] : (float)h[i] * (expf(-at) * (1.f / kShare));
     mine += v[i];
   }
-  double upto = mine;
+  float upto = mine;  // from the end when that is what counts
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
-    const double y = __shfl_up_sync(0xffffffffu, upto, off);
-    if (lane >= off) upto += y;
+    const float y = from_end ? __shfl_down_sync(0xffffffffu, upto, off) : __shfl_up_sync(0xffffffffu, upto, off);
+    if (from_end ? lane + off < 32 : lane >= off) upto += y;
   }
-  if (lane == 31) sh.scan[warp] = upto;
+  if (lane == (from_end ? 0 : 31)) sh.scan[warp] = upto;
   if (tid == 0) {
     sh.verdict.lo = sh.verdict.hi = kBins;
     sh.in_border = sh.up_to = 0.f;
   }
   __syncthreads();
-  double before = upto - mine, total = 0.0;
+  float sum = upto - mine;
+  if (from_end) room -= skipped;
 #pragma unroll
-  for (int w = 0; w < kSpWarps; ++w) {
-    if (w < warp) before += sh.scan[w];
-    total += sh.scan[w];
-  }
-  // (a logit's share is off by 2^-14, and by 2^-22 for the bin's own weight)
-  const double e = by_count ? 0.0 : kShareError, beyond = V * 1.3e-14;
-  const bool from_below = !by_count && level == 0;
+  for (int w = 0; w < kSpWarps; ++w)
+    if (from_end ? w > warp : w < warp) sum += sh.scan[w];
+  const float e = by_count ? 0.f : kShareError, beyond = (float)V * 1.3e-14f;
 #pragma unroll
-  for (int i = 0; i < kThreadBins; ++i) {
-    before += v[i];
-    const double rest = max(total - before, 0.0);
-    const bool may = from_below ? all - rest * (1.0 - e) >= target : above + before * (1.0 + e) >= target;
-    const bool must = from_below ? all - rest * (1.0 + e) - beyond >= target : above + before * (1.0 - e) >= target;
-    if (may) atomicMin(&sh.verdict.lo, tid * kThreadBins + i);
-    if (must) atomicMin(&sh.verdict.hi, tid * kThreadBins + i);
+  for (int i = 0; i < 4; ++i) {
+    const int j = from_end ? 3 - i : i;
+    if (!from_end) sum += v[j];
+    // from the end, `sum` is what bins after j hold
+    const bool may = from_end ? sum * (1.f - e) <= room : sum * (1.f + e) >= need;
+    const bool must = from_end ? sum * (1.f + e) + beyond <= room : sum * (1.f - e) >= need;
+    if (from_end) sum += v[j];
+    if (may) atomicMin(&sh.verdict.lo, tid * 4 + j);
+    if (must) atomicMin(&sh.verdict.hi, tid * 4 + j);
   }
   __syncthreads();
   const int lo = sh.verdict.lo, hi = min(sh.verdict.hi, kBins - 1);
-  float in = 0.f, up = 0.f;
+  float in = 0.f, up = 0.f;  // how many logits; from shares at most 2% too many
 #pragma unroll
-  for (int i = 0; i < kThreadBins; ++i) {
-    const int b = tid * kThreadBins + i;
-    if (b >= lo && b <= hi) in += n[i];
-    if (b <= hi) up += n[i];
+  for (int i = 0; i < 4; ++i) {
+    const int b = tid * 4 + i;
+    const float n = by_count ? (float)h[i] : (float)h[i] * (1.02f / kShare);
+    if (b >= lo && b <= hi) in += n;
+    if (b <= hi) up += n;
   }
   if (in > 0.f) atomicAdd(&sh.in_border, in);
   if (up > 0.f) atomicAdd(&sh.up_to, up);
   __syncthreads();
   if (tid == 0) {
-    const bool found = lo < kBins;
     sh.verdict.hi = hi;
-    sh.verdict.what = !found                                   ? kBitwise
+    sh.verdict.what = lo == kBins                              ? (by_count && bins.scale == kCountScale ? kWiden : kBitwise)
                       : level == 0 && sh.up_to <= (float)kList ? kGather
                       : sh.in_border <= (float)kList           ? kCollect
-                      : level == 0                             ? kZoom
+                      : level < kLevels                        ? kZoom
                                                                : kBitwise;
   }
 }
@@ -446,14 +502,19 @@ __global__ void __launch_bounds__(kSpThreads, 3) sampling_kernel(const SpArgs a)
     }
     for (int b = tid; b < kBins; b += kSpThreads) sh.hist[b] = 0u;
     if (tid == 0) {
-      sh.sum_all = sh.sum_above = 0ull;
+      sh.sum_all = sh.sum_near = sh.sum_above = 0ull;
       sh.count_all = sh.count_above = sh.listed = sh.mine = 0;
       sh.failed = false;
     }
     cp_async_wait_all();
   }
   float m = -INFINITY;
-  run.each([&](float x, int) { m = max_nan(m, x); });
+  for (int s = 0; s < run.steps; ++s) {
+    Vec x;
+    x.read(mine + s * 32);
+#pragma unroll
+    for (int i = 0; i < kN; i += 2) m = max3_nan(m, x.x[i], x.x[i + 1]);
+  }
 #pragma unroll
   for (int off = 16; off; off >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, off));
   if (lane == 0) sh.wmax[warp] = m;
@@ -493,63 +554,88 @@ __global__ void __launch_bounds__(kSpThreads, 3) sampling_kernel(const SpArgs a)
   for (int stage = 0; stage < 2; ++stage) {
     const bool by_count = stage == 0;
     if (by_count ? k >= V : top_p >= 1.f) continue;
-    Bins bins{0.f, kBinScale};
+    // top-p: from its border on there is more than (1 - p) of a weight of 1 or more, so no
+    // logit at or above it has less than (1 - p) / V; what has only adds to the sum
+    const float inv_unit = by_count ? 1.f : 1.f / run.inv_t;
+    const float near = by_count ? INFINITY : logf((float)V) - logf(1.f - top_p) + 0.05f;
+    Bins bins{0.f, by_count ? kCountScale : kWeightScale};
     Verdict v;
+    bool again = false;  // a histogram was made
 #pragma unroll 1
-    for (int level = 0;; ++level) {
+    for (int level = 0;;) {
       // histogram of what is kept so far
       const float inv_scale = 1.f / bins.scale;
-      Fixed all, over;
+      Fixed all, over;  // over: weight near the top, and once bins are cut again, above them
       int count = 0, count_over = 0;
-      run.each([&](float x, int id) {
-        if (!(x > -INFINITY) || !kept.has(ordered(x), id)) return;
-        const float d = run.scaled(x);
-        float rest;
-        const int b = bin_of(d, bins, rest);
-        ++count;
-        if (by_count) {
-          if ((unsigned)b < (unsigned)kBins) atomicAdd(&sh.hist[b], 1u);
+      const float from = level ? logit_of(bins, kBins, m, inv_unit) : -INFINITY;
+      if (by_count) {
+        run.each(from, [&](float x, int) {
+          const bool in = x > -INFINITY;
+          float rest;
+          const int b = bin_of(__fsub_rn(m, x), bins, rest);
+          count += in;
+          if (in && (unsigned)b < (unsigned)kBins) atomicAdd(&sh.hist[b], 1u);
           count_over += b < 0;
-        } else {
-          if (level == 0) all.add(expf(d));
-          else if (b < 0) over.add(expf(d));
-          if ((unsigned)b < (unsigned)kBins) {
-            const float z = rest * inv_scale;  // ln of (the bin's weight / this one)
-            const float share = fmaf(z, fmaf(z, 0.5f, -1.f), 1.f) * kShare;
-            atomicAdd(&sh.hist[b], __float_as_uint(__fadd_rn(share, kRound)) - 0x4B400000u);
+        });
+      } else {
+        run.each_vec(from, [&](const float (&x)[kN], int first) {
+          float w[kN];
+#pragma unroll
+          for (int i = 0; i < kN; ++i) {
+            const float d = run.scaled(x[i]);
+            const bool in = stage == 0 || k >= V || kept.has(x[i], first + i);
+            w[i] = in ? expf(d) : 0.f;
+            if (in && d >= -near) {
+              float rest;
+              const int b = bin_of(-d, bins, rest);
+              if (level == 0 || b < 0) over.add(w[i]);
+              if ((unsigned)b < (unsigned)kBins) {
+                const float z = rest * inv_scale;  // ln of (the bin's weight / this one)
+                const float share = fmaf(z, fmaf(z, 0.5f, -1.f), 1.f) * kShare;
+                atomicAdd(&sh.hist[b], __float_as_uint(__fadd_rn(share, kRound)) - 0x4B400000u);
+              }
+            }
           }
-        }
-      });
-      const long long sums = block_total(sh, count, level == 0 ? all.value() : over.value());
-      count_over = __reduce_add_sync(0xffffffffu, count_over);
-      if (lane == 0 && count_over) add_first32(&sh.count_above, count_over);
-      if (tid == 0) {
-        if (level == 0) add_first32(&sh.count_all, count);
-        add_first64(level == 0 ? &sh.sum_all : &sh.sum_above, (unsigned long long)sums);
+          if (level == 0) {
+#pragma unroll
+            for (int i = 0; i < kN; i += 2) all.add2(w[i], w[i + 1]);
+          }
+        });
       }
-      if (rank != 0)
-        for (int b = tid; b < kBins; b += kSpThreads) {
-          const uint32_t h = sh.hist[b];
-          if (h) add_first32(&sh.hist[b], h);
-          sh.hist[b] = 0u;  // (for the next one)
-        }
+      const long long sums = block_total(sh, count, all.value());
+      const long long overs = warp_sum(over.value());
+      count_over = __reduce_add_sync(0xffffffffu, count_over);
+      if (lane == 0) {
+        if (count_over) add_first32(&sh.count_above, count_over);
+        if (overs) add_first64(level ? &sh.sum_above : &sh.sum_near, (unsigned long long)overs);
+      }
+      if (tid == 0 && !again) {
+        add_first32(&sh.count_all, count);
+        add_first64(&sh.sum_all, (unsigned long long)sums);
+      }
+      again = true;
       cluster_sync();
       if (rank == 0) {
-        const double target = by_count ? (double)k : (double)top_p * (double)(long long)sh.sum_all * (double)kUnit;
-        const double above = by_count ? (double)sh.count_above : (double)(long long)sh.sum_above * (double)kUnit;
         if (by_count && sh.count_all <= k) {
           if (tid == 0) sh.verdict.what = kNone;
         } else {
-          find_bins(sh, bins, by_count, by_count ? target : max(target, (double)kUnit), above,
-                    (double)(long long)sh.sum_all * (double)kUnit, level, V);
+          if (tid == 0) {
+            const double all = (double)(long long)sh.sum_all, want = max((double)top_p * all, 1.0);
+            sh.need = by_count ? (float)(k - sh.count_above) : (float)((want - (double)(long long)sh.sum_above) * (double)kUnit);
+            sh.room = (float)((all - want) * (double)kUnit);
+            sh.skipped = (float)((long long)sh.sum_all - (long long)sh.sum_near) * kUnit;
+          }
+          __syncthreads();
+          find_bins(sh, bins, by_count, sh.need, sh.room, !by_count && level == 0, sh.skipped, ranks, level, V);
         }
         __syncthreads();
+        // (before the others put their lists there)
         for (int b = tid; b < kBins; b += kSpThreads) sh.hist[b] = 0u;
         if (tid == 0) {
           sh.sum_above = 0ull;
           sh.count_above = 0;
           if (sh.verdict.what == kNone || sh.verdict.what == kBitwise) {
-            sh.sum_all = 0ull;
+            sh.sum_all = sh.sum_near = 0ull;
             sh.count_all = 0;
           }
         }
@@ -558,11 +644,19 @@ __global__ void __launch_bounds__(kSpThreads, 3) sampling_kernel(const SpArgs a)
       v.what = (int)ld_peer32(&sh.verdict.what, 0);
       v.lo = (int)ld_peer32(&sh.verdict.lo, 0);
       v.hi = (int)ld_peer32(&sh.verdict.hi, 0);
+      if (rank != 0)
+        for (int b = tid; b < kBins; b += kSpThreads) sh.hist[b] = 0u;  // (for the next one)
+      __syncthreads();
+      if (v.what == kWiden) {
+        bins.scale = kWideScale;
+        continue;
+      }
       if (v.what != kZoom) break;
       // the border's bins, a little widened, are cut again
       const float width = (float)(v.hi - v.lo + 1) / bins.scale;
       bins.from += ((float)v.lo - 0.5f) / bins.scale - 0.01f * width;
       bins.scale = (float)(kBins - 1) / (1.02f * width);
+      ++level;
     }
     if (v.what == kNone) continue;
     if (v.what != kBitwise) {
@@ -570,11 +664,11 @@ __global__ void __launch_bounds__(kSpThreads, 3) sampling_kernel(const SpArgs a)
       const int lo = v.what == kGather ? -1 : v.lo;
       Fixed over;
       int count = 0;
-      run.each([&](float x, int id) {
-        if (!(x > -INFINITY) || !kept.has(ordered(x), id)) return;
-        const float d = run.scaled(x);
+      run.each(logit_of(bins, v.hi, m, inv_unit), [&](float x, int id) {
+        if (!kept.has(x, id)) return;
+        const float d = by_count ? __fsub_rn(x, m) : run.scaled(x);
         float rest;
-        const int b = bin_of(d, bins, rest);
+        const int b = bin_of(-d, bins, rest);
         if (b > v.hi) return;
         if (b < lo) {
           ++count;
@@ -610,8 +704,8 @@ __global__ void __launch_bounds__(kSpThreads, 3) sampling_kernel(const SpArgs a)
         __syncthreads();
         if (tid == 0) {
           sh.failed = n > kList;
-          sh.border_hi = kept.hi;
-          sh.border_lo = kept.lo;
+          sh.border_x = kept.x;
+          sh.border_id = kept.id;
           sh.total = 0;
         }
         constexpr int kMine = kList / kSpThreads;
@@ -658,17 +752,17 @@ __global__ void __launch_bounds__(kSpThreads, 3) sampling_kernel(const SpArgs a)
             }
             if (top_p < 1.f) {
               s = block_total(sh, unused, s);
-              const double want = (double)top_p * (double)(stage == 0 ? s : everything);
+              const long long want = (long long)ceil((double)top_p * (double)(stage == 0 ? s : everything));
 #pragma unroll
-              for (int e = 0; e < kMine; ++e) in[e] = in[e] && (place[e] == 0 || (double)before[e] < want);
+              for (int e = 0; e < kMine; ++e) in[e] = in[e] && (place[e] == 0 || before[e] < want);
             }
           } else {
             // one filter's border
-            const double want = (double)top_p * (double)everything;
-            if (!by_count && (double)base >= want) sh.failed = true;  // (it lies above the list)
+            const long long want = by_count ? 0 : (long long)ceil((double)top_p * (double)everything);
+            if (!by_count && base >= want) sh.failed = true;  // (it lies above the list)
 #pragma unroll
             for (int e = 0; e < kMine; ++e)
-              in[e] = c[e] != 0ull && (by_count ? more + place[e] < k : (double)(base + before[e]) < want);
+              in[e] = c[e] != 0ull && (by_count ? more + place[e] < k : base + before[e] < want);
           }
           // the border is the lowest that is kept
           int kept_here = 0;
@@ -679,8 +773,8 @@ __global__ void __launch_bounds__(kSpThreads, 3) sampling_kernel(const SpArgs a)
 #pragma unroll
           for (int e = 0; e < kMine; ++e) {
             if (in[e] && place[e] == kept_here - 1) {
-              sh.border_hi = (uint32_t)(c[e] >> 32);
-              sh.border_lo = (uint32_t)(kMaxVocab - 1) - ~(uint32_t)c[e];
+              sh.border_x = unordered((uint32_t)(c[e] >> 32));
+              sh.border_id = (int)~(uint32_t)c[e];
             }
             if (v.what == kGather) in[e] = in[e] && !(w[e] < min_p);
             if (in[e]) s += fw[e];
@@ -697,6 +791,10 @@ __global__ void __launch_bounds__(kSpThreads, 3) sampling_kernel(const SpArgs a)
                 if (c[e]) sh.weight[tid + e * kSpThreads] = in[e] ? (unsigned long long)fw[e] : 0ull;
                 before[e] = 0;
               }
+              if (tid < a.draws) {
+                const float u = a.u[(size_t)r * a.draws + tid];
+                sh.at[tid] = min(u > 0.f ? (long long)floor((double)u * (double)s) : 0, s - 1);
+              }
               __syncthreads();
               for (int j = 0; j < n; ++j) {
                 const uint32_t o = (uint32_t)sh.list[j];
@@ -707,9 +805,7 @@ __global__ void __launch_bounds__(kSpThreads, 3) sampling_kernel(const SpArgs a)
               }
               const float log_total = logf((float)s * kUnit);
               for (int q = 0; q < a.draws; ++q) {
-                const float u = a.u[(size_t)r * a.draws + q];
-                long long at = u > 0.f ? (long long)floor((double)u * (double)s) : 0;
-                at = min(at, s - 1);
+                const long long at = sh.at[q];
 #pragma unroll
                 for (int e = 0; e < kMine; ++e)
                   if (in[e] && at >= before[e] && at < before[e] + fw[e]) {
@@ -724,7 +820,7 @@ __global__ void __launch_bounds__(kSpThreads, 3) sampling_kernel(const SpArgs a)
         for (int b = tid; b < kBins; b += kSpThreads) sh.hist[b] = 0u;  // (it lies over the list)
         if (tid == 0) {
           sh.listed = sh.count_all = sh.count_above = 0;
-          sh.sum_all = sh.sum_above = 0ull;
+          sh.sum_all = sh.sum_near = sh.sum_above = 0ull;
         }
       } else {
         for (int b = tid; b < kBins; b += kSpThreads) sh.hist[b] = 0u;
@@ -732,8 +828,8 @@ __global__ void __launch_bounds__(kSpThreads, 3) sampling_kernel(const SpArgs a)
       if (kMode == kSample && v.what == kGather) return;  // (nothing of this CTA is read any more)
       cluster_sync();
       if (ld_peer32(&sh.failed, 0) & 0xFFu) v.what = kBitwise;
-      kept.hi = ld_peer32(&sh.border_hi, 0);
-      kept.lo = ld_peer32(&sh.border_lo, 0);
+      kept.x = __uint_as_float(ld_peer32(&sh.border_x, 0));
+      kept.id = (int)ld_peer32(&sh.border_id, 0);
       total = (long long)ld_peer64(&sh.total, 0);
     }
     if (v.what == kBitwise) {
@@ -745,13 +841,13 @@ __global__ void __launch_bounds__(kSpThreads, 3) sampling_kernel(const SpArgs a)
 
   // ---- what is kept ----
   auto weight = [&](float x, int id) -> float {  // 0: not kept
-    if (!(x > -INFINITY) || !kept.has(ordered(x), id)) return 0.f;
+    if (!kept.has(x, id)) return 0.f;
     const float w = expf(run.scaled(x));
     return w < min_p ? 0.f : w;
   };
   if (kMode == kSample || (kMode == kProbs && total < 0)) {
     Fixed f;
-    run.each([&](float x, int id) { f.add(weight(x, id)); });
+    run.each(kept.x, [&](float x, int id) { f.add(weight(x, id)); });
     int unused = 0;
     total = cluster_total(sh, turn, ranks, unused, f.value());
   }
@@ -761,10 +857,13 @@ __global__ void __launch_bounds__(kSpThreads, 3) sampling_kernel(const SpArgs a)
     for (int w = 0; w < warp; ++w) before += sh.wsum[w];
     const long long here = sh.wsum[warp];
     const float log_total = logf((float)total * kUnit);
+    if (tid < a.draws) {
+      const float u = a.u[(size_t)r * a.draws + tid];
+      sh.at[tid] = min(u > 0.f ? (long long)floor((double)u * (double)total) : 0, total - 1);
+    }
+    __syncthreads();
     for (int q = 0; q < a.draws; ++q) {
-      const float u = a.u[(size_t)r * a.draws + q];
-      long long at = u > 0.f ? (long long)floor((double)u * (double)total) : 0;
-      at = min(at, total - 1) - before;
+      long long at = sh.at[q] - before;
       if (at < 0 || at >= here) continue;
       for (int s = 0; s < run.steps; ++s) {
         Vec x;
@@ -819,7 +918,7 @@ __global__ void __launch_bounds__(kSpThreads, 3) sampling_kernel(const SpArgs a)
 #pragma unroll
       for (int i = 0; i < kN; ++i) {
         const float d = run.scaled(x.x[i]);
-        bool in = x.x[i] > -INFINITY && kept.has(ordered(x.x[i]), id + i);
+        bool in = kept.has(x.x[i], id + i);
         float w = 0.f;
         if (in && (kMode == kProbs || min_p > 0.f)) {
           w = expf(d);
