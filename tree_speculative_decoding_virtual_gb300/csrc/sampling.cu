@@ -44,10 +44,10 @@ constexpr int kSpWarps = kSpThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kMaxVocab = 262144;
 constexpr int kMaxDraws = 64;
-constexpr int kBins = 1024;
+constexpr int kBins = 2048;
 constexpr int kThreadBins = kBins / kSpThreads;
-constexpr int kList = 512;
-constexpr float kCountScale = 16.f, kWideScale = 0.25f, kWeightScale = 32.f;  // bins a unit at first
+constexpr int kList = 512, kSmallList = 64;
+constexpr float kCountScale = 32.f, kWideScale = 0.5f, kWeightScale = 64.f;  // bins a unit at first
 constexpr int kLevels = 3;          // times bins are cut again at most
 constexpr float kShare = 8192.f;    // a bin's own weight (262144 of them fit 32 bits)
 constexpr float kShareError = 1e-4f;  // (a logit's share is off by 2^-14, sums and exponentials by less)
@@ -77,8 +77,14 @@ struct Border {
 
 // Bins of a logit's distance from the maximum, from `from` on, `scale` a unit.  Top-k's
 // distance is m - x (its border has nothing to do with T), top-p's (m - x) / T.
+constexpr float kRound = 12582912.f;  // 1.5 * 2^23: a sum with it is rounded to a whole number
 struct Bins {
-  float from, scale;
+  float from, scale, shift;  // shift: kRound - from * scale
+  __device__ __forceinline__ void set(float f, float s) {
+    from = f;
+    scale = s;
+    shift = fmaf(-f, s, kRound);
+  }
 };
 
 enum { kNone, kWiden, kZoom, kCollect, kGather, kBitwise };  // what follows a histogram
@@ -97,14 +103,22 @@ struct SpShared {
   };
   float wmax[kSpWarps];
   int wcount[kSpWarps];
-  long long wsum[kSpWarps];
+  long long wsum[kSpWarps], wabove[kSpWarps];
+  int wcount_above[kSpWarps];
   float scan[kSpWarps];
-  float need, room, skipped;
-  long long at[kMaxDraws];
+  float need, room;
   float max;
-  // added up in the first CTA
-  unsigned long long sum_all, sum_near, sum_above;
+  // this CTA's parts of what the first CTA adds up
+  struct {
+    long long all, above;
+    float skipped;
+    int count, count_above;
+  } part;
+  // the first CTA's sums
+  long long sum_all, sum_above;
+  float skipped;
   int count_all, count_above, listed;
+  float u[kMaxDraws];
   // exchanged by the bitwise search and the draws (two places, by turn)
   int count[2];
   long long sum[2];
@@ -113,6 +127,7 @@ struct SpShared {
   float border_x;
   int border_id;
   long long total;
+  unsigned long long extra[kMaxCluster * kSpWarps];  // kept weight of the list, by warp run
   float in_border, up_to;  // how many logits the bins hold
   int mine;
   bool failed;
@@ -159,12 +174,6 @@ __device__ __forceinline__ uint4 ld_peer128(const void *p, uint32_t rank) {
   return v;
 }
 // Into the first CTA's shared memory.
-__device__ __forceinline__ void add_first32(void *p, uint32_t v) {
-  asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;\n" ::"r"(peer(p, 0)), "r"(v) : "memory");
-}
-__device__ __forceinline__ void add_first64(void *p, unsigned long long v) {
-  asm volatile("red.relaxed.cluster.shared::cluster.add.u64 [%0], %1;\n" ::"r"(peer(p, 0)), "l"(v) : "memory");
-}
 __device__ __forceinline__ uint32_t take_first32(void *p, uint32_t v) {
   uint32_t r;
   asm volatile("atom.relaxed.cluster.shared::cluster.add.u32 %0, [%1], %2;\n" : "=r"(r) : "r"(peer(p, 0)), "r"(v) : "memory");
@@ -204,12 +213,21 @@ struct Fixed {
 };
 constexpr float kUnit = 0x1p-43f;
 
+// ln of a sum that holds the largest weight, 1: to the last places where it is near 0 too.
+__device__ __forceinline__ float log_sum(long long total) { return log1pf((float)(total - (1ll << 43)) * kUnit); }
+
 __device__ __forceinline__ long long fixed(float w) {
   Fixed f;
   f.add(w);
   return f.value();
 }
 __device__ __forceinline__ long long warp_sum(long long x) {
+#pragma unroll
+  for (int off = 16; off; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+  return x;
+}
+
+__device__ __forceinline__ float warp_sum(float x) {
 #pragma unroll
   for (int off = 16; off; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
   return x;
@@ -245,7 +263,7 @@ struct Run {
   uint32_t rank, ranks;
 
   __device__ __forceinline__ float scaled(float x) const { return __fmul_rn(__fsub_rn(x, m), inv_t); }
-  // Calls f(logits, id of the first) for every vector of this lane that holds a logit of
+  // Calls f(logits, id of the first, the largest) for every vector of this lane that holds a logit of
   // `from` or more.
   template <class F>
   __device__ __forceinline__ void each_vec(float from, F f) const {
@@ -256,26 +274,23 @@ struct Run {
       float most = fmaxf(v.x[0], v.x[1]);
 #pragma unroll
       for (int i = 2; i < kN; i += 2) most = sm100::fmax3(most, v.x[i], v.x[i + 1]);
-      if (most >= from) f(v.x, id + s * (32 * kN));
+      if (most >= from) f(v.x, id + s * (32 * kN), most);
     }
   }
   // Calls f(logit, id) for every logit of `from` or more (and some others).
   template <class F>
   __device__ __forceinline__ void each(float from, F f) const {
-    each_vec(from, [&](const float (&x)[kN], int first) {
+    each_vec(from, [&](const float (&x)[kN], int first, float) {
 #pragma unroll
       for (int i = 0; i < kN; ++i) f(x[i], first + i);
     });
   }
 };
 
-// The bin of a distance: -1 above the bins, kBins below them.  The same rounding for
-// every logit, so that a larger logit is never in a later bin; y - kRound is the bin.
-constexpr float kRound = 12582912.f;  // 1.5 * 2^23
-__device__ __forceinline__ int bin_of(float distance, const Bins &b, float &rest) {
-  const float at = fminf(fmaxf(__fmul_rn(__fsub_rn(distance, b.from), b.scale), -1.f), (float)kBins);
-  const float y = __fadd_rn(at, kRound);
-  rest = __fsub_rn(at, __fsub_rn(y, kRound));
+// The bin of a distance: -1 above the bins, kBins below them; `y` is kRound + the bin.  The
+// same rounding for every logit, so that a larger logit is never in a later bin.
+__device__ __forceinline__ int bin_of(float distance, const Bins &b, float &y) {
+  y = fminf(fmaxf(fmaf(distance, b.scale, b.shift), kRound - 1.f), kRound + kBins);
   return (int)(__float_as_uint(y) - 0x4B400000u);
 }
 // A logit that is no larger than any of bin `last` (two bins and some rounding lower).
@@ -303,6 +318,130 @@ __device__ __forceinline__ long long block_total(SpShared &sh, int &count, long 
     count += sh.wcount[w];
   }
   return t;
+}
+
+// This CTA's sums for the first CTA.
+__device__ __forceinline__ void block_parts(SpShared &sh, long long all, long long above, float skipped, int count,
+                                            int count_above) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  all = warp_sum(all);
+  above = warp_sum(above);
+  skipped = warp_sum(skipped);
+  count = __reduce_add_sync(0xffffffffu, count);
+  count_above = __reduce_add_sync(0xffffffffu, count_above);
+  if (lane == 0) {
+    sh.wsum[warp] = all;
+    sh.wabove[warp] = above;
+    sh.scan[warp] = skipped;
+    sh.wcount[warp] = count;
+    sh.wcount_above[warp] = count_above;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    all = above = 0;
+    skipped = 0.f;
+    count = count_above = 0;
+#pragma unroll
+    for (int w = 0; w < kSpWarps; ++w) {
+      all += sh.wsum[w];
+      above += sh.wabove[w];
+      skipped += sh.scan[w];
+      count += sh.wcount[w];
+      count_above += sh.wcount_above[w];
+    }
+    sh.part.all = all;
+    sh.part.above = above;
+    sh.part.skipped = skipped;
+    sh.part.count = count;
+    sh.part.count_above = count_above;
+  }
+}
+
+// First CTA, first warp: the cluster's sums (what is added up once stays, the others are
+// new).  In two halves, so that the loads' latency passes while others are under way.
+struct Parts {
+  long long all, above;
+  float skipped;
+  int count, count_above;
+  __device__ __forceinline__ void load(SpShared &sh, uint32_t ranks) {
+    const int lane = threadIdx.x & 31;
+    const bool on = lane < (int)ranks;
+    all = on ? (long long)ld_peer64(&sh.part.all, lane) : 0;
+    above = on ? (long long)ld_peer64(&sh.part.above, lane) : 0;
+    skipped = on ? __uint_as_float(ld_peer32(&sh.part.skipped, lane)) : 0.f;
+    count = on ? (int)ld_peer32(&sh.part.count, lane) : 0;
+    count_above = on ? (int)ld_peer32(&sh.part.count_above, lane) : 0;
+  }
+  __device__ __forceinline__ void sum(SpShared &sh) {
+    all = warp_sum(all);
+    above = warp_sum(above);
+    skipped = warp_sum(skipped);
+    count = __reduce_add_sync(0xffffffffu, count);
+    count_above = __reduce_add_sync(0xffffffffu, count_above);
+    if ((threadIdx.x & 31) == 0) {
+      sh.sum_all += all;
+      sh.sum_above = above;
+      sh.skipped = skipped;
+      sh.count_all += count;
+      sh.count_above = count_above;
+    }
+  }
+};
+
+// Sum over the threads before this one.
+__device__ __forceinline__ long long block_scan(SpShared &sh, long long mine) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long upto = mine;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const long long o = __shfl_up_sync(0xffffffffu, upto, off);
+    if (lane >= off) upto += o;
+  }
+  __syncthreads();
+  if (lane == 31) sh.wsum[warp] = upto;
+  __syncthreads();
+  long long before = upto - mine;
+  for (int w = 0; w < warp; ++w) before += sh.wsum[w];
+  return before;
+}
+
+// Sorts a[0, size), size a power of two of at most twice the threads, in place (a
+// bitonic network; steps within 64 elements stay in a warp).  By the block, or its first warp.
+template <bool kDown, bool kWarp, class T>
+__device__ __forceinline__ void sort(T *a, int size) {
+  const int t = threadIdx.x;
+  if (kWarp) __syncwarp();
+  else __syncthreads();
+  for (int span = 2; span <= size; span *= 2)
+    for (int stride = span / 2; stride; stride /= 2) {
+      if (2 * t < size) {
+        const int i = 2 * t - (t & (stride - 1)), j = i + stride;
+        const T x = a[i], y = a[j];
+        const bool down = ((i & span) == 0) == kDown;
+        if (down ? x < y : y < x) {
+          a[i] = y;
+          a[j] = x;
+        }
+      }
+      // (after a span of 64 the next step crosses warps)
+      if (!kWarp && (stride > 32 || (stride == 1 && span >= 64))) __syncthreads();
+      else __syncwarp();
+    }
+  if (!kWarp) __syncthreads();
+}
+
+// Where a draw falls: the first weight whose sum exceeds this is drawn.  The product of u
+// (24 bits) and the sum is exact in 64 bits and a shift.
+__device__ __forceinline__ long long place_of(float u, long long total) {
+  if (!(u > 0.f)) return 0;
+  if (u >= 1.f) return total - 1;
+  const uint32_t bits = __float_as_uint(u);
+  const int e = (int)(bits >> 23);  // u = f 2^(e - 150), f < 2^24
+  const unsigned long long f = e ? (bits & 0x7FFFFFu) | 0x800000u : bits & 0x7FFFFFu;
+  const int shift = 150 - (e ? e : 1);
+  const unsigned long long hi = __umul64hi(f, (unsigned long long)total), lo = f * (unsigned long long)total;
+  const unsigned long long at = shift >= 128 ? 0ull : shift >= 64 ? hi >> (shift - 64) : (hi << (64 - shift)) | (lo >> shift);
+  return min((long long)at, total - 1);
 }
 
 // The same over the cluster; `turn` is which of the two places is used.
@@ -364,27 +503,51 @@ __device__ __noinline__ Border bitwise_border(SpShared &sh, const Run<kBf16> &ru
 }
 
 // First CTA: the bins that hold the border, from the cluster's histograms.
-// Counts, and the first level of top-p from its end: `need` more from the bins' top
-// on, or at most `room` left behind the border (the exact sum less the share wanted: what
-// is left is small, and known better by itself than as a difference); `skipped`: the weight
-// that was not binned.
-__device__ __forceinline__ void find_bins(SpShared &sh, const Bins bins, bool by_count, float need, float room,
-                                          bool from_end, float skipped, uint32_t ranks, int level, int V) {
+// Counts are added up from the bins' top until there are as many as wanted; so are weights,
+// but at first from their end, until there is more than may be left behind the border (the
+// exact sum less the share wanted: what is left is small, and known better by itself than as
+// a difference).
+__device__ __forceinline__ void find_bins(SpShared &sh, const Bins bins, bool by_count, int k, float top_p,
+                                          uint32_t ranks, int level, int V) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  static_assert(kThreadBins == 4, "");
-  uint32_t h[4] = {0u, 0u, 0u, 0u};
-  for (uint32_t p = 0; p < ranks; ++p) {
-    const uint4 x = ld_peer128(&sh.hist[tid * 4], p);
-    h[0] += x.x;
-    h[1] += x.y;
-    h[2] += x.z;
-    h[3] += x.w;
-  }
-  float v[4], mine = 0.f;
+  static_assert(kThreadBins == 8, "");
+  const bool from_end = !by_count && level == 0;
+  Parts parts;
+  if (warp == 0) parts.load(sh, ranks);
+  uint32_t h[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float at = bins.from + (float)(tid * 4 + i) / bins.scale;
-    v[i] = by_count ? (float)h[i] : (float)h[i] * (expf(-at) * (1.f / kShare));
+  for (uint32_t p0 = 0; p0 < kMaxCluster; p0 += 4) {  // (loads before their uses: one takes some 700 cycles)
+    uint4 x[4][2];
+#pragma unroll
+    for (uint32_t p = 0; p < 4; ++p)
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        x[p][q] = p0 + p < ranks ? ld_peer128(&sh.hist[tid * 8 + q * 4], p0 + p) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+    for (uint32_t p = 0; p < 4; ++p)
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        h[q * 4] += x[p][q].x;
+        h[q * 4 + 1] += x[p][q].y;
+        h[q * 4 + 2] += x[p][q].z;
+        h[q * 4 + 3] += x[p][q].w;
+      }
+  }
+  if (warp == 0) parts.sum(sh);
+  if (tid == 0) {
+    const double all = (double)sh.sum_all, want = max((double)top_p * all, 1.0);
+    sh.need = by_count ? (float)(k - sh.count_above) : (float)((want - (double)sh.sum_above) * (double)kUnit);
+    sh.room = (float)((all - want) * (double)kUnit);
+    sh.verdict.lo = sh.verdict.hi = kBins;
+    sh.in_border = sh.up_to = 0.f;
+  }
+  float v[8], mine = 0.f;
+  const float width = 1.f / bins.scale, step = expf(-width);
+  float own = by_count ? 1.f : expf(-(bins.from + (float)(tid * 8) * width)) * (1.f / kShare);  // a bin's weight
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    v[i] = (float)h[i] * own;
+    if (!by_count) own *= step;
     mine += v[i];
   }
   float upto = mine;  // from the end when that is what counts
@@ -394,48 +557,203 @@ __device__ __forceinline__ void find_bins(SpShared &sh, const Bins bins, bool by
     if (from_end ? lane + off < 32 : lane >= off) upto += y;
   }
   if (lane == (from_end ? 0 : 31)) sh.scan[warp] = upto;
-  if (tid == 0) {
-    sh.verdict.lo = sh.verdict.hi = kBins;
-    sh.in_border = sh.up_to = 0.f;
-  }
   __syncthreads();
   float sum = upto - mine;
-  if (from_end) room -= skipped;
+  if (from_end) sum += sh.skipped;
 #pragma unroll
   for (int w = 0; w < kSpWarps; ++w)
     if (from_end ? w > warp : w < warp) sum += sh.scan[w];
+  const float need = sh.need, room = sh.room;
   const float e = by_count ? 0.f : kShareError, beyond = (float)V * 1.3e-14f;
+  int lo = kBins, hi = kBins;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int j = from_end ? 3 - i : i;
+  for (int i = 0; i < 8; ++i) {
+    const int j = from_end ? 7 - i : i;
     if (!from_end) sum += v[j];
     // from the end, `sum` is what bins after j hold
     const bool may = from_end ? sum * (1.f - e) <= room : sum * (1.f + e) >= need;
     const bool must = from_end ? sum * (1.f + e) + beyond <= room : sum * (1.f - e) >= need;
     if (from_end) sum += v[j];
-    if (may) atomicMin(&sh.verdict.lo, tid * 4 + j);
-    if (must) atomicMin(&sh.verdict.hi, tid * 4 + j);
+    if (may) lo = min(lo, tid * 8 + j);
+    if (must) hi = min(hi, tid * 8 + j);
+  }
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  hi = __reduce_min_sync(0xffffffffu, hi);
+  if (lane == 0) {
+    atomicMin(&sh.verdict.lo, lo);
+    atomicMin(&sh.verdict.hi, hi);
   }
   __syncthreads();
-  const int lo = sh.verdict.lo, hi = min(sh.verdict.hi, kBins - 1);
+  lo = sh.verdict.lo;
+  hi = min(sh.verdict.hi, kBins - 1);
   float in = 0.f, up = 0.f;  // how many logits; from shares at most 2% too many
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int b = tid * 4 + i;
+  for (int i = 0; i < 8; ++i) {
+    const int b = tid * 8 + i;
     const float n = by_count ? (float)h[i] : (float)h[i] * (1.02f / kShare);
     if (b >= lo && b <= hi) in += n;
     if (b <= hi) up += n;
   }
-  if (in > 0.f) atomicAdd(&sh.in_border, in);
-  if (up > 0.f) atomicAdd(&sh.up_to, up);
+  in = warp_sum(in);
+  up = warp_sum(up);
+  if (lane == 0) {
+    if (in > 0.f) atomicAdd(&sh.in_border, in);
+    if (up > 0.f) atomicAdd(&sh.up_to, up);
+  }
   __syncthreads();
   if (tid == 0) {
     sh.verdict.hi = hi;
-    sh.verdict.what = lo == kBins                              ? (by_count && bins.scale == kCountScale ? kWiden : kBitwise)
-                      : level == 0 && sh.up_to <= (float)kList ? kGather
-                      : sh.in_border <= (float)kList           ? kCollect
-                      : level < kLevels                        ? kZoom
-                                                               : kBitwise;
+    const int what = by_count && sh.count_all <= k            ? kNone
+                     : lo == kBins                            ? (by_count && bins.scale == kCountScale ? kWiden : kBitwise)
+                     : level == 0 && sh.up_to <= (float)kList ? kGather
+                     : sh.in_border <= (float)kList           ? kCollect
+                     : level < kLevels                        ? kZoom
+                                                              : kBitwise;
+    sh.verdict.what = what;
+    if (what == kNone || what == kBitwise) {
+      sh.sum_all = 0;
+      sh.count_all = 0;
+    }
+  }
+}
+
+// What the first CTA knows when it has the list.
+struct Found {
+  bool gathered;  // all that may be kept is in the list
+  bool by_count;
+  int k;
+  float top_p, min_p;
+  int n, more;                 // logits in the list, above it
+  long long base, everything;  // weight above the list, of all that was binned
+};
+
+// The first CTA's end of it: ranks the list, finds the border, and where everything
+// is in the list the sum of what is kept and the draws.  By the whole block, or for
+// short lists by its first warp, which needs no barriers.
+template <bool kBf16, int kMode, bool kWarp>
+__device__ __forceinline__ void settle(SpShared &sh, const Run<kBf16> &run, const Found &f, const SpArgs &a, int r) {
+  const int tid = threadIdx.x;
+  constexpr int kScope = kWarp ? 32 : kSpThreads;
+  auto total = [&](int &count, long long mine) -> long long {
+    if constexpr (kWarp) {
+      count = __reduce_add_sync(0xffffffffu, count);
+      return warp_sum(mine);
+    } else {
+      return block_total(sh, count, mine);
+    }
+  };
+  auto scan = [&](long long mine) -> long long {
+    if constexpr (!kWarp) return block_scan(sh, mine);
+    long long upto = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const long long o = __shfl_up_sync(0xffffffffu, upto, off);
+      if (tid >= off) upto += o;
+    }
+    return upto - mine;
+  };
+  auto fence = [&]() {
+    if constexpr (kWarp) __syncwarp();
+    else __syncthreads();
+  };
+  // ranked; thread t then holds the ranks 2 t and 2 t + 1
+  const int n = f.n;
+  int size = 2;
+  while (size < n) size *= 2;
+  for (int i = n + tid; i < size; i += kScope) sh.list[i] = 0ull;
+  sort<true, kWarp>(sh.list, size);
+  const bool weigh = f.gathered || !f.by_count;
+  float x[2], w[2] = {0.f, 0.f};
+  int id[2];
+  long long fw[2], before[2];
+  bool in[2];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const unsigned long long c = 2 * tid + e < n ? sh.list[2 * tid + e] : 0ull;
+    x[e] = unordered((uint32_t)(c >> 32));
+    id[e] = (int)~(uint32_t)c;
+    in[e] = c != 0ull;
+    if (in[e] && weigh) w[e] = expf(run.scaled(x[e]));
+    fw[e] = fixed(w[e]);
+  }
+  before[0] = scan(fw[0] + fw[1]);
+  before[1] = before[0] + fw[0];
+  int here = 0;
+  if (f.gathered) {
+    // top-k, then top-p of what that left
+#pragma unroll
+    for (int e = 0; e < 2; ++e) in[e] = in[e] && 2 * tid + e < f.k;
+    if (f.top_p < 1.f) {
+      const long long left = f.by_count ? total(here, (in[0] ? fw[0] : 0) + (in[1] ? fw[1] : 0)) : f.everything;
+      const long long want = (long long)ceil((double)f.top_p * (double)left);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) in[e] = in[e] && (2 * tid + e == 0 || before[e] < want);
+    }
+  } else {
+    // one filter's border
+    const long long want = f.by_count ? 0 : (long long)ceil((double)f.top_p * (double)f.everything);
+    if (!f.by_count && f.base >= want) sh.failed = true;  // (it lies above the list)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) in[e] = in[e] && (f.by_count ? f.more + 2 * tid + e < f.k : f.base + before[e] < want);
+  }
+  // the border is the last that is kept; then min-p, which the weight alone decides
+  here = in[0] + in[1];
+  total(here, 0);
+  if (here == 0) sh.failed = true;
+  int left = 0;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    if (2 * tid + e == here - 1) {
+      sh.border_x = x[e];
+      sh.border_id = id[e];
+    }
+    if (f.gathered) in[e] = in[e] && !(w[e] < f.min_p);
+    left += in[e];
+  }
+  const long long s = total(left, (in[0] ? fw[0] : 0) + (in[1] ? fw[1] : 0));
+  if (tid == 0) sh.total = f.gathered ? s : f.by_count || f.min_p > 0.f ? -1 : f.base + s;
+  if constexpr (kMode == kSample) {
+    if (!f.gathered) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (in[e] && fw[e]) atomicAdd(&sh.extra[id[e] / a.per_warp], (unsigned long long)fw[e]);
+      return;
+    }
+    // the draws: the same by id
+    static_assert(kMaxVocab * kList <= (1 << 27), "id and rank in a word");
+    uint32_t *by_id = reinterpret_cast<uint32_t *>(sh.list);
+    float *logit = reinterpret_cast<float *>(by_id + kList);
+    fence();  // (the list was read)
+    size = 2;
+    while (size < left) size *= 2;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int i = 2 * tid + e;
+      if (i < size) by_id[i] = in[e] ? (uint32_t)id[e] * kList + i : 0xFFFFFFFFu;
+      logit[i] = x[e];
+      sh.weight[i] = (unsigned long long)fw[e];
+    }
+    sort<false, kWarp>(by_id, size);
+    int rank_of[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const uint32_t one = 2 * tid + e < left ? by_id[2 * tid + e] : 0xFFFFFFFFu;
+      rank_of[e] = one % kList;
+      id[e] = (int)(one / kList);
+      fw[e] = one != 0xFFFFFFFFu ? (long long)sh.weight[rank_of[e]] : 0;
+    }
+    before[0] = scan(fw[0] + fw[1]);
+    before[1] = before[0] + fw[0];
+    const float log_total = log_sum(s);
+    for (int q = 0; q < a.draws; ++q) {
+      const long long at = place_of(sh.u[q], s);
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (at >= before[e] && at < before[e] + fw[e]) {
+          a.tokens[(size_t)r * a.draws + q] = id[e];
+          a.logprob[(size_t)r * a.draws + q] = run.scaled(logit[rank_of[e]]) - log_total;
+        }
+    }
   }
 }
 
@@ -501,9 +819,10 @@ __global__ void __launch_bounds__(kSpThreads, 3) sampling_kernel(const SpArgs a)
       }
     }
     for (int b = tid; b < kBins; b += kSpThreads) sh.hist[b] = 0u;
+    if (kMode == kSample && tid < a.draws) sh.u[tid] = a.u[(size_t)r * a.draws + tid];
     if (tid == 0) {
-      sh.sum_all = sh.sum_near = sh.sum_above = 0ull;
-      sh.count_all = sh.count_above = sh.listed = sh.mine = 0;
+      sh.sum_all = 0;
+      sh.count_all = sh.listed = sh.mine = 0;
       sh.failed = false;
     }
     cp_async_wait_all();
@@ -557,88 +876,83 @@ __global__ void __launch_bounds__(kSpThreads, 3) sampling_kernel(const SpArgs a)
     // top-p: from its border on there is more than (1 - p) of a weight of 1 or more, so no
     // logit at or above it has less than (1 - p) / V; what has only adds to the sum
     const float inv_unit = by_count ? 1.f : 1.f / run.inv_t;
-    const float near = by_count ? INFINITY : logf((float)V) - logf(1.f - top_p) + 0.05f;
-    Bins bins{0.f, by_count ? kCountScale : kWeightScale};
+    // (and the first bins end at 32)
+    const float near = by_count ? INFINITY : fminf(logf((float)V) - logf(1.f - top_p) + 0.05f, 31.9f);
+    Bins bins;
+    bins.set(0.f, by_count ? kCountScale : kWeightScale);
     Verdict v;
     bool again = false;  // a histogram was made
 #pragma unroll 1
     for (int level = 0;;) {
       // histogram of what is kept so far
       const float inv_scale = 1.f / bins.scale;
-      Fixed all, over;  // over: weight near the top, and once bins are cut again, above them
+      // a logit's share of its bin, e^z with z = -rest / scale, to second order
+      const float share2 = 0.5f * kShare * inv_scale * inv_scale, share1 = -kShare * inv_scale;
+      Fixed all, over;    // over: weight above the bins, once they are cut again
+      float skipped = 0.f;  // weight too small to be binned
       int count = 0, count_over = 0;
       const float from = level ? logit_of(bins, kBins, m, inv_unit) : -INFINITY;
       if (by_count) {
         run.each(from, [&](float x, int) {
           const bool in = x > -INFINITY;
-          float rest;
-          const int b = bin_of(__fsub_rn(m, x), bins, rest);
+          float y;
+          const int b = bin_of(__fsub_rn(m, x), bins, y);
           count += in;
           if (in && (unsigned)b < (unsigned)kBins) atomicAdd(&sh.hist[b], 1u);
           count_over += b < 0;
         });
       } else {
-        run.each_vec(from, [&](const float (&x)[kN], int first) {
-          float w[kN];
+        const bool all_kept = k >= V;
+        auto bin = [&](float d, float w) {
+          float y;
+          const int b = bin_of(-d, bins, y);
+          if (level && b < 0) over.add(w);
+          if (!level || (unsigned)b < (unsigned)kBins) {
+            const float rest = fmaf(-d, bins.scale, __fsub_rn(bins.shift, y));
+            const float share = fmaf(rest, fmaf(rest, share2, share1), kShare + kRound);
+            atomicAdd(&sh.hist[b], __float_as_uint(share) - 0x4B400000u);
+          }
+        };
+        if (level) {
+          run.each(from, [&](float x, int id) {
+            const float d = run.scaled(x);
+            if ((all_kept || kept.has(x, id)) && d >= -near) bin(d, expf(d));
+          });
+        } else {
+          const float near_x = m - near * inv_unit * 1.00001f - fabsf(m) * 0x1p-21f;  // (or a little lower)
+          run.each_vec(-INFINITY, [&](const float (&x)[kN], int first, float most) {
+            float d[kN], w[kN];
 #pragma unroll
-          for (int i = 0; i < kN; ++i) {
-            const float d = run.scaled(x[i]);
-            const bool in = stage == 0 || k >= V || kept.has(x[i], first + i);
-            w[i] = in ? expf(d) : 0.f;
-            if (in && d >= -near) {
-              float rest;
-              const int b = bin_of(-d, bins, rest);
-              if (level == 0 || b < 0) over.add(w[i]);
-              if ((unsigned)b < (unsigned)kBins) {
-                const float z = rest * inv_scale;  // ln of (the bin's weight / this one)
-                const float share = fmaf(z, fmaf(z, 0.5f, -1.f), 1.f) * kShare;
-                atomicAdd(&sh.hist[b], __float_as_uint(__fadd_rn(share, kRound)) - 0x4B400000u);
+            for (int i = 0; i < kN; ++i) {
+              d[i] = run.scaled(x[i]);
+              w[i] = expf(d[i]);
+              if (!all_kept && !kept.has(x[i], first + i)) {
+                d[i] = -INFINITY;
+                w[i] = 0.f;
               }
             }
-          }
-          if (level == 0) {
 #pragma unroll
             for (int i = 0; i < kN; i += 2) all.add2(w[i], w[i + 1]);
-          }
-        });
+            if (most < near_x) {
+#pragma unroll
+              for (int i = 0; i < kN; i += 4) skipped += (w[i] + w[i + 1]) + (w[i + 2] + w[i + 3]);
+            } else {
+#pragma unroll
+              for (int i = 0; i < kN; ++i) {
+                if (d[i] >= -near) bin(d[i], w[i]);
+                else skipped += w[i];
+              }
+            }
+          });
+        }
       }
-      const long long sums = block_total(sh, count, all.value());
-      const long long overs = warp_sum(over.value());
-      count_over = __reduce_add_sync(0xffffffffu, count_over);
-      if (lane == 0) {
-        if (count_over) add_first32(&sh.count_above, count_over);
-        if (overs) add_first64(level ? &sh.sum_above : &sh.sum_near, (unsigned long long)overs);
-      }
-      if (tid == 0 && !again) {
-        add_first32(&sh.count_all, count);
-        add_first64(&sh.sum_all, (unsigned long long)sums);
-      }
+      block_parts(sh, again ? 0 : all.value(), over.value(), skipped, again ? 0 : count, count_over);
       again = true;
       cluster_sync();
       if (rank == 0) {
-        if (by_count && sh.count_all <= k) {
-          if (tid == 0) sh.verdict.what = kNone;
-        } else {
-          if (tid == 0) {
-            const double all = (double)(long long)sh.sum_all, want = max((double)top_p * all, 1.0);
-            sh.need = by_count ? (float)(k - sh.count_above) : (float)((want - (double)(long long)sh.sum_above) * (double)kUnit);
-            sh.room = (float)((all - want) * (double)kUnit);
-            sh.skipped = (float)((long long)sh.sum_all - (long long)sh.sum_near) * kUnit;
-          }
-          __syncthreads();
-          find_bins(sh, bins, by_count, sh.need, sh.room, !by_count && level == 0, sh.skipped, ranks, level, V);
-        }
-        __syncthreads();
+        find_bins(sh, bins, by_count, k, top_p, ranks, level, V);
         // (before the others put their lists there)
         for (int b = tid; b < kBins; b += kSpThreads) sh.hist[b] = 0u;
-        if (tid == 0) {
-          sh.sum_above = 0ull;
-          sh.count_above = 0;
-          if (sh.verdict.what == kNone || sh.verdict.what == kBitwise) {
-            sh.sum_all = sh.sum_near = 0ull;
-            sh.count_all = 0;
-          }
-        }
       }
       cluster_sync();
       v.what = (int)ld_peer32(&sh.verdict.what, 0);
@@ -648,14 +962,13 @@ __global__ void __launch_bounds__(kSpThreads, 3) sampling_kernel(const SpArgs a)
         for (int b = tid; b < kBins; b += kSpThreads) sh.hist[b] = 0u;  // (for the next one)
       __syncthreads();
       if (v.what == kWiden) {
-        bins.scale = kWideScale;
+        bins.set(0.f, kWideScale);
         continue;
       }
       if (v.what != kZoom) break;
       // the border's bins, a little widened, are cut again
       const float width = (float)(v.hi - v.lo + 1) / bins.scale;
-      bins.from += ((float)v.lo - 0.5f) / bins.scale - 0.01f * width;
-      bins.scale = (float)(kBins - 1) / (1.02f * width);
+      bins.set(bins.from + ((float)v.lo - 0.5f) / bins.scale - 0.01f * width, (float)(kBins - 1) / (1.02f * width));
       ++level;
     }
     if (v.what == kNone) continue;
@@ -664,27 +977,28 @@ __global__ void __launch_bounds__(kSpThreads, 3) sampling_kernel(const SpArgs a)
       const int lo = v.what == kGather ? -1 : v.lo;
       Fixed over;
       int count = 0;
-      run.each(logit_of(bins, v.hi, m, inv_unit), [&](float x, int id) {
-        if (!kept.has(x, id)) return;
-        const float d = by_count ? __fsub_rn(x, m) : run.scaled(x);
-        float rest;
-        const int b = bin_of(-d, bins, rest);
-        if (b > v.hi) return;
-        if (b < lo) {
-          ++count;
-          if (!by_count) over.add(expf(d));
-          return;
-        }
+      auto list = [&](float x, int id) {
         const int at = atomicAdd(rank == 0 ? &sh.listed : &sh.mine, 1);
         if (at < kList) sh.list[at] = ((unsigned long long)ordered(x) << 32) | (uint32_t)~id;
-      });
-      if (v.what == kCollect) {
-        const long long sums = block_total(sh, count, over.value());
-        if (tid == 0) {
-          add_first32(&sh.count_above, count);
-          add_first64(&sh.sum_above, (unsigned long long)sums);
+      };
+      run.each_vec(logit_of(bins, v.hi, m, inv_unit), [&](const float (&x)[kN], int first, float) {
+        float w[kN];
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+          const bool in = kept.has(x[i], first + i);
+          const float d = by_count ? __fsub_rn(x[i], m) : run.scaled(x[i]);
+          float y;
+          const int b = bin_of(-d, bins, y);
+          w[i] = in && b < lo ? expf(d) : 0.f;
+          count += in && b < lo;
+          if (in && b >= lo && b <= v.hi) list(x[i], first + i);
         }
-      }
+        if (!by_count && v.what == kCollect) {
+#pragma unroll
+          for (int i = 0; i < kN; i += 2) over.add2(w[i], w[i + 1]);
+        }
+      });
+      block_parts(sh, 0, over.value(), 0.f, 0, count);
       __syncthreads();
       if (rank != 0) {
         const int n = sh.mine;
@@ -698,8 +1012,15 @@ __global__ void __launch_bounds__(kSpThreads, 3) sampling_kernel(const SpArgs a)
       }
       cluster_sync();
       if (rank == 0) {
+        // (not with kGather: there is nothing above, and the other CTAs of a draw may be gone)
+        if (v.what == kCollect && warp == 0) {
+          Parts parts;
+          parts.load(sh, ranks);
+          parts.sum(sh);
+        }
+        __syncthreads();
         const int n = sh.listed;
-        const long long base = (long long)sh.sum_above, everything = (long long)sh.sum_all;
+        const long long base = sh.sum_above, everything = sh.sum_all;
         const int more = sh.count_above;
         __syncthreads();
         if (tid == 0) {
@@ -708,119 +1029,18 @@ __global__ void __launch_bounds__(kSpThreads, 3) sampling_kernel(const SpArgs a)
           sh.border_id = kept.id;
           sh.total = 0;
         }
-        constexpr int kMine = kList / kSpThreads;
-        unsigned long long c[kMine];
-        float w[kMine];
-        long long before[kMine], fw[kMine];
-        int place[kMine];
-        const bool weigh = v.what == kGather || !by_count;
-#pragma unroll
-        for (int e = 0; e < kMine; ++e) {
-          const int i = tid + e * kSpThreads;
-          c[e] = i < min(n, kList) ? sh.list[i] : 0ull;
-          w[e] = 0.f;
-          if (c[e] && weigh) {
-            w[e] = expf(run.scaled(unordered((uint32_t)(c[e] >> 32))));
-            sh.weight[i] = (unsigned long long)fixed(w[e]);
-          }
-          fw[e] = fixed(w[e]);
-          before[e] = 0;
-          place[e] = 0;
-        }
-        __syncthreads();
-        if (n <= kList) {
-          // rank, and the weight of what ranks higher
-          for (int j = 0; j < n; ++j) {
-            const unsigned long long o = sh.list[j];
-            const long long ow = weigh ? (long long)sh.weight[j] : 0;
-#pragma unroll
-            for (int e = 0; e < kMine; ++e)
-              if (o > c[e]) {
-                ++place[e];
-                before[e] += ow;
-              }
-          }
-          bool in[kMine];
-          if (v.what == kGather) {
-            // all that may be kept is here: top-k, then top-p of what that left, then min-p
-            long long s = 0;
-            int unused = 0;
-#pragma unroll
-            for (int e = 0; e < kMine; ++e) {
-              in[e] = c[e] != 0ull && (stage == 1 || place[e] < k);
-              if (in[e]) s += fw[e];
-            }
-            if (top_p < 1.f) {
-              s = block_total(sh, unused, s);
-              const long long want = (long long)ceil((double)top_p * (double)(stage == 0 ? s : everything));
-#pragma unroll
-              for (int e = 0; e < kMine; ++e) in[e] = in[e] && (place[e] == 0 || before[e] < want);
-            }
-          } else {
-            // one filter's border
-            const long long want = by_count ? 0 : (long long)ceil((double)top_p * (double)everything);
-            if (!by_count && base >= want) sh.failed = true;  // (it lies above the list)
-#pragma unroll
-            for (int e = 0; e < kMine; ++e)
-              in[e] = c[e] != 0ull && (by_count ? more + place[e] < k : base + before[e] < want);
-          }
-          // the border is the lowest that is kept
-          int kept_here = 0;
-          long long s = 0;
-#pragma unroll
-          for (int e = 0; e < kMine; ++e) kept_here += in[e];
-          block_total(sh, kept_here, 0);
-#pragma unroll
-          for (int e = 0; e < kMine; ++e) {
-            if (in[e] && place[e] == kept_here - 1) {
-              sh.border_x = unordered((uint32_t)(c[e] >> 32));
-              sh.border_id = (int)~(uint32_t)c[e];
-            }
-            if (v.what == kGather) in[e] = in[e] && !(w[e] < min_p);
-            if (in[e]) s += fw[e];
-          }
-          if (kept_here == 0) sh.failed = true;
-          int unused = 0;
-          s = block_total(sh, unused, s);
-          if (tid == 0) sh.total = v.what == kGather ? s : by_count || min_p > 0.f ? -1 : base + s;
-          if constexpr (kMode == kSample) {
-            if (v.what == kGather) {
-              // the draws: the weight of what is kept and has a lower id
-#pragma unroll
-              for (int e = 0; e < kMine; ++e) {
-                if (c[e]) sh.weight[tid + e * kSpThreads] = in[e] ? (unsigned long long)fw[e] : 0ull;
-                before[e] = 0;
-              }
-              if (tid < a.draws) {
-                const float u = a.u[(size_t)r * a.draws + tid];
-                sh.at[tid] = min(u > 0.f ? (long long)floor((double)u * (double)s) : 0, s - 1);
-              }
-              __syncthreads();
-              for (int j = 0; j < n; ++j) {
-                const uint32_t o = (uint32_t)sh.list[j];
-                const long long ow = (long long)sh.weight[j];
-#pragma unroll
-                for (int e = 0; e < kMine; ++e)
-                  if (o > (uint32_t)c[e]) before[e] += ow;
-              }
-              const float log_total = logf((float)s * kUnit);
-              for (int q = 0; q < a.draws; ++q) {
-                const long long at = sh.at[q];
-#pragma unroll
-                for (int e = 0; e < kMine; ++e)
-                  if (in[e] && at >= before[e] && at < before[e] + fw[e]) {
-                    a.tokens[(size_t)r * a.draws + q] = (int32_t)~(uint32_t)c[e];
-                    a.logprob[(size_t)r * a.draws + q] = run.scaled(unordered((uint32_t)(c[e] >> 32))) - log_total;
-                  }
-              }
-            }
-          }
+        if (tid < kMaxCluster * kSpWarps) sh.extra[tid] = 0ull;
+        const Found found{v.what == kGather, by_count, stage == 0 ? k : kMaxVocab, top_p, min_p, n, more, base, everything};
+        if (n <= kSmallList) {
+          if (tid < 32) settle<kBf16, kMode, true>(sh, run, found, a, r);
+        } else if (n <= kList) {
+          settle<kBf16, kMode, false>(sh, run, found, a, r);
         }
         __syncthreads();
         for (int b = tid; b < kBins; b += kSpThreads) sh.hist[b] = 0u;  // (it lies over the list)
         if (tid == 0) {
-          sh.listed = sh.count_all = sh.count_above = 0;
-          sh.sum_all = sh.sum_near = sh.sum_above = 0ull;
+          sh.listed = sh.count_all = 0;
+          sh.sum_all = 0;
         }
       } else {
         for (int b = tid; b < kBins; b += kSpThreads) sh.hist[b] = 0u;
@@ -845,25 +1065,36 @@ __global__ void __launch_bounds__(kSpThreads, 3) sampling_kernel(const SpArgs a)
     const float w = expf(run.scaled(x));
     return w < min_p ? 0.f : w;
   };
-  if (kMode == kSample || (kMode == kProbs && total < 0)) {
+  const bool summed = total >= 0;  // (and then, for draws, the runs' sums are known too)
+  if ((kMode == kSample || kMode == kProbs) && !summed) {
     Fixed f;
     run.each(kept.x, [&](float x, int id) { f.add(weight(x, id)); });
     int unused = 0;
     total = cluster_total(sh, turn, ranks, unused, f.value());
   }
   if constexpr (kMode == kSample) {
-    long long before = 0;  // of this warp's run
-    for (uint32_t p = 0; p < rank; ++p) before += (long long)ld_peer64(&sh.sum[turn ^ 1], p);
-    for (int w = 0; w < warp; ++w) before += sh.wsum[w];
-    const long long here = sh.wsum[warp];
-    const float log_total = logf((float)total * kUnit);
-    if (tid < a.draws) {
-      const float u = a.u[(size_t)r * a.draws + tid];
-      sh.at[tid] = min(u > 0.f ? (long long)floor((double)u * (double)total) : 0, total - 1);
+    // the kept weight of the runs before this warp's, and of its own
+    long long before = 0, here;
+    if (summed) {
+      long long v[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int one = 2 * lane + e;
+        v[e] = one < (int)ranks * kSpWarps
+                   ? (long long)ld_peer64(&sh.wabove[one % kSpWarps], one / kSpWarps) + (long long)ld_peer64(&sh.extra[one], 0)
+                   : 0;
+      }
+      const int own = (int)rank * kSpWarps + warp;
+      before = warp_sum((2 * lane < own ? v[0] : 0) + (2 * lane + 1 < own ? v[1] : 0));
+      here = __shfl_sync(0xffffffffu, own & 1 ? v[1] : v[0], own / 2);
+    } else {
+      for (uint32_t p = 0; p < rank; ++p) before += (long long)ld_peer64(&sh.sum[turn ^ 1], p);
+      for (int w = 0; w < warp; ++w) before += sh.wsum[w];
+      here = sh.wsum[warp];
     }
-    __syncthreads();
+    const float log_total = log_sum(total);
     for (int q = 0; q < a.draws; ++q) {
-      long long at = sh.at[q] - before;
+      long long at = place_of(sh.u[q], total) - before;
       if (at < 0 || at >= here) continue;
       for (int s = 0; s < run.steps; ++s) {
         Vec x;
