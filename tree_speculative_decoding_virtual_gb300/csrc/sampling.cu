@@ -31,6 +31,7 @@
 #include <cuda_bf16.h>
 
 #include <cmath>
+#include <mutex>
 #include <type_traits>
 
 #include "sm100_ptx.cuh"
@@ -45,8 +46,8 @@ constexpr int kMaxCluster = 8;
 constexpr int kMaxVocab = 262144;
 constexpr int kMaxDraws = 64;
 constexpr int kBins = 2048;
-constexpr int kThreadBins = kBins / kSpThreads;
-constexpr int kList = 512, kSmallList = 64;
+constexpr int kGroup = 32, kGroups = kBins / kGroup;  // bins are looked for by groups of 32 first
+constexpr int kList = 512, kSmallList = 32;
 constexpr float kCountScale = 32.f, kWideScale = 0.5f, kWeightScale = 64.f;  // bins a unit at first
 constexpr int kLevels = 3;          // times bins are cut again at most
 constexpr float kShare = 8192.f;    // a bin's own weight (262144 of them fit 32 bits)
@@ -106,7 +107,6 @@ struct SpShared {
   long long wsum[kSpWarps], wabove[kSpWarps];
   int wcount_above[kSpWarps];
   float scan[kSpWarps];
-  float need, room;
   float max;
   // this CTA's parts of what the first CTA adds up
   struct {
@@ -119,6 +119,7 @@ struct SpShared {
   float skipped;
   int count_all, count_above, listed;
   float u[kMaxDraws];
+  alignas(16) float2 groups[kGroups];  // weight, and number of logits
   // exchanged by the bitwise search and the draws (two places, by turn)
   int count[2];
   long long sum[2];
@@ -128,7 +129,6 @@ struct SpShared {
   int border_id;
   long long total;
   unsigned long long extra[kMaxCluster * kSpWarps];  // kept weight of the list, by warp run
-  float in_border, up_to;  // how many logits the bins hold
   int mine;
   bool failed;
 };
@@ -210,6 +210,12 @@ struct Fixed {
     lo += (int)(__float_as_uint(y.x) + __float_as_uint(y.y) - 0x6B800000u);
   }
   __device__ __forceinline__ long long value() const { return ((long long)hi << 23) + lo; }
+  // The sum over the warp's lanes.
+  __device__ __forceinline__ long long warp() const {
+    constexpr unsigned all = 0xffffffffu;
+    const long long h = ((long long)__reduce_add_sync(all, hi >> 8) << 8) + __reduce_add_sync(all, hi & 255u);
+    return (h << 23) + ((long long)__reduce_add_sync(all, lo >> 8) << 8) + __reduce_add_sync(all, lo & 255);
+  }
 };
 constexpr float kUnit = 0x1p-43f;
 
@@ -267,14 +273,22 @@ struct Run {
   // `from` or more.
   template <class F>
   __device__ __forceinline__ void each_vec(float from, F f) const {
-#pragma unroll 2
-    for (int s = 0; s < steps; ++s) {
-      SpVec<kBf16> v;
-      v.read(at + s * 32);
-      float most = fmaxf(v.x[0], v.x[1]);
+    constexpr int kAhead = 4;  // vectors read before the first is looked at
+#pragma unroll 1
+    for (int s0 = 0; s0 < steps; s0 += kAhead) {
+      uint4 raw[kAhead];
 #pragma unroll
-      for (int i = 2; i < kN; i += 2) most = sm100::fmax3(most, v.x[i], v.x[i + 1]);
-      if (most >= from) f(v.x, id + s * (32 * kN), most);
+      for (int j = 0; j < kAhead; ++j) raw[j] = at[min(s0 + j, steps - 1) * 32];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        if (s0 + j >= steps) break;
+        SpVec<kBf16> v;
+        v.read(&raw[j]);
+        float most = fmaxf(v.x[0], v.x[1]);
+#pragma unroll
+        for (int i = 2; i < kN; i += 2) most = sm100::fmax3(most, v.x[i], v.x[i + 1]);
+        if (most >= from) f(v.x, id + (s0 + j) * (32 * kN), most);
+      }
     }
   }
   // Calls f(logit, id) for every logit of `from` or more (and some others).
@@ -321,11 +335,10 @@ __device__ __forceinline__ long long block_total(SpShared &sh, int &count, long 
 }
 
 // This CTA's sums for the first CTA.
-__device__ __forceinline__ void block_parts(SpShared &sh, long long all, long long above, float skipped, int count,
-                                            int count_above) {
+__device__ __forceinline__ void block_parts(SpShared &sh, const Fixed &f_all, const Fixed &f_above, float skipped,
+                                            int count, int count_above) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  all = warp_sum(all);
-  above = warp_sum(above);
+  long long all = f_all.warp(), above = f_above.warp();
   skipped = warp_sum(skipped);
   count = __reduce_add_sync(0xffffffffu, count);
   count_above = __reduce_add_sync(0xffffffffu, count_above);
@@ -405,13 +418,13 @@ __device__ __forceinline__ long long block_scan(SpShared &sh, long long mine) {
   return before;
 }
 
-// Sorts a[0, size), size a power of two of at most twice the threads, in place (a
-// bitonic network; steps within 64 elements stay in a warp).  By the block, or its first warp.
-template <bool kDown, bool kWarp, class T>
+// Sorts a[0, size), size a power of two of at most twice the block's threads, in place (a
+// bitonic network; steps within 64 elements stay in a warp).  Starts and ends with a
+// barrier.
+template <bool kDown, class T>
 __device__ __forceinline__ void sort(T *a, int size) {
   const int t = threadIdx.x;
-  if (kWarp) __syncwarp();
-  else __syncthreads();
+  __syncthreads();
   for (int span = 2; span <= size; span *= 2)
     for (int stride = span / 2; stride; stride /= 2) {
       if (2 * t < size) {
@@ -424,10 +437,10 @@ __device__ __forceinline__ void sort(T *a, int size) {
         }
       }
       // (after a span of 64 the next step crosses warps)
-      if (!kWarp && (stride > 32 || (stride == 1 && span >= 64))) __syncthreads();
+      if (stride > 32 || (stride == 1 && span >= 64)) __syncthreads();
       else __syncwarp();
     }
-  if (!kWarp) __syncthreads();
+  __syncthreads();
 }
 
 // Where a draw falls: the first weight whose sum exceeds this is drawn.  The product of u
@@ -502,114 +515,137 @@ __device__ __noinline__ Border bitwise_border(SpShared &sh, const Run<kBf16> &ru
   return b;
 }
 
-// First CTA: the bins that hold the border, from the cluster's histograms.
-// Counts are added up from the bins' top until there are as many as wanted; so are weights,
-// but at first from their end, until there is more than may be left behind the border (the
-// exact sum less the share wanted: what is left is small, and known better by itself than as
-// a difference).
+// What each group of this CTA's bins holds; after a barrier behind the histogram.
+__device__ __forceinline__ void sum_groups(SpShared &sh, const Bins &bins, bool by_count) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const float width = 1.f / bins.scale;
+  const float own = by_count ? 1.f : expf(-(bins.from + (float)lane * width)) * (1.f / kShare);
+  static_assert(kGroups / kSpWarps == 8, "");
+  float n[8], w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t h = sh.hist[(warp * 8 + i) * kGroup + lane];
+    n[i] = (float)__reduce_add_sync(0xffffffffu, h);
+    w[i] = (float)h * own;
+  }
+  // eight sums over the lanes at once: lane l ends with that of group l / 4
+#pragma unroll
+  for (int off = 16, left = 4; left; off /= 2, left /= 2)
+#pragma unroll
+    for (int i = 0; i < left; ++i) {
+      const bool up = lane & off;
+      const float mine = up ? w[i + left] : w[i], theirs = up ? w[i] : w[i + left];
+      w[i] = mine + __shfl_xor_sync(0xffffffffu, theirs, off);
+    }
+  w[0] += __shfl_xor_sync(0xffffffffu, w[0], 2);
+  w[0] += __shfl_xor_sync(0xffffffffu, w[0], 1);
+  float mine = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i == lane / 4) mine = n[i];
+  const int g = warp * 8 + lane / 4;
+  // (from shares at most 2% too many)
+  if (lane % 4 == 0)
+    sh.groups[g] = by_count ? make_float2(mine, mine) : make_float2(w[0] * expf(-(float)(g * kGroup) * width), mine * (1.02f / kShare));
+}
+
+// First CTA, first warp: the bins that hold the border, from the cluster's histograms:
+// the groups that must, then the bins of two groups.  Counts are added up from the bins'
+// top until there are as many as wanted; so are weights, but at first from their end, until
+// there is more than may be left behind the border (the exact sum less the share wanted:
+// what is left is small, and known better by itself than as a difference).
 __device__ __forceinline__ void find_bins(SpShared &sh, const Bins bins, bool by_count, int k, float top_p,
                                           uint32_t ranks, int level, int V) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  static_assert(kThreadBins == 8, "");
+  const int lane = threadIdx.x;
   const bool from_end = !by_count && level == 0;
+  static_assert(kGroups == 64, "two a lane");
   Parts parts;
-  if (warp == 0) parts.load(sh, ranks);
-  uint32_t h[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+  parts.load(sh, ranks);
+  // (loads before their uses: one takes some 700 cycles)
+  uint4 x[kMaxCluster];
 #pragma unroll
-  for (uint32_t p0 = 0; p0 < kMaxCluster; p0 += 4) {  // (loads before their uses: one takes some 700 cycles)
-    uint4 x[4][2];
+  for (uint32_t p = 0; p < kMaxCluster; ++p)
+    x[p] = p < ranks ? ld_peer128(&sh.groups[2 * lane], p) : make_uint4(0u, 0u, 0u, 0u);
+  float w[2] = {0.f, 0.f}, n[2] = {0.f, 0.f};
 #pragma unroll
-    for (uint32_t p = 0; p < 4; ++p)
-#pragma unroll
-      for (int q = 0; q < 2; ++q)
-        x[p][q] = p0 + p < ranks ? ld_peer128(&sh.hist[tid * 8 + q * 4], p0 + p) : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-    for (uint32_t p = 0; p < 4; ++p)
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        h[q * 4] += x[p][q].x;
-        h[q * 4 + 1] += x[p][q].y;
-        h[q * 4 + 2] += x[p][q].z;
-        h[q * 4 + 3] += x[p][q].w;
-      }
+  for (uint32_t p = 0; p < kMaxCluster; ++p) {
+    w[0] += __uint_as_float(x[p].x);
+    n[0] += __uint_as_float(x[p].y);
+    w[1] += __uint_as_float(x[p].z);
+    n[1] += __uint_as_float(x[p].w);
   }
-  if (warp == 0) parts.sum(sh);
-  if (tid == 0) {
-    const double all = (double)sh.sum_all, want = max((double)top_p * all, 1.0);
-    sh.need = by_count ? (float)(k - sh.count_above) : (float)((want - (double)sh.sum_above) * (double)kUnit);
-    sh.room = (float)((all - want) * (double)kUnit);
-    sh.verdict.lo = sh.verdict.hi = kBins;
-    sh.in_border = sh.up_to = 0.f;
-  }
-  float v[8], mine = 0.f;
-  const float width = 1.f / bins.scale, step = expf(-width);
-  float own = by_count ? 1.f : expf(-(bins.from + (float)(tid * 8) * width)) * (1.f / kShare);  // a bin's weight
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    v[i] = (float)h[i] * own;
-    if (!by_count) own *= step;
-    mine += v[i];
-  }
-  float upto = mine;  // from the end when that is what counts
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const float y = from_end ? __shfl_down_sync(0xffffffffu, upto, off) : __shfl_up_sync(0xffffffffu, upto, off);
-    if (from_end ? lane + off < 32 : lane >= off) upto += y;
-  }
-  if (lane == (from_end ? 0 : 31)) sh.scan[warp] = upto;
-  __syncthreads();
-  float sum = upto - mine;
-  if (from_end) sum += sh.skipped;
-#pragma unroll
-  for (int w = 0; w < kSpWarps; ++w)
-    if (from_end ? w > warp : w < warp) sum += sh.scan[w];
-  const float need = sh.need, room = sh.room;
+  parts.sum(sh);
+  __syncwarp();
+  const double all = (double)sh.sum_all, want = max((double)top_p * all, 1.0);
+  const float need = by_count ? (float)(k - sh.count_above) : (float)((want - (double)sh.sum_above) * (double)kUnit);
+  const float room = (float)((all - want) * (double)kUnit), skipped = sh.skipped;
   const float e = by_count ? 0.f : kShareError, beyond = (float)V * 1.3e-14f;
-  int lo = kBins, hi = kBins;
+  // whether the border may, and must, lie at or before a bin (or group), by the sum up to it
+  // or, from the end, of what lies behind it
+  auto may = [&](float sum) { return from_end ? sum * (1.f - e) <= room : sum * (1.f + e) >= need; };
+  auto must = [&](float sum) { return from_end ? sum * (1.f + e) + beyond <= room : sum * (1.f - e) >= need; };
+  // sums over the lanes before this one, or after it
+  auto scan = [&](float v) -> float {
+    float upto = v;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int j = from_end ? 7 - i : i;
-    if (!from_end) sum += v[j];
-    // from the end, `sum` is what bins after j hold
-    const bool may = from_end ? sum * (1.f - e) <= room : sum * (1.f + e) >= need;
-    const bool must = from_end ? sum * (1.f + e) + beyond <= room : sum * (1.f - e) >= need;
-    if (from_end) sum += v[j];
-    if (may) lo = min(lo, tid * 8 + j);
-    if (must) hi = min(hi, tid * 8 + j);
-  }
-  lo = __reduce_min_sync(0xffffffffu, lo);
-  hi = __reduce_min_sync(0xffffffffu, hi);
-  if (lane == 0) {
-    atomicMin(&sh.verdict.lo, lo);
-    atomicMin(&sh.verdict.hi, hi);
-  }
-  __syncthreads();
-  lo = sh.verdict.lo;
-  hi = min(sh.verdict.hi, kBins - 1);
-  float in = 0.f, up = 0.f;  // how many logits; from shares at most 2% too many
+    for (int off = 1; off < 32; off <<= 1) {
+      const float y = from_end ? __shfl_down_sync(0xffffffffu, upto, off) : __shfl_up_sync(0xffffffffu, upto, off);
+      if (from_end ? lane + off < 32 : lane >= off) upto += y;
+    }
+    return upto - v;
+  };
+  auto first = [&](bool a, bool b) -> int {  // place 2 lane (+ 1) of the first true
+    return (int)__reduce_min_sync(0xffffffffu, (unsigned)(a ? 2 * lane : b ? 2 * lane + 1 : 64));
+  };
+  const float out = scan(w[0] + w[1]) + (from_end ? skipped : 0.f);
+  const float s0 = from_end ? out + w[1] : out + w[0], s1 = from_end ? out : out + w[0] + w[1];
+  const int glo = first(may(s0), may(s1)), ghi = min(first(must(s0), must(s1)), kGroups - 1);
+  int lo = kBins, hi = kBins - 1;
+  float in_border = 0.f, up_to = 0.f;
+  if (glo < kGroups) {
+    const int g0 = min(glo, kGroups - 2);  // the two groups that are looked at
+    uint32_t h[2] = {0u, 0u};
+    unsigned long long y[kMaxCluster];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int b = tid * 8 + i;
-    const float n = by_count ? (float)h[i] : (float)h[i] * (1.02f / kShare);
-    if (b >= lo && b <= hi) in += n;
-    if (b <= hi) up += n;
+    for (uint32_t p = 0; p < kMaxCluster; ++p)
+      y[p] = p < ranks ? ld_peer64(&sh.hist[g0 * kGroup + 2 * lane], p) : 0ull;
+#pragma unroll
+    for (uint32_t p = 0; p < kMaxCluster; ++p) {
+      h[0] += (uint32_t)y[p];
+      h[1] += (uint32_t)(y[p] >> 32);
+    }
+    const float width = 1.f / bins.scale, at = bins.from + (float)(g0 * kGroup + 2 * lane) * width;
+    const float own = by_count ? 1.f : expf(-at) * (1.f / kShare);
+    const float f0 = (float)h[0] * own, f1 = (float)h[1] * (by_count ? 1.f : own * expf(-width));
+    // what lies outside the two groups, on the side that is added up from
+    const float outside = warp_sum((from_end ? 2 * lane > g0 + 1 : 2 * lane < g0) ? w[0] : 0.f) +
+                          warp_sum((from_end ? 2 * lane + 1 > g0 + 1 : 2 * lane + 1 < g0) ? w[1] : 0.f) +
+                          (from_end ? skipped : 0.f);
+    const float in = scan(f0 + f1) + outside;
+    const float t0 = from_end ? in + f1 : in + f0, t1 = from_end ? in : in + f0 + f1;
+    const int flo = first(may(t0), may(t1)), fhi = first(must(t0), must(t1));
+    lo = g0 * kGroup + min(flo, 63);
+    const float share = by_count ? 1.f : 1.02f / kShare;
+    const float before = warp_sum((2 * lane < g0 ? n[0] : 0.f) + (2 * lane + 1 < g0 ? n[1] : 0.f));
+    if (fhi < 64) {
+      hi = g0 * kGroup + fhi;
+      in_border = warp_sum((2 * lane >= flo && 2 * lane <= fhi ? (float)h[0] : 0.f) +
+                           (2 * lane + 1 >= flo && 2 * lane + 1 <= fhi ? (float)h[1] : 0.f)) * share;
+      up_to = before + warp_sum((2 * lane <= fhi ? (float)h[0] : 0.f) + (2 * lane + 1 <= fhi ? (float)h[1] : 0.f)) * share;
+    } else {
+      hi = (ghi + 1) * kGroup - 1;
+      up_to = warp_sum((2 * lane <= ghi ? n[0] : 0.f) + (2 * lane + 1 <= ghi ? n[1] : 0.f));
+      in_border = up_to - before;
+    }
   }
-  in = warp_sum(in);
-  up = warp_sum(up);
   if (lane == 0) {
-    if (in > 0.f) atomicAdd(&sh.in_border, in);
-    if (up > 0.f) atomicAdd(&sh.up_to, up);
-  }
-  __syncthreads();
-  if (tid == 0) {
-    sh.verdict.hi = hi;
     const int what = by_count && sh.count_all <= k            ? kNone
                      : lo == kBins                            ? (by_count && bins.scale == kCountScale ? kWiden : kBitwise)
-                     : level == 0 && sh.up_to <= (float)kList ? kGather
-                     : sh.in_border <= (float)kList           ? kCollect
+                     : level == 0 && up_to <= (float)kList    ? kGather
+                     : in_border <= (float)kList              ? kCollect
                      : level < kLevels                        ? kZoom
                                                               : kBitwise;
-    sh.verdict.what = what;
+    sh.verdict = Verdict{what, lo, hi};
     if (what == kNone || what == kBitwise) {
       sh.sum_all = 0;
       sh.count_all = 0;
@@ -628,40 +664,16 @@ struct Found {
 };
 
 // The first CTA's end of it: ranks the list, finds the border, and where everything
-// is in the list the sum of what is kept and the draws.  By the whole block, or for
-// short lists by its first warp, which needs no barriers.
-template <bool kBf16, int kMode, bool kWarp>
+// is in the list the sum of what is kept and the draws.  By the whole block.
+template <bool kBf16, int kMode>
 __device__ __forceinline__ void settle(SpShared &sh, const Run<kBf16> &run, const Found &f, const SpArgs &a, int r) {
   const int tid = threadIdx.x;
-  constexpr int kScope = kWarp ? 32 : kSpThreads;
-  auto total = [&](int &count, long long mine) -> long long {
-    if constexpr (kWarp) {
-      count = __reduce_add_sync(0xffffffffu, count);
-      return warp_sum(mine);
-    } else {
-      return block_total(sh, count, mine);
-    }
-  };
-  auto scan = [&](long long mine) -> long long {
-    if constexpr (!kWarp) return block_scan(sh, mine);
-    long long upto = mine;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const long long o = __shfl_up_sync(0xffffffffu, upto, off);
-      if (tid >= off) upto += o;
-    }
-    return upto - mine;
-  };
-  auto fence = [&]() {
-    if constexpr (kWarp) __syncwarp();
-    else __syncthreads();
-  };
   // ranked; thread t then holds the ranks 2 t and 2 t + 1
   const int n = f.n;
   int size = 2;
   while (size < n) size *= 2;
-  for (int i = n + tid; i < size; i += kScope) sh.list[i] = 0ull;
-  sort<true, kWarp>(sh.list, size);
+  for (int i = n + tid; i < size; i += kSpThreads) sh.list[i] = 0ull;
+  sort<true>(sh.list, size);
   const bool weigh = f.gathered || !f.by_count;
   float x[2], w[2] = {0.f, 0.f};
   int id[2];
@@ -676,7 +688,7 @@ __device__ __forceinline__ void settle(SpShared &sh, const Run<kBf16> &run, cons
     if (in[e] && weigh) w[e] = expf(run.scaled(x[e]));
     fw[e] = fixed(w[e]);
   }
-  before[0] = scan(fw[0] + fw[1]);
+  before[0] = block_scan(sh, fw[0] + fw[1]);
   before[1] = before[0] + fw[0];
   int here = 0;
   if (f.gathered) {
@@ -684,7 +696,7 @@ __device__ __forceinline__ void settle(SpShared &sh, const Run<kBf16> &run, cons
 #pragma unroll
     for (int e = 0; e < 2; ++e) in[e] = in[e] && 2 * tid + e < f.k;
     if (f.top_p < 1.f) {
-      const long long left = f.by_count ? total(here, (in[0] ? fw[0] : 0) + (in[1] ? fw[1] : 0)) : f.everything;
+      const long long left = f.by_count ? block_total(sh, here, (in[0] ? fw[0] : 0) + (in[1] ? fw[1] : 0)) : f.everything;
       const long long want = (long long)ceil((double)f.top_p * (double)left);
 #pragma unroll
       for (int e = 0; e < 2; ++e) in[e] = in[e] && (2 * tid + e == 0 || before[e] < want);
@@ -698,7 +710,7 @@ __device__ __forceinline__ void settle(SpShared &sh, const Run<kBf16> &run, cons
   }
   // the border is the last that is kept; then min-p, which the weight alone decides
   here = in[0] + in[1];
-  total(here, 0);
+  block_total(sh, here, 0);
   if (here == 0) sh.failed = true;
   int left = 0;
 #pragma unroll
@@ -710,7 +722,7 @@ __device__ __forceinline__ void settle(SpShared &sh, const Run<kBf16> &run, cons
     if (f.gathered) in[e] = in[e] && !(w[e] < f.min_p);
     left += in[e];
   }
-  const long long s = total(left, (in[0] ? fw[0] : 0) + (in[1] ? fw[1] : 0));
+  const long long s = block_total(sh, left, (in[0] ? fw[0] : 0) + (in[1] ? fw[1] : 0));
   if (tid == 0) sh.total = f.gathered ? s : f.by_count || f.min_p > 0.f ? -1 : f.base + s;
   if constexpr (kMode == kSample) {
     if (!f.gathered) {
@@ -723,7 +735,7 @@ __device__ __forceinline__ void settle(SpShared &sh, const Run<kBf16> &run, cons
     static_assert(kMaxVocab * kList <= (1 << 27), "id and rank in a word");
     uint32_t *by_id = reinterpret_cast<uint32_t *>(sh.list);
     float *logit = reinterpret_cast<float *>(by_id + kList);
-    fence();  // (the list was read)
+    __syncthreads();  // (the list was read)
     size = 2;
     while (size < left) size *= 2;
 #pragma unroll
@@ -733,7 +745,7 @@ __device__ __forceinline__ void settle(SpShared &sh, const Run<kBf16> &run, cons
       logit[i] = x[e];
       sh.weight[i] = (unsigned long long)fw[e];
     }
-    sort<false, kWarp>(by_id, size);
+    sort<false>(by_id, size);
     int rank_of[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
@@ -742,7 +754,7 @@ __device__ __forceinline__ void settle(SpShared &sh, const Run<kBf16> &run, cons
       id[e] = (int)(one / kList);
       fw[e] = one != 0xFFFFFFFFu ? (long long)sh.weight[rank_of[e]] : 0;
     }
-    before[0] = scan(fw[0] + fw[1]);
+    before[0] = block_scan(sh, fw[0] + fw[1]);
     before[1] = before[0] + fw[0];
     const float log_total = log_sum(s);
     for (int q = 0; q < a.draws; ++q) {
@@ -753,6 +765,69 @@ __device__ __forceinline__ void settle(SpShared &sh, const Run<kBf16> &run, cons
           a.tokens[(size_t)r * a.draws + q] = id[e];
           a.logprob[(size_t)r * a.draws + q] = run.scaled(logit[rank_of[e]]) - log_total;
         }
+    }
+  }
+}
+
+// The same for at most 32 logits, by the first warp: a lane each, all compared with all.
+template <bool kBf16, int kMode>
+__device__ __forceinline__ void settle_few(SpShared &sh, const Run<kBf16> &run, const Found &f, const SpArgs &a, int r) {
+  const int lane = threadIdx.x, n = f.n;
+  const unsigned long long c = lane < n ? sh.list[lane] : 0ull;
+  const float x = unordered((uint32_t)(c >> 32));
+  const int id = (int)~(uint32_t)c;
+  const float w = lane < n ? expf(run.scaled(x)) : 0.f;
+  const long long fw = fixed(w);
+  auto shuffle = [](unsigned long long v, int from) { return __shfl_sync(0xffffffffu, v, from); };
+  int place = 0;
+  long long before = 0;
+  for (int j = 0; j < n; ++j) {
+    const unsigned long long o = shuffle(c, j);
+    const long long ow = (long long)shuffle((unsigned long long)fw, j);
+    if (o > c) {
+      ++place;
+      before += ow;
+    }
+  }
+  bool in = lane < n;
+  if (f.gathered) {
+    in = in && place < f.k;
+    if (f.top_p < 1.f) {
+      const long long left = f.by_count ? warp_sum(in ? fw : 0ll) : f.everything;
+      in = in && (place == 0 || before < (long long)ceil((double)f.top_p * (double)left));
+    }
+  } else {
+    const long long want = f.by_count ? 0 : (long long)ceil((double)f.top_p * (double)f.everything);
+    if (!f.by_count && f.base >= want) sh.failed = true;
+    in = in && (f.by_count ? f.more + place < f.k : f.base + before < want);
+  }
+  const int here = __popc(__ballot_sync(0xffffffffu, in));
+  if (here == 0) sh.failed = true;
+  if (in && place == here - 1) {
+    sh.border_x = x;
+    sh.border_id = id;
+  }
+  if (f.gathered) in = in && !(w < f.min_p);
+  const long long s = warp_sum(in ? fw : 0ll);
+  if (lane == 0) sh.total = f.gathered ? s : f.by_count || f.min_p > 0.f ? -1 : f.base + s;
+  if constexpr (kMode == kSample) {
+    if (!f.gathered) {
+      if (in && fw && !f.by_count) atomicAdd(&sh.extra[id / a.per_warp], (unsigned long long)fw);
+      return;
+    }
+    before = 0;
+    for (int j = 0; j < n; ++j) {
+      const int o = __shfl_sync(0xffffffffu, in ? id : kMaxVocab, j);
+      const long long ow = (long long)shuffle((unsigned long long)fw, j);
+      if (o < id) before += ow;
+    }
+    const float log_total = log_sum(s);
+    for (int q = 0; q < a.draws; ++q) {
+      const long long at = place_of(sh.u[q], s);
+      if (in && at >= before && at < before + fw) {
+        a.tokens[(size_t)r * a.draws + q] = id;
+        a.logprob[(size_t)r * a.draws + q] = run.scaled(x) - log_total;
+      }
     }
   }
 }
@@ -768,38 +843,20 @@ __global__ void __launch_bounds__(kSpThreads, 3) sampling_kernel(const SpArgs a)
   pdl_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_ctarank(), ranks = cluster_nctarank();
-  const int r = blockIdx.x / ranks;
-  const int64_t row = a.rows ? a.rows[r] : r;
-  const int V = a.V;
-  if (row < 0 || row >= a.num_rows) {  // (the same for the whole cluster)
-    if (row != -1 && rank == 0 && tid == 0 && a.status) atomicOr(a.status, TSD_STATUS_BAD_PATH);
-    if (kMode == kSample && rank == 0)
-      for (int i = tid; i < a.draws; i += kSpThreads) {
-        a.tokens[(size_t)r * a.draws + i] = -1;
-        a.logprob[(size_t)r * a.draws + i] = 0.f;
-      }
-    return;
-  }
-  const int pr = r / a.per_param;
-  const float T = a.temperature ? a.temperature[pr] : 1.f;
-  const bool greedy = !(T >= 1.1754944e-38f);
-  int k = a.top_k ? a.top_k[pr] : 0;
-  if (k <= 0 || k > V) k = V;
-  if (greedy) k = 1;
-  const float top_p = a.top_p ? a.top_p[pr] : 1.f;
-  const float min_p = a.min_p ? fminf(a.min_p[pr], 1.f) : 0.f;
-
-  // ---- the run of this warp, -inf past the row's end; a lane reads what it wrote itself ----
+  const int V = a.V, clusters = gridDim.x / ranks;
+  // The run of this warp, -inf past the row's end.  A lane reads nothing but what it copied
+  // itself, so the next row's copies start as soon as a lane is through with this one's.
   const int id0 = ((int)rank * kSpWarps + warp) * a.per_warp;
   uint4 *mine = smem + (size_t)warp * (a.per_warp / kN) + lane;
   Run<kBf16> run;
   run.at = mine;
   run.steps = a.per_warp / kStep;
   run.id = id0 + lane * kN;
-  run.inv_t = greedy ? 1.f : __fdiv_rn(1.f, T);
   run.rank = rank;
   run.ranks = ranks;
-  {
+  auto fetch = [&](int r) {
+    const int64_t row = r >= a.R ? -1 : a.rows ? a.rows[r] : r;
+    if (row < 0 || row >= a.num_rows) return;
     using Raw = typename std::conditional<kBf16, uint16_t, uint32_t>::type;
     const Raw *src = reinterpret_cast<const Raw *>(a.logits) + row * V;
     const bool vec = (reinterpret_cast<uintptr_t>(src) & 15) == 0;
@@ -818,15 +875,40 @@ __global__ void __launch_bounds__(kSpThreads, 3) sampling_kernel(const SpArgs a)
           mine[s * 32] = make_uint4(e[0], e[1], e[2], e[3]);
       }
     }
-    for (int b = tid; b < kBins; b += kSpThreads) sh.hist[b] = 0u;
-    if (kMode == kSample && tid < a.draws) sh.u[tid] = a.u[(size_t)r * a.draws + tid];
-    if (tid == 0) {
-      sh.sum_all = 0;
-      sh.count_all = sh.listed = sh.mine = 0;
-      sh.failed = false;
-    }
-    cp_async_wait_all();
+  };
+  const int first_row = blockIdx.x / ranks;
+  fetch(first_row);
+  for (int b = tid; b < kBins; b += kSpThreads) sh.hist[b] = 0u;
+#pragma unroll 1
+  for (int r = first_row; r < a.R; r += clusters) {
+  const int64_t row = a.rows ? a.rows[r] : r;
+  if (row < 0 || row >= a.num_rows) {  // (the same for the whole cluster)
+    if (row != -1 && rank == 0 && tid == 0 && a.status) atomicOr(a.status, TSD_STATUS_BAD_PATH);
+    if (kMode == kSample && rank == 0)
+      for (int i = tid; i < a.draws; i += kSpThreads) {
+        a.tokens[(size_t)r * a.draws + i] = -1;
+        a.logprob[(size_t)r * a.draws + i] = 0.f;
+      }
+    fetch(r + clusters);
+    continue;
   }
+  const int pr = r / a.per_param;
+  const float T = a.temperature ? a.temperature[pr] : 1.f;
+  const bool greedy = !(T >= 1.1754944e-38f);
+  int k = a.top_k ? a.top_k[pr] : 0;
+  if (k <= 0 || k > V) k = V;
+  if (greedy) k = 1;
+  const float top_p = a.top_p ? a.top_p[pr] : 1.f;
+  const float min_p = a.min_p ? fminf(a.min_p[pr], 1.f) : 0.f;
+  run.inv_t = greedy ? 1.f : __fdiv_rn(1.f, T);
+  __syncthreads();  // (the row before is done with)
+  if (kMode == kSample && tid < a.draws) sh.u[tid] = a.u[(size_t)r * a.draws + tid];
+  if (tid == 0) {
+    sh.sum_all = 0;
+    sh.count_all = sh.listed = sh.mine = 0;
+    sh.failed = false;
+  }
+  cp_async_wait_all();
   float m = -INFINITY;
   for (int s = 0; s < run.steps; ++s) {
     Vec x;
@@ -843,8 +925,10 @@ __global__ void __launch_bounds__(kSpThreads, 3) sampling_kernel(const SpArgs a)
     sh.max = m;
   }
   cluster_sync();
-  m = -INFINITY;
-  for (uint32_t p = 0; p < ranks; ++p) m = max_nan(m, __uint_as_float(ld_peer32(&sh.max, p)));
+  m = lane < (int)ranks ? __uint_as_float(ld_peer32(&sh.max, lane)) : -INFINITY;
+#pragma unroll
+  for (int off = kMaxCluster / 2; off; off >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, off));
+  m = __shfl_sync(0xffffffffu, m, 0);
   run.m = m;
 
   const bool bad = !(m < INFINITY), empty = m == -INFINITY;
@@ -860,13 +944,15 @@ __global__ void __launch_bounds__(kSpThreads, 3) sampling_kernel(const SpArgs a)
       const float x = bad ? NAN : kMode == kProbs ? 0.f : -INFINITY;
       for (int i = id0 + lane; i < min(V, id0 + a.per_warp); i += 32) a.out[(size_t)r * V + i] = x;
     }
-    cluster_sync();  // (no CTA leaves while another reads its shared memory)
-    return;
+    fetch(r + clusters);
+    cluster_sync();  // (no CTA goes on while another reads its shared memory)
+    continue;
   }
 
   int turn = 0;
   Border kept;
   long long total = -1;  // weight of what is kept, once known
+  bool through = false;  // the first CTA has all it needs for the draws
 
   // ---- the filters' borders ----
 #pragma unroll 1
@@ -946,11 +1032,17 @@ __global__ void __launch_bounds__(kSpThreads, 3) sampling_kernel(const SpArgs a)
           });
         }
       }
-      block_parts(sh, again ? 0 : all.value(), over.value(), skipped, again ? 0 : count, count_over);
+      if (again) {
+        all = Fixed();
+        count = 0;
+      }
+      block_parts(sh, all, over, skipped, count, count_over);
       again = true;
+      sum_groups(sh, bins, by_count);
       cluster_sync();
       if (rank == 0) {
-        find_bins(sh, bins, by_count, k, top_p, ranks, level, V);
+        if (warp == 0) find_bins(sh, bins, by_count, k, top_p, ranks, level, V);
+        __syncthreads();
         // (before the others put their lists there)
         for (int b = tid; b < kBins; b += kSpThreads) sh.hist[b] = 0u;
       }
@@ -989,16 +1081,19 @@ __global__ void __launch_bounds__(kSpThreads, 3) sampling_kernel(const SpArgs a)
           const float d = by_count ? __fsub_rn(x[i], m) : run.scaled(x[i]);
           float y;
           const int b = bin_of(-d, bins, y);
-          w[i] = in && b < lo ? expf(d) : 0.f;
+          w[i] = by_count ? 0.f : expf(d);
+          w[i] = in && b < lo ? w[i] : 0.f;
           count += in && b < lo;
-          if (in && b >= lo && b <= v.hi) list(x[i], first + i);
+          if (in && (unsigned)(b - lo) <= (unsigned)(v.hi - lo)) list(x[i], first + i);
         }
         if (!by_count && v.what == kCollect) {
 #pragma unroll
           for (int i = 0; i < kN; i += 2) over.add2(w[i], w[i + 1]);
         }
       });
-      block_parts(sh, 0, over.value(), 0.f, 0, count);
+      through = kMode == kSample && v.what == kGather;
+      if (through) fetch(r + clusters);
+      block_parts(sh, Fixed(), over, 0.f, 0, count);
       __syncthreads();
       if (rank != 0) {
         const int n = sh.mine;
@@ -1032,9 +1127,9 @@ __global__ void __launch_bounds__(kSpThreads, 3) sampling_kernel(const SpArgs a)
         if (tid < kMaxCluster * kSpWarps) sh.extra[tid] = 0ull;
         const Found found{v.what == kGather, by_count, stage == 0 ? k : kMaxVocab, top_p, min_p, n, more, base, everything};
         if (n <= kSmallList) {
-          if (tid < 32) settle<kBf16, kMode, true>(sh, run, found, a, r);
+          if (warp == 0) settle_few<kBf16, kMode>(sh, run, found, a, r);
         } else if (n <= kList) {
-          settle<kBf16, kMode, false>(sh, run, found, a, r);
+          settle<kBf16, kMode>(sh, run, found, a, r);
         }
         __syncthreads();
         for (int b = tid; b < kBins; b += kSpThreads) sh.hist[b] = 0u;  // (it lies over the list)
@@ -1045,7 +1140,7 @@ __global__ void __launch_bounds__(kSpThreads, 3) sampling_kernel(const SpArgs a)
       } else {
         for (int b = tid; b < kBins; b += kSpThreads) sh.hist[b] = 0u;
       }
-      if (kMode == kSample && v.what == kGather) return;  // (nothing of this CTA is read any more)
+      if (through) break;  // (nothing of this CTA is read any more)
       cluster_sync();
       if (ld_peer32(&sh.failed, 0) & 0xFFu) v.what = kBitwise;
       kept.x = __uint_as_float(ld_peer32(&sh.border_x, 0));
@@ -1058,6 +1153,7 @@ __global__ void __launch_bounds__(kSpThreads, 3) sampling_kernel(const SpArgs a)
     }
     if (v.what == kGather) break;
   }
+  if (through) continue;
 
   // ---- what is kept ----
   auto weight = [&](float x, int id) -> float {  // 0: not kept
@@ -1093,48 +1189,69 @@ __global__ void __launch_bounds__(kSpThreads, 3) sampling_kernel(const SpArgs a)
       here = sh.wsum[warp];
     }
     const float log_total = log_sum(total);
-    for (int q = 0; q < a.draws; ++q) {
-      long long at = place_of(sh.u[q], total) - before;
-      if (at < 0 || at >= here) continue;
-      for (int s = 0; s < run.steps; ++s) {
-        Vec x;
-        x.read(run.at + s * 32);
-        float w[kN];
-        long long sum = 0;
+    // one pass over the run, as long as a draw falls into what is left of it; lane q holds
+    // where draws q and q + 32 fall
+    static_assert(kMaxDraws == 64, "two draws a lane");
+    long long at[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      at[e] = lane + 32 * e < a.draws ? place_of(sh.u[lane + 32 * e], total) - before : -1;
+    constexpr int kAhead = 16 / kN;
+    for (int s0 = 0; s0 < run.steps; s0 += kAhead) {
+      if (!__any_sync(0xffffffffu, (at[0] >= 0 && at[0] < here) || (at[1] >= 0 && at[1] < here))) break;
+      float x[kAhead][kN], w[kAhead][kN];
+      Fixed f[kAhead];
+      long long all[kAhead];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        Vec v;
+        v.read(run.at + min(s0 + j, run.steps - 1) * 32);
 #pragma unroll
         for (int i = 0; i < kN; ++i) {
-          w[i] = weight(x.x[i], run.id + s * kStep + i);
-          sum += fixed(w[i]);
+          x[j][i] = v.x[i];
+          const float one = expf(run.scaled(v.x[i]));
+          w[j][i] = kept.has(v.x[i], run.id + (s0 + j) * kStep + i) && !(one < min_p) && s0 + j < run.steps ? one : 0.f;
         }
-        long long upto = sum;
 #pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-          const long long o = __shfl_up_sync(0xffffffffu, upto, off);
-          if (lane >= off) upto += o;
-        }
-        const long long all = __shfl_sync(0xffffffffu, upto, 31);
-        if (at < all) {
-          long long left = at - (upto - sum);
-          if (left >= 0 && left < sum) {
-            int i = 0;
-            float d = 0.f;
+        for (int i = 0; i < kN; i += 2) f[j].add2(w[j][i], w[j][i + 1]);
+      }
 #pragma unroll
-            for (int j = 0; j < kN; ++j) {
-              const long long one = fixed(w[j]);
-              if (i == j) {
-                d = run.scaled(x.x[j]);
-                if (left >= one && j + 1 < kN) {
-                  left -= one;
-                  ++i;
+      for (int j = 0; j < kAhead; ++j) all[j] = f[j].warp();
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          for (unsigned hits = __ballot_sync(0xffffffffu, at[e] >= 0 && at[e] < all[j]); hits; hits &= hits - 1) {
+            const int q = __ffs(hits) - 1;
+            const long long sum = f[j].value();
+            long long upto = sum;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+              const long long o = __shfl_up_sync(0xffffffffu, upto, off);
+              if (lane >= off) upto += o;
+            }
+            long long left = __shfl_sync(0xffffffffu, at[e], q) - (upto - sum);
+            if (left >= 0 && left < sum) {
+              int i = 0;
+              float d = 0.f;
+#pragma unroll
+              for (int c = 0; c < kN; ++c) {
+                const long long one = fixed(w[j][c]);
+                if (i == c) {
+                  d = run.scaled(x[j][c]);
+                  if (left >= one && c + 1 < kN) {
+                    left -= one;
+                    ++i;
+                  }
                 }
               }
+              a.tokens[(size_t)r * a.draws + q + 32 * e] = run.id + (s0 + j) * kStep + i;
+              a.logprob[(size_t)r * a.draws + q + 32 * e] = d - log_total;
             }
-            a.tokens[(size_t)r * a.draws + q] = run.id + s * kStep + i;
-            a.logprob[(size_t)r * a.draws + q] = d - log_total;
           }
-          break;
-        }
-        at -= all;
+        at[0] -= all[j];
+        at[1] -= all[j];
+        here -= all[j];
       }
     }
   } else {
@@ -1168,7 +1285,33 @@ __global__ void __launch_bounds__(kSpThreads, 3) sampling_kernel(const SpArgs a)
       }
     }
   }
+  fetch(r + clusters);
   cluster_sync();
+  }
+}
+
+// How many clusters of this launch fit the device (asked once for each shape).
+int clusters_at_once(const void *kernel, const cudaLaunchConfig_t &cfg) {
+  struct Entry {
+    const void *fn;
+    int dev, cluster;
+    size_t smem;
+    int n;
+  };
+  static std::mutex mu;
+  static Entry known[64];
+  static int used = 0;
+  const int cluster = (int)cfg.gridDim.x;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 1;
+  std::lock_guard<std::mutex> lock(mu);
+  for (int i = 0; i < used; ++i)
+    if (known[i].fn == kernel && known[i].dev == dev && known[i].cluster == cluster && known[i].smem == cfg.dynamicSmemBytes)
+      return known[i].n;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) n = sm_count() / cluster + 1;
+  if (used < 64) known[used++] = Entry{kernel, dev, cluster, cfg.dynamicSmemBytes, n};
+  return n;
 }
 
 template <bool kBf16, int kMode>
@@ -1181,18 +1324,22 @@ cudaError_t sp_launch(SpArgs &a, cudaStream_t s) {
   if (!set_smem((const void *)sampling_kernel<kBf16, kMode>, kMaxVocab / kMaxCluster * (kBf16 ? 2 : 4)))
     return cudaErrorUnknown;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)a.R * c);
   cfg.blockDim = dim3(kSpThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = c;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = c;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
+  cfg.gridDim = dim3((unsigned)c);
+  cfg.numAttrs = 1;
+  // as many clusters as run at once; each takes row after row
+  const int most = clusters_at_once((const void *)sampling_kernel<kBf16, kMode>, cfg);
+  cfg.gridDim = dim3((unsigned)(a.R < most ? a.R : most) * c);
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, sampling_kernel<kBf16, kMode>, a);
 }
