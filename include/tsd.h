@@ -755,7 +755,7 @@ int tsd_tree_path_logprobs(const void *logits, int bf16, const int32_t *tokens, 
  * sequence's keys does not matter, NaN included; a row that sees a tree node whose V has
  * a NaN or an infinity gets NaN, the rows that do not see it are as without it.
  * P is rounded to bf16; sums, and the partial results that are joined, are fp32.
- * Limits: B <= 1024, 1 <= G <= B.
+ * Limits: B <= 1024, B * Hkv <= 65535, 1 <= G <= B.
  * workspace >= tsd_tree_attn_shared_workspace_bytes(), 16-byte aligned (the plan of the
  * call and fp32 partial rows; no initial contents); calls that may run at the same time
  * need workspaces of their own.  Three launches (plan, attention, join) whose shapes

@@ -69,17 +69,19 @@ constexpr uint64_t kDrainNs = 100000000ull;
 constexpr int kMaxBatch = 1024;
 constexpr int kPlanThreads = 1024;
 constexpr int kPieces = 64;     // pieces of one key range at most
-constexpr int kRangeCost = 9;   // a unit's fixed cost, in key tiles of one row tile
+// A unit's fixed cost in a row block of one or two row tiles, in key tiles of one.
+constexpr int kRangeCost1 = 12, kRangeCost2 = 22;
 
 // One row set and its key range, for every kv head.
 struct Unit {
   long long start;     // where its cost begins
   long long row_base;  // query rows (times kv heads) of the units before
   int tiles, rows, rbs, last_w;  // rows of one kv head, their blocks, cost of a tile in the last
+  int block_base;      // row blocks (times kv heads) of the units before
   int node0;           // first entry of the node map
   int table;           // sequence whose block table is read
   int lo, hi, P;       // key slots [lo, hi); from P on they are the tree's
-  int nb, b;           // tree (own ranges)
+  int nb;              // the tree's nodes (own ranges)
   int group;           // own ranges: the shared unit of the same rows, or -1
 };
 static_assert(sizeof(Unit) == 64, "");
@@ -87,6 +89,8 @@ static_assert(sizeof(Unit) == 64, "");
 struct Plan {
   long long total, part;
 };
+
+struct Seg;
 
 struct Attn {
   const uint16_t *q, *k, *v;
@@ -99,8 +103,11 @@ struct Attn {
   int G, B, N_max, Hq, Hkv, g, W;
   float scale_log2;
   int blocks;
+  int join_heads;  // heads of a block of the join, a multiple of 8
   Plan *plan;
   Unit *units;        // [G + B]: the groups', then the sequences'
+  Seg *first_seg;     // [blocks]
+  int2 *marks;        // by row block and kv head: first and last block of its key range
   int32_t *node_map;  // packed node -> b * N_max + i
   float2 *part_ml;    // (reference in log2 units, sum; sum -1: bad page)
   float *part_o;      // unnormalised fp32 outputs
@@ -129,7 +136,7 @@ __device__ __forceinline__ long long block_scan(long long x, long long *buf, lon
   __syncthreads();
   long long before = 0;
   all = 0;
-  for (int w = 0; w < kPlanThreads / 32; ++w) {
+  for (int w = 0; w < (int)blockDim.x / 32; ++w) {
     const long long s = buf[w];
     if (w < warp) before += s;
     all += s;
@@ -148,8 +155,12 @@ __device__ __forceinline__ Unit load_unit(const Unit *at) {
   return r.u;
 }
 
+// Cost of a unit's row block of w row tiles.
+__device__ __forceinline__ long long block_cost(const Unit &u, int w) {
+  return (w == 2 ? kRangeCost2 : kRangeCost1) + (long long)u.tiles * w;
+}
 __device__ __forceinline__ long long unit_cost(const Unit &u, int Hkv) {
-  return u.rbs ? (long long)Hkv * ((long long)u.rbs * kRangeCost + (long long)u.tiles * ((u.rbs - 1) * 2 + u.last_w)) : 0;
+  return u.rbs ? (long long)Hkv * ((u.rbs - 1) * block_cost(u, 2) + block_cost(u, u.last_w)) : 0;
 }
 
 __device__ __forceinline__ void shape_unit(Unit &u, int nodes, int g) {
@@ -160,20 +171,89 @@ __device__ __forceinline__ void shape_unit(Unit &u, int nodes, int g) {
   u.last_w = u.rows - (u.rbs - 1) * kRows > kBM ? 2 : 1;
 }
 
+// A block's next piece of work: a run of key tiles for one row block of one kv head.
+struct Seg {
+  long long next;         // where the block goes on
+  long long part;         // first partial row
+  int rows, row0;         // the unit's rows of one kv head, the first of this row block
+  int h, node0, table;
+  int page, pages;        // first page of the range, its pages
+  int lo, hi, P, nb;
+  int n;                  // key tiles; 0: no more work
+  int two;                // two row tiles (each with every key tile), or one row tile whose key
+                          // tiles alternate between the chains
+  int mark;               // where the join looks for the range's blocks; -1 - that: not the first piece
+  int whole;              // 1: the range's last piece
+  int pad;
+};
+static_assert(sizeof(Seg) == 80, "five 16-byte words");
+
+// The segment at g of a unit that holds g, as far as `end`; false when none begins there
+// (s.next is moved on).
+__device__ __forceinline__ bool cut_segment(const Unit &u, long long g, long long end, int block, Seg &s) {
+  const long long full = block_cost(u, 2);
+  const long long head = (u.rbs - 1) * full + block_cost(u, u.last_w);
+  const long long local = g - u.start;
+  int rb;
+  long long x0;
+  if (local < 0x7FFFFFFF && head < 0x7FFFFFFF) {  // (a 64-bit division takes some 100 instructions)
+    const uint32_t l = (uint32_t)local;
+    s.h = (int)(l / (uint32_t)head);
+    const uint32_t in_head = l - (uint32_t)s.h * (uint32_t)head;
+    rb = min((int)(in_head / (uint32_t)full), u.rbs - 1);
+    x0 = (long long)in_head - rb * full;
+  } else {
+    s.h = (int)(local / head);
+    const long long in_head = local - s.h * head;
+    rb = (int)min(in_head / full, (long long)(u.rbs - 1));
+    x0 = in_head - rb * full;
+  }
+  const int w = rb == u.rbs - 1 ? u.last_w : 2, fixed = w == 2 ? kRangeCost2 : kRangeCost1;
+  const long long x1 = min(fixed + (long long)u.tiles * w, x0 + end - g);
+  s.next = g + x1 - x0;
+  // (w is 1 or 2)
+  const int u0 = (int)((max(x0 - fixed, 0ll) + w - 1) >> (w - 1)), u1 = (int)((max(x1 - fixed, 0ll) + w - 1) >> (w - 1));
+  if (u0 >= u1) return false;
+  s.rows = u.rows;
+  s.row0 = rb * kRows;
+  s.node0 = u.node0;
+  s.table = u.table;
+  s.page = u.lo / kPage + u0 * kTilePages;
+  s.pages = min((u.hi + kPage - 1) / kPage - s.page, (u1 - u0) * kTilePages);
+  s.lo = u.lo;
+  s.hi = u.hi;
+  s.P = u.P;
+  s.nb = u.nb;
+  s.n = u1 - u0;
+  s.two = u.rows - s.row0 > kBM;
+  s.part = u.row_base + (long long)s.h * u.rows + s.row0 + (long long)block * kRows;
+  s.mark = u.block_base + s.h * u.rbs + rb;
+  if (u0 > 0) s.mark = -1 - s.mark;
+  s.whole = u1 == u.tiles;
+  return true;
+}
+
 __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const Attn p) {
   __shared__ int off[kMaxBatch + 1];   // packed nodes before sequence b
   __shared__ int first[kMaxBatch + 1], shared[kMaxBatch], members[kMaxBatch], rep[kMaxBatch];
+  __shared__ long long starts[2 * kMaxBatch];
   __shared__ long long buf[kPlanThreads / 32];
   __shared__ int bad_groups;
   __shared__ long long longest;
   pdl_trigger();
-  const int tid = threadIdx.x, B = p.B, G = p.G;
+  const int tid = threadIdx.x, B = p.B, G = p.G;  // (at least B threads, and G <= B)
   if (tid == 0) {
     bad_groups = 0;
     longest = 0;
   }
   pdl_wait();
-  for (int i = tid; i <= G; i += kPlanThreads) first[i] = p.first[i];
+  int P = 0, nb = 0, S = 0, gr = 0, err = 0;
+  if (tid < B) {
+    P = p.prefix_len[tid];
+    nb = p.n_nodes ? p.n_nodes[tid] : p.N_max;
+    err = p.err ? p.err[tid] : 0;
+  }
+  for (int i = tid; i <= G; i += blockDim.x) first[i] = p.first[i];
   if (tid < G) {
     shared[tid] = p.shared[tid];
     members[tid] = 0;
@@ -185,11 +265,8 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const Attn p)
   if (tid == 0 && (first[0] != 0 || first[G] != B)) bad_groups = 1;
   __syncthreads();
   const bool groups_ok = !bad_groups;
-  int P = 0, nb = 0, S = 0, gr = 0;
   bool ok = false;
   if (tid < B) {
-    P = p.prefix_len[tid];
-    nb = p.n_nodes ? p.n_nodes[tid] : p.N_max;
     bool bad = !groups_ok;
     if (groups_ok) {  // the last group that begins at or before this sequence
       int hi = G - 1;
@@ -201,7 +278,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const Attn p)
       bad = nb < 1 || nb > p.N_max || P < 0 || S < 0 || S > P ||
             (int64_t)P + nb > (int64_t)p.max_blocks * kPage;
     }
-    const bool skip = p.err && p.err[tid] != 0;
+    const bool skip = err != 0;
     ok = !bad && !skip;
     if (bad && !skip && p.status) atomicOr(p.status, TSD_STATUS_BAD_LEN);
     if (ok) {
@@ -214,7 +291,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const Attn p)
   if (tid < B) off[tid] = node0;
   if (tid == 0) off[B] = (int)all;
   __syncthreads();
-  // entry e of this thread's two: a group's shared range, a sequence's own
+  // a thread's two units: a group's shared range, a sequence's own
   Unit u[2] = {};
   if (tid < G && groups_ok) {
     const bool once = members[tid] > 1;  // (one sequence alone keeps its range whole)
@@ -230,30 +307,58 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const Attn p)
     u[1].P = P;
     u[1].hi = ok ? P + nb : 0;
     u[1].node0 = node0;
-    u[1].table = u[1].b = tid;
+    u[1].table = tid;
     u[1].nb = ok ? nb : 0;
     u[1].group = split ? gr : -1;
     shape_unit(u[1], u[1].nb, p.g);
   }
+  // costs, and row blocks and rows (in one word: rows below 2^40, blocks below 2^23)
   const long long c0 = unit_cost(u[0], p.Hkv), c1 = unit_cost(u[1], p.Hkv);
   long long groups_cost, own_cost, groups_rows, own_rows;
   u[0].start = block_scan(c0, buf, groups_cost);
   u[1].start = groups_cost + block_scan(c1, buf, own_cost);
-  u[0].row_base = block_scan((long long)(u[0].rbs ? u[0].rows : 0) * p.Hkv, buf, groups_rows);
-  u[1].row_base = groups_rows + block_scan((long long)u[1].rows * p.Hkv, buf, own_rows);
-  const long long far = 2ll * max(u[0].tiles, u[1].tiles) + kRangeCost;
+  auto packed = [&](const Unit &x) { return x.rbs ? ((long long)x.rbs << 40 | x.rows) * p.Hkv : 0; };
+  const long long r0 = block_scan(packed(u[0]), buf, groups_rows), r1 = groups_rows + block_scan(packed(u[1]), buf, own_rows);
+  constexpr long long kRowBits = (1ll << 40) - 1;
+  u[0].row_base = r0 & kRowBits;
+  u[1].row_base = r1 & kRowBits;
+  u[0].block_base = (int)(r0 >> 40);
+  u[1].block_base = (int)(r1 >> 40);
+  const long long far = 2ll * max(u[0].tiles, u[1].tiles) + kRangeCost2;
   atomicMax((unsigned long long *)&longest, (unsigned long long)far);
-  if (tid < G) p.units[tid] = u[0];
-  if (tid < B) p.units[G + tid] = u[1];
-  __syncthreads();
-  if (tid == 0) {
-    const long long total = groups_cost + own_cost;
-    // (a part shorter than a unit's set-up and two tiles is mostly set-up)
-    long long part = max((total + p.blocks - 1) / p.blocks, (long long)kRangeCost + 4);
-    part = max(part, (longest + kPieces - 3) / (kPieces - 2));
-    *p.plan = Plan{total, part};
+  if (tid < G) {
+    p.units[tid] = u[0];
+    starts[tid] = u[0].start;
   }
-  for (int b = tid >> 5; b < B; b += kPlanThreads / 32)
+  if (tid < B) {
+    p.units[G + tid] = u[1];
+    starts[G + tid] = u[1].start;
+  }
+  __syncthreads();
+  const long long total = groups_cost + own_cost;
+  // (a part shorter than a unit's set-up and some tiles is mostly set-up)
+  long long part = max((total + p.blocks - 1) / p.blocks, (long long)kRangeCost1 + 4);
+  part = max(part, (longest + kPieces - 3) / (kPieces - 2));
+  if (tid == 0) *p.plan = Plan{total, part};
+  // every block's first segment
+  for (int k = tid; k < p.blocks; k += blockDim.x) {
+    long long g = (long long)k * part;
+    const long long end = min(total, g + part);
+    Seg s;
+    s.n = 0;
+    while (g < end) {
+      int at = 0, hi = G + B - 1;
+      while (at < hi) {
+        const int mid = (at + hi + 1) >> 1;
+        if (starts[mid] <= g) at = mid; else hi = mid - 1;
+      }
+      if (cut_segment(load_unit(p.units + at), g, end, k, s)) break;
+      g = s.next;
+      s.n = 0;
+    }
+    p.first_seg[k] = s;
+  }
+  for (int b = tid >> 5; b < B; b += blockDim.x / 32)
     for (int i = tid & 31; i < off[b + 1] - off[b]; i += 32) p.node_map[off[b] + i] = b * p.N_max + i;
 }
 
@@ -261,22 +366,9 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const Attn p)
 // segments
 // ---------------------------------------------------------------------------
 
-struct Seg {
-  int rows, row0;         // the unit's rows of one kv head, the first of this row block
-  int h, node0, table;
-  int page, pages;        // first page of the range, its pages
-  int lo, hi, P, nb, b;
-  int n;                  // key tiles
-  bool two;               // two row tiles (each with every key tile), or one row tile whose key
-                          // tiles alternate between the chains
-  bool more;
-  long long part;         // first partial row
-};
-
-// The next segment of the part [.., end), from g on; by a whole warp.
-__device__ __forceinline__ bool next_segment(const Attn &p, long long &g, long long part, long long total, Seg &s) {
+// The block's next segment after `g`, in the part that ends at `end`; by a whole warp.
+__device__ __forceinline__ void next_segment(const Attn &p, long long g, long long end, Seg &s) {
   const int lane = threadIdx.x & 31, count = p.G + p.B;
-  const long long end = min(total, (long long)(blockIdx.x + 1) * part);
   while (g < end) {
     // the last unit that starts at or before g (it is not empty: those after share its
     // start or a later one)
@@ -289,36 +381,10 @@ __device__ __forceinline__ bool next_segment(const Attn &p, long long &g, long l
       if (step == 1) break;
       step = (step + 31) / 32;
     }
-    const Unit u = load_unit(p.units + at);
-    const long long full = kRangeCost + 2ll * u.tiles;
-    const long long head = u.rbs * full - (long long)u.tiles * (2 - u.last_w);
-    const long long local = g - u.start;
-    s.h = (int)(local / head);
-    const long long in_head = local - s.h * head;
-    const int rb = min((int)(in_head / full), u.rbs - 1);
-    const int w = rb == u.rbs - 1 ? u.last_w : 2;
-    const long long x0 = in_head - rb * full;
-    const long long x1 = min(kRangeCost + (long long)u.tiles * w, x0 + end - g);
-    g += x1 - x0;
-    const int u0 = (int)((max(x0 - kRangeCost, 0ll) + w - 1) / w), u1 = (int)((max(x1 - kRangeCost, 0ll) + w - 1) / w);
-    if (u0 >= u1) continue;
-    s.rows = u.rows;
-    s.row0 = rb * kRows;
-    s.node0 = u.node0;
-    s.table = u.table;
-    s.page = u.lo / kPage + u0 * kTilePages;
-    s.pages = min((u.hi + kPage - 1) / kPage - s.page, (u1 - u0) * kTilePages);
-    s.lo = u.lo;
-    s.hi = u.hi;
-    s.P = u.P;
-    s.nb = u.nb;
-    s.b = u.b;
-    s.n = u1 - u0;
-    s.two = u.rows - s.row0 > kBM;
-    s.part = u.row_base + (long long)s.h * u.rows + s.row0 + (long long)blockIdx.x * kRows;
-    return true;
+    if (cut_segment(load_unit(p.units + at), g, end, blockIdx.x, s)) return;
+    g = s.next;
   }
-  return false;
+  s.n = 0;
 }
 
 template <int D>
@@ -344,8 +410,9 @@ struct Shared {
   int poisoned;
   uint32_t tmem_base;
   int abort, bad;
-  long long g, part, total;
-  Seg seg;
+  long long end;   // of the block's part
+  alignas(16) Seg seg;
+  alignas(16) Seg ahead;  // the segment after the one in work
 };
 constexpr int kBarriers = 17;
 
@@ -420,7 +487,7 @@ __device__ __noinline__ uint32_t visible32(const Attn &p, const volatile Seg &sg
     uint32_t tail = 0u;
     if (left > 0) {
       if (p.mask) {
-        const uint32_t *m = p.mask + ((size_t)sg.b * p.N_max + i) * p.W;
+        const uint32_t *m = p.mask + ((size_t)sg.table * p.N_max + i) * p.W;
         const int w = at >> 5;
         tail = __funnelshift_r(m[w], w + 1 < p.W ? m[w + 1] : 0u, at & 31);
       } else {
@@ -442,39 +509,34 @@ __device__ __forceinline__ void mask_scores(uint32_t vis, uint32_t (&s)[32]) {
     if (!((vis >> i) & 1u)) s[i] = 0xFF800000u;
 }
 
-// The block's next segment, and its barriers; every thread of the block calls it,
-// after everything of the segment before has completed.  `fresh`: there was none.
+// Goes on to the segment ahead, and lays its barriers; every thread of the block calls
+// it, after everything of the segment before has completed.  `fresh`: there was none.
 __device__ __forceinline__ bool begin_segment(const Attn &p, Shared &sh, bool fresh, int tid) {
   using namespace sm100;
   tc_fence_before();
   __syncthreads();
   if (tid < 32) {
-    long long g = sh.g;
-    Seg sg;
-    sg.more = next_segment(p, g, sh.part, sh.total, sg);
-    if (sg.more && tid < kBarriers) {
+    if (tid < kBarriers && sh.ahead.n > 0) {
       // the barriers lie one after the other, from k_full to never
       const uint32_t bar = smem_addr(&sh.k_full[0] + tid);
       // p_full: the softmax warps, and what tells that V is there (with two row tiles
       // the first chain's alone)
-      const int count = tid == 10 ? 9 : tid == 11 ? (sg.two ? 8 : 9) : tid == 14 ? 16 : 1;
+      const int count = tid == 10 ? 9 : tid == 11 ? (sh.ahead.two ? 8 : 9) : tid == 14 ? 16 : 1;
       if (!fresh) mbar_inval(bar);
       mbar_init(bar, count);
       fence_mbar_init();
     }
-    __syncwarp();
     if (tid < kMaxNodes / 32) sh.poison[tid] = 0u;
+    if (tid < 5) reinterpret_cast<int4 *>(&sh.seg)[tid] = reinterpret_cast<const int4 *>(&sh.ahead)[tid];
     if (tid == 0) {
       if (!fresh && sh.bad && p.status) atomicOr(p.status, TSD_STATUS_BAD_PAGE);
       sh.bad = 0;
       sh.poisoned = 0;
-      sh.g = g;
-      sh.seg = sg;
     }
   }
   __syncthreads();
   tc_fence_after();
-  return sh.seg.more;
+  return sh.seg.n > 0;
 }
 
 // V tile j in shared memory as the MMAs may read it: rows outside the key range, and
@@ -483,30 +545,37 @@ template <int D>
 __device__ __forceinline__ void clear_hidden(Shared &sh, const volatile Seg &sg, uint8_t *tile, int j, int lane) {
   const int s0 = sg.page * kPage + j * kBN, lo = sg.lo, hi = sg.hi, P = sg.P;
   if (s0 >= lo && s0 + kBN <= P) return;
-  // a lane's part of a row: 4 bytes of each 64-column half (a row's 128 bytes lie together,
-  // in some order)
-  auto at = [&](int r, int half) { return reinterpret_cast<uint32_t *>(tile + half * Layout<D>::kHalf + r * 128) + lane; };
-  for (int r = 0; r < min(kBN, lo - s0); ++r)
-    for (int h = 0; h < D / 64; ++h) *at(r, h) = 0u;
-  for (int r = max(0, P - s0); r < min(kBN, hi - s0); ++r) {
-    bool odd = false;
+  // A lane a row (a row's 128 bytes of a 64-column half lie together, in some order), its
+  // chunks from its own place on, so that eight lanes touch all banks.
+  for (int r0 = 0; r0 < kBN; r0 += 32) {
+    const int r = r0 + lane, s = s0 + r;
+    uint8_t *row = tile + r * 128;
+    bool clear = s < lo || s >= hi;
+    if (__any_sync(0xffffffffu, !clear && s >= P)) {
+      uint32_t most = 0u;  // bf16 magnitudes order as integers
 #pragma unroll
-    for (int h = 0; h < D / 64; ++h) {
-      const uint32_t w = *at(r, h);
-      odd = odd || (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
-    }
-    if (__any_sync(0xffffffffu, odd)) {
+      for (int h = 0; h < D / 64; ++h)
 #pragma unroll
-      for (int h = 0; h < D / 64; ++h) *at(r, h) = 0u;
-      if (lane == 0) {
-        const int node = s0 + r - P;
-        sh.poison[node >> 5] |= 1u << (node & 31);
+        for (int c = 0; c < 8; ++c) {
+          const uint4 v = *reinterpret_cast<const uint4 *>(row + h * Layout<D>::kHalf + ((c + lane) & 7) * 16);
+          most = __vmaxu2(__vmaxu2(most, v.x & 0x7FFF7FFFu), v.y & 0x7FFF7FFFu);
+          most = __vmaxu2(__vmaxu2(most, v.z & 0x7FFF7FFFu), v.w & 0x7FFF7FFFu);
+        }
+      const bool odd = !clear && s >= P && ((most & 0xFFFFu) >= 0x7F80u || (most >> 16) >= 0x7F80u);
+      if (odd) {
+        atomicOr(&sh.poison[(s - P) >> 5], 1u << ((s - P) & 31));
         sh.poisoned = 1;
       }
+      clear = clear || odd;
+    }
+    if (clear) {
+#pragma unroll
+      for (int h = 0; h < D / 64; ++h)
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          *reinterpret_cast<uint4 *>(row + h * Layout<D>::kHalf + ((c + lane) & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
     }
   }
-  for (int r = max(0, hi - s0); r < kBN; ++r)
-    for (int h = 0; h < D / 64; ++h) *at(r, h) = 0u;
   sm100::fence_proxy_async_smem();  // the tensor core reads the tile through the async proxy
   __syncwarp();
 }
@@ -538,10 +607,10 @@ shared_attn_kernel(const Attn p, const __grid_constant__ CUtensorMap map_k1,
   }
   if (warp == 1) tmem_alloc(smem_addr(&sh.tmem_base), kTmemCols);
   pdl_wait();
-  if (tid == 0) {
-    sh.part = __ldcg(&p.plan->part);
-    sh.total = __ldcg(&p.plan->total);
-    sh.g = (long long)blockIdx.x * sh.part;
+  if (tid < 5) reinterpret_cast<int4 *>(&sh.ahead)[tid] = __ldcg(reinterpret_cast<const int4 *>(p.first_seg + blockIdx.x) + tid);
+  if (tid == 32) {
+    const long long part = __ldcg(&p.plan->part), total = __ldcg(&p.plan->total);
+    sh.end = min(total, (long long)(blockIdx.x + 1) * part);
   }
   tc_fence_before();
   __syncthreads();
@@ -674,6 +743,16 @@ shared_attn_kernel(const Attn p, const __grid_constant__ CUtensorMap map_k1,
         if (u > 0) ok = tc_wait(sh.p_full[c], (u - 1) & 1, lim, abort);
         if (!__all_sync(0xffffffffu, ok)) break;
         if (lane == 0) mbar_arrive(smem_addr(&sh.p_full[c]));
+      }
+      __syncwarp();
+      // the segment after this one, while the last tile is worked on
+      Seg s;
+      next_segment(p, sg.next, sh.end, s);
+      if (lane == 0) {
+        const int mark = sg.mark;
+        if (mark >= 0) p.marks[mark].x = blockIdx.x;
+        if (sg.whole) p.marks[mark >= 0 ? mark : -1 - mark].y = blockIdx.x;
+        sh.ahead = s;
       }
       __syncwarp();
     } else {
@@ -969,118 +1048,141 @@ struct Pieces {
   int k0, n;      // first block, pieces
 };
 
-__device__ __forceinline__ Pieces pieces_of(const Unit &u, int h, int r, long long part) {
-  Pieces x;
-  const long long full = kRangeCost + 2ll * u.tiles;
-  const int rb = r / kRows, w = rb == u.rbs - 1 ? u.last_w : 2;
-  const long long at = u.start + h * (u.rbs * full - (long long)u.tiles * (2 - u.last_w)) + rb * full + kRangeCost;
-  x.k0 = (int)(at / part);
-  x.n = (int)((at + (long long)(u.tiles - 1) * w) / part) - x.k0 + 1;
-  x.row = u.row_base + (long long)h * u.rows + r;
-  return x;
-}
-
-// One warp per output row: its pieces of the shared and of the own range.
+// Blocks (node, some heads): its warps take the heads in turn.  A row's pieces of the shared and of
+// the own range are weighed by their sums and added up.
 template <int D>
 __global__ void __launch_bounds__(256) shared_join_kernel(const Attn p) {
   using namespace sm100;
   constexpr int kPer = D / 32;  // columns of a lane
+  constexpr int kAhead = 4;     // pieces read before the first is used
+  __shared__ alignas(16) Unit unit[2];
   pdl_trigger();
   pdl_wait();
-  const int64_t x = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (x >= (int64_t)p.B * p.N_max * p.Hq) return;
-  const int hq = (int)(x % p.Hq), h = hq / p.g;
-  const int64_t bi = x / p.Hq;
-  const int i = (int)(bi % p.N_max), b = (int)(bi / p.N_max);
-  const long long part = __ldcg(&p.plan->part);
-  const Unit own = load_unit(p.units + p.G + b);
-  Pieces set[2] = {};
-  int rl[2] = {};  // place in the row tile, modulo 8
-  if (i < own.nb) {
-    const int r = i * p.g + hq % p.g;
-    set[0] = pieces_of(own, h, r, part);
-    rl[0] = r & 7;
-    if (own.group >= 0) {
-      const Unit sh = load_unit(p.units + own.group);
-      const int rs = (own.node0 - sh.node0) * p.g + r;
-      set[1] = pieces_of(sh, h, rs, part);
-      rl[1] = rs & 7;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int b = blockIdx.x / p.N_max, i = blockIdx.x % p.N_max;
+  if (warp == 0) {
+    if (lane < 4) reinterpret_cast<int4 *>(&unit[0])[lane] = __ldcg(reinterpret_cast<const int4 *>(p.units + p.G + b) + lane);
+    __syncwarp();
+    const int group = unit[0].group;
+    if (group >= 0 && lane < 4)
+      reinterpret_cast<int4 *>(&unit[1])[lane] = __ldcg(reinterpret_cast<const int4 *>(p.units + group) + lane);
+  }
+  __syncthreads();
+  const Unit &own = unit[0], &shd = unit[1];
+  const bool on = i < own.nb, split = own.group >= 0;
+  const int heads = p.join_heads;  // of this block
+  for (int hq = blockIdx.y * heads + warp; hq < min(p.Hq, (int)(blockIdx.y + 1) * heads); hq += 8) {
+    const int64_t x = (int64_t)blockIdx.x * p.Hq + hq;
+    const int h = hq / p.g;
+    Pieces set[2] = {};
+    int rl[2] = {};  // place in the row tile, modulo 8
+    if (on) {
+      const int r = i * p.g + hq % p.g, rs = split ? (own.node0 - shd.node0) * p.g + r : 0;
+      const int2 m0 = __ldcg(p.marks + own.block_base + h * own.rbs + r / kRows);
+      set[0] = Pieces{own.row_base + (long long)h * own.rows + r, m0.x, m0.y - m0.x + 1};
+      rl[0] = r & 7;
+      if (split) {
+        const int2 m1 = __ldcg(p.marks + shd.block_base + h * shd.rbs + rs / kRows);
+        set[1] = Pieces{shd.row_base + (long long)h * shd.rows + rs, m1.x, m1.y - m1.x + 1};
+        rl[1] = rs & 7;
+      }
     }
-  }
-  const int n = set[0].n + set[1].n;
-  auto part_row = [&](int s) -> size_t {
-    const Pieces &y = s < set[0].n ? set[0] : set[1];
-    return (size_t)(y.row + (long long)(y.k0 + s - (s < set[0].n ? 0 : set[0].n)) * kRows);
-  };
-  // lane l holds the (reference, sum) of pieces l, l + 32, ...: at most 128
-  float2 ml[4];
-  bool bad = false;
-  float M = -INFINITY;
+    const int n = set[0].n + set[1].n;
+    auto part_row = [&](int s) -> size_t {
+      const Pieces &y = s < set[0].n ? set[0] : set[1];
+      return (size_t)(y.row + (long long)(y.k0 + s - (s < set[0].n ? 0 : set[0].n)) * kRows);
+    };
+    // lane l holds the (reference, sum) of pieces l, l + 32, ...: at most 128
+    float2 ml[4];
+    float a[kPer] = {}, M = -INFINITY;
+    float v[kAhead][kPer];
+    auto load = [&](int s0) {
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    ml[e] = make_float2(-INFINITY, 0.f);
-    if (lane + 32 * e < n) ml[e] = __ldcg(&p.part_ml[part_row(lane + 32 * e)]);
-    bad = bad || ml[e].y == -1.f;
-    M = fmaxf(M, ml[e].x);
-  }
-  bad = __any_sync(0xffffffffu, bad);
+      for (int j = 0; j < kAhead; ++j) {
+        const int s = s0 + j;
+        if (s >= n) break;
+        // (a partial row's 16-byte chunks are swizzled by its place in the row tile, which
+        // spreads the stores over the banks)
+        const int phase = s < set[0].n ? rl[0] : rl[1];
+        const float *src = p.part_o + part_row(s) * D + ((lane * kPer / 4) ^ phase) * 4 + lane * kPer % 4;
+        if constexpr (kPer == 4) {
+          const float4 y = __ldcg(reinterpret_cast<const float4 *>(src));
+          v[j][0] = y.x;
+          v[j][1] = y.y;
+          v[j][2] = y.z;
+          v[j][3] = y.w;
+        } else {
+          const float2 y = __ldcg(reinterpret_cast<const float2 *>(src));
+          v[j][0] = y.x;
+          v[j][1] = y.y;
+        }
+      }
+    };
 #pragma unroll
-  for (int off = 16; off; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-  float f[4], sum = 0.f;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    f[e] = ml[e].x == -INFINITY ? 0.f : ex2_approx(ml[e].x - M);
-    sum += f[e] * ml[e].y;
-  }
-#pragma unroll
-  for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-  const bool empty = n == 0 || bad || sum == 0.f;
-  float a[kPer];
-#pragma unroll
-  for (int c = 0; c < kPer; ++c) a[c] = 0.f;
-  for (int s = 0; s < n; ++s) {
-    const float mine = s < 64 ? (s < 32 ? f[0] : f[1]) : (s < 96 ? f[2] : f[3]);
-    const float fs = __shfl_sync(0xffffffffu, mine, s & 31);
-    if (fs == 0.f) continue;
-    // (a partial row's 16-byte chunks are swizzled by its place in the row tile, which
-    // spreads the stores over the banks)
-    const int phase = s < set[0].n ? rl[0] : rl[1];
-    const float *src = p.part_o + part_row(s) * D + ((lane * kPer / 4) ^ phase) * 4 + lane * kPer % 4;
-    if constexpr (kPer == 4) {
-      const float4 v = __ldcg(reinterpret_cast<const float4 *>(src));
-      a[0] += fs * v.x;
-      a[1] += fs * v.y;
-      a[2] += fs * v.z;
-      a[3] += fs * v.w;
-    } else {
-      const float2 v = __ldcg(reinterpret_cast<const float2 *>(src));
-      a[0] += fs * v.x;
-      a[1] += fs * v.y;
+    for (int e = 0; e < 4; ++e) {
+      ml[e] = make_float2(-INFINITY, 0.f);
+      if (lane + 32 * e < n) ml[e] = __ldcg(&p.part_ml[part_row(lane + 32 * e)]);
     }
-  }
-  const float inv = empty ? 0.f : 1.f / sum;
-  uint32_t w[kPer / 2];
+    load(0);  // (before the weights are known)
+    bool bad = false;
 #pragma unroll
-  for (int c = 0; c < kPer / 2; ++c) w[c] = empty ? 0u : pack_bf16x2(a[2 * c] * inv, a[2 * c + 1] * inv);
-  uint16_t *dst = p.out + x * D + lane * kPer;
-  if constexpr (kPer == 4)
-    *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
-  else
-    *reinterpret_cast<uint32_t *>(dst) = w[0];
-  if (lane == 0 && p.lse) p.lse[x] = empty ? -INFINITY : (M + log2f(sum)) * kLn2;
+    for (int e = 0; e < 4; ++e) {
+      bad = bad || ml[e].y == -1.f;
+      M = fmaxf(M, ml[e].x);
+    }
+    bad = __any_sync(0xffffffffu, bad);
+#pragma unroll
+    for (int off = 16; off; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+    float f[4], sum = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      f[e] = ml[e].x == -INFINITY ? 0.f : ex2_approx(ml[e].x - M);
+      sum += f[e] * ml[e].y;
+    }
+#pragma unroll
+    for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    const bool empty = n == 0 || bad || sum == 0.f;
+    for (int s0 = 0; s0 < n;) {
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        const int s = s0 + j;
+        if (s >= n) break;
+        const float mine = s < 64 ? (s < 32 ? f[0] : f[1]) : (s < 96 ? f[2] : f[3]);
+        const float fs = __shfl_sync(0xffffffffu, mine, s & 31);
+        // (a piece in which the row saw nothing has no row)
+#pragma unroll
+        for (int c = 0; c < kPer; ++c) a[c] += fs != 0.f ? fs * v[j][c] : 0.f;
+      }
+      s0 += kAhead;
+      if (s0 < n) load(s0);
+    }
+    const float inv = empty ? 0.f : 1.f / sum;
+    uint32_t w[kPer / 2];
+#pragma unroll
+    for (int c = 0; c < kPer / 2; ++c) w[c] = empty ? 0u : pack_bf16x2(a[2 * c] * inv, a[2 * c + 1] * inv);
+    uint16_t *dst = p.out + x * D + lane * kPer;
+    if constexpr (kPer == 4)
+      *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
+    else
+      *reinterpret_cast<uint32_t *>(dst) = w[0];
+    if (lane == 0 && p.lse) p.lse[x] = empty ? -INFINITY : (M + log2f(sum)) * kLn2;
+  }
 }
 
 struct Sizes {
-  size_t units, nodes, ml, o, bytes;
+  size_t units, segs, marks, nodes, ml, o, bytes;
   size_t rows;  // partial rows
 };
 
-Sizes sizes(int B, int N_max, int Hq, int D, int G) {
+Sizes sizes(int B, int N_max, int Hq, int Hkv, int D, int G) {
   Sizes z;
   z.rows = 2 * (size_t)B * N_max * Hq + (size_t)sm_count() * kRows;
   z.units = align_up(sizeof(Plan), 256);
-  z.nodes = z.units + align_up((size_t)(G + B) * sizeof(Unit), 256);
+  z.segs = z.units + align_up((size_t)(G + B) * sizeof(Unit), 256);
+  z.marks = z.segs + align_up((size_t)sm_count() * sizeof(Seg), 256);
+  // row blocks: full ones of all rows, shared and own, and a last one of each unit
+  const size_t row_blocks = (size_t)Hkv * (2 * ((size_t)B * N_max * (Hq / Hkv) / kRows) + G + B);
+  z.nodes = z.marks + align_up(row_blocks * sizeof(int2), 256);
   z.ml = z.nodes + align_up((size_t)B * N_max * sizeof(int32_t), 256);
   z.o = z.ml + align_up(z.rows * sizeof(float2), 256);
   z.bytes = z.o + z.rows * D * sizeof(float);
@@ -1090,7 +1192,9 @@ Sizes sizes(int B, int N_max, int Hq, int D, int G) {
 int check(int B, int N_max, int Hq, int Hkv, int D, int G) {
   if (B < 0 || N_max < 1 || Hq < 1 || Hkv < 1 || G < 0) return TSD_ERR_ARG;
   if (D != 64 && D != 128) return TSD_ERR_LIMIT;
-  if (N_max > kMaxNodes || Hq % Hkv != 0 || Hq / Hkv > 16 || B > kMaxBatch || Hkv > 65535) return TSD_ERR_LIMIT;
+  if (N_max > kMaxNodes || Hq % Hkv != 0 || Hq / Hkv > 16 || B > kMaxBatch ||
+      (int64_t)(B > 0 ? B : 1) * Hkv > 65535)
+    return TSD_ERR_LIMIT;
   if (B > 0 && (G < 1 || G > B)) return TSD_ERR_ARG;
   return TSD_OK;
 }
@@ -1104,11 +1208,12 @@ int launch_all(const Attn &p, cudaStream_t s) {
       !make_cache_map(&v8, p.v, p.num_blocks, p.Hkv, D, kTilePages))
     return TSD_ERR_CUDA;
   if (!set_smem((const void *)shared_attn_kernel<D>, Layout<D>::kAlloc)) return TSD_ERR_CUDA;
-  if (launch(shared_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, p) != cudaSuccess) return TSD_ERR_CUDA;
+  const int threads = p.B <= 256 ? 256 : kPlanThreads;
+  if (launch(shared_plan_kernel, dim3(1), dim3(threads), 0, s, p) != cudaSuccess) return TSD_ERR_CUDA;
   if (launch(shared_attn_kernel<D>, dim3(p.blocks), dim3(kThreads), Layout<D>::kAlloc, s, p, k1, k8, v1, v8) != cudaSuccess)
     return TSD_ERR_CUDA;
-  const int64_t rows = (int64_t)p.B * p.N_max * p.Hq;
-  if (launch(shared_join_kernel<D>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, s, p) != cudaSuccess)
+  const dim3 grid((unsigned)(p.B * p.N_max), (unsigned)((p.Hq + p.join_heads - 1) / p.join_heads));
+  if (launch(shared_join_kernel<D>, grid, dim3(256), 0, s, p) != cudaSuccess)
     return TSD_ERR_CUDA;
   return TSD_OK;
 }
@@ -1119,7 +1224,7 @@ int launch_all(const Attn &p, cudaStream_t s) {
 TSD_API size_t tsd_tree_attn_shared_workspace_bytes(int B, int N_max, int Hq, int Hkv, int D, int G) {
   using namespace tsd;
   if (B == 0 || check(B, N_max, Hq, Hkv, D, G) != TSD_OK) return 0;
-  return sizes(B, N_max, Hq, D, G).bytes;
+  return sizes(B, N_max, Hq, Hkv, D, G).bytes;
 }
 
 TSD_API int tsd_tree_attn_fwd_shared(const uint16_t *q, const uint16_t *k_cache, const uint16_t *v_cache,
@@ -1140,7 +1245,7 @@ TSD_API int tsd_tree_attn_fwd_shared(const uint16_t *q, const uint16_t *k_cache,
   if (!q || !k_cache || !v_cache || !block_table || !prefix_len || !group_first || !shared_len || !out)
     return TSD_ERR_ARG;
   if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16)) return TSD_ERR_ARG;
-  const Sizes z = sizes(B, N_max, Hq, D, G);
+  const Sizes z = sizes(B, N_max, Hq, Hkv, D, G);
   if (!workspace || ws_bytes < z.bytes) return TSD_ERR_WORKSPACE;
   if (!aligned(workspace, 16)) return TSD_ERR_ARG;
   char *ws = static_cast<char *>(workspace);
@@ -1166,8 +1271,13 @@ TSD_API int tsd_tree_attn_fwd_shared(const uint16_t *q, const uint16_t *k_cache,
   p.W = (N_max + 31) / 32;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.blocks = sm_count();
+  // a warp takes more than one head where there are rows enough to fill the GPU without
+  const int64_t turns = (int64_t)B * N_max * Hq / (64ll * p.blocks);
+  p.join_heads = 8 * (int)(turns < 1 ? 1 : turns > 8 ? 8 : turns);
   p.plan = reinterpret_cast<Plan *>(ws);
   p.units = reinterpret_cast<Unit *>(ws + z.units);
+  p.first_seg = reinterpret_cast<Seg *>(ws + z.segs);
+  p.marks = reinterpret_cast<int2 *>(ws + z.marks);
   p.node_map = reinterpret_cast<int32_t *>(ws + z.nodes);
   p.part_ml = reinterpret_cast<float2 *>(ws + z.ml);
   p.part_o = reinterpret_cast<float *>(ws + z.o);
