@@ -459,6 +459,18 @@ __device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32]) {
                :
                : "memory");
 }
+// Register split of the five warpgroups (96 a thread at launch, 480 in all).
+template <int kRegs>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kRegs));
+}
+constexpr int kRegsLaunch = 96, kRegsIssue = 64, kRegsSoftmax = 104;
+static_assert(kRegsIssue + 4 * kRegsSoftmax <= 5 * kRegsLaunch, "what the block was launched with");
+
 // Barrier of a chain's 256 softmax threads; returns whether any passed true.
 __device__ __forceinline__ bool chain_any(int c, bool x) {
   uint32_t r;
@@ -617,8 +629,11 @@ shared_attn_kernel(const Attn p, const __grid_constant__ CUtensorMap map_k1,
   tc_fence_after();
   const uint32_t tmem = sh.tmem_base;
 
+  // The roles; each takes the block's segments in turn, all of them the same ones.
   const volatile Seg &sg = sh.seg;
-  for (bool fresh = true; begin_segment(p, sh, fresh, tid); fresh = false) {
+  if (warp < kSoftmaxWarp) {
+    regs_down<kRegsIssue>();
+    for (bool fresh = true; begin_segment(p, sh, fresh, tid); fresh = false) {
     const int n = sg.n;
     const bool two = sg.two;
     const int chains = two || n > 1 ? 2 : 1;
@@ -755,8 +770,16 @@ shared_attn_kernel(const Attn p, const __grid_constant__ CUtensorMap map_k1,
         sh.ahead = s;
       }
       __syncwarp();
-    } else {
+    }
+    __syncwarp();
+    }
+  } else {
+    regs_up<kRegsSoftmax>();
+    for (bool fresh = true; begin_segment(p, sh, fresh, tid); fresh = false) {
       // ---- softmax ----
+      const int n = sg.n;
+      const bool two = sg.two;
+      const int chains = two || n > 1 ? 2 : 1;
       const int c = (warp - kSoftmaxWarp) >> 3;           // chain
       const int half = ((warp - kSoftmaxWarp) >> 2) & 1;  // which 64 keys of a tile, and columns of O
       const int rt = two ? c : 0;                         // its row tile
@@ -1002,11 +1025,18 @@ shared_attn_kernel(const Attn p, const __grid_constant__ CUtensorMap map_k1,
           tmem_ld32(tO + q * 32, o);
           tmem_wait_ld(o);
           if (joined) {
+            // (chain 1's O holds something for every row that it has a reference for)
+            const float *theirs = stage + q * 32 * kBM + rl;
+            if (__all_sync(0xffffffffu, f1 != 0.f)) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              o[i] = __float_as_uint(__uint_as_float(o[i]) * f0);
-              if (f1 != 0.f)
-                o[i] = __float_as_uint(fmaf(f1, stage[(q * 32 + i) * kBM + rl], __uint_as_float(o[i])));
+              for (int i = 0; i < 32; ++i)
+                o[i] = __float_as_uint(fmaf(f1, theirs[i * kBM], __uint_as_float(o[i]) * f0));
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                const float y = theirs[i * kBM];
+                o[i] = __float_as_uint(fmaf(f1, f1 != 0.f ? y : 0.f, __uint_as_float(o[i]) * f0));
+              }
             }
           }
           const float *v = reinterpret_cast<const float *>(o);
@@ -1029,10 +1059,10 @@ shared_attn_kernel(const Attn p, const __grid_constant__ CUtensorMap map_k1,
         }
       }
       fence_proxy_async_smem();  // (the next segment's tiles come over what was staged)
+      __syncwarp();
     }
-    __syncwarp();
+    if (lane == 0) bulk_wait();  // (the partial rows are written)
   }
-  if (warp >= kSoftmaxWarp && lane == 0) bulk_wait();  // (the partial rows are written)
   // (the last begin_segment ended with a barrier)
   if (warp == 1) tmem_dealloc(tmem, kTmemCols);
   if (tid == 0 && p.status && sh.abort) atomicOr(p.status, TSD_STATUS_TIMEOUT);
@@ -1199,6 +1229,17 @@ int check(int B, int N_max, int Hq, int Hkv, int D, int G) {
   return TSD_OK;
 }
 
+// The register split draws on what the block was launched with: a build that gives a
+// thread fewer registers must not run (it would wait forever).
+template <int D>
+bool ready() {
+  static const bool enough = [] {
+    cudaFuncAttributes a;
+    return cudaFuncGetAttributes(&a, shared_attn_kernel<D>) == cudaSuccess && a.numRegs >= kRegsLaunch;
+  }();
+  return enough && set_smem((const void *)shared_attn_kernel<D>, Layout<D>::kAlloc);
+}
+
 template <int D>
 int launch_all(const Attn &p, cudaStream_t s) {
   CUtensorMap k1, k8, v1, v8;
@@ -1207,7 +1248,7 @@ int launch_all(const Attn &p, cudaStream_t s) {
       !make_cache_map(&v1, p.v, p.num_blocks, p.Hkv, D, 1) ||
       !make_cache_map(&v8, p.v, p.num_blocks, p.Hkv, D, kTilePages))
     return TSD_ERR_CUDA;
-  if (!set_smem((const void *)shared_attn_kernel<D>, Layout<D>::kAlloc)) return TSD_ERR_CUDA;
+  if (!ready<D>()) return TSD_ERR_CUDA;
   const int threads = p.B <= 256 ? 256 : kPlanThreads;
   if (launch(shared_plan_kernel, dim3(1), dim3(threads), 0, s, p) != cudaSuccess) return TSD_ERR_CUDA;
   if (launch(shared_attn_kernel<D>, dim3(p.blocks), dim3(kThreads), Layout<D>::kAlloc, s, p, k1, k8, v1, v8) != cudaSuccess)
