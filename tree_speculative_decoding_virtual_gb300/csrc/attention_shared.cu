@@ -24,12 +24,13 @@
 //   warp 3       tells it when V is there, after clearing what no row may see
 //   warps 4-11   softmax of chain 0, warps 12-19 of chain 1: one TMEM lane (= one
 //                query row) per thread, two threads a row (64 keys each)
-// A chain is a row tile of 128 rows with its S (128 columns of TMEM; P, bf16, goes over
-// the first 64) and O.  With more than 128 rows the chains are two row tiles
+// A chain is a row tile of 128 rows with its S (128 columns of TMEM; each thread's P, bf16,
+// goes over the first half of its own scores, so that nothing but the reference ties
+// the two threads of a row together) and O.  With more than 128 rows the chains are two row tiles
 // that share every key tile; with fewer, chain c takes the key tiles j = c mod 2 of the
 // same rows and the two are joined at the end.
 //   S = Q K^T         M = 128, N = 128, bf16 in, fp32 accumulate
-//   P = exp2(S c - m) bf16, over the first half of S
+//   P = exp2(S c - m) bf16, over S
 //   O += P V          A from TMEM, V MN-major
 // The MMAs of a chain execute in issue order, S_{j+1} right behind P_j V_j, so the softmax
 // that sees S_j complete may rescale O and overwrite S_j.  A row's reference m is the
@@ -405,7 +406,7 @@ struct Shared {
   float2 ml[kBM];           // chain 1's (reference, sum) when it shares chain 0's rows
   float half[2][2][kBM];    // by chain, thread of the row, row: exchange between the two
   uint8_t asks[2][2][kBM];  // likewise
-  int stop[2][2];           // by chain and tile parity: a wait ran out
+  int stop[8][2];           // by pair of warps and tile parity: a wait ran out
   uint32_t poison[kMaxNodes / 32];  // tree nodes whose V has a NaN or an infinity
   int poisoned;
   uint32_t tmem_base;
@@ -471,19 +472,24 @@ __device__ __forceinline__ void regs_up() {
 constexpr int kRegsLaunch = 96, kRegsIssue = 64, kRegsSoftmax = 104;
 static_assert(kRegsIssue + 4 * kRegsSoftmax <= 5 * kRegsLaunch, "what the block was launched with");
 
-// Barrier of a chain's 256 softmax threads; returns whether any passed true.
-__device__ __forceinline__ bool chain_any(int c, bool x) {
+// Barrier of the two warps that share a chain's quarter of 32 rows; returns whether any
+// thread passed true.
+__device__ __forceinline__ bool pair_any(int pair, bool x) {
   uint32_t r;
   asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, 256, p;\n"
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, 64, p;\n"
       " selp.u32 %0, 1, 0, q;\n}\n"
       : "=r"(r)
-      : "r"((uint32_t)x), "r"(2 + c)
+      : "r"((uint32_t)x), "r"(1 + pair)
       : "memory");
   return r != 0;
 }
-__device__ __forceinline__ void chain_sync(int c) {
-  asm volatile("barrier.cta.sync %0, 256;\n" ::"r"(2 + c) : "memory");
+__device__ __forceinline__ void pair_sync(int pair) {
+  asm volatile("barrier.cta.sync %0, 64;\n" ::"r"(1 + pair) : "memory");
+}
+// Barrier of the four warps of both chains' same quarter.
+__device__ __forceinline__ void quarter_sync(int quarter) {
+  asm volatile("barrier.cta.sync %0, 128;\n" ::"r"(9 + quarter) : "memory");
 }
 __device__ __forceinline__ void mbar_inval(uint32_t bar) {
   asm volatile("mbarrier.inval.shared::cta.b64 [%0];\n" ::"r"(bar) : "memory");
@@ -615,7 +621,7 @@ shared_attn_kernel(const Attn p, const __grid_constant__ CUtensorMap map_k1,
     tma_prefetch_desc(&map_v8);
     sh.abort = 0;
     sh.bad = 0;
-    for (int i = 0; i < 4; ++i) sh.stop[i >> 1][i & 1] = 0;
+    for (int i = 0; i < 16; ++i) sh.stop[i >> 1][i & 1] = 0;
   }
   if (warp == 1) tmem_alloc(smem_addr(&sh.tmem_base), kTmemCols);
   pdl_wait();
@@ -701,7 +707,10 @@ shared_attn_kernel(const Attn p, const __grid_constant__ CUtensorMap map_k1,
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk) v8[kk] = desc_add(vd, kk * 16 * 128);
           tc_fence_after();
-          umma8_ts(tmem + c * kTmemChain + kTmemO, tmem + c * kTmemChain, v8, idPV, accum ? 1u : 0u);
+          // (P of keys 0 .. 63 and 64 .. 127 lies over the first half of their scores each)
+          const uint64_t va[4] = {v8[0], v8[1], v8[2], v8[3]}, vb[4] = {v8[4], v8[5], v8[6], v8[7]};
+          umma4_ts(tmem + c * kTmemChain + kTmemO, tmem + c * kTmemChain, va, idPV, accum ? 1u : 0u);
+          umma4_ts(tmem + c * kTmemChain + kTmemO, tmem + c * kTmemChain + 64, vb, idPV, 1u);
           if (final) umma_commit(smem_addr(&sh.o_final[c]));
         };
         bool ok = !p.test_stall || tc_wait(sh.never, 0, lim, abort);
@@ -783,7 +792,7 @@ shared_attn_kernel(const Attn p, const __grid_constant__ CUtensorMap map_k1,
       const int c = (warp - kSoftmaxWarp) >> 3;           // chain
       const int half = ((warp - kSoftmaxWarp) >> 2) & 1;  // which 64 keys of a tile, and columns of O
       const int rt = two ? c : 0;                         // its row tile
-      const int quarter = warp & 3;
+      const int quarter = warp & 3, pair = c * 4 + quarter;
       const int rl = quarter * 32 + lane;                 // row within the tile
       const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
       const uint32_t tS = tmem + c * kTmemChain + lane_off, tO = tS + kTmemO;
@@ -822,13 +831,8 @@ shared_attn_kernel(const Attn p, const __grid_constant__ CUtensorMap map_k1,
       const int slot0 = sg.page * kPage + half * 64, lo = sg.lo, tree_from = sg.P - 64;
       auto visible = [&](int s0) { return rvalid ? visible32(p, sg, node, s0) : 0xFFFFFFFFu; };
       for (int j = two ? 0 : c; ok && j < n; j += two ? 1 : 2, ++u) {
-        // one warp looks at the barrier, the others wait for it without polling
-        bool got = true;
-        if (((warp - kSoftmaxWarp) & 7) == 0) {
-          got = __all_sync(0xffffffffu, tc_wait(sh.s_full[c], u & 1, lim, abort));
-          if (!got) sh.stop[c][u & 1] = 1;
-        }
-        chain_sync(c);
+        const bool got = __all_sync(0xffffffffu, tc_wait(sh.s_full[c], u & 1, lim, abort));
+        if (!got) sh.stop[pair][u & 1] = 1;
         tc_fence_after();
         if ((two ? c == 1 : true) && half == 0 && quarter == 0 && lane == 0) {
           // A commit follows every earlier MMA of its thread, so K_j and the V tile
@@ -862,7 +866,7 @@ shared_attn_kernel(const Attn p, const __grid_constant__ CUtensorMap map_k1,
 #pragma unroll
             for (int i = 0; i < 32; ++i) m = fmax3(m, __uint_as_float(x[0][i]), __uint_as_float(x[1][i]));
             sh.half[c][half][rl] = m;
-            chain_sync(c);
+            pair_sync(pair);
             m = __fmul_rn(fmaxf(sh.half[c][0][rl], sh.half[c][1][rl]), mul);
             if (m > -INFINITY) {
               ref = m;
@@ -882,18 +886,13 @@ shared_attn_kernel(const Attn p, const __grid_constant__ CUtensorMap map_k1,
               else acc0 = f2_add(acc0, f2_pack(e0, e1));
             }
           }
-        } else if (u == 0) {
-          chain_sync(c);
         }
         const float2 acc = f2_unpack(f2_add(acc0, acc1));
         float sum = acc.x + acc.y;
         // Rows that need more than that: no reference yet, or P out of range.
         const bool mine = live && ((unset && (!edge || seen != 0u)) || !(sum <= kMaxSum));
-        tc_fence_before();
-        const bool any = chain_any(c, mine || !got);
-        tc_fence_after();
-        if (__builtin_expect(any, 0)) {
-          if (sh.stop[c][u & 1]) {  // the same for every warp of the chain
+        if (__builtin_expect(pair_any(pair, mine || !got), 0)) {
+          if (sh.stop[pair][u & 1]) {  // the same for both warps
             ok = false;
             break;
           }
@@ -912,7 +911,7 @@ shared_attn_kernel(const Attn p, const __grid_constant__ CUtensorMap map_k1,
             sh.half[c][half][rl] = m;
             sh.asks[c][half][rl] = mine;
           }
-          chain_sync(c);
+          pair_sync(pair);
           if (live) {
             const bool row_asks = mine || sh.asks[c][half ^ 1][rl];
             m = fmaxf(m, sh.half[c][half ^ 1][rl]);
@@ -955,13 +954,10 @@ shared_attn_kernel(const Attn p, const __grid_constant__ CUtensorMap map_k1,
               }
             }
           }
-          tc_fence_before();
-          chain_sync(c);  // S has been read again
-          tc_fence_after();
         }
         if (live) {
           l += sum;
-          tmem_st32(tS + half * 32, pk);
+          tmem_st32(tS + half * 64, pk);  // (over its own scores)
           tmem_wait_st();
         }
         tc_fence_before();
@@ -976,8 +972,9 @@ shared_attn_kernel(const Attn p, const __grid_constant__ CUtensorMap map_k1,
       // still read)
       if (ok && chains == 2) ok = __all_sync(0xffffffffu, tc_wait(sh.o_final[c ^ 1], 0, lim, abort));
       tc_fence_after();
+      pair_sync(pair);  // (what was exchanged before has been read)
       sh.half[c][half][rl] = l;
-      chain_sync(c);
+      pair_sync(pair);
       l += sh.half[c][half ^ 1][rl];
       float M = unset ? -INFINITY : ref;
       if (unset && l != l) M = 0.f;  // only NaN scores so far
@@ -999,7 +996,7 @@ shared_attn_kernel(const Attn p, const __grid_constant__ CUtensorMap map_k1,
         }
         if (half == 0) sh.ml[rl] = make_float2(M, l);
       }
-      if (joined) asm volatile("barrier.cta.sync 1, 512;\n" ::: "memory");
+      if (joined) quarter_sync(quarter);
       if (c < (two ? 2 : 1)) {
         float f0 = 1.f, f1 = 0.f;
         if (joined) {
@@ -1048,8 +1045,8 @@ shared_attn_kernel(const Attn p, const __grid_constant__ CUtensorMap map_k1,
         }
         if (half == 0 && rvalid) p.part_ml[sg.part + rt * kBM + rl] = make_float2(M, sh.bad ? -1.f : l);
         fence_proxy_async_smem();
-        chain_sync(c);
-        const int w = (warp - kSoftmaxWarp) & 7;
+        pair_sync(pair);
+        const int w = quarter * 2 + half;
         // 16 partial rows a warp, in one piece and as they lie
         const int rows = min(kBM / 8, sg.rows - sg.row0 - rt * kBM - w * (kBM / 8));
         if (lane == 0 && !*abort && rows > 0) {
