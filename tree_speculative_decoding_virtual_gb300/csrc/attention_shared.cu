@@ -757,14 +757,15 @@ shared_attn_kernel(const Attn p, const __grid_constant__ CUtensorMap map_k1,
       // counts toward the phase that is open: the one before has to be complete.  Each
       // barrier's phases are waited for one after the other.) ----
       bool ok = true;
-      if (two) ok = tc_wait(sh.k_full[0], 0, lim, abort);
       for (int j = 0; j < n; ++j) {
         const int c = two ? 0 : j & 1, u = two ? j : j >> 1;  // chain, its tile
-        if (two && j + 1 < n) ok = ok && tc_wait(sh.k_full[(j + 1) & 1], ((j + 1) >> 1) & 1, lim, abort);
-        ok = ok && tc_wait(sh.v_full[j & 1], (j >> 1) & 1, lim, abort);
+        ok = tc_wait(sh.v_full[j & 1], (j >> 1) & 1, lim, abort);
         if (!__all_sync(0xffffffffu, ok)) break;
         clear_hidden<D>(sh, sg, gbase + L::kV + (j & 1) * L::kTile, j, lane);
         if (u > 0) ok = tc_wait(sh.p_full[c], (u - 1) & 1, lim, abort);
+        // (P_{j-1} is there, so S_{j-1} was, and K_{j-1}: the phase before this one of its
+        // barrier is complete.  K_{j+3} can not be there before this arrival.)
+        if (two && j + 1 < n) ok = ok && tc_wait(sh.k_full[(j + 1) & 1], ((j + 1) >> 1) & 1, lim, abort);
         if (!__all_sync(0xffffffffu, ok)) break;
         if (lane == 0) mbar_arrive(smem_addr(&sh.p_full[c]));
       }
