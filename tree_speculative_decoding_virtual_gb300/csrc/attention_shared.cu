@@ -71,7 +71,7 @@ constexpr int kMaxBatch = 1024;
 constexpr int kPlanThreads = 1024;
 constexpr int kPieces = 64;     // pieces of one key range at most
 // A unit's fixed cost in a row block of one or two row tiles, in key tiles of one.
-constexpr int kRangeCost1 = 12, kRangeCost2 = 22;
+constexpr int kRangeCost1 = 8, kRangeCost2 = 20;
 
 // One row set and its key range, for every kv head.
 struct Unit {
