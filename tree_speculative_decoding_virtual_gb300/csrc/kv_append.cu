@@ -15,10 +15,16 @@
 // position modulo one turn, which is exact but for the frequency's last bit; the
 // rest is a fraction of a turn in [-1/2, 1/2).
 //
-// Each byte is read and written once.  A block takes a few tokens: their cosines and
-// sines are computed once, into shared memory, and used by all heads; a lane then
-// holds two 16-byte chunks of a row that turn into each other (chunks l and l + R/16,
-// or with neighbouring pairs 2l and 2l + 1).
+// Each byte is read and written once, so memory bounds many tokens and the launch few.  A
+// block takes a few tokens: their cosines and sines are computed once, into shared memory,
+// and used by all heads; a lane then holds two 16-byte chunks of a row that turn into each
+// other (chunks l and l + R/16, or with neighbouring pairs 2l and 2l + 1), and the
+// arithmetic goes two columns to an instruction.  What holds the loads in flight is the
+// number of warps: 8 blocks of 128 threads and 4 tokens.  Measured at 32768 tokens of 64 +
+// 2 x 8 heads of 128 (1.34 GB moved): 248 us, 5.4 TB/s; blocks of 256 threads with 16 tokens
+// 261 us, with the loads of two steps on the way (and half the warps) 355 us, warps that
+// keep a token's cosines in registers 282 us.  One token of 32 + 2 x 8 heads: 4.6 us; 496
+// tokens of 32 + 2 x 8 heads into 4 bits 8.7 us.
 #include <cuda_bf16.h>
 
 #include "q4.cuh"
@@ -29,9 +35,9 @@
 namespace tsd {
 namespace {
 
-constexpr int kApThreads = 256;
+constexpr int kApThreads = 128;
 constexpr int kApWarps = kApThreads / 32;
-constexpr int kApTokens = 16;  // tokens of a block at most
+constexpr int kApTokens = 4;  // tokens of a block at most
 constexpr int kMaxAxes = 4;
 
 struct AppendArgs {
@@ -59,19 +65,28 @@ __device__ __forceinline__ uint64_t turns(float inv_freq) {
   return t < 1.0 ? __double2ull_rz(t * 18446744073709551616.0) : 0ull;
 }
 
-__device__ __forceinline__ void unpack8(uint4 x, float (&f)[8]) {
+// Two neighbouring columns in one 64-bit register, as the two-wide fp32 instructions take
+// them.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  return sm100::f2_pack(lo, hi);
+}
+__device__ __forceinline__ float lo_of(uint64_t x) { return __uint_as_float((uint32_t)x); }
+__device__ __forceinline__ float hi_of(uint64_t x) { return __uint_as_float((uint32_t)(x >> 32)); }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack8(uint4 x, uint64_t (&f)[4]) {
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(w[i] << 16);
-    f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
+  for (int i = 0; i < 4; ++i) f[i] = (uint64_t)(w[i] & 0xFFFF0000u) << 32 | w[i] << 16;
 }
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+__device__ __forceinline__ uint4 pack8(const uint64_t (&f)[4]) {
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo_of(f[i]), hi_of(f[i]));
     w[i] = *reinterpret_cast<const uint32_t *>(&h);
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
@@ -80,10 +95,11 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
 // Block (x, y): tokens [x * tokens, ...), warp steps [y * steps, ...) of each.  A
 // step is 32 / (D / 16) heads of the token's row q heads, k heads, v heads.
 template <int D, bool kQ4>
-__global__ void __launch_bounds__(kApThreads) kv_append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(kApThreads, 8) kv_append_kernel(const AppendArgs a) {
   constexpr int kLanes = D / 16;       // of one head's row
   constexpr int kHeads = 32 / kLanes;  // of one warp step
-  __shared__ alignas(16) float2 cs[kApTokens][D / 2];
+  // of frequencies 8 l + 2 i and the next, at [i][l]: both cosines, then both sines
+  __shared__ float4 cs[kApTokens][4][kLanes];
   __shared__ uint4 weight[2][D / 8];
   __shared__ int slot_of[kApTokens];
   pdl_wait();
@@ -95,24 +111,15 @@ __global__ void __launch_bounds__(kApThreads) kv_append_kernel(const AppendArgs 
   const int per = min(a.steps, (heads + kHeads - 1) / kHeads - s0);  // steps of a token here
   const int l = lane % kLanes, hl = lane / kLanes;
 
-  // where step `x` of this block's nt * per lies: its lane's source, or null
+  // The block's steps go round its warps, a token's after the other's.
+  // a warp's next step: its lane's source, or null, and the two chunks there
   struct Item {
     const uint16_t *src;
+    uint4 x, y;
     int tok, h;  // h: head of the row q | k | v
   };
-  auto item = [&](int tok, int s) {
-    Item it;
-    it.tok = tok;
-    it.h = (s0 + s) * kHeads + hl;
-    it.src = nullptr;
-    if (tok < nt && it.h < heads) {
-      const int64_t t = t0 + tok;
-      it.src = it.h < a.Hq             ? a.q + t * a.q_stride + (int64_t)it.h * D
-               : it.h < a.Hq + a.Hkv ? a.k + t * a.k_stride + (int64_t)(it.h - a.Hq) * D
-                                     : a.v + t * a.v_stride + (int64_t)(it.h - a.Hq - a.Hkv) * D;
-    }
-    return it;
-  };
+  const int step_t = kApWarps / per, step_s = kApWarps % per;
+  int tok = warp / per, s = warp % per;
   // A rotated lane's two chunks, and those of a lane that only copies.
   const int half = a.interleaved ? 0 : a.R / 16;  // lanes whose chunks are half a rotation apart
   auto chunks = [&](int h, int &c0, int &c1) {
@@ -121,39 +128,50 @@ __global__ void __launch_bounds__(kApThreads) kv_append_kernel(const AppendArgs 
     c1 = apart ? l + half : 2 * l + 1;
     return apart;
   };
-  auto load = [&](const Item &it, uint4 &x, uint4 &y) {
-    x = y = make_uint4(0u, 0u, 0u, 0u);
-    if (it.src) {
+  auto fetch = [&](Item &it) {
+    it.tok = tok;
+    it.h = (s0 + s) * kHeads + hl;
+    it.src = nullptr;
+    it.x = it.y = make_uint4(0u, 0u, 0u, 0u);
+    if (tok < nt && it.h < heads) {
+      const int64_t t = t0 + tok;
+      it.src = it.h < a.Hq           ? a.q + t * a.q_stride + (int64_t)it.h * D
+               : it.h < a.Hq + a.Hkv ? a.k + t * a.k_stride + (int64_t)(it.h - a.Hq) * D
+                                     : a.v + t * a.v_stride + (int64_t)(it.h - a.Hq - a.Hkv) * D;
       int c0, c1;
       chunks(it.h, c0, c1);
-      x = __ldcs(reinterpret_cast<const uint4 *>(it.src) + c0);
-      y = __ldcs(reinterpret_cast<const uint4 *>(it.src) + c1);
+      it.x = __ldcs(reinterpret_cast<const uint4 *>(it.src) + c0);
+      it.y = __ldcs(reinterpret_cast<const uint4 *>(it.src) + c1);
+    }
+    tok += step_t;
+    s += step_s;
+    if (s >= per) {
+      s -= per;
+      ++tok;
     }
   };
-
-  const int step_t = kApWarps / per, step_s = kApWarps % per;
-  int tok = warp / per, s = warp % per;
-  Item it = item(tok, s);
-  uint4 x, y;
-  load(it, x, y);  // on the way while the angles are computed
+  Item it;  // on the way while the angles are computed, and while the step before is worked on
+  fetch(it);
 
   {
     int lanes = 1;  // threads of one token's angles: a power of two
     while (lanes < a.R / 2) lanes *= 2;
     const int j = tid & (lanes - 1);
     if (j < a.R / 2) {
-      const uint64_t turn = turns(a.inv_freq[j]);
+      const uint64_t freq = turns(a.inv_freq[j]);
       const int ax = a.freq_axis ? a.freq_axis[j] : 0;
       const int64_t off = ax > 0 && ax < a.axes ? ax * a.T : 0;
       for (int i = tid / lanes; i < nt; i += kApThreads / lanes) {
         const int64_t t = t0 + i;
         int64_t p = a.pos ? a.pos[off + t] : t % a.per_base;
         if (a.base) p += a.base[t / a.per_base];
-        const uint64_t frac = turn * (uint64_t)p;
+        const uint64_t frac = freq * (uint64_t)p;
         const float z = (float)(int32_t)((frac + 0x80000000ull) >> 32) * 0x1p-31f;
         float sn, cn;
         sincospif(z, &sn, &cn);
-        cs[i][j] = make_float2(cn * a.rot_scale, sn * a.rot_scale);
+        float *at = reinterpret_cast<float *>(&cs[i][(j & 7) >> 1][j >> 3]) + (j & 1);
+        at[0] = cn * a.rot_scale;
+        at[2] = sn * a.rot_scale;
       }
     }
     if (tid < D / 8 && a.q_weight) weight[0][tid] = reinterpret_cast<const uint4 *>(a.q_weight)[tid];
@@ -169,61 +187,56 @@ __global__ void __launch_bounds__(kApThreads) kv_append_kernel(const AppendArgs 
   }
   __syncthreads();
 
-  while (tok < nt) {  // (the same for the whole warp)
+  while (it.tok < nt) {  // (the same for the whole warp)
     const Item now = it;
-    uint4 cx = x, cy = y;
-    tok += step_t;
-    s += step_s;
-    if (s >= per) {
-      s -= per;
-      ++tok;
-    }
-    it = item(tok, s);
-    load(it, x, y);
-
+    fetch(it);
+    uint4 cx = now.x, cy = now.y;
     const bool is_q = now.h < a.Hq, is_v = now.h >= a.Hq + a.Hkv;
     int c0, c1;
     const bool apart = chunks(now.h, c0, c1);
     const uint16_t *w = is_q ? a.q_weight : a.k_weight;
     const bool normed = w && !is_v, turned = !is_v && l < a.R / 16;
     if (__any_sync(0xffffffffu, normed || turned)) {
-      float f[8], g[8];
+      uint64_t f[4], g[4];
       unpack8(cx, f);
       unpack8(cy, g);
-      float ss = 0.f;
+      if (__any_sync(0xffffffffu, normed)) {
+        uint64_t sum = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) ss += f[i] * f[i] + g[i] * g[i];
+        for (int i = 0; i < 4; ++i) sum = sm100::f2_fma(g[i], g[i], sm100::f2_fma(f[i], f[i], sum));
+        float ss = lo_of(sum) + hi_of(sum);
 #pragma unroll
-      for (int off = kLanes / 2; off; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-      if (normed) {
-        const float r = rsqrtf(ss * (1.f / D) + a.eps);
-        float wf[8], wg[8];
-        unpack8(weight[is_q ? 0 : 1][c0], wf);
-        unpack8(weight[is_q ? 0 : 1][c1], wg);
+        for (int off = kLanes / 2; off; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+        if (normed) {
+          const float r = rsqrtf(ss * (1.f / D) + a.eps);
+          const uint64_t r2 = pair(r, r);
+          uint64_t wf[4], wg[4];
+          unpack8(weight[is_q ? 0 : 1][c0], wf);
+          unpack8(weight[is_q ? 0 : 1][c1], wg);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          f[i] *= r * wf[i];
-          g[i] *= r * wg[i];
+          for (int i = 0; i < 4; ++i) {
+            f[i] = mul2(f[i], mul2(r2, wf[i]));
+            g[i] = mul2(g[i], mul2(r2, wg[i]));
+          }
         }
       }
       if (turned) {
-        const float4 *at = reinterpret_cast<const float4 *>(&cs[now.tok][l * 8]);
+        if (apart) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {  // frequencies 8 l + 2 i and the next
-          const float4 r = at[i];
-          if (apart) {
-            const float f0 = f[2 * i], f1 = f[2 * i + 1], g0 = g[2 * i], g1 = g[2 * i + 1];
-            f[2 * i] = f0 * r.x - g0 * r.y;
-            g[2 * i] = g0 * r.x + f0 * r.y;
-            f[2 * i + 1] = f1 * r.z - g1 * r.w;
-            g[2 * i + 1] = g1 * r.z + f1 * r.w;
-          } else {
-            float *e = i < 2 ? f + 4 * i : g + 4 * (i - 2);
-            const float e0 = e[0], e1 = e[1], e2 = e[2], e3 = e[3];
-            e[0] = e0 * r.x - e1 * r.y;
-            e[1] = e1 * r.x + e0 * r.y;
-            e[2] = e2 * r.z - e3 * r.w;
-            e[3] = e3 * r.z + e2 * r.w;
+          for (int i = 0; i < 4; ++i) {
+            const float4 r = cs[now.tok][i][l];
+            const uint64_t c = pair(r.x, r.y), sn = pair(r.z, r.w), x = f[i];
+            f[i] = sm100::f2_fma(x, c, mul2(g[i], sn ^ 0x8000000080000000ull));
+            g[i] = sm100::f2_fma(g[i], c, mul2(x, sn));
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {  // frequency 8 l + i turns one pair
+            uint64_t &e = i < 4 ? f[i & 3] : g[i & 3];
+            const float4 r = cs[now.tok][i / 2][l];
+            const float c = i & 1 ? r.y : r.x, sn = i & 1 ? r.w : r.z;
+            const float e0 = lo_of(e), e1 = hi_of(e);
+            e = pair(e0 * c - e1 * sn, e1 * c + e0 * sn);
           }
         }
       }
@@ -279,7 +292,7 @@ cudaError_t append_launch(AppendArgs &a, cudaStream_t s) {
   const int steps = (a.Hq + 2 * a.Hkv + kHeads - 1) / kHeads;
   // Enough blocks for every SM: few tokens are shared out by heads, many go up to
   // kApTokens a block.
-  const int64_t want = 4ll * sm_count();
+  const int64_t want = 8ll * sm_count();
   const int64_t tokens = a.T / want;
   a.tokens = (int)(tokens < 1 ? 1 : tokens > kApTokens ? kApTokens : tokens);
   const int64_t blocks = (a.T + a.tokens - 1) / a.tokens;
