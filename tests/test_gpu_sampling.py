@@ -234,3 +234,48 @@ def test_replayed_with_other_settings(tsd):
     g.replay()
     want, want_lp = tsd.token_sample(x, u, temperature=t, top_k=k)
     assert torch.equal(tokens, want) and torch.equal(lp, want_lp)
+
+
+@pytest.mark.parametrize("V,R,bf16", [(900, 700, False), (8000, 508, False), (32000, 64, True), (32000, 300, False),
+                                      (32000, 1300, True), (128256, 60, True), (128256, 160, True), (128256, 60, False)])
+def test_many_rows_are_as_each_alone(tsd, V, R, bf16):
+    """How many CTAs share a row depends on how many rows there are; the results do not:
+    sums are exact."""
+    import torch
+    rng = np.random.default_rng(V + R)
+    some = rows_of(rng, 12, V, "peaked")
+    x = T(some)[torch.arange(R, device="cuda") % 12]
+    x = x + 0.25 * torch.randint(0, 5, (R, 1), device="cuda") + torch.arange(V, device="cuda") % 7 * 0.125
+    if bf16:
+        x = x.bfloat16()
+    t, k, p, m = [T(np.array([SETTINGS[r % len(SETTINGS)][i] for r in range(R)], np.int32 if i == 1 else np.float32))
+                  for i in range(4)]
+    u = T(rng.random((R, 3)).astype(np.float32))
+    tokens, lp = tsd.token_sample(x, u, temperature=t, top_k=k, top_p=p, min_p=m)
+    rows = tsd.logits_filter(x, temperature=t, top_k=k, top_p=p, min_p=m)
+    probs = tsd.logits_filter(x, temperature=t, top_k=k, top_p=p, min_p=m, probs=True)
+    for r in list(range(0, R, max(1, R // 40))) + [R - 1]:
+        one = dict(temperature=t[r:r + 1], top_k=k[r:r + 1], top_p=p[r:r + 1], min_p=m[r:r + 1])
+        alone, alone_lp = tsd.token_sample(x[r:r + 1], u[r:r + 1], **one)
+        assert torch.equal(tokens[r:r + 1], alone) and torch.equal(lp[r:r + 1], alone_lp), r
+        assert torch.equal(rows[r:r + 1], tsd.logits_filter(x[r:r + 1], **one)), r
+        assert torch.equal(probs[r:r + 1], tsd.logits_filter(x[r:r + 1], probs=True, **one)), r
+
+
+def test_two_streams_at_once(tsd):
+    import torch
+    rng = np.random.default_rng(21)
+    x = [T(rows_of(rng, 40, 32000, "peaked")), T(rows_of(rng, 40, 32000, "plain"))]
+    u = T(rng.random((40, 2)).astype(np.float32))
+    k, p = T(np.full(40, 40, np.int32)), T(np.full(40, 0.9, np.float32))
+    want = [tsd.token_sample(x[0], u, top_k=k), tsd.token_sample(x[1], u, top_p=p)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [None, None]
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i] = tsd.token_sample(x[i], u, **(dict(top_p=p) if i else dict(top_k=k)))
+        torch.cuda.synchronize()
+        for i in range(2):
+            assert torch.equal(got[i][0], want[i][0]) and torch.equal(got[i][1], want[i][1])

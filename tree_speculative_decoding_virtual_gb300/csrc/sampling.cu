@@ -16,18 +16,27 @@
 // A border that a sum decides moves with the sum's rounding, so weights are fp32 and
 // their sums exact: fixed point of 2^-43, which no order of additions changes.
 //
-// One cluster of up to 8 CTAs a row; the row is read once and stays in shared memory,
-// each warp with a run of consecutive ids.  A filter's border is found by
-//   histogram  1024 bins of (m - x) / T, 32 a unit: counts for top-k, and for top-p
-//              weights relative to the bin's (13 bits a weight: good to 1e-4) besides the
-//              exact sum of all; the first CTA adds up the cluster's and finds the bin, or
-//              the few bins, that must hold the border
-//   list       what lies in them (a handful to some hundred) goes to the first CTA, with
-//              the exact weight above them, and is ranked there
+// A cluster of up to 8 CTAs takes row after row; a row is read once and stays in shared
+// memory, each warp with a run of consecutive ids, and the next row's copies start as soon
+// as a lane is through with this one's.  A filter's border is found by
+//   histogram  2048 bins: for top-k counts of m - x, 32 bins a unit; for top-p weights of
+//              (m - x) / T, 64 a unit, relative to the bin's (13 bits a weight: good to
+//              1e-4) besides the exact sum of all; the first CTA adds up the cluster's by
+//              groups of 32 bins, then the bins of two groups, and finds the bin, or the few
+//              bins, that must hold the border
+//   list       what lies in them (a handful to 512) goes to the first CTA, with the exact
+//              weight above them, and is ranked there (up to 32 by one warp)
 // When what lies in those bins and above fits the list (ordinary settings of top-k and
 // top-p), the first CTA has all that can be kept, and finishes alone: both filters, min-p
-// and the draws.  Bins that hold more than the list are cut into 1024 again; where that does
+// and the draws.  Bins that hold more than the list are cut into 2048 again; where that does
 // not part them either (hundreds of equal logits), the border is found bit by bit.
+//
+// What bounds it is not the one read of the row (the floor of 508 rows of 128256 fp32 logits
+// is 38 us) but some 25 instructions a logit for the histogram (10k cycles of a row's 42k
+// with 8 CTAs) and the chain of exchanges in the cluster: three barriers of 3k cycles, bins
+// 5k, list 5k, the first CTA's end 5k.  CTAs exchange by loads of what each left in its own
+// shared memory: adds from eight CTAs to one place took 6k to 14k cycles.  Measured: one row
+// 14 us, 508 rows 305 us where lists settle it.
 #include <cuda_bf16.h>
 
 #include <cmath>
@@ -45,6 +54,7 @@ constexpr int kSpWarps = kSpThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kMaxVocab = 262144;
 constexpr int kMaxDraws = 64;
+constexpr int kMaxRowBytes = kMaxVocab / kMaxCluster * 4;  // of a CTA's share
 constexpr int kBins = 2048;
 constexpr int kGroup = 32, kGroups = kBins / kGroup;  // bins are looked for by groups of 32 first
 constexpr int kList = 512, kSmallList = 32;
@@ -1290,56 +1300,81 @@ __global__ void __launch_bounds__(kSpThreads, 3) sampling_kernel(const SpArgs a)
   }
 }
 
-// How many clusters of this launch fit the device (asked once for each shape).
-int clusters_at_once(const void *kernel, const cudaLaunchConfig_t &cfg) {
-  struct Entry {
-    const void *fn;
-    int dev, cluster;
-    size_t smem;
-    int n;
-  };
+// A row's logits on c CTAs: of a warp, and the bytes of a CTA.
+template <bool kBf16>
+void sp_share(int V, int c, int &per_warp, size_t &smem) {
+  constexpr int kStep = 32 * SpVec<kBf16>::kN;
+  per_warp = ((V + c * kSpWarps - 1) / (c * kSpWarps) + kStep - 1) / kStep * kStep;
+  smem = (size_t)per_warp * kSpWarps * (kBf16 ? 2 : 4);
+}
+
+// How many clusters of c CTAs run at once, by c (asked once for each kernel, device and
+// vocabulary; 0: too much shared memory).
+struct Fits {
+  const void *fn;
+  int dev, V;
+  int n[kMaxCluster + 1];
+};
+template <bool kBf16>
+Fits clusters_at_once(const void *kernel, int V, cudaLaunchConfig_t cfg) {
   static std::mutex mu;
-  static Entry known[64];
-  static int used = 0;
-  const int cluster = (int)cfg.gridDim.x;
+  static Fits known[32];
+  static unsigned used = 0;
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 1;
+  if (cudaGetDevice(&dev) != cudaSuccess) dev = -1;
   std::lock_guard<std::mutex> lock(mu);
-  for (int i = 0; i < used; ++i)
-    if (known[i].fn == kernel && known[i].dev == dev && known[i].cluster == cluster && known[i].smem == cfg.dynamicSmemBytes)
-      return known[i].n;
-  int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) n = sm_count() / cluster + 1;
-  if (used < 64) known[used++] = Entry{kernel, dev, cluster, cfg.dynamicSmemBytes, n};
-  return n;
+  for (const Fits &k : known)
+    if (k.fn == kernel && k.dev == dev && k.V == V) return k;
+  Fits f = {kernel, dev, V, {}};
+  for (int c = 1; c <= kMaxCluster; ++c) {
+    int per_warp;
+    sp_share<kBf16>(V, c, per_warp, cfg.dynamicSmemBytes);
+    if (cfg.dynamicSmemBytes > kMaxRowBytes) continue;
+    cfg.attrs[0].val.clusterDim.x = c;
+    cfg.gridDim = dim3((unsigned)c);
+    if (cudaOccupancyMaxActiveClusters(&f.n[c], kernel, &cfg) != cudaSuccess || f.n[c] < 1) f.n[c] = sm_count() / c + 1;
+  }
+  return known[used++ % 32] = f;
 }
 
 template <bool kBf16, int kMode>
 cudaError_t sp_launch(SpArgs &a, cudaStream_t s) {
-  constexpr int kN = kBf16 ? 8 : 4, kStep = 32 * kN;
-  int c = 1;
-  while (c < kMaxCluster && (int64_t)c * kSpWarps * kStep < a.V) c *= 2;
-  a.per_warp = ((a.V + c * kSpWarps - 1) / (c * kSpWarps) + kStep - 1) / kStep * kStep;
-  const size_t smem = (size_t)a.per_warp * kSpWarps * (kBf16 ? 2 : 4);
-  if (!set_smem((const void *)sampling_kernel<kBf16, kMode>, kMaxVocab / kMaxCluster * (kBf16 ? 2 : 4)))
-    return cudaErrorUnknown;
+  if (!set_smem((const void *)sampling_kernel<kBf16, kMode>, kMaxRowBytes)) return cudaErrorUnknown;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(kSpThreads);
-  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = c;
+  attr[0].val.clusterDim.x = 1;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.gridDim = dim3((unsigned)c);
   cfg.numAttrs = 1;
-  // as many clusters as run at once; each takes row after row
-  const int most = clusters_at_once((const void *)sampling_kernel<kBf16, kMode>, cfg);
-  cfg.gridDim = dim3((unsigned)(a.R < most ? a.R : most) * c);
+  const Fits fits = clusters_at_once<kBf16>((const void *)sampling_kernel<kBf16, kMode>, a.V, cfg);
+  // As many clusters as run at once, each taking row after row.  A row costs some 20 us and
+  // 1.4 us for each 1000 logits of a CTA (fitted to clusters of 1 to 8 CTAs over 8000 to
+  // 262144 logits, 20 to 2000 rows; every choice below is the fastest measured or within 3%
+  // of it): few rows are spread over as many CTAs as can be, of many rows those CTAs stay
+  // together that let the SMs fill up.  64 rows of 128256 bf16 logits: 8 CTAs a row 60 us,
+  // 6 42 us; 508 rows: 8 CTAs 449 us, 4 343 us; 508 rows of 8000 fp32: 8 CTAs 214 us, 1 68 us.
+  int most = 1;
+  while (most < kMaxCluster && most * kSpWarps * 32 * SpVec<kBf16>::kN < a.V) ++most;
+  int best = 0;
+  int64_t least = 0;
+  for (int c = most; c >= 1; --c) {
+    if (fits.n[c] < 1) continue;
+    const int64_t cost = (int64_t)((a.R + fits.n[c] - 1) / fits.n[c]) * (a.V / c + 14000);
+    if (best == 0 || cost < least) {
+      best = c;
+      least = cost;
+    }
+  }
+  if (best == 0) return cudaErrorUnknown;  // (kMaxCluster CTAs hold kMaxVocab logits)
+  sp_share<kBf16>(a.V, best, a.per_warp, cfg.dynamicSmemBytes);
+  attr[0].val.clusterDim.x = best;
+  cfg.gridDim = dim3((unsigned)(a.R < fits.n[best] ? a.R : fits.n[best]) * best);
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, sampling_kernel<kBf16, kMode>, a);
 }
