@@ -442,15 +442,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_q4_tc_kernel(const Q4
       // that is open: the one before has to be complete.  With one row tile the
       // decoders arrive there themselves, see there.) ----
       if (lane == 0) {
-        // Each barrier's phases are waited for one after the other (a wait for a
-        // phase whose predecessor is still open returns at once): the first K tile
-        // too, which the issuing thread waits for itself.
-        tc_wait(sh.k_full[0], 0, lim, abort);
+        // A wait takes the phase before the one meant for it, or the one behind it, for the
+        // wrong one: P_{j-1} is there, so S_{j-1} was, and K_{j-1}; and K_{j+3} can not be
+        // there before this arrival.
         for (int j = 0; j < n; ++j) {
           const int k = j + 1;
-          bool ok = k >= n || tc_wait(sh.k_full[k & 1], (k >> 1) & 1, lim, abort);
-          if (ok) ok = tc_wait(sh.v_full[j & 1], (j >> 1) & 1, lim, abort);
+          bool ok = tc_wait(sh.v_full[j & 1], (j >> 1) & 1, lim, abort);
           if (ok && j > 0) ok = tc_wait(sh.p_full[0], (j - 1) & 1, lim, abort);
+          if (ok && k < n) ok = tc_wait(sh.k_full[k & 1], (k >> 1) & 1, lim, abort);
           if (!ok) break;
           mbar_arrive(smem_addr(&sh.p_full[0]));
         }

@@ -42,6 +42,16 @@
 // written) are set to zero in shared memory, and so is a tree node's with a NaN or an
 // infinity, for it may be hidden from some rows; the rows that do see it become NaN.
 //
+// What bounds it, and what it measured.  Long shared ranges with many rows: the two chains'
+// MMAs and softmaxes (3500 cycles for a tile of 256 rows; 8 trees of 127 nodes, 64 heads,
+// 32768 shared slots: 746 us, 1.5 PFLOP/s; a register split 104 / 64 and not 96 for all
+// warps 850 -> 803, a row's threads tied by a barrier of two warps 803 -> 769).  Many
+// short own ranges: the start and end of each (64 tokens behind 16384 slots: 75 us; 16
+// trees of 16 to 31 nodes: 55 us).  Tried and slower: the next range's ids, queries and
+// first tiles fetched ahead by warp 3 (791 to 902 us, 85 to 94 us; at the range's end no
+// difference), all segments cut by the plan (it takes 20 instead of 7 us), a polynomial in
+// place of half the exponentials.
+//
 // Every wait is bounded; on expiry the block flags TSD_STATUS_TIMEOUT, drains what it
 // issued, frees its tensor memory and returns.
 
@@ -70,7 +80,11 @@ constexpr uint64_t kDrainNs = 100000000ull;
 constexpr int kMaxBatch = 1024;
 constexpr int kPlanThreads = 1024;
 constexpr int kPieces = 64;     // pieces of one key range at most
-// A unit's fixed cost in a row block of one or two row tiles, in key tiles of one.
+// A range's fixed cost in a row block of one or two row tiles, in key tiles of one: what
+// its start and end take (loads of ids, queries and the first tiles one behind the other,
+// masks, the finished rows: some 14k cycles of a range of three tiles with one row tile).
+// Measured, 64 tokens / 16 trees / 8 trees of 127 nodes over 32768 slots: 8 and 20 75 / 55 /
+// 746 us, 4 and 12 80 / 60 / 857, 12 and 28 82 / 62 / 748, 8 and 32 74 / 60 / 784.
 constexpr int kRangeCost1 = 8, kRangeCost2 = 20;
 
 // One row set and its key range, for every kv head.
