@@ -57,7 +57,7 @@ constexpr int kMaxDraws = 64;
 constexpr int kMaxRowBytes = kMaxVocab / kMaxCluster * 4;  // of a CTA's share
 constexpr int kBins = 2048;
 constexpr int kGroup = 32, kGroups = kBins / kGroup;  // bins are looked for by groups of 32 first
-constexpr int kList = 512, kSmallList = 32;
+constexpr int kList = 512, kCounted = 128, kSmallList = 32;
 constexpr float kCountScale = 32.f, kWideScale = 0.5f, kWeightScale = 64.f;  // bins a unit at first
 constexpr int kLevels = 3;          // times bins are cut again at most
 constexpr float kShare = 8192.f;    // a bin's own weight (262144 of them fit 32 bits)
@@ -673,50 +673,89 @@ struct Found {
   long long base, everything;  // weight above the list, of all that was binned
 };
 
+// Over a list of at most kCounted entries, for this thread's: how many are ranked before
+// it, and their weight (kById: how much weight those of a smaller id have).
+template <bool kById>
+__device__ __forceinline__ void list_scan(const SpShared &sh, int n, unsigned long long mine, int &place, long long &before) {
+  auto less = [&](unsigned long long other) {
+    return kById ? (uint32_t)other > (uint32_t)mine : other > mine;  // (the low word is ~id)
+  };
+  place = 0;
+  before = 0;
+  if ((int)(threadIdx.x & ~31u) >= n) return;
+#pragma unroll 4
+  for (int j = 0; j < n; j += 2) {  // (an odd list ends with a zero)
+    const ulonglong2 o = *reinterpret_cast<const ulonglong2 *>(&sh.list[j]);
+    const ulonglong2 w = *reinterpret_cast<const ulonglong2 *>(&sh.weight[j]);
+    if (less(o.x)) {
+      ++place;
+      before += (long long)w.x;
+    }
+    if (less(o.y)) {
+      ++place;
+      before += (long long)w.y;
+    }
+  }
+}
+
 // The first CTA's end of it: ranks the list, finds the border, and where everything
-// is in the list the sum of what is kept and the draws.  By the whole block.
+// is in the list the sum of what is kept and the draws.  By the whole block: a short list's
+// entries are compared with all, a long one is sorted (508 rows with top-p 0.9: 310 us;
+// with all lists compared 331, and all sorted a single row takes 33 us instead of 30).
 template <bool kBf16, int kMode>
 __device__ __forceinline__ void settle(SpShared &sh, const Run<kBf16> &run, const Found &f, const SpArgs &a, int r) {
-  const int tid = threadIdx.x;
-  // ranked; thread t then holds the ranks 2 t and 2 t + 1
-  const int n = f.n;
-  int size = 2;
-  while (size < n) size *= 2;
-  for (int i = n + tid; i < size; i += kSpThreads) sh.list[i] = 0ull;
-  sort<true>(sh.list, size);
+  const int tid = threadIdx.x, n = f.n;
   const bool weigh = f.gathered || !f.by_count;
+  const bool counted = n <= kCounted;
+  unsigned long long c[2];
   float x[2], w[2] = {0.f, 0.f};
-  int id[2];
+  int id[2], place[2];
   long long fw[2], before[2];
   bool in[2];
+  if (!counted) {
+    int size = 2;
+    while (size < n) size *= 2;
+    for (int i = n + tid; i < size; i += kSpThreads) sh.list[i] = 0ull;
+    sort<true>(sh.list, size);
+  }
 #pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const unsigned long long c = 2 * tid + e < n ? sh.list[2 * tid + e] : 0ull;
-    x[e] = unordered((uint32_t)(c >> 32));
-    id[e] = (int)~(uint32_t)c;
-    in[e] = c != 0ull;
+  for (int e = 0; e < 2; ++e) {  // sorted: the ranks 2 tid and 2 tid + 1
+    const int i = counted ? tid + e * kSpThreads : 2 * tid + e;
+    in[e] = i < n;
+    c[e] = in[e] ? sh.list[i] : 0ull;
+    x[e] = unordered((uint32_t)(c[e] >> 32));
+    id[e] = (int)~(uint32_t)c[e];
     if (in[e] && weigh) w[e] = expf(run.scaled(x[e]));
     fw[e] = fixed(w[e]);
+    place[e] = i;
   }
-  before[0] = block_scan(sh, fw[0] + fw[1]);
-  before[1] = before[0] + fw[0];
+  if (counted) {
+    if (tid < kCounted) sh.weight[tid] = (unsigned long long)fw[0];
+    if (tid == n) sh.list[n] = 0ull;
+    __syncthreads();
+    list_scan<false>(sh, n, c[0], place[0], before[0]);
+    before[1] = 0;
+  } else {
+    before[0] = block_scan(sh, fw[0] + fw[1]);
+    before[1] = before[0] + fw[0];
+  }
   int here = 0;
   if (f.gathered) {
     // top-k, then top-p of what that left
 #pragma unroll
-    for (int e = 0; e < 2; ++e) in[e] = in[e] && 2 * tid + e < f.k;
+    for (int e = 0; e < 2; ++e) in[e] = in[e] && place[e] < f.k;
     if (f.top_p < 1.f) {
       const long long left = f.by_count ? block_total(sh, here, (in[0] ? fw[0] : 0) + (in[1] ? fw[1] : 0)) : f.everything;
       const long long want = (long long)ceil((double)f.top_p * (double)left);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) in[e] = in[e] && (2 * tid + e == 0 || before[e] < want);
+      for (int e = 0; e < 2; ++e) in[e] = in[e] && (place[e] == 0 || before[e] < want);
     }
   } else {
     // one filter's border
     const long long want = f.by_count ? 0 : (long long)ceil((double)f.top_p * (double)f.everything);
     if (!f.by_count && f.base >= want) sh.failed = true;  // (it lies above the list)
 #pragma unroll
-    for (int e = 0; e < 2; ++e) in[e] = in[e] && (f.by_count ? f.more + 2 * tid + e < f.k : f.base + before[e] < want);
+    for (int e = 0; e < 2; ++e) in[e] = in[e] && (f.by_count ? f.more + place[e] < f.k : f.base + before[e] < want);
   }
   // the border is the last that is kept; then min-p, which the weight alone decides
   here = in[0] + in[1];
@@ -725,12 +764,11 @@ __device__ __forceinline__ void settle(SpShared &sh, const Run<kBf16> &run, cons
   int left = 0;
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
-    if (2 * tid + e == here - 1) {
+    if (in[e] && place[e] == here - 1) {
       sh.border_x = x[e];
       sh.border_id = id[e];
     }
     if (f.gathered) in[e] = in[e] && !(w[e] < f.min_p);
-    left += in[e];
   }
   const long long s = block_total(sh, left, (in[0] ? fw[0] : 0) + (in[1] ? fw[1] : 0));
   if (tid == 0) sh.total = f.gathered ? s : f.by_count || f.min_p > 0.f ? -1 : f.base + s;
@@ -742,30 +780,37 @@ __device__ __forceinline__ void settle(SpShared &sh, const Run<kBf16> &run, cons
       return;
     }
     // the draws: the same by id
-    static_assert(kMaxVocab * kList <= (1 << 27), "id and rank in a word");
-    uint32_t *by_id = reinterpret_cast<uint32_t *>(sh.list);
-    float *logit = reinterpret_cast<float *>(by_id + kList);
-    __syncthreads();  // (the list was read)
-    size = 2;
-    while (size < left) size *= 2;
+    if (counted) {
+      if (!in[0]) fw[0] = 0;
+      if (tid < kCounted) sh.weight[tid] = (unsigned long long)fw[0];
+      __syncthreads();
+      list_scan<true>(sh, n, c[0], place[0], before[0]);
+    } else {
+      static_assert(kMaxVocab * kList <= (1 << 27), "id and rank in a word");
+      uint32_t *by_id = reinterpret_cast<uint32_t *>(sh.list);
+      float *logit = reinterpret_cast<float *>(by_id + kList);
+      __syncthreads();  // (the list was read)
+      int size = 2;
+      while (size < n) size *= 2;
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int i = 2 * tid + e;
-      if (i < size) by_id[i] = in[e] ? (uint32_t)id[e] * kList + i : 0xFFFFFFFFu;
-      logit[i] = x[e];
-      sh.weight[i] = (unsigned long long)fw[e];
-    }
-    sort<false>(by_id, size);
-    int rank_of[2];
+      for (int e = 0; e < 2; ++e) {
+        const int i = 2 * tid + e;
+        if (i < size) by_id[i] = in[e] ? (uint32_t)id[e] * kList + i : 0xFFFFFFFFu;
+        logit[i] = x[e];
+        sh.weight[i] = (unsigned long long)fw[e];
+      }
+      sort<false>(by_id, size);
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const uint32_t one = 2 * tid + e < left ? by_id[2 * tid + e] : 0xFFFFFFFFu;
-      rank_of[e] = one % kList;
-      id[e] = (int)(one / kList);
-      fw[e] = one != 0xFFFFFFFFu ? (long long)sh.weight[rank_of[e]] : 0;
+      for (int e = 0; e < 2; ++e) {
+        const uint32_t one = 2 * tid + e < size ? by_id[2 * tid + e] : 0xFFFFFFFFu;
+        const bool any = one != 0xFFFFFFFFu;
+        id[e] = (int)(one / kList);
+        fw[e] = any ? (long long)sh.weight[one % kList] : 0;
+        x[e] = any ? logit[one % kList] : 0.f;
+      }
+      before[0] = block_scan(sh, fw[0] + fw[1]);
+      before[1] = before[0] + fw[0];
     }
-    before[0] = block_scan(sh, fw[0] + fw[1]);
-    before[1] = before[0] + fw[0];
     const float log_total = log_sum(s);
     for (int q = 0; q < a.draws; ++q) {
       const long long at = place_of(sh.u[q], s);
@@ -773,7 +818,7 @@ __device__ __forceinline__ void settle(SpShared &sh, const Run<kBf16> &run, cons
       for (int e = 0; e < 2; ++e)
         if (at >= before[e] && at < before[e] + fw[e]) {
           a.tokens[(size_t)r * a.draws + q] = id[e];
-          a.logprob[(size_t)r * a.draws + q] = run.scaled(logit[rank_of[e]]) - log_total;
+          a.logprob[(size_t)r * a.draws + q] = run.scaled(x[e]) - log_total;
         }
     }
   }
@@ -1224,6 +1269,19 @@ __global__ void __launch_bounds__(kSpThreads, 3) sampling_kernel(const SpArgs a)
         }
 #pragma unroll
         for (int i = 0; i < kN; i += 2) f[j].add2(w[j][i], w[j][i + 1]);
+      }
+      Fixed together;
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        together.hi += f[j].hi;
+        together.lo += f[j].lo;
+      }
+      const long long most = together.warp();
+      if (!__any_sync(0xffffffffu, (at[0] >= 0 && at[0] < most) || (at[1] >= 0 && at[1] < most))) {
+        at[0] -= most;
+        at[1] -= most;
+        here -= most;
+        continue;
       }
 #pragma unroll
       for (int j = 0; j < kAhead; ++j) all[j] = f[j].warp();
