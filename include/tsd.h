@@ -832,7 +832,8 @@ int tsd_kv_append_rope_q4(const uint16_t *q, int64_t q_stride, const uint16_t *k
  *   top-p  the sum of w over ranks 0..r-1 is below p times the sum over what top-k
  *          left; rank 0 always        (p >= 1: off)
  *   min-p  w >= min(min_p, 1)          (min_p <= 0: off; the largest w is 1)
- * T below 2^-126 (0, for instance) keeps rank 0 alone, undivided.  The sums are exact
+ * T below 2^-126 (0, for instance) keeps rank 0 alone, undivided; an infinite T or a NaN
+ * counts as the largest float, a NaN p or min_p as off.  The sums are exact
  * to 2^-43 a token, so the result does not depend on how a row is cut up.
  *
  * tsd_token_sample: `draws` tokens of each of R rows: tokens[r][i] = the first
@@ -851,7 +852,7 @@ int tsd_kv_append_rope_q4(const uint16_t *q, int64_t q_stride, const uint16_t *k
  * logits float (bf16 == 0) or bf16; temperature, top_p, min_p float, top_k int32,
  * each NULL (off) or [ceil(R / per_param)]: entry r / per_param is row r's.
  * Limits: V <= 262144, draws <= 64, R <= 2^24.
- * One launch, no workspace: a cluster of up to 8 CTAs a row.
+ * One launch, no workspace: clusters of up to 8 CTAs that take row after row.
  */
 int tsd_token_sample(const void *logits, int bf16, const int32_t *rows, int R, int64_t num_rows, int V,
                      const float *u, int draws, const float *temperature, const int32_t *top_k,

@@ -228,3 +228,46 @@ def test_captured_and_replayed(tsd):
     tsd.kv_append_rope(q, k, v, slots - 7, kc2, vc2, inv, pos - 1000)
     want = tsd.kv_append_rope(q, k, v, slots, kc2, vc2, inv, pos)
     assert torch.equal(got, want) and torch.equal(gk, kc2)
+
+
+@pytest.mark.parametrize("q4", [False, True])
+def test_pool_past_32_bit_offsets(tsd, q4):
+    """Blocks whose byte offsets wrap to block 0 at 2^32 (bf16: 32 KB a block; 4 bits: 9 KB)."""
+    import torch
+    rng = np.random.default_rng(41)
+    Hkv, D, few = 8, 128, 4
+    shape = (Hkv, 9 * D) if q4 else (Hkv, 16, D)
+    kind, block = (torch.uint8, Hkv * 9 * D) if q4 else (torch.bfloat16, Hkv * 16 * D * 2)
+    far = -(-2 ** 32 // block)
+    append = tsd.kv_append_rope_q4 if q4 else tsd.kv_append_rope
+    q, k, v = [bf(x) for x in inputs(rng, 50, 4, Hkv, D)]
+    slots = T(rng.permutation(few * 16)[:50].astype(np.int32))
+    pos, inv = T(np.arange(50, dtype=np.int32)), T(freqs(D))
+    small = [torch.zeros((few,) + shape, dtype=kind, device="cuda") for _ in range(2)]
+    want = append(q, k, v, slots, *small, inv, pos)
+    big = [torch.empty((far + few,) + shape, dtype=kind, device="cuda") for _ in range(2)]
+    for pool in big:
+        pool[:2 * few] = 0
+        pool[far:] = 0
+    got = append(q, k, v, slots + far * 16, *big, inv, pos)
+    assert torch.equal(want, got)
+    for a, b in zip(small, big):
+        assert torch.equal(a, b[far:]) and not b[:2 * few].any()
+
+
+def test_two_streams_at_once(tsd):
+    import torch
+    rng = np.random.default_rng(42)
+    q, k, v = [bf(x) for x in inputs(rng, 300, 8, 2, 64)]
+    pos, inv = T(np.arange(300, dtype=np.int32)), T(freqs(64))
+    slots = [T(np.arange(300, dtype=np.int32) + 400 * i) for i in range(2)]
+    pools = [torch.zeros((50, 2, 16, 64), dtype=torch.bfloat16, device="cuda") for _ in range(4)]
+    want = [tsd.kv_append_rope(q, k, v, s, pools[0], pools[1], inv, pos) for s in slots]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(2)], [None, None]
+    for i in range(2):  # into the same pool, other slots
+        with torch.cuda.stream(streams[i]):
+            got[i] = tsd.kv_append_rope(q, k, v, slots[i], pools[2], pools[3], inv, pos)
+    torch.cuda.synchronize()
+    assert torch.equal(pools[0], pools[2]) and torch.equal(pools[1], pools[3])
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])

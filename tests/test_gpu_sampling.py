@@ -279,3 +279,22 @@ def test_two_streams_at_once(tsd):
         torch.cuda.synchronize()
         for i in range(2):
             assert torch.equal(got[i][0], want[i][0]) and torch.equal(got[i][1], want[i][1])
+
+
+def test_settings_out_of_range(tsd):
+    """An infinite temperature is uniform over what is not masked; NaN settings are off."""
+    import torch
+    x = T(rows_of(np.random.default_rng(31), 4, 5000, "masked"))
+    inf, nan = T(np.full(4, np.inf, np.float32)), T(np.full(4, np.nan, np.float32))
+    finite = (x > -torch.inf).float()
+    probs = tsd.logits_filter(x, inf, probs=True)
+    assert torch.allclose(probs, finite / finite.sum(1, keepdim=True), rtol=2.0 ** -20, atol=0)
+    assert torch.equal(probs, tsd.logits_filter(x, nan, probs=True))
+    tokens, lp = tsd.token_sample(x, T(np.array([[0.0, 0.3, 0.999]] * 4, np.float32)), inf)
+    assert (finite.gather(1, tokens.long()) == 1).all() and torch.isfinite(lp).all()
+    for kw in (dict(top_k=T(np.full(4, 10, np.int32))), {}):  # with another filter, and alone
+        want = tsd.logits_filter(x, **kw)
+        assert torch.equal(tsd.logits_filter(x, top_p=nan, min_p=nan, **kw), want)
+    last = tsd.logits_filter(x, inf, top_p=T(np.full(4, 0.5, np.float32)), probs=True)
+    half = (finite.sum(1) + 1).div(2, rounding_mode="floor")  # ranks before r: r of n equal weights < n / 2
+    assert torch.equal((last > 0).sum(1).float(), half)

@@ -453,3 +453,41 @@ def test_wait_limit(tsd):
     assert int(st.item()) == tsd.STATUS_TIMEOUT
     after = run(tsd, x)
     assert all(torch.equal(a, b) for a, b in zip(before, after))
+
+
+def test_pool_past_32_bit_offsets(tsd):
+    """The same blocks 2^32 bytes further on: the same rows, bit for bit."""
+    import torch
+    x = inputs(51, 5, 16, 8, 128, [(300, [20, 40]), (17, [30])], hide=0)
+    far = 2 ** 32 // (8 * 16 * 128 * 2)
+    args = [bf(x["q"]), bf(x["k"]), bf(x["v"]), T(x["table"]), T(x["P"]), T(x["n"]), T(x["mask"].view(np.int32)), T(x["err"]),
+            T(x["first"]), T(x["S"])]
+    want = tsd.tree_attn_fwd_shared(*args)
+    for i in (1, 2):
+        small = args[i]
+        args[i] = torch.empty((far + len(small),) + small.shape[1:], dtype=small.dtype, device="cuda")
+        args[i][:len(small)] = float("nan")
+        args[i][far:] = small
+    args[3] = torch.where(args[3] >= 0, args[3] + far, args[3])
+    got = tsd.tree_attn_fwd_shared(*args)
+    live = torch.arange(5, device="cuda")[None] < args[5][:, None]
+    for a, b in zip(want, got):
+        assert torch.equal(a[live], b[live])
+
+
+def test_one_prompt_of_many_tokens_in_two_groups_at_once(tsd):
+    """Two calls at once on two streams, each with a workspace of its own."""
+    import torch
+    xs = [inputs(52, 3, 8, 2, 64, [(900, [1, 5, 9, 30])]), inputs(53, 7, 8, 2, 64, [(64, [2, 2]), (128, [700, 3])])]
+    want = [run(tsd, x) for x in xs]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(2)], [[], []]
+    for _ in range(4):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(run(tsd, xs[i]))
+    torch.cuda.synchronize()
+    for i, x in enumerate(xs):
+        live = torch.arange(x["q"].shape[1], device="cuda")[None] < T(x["n"])[:, None]
+        for out, lse in got[i]:
+            assert torch.equal(out[live], want[i][0][live]) and torch.equal(lse[live], want[i][1][live])

@@ -948,13 +948,14 @@ __global__ void __launch_bounds__(kSpThreads, 3) sampling_kernel(const SpArgs a)
     continue;
   }
   const int pr = r / a.per_param;
-  const float T = a.temperature ? a.temperature[pr] : 1.f;
+  // (a T that is not finite is the largest: 0 times the -inf of a masked logit would be NaN)
+  const float T = a.temperature ? fminf(a.temperature[pr], 3.4028235e38f) : 1.f;
   const bool greedy = !(T >= 1.1754944e-38f);
   int k = a.top_k ? a.top_k[pr] : 0;
   if (k <= 0 || k > V) k = V;
   if (greedy) k = 1;
   const float top_p = a.top_p ? a.top_p[pr] : 1.f;
-  const float min_p = a.min_p ? fminf(a.min_p[pr], 1.f) : 0.f;
+  const float min_p = a.min_p && a.min_p[pr] > 0.f ? fminf(a.min_p[pr], 1.f) : 0.f;  // (NaN: off)
   run.inv_t = greedy ? 1.f : __fdiv_rn(1.f, T);
   __syncthreads();  // (the row before is done with)
   if (kMode == kSample && tid < a.draws) sh.u[tid] = a.u[(size_t)r * a.draws + tid];
@@ -1013,7 +1014,7 @@ __global__ void __launch_bounds__(kSpThreads, 3) sampling_kernel(const SpArgs a)
 #pragma unroll 1
   for (int stage = 0; stage < 2; ++stage) {
     const bool by_count = stage == 0;
-    if (by_count ? k >= V : top_p >= 1.f) continue;
+    if (by_count ? k >= V : !(top_p < 1.f)) continue;
     // top-p: from its border on there is more than (1 - p) of a weight of 1 or more, so no
     // logit at or above it has less than (1 - p) / V; what has only adds to the sum
     const float inv_unit = by_count ? 1.f : 1.f / run.inv_t;
