@@ -298,3 +298,21 @@ def test_settings_out_of_range(tsd):
     last = tsd.logits_filter(x, inf, top_p=T(np.full(4, 0.5, np.float32)), probs=True)
     half = (finite.sum(1) + 1).div(2, rounding_mode="floor")  # ranks before r: r of n equal weights < n / 2
     assert torch.equal((last > 0).sum(1).float(), half)
+
+
+@pytest.mark.parametrize("V,width", [(100000, 0.05), (262144, 1e-3), (50000, 2.0)])
+def test_dense_logits(tsd, V, width):
+    """Thousands of different logits in each of the first bins, which are cut again."""
+    import torch
+    settings = [(1.0, 0, 0.5, 0.0), (1.0, 20000, 1.0, 0.0), (0.5, 30000, 0.3, 0.0), (1.0, 0, 0.999, 0.0), (0.1, 700, 0.9, 0.5)]
+    rng = np.random.default_rng(V)
+    x = (rng.random((len(settings), V)) * width).astype(np.float32)
+    t, k, p, m = [T(np.array([s[i] for s in settings], np.int32 if i == 1 else np.float32)) for i in range(4)]
+    args = dict(temperature=t, top_k=k, top_p=p, min_p=m)
+    u = rng.random((len(settings), 4)).astype(np.float32)
+    tokens, lp = tsd.token_sample(T(x), T(u), **args)
+    rows, probs = tsd.logits_filter(T(x), **args), tsd.logits_filter(T(x), probs=True, **args)
+    tokens, lp, rows, probs = [a.cpu().numpy() for a in (tokens, lp, rows, probs)]
+    for r, setting in enumerate(settings):
+        f32 = tuple(float(np.float32(s)) if i != 1 else s for i, s in enumerate(setting))
+        check_row(x[r].astype(np.float64), f32, rows[r].astype(np.float64), probs[r].astype(np.float64), tokens[r], lp[r], u[r])
