@@ -351,8 +351,9 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const Attn p)
   }
   __syncthreads();
   const long long total = groups_cost + own_cost;
-  // (a part shorter than a unit's set-up and some tiles is mostly set-up)
-  long long part = max((total + p.blocks - 1) / p.blocks, (long long)kRangeCost1 + 4);
+  // (a part shorter than a unit's set-up and two tiles is mostly set-up: 4 tokens behind 2048
+  // slots take the attention 19.5 us, 21.6 with four tiles, 25.7 with ten)
+  long long part = max((total + p.blocks - 1) / p.blocks, (long long)kRangeCost1 + 2);
   part = max(part, (longest + kPieces - 3) / (kPieces - 2));
   if (tid == 0) *p.plan = Plan{total, part};
   // every block's first segment
