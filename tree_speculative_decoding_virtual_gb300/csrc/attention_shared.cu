@@ -15,7 +15,8 @@
 // units' key tiles (128 keys; cost 1, or 2 with more than 128 rows, and a fixed cost
 // a unit) are laid end to end and cut into equal parts, one a block, so that every SM
 // has the same work whatever the lengths; trees are packed, so that padding nodes
-// cost nothing.
+// cost nothing.  Where there are blocks enough, no part spans two units (4 tokens behind
+// 2048 slots: the attention 12 us, 19.5 with such parts).
 //
 // Block: the segments of its part in turn, each walked in 128-key tiles on the
 // 5th-generation tensor cores:
@@ -78,7 +79,7 @@ constexpr float kMaxSum = 0x1p60f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr uint64_t kDrainNs = 100000000ull;
 constexpr int kMaxBatch = 1024;
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 1024, kSmallPlan = 256;  // of the plan; up to kSmallPlan sequences the fewer
 constexpr int kPieces = 64;     // pieces of one key range at most
 // A range's fixed cost in a row block of one or two row tiles, in key tiles of one: what
 // its start and end take (loads of ids, queries and the first tiles one behind the other,
@@ -137,26 +138,37 @@ struct Attn {
 // plan
 // ---------------------------------------------------------------------------
 
-// Exclusive sum over the block's threads; `all` the sum of all.
-__device__ __forceinline__ long long block_scan(long long x, long long *buf, long long &all) {
+// Exclusive sums over the block's threads, N at a time; `all` the sums of all.
+template <int N>
+__device__ __forceinline__ void block_scan(const long long (&x)[N], long long (*buf)[4], long long (&before)[N], long long (&all)[N]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  long long incl = x;
+  long long incl[N];
 #pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, incl, off);
-    if (lane >= off) incl += y;
+  for (int e = 0; e < N; ++e) {
+    incl[e] = x[e];
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, incl[e], off);
+      if (lane >= off) incl[e] += y;
+    }
   }
   __syncthreads();
-  if (lane == 31) buf[warp] = incl;
+  if (lane == 31)
+#pragma unroll
+    for (int e = 0; e < N; ++e) buf[warp][e] = incl[e];
   __syncthreads();
-  long long before = 0;
-  all = 0;
-  for (int w = 0; w < (int)blockDim.x / 32; ++w) {
-    const long long s = buf[w];
-    if (w < warp) before += s;
-    all += s;
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    before[e] = incl[e] - x[e];
+    all[e] = 0;
   }
-  return before + incl - x;
+  for (int w = 0; w < (int)blockDim.x / 32; ++w)
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      const long long s = buf[w][e];
+      if (w < warp) before[e] += s;
+      all[e] += s;
+    }
 }
 
 // A unit as the plan kernel left it (from L2: another launch may have used the place).
@@ -170,12 +182,14 @@ __device__ __forceinline__ Unit load_unit(const Unit *at) {
   return r.u;
 }
 
-// Cost of a unit's row block of w row tiles.
-__device__ __forceinline__ long long block_cost(const Unit &u, int w) {
-  return (w == 2 ? kRangeCost2 : kRangeCost1) + (long long)u.tiles * w;
+// Cost of a unit's row block of w row tiles; `alone` > 0: what its parts of that many
+// tiles take, with no set-up.
+__device__ __forceinline__ long long block_cost(const Unit &u, int w, int alone) {
+  const int tiles = u.tiles * w;
+  return alone ? (long long)((tiles + alone - 1) / alone) * alone : (w == 2 ? kRangeCost2 : kRangeCost1) + tiles;
 }
-__device__ __forceinline__ long long unit_cost(const Unit &u, int Hkv) {
-  return u.rbs ? (long long)Hkv * ((u.rbs - 1) * block_cost(u, 2) + block_cost(u, u.last_w)) : 0;
+__device__ __forceinline__ long long unit_cost(const Unit &u, int Hkv, int alone) {
+  return u.rbs ? (long long)Hkv * ((u.rbs - 1) * block_cost(u, 2, alone) + block_cost(u, u.last_w, alone)) : 0;
 }
 
 __device__ __forceinline__ void shape_unit(Unit &u, int nodes, int g) {
@@ -205,9 +219,9 @@ static_assert(sizeof(Seg) == 80, "five 16-byte words");
 
 // The segment at g of a unit that holds g, as far as `end`; false when none begins there
 // (s.next is moved on).
-__device__ __forceinline__ bool cut_segment(const Unit &u, long long g, long long end, int block, Seg &s) {
-  const long long full = block_cost(u, 2);
-  const long long head = (u.rbs - 1) * full + block_cost(u, u.last_w);
+__device__ __forceinline__ bool cut_segment(const Unit &u, long long g, long long end, int block, int alone, Seg &s) {
+  const long long full = block_cost(u, 2, alone);
+  const long long head = (u.rbs - 1) * full + block_cost(u, u.last_w, alone);
   const long long local = g - u.start;
   int rb;
   long long x0;
@@ -223,11 +237,12 @@ __device__ __forceinline__ bool cut_segment(const Unit &u, long long g, long lon
     rb = (int)min(in_head / full, (long long)(u.rbs - 1));
     x0 = in_head - rb * full;
   }
-  const int w = rb == u.rbs - 1 ? u.last_w : 2, fixed = w == 2 ? kRangeCost2 : kRangeCost1;
-  const long long x1 = min(fixed + (long long)u.tiles * w, x0 + end - g);
+  const int w = rb == u.rbs - 1 ? u.last_w : 2, fixed = alone ? 0 : w == 2 ? kRangeCost2 : kRangeCost1;
+  const long long x1 = min(block_cost(u, w, alone), x0 + end - g);
   s.next = g + x1 - x0;
   // (w is 1 or 2)
-  const int u0 = (int)((max(x0 - fixed, 0ll) + w - 1) >> (w - 1)), u1 = (int)((max(x1 - fixed, 0ll) + w - 1) >> (w - 1));
+  const int u0 = (int)((max(x0 - fixed, 0ll) + w - 1) >> (w - 1));
+  const int u1 = min((int)((max(x1 - fixed, 0ll) + w - 1) >> (w - 1)), u.tiles);
   if (u0 >= u1) return false;
   s.rows = u.rows;
   s.row0 = rb * kRows;
@@ -252,7 +267,9 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const Attn p)
   __shared__ int off[kMaxBatch + 1];   // packed nodes before sequence b
   __shared__ int first[kMaxBatch + 1], shared[kMaxBatch], members[kMaxBatch], rep[kMaxBatch];
   __shared__ long long starts[2 * kMaxBatch];
-  __shared__ long long buf[kPlanThreads / 32];
+  __shared__ long long buf[kPlanThreads / 32][4];
+  __shared__ int2 shape[2 * kSmallPlan];
+  __shared__ int fits[kSmallPlan / 32];
   __shared__ int bad_groups;
   __shared__ long long longest;
   pdl_trigger();
@@ -301,10 +318,11 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const Attn p)
       atomicMin(&rep[gr], tid);
     }
   }
-  long long all;
-  const int node0 = (int)block_scan(ok ? nb : 0, buf, all);
+  long long nodes[1] = {ok ? nb : 0}, nodes_before[1], nodes_all[1];
+  block_scan(nodes, buf, nodes_before, nodes_all);
+  const int node0 = (int)nodes_before[0];
   if (tid < B) off[tid] = node0;
-  if (tid == 0) off[B] = (int)all;
+  if (tid == 0) off[B] = (int)nodes_all[0];
   __syncthreads();
   // a thread's two units: a group's shared range, a sequence's own
   Unit u[2] = {};
@@ -328,19 +346,64 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const Attn p)
     shape_unit(u[1], u[1].nb, p.g);
   }
   // costs, and row blocks and rows (in one word: rows below 2^40, blocks below 2^23)
-  const long long c0 = unit_cost(u[0], p.Hkv), c1 = unit_cost(u[1], p.Hkv);
-  long long groups_cost, own_cost, groups_rows, own_rows;
-  u[0].start = block_scan(c0, buf, groups_cost);
-  u[1].start = groups_cost + block_scan(c1, buf, own_cost);
   auto packed = [&](const Unit &x) { return x.rbs ? ((long long)x.rbs << 40 | x.rows) * p.Hkv : 0; };
-  const long long r0 = block_scan(packed(u[0]), buf, groups_rows), r1 = groups_rows + block_scan(packed(u[1]), buf, own_rows);
   constexpr long long kRowBits = (1ll << 40) - 1;
-  u[0].row_base = r0 & kRowBits;
-  u[1].row_base = r1 & kRowBits;
-  u[0].block_base = (int)(r0 >> 40);
-  u[1].block_base = (int)(r1 >> 40);
+  long long total, row_blocks;
+  {
+    const long long x[4] = {unit_cost(u[0], p.Hkv, 0), unit_cost(u[1], p.Hkv, 0), packed(u[0]), packed(u[1])};
+    long long before[4], all[4];
+    block_scan(x, buf, before, all);
+    u[0].start = before[0];
+    u[1].start = all[0] + before[1];
+    u[0].row_base = before[2] & kRowBits;
+    u[1].row_base = (all[2] + before[3]) & kRowBits;
+    u[0].block_base = (int)(before[2] >> 40);
+    u[1].block_base = (int)((all[2] + before[3]) >> 40);
+    total = all[0] + all[1];
+    row_blocks = (all[2] + all[3]) >> 40;
+  }
   const long long far = 2ll * max(u[0].tiles, u[1].tiles) + kRangeCost2;
   atomicMax((unsigned long long *)&longest, (unsigned long long)far);
+  __syncthreads();
+  // (a part shorter than a unit's set-up and two tiles is mostly set-up: 4 tokens behind 2048
+  // slots take the attention 19.5 us, 21.6 with four tiles, 25.7 with ten)
+  long long part = max((total + p.blocks - 1) / p.blocks, (long long)kRangeCost1 + 2);
+  const long long least = (longest + kPieces - 3) / (kPieces - 2);
+  part = max(part, least);
+  // Few row blocks: each is cut into parts of its own, so that no block begins twice, if
+  // there are blocks enough with parts that are not longer by more than half a
+  // set-up.  Each warp tries another length.
+  int alone = 0;
+  if (row_blocks <= p.blocks && blockDim.x == kSmallPlan) {
+    shape[tid] = make_int2(u[0].tiles, u[0].rbs * 2 + u[0].last_w - 2);
+    shape[kSmallPlan + tid] = make_int2(u[1].tiles, u[1].rbs * 2 + u[1].last_w - 2);
+    __syncthreads();
+    const int lane = tid & 31, warp = tid >> 5, most = (int)min(part, 1ll << 20) + kRangeCost1 / 2;
+    const int from = max((int)min(least, 1ll << 20), 2);
+    const int len = from + warp * max((most - from + 6) / 7, 1);
+    long long parts = 0;
+    for (int i = lane; i < G + kSmallPlan && i < 2 * kSmallPlan; i += 32) {
+      const int2 x = shape[i < G ? i : kSmallPlan + i - G];
+      // (x.y: row tiles of all its row blocks)
+      if (x.y > 0) parts += (x.y / 2) * ((2 * x.x + len - 1) / len) + (x.y & 1) * ((x.x + len - 1) / len);
+    }
+#pragma unroll
+    for (int off = 16; off; off >>= 1) parts += __shfl_xor_sync(0xffffffffu, parts, off);
+    if (lane == 0) fits[warp] = len <= most && parts * p.Hkv <= p.blocks ? len : 0;
+    __syncthreads();
+    for (int w = kSmallPlan / 32 - 1; w >= 0; --w)
+      if (fits[w]) alone = fits[w];
+    if (alone) {
+      part = alone;
+      const long long x[2] = {unit_cost(u[0], p.Hkv, alone), unit_cost(u[1], p.Hkv, alone)};
+      long long before[2], all[2];
+      block_scan(x, buf, before, all);
+      u[0].start = before[0];
+      u[1].start = all[0] + before[1];
+      total = all[0] + all[1];
+    }
+  }
+  if (tid == 0) *p.plan = Plan{total, part};
   if (tid < G) {
     p.units[tid] = u[0];
     starts[tid] = u[0].start;
@@ -350,12 +413,6 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const Attn p)
     starts[G + tid] = u[1].start;
   }
   __syncthreads();
-  const long long total = groups_cost + own_cost;
-  // (a part shorter than a unit's set-up and two tiles is mostly set-up: 4 tokens behind 2048
-  // slots take the attention 19.5 us, 21.6 with four tiles, 25.7 with ten)
-  long long part = max((total + p.blocks - 1) / p.blocks, (long long)kRangeCost1 + 2);
-  part = max(part, (longest + kPieces - 3) / (kPieces - 2));
-  if (tid == 0) *p.plan = Plan{total, part};
   // every block's first segment
   for (int k = tid; k < p.blocks; k += blockDim.x) {
     long long g = (long long)k * part;
@@ -368,7 +425,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const Attn p)
         const int mid = (at + hi + 1) >> 1;
         if (starts[mid] <= g) at = mid; else hi = mid - 1;
       }
-      if (cut_segment(load_unit(p.units + at), g, end, k, s)) break;
+      if (cut_segment(load_unit(p.units + at), g, end, k, alone, s)) break;
       g = s.next;
       s.n = 0;
     }
@@ -397,7 +454,7 @@ __device__ __forceinline__ void next_segment(const Attn &p, long long g, long lo
       if (step == 1) break;
       step = (step + 31) / 32;
     }
-    if (cut_segment(load_unit(p.units + at), g, end, blockIdx.x, s)) return;
+    if (cut_segment(load_unit(p.units + at), g, end, blockIdx.x, 0, s)) return;
     g = s.next;
   }
   s.n = 0;
@@ -1262,7 +1319,7 @@ int launch_all(const Attn &p, cudaStream_t s) {
       !make_cache_map(&v8, p.v, p.num_blocks, p.Hkv, D, kTilePages))
     return TSD_ERR_CUDA;
   if (!ready<D>()) return TSD_ERR_CUDA;
-  const int threads = p.B <= 256 ? 256 : kPlanThreads;
+  const int threads = p.B <= kSmallPlan ? kSmallPlan : kPlanThreads;
   if (launch(shared_plan_kernel, dim3(1), dim3(threads), 0, s, p) != cudaSuccess) return TSD_ERR_CUDA;
   if (launch(shared_attn_kernel<D>, dim3(p.blocks), dim3(kThreads), Layout<D>::kAlloc, s, p, k1, k8, v1, v8) != cudaSuccess)
     return TSD_ERR_CUDA;
