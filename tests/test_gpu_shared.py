@@ -491,3 +491,17 @@ def test_one_prompt_of_many_tokens_in_two_groups_at_once(tsd):
         live = torch.arange(x["q"].shape[1], device="cuda")[None] < T(x["n"])[:, None]
         for out, lse in got[i]:
             assert torch.equal(out[live], want[i][0][live]) and torch.equal(lse[live], want[i][1][live])
+
+
+@pytest.mark.parametrize("N,Hq,Hkv,D", [(31, 32, 8, 128), (40, 32, 8, 128), (9, 64, 8, 64), (70, 16, 16, 64)])
+def test_more_ranges_than_blocks(tsd, N, Hq, Hkv, D):
+    """Trees of many sequences: a block takes several ranges, or the ends of two."""
+    rng = np.random.default_rng(N + Hq)
+    groups = [(int(rng.integers(0, 900)), [int(o) for o in rng.integers(0, 400, m)]) for m in (9, 1, 0, 14)]
+    x = inputs(N * Hq + D, N, Hq, Hkv, D, groups, [int(i) for i in rng.integers(1, N + 1, 24)])
+    st = status_word()
+    got = run(tsd, x, status=st)
+    check(x, *got, reference(x))
+    assert int(st.item()) == 0
+    again = run(tsd, x)
+    assert all((a.nan_to_num(7.0) == b.nan_to_num(7.0)).all() for a, b in zip(got, again))

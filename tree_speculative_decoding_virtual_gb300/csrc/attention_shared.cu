@@ -365,8 +365,9 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const Attn p)
   const long long far = 2ll * max(u[0].tiles, u[1].tiles) + kRangeCost2;
   atomicMax((unsigned long long *)&longest, (unsigned long long)far);
   __syncthreads();
-  // (a part shorter than a unit's set-up and two tiles is mostly set-up: 4 tokens behind 2048
-  // slots take the attention 19.5 us, 21.6 with four tiles, 25.7 with ten)
+  // (a part shorter than a unit's set-up and two tiles is mostly set-up; longer ones leave
+  // SMs idle: 4 tokens behind 2048 slots, laid end to end, take the attention 19.5 us, 21.6
+  // with four tiles, 25.7 with ten)
   long long part = max((total + p.blocks - 1) / p.blocks, (long long)kRangeCost1 + 2);
   const long long least = (longest + kPieces - 3) / (kPieces - 2);
   part = max(part, least);
