@@ -316,3 +316,33 @@ def test_dense_logits(tsd, V, width):
     for r, setting in enumerate(settings):
         f32 = tuple(float(np.float32(s)) if i != 1 else s for i, s in enumerate(setting))
         check_row(x[r].astype(np.float64), f32, rows[r].astype(np.float64), probs[r].astype(np.float64), tokens[r], lp[r], u[r])
+
+
+def drawn(tsd, x, u, **args):
+    """token_sample into outputs that hold what no call writes."""
+    import torch
+    tokens = torch.full(u.shape, -7, dtype=torch.int32, device="cuda")
+    lp = torch.full(u.shape, 7.0, device="cuda")
+    tsd.token_sample(T(x), T(u), tokens=tokens, logprob=lp, **args)
+    return tokens.cpu().numpy(), lp.cpu().numpy()
+
+
+@pytest.mark.parametrize("R", [1, 3])
+def test_short_lists_behind_many_kept(tsd, R):
+    """More is kept than a list holds, and the border's bins hold a few logits: those of every CTA of a row, whose
+    weights the draws need by run."""
+    rng = np.random.default_rng(51)
+    V, n, draws = 262144, 2000, 64
+    x = np.full((R, V), -np.inf, np.float32)
+    for r in range(R):
+        x[r, np.sort(rng.permutation(V)[:n])] = rng.permutation(n).astype(np.float32) * np.float32(-0.001)
+    u = ((np.arange(R * draws) + rng.random(R * draws)) / (R * draws)).astype(np.float32).reshape(R, draws)
+    args = dict(top_p=T(np.full(R, 0.9, np.float32)))
+    tokens, lp = drawn(tsd, x, u, **args)
+    rows = tsd.logits_filter(T(x), **args).cpu().numpy()
+    probs = tsd.logits_filter(T(x), probs=True, **args).cpu().numpy()
+    for r in range(R):
+        check_row(x[r].astype(np.float64), (1.0, 0, float(np.float32(0.9)), 0.0), rows[r].astype(np.float64), probs[r].astype(np.float64), tokens[r], lp[r], u[r])
+    for _ in range(20):
+        again, again_lp = drawn(tsd, x, u, **args)
+        assert np.array_equal(again, tokens) and np.array_equal(again_lp, lp)

@@ -1169,18 +1169,18 @@ __global__ void __launch_bounds__(kSpThreads, 3) sampling_kernel(const SpArgs a)
           parts.load(sh, ranks);
           parts.sum(sh);
         }
-        __syncthreads();
-        const int n = sh.listed;
-        const long long base = sh.sum_above, everything = sh.sum_all;
-        const int more = sh.count_above;
-        __syncthreads();
+        // (in front of the barrier: from here on single warps set these and add to them)
         if (tid == 0) {
-          sh.failed = n > kList;
+          sh.failed = sh.listed > kList;
           sh.border_x = kept.x;
           sh.border_id = kept.id;
           sh.total = 0;
         }
         if (tid < kMaxCluster * kSpWarps) sh.extra[tid] = 0ull;
+        __syncthreads();
+        const int n = sh.listed;
+        const long long base = sh.sum_above, everything = sh.sum_all;
+        const int more = sh.count_above;
         const Found found{v.what == kGather, by_count, stage == 0 ? k : kMaxVocab, top_p, min_p, n, more, base, everything};
         if (n <= kSmallList) {
           if (warp == 0) settle_few<kBf16, kMode>(sh, run, found, a, r);
