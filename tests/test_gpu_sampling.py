@@ -346,3 +346,22 @@ def test_short_lists_behind_many_kept(tsd, R):
     for _ in range(20):
         again, again_lp = drawn(tsd, x, u, **args)
         assert np.array_equal(again, tokens) and np.array_equal(again_lp, lp)
+
+
+@pytest.mark.parametrize("top_k", [0, 50, 700])
+@pytest.mark.parametrize("V,p", [(200, -np.inf), (1000, -1e6), (5003, -1.0), (5003, -3e38), (32000, -np.inf), (262144, -1e6)])
+def test_top_p_below_zero_keeps_rank_zero(tsd, V, p, top_k):
+    """include/tsd.h: rank 0 is kept whatever p is.  Hundreds of logits lie within 32 of the maximum."""
+    rng = np.random.default_rng(V)
+    R = 3
+    x = rows_of(rng, R, V, "plain")
+    x[1] = np.round(x[1])  # the largest one more than once
+    args = dict(top_p=T(np.full(R, p, np.float32)), top_k=T(np.full(R, top_k, np.int32)))
+    best = x.argmax(1)  # (the lowest id of equal ones)
+    tokens, lp = drawn(tsd, x, rng.random((R, 3)).astype(np.float32), **args)
+    assert (tokens == best[:, None]).all() and (lp == 0).all()
+    rows = tsd.logits_filter(T(x), **args).cpu().numpy()
+    probs = tsd.logits_filter(T(x), probs=True, **args).cpu().numpy()
+    want = np.full((R, V), -np.inf, np.float32)
+    want[np.arange(R), best] = 0
+    assert np.array_equal(rows, want) and np.array_equal(probs, np.exp(want))

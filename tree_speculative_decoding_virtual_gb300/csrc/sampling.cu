@@ -954,7 +954,8 @@ __global__ void __launch_bounds__(kSpThreads, 3) sampling_kernel(const SpArgs a)
   int k = a.top_k ? a.top_k[pr] : 0;
   if (k <= 0 || k > V) k = V;
   if (greedy) k = 1;
-  const float top_p = a.top_p ? a.top_p[pr] : 1.f;
+  // (below zero is zero: rank 0 alone, and `near` below stays positive; NaN: off)
+  const float top_p = !a.top_p ? 1.f : a.top_p[pr] < 0.f ? 0.f : a.top_p[pr];
   const float min_p = a.min_p && a.min_p[pr] > 0.f ? fminf(a.min_p[pr], 1.f) : 0.f;  // (NaN: off)
   run.inv_t = greedy ? 1.f : __fdiv_rn(1.f, T);
   __syncthreads();  // (the row before is done with)
