@@ -365,3 +365,45 @@ def test_top_p_below_zero_keeps_rank_zero(tsd, V, p, top_k):
     want = np.full((R, V), -np.inf, np.float32)
     want[np.arange(R), best] = 0
     assert np.array_equal(rows, want) and np.array_equal(probs, np.exp(want))
+
+
+def gap_row():
+    """A maximum, 480 equal logits half a unit in front of what top-p 0.999 may still reach (a weight of 0.001 / V
+    and 5%), 2099 behind it: nothing lies between, and the weight of all but the maximum is the share that
+    top-p leaves out, to 10^-6."""
+    V, n, p = 2580, 480, float(np.float32(0.999))
+    near = np.log(V) - np.log(1 - p) + 0.05
+    far = np.float32(near + 0.002)
+    tail = lambda d: n * np.exp(-np.float64(np.float32(d))) + (V - 1 - n) * np.exp(-np.float64(far))
+    lo, hi = near - 0.6, near  # the tail falls with d
+    for _ in range(60):
+        d = (lo + hi) / 2
+        lo, hi = (d, hi) if tail(d) > (1 - p) * (1 + tail(d)) else (lo, d)
+    assert abs(tail(lo) - (1 - p) * (1 + tail(lo))) < 1e-6 * tail(lo) and near - lo < 0.3
+    x = np.full(V, -far, np.float32)
+    x[1000:1000 + n] = -np.float32(lo)
+    x[17] = 0.0
+    return x, p
+
+
+def thin_row():
+    """A maximum, and 262143 logits behind it that together weigh less than the 2^-24 that top-p leaves out."""
+    x = np.full(262144, -29.165, np.float32)
+    x[200000] = 0.0
+    assert np.exp(np.float64(x)).sum() * 2.0 ** -24 > 262143 * np.exp(np.float64(x[0])) * (1 + 2.0 ** -5)
+    return x, 1 - 2.0 ** -24
+
+
+@pytest.mark.parametrize("row", [gap_row, thin_row])
+def test_top_p_next_to_what_it_cannot_reach(tsd, row):
+    """Thousands of logits just below any that top-p may keep, in reach of the border's bins."""
+    one, p = row()
+    x = np.stack([one, one + np.float32(2), one])
+    x[2, [0, 1]] = -np.inf
+    args = dict(top_p=T(np.full(3, p, np.float32)))
+    u = np.array([[0.0, 0.5, 1 - 2.0 ** -24]] * 3, np.float32)
+    tokens, lp = drawn(tsd, x, u, **args)
+    rows = tsd.logits_filter(T(x), **args).cpu().numpy()
+    probs = tsd.logits_filter(T(x), probs=True, **args).cpu().numpy()
+    for r in range(3):
+        check_row(x[r].astype(np.float64), (1.0, 0, p, 0.0), rows[r].astype(np.float64), probs[r].astype(np.float64), tokens[r], lp[r], u[r])

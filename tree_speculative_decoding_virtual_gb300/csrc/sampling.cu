@@ -565,7 +565,7 @@ __device__ __forceinline__ void sum_groups(SpShared &sh, const Bins &bins, bool 
 // there is more than may be left behind the border (the exact sum less the share wanted:
 // what is left is small, and known better by itself than as a difference).
 __device__ __forceinline__ void find_bins(SpShared &sh, const Bins bins, bool by_count, int k, float top_p,
-                                          uint32_t ranks, int level, int V) {
+                                          uint32_t ranks, int level) {
   const int lane = threadIdx.x;
   const bool from_end = !by_count && level == 0;
   static_assert(kGroups == 64, "two a lane");
@@ -589,11 +589,11 @@ __device__ __forceinline__ void find_bins(SpShared &sh, const Bins bins, bool by
   const double all = (double)sh.sum_all, want = max((double)top_p * all, 1.0);
   const float need = by_count ? (float)(k - sh.count_above) : (float)((want - (double)sh.sum_above) * (double)kUnit);
   const float room = (float)((all - want) * (double)kUnit), skipped = sh.skipped;
-  const float e = by_count ? 0.f : kShareError, beyond = (float)V * 1.3e-14f;
+  const float e = by_count ? 0.f : kShareError;
   // whether the border may, and must, lie at or before a bin (or group), by the sum up to it
   // or, from the end, of what lies behind it
   auto may = [&](float sum) { return from_end ? sum * (1.f - e) <= room : sum * (1.f + e) >= need; };
-  auto must = [&](float sum) { return from_end ? sum * (1.f + e) + beyond <= room : sum * (1.f - e) >= need; };
+  auto must = [&](float sum) { return from_end ? sum * (1.f + e) <= room : sum * (1.f - e) >= need; };
   // sums over the lanes before this one, or after it
   auto scan = [&](float v) -> float {
     float upto = v;
@@ -1017,10 +1017,13 @@ __global__ void __launch_bounds__(kSpThreads, 3) sampling_kernel(const SpArgs a)
     const bool by_count = stage == 0;
     if (by_count ? k >= V : !(top_p < 1.f)) continue;
     // top-p: from its border on there is more than (1 - p) of a weight of 1 or more, so no
-    // logit at or above it has less than (1 - p) / V; what has only adds to the sum
+    // logit at or above it has less than (1 - p) / V (up to the sums' last place, 2^-43 a
+    // logit); what has only adds to the sum, and is neither binned nor listed.  The 0.05 are
+    // three bins: what lies behind the bin in front of `near`'s weighs less than 0.97 of
+    // (1 - p), so the border is found there or before, and a list's length is what was binned.
+    // (near is in (0, 29.2]; the first bins end at 32)
     const float inv_unit = by_count ? 1.f : 1.f / run.inv_t;
-    // (and the first bins end at 32)
-    const float near = by_count ? INFINITY : fminf(logf((float)V) - logf(1.f - top_p) + 0.05f, 31.9f);
+    const float near = by_count ? INFINITY : logf((float)V) - logf(1.f - top_p) + 0.05f;
     Bins bins;
     bins.set(0.f, by_count ? kCountScale : kWeightScale);
     Verdict v;
@@ -1098,7 +1101,7 @@ __global__ void __launch_bounds__(kSpThreads, 3) sampling_kernel(const SpArgs a)
       sum_groups(sh, bins, by_count);
       cluster_sync();
       if (rank == 0) {
-        if (warp == 0) find_bins(sh, bins, by_count, k, top_p, ranks, level, V);
+        if (warp == 0) find_bins(sh, bins, by_count, k, top_p, ranks, level);
         __syncthreads();
         // (before the others put their lists there)
         for (int b = tid; b < kBins; b += kSpThreads) sh.hist[b] = 0u;
@@ -1141,7 +1144,8 @@ __global__ void __launch_bounds__(kSpThreads, 3) sampling_kernel(const SpArgs a)
           w[i] = by_count ? 0.f : expf(d);
           w[i] = in && b < lo ? w[i] : 0.f;
           count += in && b < lo;
-          if (in && (unsigned)(b - lo) <= (unsigned)(v.hi - lo)) list(x[i], first + i);
+          // (the last bins may reach beyond what was binned)
+          if (in && d >= -near && (unsigned)(b - lo) <= (unsigned)(v.hi - lo)) list(x[i], first + i);
         }
         if (!by_count && v.what == kCollect) {
 #pragma unroll
