@@ -783,8 +783,9 @@ int tsd_tree_attn_fwd_shared(const uint16_t *q, const uint16_t *k_cache, const u
  *   rotation  of the first R columns of each such row (0: none; a multiple of 32, at
  *             most D): for f < R / 2 columns (f, R/2 + f), or with `interleaved`
  *             (2f, 2f + 1), as (a cos - b sin, b cos + a sin) with the angle
- *             p * inv_freq[f], cos and sin times rot_scale.  The angle is
- *             exact to 2^-24 of a turn for every position.
+ *             p * inv_freq[f], cos and sin times rot_scale.  The angle is exact to
+ *             2^-24 of a turn for every position and |inv_freq| < 2^64 (an infinity or a
+ *             NaN turns nothing).
  *   position  p = pos[axis][t] + base[t / per_base], axis = freq_axis[f].
  *             pos int32 [axes][T] (NULL: t % per_base, the place in the sequence);
  *             base int32 [ceil(T / per_base)] or NULL (0); freq_axis int32 [R/2]

@@ -271,3 +271,49 @@ def test_two_streams_at_once(tsd):
     torch.cuda.synchronize()
     assert torch.equal(pools[0], pools[2]) and torch.equal(pools[1], pools[3])
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def turn_fraction():
+    """floor(2^400 / (2 pi)), pi by Machin's formula in whole numbers."""
+    bits = 460
+
+    def atan_inverse(n):
+        total, term, k, sign = 0, (1 << bits) // n, 1, 1
+        while term:
+            total += sign * (term // k)
+            term //= n * n
+            k += 2
+            sign = -sign
+        return total
+
+    pi = 4 * (4 * atan_inverse(5) - atan_inverse(239))
+    return (1 << (400 + bits)) // (2 * pi)
+
+
+@pytest.mark.parametrize("D,pairs", [(128, False), (64, True)])
+def test_angles_of_far_positions_and_high_frequencies(tsd, D, pairs):
+    """Rows of ones and zeros turn into cosines and sines of position times frequency.  The angle is exact to 2^-24
+    of a turn (below 2^-21 radians), sincospif to 2^-22, and the result is rounded to bf16."""
+    rng = np.random.default_rng(D)
+    half, tokens = D // 2, 96
+    inv = (10.0 ** rng.uniform(-8, 7, half) * rng.choice([-1, 1], half)).astype(np.float32)
+    inv[:6] = [1.0, -100.0, 0.0, 1e-42, 1e18, -1e15]
+    pos = rng.integers(-2 ** 31, 2 ** 31, tokens).astype(np.int32)
+    pos[:4] = [2 ** 31 - 1, -2 ** 31, 0, 262144]
+    x = np.zeros((tokens, 1, D), np.float32)
+    x[..., np.arange(half) * 2 if pairs else np.arange(half)] = 1.0
+    bits = gen.bf16_bits(x)
+    kc = bf(np.zeros((1, 1, 16, D), np.uint16))
+    out = tsd.kv_append_rope(bf(bits), bf(bits), bf(bits), T(np.full(tokens, -1, np.int32)), kc, kc, T(inv), T(pos),
+                             interleaved=pairs)
+    got = oracle.bf16_to_f64(np_of(out, np.uint16))[:, 0]
+    got_cos, got_sin = (got[:, ::2], got[:, 1::2]) if pairs else (got[:, :half], got[:, half:])
+    turn = turn_fraction()
+    for f in range(half):
+        num, den = float(inv[f]).as_integer_ratio()
+        for t in range(tokens):
+            # a fraction of a turn in 2^64ths, then in [-1/2, 1/2)
+            z = ((num * int(pos[t]) * turn << 64) // (den << 400)) % (1 << 64)
+            angle = 2 * np.pi * (z - (1 << 64) * (z >> 63)) / 2.0 ** 64
+            for g, ref in ((got_cos[t, f], np.cos(angle)), (got_sin[t, f], np.sin(angle))):
+                assert abs(g - ref) <= 2.0 ** -8 * abs(ref) + 2.0 ** -21 + 2.0 ** -22, (inv[f], pos[t], g, ref)

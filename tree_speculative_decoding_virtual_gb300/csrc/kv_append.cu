@@ -12,8 +12,10 @@
 //
 // Angles: an fp32 product loses the angle of a far position (at 2^18 it is off by
 // 2^-7), so a frequency is held as 64-bit fixed-point turns and multiplied by the
-// position modulo one turn, which is exact but for the frequency's last bit; the
-// rest is a fraction of a turn in [-1/2, 1/2).
+// position modulo one turn.  The 64 bits come from a whole-number product of the
+// frequency's mantissa and 128 bits of 1 / (2 pi) and are off by less than two of their last
+// places (frequencies below 2^64), the angle at position 2^31 by less than 2^-32 of a turn;
+// the rest is a fraction of a turn in [-1/2, 1/2).
 //
 // Each byte is read and written once, so memory bounds many tokens and the launch few.  A
 // block takes a few tokens: their cosines and sines are computed once, into shared memory,
@@ -60,9 +62,18 @@ struct AppendArgs {
 
 // inv_freq / (2 pi) as a 64-bit fraction of a turn, whole turns dropped.
 __device__ __forceinline__ uint64_t turns(float inv_freq) {
-  double t = (double)inv_freq * 0.15915494309189535;
-  t -= floor(t);
-  return t < 1.0 ? __double2ull_rz(t * 18446744073709551616.0) : 0ull;
+  constexpr uint64_t kHi = 0x28BE60DB9391054Aull, kLo = 0x7F09D5F47D4D3770ull;  // 2^128 / (2 pi)
+  const uint32_t bits = __float_as_uint(inv_freq), e = bits >> 23 & 255u;
+  if (e == 255u) return 0ull;  // infinity, NaN
+  const uint64_t m = bits & 0x7FFFFFu | (e ? 0x800000u : 0u);  // |inv_freq| = m 2^(max(e, 1) - 150)
+  const int shift = 214 - (int)max(e, 1u);  // of the product, down to multiples of 2^-64: -40 .. 213
+  const uint64_t w0 = m * kLo, w1 = m * kHi + __umul64hi(m, kLo);
+  const uint64_t w2 = __umul64hi(m, kHi) + (w1 < m * kHi);
+  const int word = shift >> 6, bit = shift & 63;
+  const uint64_t x = word == 0 ? w0 : word == 1 ? w1 : word == 2 ? w2 : 0ull;
+  const uint64_t y = word == -1 ? w0 : word == 0 ? w1 : word == 1 ? w2 : 0ull;
+  const uint64_t t = bit ? x >> bit | y << (64 - bit) : x;
+  return bits >> 31 ? 0ull - t : t;
 }
 
 // Two neighbouring columns in one 64-bit register, as the two-wide fp32 instructions take
