@@ -317,3 +317,9 @@ def test_angles_of_far_positions_and_high_frequencies(tsd, D, pairs):
             angle = 2 * np.pi * (z - (1 << 64) * (z >> 63)) / 2.0 ** 64
             for g, ref in ((got_cos[t, f], np.cos(angle)), (got_sin[t, f], np.sin(angle))):
                 assert abs(g - ref) <= 2.0 ** -8 * abs(ref) + 2.0 ** -21 + 2.0 ** -22, (inv[f], pos[t], g, ref)
+
+
+@pytest.mark.parametrize("tokens,Hkv,D,R,pairs", [(5003, 1, 128, 128, False), (2500, 2, 64, 32, True)])
+def test_prompts_into_a_4_bit_cache(tsd, tokens, Hkv, D, R, pairs):
+    """Prompts whose blocks take several tokens each, queries among them: as the smaller ones."""
+    test_append_to_a_4_bit_cache(tsd, tokens, Hkv, D, R, True, pairs)
