@@ -749,13 +749,23 @@ int tsd_tree_path_logprobs(const void *logits, int bf16, const int32_t *tokens, 
  *   the table of the group's first sequence that is not skipped.
  * Other arguments, outputs and errors as tsd_tree_attn_fwd; a sequence with a
  * prefix shorter than S is skipped (TSD_STATUS_BAD_LEN), and so is one with a bad
- * block id in its key range, or in the shared range that is read for it.  mask
+ * block id among those that are read for it: its own from slot S on (S / 16 included),
+ * the shared range's in the table of the sequence that stands for the group; the
+ * other tables' first S / 16 entries are not looked at.  mask
  * NULL: node i sees the tree's nodes 0..i (a chain; with N_max = 1 the decoding of
  * one token).  A row that sees no key gets 0 / -inf.  What lies in slots outside a
  * sequence's keys does not matter, NaN included; a row that sees a tree node whose V has
  * a NaN or an infinity gets NaN, the rows that do not see it are as without it.
  * P is rounded to bf16; sums, and the partial results that are joined, are fp32.
+ * When: the shared slots' bytes and products are saved for every sequence but one, and
+ * three kernels and fp32 partial rows added.  Measured beside tsd_tree_attn_fwd (8 kv
+ * heads of 128, 32 to 64 query heads, 64 to 256 own slots): for single tokens faster from
+ * 16 sequences behind 2048 slots or 4 behind 32768 on (64 behind 16384: 6 times), slower
+ * below; for trees, whose nodes share the reads already, as fast from some 8192 slots on (1.0 to
+ * 1.2 times) and slower below (16 trees of 31 nodes behind 512: 0.6).
  * Limits: B <= 1024, B * Hkv <= 65535, 1 <= G <= B.
+ * The workspace holds some (2 * B * N_max * Hq + 256 * SMs) fp32 rows, that is 8 bytes for
+ * each value of q (17 GB at B 1024, N_max 256, 64 heads of 128).
  * workspace >= tsd_tree_attn_shared_workspace_bytes(), 16-byte aligned (the plan of the
  * call and fp32 partial rows; no initial contents); calls that may run at the same time
  * need workspaces of their own.  Three launches (plan, attention, join) whose shapes
@@ -853,7 +863,8 @@ int tsd_kv_append_rope_q4(const uint16_t *q, int64_t q_stride, const uint16_t *k
  * logits float (bf16 == 0) or bf16; temperature, top_p, min_p float, top_k int32,
  * each NULL (off) or [ceil(R / per_param)]: entry r / per_param is row r's.
  * Limits: V <= 262144, draws <= 64, R <= 2^24.
- * One launch, no workspace: clusters of up to 8 CTAs that take row after row.
+ * One launch, no workspace: clusters of up to 8 CTAs that take row after row.  Rows that
+ * do not begin on 16 bytes (V not a multiple of 4, or of 8 for bf16) take up to 30% longer.
  */
 int tsd_token_sample(const void *logits, int bf16, const int32_t *rows, int R, int64_t num_rows, int V,
                      const float *u, int draws, const float *temperature, const int32_t *top_k,

@@ -955,7 +955,9 @@ def tree_attn_fwd_shared(q, k_cache, v_cache, block_table, prefix_len, n_nodes, 
     """tree_attn_fwd for groups of sequences that hold the same keys and values in
     their first shared_len[j] slots (int32 [G]); group j is the sequences
     group_first[j] .. group_first[j + 1] - 1 (int32 [G + 1]).  mask None: node i sees
-    nodes 0..i (a chain, or one token).  Returns (out bf16 [B][N_max][Hq][D], lse
+    nodes 0..i (a chain, or one token).  Pays for single tokens from some 16 sequences
+    behind 2048 slots, or 4 behind 32768, and for trees behind 8192 slots and more;
+    tree_attn_fwd is faster below.  Returns (out bf16 [B][N_max][Hq][D], lse
     float32 [B][N_max][Hq] or None)."""
     if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.shape[2] != 16:
         raise TsdError("k_cache and v_cache must be [num_blocks][Hkv][16][D], alike")

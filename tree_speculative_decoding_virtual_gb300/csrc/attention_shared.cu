@@ -14,7 +14,10 @@
 // Plan (one block, its own kernel): lengths are known to the device alone.  The
 // units' key tiles (128 keys; cost 1, or 2 with more than 128 rows, and a fixed cost
 // a unit) are laid end to end and cut into equal parts, one a block, so that every SM
-// has the same work whatever the lengths; trees are packed, so that padding nodes
+// has the same work whatever the lengths, as long as there is enough of it: a part is no
+// shorter than a set-up and two tiles, and a range has at most 64 (counted as if it had
+// two row tiles), so one or two kv heads do not fill the GPU (4 tokens of 8 heads behind 131072
+// slots of one kv head: 67 us, of two 77, of eight 122).  Trees are packed, so that padding nodes
 // cost nothing.  Where there are blocks enough, no part spans two units (4 tokens behind
 // 2048 slots: the attention 12 us, 19.5 with such parts).
 //
@@ -37,7 +40,8 @@
 // that sees S_j complete may rescale O and overwrite S_j.  A row's reference m is the
 // maximum of its chain's first tile, and moves when 64 keys' P sum above 2^60.
 // Row sums add P before its rounding to bf16: the roundings are as often up as down,
-// and the row's lse is that of the fp32 scores.
+// and the row's lse is that of the fp32 scores.  (The tensor core takes P in V's type.  Against
+// 64 bits the outputs are off by 0.0023 of their size, by 0.0017 where nothing but they is rounded.)
 //
 // 0 times a NaN is one: V's rows outside the key range (the rest of a page, never
 // written) are set to zero in shared memory, and so is a tree node's with a NaN or an
@@ -45,10 +49,13 @@
 //
 // What bounds it, and what it measured.  Long shared ranges with many rows: the two chains'
 // MMAs and softmaxes (3500 cycles for a tile of 256 rows; 8 trees of 127 nodes, 64 heads,
-// 32768 shared slots: 746 us, 1.5 PFLOP/s; a register split 104 / 64 and not 96 for all
+// 32768 shared slots: 755 us, 1.5 PFLOP/s; a register split 104 / 64 and not 96 for all
 // warps 850 -> 803, a row's threads tied by a barrier of two warps 803 -> 769).  Many
-// short own ranges: the start and end of each (64 tokens behind 16384 slots: 75 us; 16
-// trees of 16 to 31 nodes: 55 us).  Tried and slower: the next range's ids, queries and
+// short own ranges: the start and end of each (64 tokens behind 16384 slots: 77 us; 16
+// trees of 16 to 31 nodes: 57 us).  These are the attention's; the plan takes 8 to 10, the join
+// 8 to 40.  Beside tree_attn_fwd on the same tensors, cold and with all three kernels: 64 tokens 97
+// and 568 us, 16 tokens behind 2048 slots 32 and 37, 4 behind 2048 30 and 22, behind 32768 58
+// and 85; 8 trees of 127 nodes 790 and 935, 16 of 16 to 31 nodes 75 and 65.  Tried and slower: the next range's ids, queries and
 // first tiles fetched ahead by warp 3 (791 to 902 us, 85 to 94 us; at the range's end no
 // difference), all segments cut by the plan (it takes 20 instead of 7 us), a polynomial in
 // place of half the exponentials.

@@ -23,10 +23,12 @@
 // other (chunks l and l + R/16, or with neighbouring pairs 2l and 2l + 1), and the
 // arithmetic goes two columns to an instruction.  What holds the loads in flight is the
 // number of warps: 8 blocks of 128 threads and 4 tokens.  Measured at 32768 tokens of 64 +
-// 2 x 8 heads of 128 (1.34 GB moved): 248 us, 5.4 TB/s; blocks of 256 threads with 16 tokens
+// 2 x 8 heads of 128 (1.34 GB moved): 249 us, 5.4 TB/s; blocks of 256 threads with 16 tokens
 // 261 us, with the loads of two steps on the way (and half the warps) 355 us, warps that
-// keep a token's cosines in registers 282 us.  One token of 32 + 2 x 8 heads: 4.6 us; 496
-// tokens of 32 + 2 x 8 heads into 4 bits 8.7 us.
+// keep a token's cosines in registers 282 us.  The same into 4 bits (1.25 GB): 231 us, 5.4
+// TB/s.  One token of 32 + 2 x 8 heads: 2.5 us in a graph, 8 cold; 496 tokens of 32 + 2 x 8
+// heads 10 us cold, into 16 bits and into 4: the launch, and one wave of blocks whose loads,
+// angles and stores follow one another.
 #include <cuda_bf16.h>
 
 #include "q4.cuh"

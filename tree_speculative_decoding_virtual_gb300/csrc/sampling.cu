@@ -33,10 +33,15 @@
 //
 // What bounds it is not the one read of the row (the floor of 508 rows of 128256 fp32 logits
 // is 38 us) but some 25 instructions a logit for the histogram (10k cycles of a row's 42k
-// with 8 CTAs) and the chain of exchanges in the cluster: three barriers of 3k cycles, bins
-// 5k, list 5k, the first CTA's end 5k.  CTAs exchange by loads of what each left in its own
-// shared memory: adds from eight CTAs to one place took 6k to 14k cycles.  Measured: one row
-// 14 us, 508 rows 305 us where lists settle it.
+// with 8 CTAs) and the chain of exchanges in the cluster (three barriers of 3k cycles, bins
+// 5k, list 5k, the first CTA's end 5k).  CTAs exchange by loads of what each left in its own
+// shared memory: adds from eight CTAs to one place took 6k to 14k cycles.  Measured with a cold
+// L2, 128256 logits: one fp32 row with top-k 50 and top-p 0.95 24 us (18 in a graph, 8 CTAs),
+// 63 such rows filtered 57; 64 bf16 rows of mixed settings 63 to 72 (6 CTAs); 508 fp32 rows
+// with top-p 0.9 and four draws 250 to 350 by the rows' shape, to probabilities 310 to 460
+// (8 CTAs).  Rows that do not begin on 16 bytes are copied value by value, not under the end of
+// the row before, and take up to 30% longer: 508 fp32 rows with top-p 0.9 and four draws 127 us
+// for 50256 logits, 158 for 50257; 64 bf16 rows with top-k 50 31 and 33.
 #include <cuda_bf16.h>
 
 #include <cmath>
@@ -467,7 +472,7 @@ __device__ __forceinline__ long long place_of(float u, long long total) {
   return min((long long)at, total - 1);
 }
 
-// The same over the cluster; `turn` is which of the two places is used.
+// block_total over the cluster; `turn` is which of the two places is used.
 __device__ __forceinline__ long long cluster_total(SpShared &sh, int &turn, uint32_t ranks, int &count, long long mine) {
   const long long t = block_total(sh, count, mine);
   if (threadIdx.x == 0) {
@@ -700,8 +705,9 @@ __device__ __forceinline__ void list_scan(const SpShared &sh, int n, unsigned lo
 
 // The first CTA's end of it: ranks the list, finds the border, and where everything
 // is in the list the sum of what is kept and the draws.  By the whole block: a short list's
-// entries are compared with all, a long one is sorted (508 rows with top-p 0.9: 310 us;
-// with all lists compared 331, and all sorted a single row takes 33 us instead of 30).
+// entries are compared with all, a long one is sorted (with all lists of more than
+// kSmallList sorted one row takes 29 us instead of 24, 63 filtered rows 61 instead of 57, 508
+// rows as long; comparing all took 508 rows with top-p 0.9 7% longer when it was tried).
 template <bool kBf16, int kMode>
 __device__ __forceinline__ void settle(SpShared &sh, const Run<kBf16> &run, const Found &f, const SpArgs &a, int r) {
   const int tid = threadIdx.x, n = f.n;
@@ -918,6 +924,7 @@ __global__ void __launch_bounds__(kSpThreads, 3) sampling_kernel(const SpArgs a)
     const uint32_t none = kBf16 ? 0xFF80FF80u : 0xFF800000u;
     for (int s = 0; s < run.steps; ++s) {
       const int id = run.id + s * kStep;
+      // (a row that does not begin on 16 bytes is waited for here: slower, see the top)
       if (vec && id + kN <= V) {
         cp_async_16(smem_addr(mine + s * 32), src + id);
       } else {
@@ -1419,10 +1426,11 @@ cudaError_t sp_launch(SpArgs &a, cudaStream_t s) {
   const Fits fits = clusters_at_once<kBf16>((const void *)sampling_kernel<kBf16, kMode>, a.V, cfg);
   // As many clusters as run at once, each taking row after row.  A row costs some 20 us and
   // 1.4 us for each 1000 logits of a CTA (fitted to clusters of 1 to 8 CTAs over 8000 to
-  // 262144 logits, 20 to 2000 rows; every choice below is the fastest measured or within 3%
-  // of it): few rows are spread over as many CTAs as can be, of many rows those CTAs stay
-  // together that let the SMs fill up.  64 rows of 128256 bf16 logits: 8 CTAs a row 60 us,
-  // 6 42 us; 508 rows: 8 CTAs 449 us, 4 343 us; 508 rows of 8000 fp32: 8 CTAs 214 us, 1 68 us.
+  // 262144 logits, 1 to 2000 rows; the choice is the fastest measured or within 2 us, the
+  // timer's step, of it): few rows are spread over as many CTAs as can be, of many rows those
+  // CTAs stay together that let the SMs fill up.  With top-p 0.9 and a cold L2: 64 rows of
+  // 128256 bf16 logits 8 CTAs a row 102 us, 6 74 us; 508 such rows 8 CTAs 436 us, 4 328 us;
+  // 508 rows of 8000 fp32 8 CTAs 217 us, 1 68 us.
   int most = 1;
   while (most < kMaxCluster && most * kSpWarps * 32 * SpVec<kBf16>::kN < a.V) ++most;
   int best = 0;
